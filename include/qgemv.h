@@ -342,6 +342,105 @@ qg_status qgemm_grouped(const qg_moe_layer* layer, int stage, const void* in, in
                         const float* topk_w, const float* shared_gate, const void* route_ws, void* out, int64_t ldo,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ attention over an 8-bit paged cache
+ * What a decode or prefill step runs between its QKV and output projections: qkv_append
+ * norms and rotates the queries and keys of the new tokens and writes keys and values into
+ * the cache; qattn attends to the cache.  (Conifer note: decode attention, the KV heads shared
+ * by several query heads, the length split over the GPU; TurboEXL3 article §4.3: QK-norm and
+ * partial rotary fused behind the QKV projection.)
+ *
+ * The cache is a pool of pages of page_tokens tokens each.  Keys and values are E4M3 codes with
+ * one fp32 scale per (page, KV head), value = code * scale:
+ *   k_codes, v_codes   : uint8 [n_pages][n_kv_heads][page_tokens][head_dim]
+ *   k_scales, v_scales : fp32 [n_pages][n_kv_heads], positive and finite in every page in use
+ * A sequence's token t lies in row t % page_tokens of page pages[t / page_tokens].
+ * page_tokens is 16, 32, 64 or 128; head_dim 64, 128 or 256. */
+typedef enum { QG_KV_E4M3 = 1 } qg_kv_format;
+
+typedef struct {
+  int32_t fmt;            /* qg_kv_format */
+  int32_t page_tokens;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int64_t n_pages;
+  void* k_codes;          /* device, 16-byte aligned */
+  void* v_codes;          /* device, 16-byte aligned */
+  float* k_scales;        /* device, 16-byte aligned */
+  float* v_scales;        /* device, 16-byte aligned */
+} qg_kv_cache;
+
+/* The sequences of a call.  Sequence b's new tokens are rows q_start[b] .. q_start[b+1]-1 of
+ * the call's queries (0 rows is allowed), and lens[b] is its length with them, so that its
+ * i-th new token stands at position lens[b] - (q_start[b+1] - q_start[b]) + i.  max_new and
+ * max_len bound the new tokens and the length of every sequence; the launches are shaped
+ * by them, so tight bounds are faster.  The device arrays are checked on the device:
+ * a sequence outside the bounds is skipped (as if it had no rows), a page id outside
+ * the pool hides its tokens, and either puts QG_ERR_INVALID_ARG into the workspace's status
+ * word (qg_workspace_status). */
+typedef struct {
+  int32_t n_seqs;         /* 1 .. 65535 */
+  int32_t max_new;        /* >= 1 */
+  int64_t max_len;        /* 1 .. page_stride * page_tokens, below 2^31 */
+  const int32_t* q_start; /* device [n_seqs + 1], ascending */
+  const int32_t* lens;    /* device [n_seqs] */
+  const int32_t* pages;   /* device [n_seqs][page_stride] page ids */
+  int64_t page_stride;
+} qg_kv_batch;
+
+/* Norm and rotation of the queries and keys (each optional):
+ *   y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)     over each head, in fp32
+ *   for j < R/2 the pair (a, b) = (y[j], y[j + R/2]), or (y[2j], y[2j+1]) when interleaved:
+ *   a' = a cos - b sin, b' = b cos + a sin, cos = cos_sin[p][j], sin = cos_sin[p][R/2 + j]
+ * with p the token's position and R = rotary_dim; elements from R on stay as they are. */
+typedef struct {
+  const void* q_weight;   /* device bf16 [head_dim], or NULL: queries are not normed */
+  const void* k_weight;   /* device bf16 [head_dim], or NULL: keys are not normed */
+  float eps;              /* >= 0 */
+  float weight_offset;
+  const float* cos_sin;   /* device fp32 [n_positions][rotary_dim]; NULL iff rotary_dim is 0 */
+  int64_t n_positions;    /* >= max_len of the batch when there is a rotation */
+  int32_t rotary_dim;     /* 0, or a multiple of 16 up to head_dim */
+  int32_t interleaved;    /* 0 or 1 */
+} qg_norm_rope;
+
+/* Workspace bytes of qkv_append: the status word. */
+size_t qkv_append_workspace_size(void);
+
+/* Norm, rotate and append: for every new token,
+ *   q_out = bf16(rotate(norm(q)))                        bf16 [n_tokens][n_q_heads][head_dim]
+ *   cache row of its position = E4M3(rotate(norm(k)) / k_scale), E4M3(v / v_scale)
+ * all in fp32, each value rounded once.  q, k, v, q_out: element (token, head, d) lies at
+ * token * ld + head * hs + d; ld and hs are multiples of 8 elements.  q_out may be q itself
+ * with the same strides.  q may be NULL (n_q_heads 0): only the cache is written.  norm_rope may be NULL.
+ * Scales: a page's scale for a KV head is the smallest power of two s (2^-100 .. 2^120) with
+ * amax <= 448 s, amax the largest finite magnitude that the page holds.  A page that
+ * already holds tokens keeps its scale until a new token needs a larger one; its codes
+ * are then multiplied by old / new and rounded again (exact for powers of two, but
+ * for codes that become subnormal).  Infinities saturate, NaN stays NaN; neither moves a scale.
+ * lens[b] counts the new tokens, so it is at least their number.  Two sequences of one
+ * call may share pages that neither writes.  Deterministic; one launch. */
+qg_status qkv_append(const qg_kv_cache* cache, const qg_kv_batch* batch, const qg_norm_rope* norm_rope,
+                     int64_t n_tokens, int n_q_heads, const void* q, int64_t ldq, int64_t hsq,
+                     const void* k, int64_t ldk, int64_t hsk, const void* v, int64_t ldv, int64_t hsv,
+                     void* q_out, int64_t ldqo, int64_t hsqo, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes qattn needs for these sizes on the current device (0 for sizes that qattn
+ * rejects).  Reads only the sizes of `cache` and `batch`, no pointer. */
+size_t qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int n_q_heads);
+
+/* Causal attention of the new tokens over the cache (their own keys and values have been
+ * appended before):
+ *   out[i][h] = bf16( sum_t softmax_t(scale * q[i][h] . k[t][h / G]) v[t][h / G] ),
+ *   t in max(0, p - window + 1) .. p,  p the position of row i, G = n_q_heads / n_kv_heads.
+ * window 0: no window.  A row that sees no key (p < 0, or lens 0) is zero.  scale is finite and > 0.
+ * q and out: bf16, strides as in qkv_append; rows of no sequence are left as they are.
+ * Keys beyond the position, whatever their bits, do not enter.  G is at most 128.
+ * The workspace must be zero-filled before its first use; every call leaves it ready for
+ * the next, and calls that overlap on the GPU must not share it.  Deterministic. */
+qg_status qattn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int n_q_heads,
+                const void* q, int64_t ldq, int64_t hsq, float scale, int64_t window,
+                void* out, int64_t ldo, int64_t hso, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Workspace-free variant of qgemv, for callers that cannot allocate device memory:
  * plugins hosted by a runtime that owns all of the GPU's memory and gives them no
  * allocator, and code on paths where cudaMalloc's implicit device synchronisation is not

@@ -45,6 +45,24 @@ class qg_moe_layer(ctypes.Structure):
                 ("shared_gate_up", qg_weight), ("shared_down", qg_weight)]
 
 
+class qg_kv_cache(ctypes.Structure):
+    _fields_ = [("fmt", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("k_codes", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p)]
+
+
+class qg_kv_batch(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("max_new", ctypes.c_int32), ("max_len", ctypes.c_int64),
+                ("q_start", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("pages", ctypes.c_void_p),
+                ("page_stride", ctypes.c_int64)]
+
+
+class qg_norm_rope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float), ("cos_sin", ctypes.c_void_p), ("n_positions", ctypes.c_int64),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _SIGNATURES = {
@@ -73,8 +91,15 @@ _SIGNATURES = {
     "qgemm_w4a4_workspace_size": (_SZ, [_I, _I64, _I64, _I64]),
     "qgemm_w4a4": (_I, [ctypes.POINTER(qg_weight), _P, _I64, _I64, ctypes.c_float, _P, _I64, _P, _I64, _P, _SZ,
                         _P]),
+    "qkv_append_workspace_size": (_SZ, []),
+    "qkv_append": (_I, [ctypes.POINTER(qg_kv_cache), ctypes.POINTER(qg_kv_batch), ctypes.POINTER(qg_norm_rope), _I64, _I,
+                        _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _SZ, _P]),
+    "qattn_workspace_size": (_SZ, [ctypes.POINTER(qg_kv_cache), ctypes.POINTER(qg_kv_batch), _I64, _I]),
+    "qattn": (_I, [ctypes.POINTER(qg_kv_cache), ctypes.POINTER(qg_kv_batch), _I64, _I, _P, _I64, _I64, ctypes.c_float,
+                   _I64, _P, _I64, _I64, _P, _SZ, _P]),
 }
 
+QG_KV_E4M3 = 1
 QG_MOE_GATE_UP_SWIGLU = 1
 QG_MOE_DOWN_COMBINE = 2
 
@@ -229,6 +254,27 @@ def qg_selftest_wait_timeout(ws_ptr: int, ws_bytes: int, stream: int = 0):
     """Launch the bounded-wait self-test (its wait runs out after the library's limit and
     records QG_ERR_TIMEOUT in the workspace status word)."""
     _check(lib().qg_selftest_wait_timeout(ws_ptr, ws_bytes, stream), "qg_selftest_wait_timeout")
+
+
+def qkv_append_workspace_size() -> int:
+    return lib().qkv_append_workspace_size()
+
+
+def qkv_append(cache: qg_kv_cache, batch: qg_kv_batch, norm_rope: Optional[qg_norm_rope], n_tokens: int, n_q_heads: int,
+               q_ptr: Optional[int], ldq: int, hsq: int, k_ptr: int, ldk: int, hsk: int, v_ptr: int, ldv: int, hsv: int,
+               q_out_ptr: Optional[int], ldqo: int, hsqo: int, ws_ptr: int, ws_bytes: int, stream: int = 0):
+    _check(lib().qkv_append(cache, batch, norm_rope, n_tokens, n_q_heads, q_ptr, ldq, hsq, k_ptr, ldk, hsk, v_ptr, ldv,
+                            hsv, q_out_ptr, ldqo, hsqo, ws_ptr, ws_bytes, stream), "qkv_append")
+
+
+def qattn_workspace_size(cache: qg_kv_cache, batch: qg_kv_batch, n_tokens: int, n_q_heads: int) -> int:
+    return lib().qattn_workspace_size(cache, batch, n_tokens, n_q_heads)
+
+
+def qattn(cache: qg_kv_cache, batch: qg_kv_batch, n_tokens: int, n_q_heads: int, q_ptr: int, ldq: int, hsq: int,
+          scale: float, window: int, out_ptr: int, ldo: int, hso: int, ws_ptr: int, ws_bytes: int, stream: int = 0):
+    _check(lib().qattn(cache, batch, n_tokens, n_q_heads, q_ptr, ldq, hsq, scale, window, out_ptr, ldo, hso, ws_ptr,
+                       ws_bytes, stream), "qattn")
 
 
 # ------------------------------------------------------------------ torch helpers
@@ -452,4 +498,144 @@ def moe_stage(pm: PackedMoE, stage: int, inp, t: int, topk: int, route_ws: Works
                   None if topk_w is None else topk_w.data_ptr(),
                   None if shared_gate is None else shared_gate.data_ptr(), route_ws.ptr, out.data_ptr(),
                   out.stride(0), workspace.ptr, workspace.nbytes, _stream_ptr())
+    return out
+
+
+# ------------------------------------------------------------------ attention over the 8-bit paged cache
+def _need(ok: bool, what: str):
+    if not ok:
+        raise QGError(1, what)
+
+
+class KVCache:
+    """A pool of pages of keys and values in 8 bits (``qg_kv_cache``): codes float8_e4m3fn (or uint8)
+    [n_pages, n_kv_heads, page_tokens, head_dim] and scales fp32 [n_pages, n_kv_heads], contiguous on the device."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        import torch
+        _need(k_codes.dim() == 4 and k_codes.shape == v_codes.shape, "KVCache: codes are [pages, heads, tokens, dim]")
+        _need(k_scales.shape == k_codes.shape[:2] and v_scales.shape == k_codes.shape[:2], "KVCache: scales are [pages, heads]")
+        for t in (k_codes, v_codes, k_scales, v_scales):
+            _need(t.is_contiguous() and t.device == k_codes.device, "KVCache: contiguous tensors on one device")
+        for t in (k_codes, v_codes):
+            _need(t.dtype in (torch.float8_e4m3fn, torch.uint8), "KVCache: codes are float8_e4m3fn or uint8")
+        for t in (k_scales, v_scales):
+            _need(t.dtype == torch.float32, "KVCache: scales are float32")
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = k_codes.shape
+        self.desc = qg_kv_cache(QG_KV_E4M3, self.page_tokens, self.n_kv_heads, self.head_dim, self.n_pages,
+                                k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
+
+    @staticmethod
+    def empty(n_pages: int, n_kv_heads: int, page_tokens: int, head_dim: int, device="cuda") -> "KVCache":
+        """A pool with nothing in it yet."""
+        import torch
+        shape = (n_pages, n_kv_heads, page_tokens, head_dim)
+        codes = [torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.ones(shape[:2], dtype=torch.float32, device=device) for _ in range(2)]
+        return KVCache(*codes, *scales)
+
+
+class KVBatch:
+    """The sequences of a call (``qg_kv_batch``): q_start int32 [n_seqs + 1], lens int32 [n_seqs] (with the new
+    tokens) and pages int32 [n_seqs, m] on the device; max_new and max_len bound every sequence's new tokens
+    and length.  The tensors' contents may change between calls (within the bounds)."""
+
+    def __init__(self, q_start, lens, pages, max_new: int, max_len: int):
+        import torch
+        for t in (q_start, lens, pages):
+            _need(t.dtype == torch.int32 and t.device == lens.device, "KVBatch: int32 tensors on one device")
+        n = lens.numel()
+        _need(lens.dim() == 1 and lens.is_contiguous(), "KVBatch: lens is contiguous [n_seqs]")
+        _need(q_start.shape == (n + 1,) and q_start.is_contiguous(), "KVBatch: q_start is contiguous [n_seqs + 1]")
+        _need(pages.dim() == 2 and pages.shape[0] == n and pages.stride(1) == 1, "KVBatch: pages is [n_seqs, m]")
+        _need(n == 1 or pages.stride(0) >= pages.shape[1], "KVBatch: pages' rows overlap")
+        self.q_start, self.lens, self.pages = q_start, lens, pages
+        self.n_seqs, self.max_new, self.max_len = n, int(max_new), int(max_len)
+        self._per_page = pages.shape[1]
+        self.desc = qg_kv_batch(n, self.max_new, self.max_len, q_start.data_ptr(), lens.data_ptr(), pages.data_ptr(),
+                                pages.stride(0) if n > 1 else pages.shape[1])
+
+
+class NormRope:
+    """Norm weights (bf16 [head_dim], each optional) and rotation table (fp32 [positions, rotary_dim]: the pairs'
+    cosines, then their sines) of ``kv_append`` (``qg_norm_rope``)."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps: float = 1e-6, weight_offset: float = 0.0, cos_sin=None,
+                 interleaved: bool = False):
+        import torch
+        for t in (q_weight, k_weight):
+            _need(t is None or (t.dtype == torch.bfloat16 and t.dim() == 1 and t.is_contiguous()),
+                  "NormRope: weights are contiguous bfloat16 [head_dim]")
+        _need(cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()),
+              "NormRope: cos_sin is contiguous float32 [positions, rotary_dim]")
+        self.q_weight, self.k_weight, self.cos_sin = q_weight, k_weight, cos_sin
+        self.desc = qg_norm_rope(None if q_weight is None else q_weight.data_ptr(),
+                                 None if k_weight is None else k_weight.data_ptr(), eps, weight_offset,
+                                 None if cos_sin is None else cos_sin.data_ptr(),
+                                 0 if cos_sin is None else cos_sin.shape[0],
+                                 0 if cos_sin is None else cos_sin.shape[1], 1 if interleaved else 0)
+
+
+def _heads(t, heads, dim, what):
+    """(pointer, token stride, head stride) of bf16 [tokens, heads, dim]."""
+    import torch
+    s, st = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or len(s) != 3 or s[2] != dim or (heads and s[1] != heads) or st[2] != 1:
+        raise QGError(1, f"{what}: bfloat16 [tokens, {heads or 'heads'}, {dim}] with a contiguous last dimension")
+    return t.data_ptr(), st[0], st[1]
+
+
+def kv_append(cache: KVCache, batch: KVBatch, q, k, v, norm_rope: Optional[NormRope] = None, out=None,
+              workspace: Optional[Workspace] = None):
+    """Norm and rotate the new tokens' q and k (bf16 [n, heads, head_dim]), write k and v into the cache and
+    return the queries (``qkv_append``).  q may be None: only the cache is written."""
+    import torch
+    hkv, d = cache.n_kv_heads, cache.head_dim
+    n = k.shape[0]
+    kp, ldk, hsk = _heads(k, hkv, d, "kv_append: k")
+    vp, ldv, hsv = _heads(v, hkv, d, "kv_append: v")
+    _need(v.shape[0] == n, "kv_append: as many rows of k as of v")
+    qp = op = None
+    hq = ldq = hsq = ldo = hso = 0
+    if q is not None:
+        qp, ldq, hsq = _heads(q, 0, d, "kv_append: q")
+        hq = q.shape[1]
+        if out is None:
+            out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=q.device)
+        op, ldo, hso = _heads(out, hq, d, "kv_append: out")
+        _need(q.shape[0] == n and out.shape[0] == n, "kv_append: as many rows of q and out as of k")
+    nr = None
+    if norm_rope is not None:
+        nr = norm_rope.desc
+        for w in (norm_rope.q_weight, norm_rope.k_weight):
+            _need(w is None or w.numel() == d, "kv_append: norm weights of head_dim elements")
+    if workspace is None:
+        workspace = Workspace(qkv_append_workspace_size(), k.device)
+    qkv_append(cache.desc, batch.desc, nr, n, hq, qp, ldq, hsq, kp, ldk, hsk, vp, ldv, hsv, op, ldo, hso, workspace.ptr,
+               workspace.nbytes, _stream_ptr())
+    return out
+
+
+def attention_workspace_size(cache: KVCache, batch: KVBatch, n_tokens: int, n_q_heads: int) -> int:
+    """Workspace bytes of ``attention`` for these sizes."""
+    return qattn_workspace_size(cache.desc, batch.desc, n_tokens, n_q_heads)
+
+
+def attention(cache: KVCache, batch: KVBatch, q, scale: Optional[float] = None, window: int = 0, out=None,
+              workspace: Optional[Workspace] = None):
+    """Causal attention of the new tokens q (bf16 [n, heads, head_dim]) over the cache (``qattn``);
+    scale is 1/sqrt(head_dim) unless given, window 0 means none."""
+    import torch
+    d = cache.head_dim
+    qp, ldq, hsq = _heads(q, 0, d, "attention: q")
+    n, hq = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=q.device)
+    op, ldo, hso = _heads(out, hq, d, "attention: out")
+    _need(out.shape[0] == n, "attention: as many rows of out as of q")
+    if workspace is None:
+        workspace = Workspace(attention_workspace_size(cache, batch, n, hq), q.device)
+    qattn(cache.desc, batch.desc, n, hq, qp, ldq, hsq, d ** -0.5 if scale is None else scale, window, op, ldo, hso,
+          workspace.ptr, workspace.nbytes, _stream_ptr())
     return out

@@ -1,0 +1,409 @@
+// Norm, rotate and append: what runs between a QKV projection and the attention (TurboEXL3
+// article §4.3: QK-norm and partial rotary fused behind the projection).  One launch:
+//   queries: y = x * r * (w + offset), r = 1/sqrt(mean(x^2) + eps), rotated, rounded to bf16;
+//   keys:    the same, then E4M3 codes under the scale of their (page, KV head);
+//   values:  E4M3 codes under theirs.
+//
+// A head of D elements lies across D/8 lanes, eight elements (one 16-byte load) each: the norm is a
+// shuffle sum over those lanes, and a rotation's pairs are either in one lane (interleaved) or
+// R/16 lanes apart (one shuffle), so nothing passes through shared memory.
+//
+// Keys and values are worked on by unit = (page, KV head, K or V): the page's scale depends on all
+// its new tokens, so one group of threads owns them, holds the normed values in registers
+// while it reduces their largest magnitude, and stores the codes; a page's scale has one
+// writer and no atomics.  A group is one warp for up to four new tokens a sequence (decode:
+// eight units a block, no block barrier) and a whole block for prompts.
+// The scale is a power of two: dividing by it is exact, so each code is its value rounded once,
+// and a later, larger scale moves the codes' exponents only.
+//
+// Bound by HBM: bf16 in, bf16 and bytes out.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "qg_attn.h"
+#include "qg_sync.cuh"
+
+namespace qg {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kQPasses = 4;      // heads a query lane group takes, their loads issued together
+constexpr int kWarpRows = 4;     // new tokens a sequence up to which a warp owns a unit
+
+// Two floats -> two E4M3 codes (a in the low byte), nearest even, saturating; NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ float e4m3_value(uint32_t code) {
+  __nv_fp8_e4m3 v;
+  v.__x = (uint8_t)code;
+  return static_cast<float>(v);
+}
+
+__device__ __forceinline__ void unpack8(uint4 w, float (&f)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The exponent x of the smallest power of two with amax <= 448 * 2^x (448 = 1.75 * 2^8),
+// between -100 and 120, from amax's bits.
+__device__ __forceinline__ int scale_exponent(float amax) {
+  const int bits = __float_as_int(amax);
+  const int x = (bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000 ? 1 : 0);
+  return min(max(x, -100), 120);
+}
+
+// A lane's share of the norm and rotation: eight elements from 8 * l on of a head of LPH lanes.
+template <int LPH>
+struct NormRope {
+  float w[8];
+  bool norm;
+  float eps, c[8], s[8];
+  int rot, l;
+  bool inter;
+
+  __device__ __forceinline__ void weights(const uint16_t* weight, float off, float eps_, int lane_in_head) {
+    l = lane_in_head;
+    eps = eps_;
+    norm = weight != nullptr;
+    if (norm) {
+      unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + l), w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] += off;
+    }
+  }
+  // cos and sin of this lane's elements for one position; an element outside the rotation
+  // turns by zero
+  __device__ __forceinline__ void angles(const float* cs, int rot_, int interleaved, int64_t pos) {
+    rot = rot_;
+    inter = interleaved;
+    const int half = rot / 2;
+    if (8 * l < rot) {
+      const float* row = cs + pos * rot;
+      if (inter) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
+        const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + 4 * l));
+        c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+        s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
+      } else {
+        const int j = 8 * l < half ? 8 * l : 8 * l - half;
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(row + j + i));
+          const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + j + i));
+          c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
+          s[i] = b.x, s[i + 1] = b.y, s[i + 2] = b.z, s[i + 3] = b.w;
+        }
+      }
+    }
+  }
+  // every lane of the warp calls this
+  __device__ __forceinline__ void apply(float (&y)[8]) const {
+    if (norm) {
+      float ss = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+#pragma unroll
+      for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+      const float r = __frsqrt_rn(ss * (1.0f / (8 * LPH)) + eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+    }
+    if (rot == 0) return;
+    if (inter) {
+      if (8 * l < rot) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float a = y[2 * i], b = y[2 * i + 1];
+          y[2 * i] = a * c[i] - b * s[i];
+          y[2 * i + 1] = b * c[i] + a * s[i];
+        }
+      }
+    } else {
+      const int d = rot / 16;  // lanes between the elements of a pair
+      const bool low = l < d, in = l < 2 * d;
+      const int lane = threadIdx.x & 31;
+      const int from = in ? (low ? lane + d : lane - d) : lane;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float o = __shfl_sync(0xFFFFFFFFu, y[i], from);
+        if (in) y[i] = low ? y[i] * c[i] - o * s[i] : y[i] * c[i] + o * s[i];
+      }
+    }
+  }
+};
+
+// Sequence of row i: the last one that starts at or before it.
+__device__ __forceinline__ int seq_of_row(const KvArgs& c, int64_t i) {
+  int lo = 0, hi = c.n_seqs;  // q_start[lo] <= i
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (c.q_start[m] <= i)
+      lo = m;
+    else
+      hi = m;
+  }
+  return lo;
+}
+
+// The queries: items (row, head) in order, kQPasses a lane group.
+template <int LPH>
+__device__ __forceinline__ void append_queries(const AppendArgs& a, int64_t block) {
+  constexpr int GROUPS = kAppendThreads / LPH;
+  const int l = threadIdx.x % LPH;
+  const int64_t items = a.c.n_tokens * a.hq;
+  const int64_t first = block * (GROUPS * kQPasses) + threadIdx.x / LPH;
+  NormRope<LPH> nr;
+  nr.weights(a.qw, a.woff, a.eps, l);
+  uint4 x[kQPasses];
+  int64_t row[kQPasses];
+  int head[kQPasses];
+#pragma unroll
+  for (int p = 0; p < kQPasses; ++p) {
+    const int64_t it = first + p * GROUPS;
+    row[p] = -1;
+    head[p] = 0;
+    x[p] = make_uint4(0, 0, 0, 0);
+    if (it < items) {
+      row[p] = it / a.hq;
+      head[p] = (int)(it - row[p] * a.hq);
+      x[p] = *reinterpret_cast<const uint4*>(a.q + row[p] * a.ldq + head[p] * a.hsq + 8 * l);
+    }
+  }
+  int64_t at = -1;
+  bool use = false;
+#pragma unroll
+  for (int p = 0; p < kQPasses; ++p) {
+    if (row[p] >= 0 && row[p] != at) {
+      at = row[p];
+      bool bad = false;
+      const Seq s = seq_of(a.c, seq_of_row(a.c, at), &bad);
+      use = s.len >= s.rows && at >= s.start && at < (int64_t)s.start + s.rows;
+      if (use) nr.angles(a.cs, a.rot, a.interleaved, (int64_t)s.len - s.rows + (at - s.start));
+      else nr.rot = a.rot, nr.inter = a.interleaved;
+    } else if (row[p] < 0 && at < 0) {
+      nr.rot = a.rot, nr.inter = a.interleaved;
+    }
+    float y[8];
+    unpack8(x[p], y);
+    nr.apply(y);
+    if (row[p] >= 0 && use)
+      *reinterpret_cast<uint4*>(a.qo + row[p] * a.ldo + head[p] * a.hso + 8 * l) =
+          make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
+  }
+}
+
+// Pages that hold new tokens of a sequence.
+__device__ __forceinline__ int touched_pages(const Seq& s, int page_log2) {
+  return s.rows > 0 && s.len >= s.rows ? ((s.len - 1) >> page_log2) - ((s.len - s.rows) >> page_log2) + 1 : 0;
+}
+
+// One unit: the new tokens of one page for one KV head, keys or values.
+template <int LPH, int GT, int ITER>
+__device__ __forceinline__ void append_unit(const AppendArgs& a, int64_t unit, int per_seq, bool scan, float* red) {
+  constexpr int D = 8 * LPH, TPP = GT / LPH;  // tokens a pass
+  const KvArgs& c = a.c;
+  const int g = threadIdx.x % GT, l = g % LPH;
+  const int64_t slot = unit / (2 * c.hkv);
+  const int rest = (int)(unit - slot * (2 * c.hkv));
+  const bool is_v = rest >= c.hkv;
+  const int h = is_v ? rest - c.hkv : rest;
+
+  // the slot's sequence and its page's place among the sequence's touched pages
+  bool bad = false;
+  Seq s = {0, 0, 0};
+  int j = -1, b = 0;
+  if (!scan) {
+    b = (int)(slot / per_seq);
+    if (b >= c.n_seqs) return;
+    s = seq_of(c, b, &bad);
+    j = (int)(slot - (int64_t)b * per_seq);
+    if (s.len < s.rows) bad = true;
+    if (j >= touched_pages(s, c.page_log2)) j = -1;
+  } else {
+    const int lane = threadIdx.x & 31;
+    int64_t left = slot;
+    for (int base = 0; base < c.n_seqs && j < 0; base += 32) {
+      Seq t = {0, 0, 0};
+      bool tb = false;
+      if (base + lane < c.n_seqs) t = seq_of(c, base + lane, &tb);
+      if (t.len < t.rows) tb = true;
+      bad |= tb;
+      const int n = touched_pages(t, c.page_log2);
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const int total = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      if (left < total) {
+        const int who = __ffs(__ballot_sync(0xFFFFFFFFu, sum > left)) - 1;
+        b = base + who;
+        j = (int)left - (__shfl_sync(0xFFFFFFFFu, sum, who) - __shfl_sync(0xFFFFFFFFu, n, who));
+        s.start = __shfl_sync(0xFFFFFFFFu, t.start, who);
+        s.rows = __shfl_sync(0xFFFFFFFFu, t.rows, who);
+        s.len = __shfl_sync(0xFFFFFFFFu, t.len, who);
+      } else {
+        left -= total;
+      }
+    }
+  }
+  if (bad && c.status) atomicExch(c.status, kStatusInvalid);
+  if (j < 0) return;
+  const int P = 1 << c.page_log2, first = s.len - s.rows;
+  const int pi = (first >> c.page_log2) + j;
+  const int id = c.pages[(int64_t)b * c.page_stride + pi];
+  if (id < 0 || id >= c.n_pages) {
+    if (g == 0 && c.status) atomicExch(c.status, kStatusInvalid);
+    return;
+  }
+  const int base = pi << c.page_log2;
+  const int lo = max(first, base), hi = min(s.len, base + P), held = lo - base;
+  float* scale_at = (is_v ? c.vs : c.ks) + (int64_t)id * c.hkv + h;
+  uint8_t* tile = (is_v ? c.v : c.k) + (((int64_t)id * c.hkv + h) << c.page_log2) * D;
+  const float old = held ? *scale_at : 0.0f;
+
+  const uint16_t* src = is_v ? a.vin + (int64_t)h * a.hsv : a.kin + (int64_t)h * a.hsk;
+  const int64_t ld = is_v ? a.ldv : a.ldk;
+  uint4 x[ITER];
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int t = lo + i * TPP + g / LPH;
+    x[i] = t < hi ? *reinterpret_cast<const uint4*>(src + (int64_t)(s.start + (t - first)) * ld + 8 * l)
+                  : make_uint4(0, 0, 0, 0);
+  }
+  float y[ITER][8];
+  float amax = 0.0f;
+  NormRope<LPH> nr;
+  if (!is_v) nr.weights(a.kw, a.woff, a.eps, l);
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    unpack8(x[i], y[i]);
+    if (!is_v && lo + i * TPP < hi) {  // the same for the whole group
+      const int t = min(lo + i * TPP + g / LPH, hi - 1);
+      nr.angles(a.cs, a.rot, a.interleaved, t);
+      nr.apply(y[i]);
+    }
+    if (lo + i * TPP + g / LPH < hi) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float m = fabsf(y[i][e]);
+        amax = fmaxf(amax, m <= 3.402823466e38f ? m : 0.0f);
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+  if (GT > 32) {
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+    __syncthreads();
+    amax = red[0];
+#pragma unroll
+    for (int i = 1; i < GT / 32; ++i) amax = fmaxf(amax, red[i]);
+  }
+  const float need = __int_as_float((scale_exponent(amax) + 127) << 23);
+  const float scale = fmaxf(need, old);
+  if (held && scale > old) {  // the page's older tokens move to the larger scale
+    const float ratio = old / scale;
+    for (int64_t o = (int64_t)g * 8; o < (int64_t)held * D; o += GT * 8) {
+      uint2 w = *reinterpret_cast<const uint2*>(tile + o);
+      uint32_t v[2] = {w.x, w.y};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t u = v[k];
+        v[k] = e4m3x2(e4m3_value(u & 255) * ratio, e4m3_value((u >> 8) & 255) * ratio) |
+               (e4m3x2(e4m3_value((u >> 16) & 255) * ratio, e4m3_value(u >> 24) * ratio) << 16);
+      }
+      *reinterpret_cast<uint2*>(tile + o) = make_uint2(v[0], v[1]);
+    }
+  }
+  if (GT == 32) __syncwarp();     // every thread has read the old scale (a block: before its barrier)
+  if (g == 0) *scale_at = scale;
+  const bool exact = (__float_as_int(scale) & 0x7FFFFF) == 0 && scale >= 0x1p-100f && scale <= 0x1p120f;
+  const float inv = exact ? 1.0f / scale : 0.0f;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int t = lo + i * TPP + g / LPH;
+    if (t >= hi) break;
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float* f = y[i] + 4 * k;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = exact ? f[e] * inv : f[e] / scale;
+      w[k] = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
+    }
+    *reinterpret_cast<uint2*>(tile + (int64_t)(t - base) * D + 8 * l) = make_uint2(w[0], w[1]);
+  }
+}
+
+// Blocks 0 .. kv_blocks-1 take the units, the rest the queries.
+template <int LPH, int GT, int ITER>
+__global__ void __launch_bounds__(GT > kAppendThreads ? GT : kAppendThreads)
+    append_kernel(const AppendArgs a, int64_t units, int64_t kv_blocks, int per_seq, int scan) {
+  __shared__ float red[GT > 32 ? GT / 32 : 1];
+  if ((int64_t)blockIdx.x < kv_blocks) {
+    const int64_t unit = GT == 32 ? (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    if (unit < units) append_unit<LPH, GT, ITER>(a, unit, per_seq, scan != 0, red);
+  } else if (threadIdx.x < kAppendThreads) {
+    append_queries<LPH>(a, (int64_t)blockIdx.x - kv_blocks);
+  }
+}
+
+template <int LPH, int GT, int ITER>
+int launch(const AppendArgs& a, cudaStream_t s) {
+  const KvArgs& c = a.c;
+  const int64_t P = (int64_t)1 << c.page_log2;
+  // a sequence of r new tokens touches at most (r + P - 2) / P + 1 <= r / P + 2 pages
+  const int64_t per = ((int64_t)c.max_new + P - 2) / P + 1;
+  const int64_t direct = (int64_t)c.n_seqs * per, bound = c.n_tokens / P + 2 * (int64_t)c.n_seqs;
+  const bool scan = direct > 2 * bound;  // far fewer pages than slots: find each unit's sequence by a scan
+  const int64_t units = (scan ? bound : direct) * 2 * c.hkv;
+  const int64_t kv_blocks = GT == 32 ? (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : units;
+  const int64_t per_block = kAppendThreads / LPH * kQPasses;
+  const int64_t q_blocks = (c.n_tokens * a.hq + per_block - 1) / per_block;
+  if (kv_blocks + q_blocks > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;
+  append_kernel<LPH, GT, ITER><<<(unsigned)(kv_blocks + q_blocks), std::max(GT, kAppendThreads), 0, s>>>(
+      a, units, kv_blocks, (int)per, scan ? 1 : 0);
+  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+// Threads and passes so that a page's values fit the group's registers.
+template <int LPH>
+int launch_heads(const AppendArgs& a, cudaStream_t s) {
+  if (a.c.max_new <= kWarpRows) return launch<LPH, 32, kWarpRows * LPH / 32>(a, s);
+  const int passes = ((LPH << a.c.page_log2) + kAppendThreads - 1) / kAppendThreads;
+  if (passes <= 1) return launch<LPH, 256, 1>(a, s);
+  if (passes <= 2) return launch<LPH, 256, 2>(a, s);
+  if (passes <= 4) return launch<LPH, 256, 4>(a, s);
+  if (passes <= 8) return launch<LPH, 256, 8>(a, s);
+  return launch<LPH, 512, 8>(a, s);
+}
+
+}  // namespace
+
+int launch_append(const AppendArgs& a, int head_dim, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (head_dim) {
+    case 64: return launch_heads<8>(a, s);
+    case 128: return launch_heads<16>(a, s);
+    case 256: return launch_heads<32>(a, s);
+  }
+  return QG_ERR_UNSUPPORTED;
+}
+
+}  // namespace qg

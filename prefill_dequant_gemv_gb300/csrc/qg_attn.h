@@ -1,0 +1,84 @@
+// Shared by the cache append and the attention kernels: kernel arguments, the device-side
+// reading of a batch's sequences, and E4M3 helpers.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "qg_internal.h"
+
+namespace qg {
+
+// What the kernels need of a cache and a batch.
+struct KvArgs {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int64_t n_pages;
+  int hkv, page_log2;
+  const int32_t* q_start;
+  const int32_t* lens;
+  const int32_t* pages;
+  int64_t page_stride;
+  int n_seqs, max_new;
+  int64_t max_len, n_tokens;
+  int* status;
+};
+
+struct AppendArgs {
+  KvArgs c;
+  const uint16_t* q;
+  const uint16_t* kin;
+  const uint16_t* vin;
+  uint16_t* qo;
+  int64_t ldq, hsq, ldk, hsk, ldv, hsv, ldo, hso;
+  const uint16_t* qw;
+  const uint16_t* kw;
+  const float* cs;
+  float eps, woff;
+  int hq, rot, interleaved;
+};
+
+struct AttnArgs {
+  KvArgs c;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t ldq, hsq, ldo, hso;
+  float scale;
+  int64_t window;  // 0: none
+  int hq;
+};
+
+// How qattn divides the work; a function of the sizes alone.
+struct AttnPlan {
+  size_t ws_bytes;
+};
+bool plan_attn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int hq, const DeviceInfo& dev,
+               AttnPlan* p);
+int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan& p, void* ws, void* stream);
+int launch_append(const AppendArgs& a, int head_dim, void* stream);
+
+#ifdef __CUDACC__
+// Sequence b's first row, number of rows and length.  A sequence outside the call's bounds
+// has no rows.
+struct Seq {
+  int start, rows, len;
+};
+__device__ __forceinline__ Seq seq_of(const KvArgs& c, int b, bool* bad) {
+  Seq s;
+  const int s0 = c.q_start[b], s1 = c.q_start[b + 1];
+  s.len = c.lens[b];
+  s.start = s0;
+  s.rows = s1 - s0;
+  if (s0 < 0 || s1 < s0 || s1 > c.n_tokens || s1 - s0 > c.max_new || s.len < 0 || s.len > c.max_len) {
+    s.start = 0;
+    s.rows = 0;
+    s.len = 0;
+    *bad = true;
+  }
+  return s;
+}
+#endif
+
+}  // namespace qg

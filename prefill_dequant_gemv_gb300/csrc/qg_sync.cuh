@@ -12,6 +12,7 @@ namespace qg {
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kStatusTimeout = 6;                           // QG_ERR_TIMEOUT
 constexpr int kStatusUnsupported = 2;                       // QG_ERR_UNSUPPORTED
+constexpr int kStatusInvalid = 1;                           // QG_ERR_INVALID_ARG
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
