@@ -80,12 +80,15 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
 
 }  // namespace
 
-bool plan_attn(const qg_kv_cache*, const qg_kv_batch*, int64_t, int, const DeviceInfo&, AttnPlan* p) {
-  p->ws_bytes = kWsHeader;
+bool plan_attn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t, int hq, const DeviceInfo& dev, AttnPlan* p) {
+  const int64_t rows = (int64_t)batch->max_new * (hq / cache->n_kv_heads);
+  p->decode = decode_rows(rows) != 0;
+  p->ws_bytes = p->decode ? decode_workspace(rows, cache->head_dim, dev) : kWsHeader;
   return true;
 }
 
-int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan&, void*, void* stream) {
+int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan& p, const DeviceInfo& dev, void* ws, void* stream) {
+  if (p.decode) return launch_attn_decode(a, head_dim, (int64_t)a.c.max_new * (a.hq / a.c.hkv), dev, ws, stream);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const dim3 grid((unsigned)a.c.n_tokens, (unsigned)a.hq);
   switch (head_dim) {

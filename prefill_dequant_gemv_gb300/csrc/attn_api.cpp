@@ -188,5 +188,5 @@ extern "C" qg_status qattn(const qg_kv_cache* cache, const qg_kv_batch* batch, i
   a.scale = scale;
   a.window = window;
   a.hq = n_q_heads;
-  return (qg_status)launch_attn(a, cache->head_dim, p, workspace, stream);
+  return (qg_status)launch_attn(a, cache->head_dim, p, dev, workspace, stream);
 }

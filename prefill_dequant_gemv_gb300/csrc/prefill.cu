@@ -28,6 +28,7 @@
 
 #include "qg_common.cuh"
 #include "qg_decode_tile.cuh"
+#include "qg_attn.h"
 #include "qg_internal.h"
 #include "qg_sync.cuh"
 #include "qg_tc.cuh"
@@ -311,6 +312,18 @@ bool encode_token_rows(CUtensorMap* map, const void* x, int64_t rows, int64_t k,
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_pages(CUtensorMap* map, const void* codes, int head_dim, int page_tokens, int64_t tiles, int box_tokens) {
+  EncodeFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)head_dim, (cuuint64_t)page_tokens, (cuuint64_t)tiles};
+  const cuuint64_t strides[2] = {(cuuint64_t)head_dim, (cuuint64_t)head_dim * page_tokens};
+  const cuuint32_t box[3] = {(cuuint32_t)(head_dim < 128 ? head_dim : 128), (cuuint32_t)box_tokens, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(codes), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, head_dim < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int launch_prefill(const Geometry& g, const qg_weight* w, const void* x, int64_t t, int64_t ldx, const void* res,

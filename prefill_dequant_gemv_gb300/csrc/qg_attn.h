@@ -53,10 +53,18 @@ struct AttnArgs {
 // How qattn divides the work; a function of the sizes alone.
 struct AttnPlan {
   size_t ws_bytes;
+  bool decode;  // few rows a KV head: the streaming kernel
 };
 bool plan_attn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int hq, const DeviceInfo& dev,
                AttnPlan* p);
-int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan& p, void* ws, void* stream);
+int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan& p, const DeviceInfo& dev, void* ws, void* stream);
+// The streaming kernel of up to 64 rows (new tokens x query heads a KV head).
+int decode_rows(int64_t rows);  // the row count it is built for: 16, 32, 64; 0: too many
+size_t decode_workspace(int64_t rows, int head_dim, const DeviceInfo& dev);
+int launch_attn_decode(const AttnArgs& a, int head_dim, int64_t rows, const DeviceInfo& dev, void* ws, void* stream);
+// Pages of codes as a 3-D TMA tensor (head_dim bytes x page_tokens x tiles, tile = page * n_kv_heads +
+// head): box of min(head_dim, 128) bytes x box_tokens tokens, swizzled by its width.
+bool encode_pages(CUtensorMap* map, const void* codes, int head_dim, int page_tokens, int64_t tiles, int box_tokens);
 int launch_append(const AppendArgs& a, int head_dim, void* stream);
 
 #ifdef __CUDACC__
