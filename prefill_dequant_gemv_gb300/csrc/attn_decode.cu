@@ -23,9 +23,12 @@
 //   * The pairs' keys, in tiles of 128, lie on one line, which the CTAs (one an SM) share out evenly
 //     whatever the lengths; a pair cut between CTAs leaves partial (m, l, O) rows in the workspace, and the
 //     CTA that finishes last adds them in order.  One launch.
-//   * warp 5 copies tiles into a ring by TMA, warps 6-7 bring a pair's query rows, warp 4 issues the MMAs, and
-//     warps 0-3 turn S into P, a key a thread: its column of R scores comes from tensor memory, its terms
-//     go to shared memory as 16-byte rows.  The sums of P stay per thread until the pair ends.
+//   * One warp copies tiles into a ring by TMA, two bring a pair's query rows, one issues the MMAs, and
+//     groups of four warps turn S into P, a key a thread: its column of R scores comes from tensor
+//     memory, its terms go to shared memory as 16-byte rows.  The sums of P stay per thread until the
+//     pair ends.  A tile's way through these steps is a chain of about 2500 cycles, several
+//     times what its bytes take to arrive; so several groups work on
+//     as many tiles at once, each with its own reference and accumulators, joined at the pair's end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -40,7 +43,6 @@
 namespace qg {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kTile = 128;           // keys a tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 2.0f;        // P of a key at the reference is 2^2 ...
@@ -49,38 +51,38 @@ constexpr float kHead = 6.5f;        // ... and at most 2^8.5, below E4M3's 448
 // D: head dimension; N: rows it is built for (16, 32, 64).
 template <int D, int N>
 struct Cfg {
+  // softmax groups of 128 threads (heads of 256: as many as the ring has stages)
+  static constexpr int GROUPS = D == 256 && N == 16 ? 2 : 64 / N;
+  static constexpr int THREADS = 128 * GROUPS + 128;
   static constexpr int PW = D < 128 ? D : 128;       // bytes of a panel row (a TMA box row)
   static constexpr int NP = D / PW;                  // panels
   static constexpr int PANEL = kTile * PW;
   static constexpr int KV = kTile * D;               // bytes of a key (or value) tile
   static constexpr int Q = 2 * N * D;                // both terms of the query rows
   static constexpr int QPANEL = 2 * N * PW;
-  static constexpr int P = 3 * N * kTile;
-  static constexpr bool BIG = D == 256 && N == 64;   // tensor and shared memory for one buffer of S, Q and P
-  static constexpr int B = BIG ? 1 : 2;
+  static constexpr int QB = GROUPS + 1;              // buffers of them: scores run GROUPS tiles (and pairs) ahead
+  static constexpr int P = 3 * N * kTile;            // a group's terms of P
   static constexpr int MB = NP;                      // M blocks of O (128 dims; D = 64 fills half of one)
-  static constexpr int SCOL = 2 * N, OCOL = 3 * N;   // TMEM columns of an S buffer and of a block of O
+  static constexpr int SCOL = 2 * N, OCOL = 3 * N;   // TMEM columns of a group's S and of a block of its O
   static constexpr int STAGE = 2 * KV;
-  static constexpr int FIXED = 1024 + B * (Q + P) + 8192;
+  static constexpr int FIXED = 1024 + QB * Q + GROUPS * P + 8192;
   static constexpr int S0 = (232448 - FIXED) / STAGE;
   static constexpr int S = S0 > 8 ? 8 : S0;
   static constexpr int SMEM = FIXED + S * STAGE;
-  static_assert(S >= 2 && B * SCOL + MB * OCOL <= 512, "shared and tensor memory");
+  static_assert(S >= 2 && S >= GROUPS && GROUPS * (SCOL + MB * OCOL) <= 512, "shared and tensor memory");
 };
 
 // What a stage holds.
 struct TileMeta {
-  int first, last;      // of its pair in this CTA
-  int tok0, len;
-  int cut, pad[3];      // cut: some of its rows hold no key
-  float ks[8], vs[8];   // scales of its groups of 16 keys; 0: the group holds no key
+  int tok0, len, after;  // after: tiles of its pair in this CTA before it
+  int flags;             // 1: some of its rows hold no key; 2: some row of the pair does not see all of it
+  float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
 };
 // What a query buffer holds besides the rows.
 struct PairMeta {
-  int R, len, h, start;
-  int n_tiles, low, high, pad;  // low, high: least and largest position of its rows
-  int64_t first;                // the pair's first tile on the line
-  int64_t pad2;
+  int R, h, start, n_tiles;
+  int i0, i1, pad[2];           // its tiles in this CTA
+  int64_t first, pad2;          // its first tile on the line
   float rc[64];                 // the row's power of two * scale * log2(e)
   int pos[64];
 };
@@ -88,14 +90,15 @@ template <int D, int N>
 struct Shared {
   using C = Cfg<D, N>;
   TileMeta tile[C::S];
-  PairMeta pair[C::B];
-  alignas(16) float ref[64];
-  float grow[64];
-  float red[4][64];
+  PairMeta pair[C::QB];
+  alignas(16) float ref[C::GROUPS][N];
+  float grow[C::GROUPS][N], sum[C::GROUPS][N], red[C::GROUPS][4][N];
   uint64_t kfull[C::S], vfull[C::S], empty[C::S];
-  uint64_t qfull[C::B], qfree[C::B], sfull[C::B], sfree[C::B], pfull[C::B], pvdone[C::B], ended;
+  uint64_t qfull[C::QB], qfree[C::QB];
+  uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
+  uint64_t summed, joined, ended;
   uint32_t tmem;
-  int ticket;
+  int ticket[C::GROUPS];
 };
 
 struct DecodeArgs {
@@ -159,15 +162,30 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
       "r"((uint32_t)acc)
       : "memory");
 }
-// Barrier of the four softmax warps that returns whether any thread's v is set.
-__device__ __forceinline__ bool any_of_128(bool v) {
+// Barrier of a softmax group's four warps that returns whether any thread's v is set.
+__device__ __forceinline__ bool any_of(int group, bool v) {
   uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)v)
+      : "r"(1 + group), "r"((uint32_t)v)
       : "memory");
   return r != 0;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 // First key that any row of the sequence sees, rounded down to a page; tiles of a pair (one at least where
@@ -180,11 +198,30 @@ __device__ __forceinline__ int tiles_of(const Seq& s, const AttnArgs& a) {
   return s.rows > 0 ? max(1, (s.len - first_key(s, a) + kTile - 1) / kTile) : 0;
 }
 
-// A place on the line: tile k of head h of sequence b, whose pairs have n tiles.  A whole warp walks.
+// A place on the line: tile k of head h of sequence b, whose pairs have n tiles.  A whole warp walks; lane
+// b holds sequence b of the first 32.
 struct Walk {
   int b, h, k, n, lo;
-  Seq sq;
+  Seq sq, mine;
 
+  // tiles of all sequences, each counted once (all its KV heads have as many)
+  __device__ __forceinline__ int64_t count(const AttnArgs& a, int lane, bool* bad) {
+    const KvArgs& c = a.c;
+    mine = {0, 0, 0};
+    if (lane < c.n_seqs) mine = seq_of(c, lane, bad);
+    int64_t total = __reduce_add_sync(0xFFFFFFFFu, tiles_of(mine, a));
+    for (int base = 32; base < c.n_seqs; base += 32) {
+      int t = 0;
+      if (base + lane < c.n_seqs) t = tiles_of(seq_of(c, base + lane, bad), a);
+      total += __reduce_add_sync(0xFFFFFFFFu, t);
+    }
+    return total;
+  }
+  __device__ __forceinline__ void take(const Seq& t, int who) {
+    sq.start = __shfl_sync(0xFFFFFFFFu, t.start, who);
+    sq.rows = __shfl_sync(0xFFFFFFFFu, t.rows, who);
+    sq.len = __shfl_sync(0xFFFFFFFFu, t.len, who);
+  }
   __device__ __forceinline__ void find(const AttnArgs& a, int64_t unit, int lane) {
     const KvArgs& c = a.c;
     int64_t left = unit;
@@ -192,8 +229,11 @@ struct Walk {
     b = 0, n = 1;
     sq = {0, 0, 0};
     for (int base = 0; base < c.n_seqs; base += 32) {
-      Seq t = {0, 0, 0};
-      if (base + lane < c.n_seqs) t = seq_of(c, base + lane, &ignore);
+      Seq t = mine;
+      if (base) {
+        t = {0, 0, 0};
+        if (base + lane < c.n_seqs) t = seq_of(c, base + lane, &ignore);
+      }
       const int un = tiles_of(t, a);
       int64_t sum = (int64_t)un * c.hkv;
 #pragma unroll
@@ -207,9 +247,7 @@ struct Walk {
         b = base + who;
         n = __shfl_sync(0xFFFFFFFFu, un, who);
         left -= __shfl_sync(0xFFFFFFFFu, sum, who) - (int64_t)n * c.hkv;
-        sq.start = __shfl_sync(0xFFFFFFFFu, t.start, who);
-        sq.rows = __shfl_sync(0xFFFFFFFFu, t.rows, who);
-        sq.len = __shfl_sync(0xFFFFFFFFu, t.len, who);
+        take(t, who);
         break;
       }
       left -= all;
@@ -226,7 +264,10 @@ struct Walk {
       h = 0;
       do {
         ++b;
-        sq = seq_of(a.c, b, &ignore);
+        if (b < 32)
+          take(mine, b);
+        else
+          sq = seq_of(a.c, b, &ignore);
         n = tiles_of(sq, a);
       } while (n == 0);
       lo = first_key(sq, a);
@@ -234,54 +275,83 @@ struct Walk {
   }
 };
 
+// The joining of a pair's parts by the CTA that finished last: one group's 128 threads.
 template <int D, int N>
-__global__ void __launch_bounds__(kThreads, 1)
+__device__ __forceinline__ void join_parts(const DecodeArgs& da, int tid, int R, int G, int start, int h, int64_t c0,
+                                           int parts, bool at_start) {
+  const AttnArgs& a = da.a;
+  for (int e = tid; e < R * (D / 4); e += 128) {
+    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+    float4 v = make_float4(0, 0, 0, 0);
+    float top = -INFINITY, sum = 0.0f;
+    for (int q = 0; q < parts; ++q) {
+      const int64_t sl = 2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0);
+      top = fmaxf(top, __ldcg(&da.part_ml[sl * N + row]).x);
+    }
+#pragma unroll 4
+    for (int q = 0; q < parts; ++q) {
+      const int64_t sl = 2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0);
+      const float2 z = __ldcg(&da.part_ml[sl * N + row]);
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(da.part_o + (sl * N + row) * D + d));
+      const float f = z.x == -INFINITY ? 0.0f : ex2(z.x - top);
+      v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+      sum = fmaf(z.y, f, sum);
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int t = row / G, g = row - t * G;
+    const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), y1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
+    *reinterpret_cast<uint2*>(a.out + (int64_t)(start + t) * a.ldo + (int64_t)(h * G + g) * a.hso + d) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+  }
+}
+
+template <int D, int N>
+__global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const DecodeArgs da) {
   using C = Cfg<D, N>;
+  constexpr int NG = C::GROUPS, kMma = 4 * NG;
   static_assert(sizeof(Shared<D, N>) <= 8192, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = ring + C::S * C::STAGE;
-  uint8_t* pbuf = qbuf + C::B * C::Q;
-  Shared<D, N>& sh = *reinterpret_cast<Shared<D, N>*>(pbuf + C::B * C::P);
+  uint8_t* pbuf = qbuf + C::QB * C::Q;
+  Shared<D, N>& sh = *reinterpret_cast<Shared<D, N>*>(pbuf + NG * C::P);
   const AttnArgs& a = da.a;
   const KvArgs& c = a.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.hq / c.hkv;
 
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     for (int s = 0; s < C::S; ++s) {
       mbar_init(&sh.kfull[s], 16);
       mbar_init(&sh.vfull[s], 8);
       mbar_init(&sh.empty[s], 1);
     }
-    for (int i = 0; i < C::B; ++i) {
+    for (int i = 0; i < C::QB; ++i) {
       mbar_init(&sh.qfull[i], 64);
       mbar_init(&sh.qfree[i], 1);
+    }
+    for (int i = 0; i < NG; ++i) {
       mbar_init(&sh.sfull[i], 1);
       mbar_init(&sh.sfree[i], 128);
       mbar_init(&sh.pfull[i], 128);
       mbar_init(&sh.pvdone[i], 1);
     }
+    mbar_init(&sh.summed, NG);
+    mbar_init(&sh.joined, 1);
     mbar_init(&sh.ended, 1);
     fence_mbar_init();
   }
-  if (warp == 4) {
+  if (warp == kMma) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
   pdl_wait();
-  // the line: tiles of all sequences, each counted once (all its KV heads have as many)
-  int64_t total = 0;
+  Walk w;
   bool bad = false;
-  for (int base = 0; base < c.n_seqs; base += 32) {
-    int n = 0;
-    if (base + lane < c.n_seqs) n = tiles_of(seq_of(c, base + lane, &bad), a);
-    total += __reduce_add_sync(0xFFFFFFFFu, n);
-  }
+  const int64_t total = w.count(a, lane, &bad) * c.hkv;
   if (bad && warp == 0 && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
-  total *= c.hkv;
   // with no more CTAs than tiles, each has one at least
   const int64_t grid = min((int64_t)gridDim.x, total), cta = blockIdx.x;
   const int64_t u0 = cta < grid ? cta * total / grid : 0, u1 = cta < grid ? (cta + 1) * total / grid : 0;
@@ -290,94 +360,108 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const int n = (int)(u1 - u0);
-  const uint32_t otm = tmem + C::B * C::SCOL;
+  const uint32_t otm = tmem + NG * C::SCOL;  // the groups' O follow their S
 
-  if (n > 0 && warp == 5) {  // ------------------------------------------------------------ key and value tiles
-    Walk w;
+  if (n > 0 && warp == kMma + 1) {  // ------------------------------------------------------ key and value tiles
+    // Lanes 8q .. 8q + 7 look after tile 4j + q: its eight groups of 16 keys.  Four tiles' page ids are
+    // fetched by one load, while the four before them are issued.
     w.find(a, u0, lane);
     const int P = 1 << c.page_log2, box = min(P, kTile);
-    // this lane's group of 16 keys: its page id (-1: no such keys)
-    auto page_of = [&]() {
-      const int64_t tok = (int64_t)w.lo + (int64_t)w.k * kTile + 16 * lane;
-      return lane < 8 && tok < w.sq.len ? c.pages[(int64_t)w.b * c.page_stride + (tok >> c.page_log2)] : -1;
+    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, edge = 0, walked = 0, i0 = 0;
+    auto prepare = [&]() {  // the next four tiles
+      int b = 0;
+      len = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (walked < n) {
+          if (lane >> 3 == q) {
+            b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + w.k * kTile, after = walked - i0;
+            // the rows stand at len - rows .. len - 1
+            edge = tok0 + kTile - 1 > len - w.sq.rows || (a.window && tok0 <= (int64_t)len - 1 - a.window);
+          }
+          if (++walked < n && ++w.k == w.n) {
+            w.next_pair(a);
+            i0 = walked;
+          }
+        }
+      }
+      const int64_t tok = (int64_t)tok0 + 16 * (lane & 7);
+      id = -1;
+      if (tok < len) id = c.pages[(int64_t)b * c.page_stride + (tok >> c.page_log2)];
     };
-    int id = page_of();
+    prepare();
     bool dead = false;
-    int s = 0;
+    int s = 0, i = 0;
     uint32_t lap = 0;
-    int i = 0;
-    for (; i < n; ++i) {
-      // this tile's data, and the next one's page id on its way
-      const int tok0 = w.lo + w.k * kTile, head = w.h, cid = id, len = w.sq.len;
-      const bool first = w.k == 0 || i == 0, last = w.k == w.n - 1 || i == n - 1;
-      if (i + 1 < n) {
-        if (++w.k == w.n) w.next_pair(a);
-        id = page_of();
-      }
-      if (lap && !mbar_wait_bounded(&sh.empty[s], (lap - 1) & 1, c.status)) dead = true;
-      if (__any_sync(0xFFFFFFFFu, dead)) break;
-      TileMeta& m = sh.tile[s];
-      const int tok = tok0 + 16 * lane;
-      bool ok = lane < 8 && tok < len;
-      if (ok && (cid < 0 || cid >= c.n_pages)) {
-        ok = false;
-        atomicExch(c.status, kStatusInvalid);
-      }
-      const bool cut = __any_sync(0xFFFFFFFFu, lane < 8 && (!ok || tok + 16 > len));
-      if (lane == 0) {
-        m.first = first, m.last = last, m.tok0 = tok0, m.len = len, m.cut = cut;
-      }
-      if (lane < 8) {
-        uint8_t* kd = ring + s * C::STAGE + 16 * lane * C::PW;
-        const int64_t tile = (int64_t)cid * c.hkv + head;
-        const bool lead = ok && (16 * lane) % box == 0;
-        if (ok) {
-          cp_async4(&m.ks[lane], c.ks + tile);
-          cp_async4(&m.vs[lane], c.vs + tile);
-        } else {
-          m.ks[lane] = 0.0f;
-          m.vs[lane] = 0.0f;
+    while (i < n && !dead) {
+      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge;
+      if (walked < n) prepare();
+      for (int q = 0; q < 4 && i < n; ++q, ++i) {
+        if (lap && !mbar_wait_bounded(&sh.empty[s], (lap - 1) & 1, c.status)) dead = true;
+        if (__any_sync(0xFFFFFFFFu, dead)) {
+          dead = true;
+          break;
         }
-        if (lead) {
-          mbar_arrive_expect_tx(&sh.kfull[s], box * D);
-          mbar_arrive_expect_tx(&sh.vfull[s], box * D);
+        if (lane >> 3 == q) {
+          TileMeta& m = sh.tile[s];
+          const int gl = lane & 7, tok = ctok0 + 16 * gl;
+          bool ok = tok < clen;
+          if (ok && (cid < 0 || cid >= c.n_pages)) {
+            ok = false;
+            atomicExch(c.status, kStatusInvalid);
+          }
+          const bool cut = __any_sync(0xFFu << (8 * q), !ok || tok + 16 > clen);
+          if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = (cut ? 3 : 0) | (cedge ? 2 : 0);
+          uint8_t* kd = ring + s * C::STAGE + 16 * gl * C::PW;
+          const int64_t tile = (int64_t)cid * c.hkv + chead;
+          if (ok && (16 * gl) % box == 0) {
+            mbar_arrive_expect_tx(&sh.kfull[s], box * D);
 #pragma unroll
-          for (int x = 0; x < C::NP; ++x)
-            tma_load_3d(kd + x * C::PANEL, &kmap, x * 128, tok & (P - 1), (int)tile, &sh.kfull[s]);
+            for (int x = 0; x < C::NP; ++x)
+              tma_load_3d(kd + x * C::PANEL, &kmap, x * 128, tok & (P - 1), (int)tile, &sh.kfull[s]);
+            mbar_arrive_expect_tx(&sh.vfull[s], box * D);
 #pragma unroll
-          for (int x = 0; x < C::NP; ++x)
-            tma_load_3d(kd + C::KV + x * C::PANEL, &vmap, x * 128, tok & (P - 1), (int)tile, &sh.vfull[s]);
-        } else {
-          mbar_arrive(&sh.kfull[s]);
-          mbar_arrive(&sh.vfull[s]);
+            for (int x = 0; x < C::NP; ++x)
+              tma_load_3d(kd + C::KV + x * C::PANEL, &vmap, x * 128, tok & (P - 1), (int)tile, &sh.vfull[s]);
+          } else {
+            mbar_arrive(&sh.kfull[s]);
+            mbar_arrive(&sh.vfull[s]);
+          }
+          if (ok) {
+            cp_async4(&m.ks[gl], c.ks + tile);
+            cp_async4(&m.vs[gl], c.vs + tile);
+          } else {
+            m.ks[gl] = 0.0f;
+            m.vs[gl] = 0.0f;
+          }
+          cp_async_arrive_noinc(&sh.kfull[s]);
         }
-        cp_async_arrive_noinc(&sh.kfull[s]);
+        __syncwarp();
+        if (++s == C::S) s = 0, ++lap;
       }
-      __syncwarp();
-      if (++s == C::S) s = 0, ++lap;
     }
     // no copy is left in flight into this CTA's shared memory when it ends: the last stages filled
     for (int j = max(0, i - C::S); j < i; ++j) {
       mbar_wait_bounded(&sh.kfull[j % C::S], (uint32_t)(j / C::S) & 1u, c.status);
       mbar_wait_bounded(&sh.vfull[j % C::S], (uint32_t)(j / C::S) & 1u, c.status);
     }
-  } else if (n > 0 && warp >= 6) {  // ------------------------------------------------------ query rows
+  } else if (n > 0 && warp >= kMma + 2) {  // ----------------------------------------------- query rows
     // 64 threads: D / 16 of them a row, 16 elements each
     constexpr int TPR = D / 16, RPP = 64 / TPR;
-    const int t = tid - 192, part = t % TPR;
-    Walk w;
+    const int t = threadIdx.x - 32 * (kMma + 2), part = t % TPR;
     w.find(a, u0, lane);
     int64_t u = u0;
     bool dead = false;
     for (int p = 0; u < u1; ++p) {
-      const int qb = p % C::B;
-      if (p >= C::B && !mbar_wait_bounded(&sh.qfree[qb], (uint32_t)(p / C::B - 1) & 1u, c.status)) dead = true;
+      const int qb = p % C::QB;
+      if (p >= C::QB && !mbar_wait_bounded(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
       if (__any_sync(0xFFFFFFFFu, dead)) break;
       PairMeta& m = sh.pair[qb];
       const int R = min(w.sq.rows * G, N), first_pos = w.sq.len - w.sq.rows;
+      const int64_t next = u + w.n - w.k;
       if (t == 0) {
-        m.R = R, m.len = w.sq.len, m.h = w.h, m.start = w.sq.start, m.n_tiles = w.n;
-        m.low = first_pos, m.high = w.sq.len - 1, m.first = u - w.k;
+        m.R = R, m.h = w.h, m.start = w.sq.start, m.n_tiles = w.n, m.first = u - w.k;
+        m.i0 = (int)(u - u0), m.i1 = (int)(min(next, u1) - u0);
       }
       uint8_t* qd = qbuf + qb * C::Q;
       for (int r0 = 0; r0 < N; r0 += RPP) {
@@ -434,42 +518,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       mbar_arrive(&sh.qfull[qb]);
-      u += w.n - w.k;
+      u = next;
       if (u < u1) w.next_pair(a);
     }
-  } else if (n > 0 && warp == 4) {  // ------------------------------------------------------ MMAs
+  } else if (n > 0 && warp == kMma) {  // ---------------------------------------------------- MMAs
     constexpr uint32_t kSwz = D == 64 ? 4 : 2;
     constexpr uint32_t kSbo = 8 * C::PW;
     constexpr uint32_t kQk = idesc_e4m3(2 * N, 0, 0), kPv = idesc_e4m3(3 * N, 1, 1);
     int p = -1;  // pairs begun by the score MMAs
     auto scores = [&](int i) {
-      const int s = i % C::S, sb = i % C::B;
+      const int s = i % C::S, g = i % NG;
       if (!mbar_wait_bounded(&sh.kfull[s], (uint32_t)(i / C::S) & 1u, c.status)) return false;
-      if (sh.tile[s].first) {
+      if (sh.tile[s].after == 0) {
         ++p;
-        if (!mbar_wait_bounded(&sh.qfull[p % C::B], (uint32_t)(p / C::B) & 1u, c.status)) return false;
+        if (!mbar_wait_bounded(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) return false;
       }
-      if (i >= C::B && !mbar_wait_bounded(&sh.sfree[sb], (uint32_t)(i / C::B - 1) & 1u, c.status)) return false;
+      if (i >= NG && !mbar_wait_bounded(&sh.sfree[g], (uint32_t)(i / NG - 1) & 1u, c.status)) return false;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t ka = smem_u32(ring + s * C::STAGE), qa = smem_u32(qbuf + (p % C::B) * C::Q);
+        const uint32_t ka = smem_u32(ring + s * C::STAGE), qa = smem_u32(qbuf + (p % C::QB) * C::Q);
 #pragma unroll
         for (int x = 0; x < D / 32; ++x) {
           const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
-          mma_e4m3(tmem + sb * C::SCOL, mat_desc(ka + panel * C::PANEL + off, 16, kSbo, kSwz),
+          mma_e4m3(tmem + g * C::SCOL, mat_desc(ka + panel * C::PANEL + off, 16, kSbo, kSwz),
                    mat_desc(qa + panel * C::QPANEL + off, 16, kSbo, kSwz), kQk, x > 0);
         }
-        mma_commit(&sh.sfull[sb]);
+        mma_commit(&sh.sfull[g]);
       }
       __syncwarp();
       return true;
     };
     auto outputs = [&](int i) {
-      const int s = i % C::S, pb = i % C::B;
+      const int s = i % C::S, g = i % NG;
       if (!mbar_wait_bounded(&sh.vfull[s], (uint32_t)(i / C::S) & 1u, c.status)) return false;
       const TileMeta& m = sh.tile[s];
       uint8_t* vt = ring + s * C::STAGE + C::KV;
-      if (m.cut) {  // rows without a key hold anything, NaN codes too: they must be numbers for P = 0
+      if (m.flags & 1) {  // rows without a key hold anything, NaN codes too: they must be numbers for P = 0
         for (int r = lane; r < kTile; r += 32) {
           if (m.tok0 + r >= m.len || m.ks[r >> 4] == 0.0f) {
 #pragma unroll 1
@@ -482,11 +566,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      if (!mbar_wait_bounded(&sh.pfull[pb], (uint32_t)(i / C::B) & 1u, c.status)) return false;
+      if (!mbar_wait_bounded(&sh.pfull[g], (uint32_t)(i / NG) & 1u, c.status)) return false;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t va = smem_u32(vt), pa = smem_u32(pbuf + pb * C::P);
-        const bool first = m.first;
+        const uint32_t va = smem_u32(vt), pa = smem_u32(pbuf + g * C::P), od = otm + g * (C::MB * C::OCOL);
+        const bool first = m.after < NG;  // the group's first tile of the pair
 #pragma unroll
         for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
@@ -494,213 +578,265 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
             // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
             // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
-            mma_e4m3(otm + mb * C::OCOL, mat_desc(va + mb * C::PANEL + x * 32 * C::PW, C::PANEL, kSbo, kSwz),
+            mma_e4m3(od + mb * C::OCOL, mat_desc(va + mb * C::PANEL + x * 32 * C::PW, C::PANEL, kSbo, kSwz),
                      mat_desc(pa + x * 32 * 16, 128, kTile * 16, 0), kPv, !(first && x == 0));
           }
-        mma_commit(&sh.pvdone[pb]);
+        mma_commit(&sh.pvdone[g]);
         mma_commit(&sh.empty[s]);
       }
       __syncwarp();
       return true;
     };
-    bool go = scores(0);
-    for (int i = 0; i < n && go; ++i) go = (i + 1 == n || scores(i + 1)) && outputs(i);
+    // scores run NG tiles ahead of outputs, so that every group has its next tile's at hand
+    bool go = true;
+    for (int i = 0; i < min(n, NG) && go; ++i) go = scores(i);
+    for (int i = 0; i < n && go; ++i) go = outputs(i) && (i + NG >= n || scores(i + NG));
     // every MMA has ended before the CTA's memory goes
     if (lane == 0) {
       mma_commit(&sh.ended);
       mbar_wait_bounded(&sh.ended, 0, c.status);
     }
     __syncwarp();
-  } else if (n > 0 && warp < 4) {  // ------------------------------------------------------- softmax, a key a thread
-    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
-    float l[N];
-    int p = -1;
+  } else if (n > 0 && warp < kMma) {  // ------------------------------------------------------ softmax, a key a thread
+    const int grp = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
+    const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+    const uint32_t st = tmem + lane_base + grp * C::SCOL, ot = otm + lane_base + grp * (C::MB * C::OCOL);
+    float* ref = sh.ref[grp];
+    float* grow = sh.grow[grp];
+    uint8_t* pd = pbuf + grp * C::P + tid * 16;
     bool dead = false;
-    for (int i = 0; i < n; ++i) {
-      const int s = i % C::S, sb = i % C::B;
-      if (!mbar_wait_bounded(&sh.kfull[s], (uint32_t)(i / C::S) & 1u, c.status)) dead = true;
-      const TileMeta& tm = sh.tile[s];
-      const bool first = tm.first, last = tm.last;
-      if (first && !dead) {
-        ++p;
-        if (!mbar_wait_bounded(&sh.qfull[p % C::B], (uint32_t)(p / C::B) & 1u, c.status)) dead = true;
+    int i1 = 0, s = grp % C::S;
+    uint32_t turn = 0, kpar = (grp / C::S) & 1;  // tiles of this group so far; parity of its next key tile
+    for (int p = 0; i1 < n; ++p) {
+      const PairMeta& pm = sh.pair[p % C::QB];
+      if (!mbar_wait_bounded(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) dead = true;
+      if (any_of(grp, dead)) break;
+      const int R = pm.R, i0 = pm.i0;
+      i1 = pm.i1;
+      float l[N];
 #pragma unroll
-        for (int r = 0; r < N; ++r) l[r] = 0.0f;
-      }
-      const PairMeta& pm = sh.pair[max(p, 0) % C::B];
-      const int R = pm.R;
-      if (!dead && !mbar_wait_bounded(&sh.sfull[sb], (uint32_t)(i / C::B) & 1u, c.status)) dead = true;
-      tc_fence_after();
-      // the key's scores: both terms of every row
-      float x[N];
+      for (int r = 0; r < N; ++r) l[r] = 0.0f;
+      const int mine = i0 + (grp - i0 % NG + NG) % NG;  // this group's first tile of the pair, if it has one
+      for (int i = mine; i < i1; i += NG) {
+        const bool first = i == mine;
+        if (!mbar_wait_bounded(&sh.kfull[s], kpar, c.status)) dead = true;
+        const TileMeta& tm = sh.tile[s];
+        if (!mbar_wait_bounded(&sh.sfull[grp], turn & 1, c.status)) dead = true;
+        tc_fence_after();
+        // the key's scores: both terms of every row
+        float x[N];
 #pragma unroll
-      for (int r = 0; r < N; r += 16) {
-        if (r < R) {
-          uint32_t u[16], v[16];
-          tmem_ld16(tmem + lane_base + sb * C::SCOL + r, u);
-          tmem_ld16(tmem + lane_base + sb * C::SCOL + N + r, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[r + e] = __uint_as_float(u[e]) + __uint_as_float(v[e]);
-        }
-      }
-      tc_fence_before();
-      mbar_arrive(&sh.sfree[sb]);
-      const int tok = tm.tok0 + tid;
-      const float ks = tm.ks[tid >> 4], vs = tm.vs[tid >> 4];
-      const float lvs = __log2f(vs), ivs = ks == 0.0f ? 0.0f : __frcp_rn(vs);
-      const bool edge = tm.cut || tm.tok0 + kTile - 1 > pm.low || (a.window && tm.tok0 <= (int64_t)pm.high - a.window);
-      const bool hidden = ks == 0.0f || tok >= pm.len;
-      bool over = false;
-#pragma unroll
-      for (int r = 0; r < N; r += 4) {
-        if (r < R) {
-          const float4 rc = *reinterpret_cast<const float4*>(&pm.rc[r]);
-          const float4 rf = *reinterpret_cast<const float4*>(&sh.ref[r]);
-          const float rcs[4] = {rc.x, rc.y, rc.z, rc.w}, rfs[4] = {rf.x, rf.y, rf.z, rf.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float t = fmaf(x[r + e], rcs[e] * ks, lvs);
-            if (edge) {
-              const int pos = pm.pos[r + e];
-              if (hidden || tok > pos || (a.window && tok <= (int64_t)pos - a.window)) t = -INFINITY;
-            }
-            x[r + e] = t;
-            over |= t > (first ? -INFINITY : rfs[e] + kHead);
-          }
-        }
-      }
-      if (any_of_128(over || dead)) {
-        // some key passes its row's reference: new references, and what was summed up moves to them
-        if (any_of_128(dead)) break;
-#pragma unroll
-        for (int r = 0; r < N; ++r) {
+        for (int r = 0; r < N; r += 16) {
           if (r < R) {
-            float top = x[r];
+            uint32_t u[16], v[16];
+            tmem_ld16(st + r, u);
+            tmem_ld16(st + N + r, v);
+            tmem_ld_wait();
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            if (lane == 0) sh.red[warp][r] = top;
+            for (int e = 0; e < 16; ++e) x[r + e] = __uint_as_float(u[e]) + __uint_as_float(v[e]);
           }
         }
-        any_of_128(false);
-        if (tid >= R && tid < N) sh.ref[tid] = INFINITY;  // not a row: nothing passes it
-        if (tid < R) {
-          const float top = fmaxf(fmaxf(sh.red[0][tid], sh.red[1][tid]), fmaxf(sh.red[2][tid], sh.red[3][tid]));
-          const float old = first ? -INFINITY : sh.ref[tid];
-          const float now = fmaxf(top, old);
-          sh.ref[tid] = now;
-          sh.grow[tid] = now == old ? 1.0f : ex2(old - now);
-        }
-        any_of_128(false);
-        if (!first) {
-          if (!mbar_wait_bounded(&sh.pvdone[(i - 1) % C::B], (uint32_t)((i - 1) / C::B) & 1u, c.status)) dead = true;
-          if (any_of_128(dead)) break;
-          tc_fence_after();
+        tc_fence_before();
+        mbar_arrive(&sh.sfree[grp]);
+        const float ks = tm.ks[tid >> 4], vs = tm.vs[tid >> 4];
+        const float lvs = lg2(vs), ivs = ks == 0.0f ? 0.0f : rcp(vs);
+        const int flags = tm.flags, tok = tm.tok0 + tid, most = tm.len;
+        // the group's references are free once the pair before has been joined
+        if (first && p > 0 && !mbar_wait_bounded(&sh.joined, (uint32_t)(p - 1) & 1u, c.status)) dead = true;
+        bool over = first;
 #pragma unroll
-          for (int r = 0; r < N; ++r)
-            if (r < R) l[r] *= sh.grow[r];
-#pragma unroll 1
-          for (int col = 0; col < C::MB * C::OCOL; col += 16) {
-            const int r = col % N;
-            if (r < R) {
-              uint32_t u[16];
-              tmem_ld16(otm + lane_base + col, u);
-              tmem_ld_wait();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * (r + e < R ? sh.grow[r + e] : 0.0f));
-              tmem_st16(otm + lane_base + col, u);
-            }
-          }
-          tmem_st_wait();
-          tc_fence_before();
-        }
-      } else if (first) {  // no row sees a key of the pair's first tile
-        if (tid < N) sh.ref[tid] = tid < R ? -INFINITY : INFINITY;
-        any_of_128(false);
-      }
-      // P, its sums and its terms; the buffer is free once the tile before last has been multiplied
-      if (i >= C::B && !mbar_wait_bounded(&sh.pvdone[sb], (uint32_t)(i / C::B - 1) & 1u, c.status)) dead = true;
-      uint8_t* pd = pbuf + sb * C::P + tid * 16;
-#pragma unroll
-      for (int r = 0; r < N; r += 16) {
-        uint32_t t0[4] = {0, 0, 0, 0}, t1[4] = {0, 0, 0, 0}, t2[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int q = 0; q < 16; q += 4) {
-          if (r + q < R) {
-            const float4 rf = *reinterpret_cast<const float4*>(&sh.ref[r + q]);
-            const float rfs[4] = {rf.x, rf.y, rf.z, rf.w};
-            float pr[4];
+        for (int r = 0; r < N; r += 4) {
+          if (r < R) {
+            const float4 rc = *reinterpret_cast<const float4*>(&pm.rc[r]);
+            const float4 rf = *reinterpret_cast<const float4*>(&ref[r]);
+            const float rcs[4] = {rc.x, rc.y, rc.z, rc.w}, rfs[4] = {rf.x, rf.y, rf.z, rf.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float m = rfs[e] == -INFINITY ? 0.0f : rfs[e];
-              pr[e] = r + q + e < R ? ex2(x[r + q + e] - m + kBias) : 0.0f;
-              l[r + q + e] = fmaf(pr[e], ivs, l[r + q + e]);
-            }
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t h = f16x2(pr[2 * z], pr[2 * z + 1]);
-              const uint16_t c0 = e4m3x2(h);
-              const uint32_t r1 = rest16(h, codes_f16x2(c0));
-              const uint16_t c1 = e4m3x2(r1);
-              const uint16_t c2 = e4m3x2(rest16(r1, codes_f16x2(c1)));
-              t0[q / 4] |= (uint32_t)c0 << (16 * z);
-              t1[q / 4] |= (uint32_t)c1 << (16 * z);
-              t2[q / 4] |= (uint32_t)c2 << (16 * z);
+              x[r + e] = fmaf(x[r + e], rcs[e] * ks, lvs);
+              over |= x[r + e] - rfs[e] > kHead;
             }
           }
         }
-        // N-contiguous groups of 16 columns, a key's 16 bytes after the other's
-        *reinterpret_cast<uint4*>(pd + (r / 16) * (kTile * 16)) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
-        *reinterpret_cast<uint4*>(pd + ((N + r) / 16) * (kTile * 16)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-        *reinterpret_cast<uint4*>(pd + ((2 * N + r) / 16) * (kTile * 16)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+        if (flags & 2) {  // masks
+          const bool hidden = ks == 0.0f || tok >= most;
+          over = first;
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            if (r < R) {
+              const int pos = pm.pos[r];
+              if (hidden || tok > pos || (a.window && tok <= (int64_t)pos - a.window)) x[r] = -INFINITY;
+              over |= x[r] - ref[r] > kHead;
+            }
+          }
+        }
+        if (any_of(grp, over || dead)) {
+          // some key passes its row's reference, or there is none yet: new references, and what was summed up
+          // moves to them
+          if (any_of(grp, dead)) break;
+#pragma unroll
+          for (int r = 0; r < N; ++r) {
+            if (r < R) {
+              const float top = warp_max(x[r]);
+              if (lane == 0) sh.red[grp][wq][r] = top;
+            }
+          }
+          any_of(grp, false);
+          if (tid >= R && tid < N) ref[tid] = INFINITY;  // not a row: nothing passes it
+          if (tid < R) {
+            const float* red = sh.red[grp][0];
+            const float top = fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid]));
+            const float old = first ? -INFINITY : ref[tid];
+            const float now = fmaxf(top, old);
+            ref[tid] = now;
+            grow[tid] = now == old ? 1.0f : ex2(old - now);
+          }
+          any_of(grp, false);
+          if (!first) {
+            if (!mbar_wait_bounded(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
+            if (any_of(grp, dead)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int r = 0; r < N; ++r)
+              if (r < R) l[r] *= grow[r];
+#pragma unroll 1
+            for (int col = 0; col < C::MB * C::OCOL; col += 16) {
+              const int r = col % N;
+              if (r < R) {
+                uint32_t u[16];
+                tmem_ld16(ot + col, u);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * (r + e < R ? grow[r + e] : 0.0f));
+                tmem_st16(ot + col, u);
+              }
+            }
+            tmem_st_wait();
+            tc_fence_before();
+          }
+        }
+        // P, its sums and its terms; the buffer is free once the group's tile before has been multiplied
+        if (turn && !mbar_wait_bounded(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
+#pragma unroll
+        for (int r = 0; r < N; r += 16) {
+          uint32_t t0[4] = {0, 0, 0, 0}, t1[4] = {0, 0, 0, 0}, t2[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int q = 0; q < 16; q += 4) {
+            if (r + q < R) {
+              const float4 rf = *reinterpret_cast<const float4*>(&ref[r + q]);
+              const float rfs[4] = {rf.x, rf.y, rf.z, rf.w};
+              float pr[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // a row that has seen no key has no reference: -inf - -inf is no weight
+                pr[e] = rfs[e] == -INFINITY || r + q + e >= R ? 0.0f : ex2(x[r + q + e] - rfs[e] + kBias);
+                l[r + q + e] = fmaf(pr[e], ivs, l[r + q + e]);
+              }
+#pragma unroll
+              for (int z = 0; z < 2; ++z) {
+                const uint32_t h = f16x2(pr[2 * z], pr[2 * z + 1]);
+                const uint16_t c0 = e4m3x2(h);
+                const uint32_t r1 = rest16(h, codes_f16x2(c0));
+                const uint16_t c1 = e4m3x2(r1);
+                const uint16_t c2 = e4m3x2(rest16(r1, codes_f16x2(c1)));
+                t0[q / 4] |= (uint32_t)c0 << (16 * z);
+                t1[q / 4] |= (uint32_t)c1 << (16 * z);
+                t2[q / 4] |= (uint32_t)c2 << (16 * z);
+              }
+            }
+          }
+          // N-contiguous groups of 16 columns, a key's 16 bytes after the other's
+          *reinterpret_cast<uint4*>(pd + (r / 16) * (kTile * 16)) = make_uint4(t0[0], t0[1], t0[2], t0[3]);
+          *reinterpret_cast<uint4*>(pd + ((N + r) / 16) * (kTile * 16)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(pd + ((2 * N + r) / 16) * (kTile * 16)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&sh.pfull[grp]);
+        ++turn;
+        s += NG;
+        if (s >= C::S) {
+          kpar ^= (uint32_t)(s / C::S) & 1u;
+          s %= C::S;
+        }
       }
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(&sh.pfull[sb]);
-
-      if (last) {  // the pair's last tile here
+      // the pair's end here: the group's sums, then all groups' outputs by the one that had the last tile
+      const bool took = mine < i1;
+      if (took) {
 #pragma unroll
         for (int r = 0; r < N; ++r) {
           if (r < R) {
             float v = l[r];
 #pragma unroll
             for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0) sh.red[warp][r] = v;
+            if (lane == 0) sh.red[grp][wq][r] = v;
           }
         }
-        if (!mbar_wait_bounded(&sh.pvdone[sb], (uint32_t)(i / C::B) & 1u, c.status)) dead = true;
-        if (any_of_128(dead)) break;
+        if (!mbar_wait_bounded(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
+        if (any_of(grp, dead)) break;
+        if (tid < R) {
+          const float* red = sh.red[grp][0];
+          sh.sum[grp][tid] = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
+        }
+        any_of(grp, false);
+      }
+      const bool join = (i1 - 1) % NG == grp;
+      if (tid == 0) mbar_arrive(&sh.summed);
+      if (join) {
+        if (!mbar_wait_bounded(&sh.summed, (uint32_t)p & 1u, c.status)) dead = true;
+        if (any_of(grp, dead)) break;
         tc_fence_after();
         const int64_t first_tile = pm.first;
-        const int n_tiles = pm.n_tiles, start = pm.start, h = pm.h;
+        const int n_tiles = pm.n_tiles, start = pm.start, h = pm.h, parts_here = min(NG, i1 - i0);
         const bool whole = first_tile >= u0 && first_tile + n_tiles <= u1;
         const int64_t slot = 2 * cta + (first_tile <= u0 ? 0 : 1);
+        // row's factors of the groups that took part, and its reference and sum
+        if (tid < R) {
+          float top = -INFINITY, sum = 0.0f;
+          for (int q = 0; q < parts_here; ++q) top = fmaxf(top, sh.ref[(i0 + q) % NG][tid]);
+          for (int q = 0; q < parts_here; ++q) {
+            const int gq = (i0 + q) % NG;
+            const float f = sh.ref[gq][tid] == -INFINITY ? 0.0f : ex2(sh.ref[gq][tid] - top);
+            sum = fmaf(sh.sum[gq][tid], f, sum);
+            sh.grow[gq][tid] = f;
+          }
+          if (whole)
+            sh.red[grp][0][tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+          else
+            da.part_ml[slot * N + tid] = make_float2(top, sum);
+        }
+        any_of(grp, false);
 #pragma unroll 1
         for (int mb = 0; mb < C::MB; ++mb) {
           const int d = mb * 128 + tid;
 #pragma unroll 1
           for (int r = 0; r < R; r += 8) {
-            uint32_t v0[8], v1[8], v2[8];
-            const uint32_t at = otm + lane_base + mb * C::OCOL + r;
-            tmem_ld8(at, v0);
-            tmem_ld8(at + N, v1);
-            tmem_ld8(at + 2 * N, v2);
-            tmem_ld_wait();
+            float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+            for (int q = 0; q < parts_here; ++q) {
+              const int gq = (i0 + q) % NG;
+              uint32_t v0[8], v1[8], v2[8];
+              const uint32_t at = otm + lane_base + gq * (C::MB * C::OCOL) + mb * C::OCOL + r;
+              tmem_ld8(at, v0);
+              tmem_ld8(at + N, v1);
+              tmem_ld8(at + 2 * N, v2);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                o[e] = fmaf(fmaf(__uint_as_float(v2[e]), 0x1p-8f, fmaf(__uint_as_float(v1[e]), 0x1p-4f, __uint_as_float(v0[e]))),
+                            r + e < R ? sh.grow[gq][r + e] : 0.0f, o[e]);
+            }
             if (d < D) {
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 const int row = r + e;
                 if (row < R) {
-                  const float sum = (sh.red[0][row] + sh.red[1][row]) + (sh.red[2][row] + sh.red[3][row]);
-                  const float o = fmaf(__uint_as_float(v2[e]), 0x1p-8f, fmaf(__uint_as_float(v1[e]), 0x1p-4f, __uint_as_float(v0[e])));
                   if (whole) {
                     const int t = row / G, g = row - t * G;
-                    const __nv_bfloat16 y = __float2bfloat16_rn(sum == 0.0f ? 0.0f : o / sum);
+                    const __nv_bfloat16 y = __float2bfloat16_rn(o[e] * sh.red[grp][0][row]);
                     a.out[(int64_t)(start + t) * a.ldo + (int64_t)(h * G + g) * a.hso + d] =
                         *reinterpret_cast<const uint16_t*>(&y);
                   } else {
-                    da.part_o[(slot * N + row) * D + d] = o;
-                    if (d == 0) da.part_ml[slot * N + row] = make_float2(sh.ref[row], sum);
+                    da.part_o[(slot * N + row) * D + d] = o[e];
                   }
                 }
               }
@@ -708,50 +844,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tc_fence_before();
+        any_of(grp, false);
+        // the other groups may go on with the next pair, and the query buffer is free
+        if (tid == 0) {
+          mbar_arrive(&sh.qfree[p % C::QB]);
+          mbar_arrive(&sh.joined);
+        }
         if (!whole) {
           // the CTA whose ticket completes the pair joins the parts, in their order on the line
           auto owner = [&](int64_t unit) { return ((unit + 1) * grid - 1) / total; };
           const int64_t c0 = owner(first_tile), c1 = owner(first_tile + n_tiles - 1);
           const int parts = (int)(c1 - c0 + 1);
-          any_of_128(false);
-          if (tid == 0) sh.ticket = ticket_add(da.counters + c0, 1);
-          any_of_128(false);
-          if (sh.ticket == parts - 1) {
-            const bool at_start = c0 * total / grid == first_tile;  // the first part is its CTA's first pair
-            for (int e = tid; e < R * (D / 4); e += 128) {
-              const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-              float4 v = make_float4(0, 0, 0, 0);
-              float top = -INFINITY, sum = 0.0f;
-              for (int q = 0; q < parts; ++q) {
-                const int64_t sl = 2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0);
-                top = fmaxf(top, __ldcg(&da.part_ml[sl * N + row]).x);
-              }
-              for (int q = 0; q < parts; ++q) {
-                const int64_t sl = 2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0);
-                const float2 z = __ldcg(&da.part_ml[sl * N + row]);
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(da.part_o + (sl * N + row) * D + d));
-                const float f = z.x == -INFINITY ? 0.0f : ex2(z.x - top);
-                v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
-                sum = fmaf(z.y, f, sum);
-              }
-              const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-              const int t = row / G, g = row - t * G;
-              const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), y1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-              *reinterpret_cast<uint2*>(a.out + (int64_t)(start + t) * a.ldo + (int64_t)(h * G + g) * a.hso + d) =
-                  make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
-            }
+          if (tid == 0) sh.ticket[grp] = ticket_add(da.counters + c0, 1);
+          any_of(grp, false);
+          if (sh.ticket[grp] == parts - 1) {
+            join_parts<D, N>(da, tid, R, G, start, h, c0, parts, c0 * total / grid == first_tile);
             if (tid == 0) da.counters[c0] = 0;
           }
         }
-        any_of_128(false);  // everyone is done with this pair's rows, sums and references
-        if (tid == 0) mbar_arrive(&sh.qfree[p % C::B]);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 4) tmem_dealloc(tmem, 512);
+  if (warp == kMma) tmem_dealloc(tmem, 512);
 }
 
 template <int D, int N>
@@ -767,7 +884,7 @@ int launch(const DecodeArgs& da, const CUtensorMap& km, const CUtensorMap& vm, i
       return QG_ERR_CUDA;
     configured.fetch_or(bit);
   }
-  return launch_pdl(attn_decode_kernel<D, N>, dim3(grid), dim3(kThreads), C::SMEM, s, km, vm, da) == cudaSuccess
+  return launch_pdl(attn_decode_kernel<D, N>, dim3(grid), dim3(C::THREADS), C::SMEM, s, km, vm, da) == cudaSuccess
              ? QG_OK
              : QG_ERR_CUDA;
 }
