@@ -64,12 +64,15 @@ struct Cfg {
   static constexpr int P = 3 * N * kTile;            // a group's terms of P
   static constexpr int MB = NP;                      // M blocks of O (128 dims; D = 64 fills half of one)
   static constexpr int SCOL = 2 * N, OCOL = 3 * N;   // TMEM columns of a group's S and of a block of its O
-  static constexpr int STAGE = 2 * KV;
   static constexpr int FIXED = 1024 + QB * Q + GROUPS * P + 8192;
-  static constexpr int S0 = (232448 - FIXED) / STAGE;
-  static constexpr int S = S0 > 8 ? 8 : S0;
-  static constexpr int SMEM = FIXED + S * STAGE;
-  static_assert(S >= 2 && S >= GROUPS && GROUPS * (SCOL + MB * OCOL) <= 512, "shared and tensor memory");
+  static constexpr int SLOTS = (232448 - FIXED) / KV;
+  // key tiles are done with after the scores, value tiles a softmax later
+  static constexpr int SK0 = SLOTS * 2 / 5 < 2 ? 2 : SLOTS * 2 / 5, SV0 = SLOTS - SK0;
+  static constexpr int SK = SK0 > 6 ? 6 : SK0, SV = SV0 > 8 ? 8 : SV0;
+  static constexpr int METAS = 32;                   // tiles between a key tile's issue and its outputs: fewer
+  static constexpr int SMEM = FIXED + (SK + SV) * KV;
+  static_assert(SK >= 2 && SV >= 2 && GROUPS * (SCOL + MB * OCOL) <= 512, "shared and tensor memory");
+  static_assert(SK + 3 * GROUPS < METAS && SV + GROUPS < METAS, "tiles on their way");
 };
 
 // What a stage holds.
@@ -79,21 +82,23 @@ struct TileMeta {
   float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
 };
 // What a query buffer holds besides the rows.
+template <int N>
 struct PairMeta {
-  int R, h, start, n_tiles;
-  int i0, i1, pad[2];           // its tiles in this CTA
-  int64_t first, pad2;          // its first tile on the line
-  float rc[64];                 // the row's power of two * scale * log2(e)
-  int pos[64];
+  int R, n_tiles, i0, i1;       // rows, tiles, and which of this CTA's tiles they are
+  int64_t first, base;          // its first tile on the line; its first row's output
+  alignas(16) float rc[N];      // the row's power of two * scale * log2(e)
+  int pos[N];
+  int64_t off[N];               // the row's output, from the first one's
 };
 template <int D, int N>
 struct Shared {
   using C = Cfg<D, N>;
-  TileMeta tile[C::S];
-  PairMeta pair[C::QB];
+  TileMeta tile[C::METAS];
+  PairMeta<N> pair[C::QB];
   alignas(16) float ref[C::GROUPS][N];
-  float grow[C::GROUPS][N], sum[C::GROUPS][N], red[C::GROUPS][4][N];
-  uint64_t kfull[C::S], vfull[C::S], empty[C::S];
+  alignas(16) float grow[C::GROUPS][N];
+  float sum[C::GROUPS][N], red[C::GROUPS][4][N];
+  uint64_t kfull[C::SK], kfree[C::SK], vfull[C::SV], vfree[C::SV];
   uint64_t qfull[C::QB], qfree[C::QB];
   uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
   uint64_t summed, joined, ended;
@@ -277,8 +282,8 @@ struct Walk {
 
 // The joining of a pair's parts by the CTA that finished last: one group's 128 threads.
 template <int D, int N>
-__device__ __forceinline__ void join_parts(const DecodeArgs& da, int tid, int R, int G, int start, int h, int64_t c0,
-                                           int parts, bool at_start) {
+__device__ __noinline__ void join_parts(const DecodeArgs& da, int tid, int R, int G, int64_t base, int64_t c0, int parts,
+                                        bool at_start) {
   const AttnArgs& a = da.a;
   for (int e = tid; e < R * (D / 4); e += 128) {
     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
@@ -300,7 +305,7 @@ __device__ __forceinline__ void join_parts(const DecodeArgs& da, int tid, int R,
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int t = row / G, g = row - t * G;
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), y1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-    *reinterpret_cast<uint2*>(a.out + (int64_t)(start + t) * a.ldo + (int64_t)(h * G + g) * a.hso + d) =
+    *reinterpret_cast<uint2*>(a.out + base + t * a.ldo + g * a.hso + d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
   }
 }
@@ -314,7 +319,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   static_assert(sizeof(Shared<D, N>) <= 8192, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qbuf = ring + C::S * C::STAGE;
+  uint8_t* vring = ring + C::SK * C::KV;
+  uint8_t* qbuf = vring + C::SV * C::KV;
   uint8_t* pbuf = qbuf + C::QB * C::Q;
   Shared<D, N>& sh = *reinterpret_cast<Shared<D, N>*>(pbuf + NG * C::P);
   const AttnArgs& a = da.a;
@@ -323,17 +329,20 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   const int G = a.hq / c.hkv;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::S; ++s) {
+    for (int s = 0; s < C::SK; ++s) {
       mbar_init(&sh.kfull[s], 16);
+      mbar_init(&sh.kfree[s], 1);
+    }
+    for (int s = 0; s < C::SV; ++s) {
       mbar_init(&sh.vfull[s], 8);
-      mbar_init(&sh.empty[s], 1);
+      mbar_init(&sh.vfree[s], 1);
     }
     for (int i = 0; i < C::QB; ++i) {
-      mbar_init(&sh.qfull[i], 64);
+      mbar_init(&sh.qfull[i], 32);
       mbar_init(&sh.qfree[i], 1);
     }
     for (int i = 0; i < NG; ++i) {
-      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.sfull[i], 2);  // the MMAs' end, and the issuing thread's own arrival
       mbar_init(&sh.sfree[i], 128);
       mbar_init(&sh.pfull[i], 128);
       mbar_init(&sh.pvdone[i], 1);
@@ -362,9 +371,15 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   const int n = (int)(u1 - u0);
   const uint32_t otm = tmem + NG * C::SCOL;  // the groups' O follow their S
 
-  if (n > 0 && warp == kMma + 1) {  // ------------------------------------------------------ key and value tiles
+  if (n > 0 && (warp == kMma + 1 || warp == kMma + 2)) {  // -------------------------------- key tiles, value tiles
     // Lanes 8q .. 8q + 7 look after tile 4j + q: its eight groups of 16 keys.  Four tiles' page ids are
     // fetched by one load, while the four before them are issued.
+    const bool keys = warp == kMma + 1;
+    const int stages = keys ? C::SK : C::SV;
+    uint8_t* slots = keys ? ring : vring;
+    uint64_t* full = keys ? sh.kfull : sh.vfull;
+    uint64_t* free_ = keys ? sh.kfree : sh.vfree;
+    const CUtensorMap* map = keys ? &kmap : &vmap;
     w.find(a, u0, lane);
     const int P = 1 << c.page_log2, box = min(P, kTile);
     int tok0 = 0, len = 0, head = 0, after = 0, id = -1, edge = 0, walked = 0, i0 = 0;
@@ -397,58 +412,53 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge;
       if (walked < n) prepare();
       for (int q = 0; q < 4 && i < n; ++q, ++i) {
-        if (lap && !mbar_wait_bounded(&sh.empty[s], (lap - 1) & 1, c.status)) dead = true;
+        if (lap && !mbar_wait_bounded(&free_[s], (lap - 1) & 1, c.status)) dead = true;
         if (__any_sync(0xFFFFFFFFu, dead)) {
           dead = true;
           break;
         }
         if (lane >> 3 == q) {
-          TileMeta& m = sh.tile[s];
           const int gl = lane & 7, tok = ctok0 + 16 * gl;
           bool ok = tok < clen;
           if (ok && (cid < 0 || cid >= c.n_pages)) {
             ok = false;
             atomicExch(c.status, kStatusInvalid);
           }
-          const bool cut = __any_sync(0xFFu << (8 * q), !ok || tok + 16 > clen);
-          if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = (cut ? 3 : 0) | (cedge ? 2 : 0);
-          uint8_t* kd = ring + s * C::STAGE + 16 * gl * C::PW;
           const int64_t tile = (int64_t)cid * c.hkv + chead;
+          TileMeta& m = sh.tile[i % C::METAS];
+          if (keys) {  // written before this lane's arrival, which hands it over
+            const bool cut = __any_sync(0xFFu << (8 * q), !ok || tok + 16 > clen);
+            if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = (cut ? 3 : 0) | (cedge ? 2 : 0);
+            if (!ok) m.ks[gl] = m.vs[gl] = 0.0f;
+          }
           if (ok && (16 * gl) % box == 0) {
-            mbar_arrive_expect_tx(&sh.kfull[s], box * D);
+            uint8_t* dst = slots + s * C::KV + 16 * gl * C::PW;
+            mbar_arrive_expect_tx(&full[s], box * D);
 #pragma unroll
             for (int x = 0; x < C::NP; ++x)
-              tma_load_3d(kd + x * C::PANEL, &kmap, x * 128, tok & (P - 1), (int)tile, &sh.kfull[s]);
-            mbar_arrive_expect_tx(&sh.vfull[s], box * D);
-#pragma unroll
-            for (int x = 0; x < C::NP; ++x)
-              tma_load_3d(kd + C::KV + x * C::PANEL, &vmap, x * 128, tok & (P - 1), (int)tile, &sh.vfull[s]);
+              tma_load_3d(dst + x * C::PANEL, map, x * 128, tok & (P - 1), (int)tile, &full[s]);
           } else {
-            mbar_arrive(&sh.kfull[s]);
-            mbar_arrive(&sh.vfull[s]);
+            mbar_arrive(&full[s]);
           }
-          if (ok) {
-            cp_async4(&m.ks[gl], c.ks + tile);
-            cp_async4(&m.vs[gl], c.vs + tile);
-          } else {
-            m.ks[gl] = 0.0f;
-            m.vs[gl] = 0.0f;
+          if (keys) {
+            if (ok) {
+              cp_async4(&m.ks[gl], c.ks + tile);
+              cp_async4(&m.vs[gl], c.vs + tile);
+            }
+            cp_async_arrive_noinc(&full[s]);
           }
-          cp_async_arrive_noinc(&sh.kfull[s]);
         }
         __syncwarp();
-        if (++s == C::S) s = 0, ++lap;
+        if (++s == stages) s = 0, ++lap;
       }
     }
     // no copy is left in flight into this CTA's shared memory when it ends: the last stages filled
-    for (int j = max(0, i - C::S); j < i; ++j) {
-      mbar_wait_bounded(&sh.kfull[j % C::S], (uint32_t)(j / C::S) & 1u, c.status);
-      mbar_wait_bounded(&sh.vfull[j % C::S], (uint32_t)(j / C::S) & 1u, c.status);
-    }
-  } else if (n > 0 && warp >= kMma + 2) {  // ----------------------------------------------- query rows
-    // 64 threads: D / 16 of them a row, 16 elements each
-    constexpr int TPR = D / 16, RPP = 64 / TPR;
-    const int t = threadIdx.x - 32 * (kMma + 2), part = t % TPR;
+    for (int j = max(0, i - stages); j < i; ++j)
+      mbar_wait_bounded(&full[j % stages], (uint32_t)(j / stages) & 1u, c.status);
+  } else if (n > 0 && warp == kMma + 3) {  // ----------------------------------------------- query rows
+    // D / 16 lanes a row, 16 elements each
+    constexpr int TPR = D / 16, RPP = 32 / TPR;
+    const int t = lane, part = t % TPR;
     w.find(a, u0, lane);
     int64_t u = u0;
     bool dead = false;
@@ -456,12 +466,13 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       const int qb = p % C::QB;
       if (p >= C::QB && !mbar_wait_bounded(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
       if (__any_sync(0xFFFFFFFFu, dead)) break;
-      PairMeta& m = sh.pair[qb];
+      PairMeta<N>& m = sh.pair[qb];
       const int R = min(w.sq.rows * G, N), first_pos = w.sq.len - w.sq.rows;
       const int64_t next = u + w.n - w.k;
       if (t == 0) {
-        m.R = R, m.h = w.h, m.start = w.sq.start, m.n_tiles = w.n, m.first = u - w.k;
+        m.R = R, m.n_tiles = w.n, m.first = u - w.k;
         m.i0 = (int)(u - u0), m.i1 = (int)(min(next, u1) - u0);
+        m.base = (int64_t)w.sq.start * a.ldo + (int64_t)w.h * G * a.hso;
       }
       uint8_t* qd = qbuf + qb * C::Q;
       for (int r0 = 0; r0 < N; r0 += RPP) {
@@ -513,6 +524,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           if (part == 0) {
             m.rc[row] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
             m.pos[row] = in ? first_pos + i : -1;
+            m.off[row] = i * a.ldo + g * a.hso;
           }
         }
       }
@@ -525,72 +537,101 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     constexpr uint32_t kSwz = D == 64 ? 4 : 2;
     constexpr uint32_t kSbo = 8 * C::PW;
     constexpr uint32_t kQk = idesc_e4m3(2 * N, 0, 0), kPv = idesc_e4m3(3 * N, 1, 1);
-    int p = -1;  // pairs begun by the score MMAs
-    auto scores = [&](int i) {
-      const int s = i % C::S, g = i % NG;
-      if (!mbar_wait_bounded(&sh.kfull[s], (uint32_t)(i / C::S) & 1u, c.status)) return false;
-      if (sh.tile[s].after == 0) {
-        ++p;
-        if (!mbar_wait_bounded(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) return false;
-      }
-      if (i >= NG && !mbar_wait_bounded(&sh.sfree[g], (uint32_t)(i / NG - 1) & 1u, c.status)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t ka = smem_u32(ring + s * C::STAGE), qa = smem_u32(qbuf + (p % C::QB) * C::Q);
+    // Two queues, scores and outputs, each in the tiles' order; whichever has its operands goes.
+    int js = 0, jo = 0, ks = 0, vs = 0, p = 0, qb = 0;    // tiles issued, ring stages, pairs begun by the scores
+    uint32_t kpar = 0, vpar = 0, qpar = 0;
+    int gs = 0, go = 0;                                   // their groups, and the parities of the groups' turns
+    uint32_t spar = 1, opar = 0;
+    bool begun = true;                                    // the score queue's pair has its query rows
+    unsigned long long t0 = 0;
+    int idle = 0;
+    while (jo < n) {
+      bool moved = false;
+      if (js < n && __all_sync(0xFFFFFFFFu, mbar_test(&sh.kfull[ks], kpar))) {
+        const TileMeta& m = sh.tile[js % C::METAS];
+        begun = m.after != 0 || __all_sync(0xFFFFFFFFu, mbar_test(&sh.qfull[qb], qpar));
+        if (begun && (js < NG || __all_sync(0xFFFFFFFFu, mbar_test(&sh.sfree[gs], spar)))) {
+          tc_fence_after();
+          if (m.after == 0) {  // the pair's query buffer
+            p = qb;
+            if (++qb == C::QB) qb = 0, qpar ^= 1;
+          }
+          if (lane == 0) {
+            const uint32_t ka = smem_u32(ring + ks * C::KV), qa = smem_u32(qbuf + p * C::Q);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
-          mma_e4m3(tmem + g * C::SCOL, mat_desc(ka + panel * C::PANEL + off, 16, kSbo, kSwz),
-                   mat_desc(qa + panel * C::QPANEL + off, 16, kSbo, kSwz), kQk, x > 0);
+            for (int x = 0; x < D / 32; ++x) {
+              const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
+              mma_e4m3(tmem + gs * C::SCOL, mat_desc(ka + panel * C::PANEL + off, 16, kSbo, kSwz),
+                       mat_desc(qa + panel * C::QPANEL + off, 16, kSbo, kSwz), kQk, x > 0);
+            }
+            mma_commit(&sh.sfull[gs]);
+            mbar_arrive(&sh.sfull[gs]);  // passes the tile's description on to the softmax group
+            mma_commit(&sh.kfree[ks]);
+          }
+          __syncwarp();
+          ++js;
+          if (++ks == C::SK) ks = 0, kpar ^= 1;
+          if (++gs == NG) gs = 0, spar ^= 1;
+          moved = true;
         }
-        mma_commit(&sh.sfull[g]);
       }
-      __syncwarp();
-      return true;
-    };
-    auto outputs = [&](int i) {
-      const int s = i % C::S, g = i % NG;
-      if (!mbar_wait_bounded(&sh.vfull[s], (uint32_t)(i / C::S) & 1u, c.status)) return false;
-      const TileMeta& m = sh.tile[s];
-      uint8_t* vt = ring + s * C::STAGE + C::KV;
-      if (m.flags & 1) {  // rows without a key hold anything, NaN codes too: they must be numbers for P = 0
-        for (int r = lane; r < kTile; r += 32) {
-          if (m.tok0 + r >= m.len || m.ks[r >> 4] == 0.0f) {
+      if (jo < js && __all_sync(0xFFFFFFFFu, mbar_test(&sh.pfull[go], opar)) &&
+          __all_sync(0xFFFFFFFFu, mbar_test(&sh.vfull[vs], vpar))) {
+        const TileMeta& m = sh.tile[jo % C::METAS];
+        uint8_t* vt = vring + vs * C::KV;
+        if (m.flags & 1) {  // rows without a key hold anything, NaN codes too: they must be numbers for P = 0
+          for (int r = lane; r < kTile; r += 32) {
+            if (m.tok0 + r >= m.len || m.ks[r >> 4] == 0.0f) {
 #pragma unroll 1
-            for (int x = 0; x < C::NP; ++x)
+              for (int x = 0; x < C::NP; ++x)
 #pragma unroll
-              for (int b = 0; b < C::PW; b += 16)
-                *reinterpret_cast<uint4*>(vt + x * C::PANEL + r * C::PW + b) = make_uint4(0, 0, 0, 0);
+                for (int b = 0; b < C::PW; b += 16)
+                  *reinterpret_cast<uint4*>(vt + x * C::PANEL + r * C::PW + b) = make_uint4(0, 0, 0, 0);
+            }
           }
+          fence_proxy_async_smem();
+          __syncwarp();
         }
-        fence_proxy_async_smem();
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t va = smem_u32(vt), pa = smem_u32(pbuf + go * C::P), od = otm + go * (C::MB * C::OCOL);
+          const bool first = m.after < NG;  // the group's first tile of the pair
+#pragma unroll
+          for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+            for (int x = 0; x < kTile / 32; ++x) {
+              // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
+              // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
+              // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
+              mma_e4m3(od + mb * C::OCOL, mat_desc(va + mb * C::PANEL + x * 32 * C::PW, C::PANEL, kSbo, kSwz),
+                       mat_desc(pa + x * 32 * 16, 128, kTile * 16, 0), kPv, !(first && x == 0));
+            }
+          mma_commit(&sh.pvdone[go]);
+          mma_commit(&sh.vfree[vs]);
+        }
         __syncwarp();
+        ++jo;
+        if (++vs == C::SV) vs = 0, vpar ^= 1;
+        if (++go == NG) go = 0, opar ^= 1;
+        moved = true;
       }
-      if (!mbar_wait_bounded(&sh.pfull[g], (uint32_t)(i / NG) & 1u, c.status)) return false;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t va = smem_u32(vt), pa = smem_u32(pbuf + g * C::P), od = otm + g * (C::MB * C::OCOL);
-        const bool first = m.after < NG;  // the group's first tile of the pair
-#pragma unroll
-        for (int mb = 0; mb < C::MB; ++mb)
-#pragma unroll
-          for (int x = 0; x < kTile / 32; ++x) {
-            // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
-            // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
-            // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
-            mma_e4m3(od + mb * C::OCOL, mat_desc(va + mb * C::PANEL + x * 32 * C::PW, C::PANEL, kSbo, kSwz),
-                     mat_desc(pa + x * 32 * 16, 128, kTile * 16, 0), kPv, !(first && x == 0));
-          }
-        mma_commit(&sh.pvdone[g]);
-        mma_commit(&sh.empty[s]);
+      if (moved) {
+        idle = 0;
+        t0 = 0;
+      } else if (++idle == 4096) {  // the limit of every wait, checked now and then
+        idle = 0;
+        const unsigned long long t = global_ns();
+        bool late = false;
+        if (t0 == 0)
+          t0 = t;
+        else
+          late = t - t0 > kWaitLimitNs;
+        if (__any_sync(0xFFFFFFFFu, late)) {
+          if (lane == 0) atomicExch(c.status, kStatusTimeout);
+          break;
+        }
       }
-      __syncwarp();
-      return true;
-    };
-    // scores run NG tiles ahead of outputs, so that every group has its next tile's at hand
-    bool go = true;
-    for (int i = 0; i < min(n, NG) && go; ++i) go = scores(i);
-    for (int i = 0; i < n && go; ++i) go = outputs(i) && (i + NG >= n || scores(i + NG));
+    }
     // every MMA has ended before the CTA's memory goes
     if (lane == 0) {
       mma_commit(&sh.ended);
@@ -605,10 +646,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     float* grow = sh.grow[grp];
     uint8_t* pd = pbuf + grp * C::P + tid * 16;
     bool dead = false;
-    int i1 = 0, s = grp % C::S;
-    uint32_t turn = 0, kpar = (grp / C::S) & 1;  // tiles of this group so far; parity of its next key tile
+    int i1 = 0;
+    uint32_t turn = 0;  // tiles of this group so far
     for (int p = 0; i1 < n; ++p) {
-      const PairMeta& pm = sh.pair[p % C::QB];
+      const PairMeta<N>& pm = sh.pair[p % C::QB];
       if (!mbar_wait_bounded(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) dead = true;
       if (any_of(grp, dead)) break;
       const int R = pm.R, i0 = pm.i0;
@@ -619,8 +660,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       const int mine = i0 + (grp - i0 % NG + NG) % NG;  // this group's first tile of the pair, if it has one
       for (int i = mine; i < i1; i += NG) {
         const bool first = i == mine;
-        if (!mbar_wait_bounded(&sh.kfull[s], kpar, c.status)) dead = true;
-        const TileMeta& tm = sh.tile[s];
+        const TileMeta& tm = sh.tile[i % C::METAS];
         if (!mbar_wait_bounded(&sh.sfull[grp], turn & 1, c.status)) dead = true;
         tc_fence_after();
         // the key's scores: both terms of every row
@@ -753,11 +793,6 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         tc_fence_before();
         mbar_arrive(&sh.pfull[grp]);
         ++turn;
-        s += NG;
-        if (s >= C::S) {
-          kpar ^= (uint32_t)(s / C::S) & 1u;
-          s %= C::S;
-        }
       }
       // the pair's end here: the group's sums, then all groups' outputs by the one that had the last tile
       const bool took = mine < i1;
@@ -786,7 +821,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         if (any_of(grp, dead)) break;
         tc_fence_after();
         const int64_t first_tile = pm.first;
-        const int n_tiles = pm.n_tiles, start = pm.start, h = pm.h, parts_here = min(NG, i1 - i0);
+        const int64_t base = pm.base;
+        const int n_tiles = pm.n_tiles, parts_here = min(NG, i1 - i0);
         const bool whole = first_tile >= u0 && first_tile + n_tiles <= u1;
         const int64_t slot = 2 * cta + (first_tile <= u0 ? 0 : 1);
         // row's factors of the groups that took part, and its reference and sum
@@ -811,34 +847,38 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 #pragma unroll 1
           for (int r = 0; r < R; r += 8) {
             float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 1
-            for (int q = 0; q < parts_here; ++q) {
-              const int gq = (i0 + q) % NG;
-              uint32_t v0[8], v1[8], v2[8];
-              const uint32_t at = otm + lane_base + gq * (C::MB * C::OCOL) + mb * C::OCOL + r;
-              tmem_ld8(at, v0);
-              tmem_ld8(at + N, v1);
-              tmem_ld8(at + 2 * N, v2);
-              tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                o[e] = fmaf(fmaf(__uint_as_float(v2[e]), 0x1p-8f, fmaf(__uint_as_float(v1[e]), 0x1p-4f, __uint_as_float(v0[e]))),
-                            r + e < R ? sh.grow[gq][r + e] : 0.0f, o[e]);
+            for (int gq = 0; gq < NG; ++gq) {
+              if ((gq - i0 % NG + NG) % NG < parts_here) {
+                uint32_t v0[8], v1[8], v2[8];
+                const uint32_t at = otm + lane_base + gq * (C::MB * C::OCOL) + mb * C::OCOL + r;
+                tmem_ld8(at, v0);
+                tmem_ld8(at + N, v1);
+                tmem_ld8(at + 2 * N, v2);
+                const float4 f0 = *reinterpret_cast<const float4*>(&sh.grow[gq][r]);
+                const float4 f1 = *reinterpret_cast<const float4*>(&sh.grow[gq][r + 4]);
+                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  o[e] = fmaf(fmaf(__uint_as_float(v2[e]), 0x1p-8f, fmaf(__uint_as_float(v1[e]), 0x1p-4f, __uint_as_float(v0[e]))),
+                              f[e], o[e]);
+              }
             }
             if (d < D) {
+              if (whole) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int row = r + e;
-                if (row < R) {
-                  if (whole) {
-                    const int t = row / G, g = row - t * G;
-                    const __nv_bfloat16 y = __float2bfloat16_rn(o[e] * sh.red[grp][0][row]);
-                    a.out[(int64_t)(start + t) * a.ldo + (int64_t)(h * G + g) * a.hso + d] =
-                        *reinterpret_cast<const uint16_t*>(&y);
-                  } else {
-                    da.part_o[(slot * N + row) * D + d] = o[e];
+                for (int e = 0; e < 8; ++e) {
+                  if (r + e < R) {
+                    const __nv_bfloat16 y = __float2bfloat16_rn(o[e] * sh.red[grp][0][r + e]);
+                    a.out[base + pm.off[r + e] + d] = *reinterpret_cast<const uint16_t*>(&y);
                   }
                 }
+              } else {
+                float* dst = da.part_o + (slot * N + r) * D + d;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (r + e < R) dst[e * D] = o[e];
               }
             }
           }
@@ -858,7 +898,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           if (tid == 0) sh.ticket[grp] = ticket_add(da.counters + c0, 1);
           any_of(grp, false);
           if (sh.ticket[grp] == parts - 1) {
-            join_parts<D, N>(da, tid, R, G, start, h, c0, parts, c0 * total / grid == first_tile);
+            join_parts<D, N>(da, tid, R, G, base, c0, parts, c0 * total / grid == first_tile);
             if (tid == 0) da.counters[c0] = 0;
           }
         }
