@@ -53,7 +53,11 @@ template <int D, int N>
 struct Cfg {
   // softmax groups of 128 threads (heads of 256: as many as the ring has stages)
   static constexpr int GROUPS = D == 256 && N == 16 ? 2 : 64 / N;
-  static constexpr int THREADS = 128 * GROUPS + 128;
+  static constexpr int THREADS = 128 * GROUPS + 256;
+  // registers a thread: what the launch gives, what softmax threads take, what the other two warpgroups keep
+  static constexpr int REGS = GROUPS == 4 ? 80 : GROUPS == 2 ? 128 : 168;
+  static constexpr int RSOFT = GROUPS == 4 ? 96 : GROUPS == 2 ? 168 : 232, RREST = GROUPS == 4 ? 48 : GROUPS == 2 ? 80 : 104;
+  static_assert(128 * GROUPS * RSOFT + 256 * RREST <= THREADS * REGS && THREADS * REGS <= 65536, "registers");
   static constexpr int PW = D < 128 ? D : 128;       // bytes of a panel row (a TMA box row)
   static constexpr int NP = D / PW;                  // panels
   static constexpr int PANEL = kTile * PW;
@@ -67,8 +71,9 @@ struct Cfg {
   static constexpr int FIXED = 1024 + QB * Q + GROUPS * P + 8192;
   static constexpr int SLOTS = (232448 - FIXED) / KV;
   // key tiles are done with after the scores, value tiles a softmax later
-  static constexpr int SK0 = SLOTS * 2 / 5 < 2 ? 2 : SLOTS * 2 / 5, SV0 = SLOTS - SK0;
-  static constexpr int SK = SK0 > 6 ? 6 : SK0, SV = SV0 > 8 ? 8 : SV0;
+  // (even numbers: a stage is always filled by the same one of two warps)
+  static constexpr int SK0 = SLOTS * 2 / 5 < 2 ? 2 : SLOTS * 2 / 5, SK = SK0 > 6 ? 6 : SK0 & ~1;
+  static constexpr int SV = SLOTS - SK > 8 ? 8 : (SLOTS - SK) & ~1;
   static constexpr int METAS = 32;                   // tiles between a key tile's issue and its outputs: fewer
   static constexpr int SMEM = FIXED + (SK + SV) * KV;
   static_assert(SK >= 2 && SV >= 2 && GROUPS * (SCOL + MB * OCOL) <= 512, "shared and tensor memory");
@@ -81,11 +86,15 @@ struct TileMeta {
   int flags;             // 1: some of its rows hold no key; 2: some row of the pair does not see all of it
   float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
 };
+struct ValueMeta {
+  int after, rows, groups, pad;  // as above; rows before the sequence's end; bits of the groups that hold keys
+};
 // What a query buffer holds besides the rows.
 template <int N>
 struct PairMeta {
   int R, n_tiles, i0, i1;       // rows, tiles, and which of this CTA's tiles they are
-  int64_t first, base;          // its first tile on the line; its first row's output
+  int first, pad;               // its first tile on the line
+  int64_t base;                 // its first row's output
   alignas(16) float rc[N];      // the row's power of two * scale * log2(e)
   int pos[N];
   int64_t off[N];               // the row's output, from the first one's
@@ -94,6 +103,7 @@ template <int D, int N>
 struct Shared {
   using C = Cfg<D, N>;
   TileMeta tile[C::METAS];
+  ValueMeta value[C::METAS];
   PairMeta<N> pair[C::QB];
   alignas(16) float ref[C::GROUPS][N];
   alignas(16) float grow[C::GROUPS][N];
@@ -101,7 +111,7 @@ struct Shared {
   uint64_t kfull[C::SK], kfree[C::SK], vfull[C::SV], vfree[C::SV];
   uint64_t qfull[C::QB], qfree[C::QB];
   uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
-  uint64_t summed, joined, ended;
+  uint64_t summed, joined, ended[2];
   uint32_t tmem;
   int ticket[C::GROUPS];
 };
@@ -113,6 +123,16 @@ struct DecodeArgs {
   float* part_o;   // [2 * grid][N][D]
 };
 
+// mbar_wait_bounded in few instructions: this kernel's many roles share one instruction cache.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  do {
+    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
+  } while (global_ns() - t0 < kWaitLimitNs);
+  atomicExch(status, kStatusTimeout);
+  return false;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -150,22 +170,27 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// Shared-memory matrix descriptor (version 1): start, leading and stride byte offsets, swizzle
-// (0 none, 2 128 bytes, 4 64 bytes).
-__device__ __forceinline__ uint64_t mat_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(lbo >> 4) << 16 | (uint64_t)(sbo >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)swizzle << 61;
-}
+// Shared-memory matrix descriptor (version 1) as its two halves: start and leading byte offset; stride
+// byte offset and swizzle (0 none, 2 128 bytes, 4 64 bytes).  Adding bytes / 16 to the low half moves the start.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return sbo >> 4 | 1u << 14 | swizzle << 29; }
 // kind::f8f6f4, E4M3 x E4M3 -> fp32, M = 128; ta, tb: A, B lie M- or N-contiguous.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int n, int ta, int tb) {
   return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+template <uint32_t AHI, uint32_t BHI, uint32_t IDESC>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t alo, uint32_t blo, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-      "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d), "r"(alo), "n"(AHI), "r"(blo), "n"(BHI),
+      "n"(IDESC), "r"(acc)
       : "memory");
+}
+// One lane of the warp, chosen so that the compiler knows the branch on it takes one thread.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // Barrier of a softmax group's four warps that returns whether any thread's v is set.
 __device__ __forceinline__ bool any_of(int group, bool v) {
@@ -199,9 +224,20 @@ __device__ __forceinline__ int first_key(const Seq& s, const AttnArgs& a) {
   const int64_t p = (int64_t)s.len - s.rows + 1 - a.window;
   return a.window && p > 0 ? ((int)min(p, (int64_t)s.len) >> a.c.page_log2) << a.c.page_log2 : 0;
 }
+// (the host keeps all of a call's tiles below 2^31)
 __device__ __forceinline__ int tiles_of(const Seq& s, const AttnArgs& a) {
   return s.rows > 0 ? max(1, (s.len - first_key(s, a) + kTile - 1) / kTile) : 0;
 }
+
+// The line cut into even parts: CTA c's begins at begin(c); whose tile u is.
+struct Share {
+  int each, more;
+  __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int owner(int u) const {
+    const int big = more * (each + 1);
+    return u < big ? u / (each + 1) : more + (u - big) / each;
+  }
+};
 
 // A place on the line: tile k of head h of sequence b, whose pairs have n tiles.  A whole warp walks; lane
 // b holds sequence b of the first 32.
@@ -210,11 +246,11 @@ struct Walk {
   Seq sq, mine;
 
   // tiles of all sequences, each counted once (all its KV heads have as many)
-  __device__ __forceinline__ int64_t count(const AttnArgs& a, int lane, bool* bad) {
+  __device__ __forceinline__ int count(const AttnArgs& a, int lane, bool* bad) {
     const KvArgs& c = a.c;
     mine = {0, 0, 0};
     if (lane < c.n_seqs) mine = seq_of(c, lane, bad);
-    int64_t total = __reduce_add_sync(0xFFFFFFFFu, tiles_of(mine, a));
+    int total = __reduce_add_sync(0xFFFFFFFFu, tiles_of(mine, a));
     for (int base = 32; base < c.n_seqs; base += 32) {
       int t = 0;
       if (base + lane < c.n_seqs) t = tiles_of(seq_of(c, base + lane, bad), a);
@@ -227,9 +263,9 @@ struct Walk {
     sq.rows = __shfl_sync(0xFFFFFFFFu, t.rows, who);
     sq.len = __shfl_sync(0xFFFFFFFFu, t.len, who);
   }
-  __device__ __forceinline__ void find(const AttnArgs& a, int64_t unit, int lane) {
+  __device__ __forceinline__ void find(const AttnArgs& a, int unit, int lane) {
     const KvArgs& c = a.c;
-    int64_t left = unit;
+    int left = unit;
     bool ignore = false;
     b = 0, n = 1;
     sq = {0, 0, 0};
@@ -240,25 +276,25 @@ struct Walk {
         if (base + lane < c.n_seqs) t = seq_of(c, base + lane, &ignore);
       }
       const int un = tiles_of(t, a);
-      int64_t sum = (int64_t)un * c.hkv;
+      int sum = un * c.hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
         if (lane >= o) sum += v;
       }
-      const int64_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      const int all = __shfl_sync(0xFFFFFFFFu, sum, 31);
       if (left < all) {
         const int who = __ffs(__ballot_sync(0xFFFFFFFFu, sum > left)) - 1;
         b = base + who;
         n = __shfl_sync(0xFFFFFFFFu, un, who);
-        left -= __shfl_sync(0xFFFFFFFFu, sum, who) - (int64_t)n * c.hkv;
+        left -= __shfl_sync(0xFFFFFFFFu, sum, who) - n * c.hkv;
         take(t, who);
         break;
       }
       left -= all;
     }
-    h = (int)(left / n);
-    k = (int)(left - (int64_t)h * n);
+    h = left / n;
+    k = left - h * n;
     lo = first_key(sq, a);
   }
   // the next pair; there is one
@@ -280,33 +316,79 @@ struct Walk {
   }
 };
 
-// The joining of a pair's parts by the CTA that finished last: one group's 128 threads.
+// The joining of a pair's parts by the CTA that finished last: one group's 128 threads.  weights: shared
+// memory for N floats a part, 32 parts at a time.
 template <int D, int N>
-__device__ __noinline__ void join_parts(const DecodeArgs& da, int tid, int R, int G, int64_t base, int64_t c0, int parts,
-                                        bool at_start) {
+__device__ __noinline__ void join_parts(const DecodeArgs& da, int grp, int tid, int R, int G, int64_t base, int c0, int parts,
+                                        bool at_start, void* scratch) {
   const AttnArgs& a = da.a;
-  for (int e = tid; e < R * (D / 4); e += 128) {
-    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-    float4 v = make_float4(0, 0, 0, 0);
+  constexpr int V = D / 4, E = (N * V + 127) / 128;  // float4s a row, and a thread
+  auto slot = [&](int q) { return (int64_t)(2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0)); };
+  float* wt = static_cast<float*>(scratch);  // [32][N] weights, then [N] 1 / sum
+  float* inv = wt + 32 * N;
+  // references and sums: a warp a row, a lane a part
+  for (int row = tid >> 5; row < R; row += 4) {
+    const int lane = tid & 31;
     float top = -INFINITY, sum = 0.0f;
-    for (int q = 0; q < parts; ++q) {
-      const int64_t sl = 2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0);
-      top = fmaxf(top, __ldcg(&da.part_ml[sl * N + row]).x);
+    for (int q = lane; q < parts; q += 32) top = fmaxf(top, __ldcg(&da.part_ml[slot(q) * N + row]).x);
+    top = warp_max(top);
+    for (int q = lane; q < parts; q += 32) {
+      const float2 z = __ldcg(&da.part_ml[slot(q) * N + row]);
+      sum = fmaf(z.y, z.x == -INFINITY ? 0.0f : ex2(z.x - top), sum);
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) {
+      inv[row] = sum == 0.0f ? 0.0f : 1.0f / sum;
+      inv[N + row] = top;
+    }
+  }
+  any_of(grp, false);
+#pragma unroll 1
+  for (int e0 = 0; e0 < E; e0 += 4) {
+    float4 v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = make_float4(0, 0, 0, 0);
+    for (int q0 = 0; q0 < parts; q0 += 32) {
+      const int m = min(32, parts - q0);
+      for (int t = tid; t < m * N; t += 128) {
+        const int q = t / N, row = t % N;
+        float f = 0.0f;
+        if (row < R) {
+          const float z = __ldcg(&da.part_ml[slot(q0 + q) * N + row]).x;
+          f = z == -INFINITY ? 0.0f : ex2(z - inv[N + row]);
+        }
+        wt[t] = f;
+      }
+      any_of(grp, false);
 #pragma unroll 4
-    for (int q = 0; q < parts; ++q) {
-      const int64_t sl = 2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0);
-      const float2 z = __ldcg(&da.part_ml[sl * N + row]);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(da.part_o + (sl * N + row) * D + d));
-      const float f = z.x == -INFINITY ? 0.0f : ex2(z.x - top);
-      v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
-      sum = fmaf(z.y, f, sum);
+      for (int q = 0; q < m; ++q) {
+        const float4* src = reinterpret_cast<const float4*>(da.part_o + slot(q0 + q) * N * D);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int e = (e0 + x) * 128 + tid;
+          if (e < R * V) {
+            const float4 y = __ldcg(src + e);
+            const float f = wt[q * N + e / V];
+            v[x].x = fmaf(y.x, f, v[x].x), v[x].y = fmaf(y.y, f, v[x].y);
+            v[x].z = fmaf(y.z, f, v[x].z), v[x].w = fmaf(y.w, f, v[x].w);
+          }
+        }
+      }
+      any_of(grp, false);
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int t = row / G, g = row - t * G;
-    const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x * inv, v.y * inv), y1 = __floats2bfloat162_rn(v.z * inv, v.w * inv);
-    *reinterpret_cast<uint2*>(a.out + base + t * a.ldo + g * a.hso + d) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int e = (e0 + x) * 128 + tid;
+      if (e < R * V) {
+        const int row = e / V, d = (e % V) * 4, t = row / G, g = row - t * G;
+        const float f = inv[row];
+        const __nv_bfloat162 y0 = __floats2bfloat162_rn(v[x].x * f, v[x].y * f);
+        const __nv_bfloat162 y1 = __floats2bfloat162_rn(v[x].z * f, v[x].w * f);
+        *reinterpret_cast<uint2*>(a.out + base + t * a.ldo + g * a.hso + d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+      }
+    }
   }
 }
 
@@ -349,7 +431,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     }
     mbar_init(&sh.summed, NG);
     mbar_init(&sh.joined, 1);
-    mbar_init(&sh.ended, 1);
+    mbar_init(&sh.ended[0], 1);
+    mbar_init(&sh.ended[1], 1);
     fence_mbar_init();
   }
   if (warp == kMma) {
@@ -359,60 +442,64 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   pdl_wait();
   Walk w;
   bool bad = false;
-  const int64_t total = w.count(a, lane, &bad) * c.hkv;
+  const int total = w.count(a, lane, &bad) * c.hkv;
   if (bad && warp == 0 && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
   // with no more CTAs than tiles, each has one at least
-  const int64_t grid = min((int64_t)gridDim.x, total), cta = blockIdx.x;
-  const int64_t u0 = cta < grid ? cta * total / grid : 0, u1 = cta < grid ? (cta + 1) * total / grid : 0;
+  const int grid = min((int)gridDim.x, total), cta = blockIdx.x;
+  const Share share = {total / max(grid, 1), total % max(grid, 1)};
+  const int u0 = cta < grid ? share.begin(cta) : 0, u1 = cta < grid ? share.begin(cta + 1) : 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int n = (int)(u1 - u0);
+  const int n = u1 - u0;
   const uint32_t otm = tmem + NG * C::SCOL;  // the groups' O follow their S
 
-  if (n > 0 && (warp == kMma + 1 || warp == kMma + 2)) {  // -------------------------------- key tiles, value tiles
-    // Lanes 8q .. 8q + 7 look after tile 4j + q: its eight groups of 16 keys.  Four tiles' page ids are
-    // fetched by one load, while the four before them are issued.
-    const bool keys = warp == kMma + 1;
+  if (n > 0 && warp >= kMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
+    if (warp > kMma && warp < kMma + 6) w.find(a, u0, lane);
+  if (warp > kMma && warp < kMma + 5) {  // -------------------------------------- key tiles, value tiles
+    // Two warps for the keys, two for the values, each with every other tile: a tile's copies take
+    // one warp some 600 to 1100 cycles to issue.  Lanes 8q .. 8q + 7 look after tile 8j + 2q + odd: its eight
+    // groups of 16 keys.  Four tiles' page ids are fetched by one load, while the four before them are issued.
+    const bool keys = warp < kMma + 3;
+    const int odd = (warp - kMma - 1) & 1;
     const int stages = keys ? C::SK : C::SV;
     uint8_t* slots = keys ? ring : vring;
     uint64_t* full = keys ? sh.kfull : sh.vfull;
     uint64_t* free_ = keys ? sh.kfree : sh.vfree;
     const CUtensorMap* map = keys ? &kmap : &vmap;
-    w.find(a, u0, lane);
     const int P = 1 << c.page_log2, box = min(P, kTile);
-    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, edge = 0, walked = 0, i0 = 0;
-    auto prepare = [&]() {  // the next four tiles
+    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, edge = 0, walked = 0, i0 = 0, ready = 0;
+    bool dead = false;
+    int s = odd, i = odd, lap = 0;
+    while (i < n && !dead) {
+      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge, cready = ready;
+      // the next four tiles (the first time, the first four)
       int b = 0;
       len = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (walked < n) {
-          if (lane >> 3 == q) {
+      ready = 0;
+#pragma unroll 1
+      for (int q = 0; q < 8 && walked < n; ++q) {
+        if ((q & 1) == odd) {
+          if (lane >> 3 == q >> 1) {
             b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + w.k * kTile, after = walked - i0;
             // the rows stand at len - rows .. len - 1
             edge = tok0 + kTile - 1 > len - w.sq.rows || (a.window && tok0 <= (int64_t)len - 1 - a.window);
           }
-          if (++walked < n && ++w.k == w.n) {
-            w.next_pair(a);
-            i0 = walked;
-          }
+          ++ready;
+        }
+        if (++walked < n && ++w.k == w.n) {
+          w.next_pair(a);
+          i0 = walked;
         }
       }
-      const int64_t tok = (int64_t)tok0 + 16 * (lane & 7);
       id = -1;
-      if (tok < len) id = c.pages[(int64_t)b * c.page_stride + (tok >> c.page_log2)];
-    };
-    prepare();
-    bool dead = false;
-    int s = 0, i = 0;
-    uint32_t lap = 0;
-    while (i < n && !dead) {
-      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge;
-      if (walked < n) prepare();
-      for (int q = 0; q < 4 && i < n; ++q, ++i) {
-        if (lap && !mbar_wait_bounded(&free_[s], (lap - 1) & 1, c.status)) dead = true;
+      const int64_t next = (int64_t)tok0 + 16 * (lane & 7);
+      if (next < len) id = c.pages[(int64_t)b * c.page_stride + (next >> c.page_log2)];
+#pragma unroll 1
+      for (int q = 0; q < cready; ++q, i += 2) {
+        if (lap && !wait(&free_[s], (lap - 1) & 1, c.status)) dead = true;
         if (__any_sync(0xFFFFFFFFu, dead)) {
           dead = true;
           break;
@@ -430,6 +517,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             const bool cut = __any_sync(0xFFu << (8 * q), !ok || tok + 16 > clen);
             if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = (cut ? 3 : 0) | (cedge ? 2 : 0);
             if (!ok) m.ks[gl] = m.vs[gl] = 0.0f;
+          } else {
+            const uint32_t groups = __ballot_sync(0xFFu << (8 * q), ok) >> (8 * q);
+            if (gl == 0) {
+              ValueMeta& vm = sh.value[i % C::METAS];
+              vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu);
+            }
           }
           if (ok && (16 * gl) % box == 0) {
             uint8_t* dst = slots + s * C::KV + 16 * gl * C::PW;
@@ -449,32 +542,34 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           }
         }
         __syncwarp();
-        if (++s == stages) s = 0, ++lap;
+        s += 2;
+        if (s >= stages) s -= stages, ++lap;
       }
     }
     // no copy is left in flight into this CTA's shared memory when it ends: the last stages filled
-    for (int j = max(0, i - stages); j < i; ++j)
-      mbar_wait_bounded(&full[j % stages], (uint32_t)(j / stages) & 1u, c.status);
-  } else if (n > 0 && warp == kMma + 3) {  // ----------------------------------------------- query rows
+#pragma unroll 1
+    for (int j = max(odd, i - stages); j < i; j += 2)
+      wait(&full[j % stages], (uint32_t)(j / stages) & 1u, c.status);
+  } else if (warp == kMma + 5) {  // ----------------------------------------------- query rows
     // D / 16 lanes a row, 16 elements each
     constexpr int TPR = D / 16, RPP = 32 / TPR;
     const int t = lane, part = t % TPR;
-    w.find(a, u0, lane);
-    int64_t u = u0;
+    int u = u0;
     bool dead = false;
     for (int p = 0; u < u1; ++p) {
       const int qb = p % C::QB;
-      if (p >= C::QB && !mbar_wait_bounded(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
+      if (p >= C::QB && !wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
       if (__any_sync(0xFFFFFFFFu, dead)) break;
       PairMeta<N>& m = sh.pair[qb];
       const int R = min(w.sq.rows * G, N), first_pos = w.sq.len - w.sq.rows;
-      const int64_t next = u + w.n - w.k;
+      const int next = u + w.n - w.k;
       if (t == 0) {
         m.R = R, m.n_tiles = w.n, m.first = u - w.k;
-        m.i0 = (int)(u - u0), m.i1 = (int)(min(next, u1) - u0);
+        m.i0 = u - u0, m.i1 = min(next, u1) - u0;
         m.base = (int64_t)w.sq.start * a.ldo + (int64_t)w.h * G * a.hso;
       }
       uint8_t* qd = qbuf + qb * C::Q;
+#pragma unroll 1
       for (int r0 = 0; r0 < N; r0 += RPP) {
         const int row = r0 + t / TPR;
         const bool in = row < R;
@@ -533,112 +628,102 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       u = next;
       if (u < u1) w.next_pair(a);
     }
-  } else if (n > 0 && warp == kMma) {  // ---------------------------------------------------- MMAs
-    constexpr uint32_t kSwz = D == 64 ? 4 : 2;
-    constexpr uint32_t kSbo = 8 * C::PW;
-    constexpr uint32_t kQk = idesc_e4m3(2 * N, 0, 0), kPv = idesc_e4m3(3 * N, 1, 1);
-    // Two queues, scores and outputs, each in the tiles' order; whichever has its operands goes.
-    int js = 0, jo = 0, ks = 0, vs = 0, p = 0, qb = 0;    // tiles issued, ring stages, pairs begun by the scores
-    uint32_t kpar = 0, vpar = 0, qpar = 0;
-    int gs = 0, go = 0;                                   // their groups, and the parities of the groups' turns
-    uint32_t spar = 1, opar = 0;
-    bool begun = true;                                    // the score queue's pair has its query rows
-    unsigned long long t0 = 0;
-    int idle = 0;
-    while (jo < n) {
-      bool moved = false;
-      if (js < n && __all_sync(0xFFFFFFFFu, mbar_test(&sh.kfull[ks], kpar))) {
-        const TileMeta& m = sh.tile[js % C::METAS];
-        begun = m.after != 0 || __all_sync(0xFFFFFFFFu, mbar_test(&sh.qfull[qb], qpar));
-        if (begun && (js < NG || __all_sync(0xFFFFFFFFu, mbar_test(&sh.sfree[gs], spar)))) {
-          tc_fence_after();
-          if (m.after == 0) {  // the pair's query buffer
-            p = qb;
-            if (++qb == C::QB) qb = 0, qpar ^= 1;
-          }
-          if (lane == 0) {
-            const uint32_t ka = smem_u32(ring + ks * C::KV), qa = smem_u32(qbuf + p * C::Q);
-#pragma unroll
-            for (int x = 0; x < D / 32; ++x) {
-              const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
-              mma_e4m3(tmem + gs * C::SCOL, mat_desc(ka + panel * C::PANEL + off, 16, kSbo, kSwz),
-                       mat_desc(qa + panel * C::QPANEL + off, 16, kSbo, kSwz), kQk, x > 0);
-            }
-            mma_commit(&sh.sfull[gs]);
-            mbar_arrive(&sh.sfull[gs]);  // passes the tile's description on to the softmax group
-            mma_commit(&sh.kfree[ks]);
-          }
-          __syncwarp();
-          ++js;
-          if (++ks == C::SK) ks = 0, kpar ^= 1;
-          if (++gs == NG) gs = 0, spar ^= 1;
-          moved = true;
-        }
-      }
-      if (jo < js && __all_sync(0xFFFFFFFFu, mbar_test(&sh.pfull[go], opar)) &&
-          __all_sync(0xFFFFFFFFu, mbar_test(&sh.vfull[vs], vpar))) {
-        const TileMeta& m = sh.tile[jo % C::METAS];
-        uint8_t* vt = vring + vs * C::KV;
-        if (m.flags & 1) {  // rows without a key hold anything, NaN codes too: they must be numbers for P = 0
-          for (int r = lane; r < kTile; r += 32) {
-            if (m.tok0 + r >= m.len || m.ks[r >> 4] == 0.0f) {
+  } else if (warp == kMma) {  // ---------------------------------------------------- score MMAs
+    // One thread issues them, and its instructions set the pace: descriptors are one add each, and the output
+    // MMAs have a warp of their own.
+    constexpr uint32_t kSwz = D == 64 ? 4 : 2, kHi = desc_hi(8 * C::PW, kSwz), kQk = idesc_e4m3(2 * N, 0, 0);
+    int ks = 0, g = 0, qb = -1;
+    uint32_t kpar = 0, spar = 1, qpar = 1;
+    const uint32_t k0 = desc_lo(smem_u32(ring), 16), q0 = desc_lo(smem_u32(qbuf), 16);
+    bool dead = false;
 #pragma unroll 1
-              for (int x = 0; x < C::NP; ++x)
-#pragma unroll
-                for (int b = 0; b < C::PW; b += 16)
-                  *reinterpret_cast<uint4*>(vt + x * C::PANEL + r * C::PW + b) = make_uint4(0, 0, 0, 0);
-            }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t va = smem_u32(vt), pa = smem_u32(pbuf + go * C::P), od = otm + go * (C::MB * C::OCOL);
-          const bool first = m.after < NG;  // the group's first tile of the pair
-#pragma unroll
-          for (int mb = 0; mb < C::MB; ++mb)
-#pragma unroll
-            for (int x = 0; x < kTile / 32; ++x) {
-              // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
-              // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
-              // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
-              mma_e4m3(od + mb * C::OCOL, mat_desc(va + mb * C::PANEL + x * 32 * C::PW, C::PANEL, kSbo, kSwz),
-                       mat_desc(pa + x * 32 * 16, 128, kTile * 16, 0), kPv, !(first && x == 0));
-            }
-          mma_commit(&sh.pvdone[go]);
-          mma_commit(&sh.vfree[vs]);
-        }
-        __syncwarp();
-        ++jo;
-        if (++vs == C::SV) vs = 0, vpar ^= 1;
-        if (++go == NG) go = 0, opar ^= 1;
-        moved = true;
+    for (int i = 0; i < n && !dead; ++i) {
+      dead = !wait(&sh.kfull[ks], kpar, c.status);
+      if (!dead && sh.tile[i % C::METAS].after == 0) {
+        if (++qb == C::QB) qb = 0;
+        if (qb == 0) qpar ^= 1;
+        dead = !wait(&sh.qfull[qb], qpar, c.status);
       }
-      if (moved) {
-        idle = 0;
-        t0 = 0;
-      } else if (++idle == 4096) {  // the limit of every wait, checked now and then
-        idle = 0;
-        const unsigned long long t = global_ns();
-        bool late = false;
-        if (t0 == 0)
-          t0 = t;
-        else
-          late = t - t0 > kWaitLimitNs;
-        if (__any_sync(0xFFFFFFFFu, late)) {
-          if (lane == 0) atomicExch(c.status, kStatusTimeout);
-          break;
+      if (!dead && i >= NG) dead = !wait(&sh.sfree[g], spar, c.status);
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      tc_fence_after();
+      if (!dead && elect()) {
+        const uint32_t ka = k0 + ks * (C::KV / 16), qa = q0 + qb * (C::Q / 16), d = tmem + g * C::SCOL;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
+          mma_e4m3<kHi, kHi, kQk>(d, ka + (panel * C::PANEL + off) / 16, qa + (panel * C::QPANEL + off) / 16, x > 0);
         }
+        mma_commit(&sh.sfull[g]);
+        mbar_arrive(&sh.sfull[g]);  // passes the tile's description on to the softmax group
+        mma_commit(&sh.kfree[ks]);
       }
+      __syncwarp();
+      if (++ks == C::SK) ks = 0, kpar ^= 1;
+      if (++g == NG) g = 0, spar ^= 1;
     }
     // every MMA has ended before the CTA's memory goes
-    if (lane == 0) {
-      mma_commit(&sh.ended);
-      mbar_wait_bounded(&sh.ended, 0, c.status);
+    if (elect()) {
+      mma_commit(&sh.ended[0]);
+      wait(&sh.ended[0], 0, c.status);
     }
     __syncwarp();
-  } else if (n > 0 && warp < kMma) {  // ------------------------------------------------------ softmax, a key a thread
+  } else if (warp == kMma + 6) {  // ------------------------------------------------ output MMAs
+    // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
+    // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
+    // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
+    constexpr uint32_t kHi = desc_hi(8 * C::PW, D == 64 ? 4 : 2), kPHi = desc_hi(kTile * 16, 0);
+    constexpr uint32_t kPv = idesc_e4m3(3 * N, 1, 1);
+    int vs = 0, g = 0;
+    uint32_t vpar = 0, ppar = 0;
+    const uint32_t v0 = desc_lo(smem_u32(vring), C::PANEL), p0 = desc_lo(smem_u32(pbuf), 128);
+    bool dead = false;
+#pragma unroll 1
+    for (int i = 0; i < n && !dead; ++i) {
+      dead = !wait(&sh.vfull[vs], vpar, c.status);
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      if (dead) break;
+      const ValueMeta m = sh.value[i % C::METAS];
+      if (m.groups != 0xFF || m.rows < kTile) {  // rows without a key hold anything, NaN codes too: numbers for P = 0
+        uint8_t* vt = vring + vs * C::KV;
+#pragma unroll 1
+        for (int gr = 0; gr < 8; ++gr) {  // groups of 16 rows: from row `from` of each on
+          const int from = (m.groups >> gr & 1) ? min(max(m.rows - 16 * gr, 0), 16) : 0;
+#pragma unroll 4
+          for (int e = from * (C::PW / 16) + lane; e < C::PW; e += 32)
+#pragma unroll
+            for (int x = 0; x < C::NP; ++x)
+              *reinterpret_cast<uint4*>(vt + x * C::PANEL + (gr * C::PW + e) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      dead = !wait(&sh.pfull[g], ppar, c.status);
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      tc_fence_after();
+      const uint32_t acc = m.after >= NG;  // not the group's first tile of the pair
+      if (!dead && elect()) {
+        const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + g * (C::MB * C::OCOL);
+#pragma unroll
+        for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+          for (int x = 0; x < kTile / 32; ++x)
+            mma_e4m3<kHi, kPHi, kPv>(d + mb * C::OCOL, va + (mb * C::PANEL + x * 32 * C::PW) / 16, pa + x * 32, x ? 1u : acc);
+        mma_commit(&sh.pvdone[g]);
+        mma_commit(&sh.vfree[vs]);
+      }
+      __syncwarp();
+      if (++vs == C::SV) vs = 0, vpar ^= 1;
+      if (++g == NG) g = 0, ppar ^= 1;
+    }
+    if (elect()) {
+      mma_commit(&sh.ended[1]);
+      wait(&sh.ended[1], 0, c.status);
+    }
+    __syncwarp();
+  }
+  } else if (n > 0) {  // ------------------------------------------------------------------- softmax, a key a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::RSOFT));
     const int grp = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
     const uint32_t st = tmem + lane_base + grp * C::SCOL, ot = otm + lane_base + grp * (C::MB * C::OCOL);
@@ -650,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     uint32_t turn = 0;  // tiles of this group so far
     for (int p = 0; i1 < n; ++p) {
       const PairMeta<N>& pm = sh.pair[p % C::QB];
-      if (!mbar_wait_bounded(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) dead = true;
+      if (!wait(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) dead = true;
       if (any_of(grp, dead)) break;
       const int R = pm.R, i0 = pm.i0;
       i1 = pm.i1;
@@ -661,7 +746,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       for (int i = mine; i < i1; i += NG) {
         const bool first = i == mine;
         const TileMeta& tm = sh.tile[i % C::METAS];
-        if (!mbar_wait_bounded(&sh.sfull[grp], turn & 1, c.status)) dead = true;
+        if (!wait(&sh.sfull[grp], turn & 1, c.status)) dead = true;
         tc_fence_after();
         // the key's scores: both terms of every row
         float x[N];
@@ -682,7 +767,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         const float lvs = lg2(vs), ivs = ks == 0.0f ? 0.0f : rcp(vs);
         const int flags = tm.flags, tok = tm.tok0 + tid, most = tm.len;
         // the group's references are free once the pair before has been joined
-        if (first && p > 0 && !mbar_wait_bounded(&sh.joined, (uint32_t)(p - 1) & 1u, c.status)) dead = true;
+        if (first && p > 0 && !wait(&sh.joined, (uint32_t)(p - 1) & 1u, c.status)) dead = true;
         bool over = first;
 #pragma unroll
         for (int r = 0; r < N; r += 4) {
@@ -709,10 +794,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             }
           }
         }
-        if (any_of(grp, over || dead)) {
+        if (first || any_of(grp, over || dead)) {
           // some key passes its row's reference, or there is none yet: new references, and what was summed up
           // moves to them
-          if (any_of(grp, dead)) break;
 #pragma unroll
           for (int r = 0; r < N; ++r) {
             if (r < R) {
@@ -720,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
               if (lane == 0) sh.red[grp][wq][r] = top;
             }
           }
-          any_of(grp, false);
+          if (any_of(grp, dead)) break;
           if (tid >= R && tid < N) ref[tid] = INFINITY;  // not a row: nothing passes it
           if (tid < R) {
             const float* red = sh.red[grp][0];
@@ -732,7 +816,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           }
           any_of(grp, false);
           if (!first) {
-            if (!mbar_wait_bounded(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
+            if (!wait(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
             if (any_of(grp, dead)) break;
             tc_fence_after();
 #pragma unroll
@@ -755,7 +839,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           }
         }
         // P, its sums and its terms; the buffer is free once the group's tile before has been multiplied
-        if (turn && !mbar_wait_bounded(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
+        if (turn && !wait(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
 #pragma unroll
         for (int r = 0; r < N; r += 16) {
           uint32_t t0[4] = {0, 0, 0, 0}, t1[4] = {0, 0, 0, 0}, t2[4] = {0, 0, 0, 0};
@@ -806,7 +890,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             if (lane == 0) sh.red[grp][wq][r] = v;
           }
         }
-        if (!mbar_wait_bounded(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
+        if (!wait(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
         if (any_of(grp, dead)) break;
         if (tid < R) {
           const float* red = sh.red[grp][0];
@@ -817,14 +901,14 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       const bool join = (i1 - 1) % NG == grp;
       if (tid == 0) mbar_arrive(&sh.summed);
       if (join) {
-        if (!mbar_wait_bounded(&sh.summed, (uint32_t)p & 1u, c.status)) dead = true;
+        if (!wait(&sh.summed, (uint32_t)p & 1u, c.status)) dead = true;
         if (any_of(grp, dead)) break;
         tc_fence_after();
-        const int64_t first_tile = pm.first;
+        const int first_tile = pm.first;
         const int64_t base = pm.base;
         const int n_tiles = pm.n_tiles, parts_here = min(NG, i1 - i0);
         const bool whole = first_tile >= u0 && first_tile + n_tiles <= u1;
-        const int64_t slot = 2 * cta + (first_tile <= u0 ? 0 : 1);
+        const int slot = 2 * cta + (first_tile <= u0 ? 0 : 1);
         // row's factors of the groups that took part, and its reference and sum
         if (tid < R) {
           float top = -INFINITY, sum = 0.0f;
@@ -875,7 +959,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
                   }
                 }
               } else {
-                float* dst = da.part_o + (slot * N + r) * D + d;
+                float* dst = da.part_o + ((int64_t)slot * N + r) * D + d;
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                   if (r + e < R) dst[e * D] = o[e];
@@ -892,13 +976,11 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         }
         if (!whole) {
           // the CTA whose ticket completes the pair joins the parts, in their order on the line
-          auto owner = [&](int64_t unit) { return ((unit + 1) * grid - 1) / total; };
-          const int64_t c0 = owner(first_tile), c1 = owner(first_tile + n_tiles - 1);
-          const int parts = (int)(c1 - c0 + 1);
+          const int c0 = share.owner(first_tile), parts = share.owner(first_tile + n_tiles - 1) - c0 + 1;
           if (tid == 0) sh.ticket[grp] = ticket_add(da.counters + c0, 1);
           any_of(grp, false);
           if (sh.ticket[grp] == parts - 1) {
-            join_parts<D, N>(da, tid, R, G, base, c0, parts, c0 * total / grid == first_tile);
+            join_parts<D, N>(da, grp, tid, R, G, base, c0, parts, share.begin(c0) == first_tile, pbuf + grp * C::P);
             if (tid == 0) da.counters[c0] = 0;
           }
         }
@@ -964,6 +1046,7 @@ int launch_attn_decode(const AttnArgs& a, int head_dim, int64_t rows, const Devi
   da.part_o = reinterpret_cast<float*>(w + 2 * (size_t)dev.sms * r * sizeof(float2));
   // no more CTAs than tiles that there can be
   const int64_t most = (int64_t)a.c.n_seqs * a.c.hkv * ((a.c.max_len + kTile - 1) / kTile);
+  if (most > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;  // the line's places are 32-bit
   const int grid = (int)std::min<int64_t>(dev.sms, most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (head_dim) {
