@@ -39,13 +39,13 @@ __global__ void __launch_bounds__(128) attn_simple_kernel(const AttnArgs a) {
   if (bad && threadIdx.x == 0) atomicExch(c.status, kStatusInvalid);
   if (row < s.start || row >= (int64_t)s.start + s.rows) return;
   const int pos = s.len - s.rows + (int)(row - s.start);
-  const int from = a.window && pos + 1 > a.window ? (int)(pos + 1 - a.window) : 0;
+  const int from = pos >= a.window ? pos + 1 - a.window : 0;  // a row before the sequence (pos < 0) sees nothing
   float q[E], o[E], m = -INFINITY, l = 0.0f;
   for (int e = 0; e < E; ++e) {
     q[e] = __uint_as_float((uint32_t)a.q[row * a.ldq + head * a.hsq + lane * E + e] << 16);
     o[e] = 0.0f;
   }
-  for (int t = from + warp; t <= pos; t += 4) {
+  for (int t = from + warp; pos >= 0 && t <= pos; t += 4) {
     const int id = c.pages[(int64_t)lo * c.page_stride + (t >> c.page_log2)];
     if (id < 0 || id >= c.n_pages) {
       if (lane == 0) atomicExch(c.status, kStatusInvalid);

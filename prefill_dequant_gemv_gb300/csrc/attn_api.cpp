@@ -186,7 +186,7 @@ extern "C" qg_status qattn(const qg_kv_cache* cache, const qg_kv_batch* batch, i
   a.ldo = ldo;
   a.hso = hso;
   a.scale = scale;
-  a.window = window;
+  a.window = window && window < 0x7FFFFFFF ? (int)window : 0x7FFFFFFF;
   a.hq = n_q_heads;
   return (qg_status)launch_attn(a, cache->head_dim, p, dev, workspace, stream);
 }

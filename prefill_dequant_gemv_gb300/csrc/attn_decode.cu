@@ -222,7 +222,7 @@ __device__ __forceinline__ float lg2(float x) {
 // there are rows, so that rows without a key are written).
 __device__ __forceinline__ int first_key(const Seq& s, const AttnArgs& a) {
   const int64_t p = (int64_t)s.len - s.rows + 1 - a.window;
-  return a.window && p > 0 ? ((int)min(p, (int64_t)s.len) >> a.c.page_log2) << a.c.page_log2 : 0;
+  return p > 0 ? ((int)p >> a.c.page_log2) << a.c.page_log2 : 0;
 }
 // (the host keeps all of a call's tiles below 2^31)
 __device__ __forceinline__ int tiles_of(const Seq& s, const AttnArgs& a) {
@@ -476,22 +476,39 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     while (i < n && !dead) {
       const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge, cready = ready;
       // the next four tiles (the first time, the first four)
-      int b = 0;
-      len = 0;
-      ready = 0;
-#pragma unroll 1
-      for (int q = 0; q < 8 && walked < n; ++q) {
-        if ((q & 1) == odd) {
-          if (lane >> 3 == q >> 1) {
-            b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + w.k * kTile, after = walked - i0;
-            // the rows stand at len - rows .. len - 1
-            edge = tok0 + kTile - 1 > len - w.sq.rows || (a.window && tok0 <= (int64_t)len - 1 - a.window);
-          }
-          ++ready;
-        }
-        if (++walked < n && ++w.k == w.n) {
+      int b = w.b;
+      // the rows stand at len - rows .. len - 1
+      auto describe = [&](int k) {
+        b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + k * kTile;
+        edge = tok0 + kTile - 1 > len - w.sq.rows || tok0 <= len - 1 - a.window;
+      };
+      if (w.k + 8 <= w.n && walked + 8 <= n) {  // all of one pair
+        const int q = 2 * (lane >> 3) + odd;
+        describe(w.k + q);
+        after = walked + q - i0;
+        ready = 4;
+        walked += 8;
+        w.k += 8;
+        if (w.k == w.n && walked < n) {
           w.next_pair(a);
           i0 = walked;
+        }
+      } else {
+        len = 0;
+        ready = 0;
+#pragma unroll 1
+        for (int q = 0; q < 8 && walked < n; ++q) {
+          if ((q & 1) == odd) {
+            if (lane >> 3 == q >> 1) {
+              describe(w.k);
+              after = walked - i0;
+            }
+            ++ready;
+          }
+          if (++walked < n && ++w.k == w.n) {
+            w.next_pair(a);
+            i0 = walked;
+          }
         }
       }
       id = -1;
@@ -618,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           *reinterpret_cast<uint4*>(qd + panel * C::QPANEL + rl * C::PW + cl * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           if (part == 0) {
             m.rc[row] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
-            m.pos[row] = in ? first_pos + i : -1;
+            m.pos[row] = in ? max(first_pos + i, -1) : -1;
             m.off[row] = i * a.ldo + g * a.hso;
           }
         }
@@ -789,7 +806,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           for (int r = 0; r < N; ++r) {
             if (r < R) {
               const int pos = pm.pos[r];
-              if (hidden || tok > pos || (a.window && tok <= (int64_t)pos - a.window)) x[r] = -INFINITY;
+              if (hidden || tok > pos || tok <= pos - a.window) x[r] = -INFINITY;
               over |= x[r] - ref[r] > kHead;
             }
           }
@@ -881,20 +898,23 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       // the pair's end here: the group's sums, then all groups' outputs by the one that had the last tile
       const bool took = mine < i1;
       if (took) {
+        if (!wait(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
+        // rows' sums over the group's threads, by way of P's buffer, which nothing reads any more
+        float* lp = reinterpret_cast<float*>(pbuf + grp * C::P);
 #pragma unroll
         for (int r = 0; r < N; ++r) {
           if (r < R) {
-            float v = l[r];
-#pragma unroll
-            for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-            if (lane == 0) sh.red[grp][wq][r] = v;
+            const float v = l[r] + __shfl_xor_sync(0xFFFFFFFFu, l[r], 16);
+            if (lane < 16) lp[r * 64 + wq * 16 + lane] = v;
           }
         }
-        if (!wait(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
         if (any_of(grp, dead)) break;
-        if (tid < R) {
-          const float* red = sh.red[grp][0];
-          sh.sum[grp][tid] = (red[tid] + red[N + tid]) + (red[2 * N + tid] + red[3 * N + tid]);
+#pragma unroll 1
+        for (int r = wq; r < R; r += 4) {
+          float v = lp[r * 64 + lane] + lp[r * 64 + 32 + lane];
+#pragma unroll
+          for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+          if (lane == 0) sh.sum[grp][r] = v;
         }
         any_of(grp, false);
       }
@@ -909,14 +929,19 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         const int n_tiles = pm.n_tiles, parts_here = min(NG, i1 - i0);
         const bool whole = first_tile >= u0 && first_tile + n_tiles <= u1;
         const int slot = 2 * cta + (first_tile <= u0 ? 0 : 1);
-        // row's factors of the groups that took part, and its reference and sum
+        // row's factors of the groups (0 without a tile of this pair), and its reference and sum
         if (tid < R) {
-          float top = -INFINITY, sum = 0.0f;
-          for (int q = 0; q < parts_here; ++q) top = fmaxf(top, sh.ref[(i0 + q) % NG][tid]);
-          for (int q = 0; q < parts_here; ++q) {
-            const int gq = (i0 + q) % NG;
-            const float f = sh.ref[gq][tid] == -INFINITY ? 0.0f : ex2(sh.ref[gq][tid] - top);
-            sum = fmaf(sh.sum[gq][tid], f, sum);
+          float top = -INFINITY, sum = 0.0f, m[NG];
+#pragma unroll
+          for (int gq = 0; gq < NG; ++gq) {
+            const int q = gq - i0 % NG;
+            m[gq] = (q < 0 ? q + NG : q) < parts_here ? sh.ref[gq][tid] : -INFINITY;
+            top = fmaxf(top, m[gq]);
+          }
+#pragma unroll
+          for (int gq = 0; gq < NG; ++gq) {
+            const float f = m[gq] == -INFINITY ? 0.0f : ex2(m[gq] - top);
+            if (f != 0.0f) sum = fmaf(sh.sum[gq][tid], f, sum);
             sh.grow[gq][tid] = f;
           }
           if (whole)
@@ -926,43 +951,36 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         }
         any_of(grp, false);
 #pragma unroll 1
-        for (int mb = 0; mb < C::MB; ++mb) {
-          const int d = mb * 128 + tid;
-#pragma unroll 1
-          for (int r = 0; r < R; r += 8) {
-            float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int e = 0; e < C::MB * ((R + 3) / 4); ++e) {  // blocks of 128 dims x 4 rows
+          const int mb = C::MB == 1 ? 0 : e & 1, r = C::MB == 1 ? 4 * e : (e >> 1) * 4, d = mb * 128 + tid;
+          uint32_t v[NG][3][4];
 #pragma unroll
-            for (int gq = 0; gq < NG; ++gq) {
-              if ((gq - i0 % NG + NG) % NG < parts_here) {
-                uint32_t v0[8], v1[8], v2[8];
-                const uint32_t at = otm + lane_base + gq * (C::MB * C::OCOL) + mb * C::OCOL + r;
-                tmem_ld8(at, v0);
-                tmem_ld8(at + N, v1);
-                tmem_ld8(at + 2 * N, v2);
-                const float4 f0 = *reinterpret_cast<const float4*>(&sh.grow[gq][r]);
-                const float4 f1 = *reinterpret_cast<const float4*>(&sh.grow[gq][r + 4]);
-                const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
-                tmem_ld_wait();
+          for (int gq = 0; gq < NG; ++gq)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  o[e] = fmaf(fmaf(__uint_as_float(v2[e]), 0x1p-8f, fmaf(__uint_as_float(v1[e]), 0x1p-4f, __uint_as_float(v0[e]))),
-                              f[e], o[e]);
-              }
+            for (int t = 0; t < 3; ++t) tmem_ld4(otm + lane_base + (gq * C::MB + mb) * C::OCOL + t * N + r, v[gq][t]);
+          tmem_ld_wait();
+          float o[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int gq = 0; gq < NG; ++gq) {
+            const float4 f4 = *reinterpret_cast<const float4*>(&sh.grow[gq][r]);
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+              const float y = fmaf(__uint_as_float(v[gq][2][z]), 0x1p-8f,
+                                   fmaf(__uint_as_float(v[gq][1][z]), 0x1p-4f, __uint_as_float(v[gq][0][z])));
+              if (f[z] != 0.0f) o[z] = fmaf(y, f[z], o[z]);  // a group without a tile of this pair holds anything
             }
-            if (d < D) {
-              if (whole) {
+          }
+          if (d < D) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  if (r + e < R) {
-                    const __nv_bfloat16 y = __float2bfloat16_rn(o[e] * sh.red[grp][0][r + e]);
-                    a.out[base + pm.off[r + e] + d] = *reinterpret_cast<const uint16_t*>(&y);
-                  }
+            for (int z = 0; z < 4; ++z) {
+              if (r + z < R) {
+                if (whole) {
+                  const __nv_bfloat16 y = __float2bfloat16_rn(o[z] * sh.red[grp][0][r + z]);
+                  a.out[base + pm.off[r + z] + d] = *reinterpret_cast<const uint16_t*>(&y);
+                } else {
+                  da.part_o[((int64_t)slot * N + r + z) * D + d] = o[z];
                 }
-              } else {
-                float* dst = da.part_o + ((int64_t)slot * N + r) * D + d;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (r + e < R) dst[e * D] = o[e];
               }
             }
           }

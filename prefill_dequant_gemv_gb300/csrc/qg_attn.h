@@ -46,7 +46,7 @@ struct AttnArgs {
   uint16_t* out;
   int64_t ldq, hsq, ldo, hso;
   float scale;
-  int64_t window;  // 0: none
+  int window;  // keys a row sees at most; none: 2^31 - 1
   int hq;
 };
 
