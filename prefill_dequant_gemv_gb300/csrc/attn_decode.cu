@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       mbar_init(&sh.vfree[s], 1);
     }
     for (int i = 0; i < C::QB; ++i) {
-      mbar_init(&sh.qfull[i], 32);
+      mbar_init(&sh.qfull[i], 64);
       mbar_init(&sh.qfree[i], 1);
     }
     for (int i = 0; i < NG; ++i) {
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 
   if (n > 0 && warp >= kMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
-    if (warp > kMma && warp < kMma + 6) w.find(a, u0, lane);
+    if (warp != kMma && warp != kMma + 7) w.find(a, u0, lane);
   if (warp > kMma && warp < kMma + 5) {  // -------------------------------------- key tiles, value tiles
     // Two warps for the keys, two for the values, each with every other tile: a tile's copies take
     // one warp some 600 to 1100 cycles to issue.  Lanes 8q .. 8q + 7 look after tile 8j + 2q + odd: its eight
@@ -567,78 +567,90 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 #pragma unroll 1
     for (int j = max(odd, i - stages); j < i; j += 2)
       wait(&full[j % stages], (uint32_t)(j / stages) & 1u, c.status);
-  } else if (warp == kMma + 5) {  // ----------------------------------------------- query rows
-    // D / 16 lanes a row, 16 elements each
+  } else if (warp == kMma + 5 || warp == kMma + 6) {  // -------------------------- query rows
+    // Two warps; D / 16 lanes a row, 16 elements each; the loads of four rows a lane group are issued together.
+    // Rows past R stay as they are: their columns of S are not looked at.
     constexpr int TPR = D / 16, RPP = 32 / TPR;
-    const int t = lane, part = t % TPR;
+    const int part = lane % TPR, mine = (warp - kMma - 5) * RPP + lane / TPR;
     int u = u0;
     bool dead = false;
     for (int p = 0; u < u1; ++p) {
       const int qb = p % C::QB;
-      if (p >= C::QB && !wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
-      if (__any_sync(0xFFFFFFFFu, dead)) break;
-      PairMeta<N>& m = sh.pair[qb];
       const int R = min(w.sq.rows * G, N), first_pos = w.sq.len - w.sq.rows;
       const int next = u + w.n - w.k;
-      if (t == 0) {
+      const int64_t qbase = (int64_t)w.sq.start * a.ldq + (int64_t)w.h * G * a.hsq + 16 * part;
+      PairMeta<N>& m = sh.pair[qb];
+      uint8_t* qd = qbuf + qb * C::Q;
+      bool waited = p < C::QB;
+#pragma unroll 1
+      for (int r0 = mine; __any_sync(0xFFFFFFFFu, r0 < R); r0 += 8 * RPP) {
+        uint4 x[4][2];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int row = r0 + 2 * RPP * y, i = row / G, g = row - i * G;
+          x[y][0] = x[y][1] = make_uint4(0, 0, 0, 0);
+          if (row < R) {
+            const uint4* qp = reinterpret_cast<const uint4*>(a.q + qbase + i * a.ldq + g * a.hsq);
+            x[y][0] = qp[0];
+            x[y][1] = qp[1];
+          }
+        }
+        if (!waited) {
+          if (!wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
+          waited = true;
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int row = r0 + 2 * RPP * y;
+          if (!__any_sync(0xFFFFFFFFu, row < R)) break;
+          const uint32_t v[8] = {x[y][0].x, x[y][0].y, x[y][0].z, x[y][0].w, x[y][1].x, x[y][1].y, x[y][1].z, x[y][1].w};
+          float amax = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
+#pragma unroll
+          for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          // a power of two that brings the row's largest element to [128, 256)
+          const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
+          const float down = __int_as_float((127 - e2) << 23);
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint16_t hh[2], ll[2];
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+              const uint32_t b = v[2 * e + z];
+              // bf16's bits fit fp16 at this size but for the smallest elements
+              const uint32_t h16 = f16x2(__uint_as_float(b << 16) * down, __uint_as_float(b & 0xFFFF0000u) * down);
+              hh[z] = e4m3x2(h16);
+              uint32_t d16;
+              asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d16) : "r"(h16), "r"(codes_f16x2(hh[z])));
+              ll[z] = e4m3x2(d16);
+            }
+            hi[e] = hh[0] | (uint32_t)hh[1] << 16;
+            lo[e] = ll[0] | (uint32_t)ll[1] << 16;
+          }
+          if (row < R) {
+            // rows of PW bytes in the swizzle of the key tiles: term, then row (N is a multiple of the swizzle's 8 rows)
+            const int panel = part / (C::PW / 16), chunk = part % (C::PW / 16);
+            const int at = panel * C::QPANEL + row * C::PW + (D == 64 ? chunk ^ ((row >> 1) & 3) : chunk ^ (row & 7)) * 16;
+            *reinterpret_cast<uint4*>(qd + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(qd + at + N * C::PW) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (part == 0) {
+              const int i = row / G, g = row - i * G;
+              m.rc[row] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
+              m.pos[row] = max(first_pos + i, -1);
+              m.off[row] = i * a.ldo + g * a.hso;
+            }
+          }
+        }
+      }
+      if (!waited && !wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
+      if (__any_sync(0xFFFFFFFFu, dead)) break;
+      if (warp == kMma + 5 && lane == 0) {
         m.R = R, m.n_tiles = w.n, m.first = u - w.k;
         m.i0 = u - u0, m.i1 = min(next, u1) - u0;
         m.base = (int64_t)w.sq.start * a.ldo + (int64_t)w.h * G * a.hso;
-      }
-      uint8_t* qd = qbuf + qb * C::Q;
-#pragma unroll 1
-      for (int r0 = 0; r0 < N; r0 += RPP) {
-        const int row = r0 + t / TPR;
-        const bool in = row < R;
-        const int i = in ? row / G : 0, g = in ? row - i * G : 0;
-        uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (in) {
-          const uint4* qp = reinterpret_cast<const uint4*>(a.q + (int64_t)(w.sq.start + i) * a.ldq +
-                                                           (int64_t)(w.h * G + g) * a.hsq + 16 * part);
-          x[0] = qp[0];
-          x[1] = qp[1];
-        }
-        const uint32_t v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-        float amax = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
-#pragma unroll
-        for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-        // a power of two that brings the row's largest element to [128, 256)
-        const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
-        const float down = __int_as_float((127 - e2) << 23);
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint16_t hh[2], ll[2];
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {
-            const uint32_t y = v[2 * e + z];
-            // bf16's bits fit fp16 at this size but for the smallest elements
-            const uint32_t h16 = f16x2(__uint_as_float(y << 16) * down, __uint_as_float(y & 0xFFFF0000u) * down);
-            hh[z] = e4m3x2(h16);
-            uint32_t d16;
-            asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d16) : "r"(h16), "r"(codes_f16x2(hh[z])));
-            ll[z] = e4m3x2(d16);
-          }
-          hi[e] = hh[0] | (uint32_t)hh[1] << 16;
-          lo[e] = ll[0] | (uint32_t)ll[1] << 16;
-        }
-        // rows of PW bytes in the swizzle of the key tiles: term, then row
-        const int panel = part / (C::PW / 16), chunk = part % (C::PW / 16);
-        const int rh = row, rl = N + row;
-        const int ch = D == 64 ? chunk ^ ((rh >> 1) & 3) : chunk ^ (rh & 7);
-        const int cl = D == 64 ? chunk ^ ((rl >> 1) & 3) : chunk ^ (rl & 7);
-        if (row < N) {
-          *reinterpret_cast<uint4*>(qd + panel * C::QPANEL + rh * C::PW + ch * 16) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-          *reinterpret_cast<uint4*>(qd + panel * C::QPANEL + rl * C::PW + cl * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          if (part == 0) {
-            m.rc[row] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
-            m.pos[row] = in ? max(first_pos + i, -1) : -1;
-            m.off[row] = i * a.ldo + g * a.hso;
-          }
-        }
       }
       fence_proxy_async_smem();
       mbar_arrive(&sh.qfull[qb]);
@@ -685,7 +697,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       wait(&sh.ended[0], 0, c.status);
     }
     __syncwarp();
-  } else if (warp == kMma + 6) {  // ------------------------------------------------ output MMAs
+  } else if (warp == kMma + 7) {  // ------------------------------------------------ output MMAs
     // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
     // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
     // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
