@@ -37,6 +37,7 @@
 #include <atomic>
 
 #include "qg_attn.h"
+#include "qg_attn_dev.cuh"
 #include "qg_sync.cuh"
 #include "qg_tc.cuh"
 
@@ -44,7 +45,6 @@ namespace qg {
 namespace {
 
 constexpr int kTile = 128;           // keys a tile
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kBias = 2.0f;        // P of a key at the reference is 2^2 ...
 constexpr float kHead = 6.5f;        // ... and at most 2^8.5, below E4M3's 448
 
@@ -122,101 +122,6 @@ struct DecodeArgs {
   float2* part_ml; // [2 * grid][N]
   float* part_o;   // [2 * grid][N][D]
 };
-
-// mbar_wait_bounded in few instructions: this kernel's many roles share one instruction cache.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
-  do {
-    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
-  } while (global_ns() - t0 < kWaitLimitNs);
-  atomicExch(status, kStatusTimeout);
-  return false;
-}
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t f16x2(float a, float b) {  // a in the low half
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-__device__ __forceinline__ uint16_t e4m3x2(uint32_t h) {  // two fp16 -> two codes, the low half in the low byte
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
-  return r;
-}
-__device__ __forceinline__ uint32_t codes_f16x2(uint16_t c) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
-  return r;
-}
-// 16 * (h - c) of two fp16 pairs: exact where c is h rounded to fewer bits
-__device__ __forceinline__ uint32_t rest16(uint32_t h, uint32_t c) {
-  uint32_t d, r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(c));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x4C004C00u));
-  return r;
-}
-__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
-          "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-// Shared-memory matrix descriptor (version 1) as its two halves: start and leading byte offset; stride
-// byte offset and swizzle (0 none, 2 128 bytes, 4 64 bytes).  Adding bytes / 16 to the low half moves the start.
-__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
-constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return sbo >> 4 | 1u << 14 | swizzle << 29; }
-// kind::f8f6f4, E4M3 x E4M3 -> fp32, M = 128; ta, tb: A, B lie M- or N-contiguous.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int n, int ta, int tb) {
-  return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
-}
-template <uint32_t AHI, uint32_t BHI, uint32_t IDESC>
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t alo, uint32_t blo, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d), "r"(alo), "n"(AHI), "r"(blo), "n"(BHI),
-      "n"(IDESC), "r"(acc)
-      : "memory");
-}
-// One lane of the warp, chosen so that the compiler knows the branch on it takes one thread.
-__device__ __forceinline__ bool elect() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-// Barrier of a softmax group's four warps that returns whether any thread's v is set.
-__device__ __forceinline__ bool any_of(int group, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"(1 + group), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
-__device__ __forceinline__ float warp_max(float v) {
-  float r;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float lg2(float x) {
-  float r;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // First key that any row of the sequence sees, rounded down to a page; tiles of a pair (one at least where
 // there are rows, so that rows without a key are written).
@@ -613,29 +518,14 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           // a power of two that brings the row's largest element to [128, 256)
           const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
           const float down = __int_as_float((127 - e2) << 23);
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint16_t hh[2], ll[2];
-#pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const uint32_t b = v[2 * e + z];
-              // bf16's bits fit fp16 at this size but for the smallest elements
-              const uint32_t h16 = f16x2(__uint_as_float(b << 16) * down, __uint_as_float(b & 0xFFFF0000u) * down);
-              hh[z] = e4m3x2(h16);
-              uint32_t d16;
-              asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d16) : "r"(h16), "r"(codes_f16x2(hh[z])));
-              ll[z] = e4m3x2(d16);
-            }
-            hi[e] = hh[0] | (uint32_t)hh[1] << 16;
-            lo[e] = ll[0] | (uint32_t)ll[1] << 16;
-          }
+          uint4 hi, lo;
+          split_query(x[y], down, &hi, &lo);
           if (row < R) {
             // rows of PW bytes in the swizzle of the key tiles: term, then row (N is a multiple of the swizzle's 8 rows)
             const int panel = part / (C::PW / 16), chunk = part % (C::PW / 16);
             const int at = panel * C::QPANEL + row * C::PW + (D == 64 ? chunk ^ ((row >> 1) & 3) : chunk ^ (row & 7)) * 16;
-            *reinterpret_cast<uint4*>(qd + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(qd + at + N * C::PW) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<uint4*>(qd + at) = hi;
+            *reinterpret_cast<uint4*>(qd + at + N * C::PW) = lo;
             if (part == 0) {
               const int i = row / G, g = row - i * G;
               m.rc[row] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
@@ -1048,19 +938,17 @@ int launch_rows(int rows, const DecodeArgs& da, const CUtensorMap& km, const CUt
   return launch<D, 64>(da, km, vm, grid, s);
 }
 
-constexpr size_t kCounterBytes = 4096;  // counters of up to 1024 CTAs, at the same place whatever the call
-
 }  // namespace
 
 int decode_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0; }
 
 size_t decode_workspace(int64_t rows, int head_dim, const DeviceInfo& dev) {
   const size_t r = (size_t)decode_rows(rows), slots = 2 * (size_t)dev.sms;
-  return kWsHeader + kCounterBytes + slots * r * sizeof(float2) + slots * r * head_dim * sizeof(float);
+  return kWsHeader + kAttnCounterBytes + slots * r * sizeof(float2) + slots * r * head_dim * sizeof(float);
 }
 
 int launch_attn_decode(const AttnArgs& a, int head_dim, int64_t rows, const DeviceInfo& dev, void* ws, void* stream) {
-  if (dev.sms > 1024) return QG_ERR_UNSUPPORTED;
+  if (dev.sms * sizeof(int) > kAttnCounterBytes) return QG_ERR_UNSUPPORTED;
   const int page = 1 << a.c.page_log2, box = std::min(page, kTile);
   CUtensorMap km, vm;
   if (!encode_pages(&km, a.c.k, head_dim, page, a.c.n_pages * a.c.hkv, box) ||
@@ -1071,7 +959,7 @@ int launch_attn_decode(const AttnArgs& a, int head_dim, int64_t rows, const Devi
   da.a = a;
   uint8_t* w = static_cast<uint8_t*>(ws) + kWsHeader;
   da.counters = reinterpret_cast<int*>(w);
-  w += kCounterBytes;
+  w += kAttnCounterBytes;
   da.part_ml = reinterpret_cast<float2*>(w);
   da.part_o = reinterpret_cast<float*>(w + 2 * (size_t)dev.sms * r * sizeof(float2));
   // no more CTAs than tiles that there can be

@@ -1,0 +1,656 @@
+// Attention of many rows a KV head over the 8-bit paged cache (prompts and chunks of prompts): a CTA
+// takes MT tiles of 128 query rows of one (sequence, KV head) -- row = token * G + query head, so the G
+// heads share what is loaded -- through the keys that they see, BN at a time, with an online softmax.
+//
+// The mathematics is the few-row kernel's: t_j = scale * ks_j * (q . k_j) * log2(e) + log2(vs_j), P_j = 2^(t_j - m),
+//   out = sum P_j v_j / sum (P_j / vs_j),   m moving only when a row's maximum has grown by 2^8.
+//
+// Bound by the tensor cores and, about as much, by the softmax's exponentials and conversions, so:
+//   * scores run on the E4M3 tensor cores, the key codes as they come from the cache and a query row as
+//     the sum of two E4M3 terms (bf16's 8 significant bits), which costs what one fp16 product of
+//     converted keys would, without the conversion and at half its shared-memory traffic;
+//   * P is rounded to fp16 and stays in tensor memory, over the scores it came from, as the A operand
+//     of the second product; splitting it into E4M3 terms would cost three conversions an element where
+//     this needs one, and the value codes are converted once for all rows instead, by a
+//     warpgroup of their own, into the fp16 tile that the second product reads transposed;
+//   * a thread owns a row: no reduction crosses threads.
+// Few tiles are split over the keys (parts of a row join in order in the CTA that finishes last).
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "qg_attn.h"
+#include "qg_attn_dev.cuh"
+#include "qg_sync.cuh"
+#include "qg_tc.cuh"
+
+namespace qg {
+namespace {
+
+constexpr float kLazy = 8.0f;  // P stays below 2^8
+
+template <int D>
+struct Cfg {
+  static constexpr int MT = D == 256 ? 1 : 2;         // row tiles of 128
+  static constexpr int BN = D == 256 ? 64 : 128;      // keys a step
+  static constexpr int ROWS = 128 * MT;
+  static constexpr int THREADS = 128 * (MT + 2);
+  static constexpr int PW = D < 128 ? D : 128;        // bytes of a row of a code panel
+  static constexpr int NP = D / PW;
+  static constexpr int KV = BN * D;                   // bytes of a tile of key (or value) codes
+  static constexpr int Q = 2 * 128 * D;               // both terms of a row tile
+  static constexpr int VF = 2 * KV;                   // values in fp16
+  static constexpr int VPANEL = BN * 128;             // 64 dims of all keys
+  static constexpr int KS = D == 64 ? 4 : 3, VS = 2, FS = 2;
+  static constexpr int SB = MT == 1 ? 2 : 1;          // score buffers a row tile
+  static constexpr int OCOL = MT * SB * BN;           // TMEM column of the outputs
+  static constexpr int SMEM = 1024 + MT * Q + KS * KV + VS * KV + FS * VF + 4096;
+  static_assert(SMEM <= 232448 && OCOL + MT * D <= 512, "shared and tensor memory");
+};
+
+struct StepMeta {
+  float ks[8], lvs[8], ivs[8];  // scale, log2 and reciprocal of the value scale of each 16 keys; ks 0: hidden
+  int cut, pad[7];              // some of its keys are hidden
+};
+template <int D>
+struct Shared {
+  using C = Cfg<D>;
+  StepMeta step[8];
+  uint64_t kfull[C::KS], kfree[C::KS], cfull[C::VS], cfree[C::VS], vfull[C::FS], vfree[C::FS];
+  uint64_t qfull, sfull[C::MT * C::SB], pfull[C::MT * C::SB], odone[C::MT], ended;
+  uint32_t tmem;
+  int work[8];
+  int ticket;
+};
+
+struct PrefillArgs {
+  AttnArgs a;
+  int splits;
+  int64_t blocks;   // upper bound of row blocks
+  int* counters;    // [blocks * hkv]
+  float2* part_ml;  // [blocks * hkv * splits][ROWS]
+  float* part_o;    // [blocks * hkv * splits][ROWS][D]
+};
+
+constexpr uint32_t idesc_f16(int n) {  // f16 x f16 -> fp32, M = 128, B N-contiguous
+  return (1u << 4) | (1u << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+template <uint32_t BHI, uint32_t IDESC>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d), "r"(a), "r"(blo), "n"(BHI), "n"(IDESC),
+      "r"(acc)
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
+    attn_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                        const PrefillArgs pa) {
+  using C = Cfg<D>;
+  constexpr int MT = C::MT, BN = C::BN;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* qbuf = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kring = qbuf + MT * C::Q;
+  uint8_t* cring = kring + C::KS * C::KV;
+  uint8_t* vring = cring + C::VS * C::KV;
+  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(vring + C::FS * C::VF);
+  static_assert(sizeof(Shared<D>) <= 3072, "shared memory");
+  const AttnArgs& a = pa.a;
+  const KvArgs& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
+  const int G = a.hq / c.hkv;
+  constexpr int kMma = 4 * (MT + 1);  // first warp of the last warpgroup
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::KS; ++i) mbar_init(&sh.kfull[i], 9), mbar_init(&sh.kfree[i], 1);
+    for (int i = 0; i < C::VS; ++i) mbar_init(&sh.cfull[i], 8), mbar_init(&sh.cfree[i], 128);
+    for (int i = 0; i < C::FS; ++i) mbar_init(&sh.vfull[i], 128), mbar_init(&sh.vfree[i], 1);
+    for (int i = 0; i < MT * C::SB; ++i) mbar_init(&sh.sfull[i], 2), mbar_init(&sh.pfull[i], 128);
+    for (int i = 0; i < MT; ++i) mbar_init(&sh.odone[i], 1);
+    mbar_init(&sh.qfull, 128 * MT);
+    mbar_init(&sh.ended, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(&sh.tmem, 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  // this CTA's row block: the blocks of all sequences in a row, the last ones (with the most keys) first
+  if (warp == 0) {
+    bool bad = false;
+    int total = 0;
+    auto blocks_of = [&](const Seq& s) { return (int)(((int64_t)s.rows * G + C::ROWS - 1) / C::ROWS); };
+    for (int base = 0; base < c.n_seqs; base += 32) {
+      int nb = 0;
+      if (base + lane < c.n_seqs) nb = blocks_of(seq_of(c, base + lane, &bad));
+      total += __reduce_add_sync(0xFFFFFFFFu, nb);
+    }
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicExch(c.status, kStatusInvalid);
+    int left = total - 1 - (int)blockIdx.x;
+    int ok = left >= 0;
+    for (int base = 0; ok && base < c.n_seqs; base += 32) {
+      Seq s = {0, 0, 0};
+      bool ignore = false;
+      if (base + lane < c.n_seqs) s = seq_of(c, base + lane, &ignore);
+      const int nb = blocks_of(s);
+      int sum = nb;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += v;
+      }
+      const int all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      if (left < all) {
+        const int who = __ffs(__ballot_sync(0xFFFFFFFFu, sum > left)) - 1;
+        if (lane == who) {
+          sh.work[0] = base + who;
+          sh.work[1] = left - (sum - nb);
+          sh.work[2] = s.start, sh.work[3] = s.rows, sh.work[4] = s.len;
+        }
+        break;
+      }
+      left -= all;
+    }
+    if (lane == 0) sh.work[5] = ok;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const bool run = sh.work[5] != 0;
+  const int seq = sh.work[0], start = sh.work[2], rows = sh.work[3], len = sh.work[4];
+  const int head = blockIdx.y / pa.splits, split = blockIdx.y % pa.splits;
+  const int64_t row0 = (int64_t)sh.work[1] * C::ROWS, all_rows = (int64_t)rows * G;
+  const int R = run ? (int)min((int64_t)C::ROWS, all_rows - row0) : 0;  // rows of this block
+  // its keys: from the first one that its first row sees (a whole page) to its last row's own
+  const int pos0 = len - rows + (int)(row0 / G), pos1 = run ? len - rows + (int)((row0 + R - 1) / G) : 0;
+  const int plog = c.page_log2, P = 1 << plog;
+  const int key0 = pos0 >= a.window ? (pos0 - a.window + 1) >> plog << plog : 0, key1 = max(pos1 + 1, 0);
+  const int steps_all = key1 > key0 ? (key1 - key0 + BN - 1) / BN : 0;
+  const int s0 = (int)((int64_t)steps_all * split / pa.splits), s1 = (int)((int64_t)steps_all * (split + 1) / pa.splits);
+  const int n = run ? s1 - s0 : 0, first_key = key0 + s0 * BN;
+  const int tiles = MT == 2 && R <= 128 ? 1 : MT;  // row tiles in use
+
+  if (run && warp == kMma + 1) {  // --------------------------------------------------------- tiles of codes
+    // Lane g looks after keys 16g .. of a step (g < BN / 16); page ids come two steps ahead, scales one.
+    constexpr int NG = BN / 16;
+    const int box = min(P, BN);
+    auto page_of = [&](int i) {
+      const int64_t tok = (int64_t)first_key + (int64_t)i * BN + 16 * lane;
+      return i < n && lane < NG && tok < key1 ? c.pages[(int64_t)seq * c.page_stride + (tok >> plog)] : -1;
+    };
+    int id = page_of(0), id1 = page_of(1);
+    bool dead = false;
+    int ks = 0, vs = 0, klap = 0, vlap = 0;
+    int i = 0;
+    for (; i < n; ++i) {
+      const int tok = first_key + i * BN + 16 * lane, id2 = page_of(i + 2);
+      bool ok = lane < NG && tok < key1;
+      if (ok && (id < 0 || id >= c.n_pages)) {
+        ok = false;
+        atomicExch(c.status, kStatusInvalid);
+      }
+      const int64_t tile = (int64_t)id * c.hkv + head;
+      float sk = 0.0f, sv = 0.0f;
+      if (ok) {
+        sk = c.ks[tile];
+        sv = c.vs[tile];
+      }
+      const bool lead = ok && (16 * lane) % box == 0;
+      if (klap && !wait(&sh.kfree[ks], (klap - 1) & 1, c.status)) dead = true;
+      if (__any_sync(0xFFFFFFFFu, dead)) break;
+      if (lane < NG || lane < 8) {
+        if (lead) {
+          mbar_arrive_expect_tx(&sh.kfull[ks], box * D);
+#pragma unroll
+          for (int x = 0; x < C::NP; ++x)
+            tma_load_3d(kring + ks * C::KV + x * BN * C::PW + 16 * lane * C::PW, &kmap, x * 128, tok & (P - 1), (int)tile,
+                        &sh.kfull[ks]);
+        } else if (lane < 8) {
+          mbar_arrive(&sh.kfull[ks]);
+        }
+      }
+      if (vlap && !wait(&sh.cfree[vs], (vlap - 1) & 1, c.status)) dead = true;
+      if (__any_sync(0xFFFFFFFFu, dead)) {
+        ++i;  // this step's keys are on their way
+        break;
+      }
+      // the step's description goes with the value codes' barrier to the converters, and with the keys' to the rest
+      StepMeta& m = sh.step[i & 7];
+      const bool cut = __any_sync(0xFFFFFFFFu, lane < NG && (!ok || tok + 16 > key1));
+      if (lane < NG) {
+        m.ks[lane] = sk;
+        m.lvs[lane] = ok ? lg2(sv) : 0.0f;
+        m.ivs[lane] = ok ? rcp(sv) : 0.0f;
+      }
+      if (lane == 0) m.cut = cut;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.kfull[ks]);
+      if (lead) {
+        mbar_arrive_expect_tx(&sh.cfull[vs], box * D);
+#pragma unroll
+        for (int x = 0; x < C::NP; ++x)
+          tma_load_3d(cring + vs * C::KV + x * BN * C::PW + 16 * lane * C::PW, &vmap, x * 128, tok & (P - 1), (int)tile,
+                      &sh.cfull[vs]);
+      } else if (lane < 8) {
+        mbar_arrive(&sh.cfull[vs]);
+      }
+      __syncwarp();
+      id = id1;
+      id1 = id2;
+      if (++ks == C::KS) ks = 0, ++klap;
+      if (++vs == C::VS) vs = 0, ++vlap;
+    }
+    // no copy is left in flight into this CTA's shared memory when it ends
+    if (!dead) {
+      for (int j = max(0, i - C::KS); j < i; ++j) wait(&sh.kfull[j % C::KS], (uint32_t)(j / C::KS) & 1u, c.status);
+      for (int j = max(0, i - C::VS); j < i; ++j) wait(&sh.cfull[j % C::VS], (uint32_t)(j / C::VS) & 1u, c.status);
+    } else {
+      const unsigned long long t0 = global_ns();  // a pipeline that gave up: any copy has landed long before
+      while (global_ns() - t0 < 1000000ull) {
+      }
+    }
+  } else if (run && warp == kMma) {  // ------------------------------------------------------ MMAs
+    constexpr uint32_t kSwz = D == 64 ? 4 : 2, kHi = desc_hi(8 * C::PW, kSwz), kVHi = desc_hi(1024, 2);
+    constexpr uint32_t kQk = idesc_e4m3(BN, 0, 0), kPv = idesc_f16(D);
+    const uint32_t q0 = desc_lo(smem_u32(qbuf), 16), k0 = desc_lo(smem_u32(kring), 16);
+    const uint32_t v0 = desc_lo(smem_u32(vring), C::VPANEL);
+    int ks = 0, fs = 0;
+    uint32_t kpar = 0, vpar = 0;
+    auto scores = [&](int m, int sb) {
+      if (elect()) {
+        const uint32_t d = tmem + (m * C::SB + sb) * BN;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
+            mma_e4m3<kHi, kHi, kQk>(d, q0 + (m * C::Q + t * 128 * D + panel * 128 * C::PW + off) / 16,
+                                    k0 + (ks * C::KV + panel * BN * C::PW + off) / 16, t + x > 0);
+          }
+        mma_commit(&sh.sfull[m * C::SB + sb]);
+        mbar_arrive(&sh.sfull[m * C::SB + sb]);  // passes the step's description on
+        if (m == tiles - 1) mma_commit(&sh.kfree[ks]);
+      }
+      __syncwarp();
+    };
+    auto outputs = [&](int m, int sb, int i) {
+      if (elect()) {
+        const uint32_t p = tmem + (m * C::SB + sb) * BN, d = tmem + C::OCOL + m * D;
+#pragma unroll
+        for (int x = 0; x < BN / 16; ++x)
+          mma_f16_ts<kVHi, kPv>(d, p + 8 * x, v0 + (fs * C::VF + x * 16 * 128) / 16, (i > 0) | (x > 0));
+        if (m == tiles - 1) mma_commit(&sh.vfree[fs]);
+        if (i == n - 1) mma_commit(&sh.odone[m]);
+      }
+      __syncwarp();
+    };
+    bool ok = n == 0 || (wait(&sh.qfull, 0, c.status) && wait(&sh.kfull[0], 0, c.status));
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    tc_fence_after();
+    if (n > 0 && ok) {
+      for (int m = 0; m < tiles; ++m) scores(m, 0);
+      if (++ks == C::KS) ks = 0, kpar ^= 1;
+    }
+    for (int i = 0; i < n && ok; ++i) {
+      const int sb = MT == 1 ? i & 1 : 0;
+      const uint32_t ppar = (MT == 1 ? i >> 1 : i) & 1;
+      if (MT == 1) {  // the next scores go to the other buffer, whose P has been multiplied by then
+        if (i + 1 < n) {
+          ok = __all_sync(0xFFFFFFFFu, wait(&sh.kfull[ks], kpar, c.status));
+          if (!ok) break;
+          tc_fence_after();
+          scores(0, sb ^ 1);
+          if (++ks == C::KS) ks = 0, kpar ^= 1;
+        }
+        ok = wait(&sh.vfull[fs], vpar, c.status) && wait(&sh.pfull[sb], ppar, c.status);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        outputs(0, sb, i);
+      } else {  // a row tile's P lies over its scores: multiply it, then its next scores; the other tile's softmax meanwhile
+        for (int m = 0; m < tiles && ok; ++m) {
+          ok = (m > 0 || wait(&sh.vfull[fs], vpar, c.status)) && wait(&sh.pfull[m], ppar, c.status);
+          if (ok && m == 0 && i + 1 < n) ok = wait(&sh.kfull[ks], kpar, c.status);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          outputs(m, 0, i);
+          if (i + 1 < n) scores(m, 0);
+        }
+        if (i + 1 < n && ++ks == C::KS) ks = 0, kpar ^= 1;
+      }
+      if (++fs == C::FS) fs = 0, vpar ^= 1;
+    }
+    // every MMA has ended before the CTA's memory goes
+    if (elect()) {
+      mma_commit(&sh.ended);
+      wait(&sh.ended, 0, c.status);
+    }
+    __syncwarp();
+  } else if (run && warp >= 4 * MT && warp < kMma) {  // ------------------------------------ value codes -> fp16
+    // a key a thread (two threads a key where there are 64)
+    constexpr int TPK = 128 / BN, CH = D / 16 / TPK;  // chunks of 16 codes a thread
+    const int key = tid % BN, part = tid / BN;
+    bool dead = false;
+    int vs = 0, fs = 0;
+    uint32_t cpar = 0, fpar = 1;
+    for (int i = 0; i < n; ++i) {
+      if (!wait(&sh.cfull[vs], cpar, c.status)) dead = true;
+      if (i >= C::FS && !dead && !wait(&sh.vfree[fs], fpar, c.status)) dead = true;
+      if (dead) break;
+      const uint8_t* src = cring + vs * C::KV;
+      uint8_t* dst = vring + fs * C::VF;
+      // keys that nobody may see hold anything, NaN codes too: they must be numbers for P = 0
+      const bool real = first_key + i * BN + key < key1 && sh.step[i & 7].ks[key >> 4] != 0.0f;
+#pragma unroll
+      for (int x = 0; x < CH; ++x) {
+        const int ch = part * CH + x, panel = ch / (C::PW / 16), cc = ch % (C::PW / 16);
+        const int sw = D == 64 ? cc ^ ((key >> 1) & 3) : cc ^ (key & 7);
+        uint4 w = *reinterpret_cast<const uint4*>(src + panel * BN * C::PW + key * C::PW + sw * 16);
+        if (!real) w = make_uint4(0, 0, 0, 0);
+        // 16 values: two 16-byte chunks of the 64-dim panel ch / 4
+        uint8_t* row = dst + (ch / 4) * C::VPANEL + key * 128;
+        const int c0 = (ch % 4) * 2;
+        *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) =
+            make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y));
+        *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
+            make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w));
+      }
+      mbar_arrive(&sh.cfree[vs]);
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.vfull[fs]);
+      if (++vs == C::VS) vs = 0, cpar ^= 1;
+      if (++fs == C::FS) fs = 0, fpar ^= 1;
+    }
+  } else if (run && warp < 4 * MT) {  // ----------------------------------------------------- softmax, a row a thread
+    const int mt = warp >> 2, wq = warp & 3;
+    const int row = mt * 128 + tid;  // in the block
+    const bool in = row < R;
+    const int64_t r = row0 + row;
+    const int tok = in ? (int)(r / G) : 0, g = in ? (int)(r - (int64_t)tok * G) : 0;
+    const int pos = max(in ? len - rows + tok : pos1, -1);
+    const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+    // the query row as two E4M3 terms
+    const uint16_t* qp = a.q + (int64_t)(start + tok) * a.ldq + (int64_t)(head * G + g) * a.hsq;
+    float amax = 0.0f;
+    if (n > 0) {
+#pragma unroll 8
+      for (int x = 0; x < D / 8; ++x) {
+        const uint4 v = in ? *reinterpret_cast<const uint4*>(qp + 8 * x) : make_uint4(0, 0, 0, 0);
+        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int z = 0; z < 4; ++z)
+          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[z] << 16)), fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
+      }
+    }
+    // a power of two that brings the row's largest element to [128, 256)
+    const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
+    const float down = __int_as_float((127 - e2) << 23), rc = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
+    if (n > 0) {
+      uint8_t* qd = qbuf + mt * C::Q;
+#pragma unroll 2
+      for (int x = 0; x < D / 16; ++x) {
+        uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (in) v[0] = *reinterpret_cast<const uint4*>(qp + 16 * x), v[1] = *reinterpret_cast<const uint4*>(qp + 16 * x + 8);
+        uint4 hi, lo;
+        split_query(v, down, &hi, &lo);
+        const int panel = x / (C::PW / 16), cc = x % (C::PW / 16), sw = D == 64 ? cc ^ ((tid >> 1) & 3) : cc ^ (tid & 7);
+        uint8_t* at = qd + panel * 128 * C::PW + tid * C::PW + sw * 16;
+        *reinterpret_cast<uint4*>(at) = hi;
+        *reinterpret_cast<uint4*>(at + 128 * D) = lo;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.qfull);
+    }
+    float m = -INFINITY, l = 0.0f;
+    // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
+    const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
+    bool dead = false;
+    const uint32_t ot = tmem + lane_base + C::OCOL + mt * D;
+    for (int i = 0; i < n && mt < tiles; ++i) {
+      const int sb = MT == 1 ? i & 1 : 0, buf = mt * C::SB + sb;
+      if (!wait(&sh.sfull[buf], (MT == 1 ? i >> 1 : i) & 1, c.status)) dead = true;
+      dead = __any_sync(0xFFFFFFFFu, dead);
+      if (dead) break;
+      tc_fence_after();
+      const StepMeta& sm = sh.step[i & 7];
+      const uint32_t st = tmem + lane_base + buf * BN;
+      const int t0 = first_key + i * BN;
+      const bool masked = sm.cut || t0 + BN - 1 > see || t0 <= skip;
+      // the row's largest t (its factor stays above 0, so that a masked score stays -inf)
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int x = 0; x < BN; x += 32) {
+        uint32_t s[32];
+        tmem_ld32(st + x, s);
+        tmem_ld_wait();
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int t = t0 + x + e;
+            if (t > pos || t <= pos - a.window) s[e] = 0xFF800000u;
+          }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float mx = __uint_as_float(s[16 * h]);
+#pragma unroll
+          for (int e = 1; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(s[16 * h + e]));
+          const float ks = sm.ks[x / 16 + h];
+          const float t = fmaf(mx, fmaxf(rc * ks, 0x1p-126f), sm.lvs[x / 16 + h]);
+          if (ks != 0.0f && mx != -INFINITY) top = fmaxf(top, t);
+        }
+      }
+      const bool grow = top > m + kLazy || (m == -INFINITY && top != -INFINITY);
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float w = grow ? ex2(m - top) : 1.0f;
+        if (grow) m = top;
+        l *= w;
+        if (i > 0) {
+          if (MT == 1) {  // the product before may still run
+            if (!wait(&sh.vfree[(i - 1) % C::FS], (uint32_t)((i - 1) / C::FS) & 1u, c.status)) dead = true;
+            dead = __any_sync(0xFFFFFFFFu, dead);
+            if (dead) break;
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int x = 0; x < D; x += 32) {
+            uint32_t o[32];
+            tmem_ld32(ot + x, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
+            tmem_st32(ot + x, o);
+          }
+          tmem_st_wait();
+        }
+      }
+      const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+      for (int x = 0; x < BN; x += 32) {
+        uint32_t s[32];
+        tmem_ld32(st + x, s);
+        tmem_ld_wait();
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int t = t0 + x + e;
+            if (t > pos || t <= pos - a.window) s[e] = 0xFF800000u;
+          }
+        }
+        uint32_t p[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float ks = sm.ks[x / 16 + h], f = fmaxf(rc * ks, 0x1p-126f), off = sm.lvs[x / 16 + h] - ref;
+          float sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float p0 = ex2(fmaf(__uint_as_float(s[16 * h + e]), f, off));
+            float p1 = ex2(fmaf(__uint_as_float(s[16 * h + e + 1]), f, off));
+            sum += p0 + p1;
+            p[8 * h + e / 2] = f16x2(p0, p1);
+          }
+          if (masked && ks == 0.0f) {  // hidden keys: their scores may be NaN
+            sum = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[8 * h + e] = 0u;
+          }
+          l = fmaf(sum, sm.ivs[x / 16 + h], l);
+        }
+        tmem_st16(st + x / 2, p);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      mbar_arrive(&sh.pfull[buf]);
+    }
+    if (n > 0 && mt < tiles && !dead && !wait(&sh.odone[mt], 0, c.status)) dead = true;
+    dead = __any_sync(0xFFFFFFFFu, dead);
+    tc_fence_after();
+    if (!dead && mt < tiles) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      const int64_t part = ((int64_t)blockIdx.x * c.hkv + head) * pa.splits + split;
+      uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso;
+#pragma unroll 1
+      for (int x = 0; x < D; x += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(ot + x, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
+        }
+        if (in) {
+          if (pa.splits == 1) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              uint32_t y[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                y[z] = bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+              *reinterpret_cast<uint4*>(out + x + e) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          } else {
+            float* dst = pa.part_o + (part * C::ROWS + row) * D + x;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
+      }
+      if (in && pa.splits > 1) pa.part_ml[part * C::ROWS + row] = make_float2(m, l);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (!run || pa.splits == 1) return;
+  // the CTA whose ticket completes the block joins its parts, in order
+  int* counter = pa.counters + (int64_t)blockIdx.x * c.hkv + head;
+  if (threadIdx.x == 0) sh.ticket = ticket_add(counter, 1);
+  __syncthreads();
+  if (sh.ticket != pa.splits - 1) return;
+  const int64_t part0 = ((int64_t)blockIdx.x * c.hkv + head) * pa.splits;
+  for (int e = threadIdx.x; e < R * (D / 8); e += C::THREADS) {
+    const int row = e / (D / 8), d = e % (D / 8) * 8;
+    float top = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int s = 0; s < pa.splits; ++s) top = fmaxf(top, __ldcg(&pa.part_ml[(part0 + s) * C::ROWS + row]).x);
+#pragma unroll 2
+    for (int s = 0; s < pa.splits; ++s) {
+      const float2 z = __ldcg(&pa.part_ml[(part0 + s) * C::ROWS + row]);
+      const float4* src = reinterpret_cast<const float4*>(pa.part_o + ((part0 + s) * C::ROWS + row) * D + d);
+      const float4 y0 = __ldcg(src), y1 = __ldcg(src + 1);
+      const float f = z.x == -INFINITY ? 0.0f : ex2(z.x - top);
+      const float y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] = fmaf(y[k], f, o[k]);
+      l = fmaf(z.y, f, l);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const int64_t r = row0 + row;
+    const int tok = (int)(r / G), g = (int)(r - (int64_t)tok * G);
+    *reinterpret_cast<uint4*>(a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + d) =
+        make_uint4(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv), bf16x2(o[4] * inv, o[5] * inv),
+                   bf16x2(o[6] * inv, o[7] * inv));
+  }
+  if (threadIdx.x == 0) *counter = 0;
+}
+
+template <int D>
+int launch(const AttnArgs& a, const PrefillPlan& p, void* ws, cudaStream_t s) {
+  using C = Cfg<D>;
+  static std::atomic<unsigned long long> configured{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return QG_ERR_CUDA;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(configured.load() & bit)) {
+    if (cudaFuncSetAttribute((const void*)attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
+        cudaSuccess)
+      return QG_ERR_CUDA;
+    configured.fetch_or(bit);
+  }
+  const int page = 1 << a.c.page_log2, box = std::min(page, C::BN);
+  CUtensorMap km, vm;
+  if (!encode_pages(&km, a.c.k, D, page, a.c.n_pages * a.c.hkv, box) ||
+      !encode_pages(&vm, a.c.v, D, page, a.c.n_pages * a.c.hkv, box))
+    return QG_ERR_CUDA;
+  PrefillArgs pa;
+  pa.a = a;
+  pa.splits = p.splits;
+  pa.blocks = p.blocks;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  pa.counters = reinterpret_cast<int*>(w + kWsHeader);
+  pa.part_ml = reinterpret_cast<float2*>(w + p.off_ml);
+  pa.part_o = reinterpret_cast<float*>(w + p.off_o);
+  return launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)p.blocks, (unsigned)(a.c.hkv * p.splits)), dim3(C::THREADS),
+                    C::SMEM, s, km, vm, pa) == cudaSuccess
+             ? QG_OK
+             : QG_ERR_CUDA;
+}
+
+}  // namespace
+
+bool plan_prefill(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int hq, const DeviceInfo& dev,
+                  PrefillPlan* p) {
+  const int64_t G = hq / cache->n_kv_heads, rows = cache->head_dim == 256 ? 128 : 256;
+  const int64_t each = (batch->max_new * G + rows - 1) / rows;
+  // a sequence of t tokens has at most t * G / rows + 1 blocks
+  p->blocks = std::min<int64_t>(each * batch->n_seqs, n_tokens * G / rows + batch->n_seqs);
+  const int64_t items = p->blocks * cache->n_kv_heads;
+  if (p->blocks > 0x7FFFFFFF || items > 0x7FFFFFFF) return false;
+  // blocks that leave the GPU's last wave emptier than half a wave of many are cut along the keys, into
+  // parts of 1024 keys at least
+  int64_t s = std::min<int64_t>(2 * (int64_t)dev.sms / std::max<int64_t>(items, 1), batch->max_len / 1024);
+  s = std::min<int64_t>(std::max<int64_t>(s, 1), 32);
+  p->splits = (int)s;
+  p->off_ml = kWsHeader + kAttnCounterBytes;
+  p->off_o = p->off_ml;
+  p->ws_bytes = p->off_ml;
+  if (s > 1) {
+    p->off_o = p->off_ml + (size_t)(items * s * rows) * sizeof(float2);
+    p->ws_bytes = p->off_o + (size_t)(items * s * rows) * cache->head_dim * sizeof(float);
+  }
+  return s == 1 || items * sizeof(int) <= kAttnCounterBytes;
+}
+
+int launch_attn_prefill(const AttnArgs& a, int head_dim, const PrefillPlan& p, void* ws, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (head_dim) {
+    case 64: return launch<64>(a, p, ws, s);
+    case 128: return launch<128>(a, p, ws, s);
+    case 256: return launch<256>(a, p, ws, s);
+  }
+  return QG_ERR_UNSUPPORTED;
+}
+
+}  // namespace qg

@@ -51,10 +51,18 @@ struct AttnArgs {
 };
 
 // How qattn divides the work; a function of the sizes alone.
+struct PrefillPlan {
+  int64_t blocks;  // upper bound of the row blocks of a KV head
+  int splits;      // parts of a block along the keys
+  size_t off_ml, off_o, ws_bytes;
+};
 struct AttnPlan {
   size_t ws_bytes;
   bool decode;  // few rows a KV head: the streaming kernel
+  PrefillPlan prefill;
 };
+// Counters of the joins, right behind the workspace's header whatever the call.
+constexpr size_t kAttnCounterBytes = 4096;
 bool plan_attn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int hq, const DeviceInfo& dev,
                AttnPlan* p);
 int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan& p, const DeviceInfo& dev, void* ws, void* stream);
@@ -62,6 +70,10 @@ int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan& p, const Device
 int decode_rows(int64_t rows);  // the row count it is built for: 16, 32, 64; 0: too many
 size_t decode_workspace(int64_t rows, int head_dim, const DeviceInfo& dev);
 int launch_attn_decode(const AttnArgs& a, int head_dim, int64_t rows, const DeviceInfo& dev, void* ws, void* stream);
+// The row-block kernel of more rows.
+bool plan_prefill(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int hq, const DeviceInfo& dev,
+                  PrefillPlan* p);
+int launch_attn_prefill(const AttnArgs& a, int head_dim, const PrefillPlan& p, void* ws, void* stream);
 // Pages of codes as a 3-D TMA tensor (head_dim bytes x page_tokens x tiles, tile = page * n_kv_heads +
 // head): box of min(head_dim, 128) bytes x box_tokens tokens, swizzled by its width.
 bool encode_pages(CUtensorMap* map, const void* codes, int head_dim, int page_tokens, int64_t tiles, int box_tokens);

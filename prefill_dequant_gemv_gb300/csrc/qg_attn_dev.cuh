@@ -1,0 +1,142 @@
+// Device helpers of the attention kernels: bounded waits, conversions between fp16 and E4M3, TMA of page
+// boxes, and the E4M3 MMAs (tcgen05, kind::f8f6f4).
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "qg_sync.cuh"
+
+namespace qg {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// mbar_wait_bounded in few instructions: this kernel's many roles share one instruction cache.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  do {
+    if (mbar_try_wait_sleep(bar, parity, 1000000u)) return true;
+  } while (global_ns() - t0 < kWaitLimitNs);
+  atomicExch(status, kStatusTimeout);
+  return false;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {  // a in the low half
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+__device__ __forceinline__ uint16_t e4m3x2(uint32_t h) {  // two fp16 -> two codes, the low half in the low byte
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+__device__ __forceinline__ uint32_t codes_f16x2(uint16_t c) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+// 16 * (h - c) of two fp16 pairs: exact where c is h rounded to fewer bits
+__device__ __forceinline__ uint32_t rest16(uint32_t h, uint32_t c) {
+  uint32_t d, r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(c));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x4C004C00u));
+  return r;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::
+          "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// Shared-memory matrix descriptor (version 1) as its two halves: start and leading byte offset; stride
+// byte offset and swizzle (0 none, 2 128 bytes, 4 64 bytes).  Adding bytes / 16 to the low half moves the start.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
+constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return sbo >> 4 | 1u << 14 | swizzle << 29; }
+// kind::f8f6f4, E4M3 x E4M3 -> fp32, M = 128; ta, tb: A, B lie M- or N-contiguous.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int n, int ta, int tb) {
+  return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+}
+template <uint32_t AHI, uint32_t BHI, uint32_t IDESC>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t alo, uint32_t blo, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %6, 0;\n\tmov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d), "r"(alo), "n"(AHI), "r"(blo), "n"(BHI),
+      "n"(IDESC), "r"(acc)
+      : "memory");
+}
+// One lane of the warp, chosen so that the compiler knows the branch on it takes one thread.
+__device__ __forceinline__ bool elect() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// Barrier of a softmax group's four warps that returns whether any thread's v is set.
+__device__ __forceinline__ bool any_of(int group, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(1 + group), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float warp_max(float v) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float lg2(float x) {
+  float r;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 16 bf16 values of a query row, times the power of two `down`, as two E4M3 terms whose sum they are: bf16
+// has 8 significant bits, a term 4 and a sign.  Exact but for elements 2^-9 below the row's largest.
+__device__ __forceinline__ void split_query(const uint4 (&x)[2], float down, uint4* hi, uint4* lo) {
+  const uint32_t v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint16_t hh[2], ll[2];
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+      const uint32_t b = v[2 * e + z];
+      // bf16's bits fit fp16 at this size but for the smallest elements
+      const uint32_t h16 = f16x2(__uint_as_float(b << 16) * down, __uint_as_float(b & 0xFFFF0000u) * down);
+      hh[z] = e4m3x2(h16);
+      uint32_t d16;
+      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d16) : "r"(h16), "r"(codes_f16x2(hh[z])));
+      ll[z] = e4m3x2(d16);
+    }
+    h[e] = hh[0] | (uint32_t)hh[1] << 16;
+    l[e] = ll[0] | (uint32_t)ll[1] << 16;
+  }
+  *hi = make_uint4(h[0], h[1], h[2], h[3]);
+  *lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+// Two codes of a word (its low or high half) -> two fp16 values.
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return codes_f16x2((uint16_t)w); }
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return codes_f16x2((uint16_t)(w >> 16)); }
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {  // a in the low half
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+}  // namespace qg
