@@ -820,6 +820,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         }
         any_of(grp, false);
       }
+      // A group without a tile of this pair waits for the join before it all the same: nobody is two pairs
+      // ahead of a join, so no phase of the two barriers below is missed or arrived at twice.
+      if (!took) {
+        if (p > 0 && !wait(&sh.joined, (uint32_t)(p - 1) & 1u, c.status)) dead = true;
+        if (any_of(grp, dead)) break;
+      }
       const bool join = (i1 - 1) % NG == grp;
       if (tid == 0) mbar_arrive(&sh.summed);
       if (join) {

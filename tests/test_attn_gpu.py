@@ -73,6 +73,34 @@ def check_attention(got, ref, d, keys):
     assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], ref[0][bad][:5])
 
 
+def _device_reference(c, qh, window, scale):
+    """The oracle's attention in torch float64 on the GPU, for batches too large for loops over rows."""
+    from oracle.attention import e4m3_decode
+    grid = torch.from_numpy(np.nan_to_num(e4m3_decode(np.arange(256)))).cuda()
+    out, mag, load, vmax = (torch.zeros(c.n, qh.shape[1], w, dtype=torch.float64, device="cuda") for w in (c.d, c.d, 1, 1))
+    kc, vc = (torch.from_numpy(x).cuda().long() for x in (c.kc, c.vc))
+    ks, vs = (torch.from_numpy(np.nan_to_num(x)).cuda().double() for x in (c.ks, c.vs))
+    grp = qh.shape[1] // c.hkv
+    for b, (t, length) in enumerate(zip(c.news, c.lens)):
+        if not t or not length:
+            continue
+        ids = torch.from_numpy(c.pages[b, :-(-length // c.page)]).cuda().long()
+        pos = torch.arange(length - t, length, device="cuda")[:, None]
+        j = torch.arange(length, device="cuda")
+        see = (j <= pos) & ((j > pos - window) if window else True)
+        k, v = ((grid[x[ids]] * y[ids][..., None, None]).transpose(0, 1).reshape(c.hkv, -1, c.d)[:, :length]
+                for x, y in ((kc, ks), (vc, vs)))
+        q = qh[c.starts[b]:c.starts[b + 1]].cuda().double().view(t, c.hkv, grp, c.d).permute(1, 2, 0, 3)
+        s = torch.matmul(q, k[:, None].transpose(-1, -2)) * scale
+        p = torch.softmax(s.masked_fill(~see, -torch.inf), -1)
+        r = slice(c.starts[b], c.starts[b + 1])
+        put = lambda x: x.permute(2, 0, 1, 3).reshape(t, -1, x.shape[-1])  # noqa: E731
+        out[r], mag[r] = put(torch.matmul(p, v[:, None])), put(torch.matmul(p, v.abs()[:, None]))
+        load[r] = put((torch.matmul(q.abs(), k.abs()[:, None].transpose(-1, -2)) * scale).amax(-1, keepdim=True))
+        vmax[r] = v.abs().amax()
+    return out.cpu().numpy(), mag.cpu().numpy(), load[..., 0].cpu().numpy(), vmax[..., 0].cpu().numpy()
+
+
 # ------------------------------------------------------------------ append
 def _table(rot, n):
     if not rot:
@@ -208,6 +236,43 @@ def test_attention_against_oracle(d, page, hkv, hq, news, lens, window):
     assert torch.equal(got, q.attention(cache, batch, qd, window=window, workspace=ws))  # again, bit for bit
     loose = c.device(q, max_new=max(news) + 300, max_len=(c.pages.shape[1]) * page)[1]  # looser bounds
     check_attention(q.attention(cache, loose, qd, window=window), c.attention(qh, d ** -0.5, window), d, max(lens))
+
+
+@pytest.mark.parametrize("d,hkv,hq,page,new,most", [(128, 4, 20, 32, 1, 900), (64, 4, 32, 16, 1, 500), (256, 2, 12, 64, 2, 700),
+                                                    (128, 8, 8, 64, 3, 6000), (64, 2, 40, 128, 3, 3000), (256, 4, 4, 16, 1, 5000)])
+def test_many_sequences_of_all_lengths(d, hkv, hq, page, new, most):
+    """More work than CTAs: pairs of fewer tiles than a CTA works on at once, rings that go round, pairs cut between
+    CTAs.  Every one of many calls gives the same bits."""
+    q = qlib()
+    rng = np.random.default_rng(most)
+    lens = [int(x) for x in np.exp(rng.uniform(np.log(new), np.log(most), 96))] + [most, new]
+    c = Case(most, [new if i % 7 else 0 for i in range(len(lens))], lens, page, hkv, d)
+    qh = c.heads(hq, 2.0)
+    cache, batch = c.device(q)
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, c.n, hq))
+    qd = qh.cuda()
+    first = q.attention(cache, batch, qd, workspace=ws).clone()
+    check_attention(first, _device_reference(c, qh, 0, d ** -0.5), d, most)
+    outs = [q.attention(cache, batch, qd, workspace=ws) for _ in range(200)]
+    assert ws.status() == 0
+    assert all(torch.equal(first, o) for o in outs)
+
+
+@pytest.mark.parametrize("d,hkv,hq,page,news,lens,window", [
+    (128, 8, 40, 64, [1500, 300, 1, 700], [1500, 4000, 900, 701], 0), (256, 4, 24, 16, [600, 20], [5000, 20], 0),
+    (64, 4, 32, 32, [999, 1200, 64], [1000, 1500, 3000], 700)])
+def test_long_prompts(d, hkv, hq, page, news, lens, window):
+    q = qlib()
+    c = Case(sum(news), news, lens, page, hkv, d)
+    qh = c.heads(hq, 2.0)
+    cache, batch = c.device(q)
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, c.n, hq))
+    qd = qh.cuda()
+    first = q.attention(cache, batch, qd, window=window, workspace=ws).clone()
+    check_attention(first, _device_reference(c, qh, window, d ** -0.5), d, max(lens))
+    outs = [q.attention(cache, batch, qd, window=window, workspace=ws) for _ in range(50)]
+    assert ws.status() == 0
+    assert all(torch.equal(first, o) for o in outs)
 
 
 @pytest.mark.parametrize("news,lens", [([1, 1], [300, 40]), ([150], [400])])
