@@ -4,9 +4,9 @@
 //   keys:    the same, then E4M3 codes under the scale of their (page, KV head);
 //   values:  E4M3 codes under theirs.
 //
-// A head of D elements lies across D/8 lanes, eight elements (one 16-byte load) each: the norm is a
-// shuffle sum over those lanes, and a rotation's pairs are either in one lane (interleaved) or
-// R/16 lanes apart (one shuffle), so nothing passes through shared memory.
+// A head of D elements lies across D/8 lanes, eight elements each in two runs of four that hold both
+// elements of a rotation's pairs: 4l .. and R/2 + 4l .. (pairs R/2 apart), or 8l .. (neighbours).  So the norm's
+// sum is the only thing that crosses lanes, and a lane needs four angles.
 //
 // Keys and values are worked on by unit = (page, KV head, K or V): the page's scale depends on all
 // its new tokens, so one group of threads owns them, holds the normed values in registers
@@ -30,7 +30,7 @@ namespace qg {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kQPasses = 4;      // heads a query lane group takes, their loads issued together
+constexpr int kQHeads = 4;       // heads of one token a query lane group takes: one position, one set of angles
 constexpr int kWarpRows = 4;     // new tokens a sequence up to which a warp owns a unit
 
 // Two floats -> two E4M3 codes (a in the low byte), nearest even, saturating; NaN stays NaN.
@@ -45,17 +45,32 @@ __device__ __forceinline__ float e4m3_value(uint32_t code) {
   return static_cast<float>(v);
 }
 
-__device__ __forceinline__ void unpack8(uint4 w, float (&f)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(u[i] << 16);
-    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-  }
+// Two fp32 numbers in a register pair, worked on by one instruction.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ uint64_t pair(F2 v) { return (uint64_t)__float_as_uint(v.y) << 32 | __float_as_uint(v.x); }
+__device__ __forceinline__ F2 unpair(uint64_t v) {
+  return {__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32))};
 }
-__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)));
+  return unpair(d);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(pair(a)), "l"(pair(b)), "l"(pair(c)));
+  return unpair(d);
+}
+__device__ __forceinline__ void unpack8(uint2 v, uint2 w, F2 (&f)[4]) {
+  const uint32_t u[4] = {v.x, v.y, w.x, w.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = {__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u)};
+}
+__device__ __forceinline__ uint32_t bf16x2(F2 v) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(v.x, v.y);
+  return *reinterpret_cast<const uint32_t*>(&r);
 }
 
 // The exponent x of the smallest power of two with amax <= 448 * 2^x (448 = 1.75 * 2^8),
@@ -66,81 +81,61 @@ __device__ __forceinline__ int scale_exponent(float amax) {
   return min(max(x, -100), 120);
 }
 
-// A lane's share of the norm and rotation: eight elements from 8 * l on of a head of LPH lanes.
+// A lane's share of the norm and rotation of a head of LPH lanes: four elements from a on and four from b on.
 template <int LPH>
 struct NormRope {
-  float w[8];
-  bool norm;
-  float eps, c[8], s[8];
-  int rot, l;
-  bool inter;
+  F2 w[4], c[2], s[2];
+  float eps;
+  int a, b;
+  bool norm, inter, turn;  // turn: this lane's elements are rotated
 
-  __device__ __forceinline__ void weights(const uint16_t* weight, float off, float eps_, int lane_in_head) {
-    l = lane_in_head;
+  __device__ __forceinline__ void init(const uint16_t* weight, float off, float eps_, int rot, int interleaved, int l) {
     eps = eps_;
+    inter = interleaved;
+    turn = 8 * l < rot;
+    a = turn && !inter ? 4 * l : 8 * l;
+    b = turn && !inter ? rot / 2 + 4 * l : 8 * l + 4;
     norm = weight != nullptr;
     if (norm) {
-      unpack8(__ldg(reinterpret_cast<const uint4*>(weight) + l), w);
+      unpack8(__ldg(reinterpret_cast<const uint2*>(weight + a)), __ldg(reinterpret_cast<const uint2*>(weight + b)), w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] += off;
+      for (int i = 0; i < 4; ++i) w[i].x += off, w[i].y += off;
     }
   }
-  // cos and sin of this lane's elements for one position; an element outside the rotation
-  // turns by zero
-  __device__ __forceinline__ void angles(const float* cs, int rot_, int interleaved, int64_t pos) {
-    rot = rot_;
-    inter = interleaved;
-    const int half = rot / 2;
-    if (8 * l < rot) {
-      const float* row = cs + pos * rot;
-      if (inter) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
-        const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + 4 * l));
-        c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
-        s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
-      } else {
-        const int j = 8 * l < half ? 8 * l : 8 * l - half;
-#pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(row + j + i));
-          const float4 b = __ldg(reinterpret_cast<const float4*>(row + half + j + i));
-          c[i] = a.x, c[i + 1] = a.y, c[i + 2] = a.z, c[i + 3] = a.w;
-          s[i] = b.x, s[i + 1] = b.y, s[i + 2] = b.z, s[i + 3] = b.w;
-        }
-      }
+  __device__ __forceinline__ void angles(const float* cs, int rot, int64_t pos, int l) {
+    if (turn) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(cs + pos * rot + 4 * l));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(cs + pos * rot + rot / 2 + 4 * l));
+      c[0] = {x.x, x.y}, c[1] = {x.z, x.w};
+      s[0] = {y.x, y.y}, s[1] = {y.z, y.w};
     }
   }
   // every lane of the warp calls this
-  __device__ __forceinline__ void apply(float (&y)[8]) const {
+  __device__ __forceinline__ void apply(F2 (&y)[4]) const {
     if (norm) {
-      float ss = 0.0f;
+      F2 q = mul2(y[0], y[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+      for (int i = 1; i < 4; ++i) q = fma2(y[i], y[i], q);
+      float ss = q.x + q.y;
 #pragma unroll
       for (int o = LPH / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      const float r = __frsqrt_rn(ss * (1.0f / (8 * LPH)) + eps);
+      const float r = rsqrtf(fmaf(ss, 1.0f / (8 * LPH), eps));
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = y[i] * r * w[i];
+      for (int i = 0; i < 4; ++i) y[i] = mul2(mul2(y[i], {r, r}), w[i]);
     }
-    if (rot == 0) return;
+    if (!turn) return;
     if (inter) {
-      if (8 * l < rot) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = y[2 * i], b = y[2 * i + 1];
-          y[2 * i] = a * c[i] - b * s[i];
-          y[2 * i + 1] = b * c[i] + a * s[i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const float cc = i & 1 ? c[i / 2].y : c[i / 2].x, sn = i & 1 ? s[i / 2].y : s[i / 2].x;
+        y[i] = {y[i].x * cc - y[i].y * sn, y[i].y * cc + y[i].x * sn};
       }
     } else {
-      const int d = rot / 16;  // lanes between the elements of a pair
-      const bool low = l < d, in = l < 2 * d;
-      const int lane = threadIdx.x & 31;
-      const int from = in ? (low ? lane + d : lane - d) : lane;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float o = __shfl_sync(0xFFFFFFFFu, y[i], from);
-        if (in) y[i] = low ? y[i] * c[i] - o * s[i] : y[i] * c[i] + o * s[i];
+      for (int i = 0; i < 2; ++i) {
+        const F2 u = y[i], v = y[2 + i];
+        y[i] = fma2(v, {-s[i].x, -s[i].y}, mul2(u, c[i]));
+        y[2 + i] = fma2(u, s[i], mul2(v, c[i]));
       }
     }
   }
@@ -159,50 +154,44 @@ __device__ __forceinline__ int seq_of_row(const KvArgs& c, int64_t i) {
   return lo;
 }
 
-// The queries: items (row, head) in order, kQPasses a lane group.
+// The queries: a lane group takes kQHeads heads of one token, their loads issued together.
 template <int LPH>
-__device__ __forceinline__ void append_queries(const AppendArgs& a, int64_t block) {
+__device__ __forceinline__ void append_queries(const AppendArgs& a, uint32_t block) {
   constexpr int GROUPS = kAppendThreads / LPH;
   const int l = threadIdx.x % LPH;
-  const int64_t items = a.c.n_tokens * a.hq;
-  const int64_t first = block * (GROUPS * kQPasses) + threadIdx.x / LPH;
+  const uint32_t per = (uint32_t)(a.hq + kQHeads - 1) / kQHeads;
+  const uint32_t item = block * GROUPS + threadIdx.x / LPH, row = item / per;
+  const int h0 = (int)(item - row * per) * kQHeads;
   NormRope<LPH> nr;
-  nr.weights(a.qw, a.woff, a.eps, l);
-  uint4 x[kQPasses];
-  int64_t row[kQPasses];
-  int head[kQPasses];
+  nr.init(a.qw, a.woff, a.eps, a.rot, a.interleaved, l);
+  uint2 x[kQHeads][2];
+  const bool in = row < a.c.n_tokens;
+  const uint16_t* src = a.q + (int64_t)row * a.ldq + h0 * a.hsq;
 #pragma unroll
-  for (int p = 0; p < kQPasses; ++p) {
-    const int64_t it = first + p * GROUPS;
-    row[p] = -1;
-    head[p] = 0;
-    x[p] = make_uint4(0, 0, 0, 0);
-    if (it < items) {
-      row[p] = it / a.hq;
-      head[p] = (int)(it - row[p] * a.hq);
-      x[p] = *reinterpret_cast<const uint4*>(a.q + row[p] * a.ldq + head[p] * a.hsq + 8 * l);
+  for (int p = 0; p < kQHeads; ++p, src += a.hsq) {
+    x[p][0] = x[p][1] = make_uint2(0, 0);
+    if (in && h0 + p < a.hq) {
+      x[p][0] = *reinterpret_cast<const uint2*>(src + nr.a);
+      x[p][1] = *reinterpret_cast<const uint2*>(src + nr.b);
     }
   }
-  int64_t at = -1;
   bool use = false;
+  if (in) {
+    bool bad = false;
+    const Seq s = seq_of(a.c, seq_of_row(a.c, row), &bad);
+    use = s.len >= s.rows && row >= (uint32_t)s.start && row < (uint32_t)(s.start + s.rows);
+    if (use) nr.angles(a.cs, a.rot, (int64_t)s.len - s.rows + (int)(row - s.start), l);
+  }
+  uint16_t* dst = a.qo + (int64_t)row * a.ldo + h0 * a.hso;
 #pragma unroll
-  for (int p = 0; p < kQPasses; ++p) {
-    if (row[p] >= 0 && row[p] != at) {
-      at = row[p];
-      bool bad = false;
-      const Seq s = seq_of(a.c, seq_of_row(a.c, at), &bad);
-      use = s.len >= s.rows && at >= s.start && at < (int64_t)s.start + s.rows;
-      if (use) nr.angles(a.cs, a.rot, a.interleaved, (int64_t)s.len - s.rows + (at - s.start));
-      else nr.rot = a.rot, nr.inter = a.interleaved;
-    } else if (row[p] < 0 && at < 0) {
-      nr.rot = a.rot, nr.inter = a.interleaved;
-    }
-    float y[8];
-    unpack8(x[p], y);
+  for (int p = 0; p < kQHeads; ++p, dst += a.hso) {
+    F2 y[4];
+    unpack8(x[p][0], x[p][1], y);
     nr.apply(y);
-    if (row[p] >= 0 && use)
-      *reinterpret_cast<uint4*>(a.qo + row[p] * a.ldo + head[p] * a.hso + 8 * l) =
-          make_uint4(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]), bf16x2(y[4], y[5]), bf16x2(y[6], y[7]));
+    if (use && h0 + p < a.hq) {
+      *reinterpret_cast<uint2*>(dst + nr.a) = make_uint2(bf16x2(y[0]), bf16x2(y[1]));
+      *reinterpret_cast<uint2*>(dst + nr.b) = make_uint2(bf16x2(y[2]), bf16x2(y[3]));
+    }
   }
 }
 
@@ -279,32 +268,43 @@ __device__ __forceinline__ void append_unit(const AppendArgs& a, int64_t unit, i
 
   const uint16_t* src = is_v ? a.vin + (int64_t)h * a.hsv : a.kin + (int64_t)h * a.hsk;
   const int64_t ld = is_v ? a.ldv : a.ldk;
-  uint4 x[ITER];
+  NormRope<LPH> nr;
+  nr.init(is_v ? nullptr : a.kw, a.woff, a.eps, is_v ? 0 : a.rot, a.interleaved, l);
+  uint2 x[ITER][2];
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
     const int t = lo + i * TPP + g / LPH;
-    x[i] = t < hi ? *reinterpret_cast<const uint4*>(src + (int64_t)(s.start + (t - first)) * ld + 8 * l)
-                  : make_uint4(0, 0, 0, 0);
+    x[i][0] = x[i][1] = make_uint2(0, 0);
+    if (t < hi) {
+      const uint16_t* at = src + (int64_t)(s.start + (t - first)) * ld;
+      x[i][0] = *reinterpret_cast<const uint2*>(at + nr.a);
+      x[i][1] = *reinterpret_cast<const uint2*>(at + nr.b);
+    }
   }
-  float y[ITER][8];
+  F2 y[ITER][4];
   float amax = 0.0f;
-  NormRope<LPH> nr;
-  if (!is_v) nr.weights(a.kw, a.woff, a.eps, l);
 #pragma unroll
   for (int i = 0; i < ITER; ++i) {
-    unpack8(x[i], y[i]);
+    unpack8(x[i][0], x[i][1], y[i]);
     if (!is_v && lo + i * TPP < hi) {  // the same for the whole group
-      const int t = min(lo + i * TPP + g / LPH, hi - 1);
-      nr.angles(a.cs, a.rot, a.interleaved, t);
+      nr.angles(a.cs, a.rot, min(lo + i * TPP + g / LPH, hi - 1), l);
       nr.apply(y[i]);
     }
     if (lo + i * TPP + g / LPH < hi) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float m = fabsf(y[i][e]);
-        amax = fmaxf(amax, m <= 3.402823466e38f ? m : 0.0f);
-      }
+      for (int e = 0; e < 4; ++e) amax = fmaxf(amax, fmaxf(fabsf(y[i][e].x), fabsf(y[i][e].y)));  // NaN does not count
     }
+  }
+  if (amax == INFINITY) {  // nor do infinities
+    amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < ITER; ++i)
+      if (lo + i * TPP + g / LPH < hi)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float u = fabsf(y[i][e].x), v = fabsf(y[i][e].y);
+          amax = fmaxf(amax, fmaxf(u < INFINITY ? u : 0.0f, v < INFINITY ? v : 0.0f));
+        }
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
@@ -339,15 +339,16 @@ __device__ __forceinline__ void append_unit(const AppendArgs& a, int64_t unit, i
   for (int i = 0; i < ITER; ++i) {
     const int t = lo + i * TPP + g / LPH;
     if (t >= hi) break;
-    uint32_t w[2];
+    uint8_t* at = tile + (int64_t)(t - base) * D;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      float* f = y[i] + 4 * k;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) f[e] = exact ? f[e] * inv : f[e] / scale;
-      w[k] = e4m3x2(f[0], f[1]) | (e4m3x2(f[2], f[3]) << 16);
+      F2 u = y[i][2 * k], v = y[i][2 * k + 1];
+      if (exact)
+        u = mul2(u, {inv, inv}), v = mul2(v, {inv, inv});
+      else
+        u = {u.x / scale, u.y / scale}, v = {v.x / scale, v.y / scale};
+      *reinterpret_cast<uint32_t*>(at + (k ? nr.b : nr.a)) = e4m3x2(u.x, u.y) | (e4m3x2(v.x, v.y) << 16);
     }
-    *reinterpret_cast<uint2*>(tile + (int64_t)(t - base) * D + 8 * l) = make_uint2(w[0], w[1]);
   }
 }
 
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(GT > kAppendThreads ? GT : kAppendThreads)
     const int64_t unit = GT == 32 ? (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (unit < units) append_unit<LPH, GT, ITER>(a, unit, per_seq, scan != 0, red);
   } else if (threadIdx.x < kAppendThreads) {
-    append_queries<LPH>(a, (int64_t)blockIdx.x - kv_blocks);
+    append_queries<LPH>(a, (uint32_t)(blockIdx.x - kv_blocks));
   }
 }
 
@@ -374,9 +375,9 @@ int launch(const AppendArgs& a, cudaStream_t s) {
   const bool scan = direct > 2 * bound;  // far fewer pages than slots: find each unit's sequence by a scan
   const int64_t units = (scan ? bound : direct) * 2 * c.hkv;
   const int64_t kv_blocks = GT == 32 ? (units + kAppendThreads / 32 - 1) / (kAppendThreads / 32) : units;
-  const int64_t per_block = kAppendThreads / LPH * kQPasses;
-  const int64_t q_blocks = (c.n_tokens * a.hq + per_block - 1) / per_block;
-  if (kv_blocks + q_blocks > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;
+  const int64_t q_items = c.n_tokens * ((a.hq + kQHeads - 1) / kQHeads), groups = kAppendThreads / LPH;
+  const int64_t q_blocks = (q_items + groups - 1) / groups;
+  if (kv_blocks + q_blocks > 0x7FFFFFFF || q_items + groups > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;
   append_kernel<LPH, GT, ITER><<<(unsigned)(kv_blocks + q_blocks), std::max(GT, kAppendThreads), 0, s>>>(
       a, units, kv_blocks, (int)per, scan ? 1 : 0);
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
