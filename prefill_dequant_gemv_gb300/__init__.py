@@ -507,6 +507,18 @@ def _need(ok: bool, what: str):
         raise QGError(1, what)
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream of a device, as torch keeps it."""
+    import torch
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+def _raw_stream_getter():
+    """torch's own accessor of the current stream's handle (0.1 us a call; a Stream object takes 1.2) where it has one."""
+    import torch
+    return getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 class KVCache:
     """A pool of pages of keys and values in 8 bits (``qg_kv_cache``): codes float8_e4m3fn (or uint8)
     [n_pages, n_kv_heads, page_tokens, head_dim] and scales fp32 [n_pages, n_kv_heads], contiguous on the device."""
@@ -522,7 +534,10 @@ class KVCache:
         for t in (k_scales, v_scales):
             _need(t.dtype == torch.float32, "KVCache: scales are float32")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = k_codes.shape
+        self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = (int(x) for x in k_codes.shape)
+        # what each call needs of torch, looked up once: calls of a decode step are short
+        self.bf16, self.index = torch.bfloat16, k_codes.device.index
+        self.raw_stream = _raw_stream_getter()
         self.desc = qg_kv_cache(QG_KV_E4M3, self.page_tokens, self.n_kv_heads, self.head_dim, self.n_pages,
                                 k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
 
@@ -570,6 +585,9 @@ class NormRope:
         _need(cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()),
               "NormRope: cos_sin is contiguous float32 [positions, rotary_dim]")
         self.q_weight, self.k_weight, self.cos_sin = q_weight, k_weight, cos_sin
+        dims = {w.numel() for w in (q_weight, k_weight) if w is not None}
+        _need(len(dims) < 2, "NormRope: weights of one length")
+        self.dim = dims.pop() if dims else None
         self.desc = qg_norm_rope(None if q_weight is None else q_weight.data_ptr(),
                                  None if k_weight is None else k_weight.data_ptr(), eps, weight_offset,
                                  None if cos_sin is None else cos_sin.data_ptr(),
@@ -577,12 +595,13 @@ class NormRope:
                                  0 if cos_sin is None else cos_sin.shape[1], 1 if interleaved else 0)
 
 
-def _heads(t, heads, dim, what):
-    """(pointer, token stride, head stride) of bf16 [tokens, heads, dim]."""
-    import torch
+def _heads(t, n, heads, cache, what):
+    """(pointer, token stride, head stride) of bf16 [n, heads, head_dim]; n or heads None: any."""
     s, st = t.shape, t.stride()
-    if t.dtype != torch.bfloat16 or len(s) != 3 or s[2] != dim or (heads and s[1] != heads) or st[2] != 1:
-        raise QGError(1, f"{what}: bfloat16 [tokens, {heads or 'heads'}, {dim}] with a contiguous last dimension")
+    if (t.dtype is not cache.bf16 or len(s) != 3 or s[2] != cache.head_dim or st[2] != 1
+            or (n is not None and s[0] != n) or (heads is not None and s[1] != heads)):
+        raise QGError(1, f"{what}: bfloat16 [{'tokens' if n is None else n}, {'heads' if heads is None else heads}, "
+                         f"{cache.head_dim}] with a contiguous last dimension")
     return t.data_ptr(), st[0], st[1]
 
 
@@ -590,30 +609,28 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, norm_rope: Optional[NormR
               workspace: Optional[Workspace] = None):
     """Norm and rotate the new tokens' q and k (bf16 [n, heads, head_dim]), write k and v into the cache and
     return the queries (``qkv_append``).  q may be None: only the cache is written."""
-    import torch
-    hkv, d = cache.n_kv_heads, cache.head_dim
+    hkv = cache.n_kv_heads
+    kp, ldk, hsk = _heads(k, None, hkv, cache, "kv_append: k")
     n = k.shape[0]
-    kp, ldk, hsk = _heads(k, hkv, d, "kv_append: k")
-    vp, ldv, hsv = _heads(v, hkv, d, "kv_append: v")
-    _need(v.shape[0] == n, "kv_append: as many rows of k as of v")
+    vp, ldv, hsv = _heads(v, n, hkv, cache, "kv_append: v")
     qp = op = None
     hq = ldq = hsq = ldo = hso = 0
     if q is not None:
-        qp, ldq, hsq = _heads(q, 0, d, "kv_append: q")
+        qp, ldq, hsq = _heads(q, n, None, cache, "kv_append: q")
         hq = q.shape[1]
         if out is None:
-            out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=q.device)
-        op, ldo, hso = _heads(out, hq, d, "kv_append: out")
-        _need(q.shape[0] == n and out.shape[0] == n, "kv_append: as many rows of q and out as of k")
+            out = q.new_empty((n, hq, cache.head_dim))
+        op, ldo, hso = _heads(out, n, hq, cache, "kv_append: out")
     nr = None
     if norm_rope is not None:
         nr = norm_rope.desc
-        for w in (norm_rope.q_weight, norm_rope.k_weight):
-            _need(w is None or w.numel() == d, "kv_append: norm weights of head_dim elements")
+        _need(norm_rope.dim in (None, cache.head_dim), "kv_append: norm weights of head_dim elements")
     if workspace is None:
         workspace = Workspace(qkv_append_workspace_size(), k.device)
-    qkv_append(cache.desc, batch.desc, nr, n, hq, qp, ldq, hsq, kp, ldk, hsk, vp, ldv, hsv, op, ldo, hso, workspace.ptr,
-               workspace.nbytes, _stream_ptr())
+    st = (_lib or lib()).qkv_append(cache.desc, batch.desc, nr, n, hq, qp, ldq, hsq, kp, ldk, hsk, vp, ldv, hsv, op, ldo, hso,
+                                    workspace.ptr, workspace.nbytes, cache.raw_stream(cache.index))
+    if st:
+        raise QGError(st, "qkv_append")
     return out
 
 
@@ -626,16 +643,15 @@ def attention(cache: KVCache, batch: KVBatch, q, scale: Optional[float] = None, 
               workspace: Optional[Workspace] = None):
     """Causal attention of the new tokens q (bf16 [n, heads, head_dim]) over the cache (``qattn``);
     scale is 1/sqrt(head_dim) unless given, window 0 means none."""
-    import torch
-    d = cache.head_dim
-    qp, ldq, hsq = _heads(q, 0, d, "attention: q")
-    n, hq = q.shape[0], q.shape[1]
+    qp, ldq, hsq = _heads(q, None, None, cache, "attention: q")
+    n, hq, d = q.shape
     if out is None:
-        out = torch.empty((n, hq, d), dtype=torch.bfloat16, device=q.device)
-    op, ldo, hso = _heads(out, hq, d, "attention: out")
-    _need(out.shape[0] == n, "attention: as many rows of out as of q")
+        out = q.new_empty((n, hq, d))
+    op, ldo, hso = _heads(out, n, hq, cache, "attention: out")
     if workspace is None:
         workspace = Workspace(attention_workspace_size(cache, batch, n, hq), q.device)
-    qattn(cache.desc, batch.desc, n, hq, qp, ldq, hsq, d ** -0.5 if scale is None else scale, window, op, ldo, hso,
-          workspace.ptr, workspace.nbytes, _stream_ptr())
+    st = (_lib or lib()).qattn(cache.desc, batch.desc, n, hq, qp, ldq, hsq, d ** -0.5 if scale is None else scale, window,
+                               op, ldo, hso, workspace.ptr, workspace.nbytes, cache.raw_stream(cache.index))
+    if st:
+        raise QGError(st, "qattn")
     return out

@@ -64,19 +64,22 @@ struct Cfg {
   static constexpr int KV = kTile * D;               // bytes of a key (or value) tile
   static constexpr int Q = 2 * N * D;                // both terms of the query rows
   static constexpr int QPANEL = 2 * N * PW;
-  static constexpr int QB = GROUPS + 1;              // buffers of them: scores run GROUPS tiles (and pairs) ahead
+  static constexpr int QB = 2;                       // buffers of them
   static constexpr int P = 3 * N * kTile;            // a group's terms of P
   static constexpr int MB = NP;                      // M blocks of O (128 dims; D = 64 fills half of one)
   static constexpr int SCOL = 2 * N, OCOL = 3 * N;   // TMEM columns of a group's S and of a block of its O
-  static constexpr int FIXED = 1024 + QB * Q + GROUPS * P + 8192;
+  static constexpr int OSET = GROUPS * MB * OCOL;    // all groups' O
+  static constexpr int OB = GROUPS * SCOL + 2 * OSET <= 512 ? 2 : 1;  // sets: two pairs can be at work
+  static constexpr int PRODUCERS = D == 256 ? 1 : 2; // warps that copy keys, and values
+  static constexpr int FIXED = 1024 + QB * Q + GROUPS * P + 9216;
   static constexpr int SLOTS = (232448 - FIXED) / KV;
   // key tiles are done with after the scores, value tiles a softmax later
-  // (even numbers: a stage is always filled by the same one of two warps)
-  static constexpr int SK0 = SLOTS * 2 / 5 < 2 ? 2 : SLOTS * 2 / 5, SK = SK0 > 6 ? 6 : SK0 & ~1;
-  static constexpr int SV = SLOTS - SK > 8 ? 8 : (SLOTS - SK) & ~1;
+  // (whole multiples of PRODUCERS: a stage is always filled by the same warp)
+  static constexpr int SK0 = SLOTS * 2 / 5 < 2 ? 2 : SLOTS * 2 / 5, SK = (SK0 > 6 ? 6 : SK0) / PRODUCERS * PRODUCERS;
+  static constexpr int SV = (SLOTS - SK > 8 ? 8 : SLOTS - SK) / PRODUCERS * PRODUCERS;
   static constexpr int METAS = 32;                   // tiles between a key tile's issue and its outputs: fewer
   static constexpr int SMEM = FIXED + (SK + SV) * KV;
-  static_assert(SK >= 2 && SV >= 2 && GROUPS * (SCOL + MB * OCOL) <= 512, "shared and tensor memory");
+  static_assert(SK >= 2 && SV >= 2 && GROUPS * SCOL + OB * OSET <= 512, "shared and tensor memory");
   static_assert(SK + 3 * GROUPS < METAS && SV + GROUPS < METAS, "tiles on their way");
 };
 
@@ -87,7 +90,7 @@ struct TileMeta {
   float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
 };
 struct ValueMeta {
-  int after, rows, groups, pad;  // as above; rows before the sequence's end; bits of the groups that hold keys
+  int after, rows, groups, set;  // as above; rows before the sequence's end; bits of the groups that hold keys; its O
 };
 // What a query buffer holds besides the rows.
 template <int N>
@@ -105,13 +108,13 @@ struct Shared {
   TileMeta tile[C::METAS];
   ValueMeta value[C::METAS];
   PairMeta<N> pair[C::QB];
-  alignas(16) float ref[C::GROUPS][N];
-  alignas(16) float grow[C::GROUPS][N];
-  float sum[C::GROUPS][N], red[C::GROUPS][4][N];
+  alignas(16) float ref[C::OB][C::GROUPS][N];
+  alignas(16) float factor[C::GROUPS][N];  // of a group's O at the join
+  float sum[C::OB][C::GROUPS][N], grow[C::GROUPS][N], red[C::GROUPS][4][N], inv[N];
   uint64_t kfull[C::SK], kfree[C::SK], vfull[C::SV], vfree[C::SV];
   uint64_t qfull[C::QB], qfree[C::QB];
   uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
-  uint64_t summed, joined, ended[2];
+  uint64_t summed[C::OB], joined[C::OB], ended[2];
   uint32_t tmem;
   int ticket[C::GROUPS];
 };
@@ -151,17 +154,27 @@ struct Walk {
   Seq sq, mine;
 
   // tiles of all sequences, each counted once (all its KV heads have as many)
-  __device__ __forceinline__ int count(const AttnArgs& a, int lane, bool* bad) {
+  __device__ __forceinline__ int count(const AttnArgs& a, int lane, bool* bad, int* most) {
     const KvArgs& c = a.c;
     mine = {0, 0, 0};
     if (lane < c.n_seqs) mine = seq_of(c, lane, bad);
-    int total = __reduce_add_sync(0xFFFFFFFFu, tiles_of(mine, a));
+    const int first = tiles_of(mine, a);
+    int total = __reduce_add_sync(0xFFFFFFFFu, first);
+    *most = __reduce_max_sync(0xFFFFFFFFu, first);  // of the first 32 sequences
     for (int base = 32; base < c.n_seqs; base += 32) {
       int t = 0;
       if (base + lane < c.n_seqs) t = tiles_of(seq_of(c, base + lane, bad), a);
       total += __reduce_add_sync(0xFFFFFFFFu, t);
     }
     return total;
+  }
+  // pair number `pair` of at most 32 sequences: its tiles [u0, u1)
+  __device__ __forceinline__ void pair_of(const AttnArgs& a, int pair, int lane, int* u0, int* u1) const {
+    const int tiles = tiles_of(mine, a), which = pair / a.c.hkv, head = pair - which * a.c.hkv;
+    const int before = __reduce_add_sync(0xFFFFFFFFu, lane < which ? tiles : 0);
+    const int n = which < 32 ? __shfl_sync(0xFFFFFFFFu, tiles, which & 31) : 0;
+    *u0 = before * a.c.hkv + head * n;
+    *u1 = *u0 + n;
   }
   __device__ __forceinline__ void take(const Seq& t, int who) {
     sq.start = __shfl_sync(0xFFFFFFFFu, t.start, who);
@@ -302,8 +315,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     attn_decode_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const DecodeArgs da) {
   using C = Cfg<D, N>;
-  constexpr int NG = C::GROUPS, kMma = 4 * NG;
-  static_assert(sizeof(Shared<D, N>) <= 8192, "shared memory");
+  constexpr int NG = C::GROUPS, NPR = C::PRODUCERS, kMma = 4 * NG;
+  static_assert(sizeof(Shared<D, N>) <= 9216 && C::SK <= 8 && C::SV <= 8, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* vring = ring + C::SK * C::KV;
@@ -315,30 +328,20 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.hq / c.hkv;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::SK; ++s) {
-      mbar_init(&sh.kfull[s], 16);
-      mbar_init(&sh.kfree[s], 1);
+  {  // a thread an entry
+    const int t = threadIdx.x;
+    if (t < C::SK) mbar_init(&sh.kfull[t], 16), mbar_init(&sh.kfree[t], 1);
+    if (t < C::SV) mbar_init(&sh.vfull[t], 8), mbar_init(&sh.vfree[t], 1);
+    if (t < C::QB) mbar_init(&sh.qfull[t], 64), mbar_init(&sh.qfree[t], 1);
+    if (t < NG) {
+      mbar_init(&sh.sfull[t], 2);  // the MMAs' end, and the issuing thread's own arrival
+      mbar_init(&sh.sfree[t], 128);
+      mbar_init(&sh.pfull[t], 128);
+      mbar_init(&sh.pvdone[t], 1);
     }
-    for (int s = 0; s < C::SV; ++s) {
-      mbar_init(&sh.vfull[s], 8);
-      mbar_init(&sh.vfree[s], 1);
-    }
-    for (int i = 0; i < C::QB; ++i) {
-      mbar_init(&sh.qfull[i], 64);
-      mbar_init(&sh.qfree[i], 1);
-    }
-    for (int i = 0; i < NG; ++i) {
-      mbar_init(&sh.sfull[i], 2);  // the MMAs' end, and the issuing thread's own arrival
-      mbar_init(&sh.sfree[i], 128);
-      mbar_init(&sh.pfull[i], 128);
-      mbar_init(&sh.pvdone[i], 1);
-    }
-    mbar_init(&sh.summed, NG);
-    mbar_init(&sh.joined, 1);
-    mbar_init(&sh.ended[0], 1);
-    mbar_init(&sh.ended[1], 1);
-    fence_mbar_init();
+    if (t < C::OB) mbar_init(&sh.summed[t], NG), mbar_init(&sh.joined[t], 1);
+    if (t < 2) mbar_init(&sh.ended[t], 1);
+    if (t < 8) fence_mbar_init();
   }
   if (warp == kMma) {
     tmem_alloc(&sh.tmem, 512);
@@ -347,12 +350,17 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   pdl_wait();
   Walk w;
   bool bad = false;
-  const int total = w.count(a, lane, &bad) * c.hkv;
+  int most = 0;
+  const int total = w.count(a, lane, &bad, &most) * c.hkv;
   if (bad && warp == 0 && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
   // with no more CTAs than tiles, each has one at least
   const int grid = min((int)gridDim.x, total), cta = blockIdx.x;
   const Share share = {total / max(grid, 1), total % max(grid, 1)};
-  const int u0 = cta < grid ? share.begin(cta) : 0, u1 = cta < grid ? share.begin(cta + 1) : 0;
+  int u0 = cta < grid ? share.begin(cta) : 0, u1 = cta < grid ? share.begin(cta + 1) : 0;
+  // A few short pairs: a CTA a pair.  Its groups take most tiles at once, and a join between CTAs costs more
+  // than a second round (one sequence of 777 keys, 8 KV heads of 128: 11.5 us so, 15.4 cut into 56 CTAs).
+  if (most <= 2 * NG && c.n_seqs <= 32 && c.n_seqs * c.hkv <= (int)gridDim.x) w.pair_of(a, cta, lane, &u0, &u1);
+  if (warp > kMma) w.find(a, u0, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -362,24 +370,23 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 
   if (n > 0 && warp >= kMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
-    if (warp != kMma && warp != kMma + 7) w.find(a, u0, lane);
-  if (warp > kMma && warp < kMma + 5) {  // -------------------------------------- key tiles, value tiles
-    // Two warps for the keys, two for the values, each with every other tile: a tile's copies take
-    // one warp some 600 to 1100 cycles to issue.  Lanes 8q .. 8q + 7 look after tile 8j + 2q + odd: its eight
+  if (warp > kMma && warp <= kMma + 2 * NPR) {  // -------------------------------- key tiles, value tiles
+    // NPR warps for the keys, as many for the values, each with every NPR-th tile: a tile's copies take
+    // one warp some 600 to 1100 cycles to issue.  Lanes 8q .. 8q + 7 look after one of four tiles: its eight
     // groups of 16 keys.  Four tiles' page ids are fetched by one load, while the four before them are issued.
-    const bool keys = warp < kMma + 3;
-    const int odd = (warp - kMma - 1) & 1;
+    const bool keys = warp <= kMma + NPR;
+    const int odd = NPR == 2 ? (warp - kMma - 1) & 1 : 0;
     const int stages = keys ? C::SK : C::SV;
     uint8_t* slots = keys ? ring : vring;
     uint64_t* full = keys ? sh.kfull : sh.vfull;
     uint64_t* free_ = keys ? sh.kfree : sh.vfree;
     const CUtensorMap* map = keys ? &kmap : &vmap;
     const int P = 1 << c.page_log2, box = min(P, kTile);
-    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, edge = 0, walked = 0, i0 = 0, ready = 0;
+    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, edge = 0, walked = 0, i0 = 0, ready = 0, set = 0, pairs = 0;
     bool dead = false;
     int s = odd, i = odd, lap = 0;
     while (i < n && !dead) {
-      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge, cready = ready;
+      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge, cready = ready, cset = set;
       // the next four tiles (the first time, the first four)
       int b = w.b;
       // the rows stand at len - rows .. len - 1
@@ -387,32 +394,36 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + k * kTile;
         edge = tok0 + kTile - 1 > len - w.sq.rows || tok0 <= len - 1 - a.window;
       };
-      if (w.k + 8 <= w.n && walked + 8 <= n) {  // all of one pair
-        const int q = 2 * (lane >> 3) + odd;
+      if (w.k + 4 * NPR <= w.n && walked + 4 * NPR <= n) {  // all of one pair
+        const int q = NPR * (lane >> 3) + odd;
         describe(w.k + q);
         after = walked + q - i0;
+        set = pairs % C::OB;
         ready = 4;
-        walked += 8;
-        w.k += 8;
+        walked += 4 * NPR;
+        w.k += 4 * NPR;
         if (w.k == w.n && walked < n) {
           w.next_pair(a);
           i0 = walked;
+          ++pairs;
         }
       } else {
         len = 0;
         ready = 0;
 #pragma unroll 1
-        for (int q = 0; q < 8 && walked < n; ++q) {
-          if ((q & 1) == odd) {
-            if (lane >> 3 == q >> 1) {
+        for (int q = 0; q < 4 * NPR && walked < n; ++q) {
+          if (q % NPR == odd) {
+            if (lane >> 3 == q / NPR) {
               describe(w.k);
               after = walked - i0;
+              set = pairs % C::OB;
             }
             ++ready;
           }
           if (++walked < n && ++w.k == w.n) {
             w.next_pair(a);
             i0 = walked;
+            ++pairs;
           }
         }
       }
@@ -420,7 +431,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       const int64_t next = (int64_t)tok0 + 16 * (lane & 7);
       if (next < len) id = c.pages[(int64_t)b * c.page_stride + (next >> c.page_log2)];
 #pragma unroll 1
-      for (int q = 0; q < cready; ++q, i += 2) {
+      for (int q = 0; q < cready; ++q, i += NPR) {
         if (lap && !wait(&free_[s], (lap - 1) & 1, c.status)) dead = true;
         if (__any_sync(0xFFFFFFFFu, dead)) {
           dead = true;
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             const uint32_t groups = __ballot_sync(0xFFu << (8 * q), ok) >> (8 * q);
             if (gl == 0) {
               ValueMeta& vm = sh.value[i % C::METAS];
-              vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu);
+              vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu), vm.set = cset;
             }
           }
           if (ok && (16 * gl) % box == 0) {
@@ -464,13 +475,13 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           }
         }
         __syncwarp();
-        s += 2;
+        s += NPR;
         if (s >= stages) s -= stages, ++lap;
       }
     }
     // no copy is left in flight into this CTA's shared memory when it ends: the last stages filled
 #pragma unroll 1
-    for (int j = max(odd, i - stages); j < i; j += 2)
+    for (int j = max(odd, i - stages); j < i; j += NPR)
       wait(&full[j % stages], (uint32_t)(j / stages) & 1u, c.status);
   } else if (warp == kMma + 5 || warp == kMma + 6) {  // -------------------------- query rows
     // Two warps; D / 16 lanes a row, 16 elements each; the loads of four rows a lane group are issued together.
@@ -622,7 +633,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       tc_fence_after();
       const uint32_t acc = m.after >= NG;  // not the group's first tile of the pair
       if (!dead && elect()) {
-        const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + g * (C::MB * C::OCOL);
+        const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + m.set * C::OSET + g * (C::MB * C::OCOL);
 #pragma unroll
         for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
@@ -645,8 +656,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::RSOFT));
     const int grp = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-    const uint32_t st = tmem + lane_base + grp * C::SCOL, ot = otm + lane_base + grp * (C::MB * C::OCOL);
-    float* ref = sh.ref[grp];
+    const uint32_t st = tmem + lane_base + grp * C::SCOL;
     float* grow = sh.grow[grp];
     uint8_t* pd = pbuf + grp * C::P + tid * 16;
     bool dead = false;
@@ -656,7 +666,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       const PairMeta<N>& pm = sh.pair[p % C::QB];
       if (!wait(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) dead = true;
       if (any_of(grp, dead)) break;
-      const int R = pm.R, i0 = pm.i0;
+      const int R = pm.R, i0 = pm.i0, set = p % C::OB;
+      float* ref = sh.ref[set][grp];
+      const uint32_t ot = otm + lane_base + set * C::OSET + grp * (C::MB * C::OCOL);
       i1 = pm.i1;
       float l[N];
 #pragma unroll
@@ -685,8 +697,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         const float ks = tm.ks[tid >> 4], vs = tm.vs[tid >> 4];
         const float lvs = lg2(vs), ivs = ks == 0.0f ? 0.0f : rcp(vs);
         const int flags = tm.flags, tok = tm.tok0 + tid, most = tm.len;
-        // the group's references are free once the pair before has been joined
-        if (first && p > 0 && !wait(&sh.joined, (uint32_t)(p - 1) & 1u, c.status)) dead = true;
+        // the group's references and outputs are free once the pair that had them before has been joined
+        if (first && p >= C::OB && !wait(&sh.joined[set], (uint32_t)(p / C::OB - 1) & 1u, c.status)) dead = true;
         bool over = first;
 #pragma unroll
         for (int r = 0; r < N; r += 4) {
@@ -816,20 +828,20 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           float v = lp[r * 64 + lane] + lp[r * 64 + 32 + lane];
 #pragma unroll
           for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-          if (lane == 0) sh.sum[grp][r] = v;
+          if (lane == 0) sh.sum[set][grp][r] = v;
         }
         any_of(grp, false);
       }
-      // A group without a tile of this pair waits for the join before it all the same: nobody is two pairs
+      // A group without a tile of this pair waits for that join all the same: nobody is OB pairs
       // ahead of a join, so no phase of the two barriers below is missed or arrived at twice.
       if (!took) {
-        if (p > 0 && !wait(&sh.joined, (uint32_t)(p - 1) & 1u, c.status)) dead = true;
+        if (p >= C::OB && !wait(&sh.joined[set], (uint32_t)(p / C::OB - 1) & 1u, c.status)) dead = true;
         if (any_of(grp, dead)) break;
       }
       const bool join = (i1 - 1) % NG == grp;
-      if (tid == 0) mbar_arrive(&sh.summed);
+      if (tid == 0) mbar_arrive(&sh.summed[set]);
       if (join) {
-        if (!wait(&sh.summed, (uint32_t)p & 1u, c.status)) dead = true;
+        if (!wait(&sh.summed[set], (uint32_t)(p / C::OB) & 1u, c.status)) dead = true;
         if (any_of(grp, dead)) break;
         tc_fence_after();
         const int first_tile = pm.first;
@@ -843,17 +855,17 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 #pragma unroll
           for (int gq = 0; gq < NG; ++gq) {
             const int q = gq - i0 % NG;
-            m[gq] = (q < 0 ? q + NG : q) < parts_here ? sh.ref[gq][tid] : -INFINITY;
+            m[gq] = (q < 0 ? q + NG : q) < parts_here ? sh.ref[set][gq][tid] : -INFINITY;
             top = fmaxf(top, m[gq]);
           }
 #pragma unroll
           for (int gq = 0; gq < NG; ++gq) {
             const float f = m[gq] == -INFINITY ? 0.0f : ex2(m[gq] - top);
-            if (f != 0.0f) sum = fmaf(sh.sum[gq][tid], f, sum);
-            sh.grow[gq][tid] = f;
+            if (f != 0.0f) sum = fmaf(sh.sum[set][gq][tid], f, sum);
+            sh.factor[gq][tid] = f;
           }
           if (whole)
-            sh.red[grp][0][tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
+            sh.inv[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
           else
             da.part_ml[slot * N + tid] = make_float2(top, sum);
         }
@@ -865,12 +877,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 #pragma unroll
           for (int gq = 0; gq < NG; ++gq)
 #pragma unroll
-            for (int t = 0; t < 3; ++t) tmem_ld4(otm + lane_base + (gq * C::MB + mb) * C::OCOL + t * N + r, v[gq][t]);
+            for (int t = 0; t < 3; ++t) tmem_ld4(otm + lane_base + set * C::OSET + (gq * C::MB + mb) * C::OCOL + t * N + r, v[gq][t]);
           tmem_ld_wait();
           float o[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int gq = 0; gq < NG; ++gq) {
-            const float4 f4 = *reinterpret_cast<const float4*>(&sh.grow[gq][r]);
+            const float4 f4 = *reinterpret_cast<const float4*>(&sh.factor[gq][r]);
             const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
@@ -884,7 +896,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             for (int z = 0; z < 4; ++z) {
               if (r + z < R) {
                 if (whole) {
-                  const __nv_bfloat16 y = __float2bfloat16_rn(o[z] * sh.red[grp][0][r + z]);
+                  const __nv_bfloat16 y = __float2bfloat16_rn(o[z] * sh.inv[r + z]);
                   a.out[base + pm.off[r + z] + d] = *reinterpret_cast<const uint16_t*>(&y);
                 } else {
                   da.part_o[((int64_t)slot * N + r + z) * D + d] = o[z];
@@ -898,7 +910,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         // the other groups may go on with the next pair, and the query buffer is free
         if (tid == 0) {
           mbar_arrive(&sh.qfree[p % C::QB]);
-          mbar_arrive(&sh.joined);
+          mbar_arrive(&sh.joined[set]);
         }
         if (!whole) {
           // the CTA whose ticket completes the pair joins the parts, in their order on the line
