@@ -45,6 +45,7 @@ namespace qg {
 namespace {
 
 constexpr int kTile = 128;           // keys a tile
+constexpr int kMostCtas = 256;
 constexpr float kBias = 2.0f;        // P of a key at the reference is 2^2 ...
 constexpr float kHead = 6.5f;        // ... and at most 2^8.5, below E4M3's 448
 
@@ -86,17 +87,18 @@ struct Cfg {
 // What a stage holds.
 struct TileMeta {
   int tok0, len, after;  // after: tiles of its pair in this CTA before it
-  int flags;             // 1: some of its rows hold no key; 2: some row of the pair does not see all of it
+  int flags;             // 1: some of its rows hold no key; 2: some row of the pair does not see all of it; 4: the CTA's last
   float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
 };
 struct ValueMeta {
-  int after, rows, groups, set;  // as above; rows before the sequence's end; bits of the groups that hold keys; its O
+  int after, rows, groups, set;  // as above; rows before the sequence's end; bits of the groups that hold keys; its O, 4: last
 };
 // What a query buffer holds besides the rows.
 template <int N>
 struct PairMeta {
   int R, n_tiles, i0, i1;       // rows, tiles, and which of this CTA's tiles they are
-  int first, pad;               // its first tile on the line
+  int first, skipped;           // its first tile's place on the line, and how many tiles of it earlier CTAs have
+  int last, pad;                // the CTA's last pair
   int64_t base;                 // its first row's output
   alignas(16) float rc[N];      // the row's power of two * scale * log2(e)
   int pos[N];
@@ -116,7 +118,9 @@ struct Shared {
   uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
   uint64_t summed[C::OB], joined[C::OB], ended[2];
   uint32_t tmem;
-  int ticket[C::GROUPS];
+  int joins;      // pairs whose parts this CTA has to join in the end, at most two
+  int join[2][4];  // rows, first CTA, parts, whether the first part is its CTA's first pair
+  int64_t join_base[2];
 };
 
 struct DecodeArgs {
@@ -147,32 +151,40 @@ struct Share {
   }
 };
 
+// A pair takes as long as its tiles and some two more (its rows, its end): the line counts a pair's tiles and
+// kPairCost places behind them, which no tile stands at.
+constexpr int kPairCost = 2;
+__device__ __forceinline__ int places_of(const Seq& s, const AttnArgs& a) {
+  const int n = tiles_of(s, a);
+  return n ? n + kPairCost : 0;
+}
+
 // A place on the line: tile k of head h of sequence b, whose pairs have n tiles.  A whole warp walks; lane
 // b holds sequence b of the first 32.
 struct Walk {
   int b, h, k, n, lo;
   Seq sq, mine;
 
-  // tiles of all sequences, each counted once (all its KV heads have as many)
+  // places of all sequences, each counted once (all its KV heads have as many); most: of one pair
   __device__ __forceinline__ int count(const AttnArgs& a, int lane, bool* bad, int* most) {
     const KvArgs& c = a.c;
     mine = {0, 0, 0};
     if (lane < c.n_seqs) mine = seq_of(c, lane, bad);
-    const int first = tiles_of(mine, a);
+    const int first = places_of(mine, a);
     int total = __reduce_add_sync(0xFFFFFFFFu, first);
     *most = __reduce_max_sync(0xFFFFFFFFu, first);  // of the first 32 sequences
     for (int base = 32; base < c.n_seqs; base += 32) {
       int t = 0;
-      if (base + lane < c.n_seqs) t = tiles_of(seq_of(c, base + lane, bad), a);
+      if (base + lane < c.n_seqs) t = places_of(seq_of(c, base + lane, bad), a);
       total += __reduce_add_sync(0xFFFFFFFFu, t);
     }
     return total;
   }
-  // pair number `pair` of at most 32 sequences: its tiles [u0, u1)
+  // pair number `pair` of at most 32 sequences: its places [u0, u1)
   __device__ __forceinline__ void pair_of(const AttnArgs& a, int pair, int lane, int* u0, int* u1) const {
-    const int tiles = tiles_of(mine, a), which = pair / a.c.hkv, head = pair - which * a.c.hkv;
-    const int before = __reduce_add_sync(0xFFFFFFFFu, lane < which ? tiles : 0);
-    const int n = which < 32 ? __shfl_sync(0xFFFFFFFFu, tiles, which & 31) : 0;
+    const int here = places_of(mine, a), which = pair / a.c.hkv, head = pair - which * a.c.hkv;
+    const int before = __reduce_add_sync(0xFFFFFFFFu, lane < which ? here : 0);
+    const int n = which < 32 ? __shfl_sync(0xFFFFFFFFu, here, which & 31) : 0;
     *u0 = before * a.c.hkv + head * n;
     *u1 = *u0 + n;
   }
@@ -181,9 +193,27 @@ struct Walk {
     sq.rows = __shfl_sync(0xFFFFFFFFu, t.rows, who);
     sq.len = __shfl_sync(0xFFFFFFFFu, t.len, who);
   }
-  __device__ __forceinline__ void find(const AttnArgs& a, int unit, int lane) {
+  // the next pair; there is one
+  __device__ __forceinline__ void next_pair(const AttnArgs& a) {
+    k = 0;
+    if (++h == a.c.hkv) {
+      bool ignore = false;
+      h = 0;
+      do {
+        ++b;
+        if (b < 32)
+          take(mine, b);
+        else
+          sq = seq_of(a.c, b, &ignore);
+        n = tiles_of(sq, a);
+      } while (n == 0);
+      lo = first_key(sq, a);
+    }
+  }
+  // To a CTA's first tile: the first at or behind place u0; returns its place, or u1 where there is none before u1.
+  __device__ __forceinline__ int find(const AttnArgs& a, int u0, int u1, int lane) {
     const KvArgs& c = a.c;
-    int left = unit;
+    int left = u0;
     bool ignore = false;
     b = 0, n = 1;
     sq = {0, 0, 0};
@@ -193,7 +223,7 @@ struct Walk {
         t = {0, 0, 0};
         if (base + lane < c.n_seqs) t = seq_of(c, base + lane, &ignore);
       }
-      const int un = tiles_of(t, a);
+      const int un = places_of(t, a);
       int sum = un * c.hkv;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -213,99 +243,92 @@ struct Walk {
     }
     h = left / n;
     k = left - h * n;
+    n -= kPairCost;
     lo = first_key(sq, a);
-  }
-  // the next pair; there is one
-  __device__ __forceinline__ void next_pair(const AttnArgs& a) {
-    k = 0;
-    if (++h == a.c.hkv) {
-      bool ignore = false;
-      h = 0;
-      do {
-        ++b;
-        if (b < 32)
-          take(mine, b);
-        else
-          sq = seq_of(a.c, b, &ignore);
-        n = tiles_of(sq, a);
-      } while (n == 0);
-      lo = first_key(sq, a);
+    if (u0 >= u1) return u1;
+    if (k >= n) {  // behind a pair's tiles: on to the next one's
+      u0 += n + kPairCost - k;
+      if (u0 >= u1) return u1;
+      next_pair(a);
     }
+    return u0;
   }
 };
 
-// The joining of a pair's parts by the CTA that finished last: one group's 128 threads.  weights: shared
-// memory for N floats a part, 32 parts at a time.
+// The joining of a pair's parts, in their order on the line, by the CTA that finished last: its softmax
+// threads (the others have given up their registers), with its rings as scratch.  Latency is all of it (a load takes some 1900 cycles, other SMs having just written
+// the parts), so loads go out many at a time.
 template <int D, int N>
-__device__ __noinline__ void join_parts(const DecodeArgs& da, int grp, int tid, int R, int G, int64_t base, int c0, int parts,
-                                        bool at_start, void* scratch) {
+__device__ __noinline__ void join_parts(const DecodeArgs& da, int R, int G, int64_t base, int c0, int parts, bool at_start,
+                                        uint8_t* scratch) {
+  using C = Cfg<D, N>;
   const AttnArgs& a = da.a;
-  constexpr int V = D / 4, E = (N * V + 127) / 128;  // float4s a row, and a thread
+  constexpr int T = 128 * C::GROUPS, W = T / 32, V = D / 4;  // float4s a row
+  static_assert((C::SK + C::SV) * C::KV >= T * 16 + kMostCtas * N * 4, "scratch");
   auto slot = [&](int q) { return (int64_t)(2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0)); };
-  float* wt = static_cast<float*>(scratch);  // [32][N] weights, then [N] 1 / sum
-  float* inv = wt + 32 * N;
-  // references and sums: a warp a row, a lane a part
-  for (int row = tid >> 5; row < R; row += 4) {
-    const int lane = tid & 31;
-    float top = -INFINITY, sum = 0.0f;
-    for (int q = lane; q < parts; q += 32) top = fmaxf(top, __ldcg(&da.part_ml[slot(q) * N + row]).x);
-    top = warp_max(top);
+  float4* sums = reinterpret_cast<float4*>(scratch);    // [T]
+  float* wt = reinterpret_cast<float*>(scratch) + T * 4;  // [parts][N]: weights over the sum
+  const int tid = threadIdx.x, lane = tid & 31;
+  named_sync(15, T);
+  for (int row = tid >> 5; row < R; row += W) {  // a warp a row, a lane a part
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 2
     for (int q = lane; q < parts; q += 32) {
       const float2 z = __ldcg(&da.part_ml[slot(q) * N + row]);
-      sum = fmaf(z.y, z.x == -INFINITY ? 0.0f : ex2(z.x - top), sum);
+      const float t = fmaxf(m, z.x);
+      if (t != -INFINITY) l = fmaf(l, ex2(m - t), z.y * ex2(z.x - t));
+      m = t;
+      wt[q * N + row] = z.x;
     }
+    const float top = warp_max(m);
+    float sum = m == -INFINITY ? 0.0f : l * ex2(m - top);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) {
-      inv[row] = sum == 0.0f ? 0.0f : 1.0f / sum;
-      inv[N + row] = top;
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int q = lane; q < parts; q += 32) {
+      const float z = wt[q * N + row];
+      wt[q * N + row] = z == -INFINITY ? 0.0f : ex2(z - top) * inv;
     }
   }
-  any_of(grp, false);
+  named_sync(15, T);
+  // where there are fewer float4s than threads, several threads share one's parts
+  const int E = R * V, share = max(T / E, 1);
 #pragma unroll 1
-  for (int e0 = 0; e0 < E; e0 += 4) {
-    float4 v[4];
+  for (int e0 = 0; e0 < E; e0 += T) {
+    const int e = share > 1 ? tid % E : e0 + tid, sub = share > 1 ? tid / E : 0;
+    const bool in = e < E && sub < share;
+    float4 v = make_float4(0, 0, 0, 0);
+    if (in) {
+      const float* w = wt + e / V;
+#pragma unroll 1
+      for (int q = sub; q < parts; q += 8 * share) {
+        float4 y[8];
 #pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] = make_float4(0, 0, 0, 0);
-    for (int q0 = 0; q0 < parts; q0 += 32) {
-      const int m = min(32, parts - q0);
-      for (int t = tid; t < m * N; t += 128) {
-        const int q = t / N, row = t % N;
-        float f = 0.0f;
-        if (row < R) {
-          const float z = __ldcg(&da.part_ml[slot(q0 + q) * N + row]).x;
-          f = z == -INFINITY ? 0.0f : ex2(z - inv[N + row]);
-        }
-        wt[t] = f;
-      }
-      any_of(grp, false);
-#pragma unroll 4
-      for (int q = 0; q < m; ++q) {
-        const float4* src = reinterpret_cast<const float4*>(da.part_o + slot(q0 + q) * N * D);
+        for (int k = 0; k < 8; ++k)  // past the last part: the last one again, with weight 0
+          y[k] = __ldcg(reinterpret_cast<const float4*>(da.part_o + slot(min(q + k * share, parts - 1)) * N * D) + e);
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int e = (e0 + x) * 128 + tid;
-          if (e < R * V) {
-            const float4 y = __ldcg(src + e);
-            const float f = wt[q * N + e / V];
-            v[x].x = fmaf(y.x, f, v[x].x), v[x].y = fmaf(y.y, f, v[x].y);
-            v[x].z = fmaf(y.z, f, v[x].z), v[x].w = fmaf(y.w, f, v[x].w);
+        for (int k = 0; k < 8; ++k) {
+          const float f = q + k * share < parts ? w[(q + k * share) * N] : 0.0f;
+          if (f != 0.0f) {  // a part without a key holds anything
+            v.x = fmaf(y[k].x, f, v.x), v.y = fmaf(y[k].y, f, v.y), v.z = fmaf(y[k].z, f, v.z), v.w = fmaf(y[k].w, f, v.w);
           }
         }
       }
-      any_of(grp, false);
     }
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const int e = (e0 + x) * 128 + tid;
-      if (e < R * V) {
-        const int row = e / V, d = (e % V) * 4, t = row / G, g = row - t * G;
-        const float f = inv[row];
-        const __nv_bfloat162 y0 = __floats2bfloat162_rn(v[x].x * f, v[x].y * f);
-        const __nv_bfloat162 y1 = __floats2bfloat162_rn(v[x].z * f, v[x].w * f);
-        *reinterpret_cast<uint2*>(a.out + base + t * a.ldo + g * a.hso + d) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
-      }
+    if (share > 1) {
+      sums[tid] = v;
+      named_sync(15, T);
+      if (tid < E)
+        for (int k = 1; k < share; ++k) {
+          const float4 y = sums[k * E + tid];
+          v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        }
+    }
+    if (in && sub == 0) {
+      const int row = e / V, d = (e % V) * 4, t = row / G, g = row - t * G;
+      const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x, v.y), y1 = __floats2bfloat162_rn(v.z, v.w);
+      *reinterpret_cast<uint2*>(a.out + base + t * a.ldo + g * a.hso + d) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
     }
   }
 }
@@ -351,24 +374,25 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   Walk w;
   bool bad = false;
   int most = 0;
-  const int total = w.count(a, lane, &bad, &most) * c.hkv;
+  const int total = w.count(a, lane, &bad, &most) * c.hkv;  // places
   if (bad && warp == 0 && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
-  // with no more CTAs than tiles, each has one at least
+  // with no more CTAs than places, each has one at least
   const int grid = min((int)gridDim.x, total), cta = blockIdx.x;
   const Share share = {total / max(grid, 1), total % max(grid, 1)};
   int u0 = cta < grid ? share.begin(cta) : 0, u1 = cta < grid ? share.begin(cta + 1) : 0;
   // A few short pairs: a CTA a pair.  Its groups take most tiles at once, and a join between CTAs costs more
   // than a second round (one sequence of 777 keys, 8 KV heads of 128: 11.5 us so, 15.4 cut into 56 CTAs).
-  if (most <= 2 * NG && c.n_seqs <= 32 && c.n_seqs * c.hkv <= (int)gridDim.x) w.pair_of(a, cta, lane, &u0, &u1);
-  if (warp > kMma) w.find(a, u0, lane);
+  if (most <= 2 * NG + kPairCost && c.n_seqs <= 32 && c.n_seqs * c.hkv <= (int)gridDim.x) w.pair_of(a, cta, lane, &u0, &u1);
+  int place = u1;  // of this CTA's first tile
+  if (warp > kMma && warp < kMma + 7) place = w.find(a, u0, u1, lane);
+  if (threadIdx.x == 0) sh.joins = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const int n = u1 - u0;
   const uint32_t otm = tmem + NG * C::SCOL;  // the groups' O follow their S
 
-  if (n > 0 && warp >= kMma) {
+  if (u1 > u0 && warp >= kMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
   if (warp > kMma && warp <= kMma + 2 * NPR) {  // -------------------------------- key tiles, value tiles
     // NPR warps for the keys, as many for the values, each with every NPR-th tile: a tile's copies take
@@ -382,49 +406,55 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     uint64_t* free_ = keys ? sh.kfree : sh.vfree;
     const CUtensorMap* map = keys ? &kmap : &vmap;
     const int P = 1 << c.page_log2, box = min(P, kTile);
-    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, edge = 0, walked = 0, i0 = 0, ready = 0, set = 0, pairs = 0;
-    bool dead = false;
+    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, flags = 0, ready = 0, set = 0, pairs = 0, in_pair = 0;
+    bool dead = false, done = place >= u1;
     int s = odd, i = odd, lap = 0;
-    while (i < n && !dead) {
-      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cedge = edge, cready = ready, cset = set;
+    if (done && keys && odd == 0) {  // no tile for this CTA
+      if (lane == 0) sh.tile[0].after = -1;
+      __syncwarp();
+      if (lane < 16) mbar_arrive(&full[0]);
+    } else if (done && odd == 0) {
+      if (lane == 0) sh.value[0].after = -1;
+      __syncwarp();
+      if (lane < 8) mbar_arrive(&full[0]);
+    }
+    do {
+      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cflags = flags, cready = ready, cset = set;
       // the next four tiles (the first time, the first four)
       int b = w.b;
-      // the rows stand at len - rows .. len - 1
-      auto describe = [&](int k) {
-        b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + k * kTile;
-        edge = tok0 + kTile - 1 > len - w.sq.rows || tok0 <= len - 1 - a.window;
+      len = 0;
+      ready = 0;
+      auto describe = [&](int q) {  // tile q places on, in the pair at hand
+        const int k = w.k + q, at = place + q + 1;
+        b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + k * kTile, after = in_pair + q, set = pairs % C::OB;
+        // the rows stand at len - rows .. len - 1
+        flags = tok0 + kTile - 1 > len - w.sq.rows || tok0 <= len - 1 - a.window ? 2 : 0;
+        if (at >= u1 || (k == w.n - 1 && at + kPairCost >= u1)) flags |= 4;
       };
-      if (w.k + 4 * NPR <= w.n && walked + 4 * NPR <= n) {  // all of one pair
-        const int q = NPR * (lane >> 3) + odd;
-        describe(w.k + q);
-        after = walked + q - i0;
-        set = pairs % C::OB;
-        ready = 4;
-        walked += 4 * NPR;
-        w.k += 4 * NPR;
-        if (w.k == w.n && walked < n) {
-          w.next_pair(a);
-          i0 = walked;
+      auto walk = [&](int q) {
+        place += q;
+        in_pair += q;
+        w.k += q;
+        if (w.k == w.n) {
+          place += kPairCost;
+          in_pair = 0;
           ++pairs;
+          if (place < u1) w.next_pair(a);
         }
+        done = place >= u1;
+      };
+      if (!done && w.k + 4 * NPR <= w.n && place + 4 * NPR <= u1) {  // all of one pair
+        describe(NPR * (lane >> 3) + odd);
+        ready = 4;
+        walk(4 * NPR);
       } else {
-        len = 0;
-        ready = 0;
 #pragma unroll 1
-        for (int q = 0; q < 4 * NPR && walked < n; ++q) {
+        for (int q = 0; q < 4 * NPR && !done; ++q) {
           if (q % NPR == odd) {
-            if (lane >> 3 == q / NPR) {
-              describe(w.k);
-              after = walked - i0;
-              set = pairs % C::OB;
-            }
+            if (lane >> 3 == q / NPR) describe(0);
             ++ready;
           }
-          if (++walked < n && ++w.k == w.n) {
-            w.next_pair(a);
-            i0 = walked;
-            ++pairs;
-          }
+          walk(1);
         }
       }
       id = -1;
@@ -448,13 +478,13 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           TileMeta& m = sh.tile[i % C::METAS];
           if (keys) {  // written before this lane's arrival, which hands it over
             const bool cut = __any_sync(0xFFu << (8 * q), !ok || tok + 16 > clen);
-            if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = (cut ? 3 : 0) | (cedge ? 2 : 0);
+            if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = cflags | (cut ? 3 : 0);
             if (!ok) m.ks[gl] = m.vs[gl] = 0.0f;
           } else {
             const uint32_t groups = __ballot_sync(0xFFu << (8 * q), ok) >> (8 * q);
             if (gl == 0) {
               ValueMeta& vm = sh.value[i % C::METAS];
-              vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu), vm.set = cset;
+              vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu), vm.set = cset | (cflags & 4);
             }
           }
           if (ok && (16 * gl) % box == 0) {
@@ -478,7 +508,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         s += NPR;
         if (s >= stages) s -= stages, ++lap;
       }
-    }
+    } while (!dead && (ready || !done));
     // no copy is left in flight into this CTA's shared memory when it ends: the last stages filled
 #pragma unroll 1
     for (int j = max(odd, i - stages); j < i; j += NPR)
@@ -488,12 +518,16 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     // Rows past R stay as they are: their columns of S are not looked at.
     constexpr int TPR = D / 16, RPP = 32 / TPR;
     const int part = lane % TPR, mine = (warp - kMma - 5) * RPP + lane / TPR;
-    int u = u0;
     bool dead = false;
-    for (int p = 0; u < u1; ++p) {
+    if (place >= u1) {  // no pair for this CTA
+      if (lane == 0) sh.pair[0].i1 = 0;
+      __syncwarp();
+      mbar_arrive(&sh.qfull[0]);
+    }
+    for (int p = 0, i0 = 0; place < u1; ++p) {
       const int qb = p % C::QB;
       const int R = min(w.sq.rows * G, N), first_pos = w.sq.len - w.sq.rows;
-      const int next = u + w.n - w.k;
+      const int i1 = i0 + min(w.n - w.k, u1 - place), next = place + w.n - w.k + kPairCost;
       const int64_t qbase = (int64_t)w.sq.start * a.ldq + (int64_t)w.h * G * a.hsq + 16 * part;
       PairMeta<N>& m = sh.pair[qb];
       uint8_t* qd = qbuf + qb * C::Q;
@@ -549,14 +583,15 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       if (!waited && !wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
       if (__any_sync(0xFFFFFFFFu, dead)) break;
       if (warp == kMma + 5 && lane == 0) {
-        m.R = R, m.n_tiles = w.n, m.first = u - w.k;
-        m.i0 = u - u0, m.i1 = min(next, u1) - u0;
+        m.R = R, m.n_tiles = w.n, m.first = place - w.k, m.skipped = w.k;
+        m.i0 = i0, m.i1 = i1, m.last = next >= u1;
         m.base = (int64_t)w.sq.start * a.ldo + (int64_t)w.h * G * a.hso;
       }
       fence_proxy_async_smem();
       mbar_arrive(&sh.qfull[qb]);
-      u = next;
-      if (u < u1) w.next_pair(a);
+      place = next;
+      i0 = i1;
+      if (place < u1) w.next_pair(a);
     }
   } else if (warp == kMma) {  // ---------------------------------------------------- score MMAs
     // One thread issues them, and its instructions set the pace: descriptors are one add each, and the output
@@ -565,11 +600,14 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     int ks = 0, g = 0, qb = -1;
     uint32_t kpar = 0, spar = 1, qpar = 1;
     const uint32_t k0 = desc_lo(smem_u32(ring), 16), q0 = desc_lo(smem_u32(qbuf), 16);
-    bool dead = false;
+    bool dead = false, last = false;
 #pragma unroll 1
-    for (int i = 0; i < n && !dead; ++i) {
+    for (int i = 0; !last && !dead; ++i) {
       dead = !wait(&sh.kfull[ks], kpar, c.status);
-      if (!dead && sh.tile[i % C::METAS].after == 0) {
+      const int after = sh.tile[i % C::METAS].after;
+      last = sh.tile[i % C::METAS].flags & 4;
+      if (after < 0) break;
+      if (!dead && after == 0) {
         if (++qb == C::QB) qb = 0;
         if (qb == 0) qpar ^= 1;
         dead = !wait(&sh.qfull[qb], qpar, c.status);
@@ -607,13 +645,15 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     int vs = 0, g = 0;
     uint32_t vpar = 0, ppar = 0;
     const uint32_t v0 = desc_lo(smem_u32(vring), C::PANEL), p0 = desc_lo(smem_u32(pbuf), 128);
-    bool dead = false;
+    bool dead = false, last = false;
 #pragma unroll 1
-    for (int i = 0; i < n && !dead; ++i) {
+    for (int i = 0; !last && !dead; ++i) {
       dead = !wait(&sh.vfull[vs], vpar, c.status);
       dead = __any_sync(0xFFFFFFFFu, dead);
       if (dead) break;
       const ValueMeta m = sh.value[i % C::METAS];
+      if (m.after < 0) break;
+      last = m.set & 4;
       if (m.groups != 0xFF || m.rows < kTile) {  // rows without a key hold anything, NaN codes too: numbers for P = 0
         uint8_t* vt = vring + vs * C::KV;
 #pragma unroll 1
@@ -633,7 +673,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       tc_fence_after();
       const uint32_t acc = m.after >= NG;  // not the group's first tile of the pair
       if (!dead && elect()) {
-        const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + m.set * C::OSET + g * (C::MB * C::OCOL);
+        const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + (m.set & 3) * C::OSET + g * (C::MB * C::OCOL);
 #pragma unroll
         for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
@@ -652,7 +692,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     }
     __syncwarp();
   }
-  } else if (n > 0) {  // ------------------------------------------------------------------- softmax, a key a thread
+  } else if (u1 > u0) {  // ------------------------------------------------------------------- softmax, a key a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::RSOFT));
     const int grp = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
@@ -660,16 +700,17 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     float* grow = sh.grow[grp];
     uint8_t* pd = pbuf + grp * C::P + tid * 16;
     bool dead = false;
-    int i1 = 0;
+    bool last = false;
     uint32_t turn = 0;  // tiles of this group so far
-    for (int p = 0; i1 < n; ++p) {
+    for (int p = 0; !last; ++p) {
       const PairMeta<N>& pm = sh.pair[p % C::QB];
       if (!wait(&sh.qfull[p % C::QB], (uint32_t)(p / C::QB) & 1u, c.status)) dead = true;
       if (any_of(grp, dead)) break;
-      const int R = pm.R, i0 = pm.i0, set = p % C::OB;
+      const int R = pm.R, i0 = pm.i0, i1 = pm.i1, set = p % C::OB;
+      if (i1 == 0) break;
+      last = pm.last;
       float* ref = sh.ref[set][grp];
       const uint32_t ot = otm + lane_base + set * C::OSET + grp * (C::MB * C::OCOL);
-      i1 = pm.i1;
       float l[N];
 #pragma unroll
       for (int r = 0; r < N; ++r) l[r] = 0.0f;
@@ -847,8 +888,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         const int first_tile = pm.first;
         const int64_t base = pm.base;
         const int n_tiles = pm.n_tiles, parts_here = min(NG, i1 - i0);
-        const bool whole = first_tile >= u0 && first_tile + n_tiles <= u1;
-        const int slot = 2 * cta + (first_tile <= u0 ? 0 : 1);
+        const bool whole = pm.skipped == 0 && i1 - i0 == n_tiles;
+        const int slot = 2 * cta + (i0 == 0 ? 0 : 1);
         // row's factors of the groups (0 without a tile of this pair), and its reference and sum
         if (tid < R) {
           float top = -INFINITY, sum = 0.0f, m[NG];
@@ -913,13 +954,15 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           mbar_arrive(&sh.joined[set]);
         }
         if (!whole) {
-          // the CTA whose ticket completes the pair joins the parts, in their order on the line
-          const int c0 = share.owner(first_tile), parts = share.owner(first_tile + n_tiles - 1) - c0 + 1;
-          if (tid == 0) sh.ticket[grp] = ticket_add(da.counters + c0, 1);
+          // the CTA whose ticket completes the pair joins its parts, when all its own work is done
           any_of(grp, false);
-          if (sh.ticket[grp] == parts - 1) {
-            join_parts<D, N>(da, grp, tid, R, G, base, c0, parts, share.begin(c0) == first_tile, pbuf + grp * C::P);
-            if (tid == 0) da.counters[c0] = 0;
+          const int c0 = share.owner(first_tile), parts = share.owner(first_tile + n_tiles - 1) - c0 + 1;
+          if (tid == 0 && ticket_add(da.counters + c0, 1) == parts - 1) {
+            da.counters[c0] = 0;
+            const int at = atomicAdd(&sh.joins, 1);
+            sh.join[at][0] = R, sh.join[at][1] = c0, sh.join[at][2] = parts;
+            sh.join[at][3] = first_tile - share.begin(c0) <= kPairCost;
+            sh.join_base[at] = base;
           }
         }
       }
@@ -929,6 +972,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMma) tmem_dealloc(tmem, 512);
+  for (int j = 0; j < sh.joins && warp < kMma; ++j)
+    join_parts<D, N>(da, sh.join[j][0], G, sh.join_base[j], sh.join[j][1], sh.join[j][2], sh.join[j][3], ring);
 }
 
 template <int D, int N>
@@ -981,9 +1026,9 @@ int launch_attn_decode(const AttnArgs& a, int head_dim, int64_t rows, const Devi
   da.part_ml = reinterpret_cast<float2*>(w);
   da.part_o = reinterpret_cast<float*>(w + 2 * (size_t)dev.sms * r * sizeof(float2));
   // no more CTAs than tiles that there can be
-  const int64_t most = (int64_t)a.c.n_seqs * a.c.hkv * ((a.c.max_len + kTile - 1) / kTile);
-  if (most > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;  // the line's places are 32-bit
-  const int grid = (int)std::min<int64_t>(dev.sms, most);
+  const int64_t pairs = (int64_t)a.c.n_seqs * a.c.hkv, most = pairs * ((a.c.max_len + kTile - 1) / kTile);
+  if (most + kPairCost * pairs > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;  // the line's places are 32-bit
+  const int grid = (int)std::min<int64_t>(std::min(dev.sms, kMostCtas), most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (head_dim) {
     case 64: return launch_rows<64>(r, da, km, vm, grid, s);
