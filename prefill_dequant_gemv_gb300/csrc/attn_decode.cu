@@ -116,7 +116,7 @@ struct Shared {
   uint64_t kfull[C::SK], kfree[C::SK], vfull[C::SV], vfree[C::SV];
   uint64_t qfull[C::QB], qfree[C::QB];
   uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
-  uint64_t summed[C::OB], joined[C::OB], ended[2];
+  uint64_t summed[C::OB], joined[C::OB], ended[2], joinbar;
   uint32_t tmem;
   int joins;      // pairs whose parts this CTA has to join in the end, at most two
   int join[2][4];  // rows, first CTA, parts, whether the first part is its CTA's first pair
@@ -151,9 +151,10 @@ struct Share {
   }
 };
 
-// A pair takes as long as its tiles and some two more (its rows, its end): the line counts a pair's tiles and
+// A pair takes as long as its tiles and some six more (its rows, its end; 2, 3, 4, 6, 8 and 12 give 117, 110, 109,
+// 107, 110 and 111 us for 64 ragged sequences, and 50, 45, 43, 41, 42 and 43 us for 16 x 4 rows): the line counts a pair's tiles and
 // kPairCost places behind them, which no tile stands at.
-constexpr int kPairCost = 2;
+constexpr int kPairCost = 6;
 __device__ __forceinline__ int places_of(const Seq& s, const AttnArgs& a) {
   const int n = tiles_of(s, a);
   return n ? n + kPairCost : 0;
@@ -256,76 +257,66 @@ struct Walk {
 };
 
 // The joining of a pair's parts, in their order on the line, by the CTA that finished last: its softmax
-// threads (the others have given up their registers), with its rings as scratch.  Latency is all of it (a load takes some 1900 cycles, other SMs having just written
-// the parts), so loads go out many at a time.
+// threads (the others have given up their registers).  A load of what other SMs have just written takes some 1900
+// cycles, so the parts come by bulk copies into the rings, all of a round at once, and the weights meanwhile.
 template <int D, int N>
 __device__ __noinline__ void join_parts(const DecodeArgs& da, int R, int G, int64_t base, int c0, int parts, bool at_start,
-                                        uint8_t* scratch) {
+                                        uint8_t* scratch, uint64_t* bar, uint32_t* phase) {
   using C = Cfg<D, N>;
   const AttnArgs& a = da.a;
-  constexpr int T = 128 * C::GROUPS, W = T / 32, V = D / 4;  // float4s a row
-  static_assert((C::SK + C::SV) * C::KV >= T * 16 + kMostCtas * N * 4, "scratch");
+  constexpr int T = 128 * C::GROUPS, W = T / 32, WT = kMostCtas * N * 4, ROOM = (C::SK + C::SV) * C::KV - WT;
+  static_assert(ROOM >= kMostCtas * 128, "scratch");
   auto slot = [&](int q) { return (int64_t)(2 * (c0 + q) + (q == 0 && !at_start ? 1 : 0)); };
-  float4* sums = reinterpret_cast<float4*>(scratch);    // [T]
-  float* wt = reinterpret_cast<float*>(scratch) + T * 4;  // [parts][N]: weights over the sum
-  const int tid = threadIdx.x, lane = tid & 31;
-  named_sync(15, T);
-  for (int row = tid >> 5; row < R; row += W) {  // a warp a row, a lane a part
-    float m = -INFINITY, l = 0.0f;
+  float* wt = reinterpret_cast<float*>(scratch);  // [parts][N]: weights over the sum
+  uint8_t* buf = scratch + WT;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int all = R * D, most = min(all, ROOM / parts / 16 * 4);  // floats of a part, and in one round
+  bool dead = false;
+#pragma unroll 1
+  for (int f0 = 0; f0 < all; f0 += most) {
+    const int floats = min(most, all - f0);
+    fence_proxy_async_all();  // shared memory read, and the parts written, by ordinary accesses before
+    named_sync(15, T);
+    if (tid == 0) mbar_arrive_expect_tx(bar, (uint32_t)(parts * floats * 4));
+    if (lane == 0)
+      for (int q = warp; q < parts; q += W)
+        bulk_g2s(buf + q * floats * 4, da.part_o + slot(q) * N * D + f0, (uint32_t)(floats * 4), bar);
+    if (f0 == 0) {
+      for (int row = warp; row < R; row += W) {  // a warp a row, a lane a part
+        float m = -INFINITY, l = 0.0f;
 #pragma unroll 2
-    for (int q = lane; q < parts; q += 32) {
-      const float2 z = __ldcg(&da.part_ml[slot(q) * N + row]);
-      const float t = fmaxf(m, z.x);
-      if (t != -INFINITY) l = fmaf(l, ex2(m - t), z.y * ex2(z.x - t));
-      m = t;
-      wt[q * N + row] = z.x;
-    }
-    const float top = warp_max(m);
-    float sum = m == -INFINITY ? 0.0f : l * ex2(m - top);
+        for (int q = lane; q < parts; q += 32) {
+          const float2 z = __ldcg(&da.part_ml[slot(q) * N + row]);
+          const float t = fmaxf(m, z.x);
+          if (t != -INFINITY) l = fmaf(l, ex2(m - t), z.y * ex2(z.x - t));
+          m = t;
+          wt[q * N + row] = z.x;
+        }
+        const float top = warp_max(m);
+        float sum = m == -INFINITY ? 0.0f : l * ex2(m - top);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int q = lane; q < parts; q += 32) {
-      const float z = wt[q * N + row];
-      wt[q * N + row] = z == -INFINITY ? 0.0f : ex2(z - top) * inv;
-    }
-  }
-  named_sync(15, T);
-  // where there are fewer float4s than threads, several threads share one's parts
-  const int E = R * V, share = max(T / E, 1);
-#pragma unroll 1
-  for (int e0 = 0; e0 < E; e0 += T) {
-    const int e = share > 1 ? tid % E : e0 + tid, sub = share > 1 ? tid / E : 0;
-    const bool in = e < E && sub < share;
-    float4 v = make_float4(0, 0, 0, 0);
-    if (in) {
-      const float* w = wt + e / V;
-#pragma unroll 1
-      for (int q = sub; q < parts; q += 8 * share) {
-        float4 y[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)  // past the last part: the last one again, with weight 0
-          y[k] = __ldcg(reinterpret_cast<const float4*>(da.part_o + slot(min(q + k * share, parts - 1)) * N * D) + e);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float f = q + k * share < parts ? w[(q + k * share) * N] : 0.0f;
-          if (f != 0.0f) {  // a part without a key holds anything
-            v.x = fmaf(y[k].x, f, v.x), v.y = fmaf(y[k].y, f, v.y), v.z = fmaf(y[k].z, f, v.z), v.w = fmaf(y[k].w, f, v.w);
-          }
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        for (int q = lane; q < parts; q += 32) {
+          const float z = wt[q * N + row];
+          wt[q * N + row] = z == -INFINITY ? 0.0f : ex2(z - top) * inv;
         }
       }
-    }
-    if (share > 1) {
-      sums[tid] = v;
       named_sync(15, T);
-      if (tid < E)
-        for (int k = 1; k < share; ++k) {
-          const float4 y = sums[k * E + tid];
-          v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-        }
     }
-    if (in && sub == 0) {
-      const int row = e / V, d = (e % V) * 4, t = row / G, g = row - t * G;
+    if (!dead && !wait(bar, *phase & 1, da.a.c.status)) dead = true;
+    *phase += 1;
+#pragma unroll 1
+    for (int e = 4 * tid; e < floats && !dead; e += 4 * T) {
+      const int row = (f0 + e) / D, d = (f0 + e) % D, t = row / G, g = row - t * G;
+      float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+      for (int q = 0; q < parts; ++q) {
+        const float4 y = *reinterpret_cast<const float4*>(buf + (q * floats + e) * 4);
+        const float f = wt[q * N + row];
+        if (f != 0.0f)  // a part without a key holds anything
+          v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+      }
       const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x, v.y), y1 = __floats2bfloat162_rn(v.z, v.w);
       *reinterpret_cast<uint2*>(a.out + base + t * a.ldo + g * a.hso + d) =
           make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
@@ -364,12 +355,14 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     }
     if (t < C::OB) mbar_init(&sh.summed[t], NG), mbar_init(&sh.joined[t], 1);
     if (t < 2) mbar_init(&sh.ended[t], 1);
+    if (t == 2) mbar_init(&sh.joinbar, 1);
     if (t < 8) fence_mbar_init();
   }
   if (warp == kMma) {
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
+  pdl_launch_dependents();  // the next kernel's CTAs may take the SMs that this one leaves free, and wait there
   pdl_wait();
   Walk w;
   bool bad = false;
@@ -972,8 +965,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kMma) tmem_dealloc(tmem, 512);
+  uint32_t phase = 0;
   for (int j = 0; j < sh.joins && warp < kMma; ++j)
-    join_parts<D, N>(da, sh.join[j][0], G, sh.join_base[j], sh.join[j][1], sh.join[j][2], sh.join[j][3], ring);
+    join_parts<D, N>(da, sh.join[j][0], G, sh.join_base[j], sh.join[j][1], sh.join[j][2], sh.join[j][3], ring, &sh.joinbar, &phase);
 }
 
 template <int D, int N>

@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     tmem_alloc(&sh.tmem, 512);
     tmem_relinquish();
   }
+  pdl_launch_dependents();
   pdl_wait();
   // this CTA's row block: the blocks of all sequences in a row, the last ones (with the most keys) first
   if (warp == 0) {

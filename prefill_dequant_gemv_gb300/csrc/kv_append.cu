@@ -357,6 +357,8 @@ template <int LPH, int GT, int ITER>
 __global__ void __launch_bounds__(GT > kAppendThreads ? GT : kAppendThreads)
     append_kernel(const AppendArgs a, int64_t units, int64_t kv_blocks, int per_seq, int scan) {
   __shared__ float red[GT > 32 ? GT / 32 : 1];
+  pdl_launch_dependents();
+  pdl_wait();
   if ((int64_t)blockIdx.x < kv_blocks) {
     const int64_t unit = GT == 32 ? (int64_t)blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (unit < units) append_unit<LPH, GT, ITER>(a, unit, per_seq, scan != 0, red);
@@ -378,9 +380,10 @@ int launch(const AppendArgs& a, cudaStream_t s) {
   const int64_t q_items = c.n_tokens * ((a.hq + kQHeads - 1) / kQHeads), groups = kAppendThreads / LPH;
   const int64_t q_blocks = (q_items + groups - 1) / groups;
   if (kv_blocks + q_blocks > 0x7FFFFFFF || q_items + groups > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;
-  append_kernel<LPH, GT, ITER><<<(unsigned)(kv_blocks + q_blocks), std::max(GT, kAppendThreads), 0, s>>>(
-      a, units, kv_blocks, (int)per, scan ? 1 : 0);
-  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+  return launch_pdl(append_kernel<LPH, GT, ITER>, dim3((unsigned)(kv_blocks + q_blocks)), dim3(std::max(GT, kAppendThreads)), 0,
+                    s, a, units, kv_blocks, (int)per, scan ? 1 : 0) == cudaSuccess
+             ? QG_OK
+             : QG_ERR_CUDA;
 }
 
 // Threads and passes so that a page's values fit the group's registers.

@@ -21,6 +21,8 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, int* status
   atomicExch(status, kStatusTimeout);
   return false;
 }
+// Ordinary accesses of global and shared memory before bulk copies of the same.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
