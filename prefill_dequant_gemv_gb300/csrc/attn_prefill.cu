@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "qg_attn.h"
 #include "qg_attn_dev.cuh"
@@ -38,6 +39,9 @@ struct Cfg {
   static constexpr int BN = D == 256 ? 64 : 128;      // keys a step
   static constexpr int ROWS = 128 * MT;
   static constexpr int THREADS = 128 * (MT + 2);
+  // registers a thread: what the launch gives, what softmax threads take, what the other two warpgroups keep
+  static constexpr int REGS = MT == 2 ? 128 : 168, RSOFT = MT == 2 ? 152 : 216, RREST = MT == 2 ? 104 : 144;
+  static_assert(128 * MT * RSOFT + 256 * RREST <= THREADS * REGS && THREADS * REGS <= 65536, "registers");
   static constexpr int PW = D < 128 ? D : 128;        // bytes of a row of a code panel
   static constexpr int NP = D / PW;
   static constexpr int KV = BN * D;                   // bytes of a tile of key (or value) codes
@@ -106,6 +110,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const int G = a.hq / c.hkv;
   constexpr int kMma = 4 * (MT + 1);  // first warp of the last warpgroup
 
+  // all heads and splits of a row block before the next block
+  const int wide = c.hkv * pa.splits, block = blockIdx.x / wide, head = blockIdx.x % wide / pa.splits;
+  const int split = blockIdx.x % pa.splits;
+
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KS; ++i) mbar_init(&sh.kfull[i], 9), mbar_init(&sh.kfree[i], 1);
     for (int i = 0; i < C::VS; ++i) mbar_init(&sh.cfull[i], 8), mbar_init(&sh.cfree[i], 128);
@@ -132,8 +140,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (base + lane < c.n_seqs) nb = blocks_of(seq_of(c, base + lane, &bad));
       total += __reduce_add_sync(0xFFFFFFFFu, nb);
     }
-    if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicExch(c.status, kStatusInvalid);
-    int left = total - 1 - (int)blockIdx.x;
+    if (bad && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
+    int left = total - 1 - block;
     int ok = left >= 0;
     for (int base = 0; ok && base < c.n_seqs; base += 32) {
       Seq s = {0, 0, 0};
@@ -166,7 +174,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const uint32_t tmem = sh.tmem;
   const bool run = sh.work[5] != 0;
   const int seq = sh.work[0], start = sh.work[2], rows = sh.work[3], len = sh.work[4];
-  const int head = blockIdx.y / pa.splits, split = blockIdx.y % pa.splits;
   const int64_t row0 = (int64_t)sh.work[1] * C::ROWS, all_rows = (int64_t)rows * G;
   const int R = run ? (int)min((int64_t)C::ROWS, all_rows - row0) : 0;  // rows of this block
   // its keys: from the first one that its first row sees (a whole page) to its last row's own
@@ -178,6 +185,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const int n = run ? s1 - s0 : 0, first_key = key0 + s0 * BN;
   const int tiles = MT == 2 && R <= 128 ? 1 : MT;  // row tiles in use
 
+  if (warp >= 4 * MT) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
   if (run && warp == kMma + 1) {  // --------------------------------------------------------- tiles of codes
     // Lane g looks after keys 16g .. of a step (g < BN / 16); page ids come two steps ahead, scales one.
     constexpr int NG = BN / 16;
@@ -370,7 +379,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (++vs == C::VS) vs = 0, cpar ^= 1;
       if (++fs == C::FS) fs = 0, fpar ^= 1;
     }
-  } else if (run && warp < 4 * MT) {  // ----------------------------------------------------- softmax, a row a thread
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::RSOFT));
+    if (run) {  // ---------------------------------------------------------------------------- softmax, a row a thread
     const int mt = warp >> 2, wq = warp & 3;
     const int row = mt * 128 + tid;  // in the block
     const bool in = row < R;
@@ -425,30 +437,40 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const uint32_t st = tmem + lane_base + buf * BN;
       const int t0 = first_key + i * BN;
       const bool masked = sm.cut || t0 + BN - 1 > see || t0 <= skip;
-      // the row's largest t (its factor stays above 0, so that a masked score stays -inf)
+      // 16 keys of the row at a time, the next 16 on their way from tensor memory; masked ones are -inf
+      auto mask = [&](uint32_t(&v)[16], int gr, float ks) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int t = t0 + 16 * gr + e;
+          if (t > pos || t <= pos - a.window || ks == 0.0f) v[e] = 0xFF800000u;
+        }
+      };
+      // the row's largest t
       float top = -INFINITY;
-#pragma unroll 1
-      for (int x = 0; x < BN; x += 32) {
-        uint32_t s[32];
-        tmem_ld32(st + x, s);
-        tmem_ld_wait();
-        if (masked) {
+      auto largest = [&](auto with_mask) {
+        uint32_t s[2][16];
+        tmem_ld16(st, s[0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int t = t0 + x + e;
-            if (t > pos || t <= pos - a.window) s[e] = 0xFF800000u;
-          }
+        for (int gr = 0; gr < BN / 16; ++gr) {
+          uint32_t(&v)[16] = s[gr & 1];
+          tmem_ld_wait16(v);
+          if (gr + 1 < BN / 16) tmem_ld16(st + 16 * (gr + 1), s[(gr + 1) & 1]);
+          const float ks = sm.ks[gr];
+          if (decltype(with_mask)::value) mask(v, gr, ks);
+          float mx[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4])),
+                          fmaxf(__uint_as_float(v[e + 8]), __uint_as_float(v[e + 12])));
+          // (a factor above 0, so that a masked score stays -inf)
+          top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(rc * ks, 0x1p-126f), sm.lvs[gr]));
         }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float mx = __uint_as_float(s[16 * h]);
-#pragma unroll
-          for (int e = 1; e < 16; ++e) mx = fmaxf(mx, __uint_as_float(s[16 * h + e]));
-          const float ks = sm.ks[x / 16 + h];
-          const float t = fmaf(mx, fmaxf(rc * ks, 0x1p-126f), sm.lvs[x / 16 + h]);
-          if (ks != 0.0f && mx != -INFINITY) top = fmaxf(top, t);
-        }
-      }
+      };
+      // (the masks as code of their own: as predicates in the common code they took a third of its time)
+      if (masked)
+        largest(std::true_type());
+      else
+        largest(std::false_type());
       const bool grow = top > m + kLazy || (m == -INFINITY && top != -INFINITY);
       if (__any_sync(0xFFFFFFFFu, grow)) {
         const float w = grow ? ex2(m - top) : 1.0f;
@@ -465,7 +487,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           for (int x = 0; x < D; x += 32) {
             uint32_t o[32];
             tmem_ld32(ot + x, o);
-            tmem_ld_wait();
+            tmem_ld_wait32(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
             tmem_st32(ot + x, o);
@@ -474,39 +496,32 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll 1
-      for (int x = 0; x < BN; x += 32) {
-        uint32_t s[32];
-        tmem_ld32(st + x, s);
-        tmem_ld_wait();
-        if (masked) {
+      auto weights = [&](auto with_mask) {
+        uint32_t s[2][16], p[16];
+        tmem_ld16(st, s[0]);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int t = t0 + x + e;
-            if (t > pos || t <= pos - a.window) s[e] = 0xFF800000u;
-          }
-        }
-        uint32_t p[16];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float ks = sm.ks[x / 16 + h], f = fmaxf(rc * ks, 0x1p-126f), off = sm.lvs[x / 16 + h] - ref;
-          float sum = 0.0f;
+        for (int gr = 0; gr < BN / 16; ++gr) {
+          uint32_t(&v)[16] = s[gr & 1];
+          tmem_ld_wait16(v);
+          if (gr + 1 < BN / 16) tmem_ld16(st + 16 * (gr + 1), s[(gr + 1) & 1]);
+          const float ks = sm.ks[gr], off = sm.lvs[gr] - ref, f = fmaxf(rc * ks, 0x1p-126f);
+          if (decltype(with_mask)::value) mask(v, gr, ks);
+          float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            float p0 = ex2(fmaf(__uint_as_float(s[16 * h + e]), f, off));
-            float p1 = ex2(fmaf(__uint_as_float(s[16 * h + e + 1]), f, off));
-            sum += p0 + p1;
-            p[8 * h + e / 2] = f16x2(p0, p1);
+            const float p0 = ex2(fmaf(__uint_as_float(v[e]), f, off)), p1 = ex2(fmaf(__uint_as_float(v[e + 1]), f, off));
+            sum0 += p0;
+            sum1 += p1;
+            p[8 * (gr & 1) + e / 2] = f16x2(p0, p1);
           }
-          if (masked && ks == 0.0f) {  // hidden keys: their scores may be NaN
-            sum = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) p[8 * h + e] = 0u;
-          }
-          l = fmaf(sum, sm.ivs[x / 16 + h], l);
+          l = fmaf(sum0 + sum1, sm.ivs[gr], l);
+          if (gr & 1) tmem_st16(st + 8 * (gr - 1), p);  // over scores that have been read
         }
-        tmem_st16(st + x / 2, p);
-      }
+      };
+      if (masked)
+        weights(std::true_type());
+      else
+        weights(std::false_type());
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&sh.pfull[buf]);
@@ -516,7 +531,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     tc_fence_after();
     if (!dead && mt < tiles) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t part = ((int64_t)blockIdx.x * c.hkv + head) * pa.splits + split;
+      const int64_t part = blockIdx.x;  // of (block, head), split by split
       uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso;
 #pragma unroll 1
       for (int x = 0; x < D; x += 32) {
@@ -549,6 +564,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (in && pa.splits > 1) pa.part_ml[part * C::ROWS + row] = make_float2(m, l);
     }
     tc_fence_before();
+    }
   }
   __syncthreads();
   if (warp == kMma) {
@@ -557,11 +573,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   }
   if (!run || pa.splits == 1) return;
   // the CTA whose ticket completes the block joins its parts, in order
-  int* counter = pa.counters + (int64_t)blockIdx.x * c.hkv + head;
+  int* counter = pa.counters + blockIdx.x / pa.splits;
   if (threadIdx.x == 0) sh.ticket = ticket_add(counter, 1);
   __syncthreads();
   if (sh.ticket != pa.splits - 1) return;
-  const int64_t part0 = ((int64_t)blockIdx.x * c.hkv + head) * pa.splits;
+  const int64_t part0 = blockIdx.x / pa.splits * pa.splits;
   for (int e = threadIdx.x; e < R * (D / 8); e += C::THREADS) {
     const int row = e / (D / 8), d = e % (D / 8) * 8;
     float top = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -613,7 +629,7 @@ int launch(const AttnArgs& a, const PrefillPlan& p, void* ws, cudaStream_t s) {
   pa.counters = reinterpret_cast<int*>(w + kWsHeader);
   pa.part_ml = reinterpret_cast<float2*>(w + p.off_ml);
   pa.part_o = reinterpret_cast<float*>(w + p.off_o);
-  return launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)p.blocks, (unsigned)(a.c.hkv * p.splits)), dim3(C::THREADS),
+  return launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)(p.blocks * a.c.hkv * p.splits)), dim3(C::THREADS),
                     C::SMEM, s, km, vm, pa) == cudaSuccess
              ? QG_OK
              : QG_ERR_CUDA;
@@ -628,7 +644,7 @@ bool plan_prefill(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_
   // a sequence of t tokens has at most t * G / rows + 1 blocks
   p->blocks = std::min<int64_t>(each * batch->n_seqs, n_tokens * G / rows + batch->n_seqs);
   const int64_t items = p->blocks * cache->n_kv_heads;
-  if (p->blocks > 0x7FFFFFFF || items > 0x7FFFFFFF) return false;
+  if (items > 0x7FFFFFFF / 32) return false;
   // blocks that leave the GPU's last wave emptier than half a wave of many are cut along the keys, into
   // parts of 1024 keys at least
   int64_t s = std::min<int64_t>(2 * (int64_t)dev.sms / std::max<int64_t>(items, 1), batch->max_len / 1024);
