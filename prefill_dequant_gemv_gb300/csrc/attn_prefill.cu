@@ -13,7 +13,8 @@
 //     of the second product; splitting it into E4M3 terms would cost three conversions an element where
 //     this needs one, and the value codes are converted once for all rows instead, by a
 //     warpgroup of their own, into the fp16 tile that the second product reads transposed;
-//   * a thread owns a row: no reduction crosses threads.
+//   * a row belongs to two threads, each with half of a step's keys and of the outputs: with one thread a row the
+//     softmax of a step took 2300 cycles against the 1050 of its products, and two row tiles cannot hide that.
 // Few tiles are split over the keys (parts of a row join in order in the CTA that finishes last).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -21,7 +22,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "qg_attn.h"
 #include "qg_attn_dev.cuh"
@@ -38,10 +38,11 @@ struct Cfg {
   static constexpr int MT = D == 256 ? 1 : 2;         // row tiles of 128
   static constexpr int BN = D == 256 ? 64 : 128;      // keys a step
   static constexpr int ROWS = 128 * MT;
-  static constexpr int THREADS = 128 * (MT + 2);
+  static constexpr int SOFT = 256 * MT;               // softmax threads: two a row
+  static constexpr int THREADS = SOFT + 256;
   // registers a thread: what the launch gives, what softmax threads take, what the other two warpgroups keep
-  static constexpr int REGS = MT == 2 ? 128 : 168, RSOFT = MT == 2 ? 152 : 216, RREST = MT == 2 ? 104 : 144;
-  static_assert(128 * MT * RSOFT + 256 * RREST <= THREADS * REGS && THREADS * REGS <= 65536, "registers");
+  static constexpr int REGS = MT == 2 ? 80 : 128, RSOFT = MT == 2 ? 96 : 144, RREST = MT == 2 ? 48 : 112;
+  static_assert(SOFT * RSOFT + 256 * RREST <= THREADS * REGS && THREADS * REGS <= 65536, "registers");
   static constexpr int PW = D < 128 ? D : 128;        // bytes of a row of a code panel
   static constexpr int NP = D / PW;
   static constexpr int KV = BN * D;                   // bytes of a tile of key (or value) codes
@@ -51,7 +52,7 @@ struct Cfg {
   static constexpr int KS = D == 64 ? 4 : 3, VS = 2, FS = 2;
   static constexpr int SB = MT == 1 ? 2 : 1;          // score buffers a row tile
   static constexpr int OCOL = MT * SB * BN;           // TMEM column of the outputs
-  static constexpr int SMEM = 1024 + MT * Q + KS * KV + VS * KV + FS * VF + 4096;
+  static constexpr int SMEM = 1024 + MT * Q + KS * KV + VS * KV + FS * VF + 8192;
   static_assert(SMEM <= 232448 && OCOL + MT * D <= 512, "shared and tensor memory");
 };
 
@@ -64,6 +65,8 @@ struct Shared {
   using C = Cfg<D>;
   StepMeta step[8];
   uint64_t kfull[C::KS], kfree[C::KS], cfull[C::VS], cfree[C::VS], vfull[C::FS], vfree[C::FS];
+  float other[2][C::MT][2][128];  // what the two threads of a row tell each other
+  float rc[C::ROWS];              // a row's power of two * scale * log2(e)
   uint64_t qfull, sfull[C::MT * C::SB], pfull[C::MT * C::SB], odone[C::MT], ended;
   uint32_t tmem;
   int work[8];
@@ -91,6 +94,17 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t blo,
       : "memory");
 }
 
+// Barrier of the 256 softmax threads of a row tile that returns whether any thread's v is set.
+__device__ __forceinline__ bool any_of_pair(int tile, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(1 + tile), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     attn_prefill_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -103,12 +117,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   uint8_t* cring = kring + C::KS * C::KV;
   uint8_t* vring = cring + C::VS * C::KV;
   Shared<D>& sh = *reinterpret_cast<Shared<D>*>(vring + C::FS * C::VF);
-  static_assert(sizeof(Shared<D>) <= 3072, "shared memory");
+  static_assert(sizeof(Shared<D>) <= 7168, "shared memory");
   const AttnArgs& a = pa.a;
   const KvArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
   const int G = a.hq / c.hkv;
-  constexpr int kMma = 4 * (MT + 1);  // first warp of the last warpgroup
+  constexpr int kConv = 8 * MT, kMma = kConv + 4;  // first warps of the converters' and the last warpgroup
 
   // all heads and splits of a row block before the next block
   const int wide = c.hkv * pa.splits, block = blockIdx.x / wide, head = blockIdx.x % wide / pa.splits;
@@ -118,9 +132,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     for (int i = 0; i < C::KS; ++i) mbar_init(&sh.kfull[i], 9), mbar_init(&sh.kfree[i], 1);
     for (int i = 0; i < C::VS; ++i) mbar_init(&sh.cfull[i], 8), mbar_init(&sh.cfree[i], 128);
     for (int i = 0; i < C::FS; ++i) mbar_init(&sh.vfull[i], 128), mbar_init(&sh.vfree[i], 1);
-    for (int i = 0; i < MT * C::SB; ++i) mbar_init(&sh.sfull[i], 2), mbar_init(&sh.pfull[i], 128);
+    for (int i = 0; i < MT * C::SB; ++i) mbar_init(&sh.sfull[i], 2), mbar_init(&sh.pfull[i], 256);
     for (int i = 0; i < MT; ++i) mbar_init(&sh.odone[i], 1);
-    mbar_init(&sh.qfull, 128 * MT);
+    mbar_init(&sh.qfull, C::SOFT);
     mbar_init(&sh.ended, 1);
     fence_mbar_init();
   }
@@ -185,7 +199,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   const int n = run ? s1 - s0 : 0, first_key = key0 + s0 * BN;
   const int tiles = MT == 2 && R <= 128 ? 1 : MT;  // row tiles in use
 
-  if (warp >= 4 * MT) {
+  if (warp >= kConv) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
   if (run && warp == kMma + 1) {  // --------------------------------------------------------- tiles of codes
     // Lane g looks after keys 16g .. of a step (g < BN / 16); page ids come two steps ahead, scales one.
@@ -295,7 +309,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const uint32_t p = tmem + (m * C::SB + sb) * BN, d = tmem + C::OCOL + m * D;
 #pragma unroll
         for (int x = 0; x < BN / 16; ++x)
-          mma_f16_ts<kVHi, kPv>(d, p + 8 * x, v0 + (fs * C::VF + x * 16 * 128) / 16, (i > 0) | (x > 0));
+          mma_f16_ts<kVHi, kPv>(d, p + (x < BN / 32 ? 8 * x : BN / 2 + 8 * (x - BN / 32)), v0 + (fs * C::VF + x * 16 * 128) / 16, (i > 0) | (x > 0));
         if (m == tiles - 1) mma_commit(&sh.vfree[fs]);
         if (i == n - 1) mma_commit(&sh.odone[m]);
       }
@@ -344,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       wait(&sh.ended, 0, c.status);
     }
     __syncwarp();
-  } else if (run && warp >= 4 * MT && warp < kMma) {  // ------------------------------------ value codes -> fp16
+  } else if (run && warp >= kConv && warp < kMma) {  // ------------------------------------ value codes -> fp16
     // a key a thread (two threads a key where there are 64)
     constexpr int TPK = 128 / BN, CH = D / 16 / TPK;  // chunks of 16 codes a thread
     const int key = tid % BN, part = tid / BN;
@@ -383,41 +397,52 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::RSOFT));
     if (run) {  // ---------------------------------------------------------------------------- softmax, a row a thread
-    const int mt = warp >> 2, wq = warp & 3;
+    const int mt = warp >> 3, half = warp >> 2 & 1, wq = warp & 3;
     const int row = mt * 128 + tid;  // in the block
     const bool in = row < R;
     const int64_t r = row0 + row;
     const int tok = in ? (int)(r / G) : 0, g = in ? (int)(r - (int64_t)tok * G) : 0;
     const int pos = max(in ? len - rows + tok : pos1, -1);
     const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-    // the query row as two E4M3 terms
-    const uint16_t* qp = a.q + (int64_t)(start + tok) * a.ldq + (int64_t)(head * G + g) * a.hsq;
-    float amax = 0.0f;
-    if (n > 0) {
-#pragma unroll 8
-      for (int x = 0; x < D / 8; ++x) {
-        const uint4 v = in ? *reinterpret_cast<const uint4*>(qp + 8 * x) : make_uint4(0, 0, 0, 0);
-        const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+    if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
+      constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP, UN = PASSES < 4 ? PASSES : 4;
+      const int part = threadIdx.x % TPR;
+#pragma unroll 1
+      for (int p0 = 0; p0 < PASSES; p0 += UN) {
+        uint4 v[UN][2];
 #pragma unroll
-        for (int z = 0; z < 4; ++z)
-          amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[z] << 16)), fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
-      }
-    }
-    // a power of two that brings the row's largest element to [128, 256)
-    const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
-    const float down = __int_as_float((127 - e2) << 23), rc = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
-    if (n > 0) {
-      uint8_t* qd = qbuf + mt * C::Q;
-#pragma unroll 2
-      for (int x = 0; x < D / 16; ++x) {
-        uint4 v[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-        if (in) v[0] = *reinterpret_cast<const uint4*>(qp + 16 * x), v[1] = *reinterpret_cast<const uint4*>(qp + 16 * x + 8);
-        uint4 hi, lo;
-        split_query(v, down, &hi, &lo);
-        const int panel = x / (C::PW / 16), cc = x % (C::PW / 16), sw = D == 64 ? cc ^ ((tid >> 1) & 3) : cc ^ (tid & 7);
-        uint8_t* at = qd + panel * 128 * C::PW + tid * C::PW + sw * 16;
-        *reinterpret_cast<uint4*>(at) = hi;
-        *reinterpret_cast<uint4*>(at + 128 * D) = lo;
+        for (int y = 0; y < UN; ++y) {
+          const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
+          v[y][0] = v[y][1] = make_uint4(0, 0, 0, 0);
+          if (qr < R) {
+            const int64_t rr = row0 + qr;
+            const int qt = (int)(rr / G), qg = (int)(rr - (int64_t)qt * G);
+            const uint4* qp = reinterpret_cast<const uint4*>(a.q + (int64_t)(start + qt) * a.ldq +
+                                                             (int64_t)(head * G + qg) * a.hsq + 16 * part);
+            v[y][0] = qp[0];
+            v[y][1] = qp[1];
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < UN; ++y) {
+          const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
+          const uint32_t e[8] = {v[y][0].x, v[y][0].y, v[y][0].z, v[y][0].w, v[y][1].x, v[y][1].y, v[y][1].z, v[y][1].w};
+          float amax = 0.0f;
+#pragma unroll
+          for (int z = 0; z < 8; ++z)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[z] << 16)), fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
+#pragma unroll
+          for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          // a power of two that brings the row's largest element to [128, 256)
+          const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
+          uint4 hi, lo;
+          split_query(v[y], __int_as_float((127 - e2) << 23), &hi, &lo);
+          const int panel = part / (C::PW / 16), cc = part % (C::PW / 16), sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
+          uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;
+          *reinterpret_cast<uint4*>(at) = hi;
+          *reinterpret_cast<uint4*>(at + 128 * D) = lo;
+          if (part == 0) sh.rc[qr] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(&sh.qfull);
@@ -426,127 +451,120 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
     const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
     bool dead = false;
-    const uint32_t ot = tmem + lane_base + C::OCOL + mt * D;
+    constexpr int GH = BN / 32;  // groups of 16 keys of this thread's half
+    const uint32_t ot = tmem + lane_base + C::OCOL + mt * D + half * (D / 2);
     for (int i = 0; i < n && mt < tiles; ++i) {
       const int sb = MT == 1 ? i & 1 : 0, buf = mt * C::SB + sb;
       if (!wait(&sh.sfull[buf], (MT == 1 ? i >> 1 : i) & 1, c.status)) dead = true;
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      if (dead) break;
       tc_fence_after();
       const StepMeta& sm = sh.step[i & 7];
-      const uint32_t st = tmem + lane_base + buf * BN;
-      const int t0 = first_key + i * BN;
-      const bool masked = sm.cut || t0 + BN - 1 > see || t0 <= skip;
-      // 16 keys of the row at a time, the next 16 on their way from tensor memory; masked ones are -inf
-      auto mask = [&](uint32_t(&v)[16], int gr, float ks) {
+      const uint32_t st = tmem + lane_base + buf * BN + half * (BN / 2);
+      const int t0 = first_key + i * BN + half * (BN / 2), g0 = half * GH;
+      const bool masked = sm.cut || t0 + BN / 2 - 1 > see || t0 <= skip;
+      const float rc = sh.rc[row];
+      // this thread's scores, read once; masked ones are -inf
+      uint32_t s[GH][16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = t0 + 16 * gr + e;
-          if (t > pos || t <= pos - a.window || ks == 0.0f) v[e] = 0xFF800000u;
+      for (int gr = 0; gr < GH; ++gr) tmem_ld16(st + 16 * gr, s[gr]);
+#pragma unroll
+      for (int gr = 0; gr < GH; ++gr) tmem_ld_wait16(s[gr]);
+      if (masked) {
+        asm volatile("" ::: "memory");  // a branch: as predicates the masks took a third of every step's time
+#pragma unroll
+        for (int gr = 0; gr < GH; ++gr) {
+          const bool hidden = sm.ks[g0 + gr] == 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const int t = t0 + 16 * gr + e;
+            if (t > pos || t <= pos - a.window || hidden) s[gr][e] = 0xFF800000u;
+          }
         }
-      };
+      }
       // the row's largest t
       float top = -INFINITY;
-      auto largest = [&](auto with_mask) {
-        uint32_t s[2][16];
-        tmem_ld16(st, s[0]);
 #pragma unroll
-        for (int gr = 0; gr < BN / 16; ++gr) {
-          uint32_t(&v)[16] = s[gr & 1];
-          tmem_ld_wait16(v);
-          if (gr + 1 < BN / 16) tmem_ld16(st + 16 * (gr + 1), s[(gr + 1) & 1]);
-          const float ks = sm.ks[gr];
-          if (decltype(with_mask)::value) mask(v, gr, ks);
-          float mx[4];
+      for (int gr = 0; gr < GH; ++gr) {
+        float mx[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = fmaxf(fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 4])),
-                          fmaxf(__uint_as_float(v[e + 8]), __uint_as_float(v[e + 12])));
-          // (a factor above 0, so that a masked score stays -inf)
-          top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(rc * ks, 0x1p-126f), sm.lvs[gr]));
-        }
-      };
-      // (the masks as code of their own: as predicates in the common code they took a third of its time)
-      if (masked)
-        largest(std::true_type());
-      else
-        largest(std::false_type());
+        for (int e = 0; e < 4; ++e)
+          mx[e] = fmaxf(fmaxf(__uint_as_float(s[gr][e]), __uint_as_float(s[gr][e + 4])),
+                        fmaxf(__uint_as_float(s[gr][e + 8]), __uint_as_float(s[gr][e + 12])));
+        // (a factor above 0, so that a masked score stays -inf)
+        top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f),
+                              sm.lvs[g0 + gr]));
+      }
+      float(&other)[2][128] = sh.other[i & 1][mt];
+      other[half][tid] = top;
+      dead = any_of_pair(mt, dead);
+      if (dead) break;
+      top = fmaxf(top, other[half ^ 1][tid]);
       const bool grow = top > m + kLazy || (m == -INFINITY && top != -INFINITY);
       if (__any_sync(0xFFFFFFFFu, grow)) {
         const float w = grow ? ex2(m - top) : 1.0f;
         if (grow) m = top;
         l *= w;
         if (i > 0) {
-          if (MT == 1) {  // the product before may still run
-            if (!wait(&sh.vfree[(i - 1) % C::FS], (uint32_t)((i - 1) / C::FS) & 1u, c.status)) dead = true;
-            dead = __any_sync(0xFFFFFFFFu, dead);
-            if (dead) break;
-            tc_fence_after();
-          }
+          // (heads of 256: the product before may still run)
+          if (MT == 1 && !wait(&sh.vfree[(i - 1) % C::FS], (uint32_t)((i - 1) / C::FS) & 1u, c.status)) dead = true;
+          tc_fence_after();
 #pragma unroll 1
-          for (int x = 0; x < D; x += 32) {
-            uint32_t o[32];
-            tmem_ld32(ot + x, o);
-            tmem_ld_wait32(o);
+          for (int x = 0; x < D / 2; x += 16) {
+            uint32_t o[16];
+            tmem_ld16(ot + x, o);
+            tmem_ld_wait16(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
-            tmem_st32(ot + x, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
+            tmem_st16(ot + x, o);
           }
           tmem_st_wait();
         }
       }
       const float ref = m == -INFINITY ? 0.0f : m;
-      auto weights = [&](auto with_mask) {
-        uint32_t s[2][16], p[16];
-        tmem_ld16(st, s[0]);
 #pragma unroll
-        for (int gr = 0; gr < BN / 16; ++gr) {
-          uint32_t(&v)[16] = s[gr & 1];
-          tmem_ld_wait16(v);
-          if (gr + 1 < BN / 16) tmem_ld16(st + 16 * (gr + 1), s[(gr + 1) & 1]);
-          const float ks = sm.ks[gr], off = sm.lvs[gr] - ref, f = fmaxf(rc * ks, 0x1p-126f);
-          if (decltype(with_mask)::value) mask(v, gr, ks);
-          float sum0 = 0.0f, sum1 = 0.0f;
+      for (int gr = 0; gr < GH; ++gr) {
+        uint32_t p[8];
+        const float off = sm.lvs[g0 + gr] - ref, f = fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f);
+        float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(v[e]), f, off)), p1 = ex2(fmaf(__uint_as_float(v[e + 1]), f, off));
-            sum0 += p0;
-            sum1 += p1;
-            p[8 * (gr & 1) + e / 2] = f16x2(p0, p1);
-          }
-          l = fmaf(sum0 + sum1, sm.ivs[gr], l);
-          if (gr & 1) tmem_st16(st + 8 * (gr - 1), p);  // over scores that have been read
+        for (int e = 0; e < 16; e += 2) {
+          const float p0 = ex2(fmaf(__uint_as_float(s[gr][e]), f, off)), p1 = ex2(fmaf(__uint_as_float(s[gr][e + 1]), f, off));
+          sum0 += p0;
+          sum1 += p1;
+          p[e / 2] = f16x2(p0, p1);
         }
-      };
-      if (masked)
-        weights(std::true_type());
-      else
-        weights(std::false_type());
+        l = fmaf(sum0 + sum1, sm.ivs[g0 + gr], l);
+        tmem_st8(st + 8 * gr, p);  // over the scores of this half
+      }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(&sh.pfull[buf]);
     }
     if (n > 0 && mt < tiles && !dead && !wait(&sh.odone[mt], 0, c.status)) dead = true;
-    dead = __any_sync(0xFFFFFFFFu, dead);
-    tc_fence_after();
+    if (mt < tiles) {
+      float(&other)[2][128] = sh.other[n & 1][mt];
+      other[half][tid] = l;
+      dead = any_of_pair(mt, dead);
+      l += other[half ^ 1][tid];
+      tc_fence_after();
+    }
     if (!dead && mt < tiles) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       const int64_t part = blockIdx.x;  // of (block, head), split by split
-      uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso;
+      uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
 #pragma unroll 1
-      for (int x = 0; x < D; x += 32) {
-        uint32_t o[32];
+      for (int x = 0; x < D / 2; x += 16) {
+        uint32_t o[16];
         if (n > 0) {
-          tmem_ld32(ot + x, o);
-          tmem_ld_wait();
+          tmem_ld16(ot + x, o);
+          tmem_ld_wait16(o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+          for (int e = 0; e < 16; ++e) o[e] = 0u;
         }
         if (in) {
           if (pa.splits == 1) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
+            for (int e = 0; e < 16; e += 8) {
               uint32_t y[4];
 #pragma unroll
               for (int z = 0; z < 4; ++z)
@@ -554,14 +572,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               *reinterpret_cast<uint4*>(out + x + e) = make_uint4(y[0], y[1], y[2], y[3]);
             }
           } else {
-            float* dst = pa.part_o + (part * C::ROWS + row) * D + x;
+            float* dst = pa.part_o + (part * C::ROWS + row) * D + half * (D / 2) + x;
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
+            for (int e = 0; e < 16; e += 4)
               *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
           }
         }
       }
-      if (in && pa.splits > 1) pa.part_ml[part * C::ROWS + row] = make_float2(m, l);
+      if (in && half == 0 && pa.splits > 1) pa.part_ml[part * C::ROWS + row] = make_float2(m, l);
     }
     tc_fence_before();
     }
