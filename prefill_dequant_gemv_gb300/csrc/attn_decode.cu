@@ -374,7 +374,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   const Share share = {total / max(grid, 1), total % max(grid, 1)};
   int u0 = cta < grid ? share.begin(cta) : 0, u1 = cta < grid ? share.begin(cta + 1) : 0;
   // A few short pairs: a CTA a pair.  Its groups take most tiles at once, and a join between CTAs costs more
-  // than a second round (one sequence of 777 keys, 8 KV heads of 128: 11.5 us so, 15.4 cut into 56 CTAs).
+  // than a second round (one sequence of 777 keys, 8 KV heads of 128: 13.9 us so, some 15 cut into 56 CTAs).
   if (most <= 2 * NG + kPairCost && c.n_seqs <= 32 && c.n_seqs * c.hkv <= (int)gridDim.x) w.pair_of(a, cta, lane, &u0, &u1);
   int place = u1;  // of this CTA's first tile
   if (warp > kMma && warp < kMma + 7) place = w.find(a, u0, u1, lane);
@@ -387,304 +387,304 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 
   if (u1 > u0 && warp >= kMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
-  if (warp > kMma && warp <= kMma + 2 * NPR) {  // -------------------------------- key tiles, value tiles
-    // NPR warps for the keys, as many for the values, each with every NPR-th tile: a tile's copies take
-    // one warp some 600 to 1100 cycles to issue.  Lanes 8q .. 8q + 7 look after one of four tiles: its eight
-    // groups of 16 keys.  Four tiles' page ids are fetched by one load, while the four before them are issued.
-    const bool keys = warp <= kMma + NPR;
-    const int odd = NPR == 2 ? (warp - kMma - 1) & 1 : 0;
-    const int stages = keys ? C::SK : C::SV;
-    uint8_t* slots = keys ? ring : vring;
-    uint64_t* full = keys ? sh.kfull : sh.vfull;
-    uint64_t* free_ = keys ? sh.kfree : sh.vfree;
-    const CUtensorMap* map = keys ? &kmap : &vmap;
-    const int P = 1 << c.page_log2, box = min(P, kTile);
-    int tok0 = 0, len = 0, head = 0, after = 0, id = -1, flags = 0, ready = 0, set = 0, pairs = 0, in_pair = 0;
-    bool dead = false, done = place >= u1;
-    int s = odd, i = odd, lap = 0;
-    if (done && keys && odd == 0) {  // no tile for this CTA
-      if (lane == 0) sh.tile[0].after = -1;
-      __syncwarp();
-      if (lane < 16) mbar_arrive(&full[0]);
-    } else if (done && odd == 0) {
-      if (lane == 0) sh.value[0].after = -1;
-      __syncwarp();
-      if (lane < 8) mbar_arrive(&full[0]);
-    }
-    do {
-      const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cflags = flags, cready = ready, cset = set;
-      // the next four tiles (the first time, the first four)
-      int b = w.b;
-      len = 0;
-      ready = 0;
-      auto describe = [&](int q) {  // tile q places on, in the pair at hand
-        const int k = w.k + q, at = place + q + 1;
-        b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + k * kTile, after = in_pair + q, set = pairs % C::OB;
-        // the rows stand at len - rows .. len - 1
-        flags = tok0 + kTile - 1 > len - w.sq.rows || tok0 <= len - 1 - a.window ? 2 : 0;
-        if (at >= u1 || (k == w.n - 1 && at + kPairCost >= u1)) flags |= 4;
-      };
-      auto walk = [&](int q) {
-        place += q;
-        in_pair += q;
-        w.k += q;
-        if (w.k == w.n) {
-          place += kPairCost;
-          in_pair = 0;
-          ++pairs;
-          if (place < u1) w.next_pair(a);
-        }
-        done = place >= u1;
-      };
-      if (!done && w.k + 4 * NPR <= w.n && place + 4 * NPR <= u1) {  // all of one pair
-        describe(NPR * (lane >> 3) + odd);
-        ready = 4;
-        walk(4 * NPR);
-      } else {
-#pragma unroll 1
-        for (int q = 0; q < 4 * NPR && !done; ++q) {
-          if (q % NPR == odd) {
-            if (lane >> 3 == q / NPR) describe(0);
-            ++ready;
-          }
-          walk(1);
-        }
-      }
-      id = -1;
-      const int64_t next = (int64_t)tok0 + 16 * (lane & 7);
-      if (next < len) id = c.pages[(int64_t)b * c.page_stride + (next >> c.page_log2)];
-#pragma unroll 1
-      for (int q = 0; q < cready; ++q, i += NPR) {
-        if (lap && !wait(&free_[s], (lap - 1) & 1, c.status)) dead = true;
-        if (__any_sync(0xFFFFFFFFu, dead)) {
-          dead = true;
-          break;
-        }
-        if (lane >> 3 == q) {
-          const int gl = lane & 7, tok = ctok0 + 16 * gl;
-          bool ok = tok < clen;
-          if (ok && (cid < 0 || cid >= c.n_pages)) {
-            ok = false;
-            atomicExch(c.status, kStatusInvalid);
-          }
-          const int64_t tile = (int64_t)cid * c.hkv + chead;
-          TileMeta& m = sh.tile[i % C::METAS];
-          if (keys) {  // written before this lane's arrival, which hands it over
-            const bool cut = __any_sync(0xFFu << (8 * q), !ok || tok + 16 > clen);
-            if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = cflags | (cut ? 3 : 0);
-            if (!ok) m.ks[gl] = m.vs[gl] = 0.0f;
-          } else {
-            const uint32_t groups = __ballot_sync(0xFFu << (8 * q), ok) >> (8 * q);
-            if (gl == 0) {
-              ValueMeta& vm = sh.value[i % C::METAS];
-              vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu), vm.set = cset | (cflags & 4);
-            }
-          }
-          if (ok && (16 * gl) % box == 0) {
-            uint8_t* dst = slots + s * C::KV + 16 * gl * C::PW;
-            mbar_arrive_expect_tx(&full[s], box * D);
-#pragma unroll
-            for (int x = 0; x < C::NP; ++x)
-              tma_load_3d(dst + x * C::PANEL, map, x * 128, tok & (P - 1), (int)tile, &full[s]);
-          } else {
-            mbar_arrive(&full[s]);
-          }
-          if (keys) {
-            if (ok) {
-              cp_async4(&m.ks[gl], c.ks + tile);
-              cp_async4(&m.vs[gl], c.vs + tile);
-            }
-            cp_async_arrive_noinc(&full[s]);
-          }
-        }
+    if (warp > kMma && warp <= kMma + 2 * NPR) {  // -------------------------------- key tiles, value tiles
+      // NPR warps for the keys, as many for the values, each with every NPR-th tile: a tile's copies take
+      // one warp some 600 to 1100 cycles to issue.  Lanes 8q .. 8q + 7 look after one of four tiles: its eight
+      // groups of 16 keys.  Four tiles' page ids are fetched by one load, while the four before them are issued.
+      const bool keys = warp <= kMma + NPR;
+      const int odd = NPR == 2 ? (warp - kMma - 1) & 1 : 0;
+      const int stages = keys ? C::SK : C::SV;
+      uint8_t* slots = keys ? ring : vring;
+      uint64_t* full = keys ? sh.kfull : sh.vfull;
+      uint64_t* free_ = keys ? sh.kfree : sh.vfree;
+      const CUtensorMap* map = keys ? &kmap : &vmap;
+      const int P = 1 << c.page_log2, box = min(P, kTile);
+      int tok0 = 0, len = 0, head = 0, after = 0, id = -1, flags = 0, ready = 0, set = 0, pairs = 0, in_pair = 0;
+      bool dead = false, done = place >= u1;
+      int s = odd, i = odd, lap = 0;
+      if (done && keys && odd == 0) {  // no tile for this CTA
+        if (lane == 0) sh.tile[0].after = -1;
         __syncwarp();
-        s += NPR;
-        if (s >= stages) s -= stages, ++lap;
+        if (lane < 16) mbar_arrive(&full[0]);
+      } else if (done && odd == 0) {
+        if (lane == 0) sh.value[0].after = -1;
+        __syncwarp();
+        if (lane < 8) mbar_arrive(&full[0]);
       }
-    } while (!dead && (ready || !done));
-    // no copy is left in flight into this CTA's shared memory when it ends: the last stages filled
+      do {
+        const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cflags = flags, cready = ready, cset = set;
+        // the next four tiles (the first time, the first four)
+        int b = w.b;
+        len = 0;
+        ready = 0;
+        auto describe = [&](int q) {  // tile q places on, in the pair at hand
+          const int k = w.k + q, at = place + q + 1;
+          b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + k * kTile, after = in_pair + q, set = pairs % C::OB;
+          // the rows stand at len - rows .. len - 1
+          flags = tok0 + kTile - 1 > len - w.sq.rows || tok0 <= len - 1 - a.window ? 2 : 0;
+          if (at >= u1 || (k == w.n - 1 && at + kPairCost >= u1)) flags |= 4;
+        };
+        auto walk = [&](int q) {
+          place += q;
+          in_pair += q;
+          w.k += q;
+          if (w.k == w.n) {
+            place += kPairCost;
+            in_pair = 0;
+            ++pairs;
+            if (place < u1) w.next_pair(a);
+          }
+          done = place >= u1;
+        };
+        if (!done && w.k + 4 * NPR <= w.n && place + 4 * NPR <= u1) {  // all of one pair
+          describe(NPR * (lane >> 3) + odd);
+          ready = 4;
+          walk(4 * NPR);
+        } else {
 #pragma unroll 1
-    for (int j = max(odd, i - stages); j < i; j += NPR)
-      wait(&full[j % stages], (uint32_t)(j / stages) & 1u, c.status);
-  } else if (warp == kMma + 5 || warp == kMma + 6) {  // -------------------------- query rows
-    // Two warps; D / 16 lanes a row, 16 elements each; the loads of four rows a lane group are issued together.
-    // Rows past R stay as they are: their columns of S are not looked at.
-    constexpr int TPR = D / 16, RPP = 32 / TPR;
-    const int part = lane % TPR, mine = (warp - kMma - 5) * RPP + lane / TPR;
-    bool dead = false;
-    if (place >= u1) {  // no pair for this CTA
-      if (lane == 0) sh.pair[0].i1 = 0;
-      __syncwarp();
-      mbar_arrive(&sh.qfull[0]);
-    }
-    for (int p = 0, i0 = 0; place < u1; ++p) {
-      const int qb = p % C::QB;
-      const int R = min(w.sq.rows * G, N), first_pos = w.sq.len - w.sq.rows;
-      const int i1 = i0 + min(w.n - w.k, u1 - place), next = place + w.n - w.k + kPairCost;
-      const int64_t qbase = (int64_t)w.sq.start * a.ldq + (int64_t)w.h * G * a.hsq + 16 * part;
-      PairMeta<N>& m = sh.pair[qb];
-      uint8_t* qd = qbuf + qb * C::Q;
-      bool waited = p < C::QB;
-#pragma unroll 1
-      for (int r0 = mine; __any_sync(0xFFFFFFFFu, r0 < R); r0 += 8 * RPP) {
-        uint4 x[4][2];
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int row = r0 + 2 * RPP * y, i = row / G, g = row - i * G;
-          x[y][0] = x[y][1] = make_uint4(0, 0, 0, 0);
-          if (row < R) {
-            const uint4* qp = reinterpret_cast<const uint4*>(a.q + qbase + i * a.ldq + g * a.hsq);
-            x[y][0] = qp[0];
-            x[y][1] = qp[1];
+          for (int q = 0; q < 4 * NPR && !done; ++q) {
+            if (q % NPR == odd) {
+              if (lane >> 3 == q / NPR) describe(0);
+              ++ready;
+            }
+            walk(1);
           }
         }
-        if (!waited) {
-          if (!wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
-          waited = true;
+        id = -1;
+        const int64_t next = (int64_t)tok0 + 16 * (lane & 7);
+        if (next < len) id = c.pages[(int64_t)b * c.page_stride + (next >> c.page_log2)];
+#pragma unroll 1
+        for (int q = 0; q < cready; ++q, i += NPR) {
+          if (lap && !wait(&free_[s], (lap - 1) & 1, c.status)) dead = true;
+          if (__any_sync(0xFFFFFFFFu, dead)) {
+            dead = true;
+            break;
+          }
+          if (lane >> 3 == q) {
+            const int gl = lane & 7, tok = ctok0 + 16 * gl;
+            bool ok = tok < clen;
+            if (ok && (cid < 0 || cid >= c.n_pages)) {
+              ok = false;
+              atomicExch(c.status, kStatusInvalid);
+            }
+            const int64_t tile = (int64_t)cid * c.hkv + chead;
+            TileMeta& m = sh.tile[i % C::METAS];
+            if (keys) {  // written before this lane's arrival, which hands it over
+              const bool cut = __any_sync(0xFFu << (8 * q), !ok || tok + 16 > clen);
+              if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = cflags | (cut ? 3 : 0);
+              if (!ok) m.ks[gl] = m.vs[gl] = 0.0f;
+            } else {
+              const uint32_t groups = __ballot_sync(0xFFu << (8 * q), ok) >> (8 * q);
+              if (gl == 0) {
+                ValueMeta& vm = sh.value[i % C::METAS];
+                vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu), vm.set = cset | (cflags & 4);
+              }
+            }
+            if (ok && (16 * gl) % box == 0) {
+              uint8_t* dst = slots + s * C::KV + 16 * gl * C::PW;
+              mbar_arrive_expect_tx(&full[s], box * D);
+#pragma unroll
+              for (int x = 0; x < C::NP; ++x)
+                tma_load_3d(dst + x * C::PANEL, map, x * 128, tok & (P - 1), (int)tile, &full[s]);
+            } else {
+              mbar_arrive(&full[s]);
+            }
+            if (keys) {
+              if (ok) {
+                cp_async4(&m.ks[gl], c.ks + tile);
+                cp_async4(&m.vs[gl], c.vs + tile);
+              }
+              cp_async_arrive_noinc(&full[s]);
+            }
+          }
+          __syncwarp();
+          s += NPR;
+          if (s >= stages) s -= stages, ++lap;
         }
+      } while (!dead && (ready || !done));
+      // no copy is left in flight into this CTA's shared memory when it ends: the last stages filled
+#pragma unroll 1
+      for (int j = max(odd, i - stages); j < i; j += NPR)
+        wait(&full[j % stages], (uint32_t)(j / stages) & 1u, c.status);
+    } else if (warp == kMma + 5 || warp == kMma + 6) {  // -------------------------- query rows
+      // Two warps; D / 16 lanes a row, 16 elements each; the loads of four rows a lane group are issued together.
+      // Rows past R stay as they are: their columns of S are not looked at.
+      constexpr int TPR = D / 16, RPP = 32 / TPR;
+      const int part = lane % TPR, mine = (warp - kMma - 5) * RPP + lane / TPR;
+      bool dead = false;
+      if (place >= u1) {  // no pair for this CTA
+        if (lane == 0) sh.pair[0].i1 = 0;
+        __syncwarp();
+        mbar_arrive(&sh.qfull[0]);
+      }
+      for (int p = 0, i0 = 0; place < u1; ++p) {
+        const int qb = p % C::QB;
+        const int R = min(w.sq.rows * G, N), first_pos = w.sq.len - w.sq.rows;
+        const int i1 = i0 + min(w.n - w.k, u1 - place), next = place + w.n - w.k + kPairCost;
+        const int64_t qbase = (int64_t)w.sq.start * a.ldq + (int64_t)w.h * G * a.hsq + 16 * part;
+        PairMeta<N>& m = sh.pair[qb];
+        uint8_t* qd = qbuf + qb * C::Q;
+        bool waited = p < C::QB;
+#pragma unroll 1
+        for (int r0 = mine; __any_sync(0xFFFFFFFFu, r0 < R); r0 += 8 * RPP) {
+          uint4 x[4][2];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int row = r0 + 2 * RPP * y;
-          if (!__any_sync(0xFFFFFFFFu, row < R)) break;
-          const uint32_t v[8] = {x[y][0].x, x[y][0].y, x[y][0].z, x[y][0].w, x[y][1].x, x[y][1].y, x[y][1].z, x[y][1].w};
-          float amax = 0.0f;
+          for (int y = 0; y < 4; ++y) {
+            const int row = r0 + 2 * RPP * y, i = row / G, g = row - i * G;
+            x[y][0] = x[y][1] = make_uint4(0, 0, 0, 0);
+            if (row < R) {
+              const uint4* qp = reinterpret_cast<const uint4*>(a.q + qbase + i * a.ldq + g * a.hsq);
+              x[y][0] = qp[0];
+              x[y][1] = qp[1];
+            }
+          }
+          if (!waited) {
+            if (!wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
+            waited = true;
+          }
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
+          for (int y = 0; y < 4; ++y) {
+            const int row = r0 + 2 * RPP * y;
+            if (!__any_sync(0xFFFFFFFFu, row < R)) break;
+            const uint32_t v[8] = {x[y][0].x, x[y][0].y, x[y][0].z, x[y][0].w, x[y][1].x, x[y][1].y, x[y][1].z, x[y][1].w};
+            float amax = 0.0f;
 #pragma unroll
-          for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-          // a power of two that brings the row's largest element to [128, 256)
-          const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
-          const float down = __int_as_float((127 - e2) << 23);
-          uint4 hi, lo;
-          split_query(x[y], down, &hi, &lo);
-          if (row < R) {
-            // rows of PW bytes in the swizzle of the key tiles: term, then row (N is a multiple of the swizzle's 8 rows)
-            const int panel = part / (C::PW / 16), chunk = part % (C::PW / 16);
-            const int at = panel * C::QPANEL + row * C::PW + (D == 64 ? chunk ^ ((row >> 1) & 3) : chunk ^ (row & 7)) * 16;
-            *reinterpret_cast<uint4*>(qd + at) = hi;
-            *reinterpret_cast<uint4*>(qd + at + N * C::PW) = lo;
-            if (part == 0) {
-              const int i = row / G, g = row - i * G;
-              m.rc[row] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
-              m.pos[row] = max(first_pos + i, -1);
-              m.off[row] = i * a.ldo + g * a.hso;
+            for (int e = 0; e < 8; ++e)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
+#pragma unroll
+            for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            // a power of two that brings the row's largest element to [128, 256)
+            const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
+            const float down = __int_as_float((127 - e2) << 23);
+            uint4 hi, lo;
+            split_query(x[y], down, &hi, &lo);
+            if (row < R) {
+              // rows of PW bytes in the swizzle of the key tiles: term, then row (N is a multiple of the swizzle's 8 rows)
+              const int panel = part / (C::PW / 16), chunk = part % (C::PW / 16);
+              const int at = panel * C::QPANEL + row * C::PW + (D == 64 ? chunk ^ ((row >> 1) & 3) : chunk ^ (row & 7)) * 16;
+              *reinterpret_cast<uint4*>(qd + at) = hi;
+              *reinterpret_cast<uint4*>(qd + at + N * C::PW) = lo;
+              if (part == 0) {
+                const int i = row / G, g = row - i * G;
+                m.rc[row] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
+                m.pos[row] = max(first_pos + i, -1);
+                m.off[row] = i * a.ldo + g * a.hso;
+              }
             }
           }
         }
-      }
-      if (!waited && !wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
-      if (__any_sync(0xFFFFFFFFu, dead)) break;
-      if (warp == kMma + 5 && lane == 0) {
-        m.R = R, m.n_tiles = w.n, m.first = place - w.k, m.skipped = w.k;
-        m.i0 = i0, m.i1 = i1, m.last = next >= u1;
-        m.base = (int64_t)w.sq.start * a.ldo + (int64_t)w.h * G * a.hso;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.qfull[qb]);
-      place = next;
-      i0 = i1;
-      if (place < u1) w.next_pair(a);
-    }
-  } else if (warp == kMma) {  // ---------------------------------------------------- score MMAs
-    // One thread issues them, and its instructions set the pace: descriptors are one add each, and the output
-    // MMAs have a warp of their own.
-    constexpr uint32_t kSwz = D == 64 ? 4 : 2, kHi = desc_hi(8 * C::PW, kSwz), kQk = idesc_e4m3(2 * N, 0, 0);
-    int ks = 0, g = 0, qb = -1;
-    uint32_t kpar = 0, spar = 1, qpar = 1;
-    const uint32_t k0 = desc_lo(smem_u32(ring), 16), q0 = desc_lo(smem_u32(qbuf), 16);
-    bool dead = false, last = false;
-#pragma unroll 1
-    for (int i = 0; !last && !dead; ++i) {
-      dead = !wait(&sh.kfull[ks], kpar, c.status);
-      const int after = sh.tile[i % C::METAS].after;
-      last = sh.tile[i % C::METAS].flags & 4;
-      if (after < 0) break;
-      if (!dead && after == 0) {
-        if (++qb == C::QB) qb = 0;
-        if (qb == 0) qpar ^= 1;
-        dead = !wait(&sh.qfull[qb], qpar, c.status);
-      }
-      if (!dead && i >= NG) dead = !wait(&sh.sfree[g], spar, c.status);
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      tc_fence_after();
-      if (!dead && elect()) {
-        const uint32_t ka = k0 + ks * (C::KV / 16), qa = q0 + qb * (C::Q / 16), d = tmem + g * C::SCOL;
-#pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
-          mma_e4m3<kHi, kHi, kQk>(d, ka + (panel * C::PANEL + off) / 16, qa + (panel * C::QPANEL + off) / 16, x > 0);
-        }
-        mma_commit(&sh.sfull[g]);
-        mbar_arrive(&sh.sfull[g]);  // passes the tile's description on to the softmax group
-        mma_commit(&sh.kfree[ks]);
-      }
-      __syncwarp();
-      if (++ks == C::SK) ks = 0, kpar ^= 1;
-      if (++g == NG) g = 0, spar ^= 1;
-    }
-    // every MMA has ended before the CTA's memory goes
-    if (elect()) {
-      mma_commit(&sh.ended[0]);
-      wait(&sh.ended[0], 0, c.status);
-    }
-    __syncwarp();
-  } else if (warp == kMma + 7) {  // ------------------------------------------------ output MMAs
-    // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
-    // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
-    // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
-    constexpr uint32_t kHi = desc_hi(8 * C::PW, D == 64 ? 4 : 2), kPHi = desc_hi(kTile * 16, 0);
-    constexpr uint32_t kPv = idesc_e4m3(3 * N, 1, 1);
-    int vs = 0, g = 0;
-    uint32_t vpar = 0, ppar = 0;
-    const uint32_t v0 = desc_lo(smem_u32(vring), C::PANEL), p0 = desc_lo(smem_u32(pbuf), 128);
-    bool dead = false, last = false;
-#pragma unroll 1
-    for (int i = 0; !last && !dead; ++i) {
-      dead = !wait(&sh.vfull[vs], vpar, c.status);
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      if (dead) break;
-      const ValueMeta m = sh.value[i % C::METAS];
-      if (m.after < 0) break;
-      last = m.set & 4;
-      if (m.groups != 0xFF || m.rows < kTile) {  // rows without a key hold anything, NaN codes too: numbers for P = 0
-        uint8_t* vt = vring + vs * C::KV;
-#pragma unroll 1
-        for (int gr = 0; gr < 8; ++gr) {  // groups of 16 rows: from row `from` of each on
-          const int from = (m.groups >> gr & 1) ? min(max(m.rows - 16 * gr, 0), 16) : 0;
-#pragma unroll 4
-          for (int e = from * (C::PW / 16) + lane; e < C::PW; e += 32)
-#pragma unroll
-            for (int x = 0; x < C::NP; ++x)
-              *reinterpret_cast<uint4*>(vt + x * C::PANEL + (gr * C::PW + e) * 16) = make_uint4(0, 0, 0, 0);
+        if (!waited && !wait(&sh.qfree[qb], (uint32_t)(p / C::QB - 1) & 1u, c.status)) dead = true;
+        if (__any_sync(0xFFFFFFFFu, dead)) break;
+        if (warp == kMma + 5 && lane == 0) {
+          m.R = R, m.n_tiles = w.n, m.first = place - w.k, m.skipped = w.k;
+          m.i0 = i0, m.i1 = i1, m.last = next >= u1;
+          m.base = (int64_t)w.sq.start * a.ldo + (int64_t)w.h * G * a.hso;
         }
         fence_proxy_async_smem();
-        __syncwarp();
+        mbar_arrive(&sh.qfull[qb]);
+        place = next;
+        i0 = i1;
+        if (place < u1) w.next_pair(a);
       }
-      dead = !wait(&sh.pfull[g], ppar, c.status);
-      dead = __any_sync(0xFFFFFFFFu, dead);
-      tc_fence_after();
-      const uint32_t acc = m.after >= NG;  // not the group's first tile of the pair
-      if (!dead && elect()) {
-        const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + (m.set & 3) * C::OSET + g * (C::MB * C::OCOL);
+    } else if (warp == kMma) {  // ---------------------------------------------------- score MMAs
+      // One thread issues them, and its instructions set the pace: descriptors are one add each, and the output
+      // MMAs have a warp of their own.
+      constexpr uint32_t kSwz = D == 64 ? 4 : 2, kHi = desc_hi(8 * C::PW, kSwz), kQk = idesc_e4m3(2 * N, 0, 0);
+      int ks = 0, g = 0, qb = -1;
+      uint32_t kpar = 0, spar = 1, qpar = 1;
+      const uint32_t k0 = desc_lo(smem_u32(ring), 16), q0 = desc_lo(smem_u32(qbuf), 16);
+      bool dead = false, last = false;
+#pragma unroll 1
+      for (int i = 0; !last && !dead; ++i) {
+        dead = !wait(&sh.kfull[ks], kpar, c.status);
+        const int after = sh.tile[i % C::METAS].after;
+        last = sh.tile[i % C::METAS].flags & 4;
+        if (after < 0) break;
+        if (!dead && after == 0) {
+          if (++qb == C::QB) qb = 0;
+          if (qb == 0) qpar ^= 1;
+          dead = !wait(&sh.qfull[qb], qpar, c.status);
+        }
+        if (!dead && i >= NG) dead = !wait(&sh.sfree[g], spar, c.status);
+        dead = __any_sync(0xFFFFFFFFu, dead);
+        tc_fence_after();
+        if (!dead && elect()) {
+          const uint32_t ka = k0 + ks * (C::KV / 16), qa = q0 + qb * (C::Q / 16), d = tmem + g * C::SCOL;
 #pragma unroll
-        for (int mb = 0; mb < C::MB; ++mb)
-#pragma unroll
-          for (int x = 0; x < kTile / 32; ++x)
-            mma_e4m3<kHi, kPHi, kPv>(d + mb * C::OCOL, va + (mb * C::PANEL + x * 32 * C::PW) / 16, pa + x * 32, x ? 1u : acc);
-        mma_commit(&sh.pvdone[g]);
-        mma_commit(&sh.vfree[vs]);
+          for (int x = 0; x < D / 32; ++x) {
+            const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
+            mma_e4m3<kHi, kHi, kQk>(d, ka + (panel * C::PANEL + off) / 16, qa + (panel * C::QPANEL + off) / 16, x > 0);
+          }
+          mma_commit(&sh.sfull[g]);
+          mbar_arrive(&sh.sfull[g]);  // passes the tile's description on to the softmax group
+          mma_commit(&sh.kfree[ks]);
+        }
+        __syncwarp();
+        if (++ks == C::SK) ks = 0, kpar ^= 1;
+        if (++g == NG) g = 0, spar ^= 1;
+      }
+      // every MMA has ended before the CTA's memory goes
+      if (elect()) {
+        mma_commit(&sh.ended[0]);
+        wait(&sh.ended[0], 0, c.status);
       }
       __syncwarp();
-      if (++vs == C::SV) vs = 0, vpar ^= 1;
-      if (++g == NG) g = 0, ppar ^= 1;
+    } else if (warp == kMma + 7) {  // ------------------------------------------------ output MMAs
+      // A: V^T, dims contiguous: groups of 8 keys 8 * PW bytes apart; for D = 64 the upper 64 of the
+      // 128 rows are the next 8 KB (in the ring or right behind it): lanes that nobody reads.
+      // B: P^T, rows contiguous in groups of 16, no swizzle: groups of 8 keys 128 bytes apart
+      constexpr uint32_t kHi = desc_hi(8 * C::PW, D == 64 ? 4 : 2), kPHi = desc_hi(kTile * 16, 0);
+      constexpr uint32_t kPv = idesc_e4m3(3 * N, 1, 1);
+      int vs = 0, g = 0;
+      uint32_t vpar = 0, ppar = 0;
+      const uint32_t v0 = desc_lo(smem_u32(vring), C::PANEL), p0 = desc_lo(smem_u32(pbuf), 128);
+      bool dead = false, last = false;
+#pragma unroll 1
+      for (int i = 0; !last && !dead; ++i) {
+        dead = !wait(&sh.vfull[vs], vpar, c.status);
+        dead = __any_sync(0xFFFFFFFFu, dead);
+        if (dead) break;
+        const ValueMeta m = sh.value[i % C::METAS];
+        if (m.after < 0) break;
+        last = m.set & 4;
+        if (m.groups != 0xFF || m.rows < kTile) {  // rows without a key hold anything, NaN codes too: numbers for P = 0
+          uint8_t* vt = vring + vs * C::KV;
+#pragma unroll 1
+          for (int gr = 0; gr < 8; ++gr) {  // groups of 16 rows: from row `from` of each on
+            const int from = (m.groups >> gr & 1) ? min(max(m.rows - 16 * gr, 0), 16) : 0;
+#pragma unroll 4
+            for (int e = from * (C::PW / 16) + lane; e < C::PW; e += 32)
+#pragma unroll
+              for (int x = 0; x < C::NP; ++x)
+                *reinterpret_cast<uint4*>(vt + x * C::PANEL + (gr * C::PW + e) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        dead = !wait(&sh.pfull[g], ppar, c.status);
+        dead = __any_sync(0xFFFFFFFFu, dead);
+        tc_fence_after();
+        const uint32_t acc = m.after >= NG;  // not the group's first tile of the pair
+        if (!dead && elect()) {
+          const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + (m.set & 3) * C::OSET + g * (C::MB * C::OCOL);
+#pragma unroll
+          for (int mb = 0; mb < C::MB; ++mb)
+#pragma unroll
+            for (int x = 0; x < kTile / 32; ++x)
+              mma_e4m3<kHi, kPHi, kPv>(d + mb * C::OCOL, va + (mb * C::PANEL + x * 32 * C::PW) / 16, pa + x * 32, x ? 1u : acc);
+          mma_commit(&sh.pvdone[g]);
+          mma_commit(&sh.vfree[vs]);
+        }
+        __syncwarp();
+        if (++vs == C::SV) vs = 0, vpar ^= 1;
+        if (++g == NG) g = 0, ppar ^= 1;
+      }
+      if (elect()) {
+        mma_commit(&sh.ended[1]);
+        wait(&sh.ended[1], 0, c.status);
+      }
+      __syncwarp();
     }
-    if (elect()) {
-      mma_commit(&sh.ended[1]);
-      wait(&sh.ended[1], 0, c.status);
-    }
-    __syncwarp();
-  }
   } else if (u1 > u0) {  // ------------------------------------------------------------------- softmax, a key a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::RSOFT));
     const int grp = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;

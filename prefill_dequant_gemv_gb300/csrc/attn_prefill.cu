@@ -76,7 +76,6 @@ struct Shared {
 struct PrefillArgs {
   AttnArgs a;
   int splits;
-  int64_t blocks;   // upper bound of row blocks
   int* counters;    // [blocks * hkv]
   float2* part_ml;  // [blocks * hkv * splits][ROWS]
   float* part_o;    // [blocks * hkv * splits][ROWS][D]
@@ -201,387 +200,387 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
   if (warp >= kConv) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
-  if (run && warp == kMma + 1) {  // --------------------------------------------------------- tiles of codes
-    // Lane g looks after keys 16g .. of a step (g < BN / 16); page ids come two steps ahead, scales one.
-    constexpr int NG = BN / 16;
-    const int box = min(P, BN);
-    auto page_of = [&](int i) {
-      const int64_t tok = (int64_t)first_key + (int64_t)i * BN + 16 * lane;
-      return i < n && lane < NG && tok < key1 ? c.pages[(int64_t)seq * c.page_stride + (tok >> plog)] : -1;
-    };
-    int id = page_of(0), id1 = page_of(1);
-    bool dead = false;
-    int ks = 0, vs = 0, klap = 0, vlap = 0;
-    int i = 0;
-    for (; i < n; ++i) {
-      const int tok = first_key + i * BN + 16 * lane, id2 = page_of(i + 2);
-      bool ok = lane < NG && tok < key1;
-      if (ok && (id < 0 || id >= c.n_pages)) {
-        ok = false;
-        atomicExch(c.status, kStatusInvalid);
-      }
-      const int64_t tile = (int64_t)id * c.hkv + head;
-      float sk = 0.0f, sv = 0.0f;
-      if (ok) {
-        sk = c.ks[tile];
-        sv = c.vs[tile];
-      }
-      const bool lead = ok && (16 * lane) % box == 0;
-      if (klap && !wait(&sh.kfree[ks], (klap - 1) & 1, c.status)) dead = true;
-      if (__any_sync(0xFFFFFFFFu, dead)) break;
-      if (lane < NG || lane < 8) {
+    if (run && warp == kMma + 1) {  // --------------------------------------------------------- tiles of codes
+      // Lane g looks after keys 16g .. of a step (g < BN / 16); page ids come two steps ahead, scales one.
+      constexpr int NG = BN / 16;
+      const int box = min(P, BN);
+      auto page_of = [&](int i) {
+        const int64_t tok = (int64_t)first_key + (int64_t)i * BN + 16 * lane;
+        return i < n && lane < NG && tok < key1 ? c.pages[(int64_t)seq * c.page_stride + (tok >> plog)] : -1;
+      };
+      int id = page_of(0), id1 = page_of(1);
+      bool dead = false;
+      int ks = 0, vs = 0, klap = 0, vlap = 0;
+      int i = 0;
+      for (; i < n; ++i) {
+        const int tok = first_key + i * BN + 16 * lane, id2 = page_of(i + 2);
+        bool ok = lane < NG && tok < key1;
+        if (ok && (id < 0 || id >= c.n_pages)) {
+          ok = false;
+          atomicExch(c.status, kStatusInvalid);
+        }
+        const int64_t tile = (int64_t)id * c.hkv + head;
+        float sk = 0.0f, sv = 0.0f;
+        if (ok) {
+          sk = c.ks[tile];
+          sv = c.vs[tile];
+        }
+        const bool lead = ok && (16 * lane) % box == 0;
+        if (klap && !wait(&sh.kfree[ks], (klap - 1) & 1, c.status)) dead = true;
+        if (__any_sync(0xFFFFFFFFu, dead)) break;
+        if (lane < NG || lane < 8) {
+          if (lead) {
+            mbar_arrive_expect_tx(&sh.kfull[ks], box * D);
+#pragma unroll
+            for (int x = 0; x < C::NP; ++x)
+              tma_load_3d(kring + ks * C::KV + x * BN * C::PW + 16 * lane * C::PW, &kmap, x * 128, tok & (P - 1), (int)tile,
+                          &sh.kfull[ks]);
+          } else if (lane < 8) {
+            mbar_arrive(&sh.kfull[ks]);
+          }
+        }
+        if (vlap && !wait(&sh.cfree[vs], (vlap - 1) & 1, c.status)) dead = true;
+        if (__any_sync(0xFFFFFFFFu, dead)) {
+          ++i;  // this step's keys are on their way
+          break;
+        }
+        // the step's description goes with the value codes' barrier to the converters, and with the keys' to the rest
+        StepMeta& m = sh.step[i & 7];
+        const bool cut = __any_sync(0xFFFFFFFFu, lane < NG && (!ok || tok + 16 > key1));
+        if (lane < NG) {
+          m.ks[lane] = sk;
+          m.lvs[lane] = ok ? lg2(sv) : 0.0f;
+          m.ivs[lane] = ok ? rcp(sv) : 0.0f;
+        }
+        if (lane == 0) m.cut = cut;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kfull[ks]);
         if (lead) {
-          mbar_arrive_expect_tx(&sh.kfull[ks], box * D);
+          mbar_arrive_expect_tx(&sh.cfull[vs], box * D);
 #pragma unroll
           for (int x = 0; x < C::NP; ++x)
-            tma_load_3d(kring + ks * C::KV + x * BN * C::PW + 16 * lane * C::PW, &kmap, x * 128, tok & (P - 1), (int)tile,
-                        &sh.kfull[ks]);
+            tma_load_3d(cring + vs * C::KV + x * BN * C::PW + 16 * lane * C::PW, &vmap, x * 128, tok & (P - 1), (int)tile,
+                        &sh.cfull[vs]);
         } else if (lane < 8) {
-          mbar_arrive(&sh.kfull[ks]);
+          mbar_arrive(&sh.cfull[vs]);
+        }
+        __syncwarp();
+        id = id1;
+        id1 = id2;
+        if (++ks == C::KS) ks = 0, ++klap;
+        if (++vs == C::VS) vs = 0, ++vlap;
+      }
+      // no copy is left in flight into this CTA's shared memory when it ends
+      if (!dead) {
+        for (int j = max(0, i - C::KS); j < i; ++j) wait(&sh.kfull[j % C::KS], (uint32_t)(j / C::KS) & 1u, c.status);
+        for (int j = max(0, i - C::VS); j < i; ++j) wait(&sh.cfull[j % C::VS], (uint32_t)(j / C::VS) & 1u, c.status);
+      } else {
+        const unsigned long long t0 = global_ns();  // a pipeline that gave up: any copy has landed long before
+        while (global_ns() - t0 < 1000000ull) {
         }
       }
-      if (vlap && !wait(&sh.cfree[vs], (vlap - 1) & 1, c.status)) dead = true;
-      if (__any_sync(0xFFFFFFFFu, dead)) {
-        ++i;  // this step's keys are on their way
-        break;
-      }
-      // the step's description goes with the value codes' barrier to the converters, and with the keys' to the rest
-      StepMeta& m = sh.step[i & 7];
-      const bool cut = __any_sync(0xFFFFFFFFu, lane < NG && (!ok || tok + 16 > key1));
-      if (lane < NG) {
-        m.ks[lane] = sk;
-        m.lvs[lane] = ok ? lg2(sv) : 0.0f;
-        m.ivs[lane] = ok ? rcp(sv) : 0.0f;
-      }
-      if (lane == 0) m.cut = cut;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.kfull[ks]);
-      if (lead) {
-        mbar_arrive_expect_tx(&sh.cfull[vs], box * D);
+    } else if (run && warp == kMma) {  // ------------------------------------------------------ MMAs
+      constexpr uint32_t kSwz = D == 64 ? 4 : 2, kHi = desc_hi(8 * C::PW, kSwz), kVHi = desc_hi(1024, 2);
+      constexpr uint32_t kQk = idesc_e4m3(BN, 0, 0), kPv = idesc_f16(D);
+      const uint32_t q0 = desc_lo(smem_u32(qbuf), 16), k0 = desc_lo(smem_u32(kring), 16);
+      const uint32_t v0 = desc_lo(smem_u32(vring), C::VPANEL);
+      int ks = 0, fs = 0;
+      uint32_t kpar = 0, vpar = 0;
+      auto scores = [&](int m, int sb) {
+        if (elect()) {
+          const uint32_t d = tmem + (m * C::SB + sb) * BN;
 #pragma unroll
-        for (int x = 0; x < C::NP; ++x)
-          tma_load_3d(cring + vs * C::KV + x * BN * C::PW + 16 * lane * C::PW, &vmap, x * 128, tok & (P - 1), (int)tile,
-                      &sh.cfull[vs]);
-      } else if (lane < 8) {
-        mbar_arrive(&sh.cfull[vs]);
-      }
-      __syncwarp();
-      id = id1;
-      id1 = id2;
-      if (++ks == C::KS) ks = 0, ++klap;
-      if (++vs == C::VS) vs = 0, ++vlap;
-    }
-    // no copy is left in flight into this CTA's shared memory when it ends
-    if (!dead) {
-      for (int j = max(0, i - C::KS); j < i; ++j) wait(&sh.kfull[j % C::KS], (uint32_t)(j / C::KS) & 1u, c.status);
-      for (int j = max(0, i - C::VS); j < i; ++j) wait(&sh.cfull[j % C::VS], (uint32_t)(j / C::VS) & 1u, c.status);
-    } else {
-      const unsigned long long t0 = global_ns();  // a pipeline that gave up: any copy has landed long before
-      while (global_ns() - t0 < 1000000ull) {
-      }
-    }
-  } else if (run && warp == kMma) {  // ------------------------------------------------------ MMAs
-    constexpr uint32_t kSwz = D == 64 ? 4 : 2, kHi = desc_hi(8 * C::PW, kSwz), kVHi = desc_hi(1024, 2);
-    constexpr uint32_t kQk = idesc_e4m3(BN, 0, 0), kPv = idesc_f16(D);
-    const uint32_t q0 = desc_lo(smem_u32(qbuf), 16), k0 = desc_lo(smem_u32(kring), 16);
-    const uint32_t v0 = desc_lo(smem_u32(vring), C::VPANEL);
-    int ks = 0, fs = 0;
-    uint32_t kpar = 0, vpar = 0;
-    auto scores = [&](int m, int sb) {
-      if (elect()) {
-        const uint32_t d = tmem + (m * C::SB + sb) * BN;
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+            for (int x = 0; x < D / 32; ++x) {
+              const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
+              mma_e4m3<kHi, kHi, kQk>(d, q0 + (m * C::Q + t * 128 * D + panel * 128 * C::PW + off) / 16,
+                                      k0 + (ks * C::KV + panel * BN * C::PW + off) / 16, t + x > 0);
+            }
+          mma_commit(&sh.sfull[m * C::SB + sb]);
+          mbar_arrive(&sh.sfull[m * C::SB + sb]);  // passes the step's description on
+          if (m == tiles - 1) mma_commit(&sh.kfree[ks]);
+        }
+        __syncwarp();
+      };
+      auto outputs = [&](int m, int sb, int i) {
+        if (elect()) {
+          const uint32_t p = tmem + (m * C::SB + sb) * BN, d = tmem + C::OCOL + m * D;
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
-            mma_e4m3<kHi, kHi, kQk>(d, q0 + (m * C::Q + t * 128 * D + panel * 128 * C::PW + off) / 16,
-                                    k0 + (ks * C::KV + panel * BN * C::PW + off) / 16, t + x > 0);
+          for (int x = 0; x < BN / 16; ++x)
+            mma_f16_ts<kVHi, kPv>(d, p + (x < BN / 32 ? 8 * x : BN / 2 + 8 * (x - BN / 32)), v0 + (fs * C::VF + x * 16 * 128) / 16, (i > 0) | (x > 0));
+          if (m == tiles - 1) mma_commit(&sh.vfree[fs]);
+          if (i == n - 1) mma_commit(&sh.odone[m]);
+        }
+        __syncwarp();
+      };
+      bool ok = n == 0 || (wait(&sh.qfull, 0, c.status) && wait(&sh.kfull[0], 0, c.status));
+      ok = __all_sync(0xFFFFFFFFu, ok);
+      tc_fence_after();
+      if (n > 0 && ok) {
+        for (int m = 0; m < tiles; ++m) scores(m, 0);
+        if (++ks == C::KS) ks = 0, kpar ^= 1;
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const int sb = MT == 1 ? i & 1 : 0;
+        const uint32_t ppar = (MT == 1 ? i >> 1 : i) & 1;
+        if (MT == 1) {  // the next scores go to the other buffer, whose P has been multiplied by then
+          if (i + 1 < n) {
+            ok = __all_sync(0xFFFFFFFFu, wait(&sh.kfull[ks], kpar, c.status));
+            if (!ok) break;
+            tc_fence_after();
+            scores(0, sb ^ 1);
+            if (++ks == C::KS) ks = 0, kpar ^= 1;
           }
-        mma_commit(&sh.sfull[m * C::SB + sb]);
-        mbar_arrive(&sh.sfull[m * C::SB + sb]);  // passes the step's description on
-        if (m == tiles - 1) mma_commit(&sh.kfree[ks]);
-      }
-      __syncwarp();
-    };
-    auto outputs = [&](int m, int sb, int i) {
-      if (elect()) {
-        const uint32_t p = tmem + (m * C::SB + sb) * BN, d = tmem + C::OCOL + m * D;
-#pragma unroll
-        for (int x = 0; x < BN / 16; ++x)
-          mma_f16_ts<kVHi, kPv>(d, p + (x < BN / 32 ? 8 * x : BN / 2 + 8 * (x - BN / 32)), v0 + (fs * C::VF + x * 16 * 128) / 16, (i > 0) | (x > 0));
-        if (m == tiles - 1) mma_commit(&sh.vfree[fs]);
-        if (i == n - 1) mma_commit(&sh.odone[m]);
-      }
-      __syncwarp();
-    };
-    bool ok = n == 0 || (wait(&sh.qfull, 0, c.status) && wait(&sh.kfull[0], 0, c.status));
-    ok = __all_sync(0xFFFFFFFFu, ok);
-    tc_fence_after();
-    if (n > 0 && ok) {
-      for (int m = 0; m < tiles; ++m) scores(m, 0);
-      if (++ks == C::KS) ks = 0, kpar ^= 1;
-    }
-    for (int i = 0; i < n && ok; ++i) {
-      const int sb = MT == 1 ? i & 1 : 0;
-      const uint32_t ppar = (MT == 1 ? i >> 1 : i) & 1;
-      if (MT == 1) {  // the next scores go to the other buffer, whose P has been multiplied by then
-        if (i + 1 < n) {
-          ok = __all_sync(0xFFFFFFFFu, wait(&sh.kfull[ks], kpar, c.status));
-          if (!ok) break;
-          tc_fence_after();
-          scores(0, sb ^ 1);
-          if (++ks == C::KS) ks = 0, kpar ^= 1;
-        }
-        ok = wait(&sh.vfull[fs], vpar, c.status) && wait(&sh.pfull[sb], ppar, c.status);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        outputs(0, sb, i);
-      } else {  // a row tile's P lies over its scores: multiply it, then its next scores; the other tile's softmax meanwhile
-        for (int m = 0; m < tiles && ok; ++m) {
-          ok = (m > 0 || wait(&sh.vfull[fs], vpar, c.status)) && wait(&sh.pfull[m], ppar, c.status);
-          if (ok && m == 0 && i + 1 < n) ok = wait(&sh.kfull[ks], kpar, c.status);
+          ok = wait(&sh.vfull[fs], vpar, c.status) && wait(&sh.pfull[sb], ppar, c.status);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
-          outputs(m, 0, i);
-          if (i + 1 < n) scores(m, 0);
+          outputs(0, sb, i);
+        } else {  // a row tile's P lies over its scores: multiply it, then its next scores; the other tile's softmax meanwhile
+          for (int m = 0; m < tiles && ok; ++m) {
+            ok = (m > 0 || wait(&sh.vfull[fs], vpar, c.status)) && wait(&sh.pfull[m], ppar, c.status);
+            if (ok && m == 0 && i + 1 < n) ok = wait(&sh.kfull[ks], kpar, c.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            tc_fence_after();
+            outputs(m, 0, i);
+            if (i + 1 < n) scores(m, 0);
+          }
+          if (i + 1 < n && ++ks == C::KS) ks = 0, kpar ^= 1;
         }
-        if (i + 1 < n && ++ks == C::KS) ks = 0, kpar ^= 1;
+        if (++fs == C::FS) fs = 0, vpar ^= 1;
       }
-      if (++fs == C::FS) fs = 0, vpar ^= 1;
-    }
-    // every MMA has ended before the CTA's memory goes
-    if (elect()) {
-      mma_commit(&sh.ended);
-      wait(&sh.ended, 0, c.status);
-    }
-    __syncwarp();
-  } else if (run && warp >= kConv && warp < kMma) {  // ------------------------------------ value codes -> fp16
-    // a key a thread (two threads a key where there are 64)
-    constexpr int TPK = 128 / BN, CH = D / 16 / TPK;  // chunks of 16 codes a thread
-    const int key = tid % BN, part = tid / BN;
-    bool dead = false;
-    int vs = 0, fs = 0;
-    uint32_t cpar = 0, fpar = 1;
-    for (int i = 0; i < n; ++i) {
-      if (!wait(&sh.cfull[vs], cpar, c.status)) dead = true;
-      if (i >= C::FS && !dead && !wait(&sh.vfree[fs], fpar, c.status)) dead = true;
-      if (dead) break;
-      const uint8_t* src = cring + vs * C::KV;
-      uint8_t* dst = vring + fs * C::VF;
-      // keys that nobody may see hold anything, NaN codes too: they must be numbers for P = 0
-      const bool real = first_key + i * BN + key < key1 && sh.step[i & 7].ks[key >> 4] != 0.0f;
+      // every MMA has ended before the CTA's memory goes
+      if (elect()) {
+        mma_commit(&sh.ended);
+        wait(&sh.ended, 0, c.status);
+      }
+      __syncwarp();
+    } else if (run && warp >= kConv && warp < kMma) {  // ------------------------------------ value codes -> fp16
+      // a key a thread (two threads a key where there are 64)
+      constexpr int TPK = 128 / BN, CH = D / 16 / TPK;  // chunks of 16 codes a thread
+      const int key = tid % BN, part = tid / BN;
+      bool dead = false;
+      int vs = 0, fs = 0;
+      uint32_t cpar = 0, fpar = 1;
+      for (int i = 0; i < n; ++i) {
+        if (!wait(&sh.cfull[vs], cpar, c.status)) dead = true;
+        if (i >= C::FS && !dead && !wait(&sh.vfree[fs], fpar, c.status)) dead = true;
+        if (dead) break;
+        const uint8_t* src = cring + vs * C::KV;
+        uint8_t* dst = vring + fs * C::VF;
+        // keys that nobody may see hold anything, NaN codes too: they must be numbers for P = 0
+        const bool real = first_key + i * BN + key < key1 && sh.step[i & 7].ks[key >> 4] != 0.0f;
 #pragma unroll
-      for (int x = 0; x < CH; ++x) {
-        const int ch = part * CH + x, panel = ch / (C::PW / 16), cc = ch % (C::PW / 16);
-        const int sw = D == 64 ? cc ^ ((key >> 1) & 3) : cc ^ (key & 7);
-        uint4 w = *reinterpret_cast<const uint4*>(src + panel * BN * C::PW + key * C::PW + sw * 16);
-        if (!real) w = make_uint4(0, 0, 0, 0);
-        // 16 values: two 16-byte chunks of the 64-dim panel ch / 4
-        uint8_t* row = dst + (ch / 4) * C::VPANEL + key * 128;
-        const int c0 = (ch % 4) * 2;
-        *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) =
-            make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y));
-        *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
-            make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w));
+        for (int x = 0; x < CH; ++x) {
+          const int ch = part * CH + x, panel = ch / (C::PW / 16), cc = ch % (C::PW / 16);
+          const int sw = D == 64 ? cc ^ ((key >> 1) & 3) : cc ^ (key & 7);
+          uint4 w = *reinterpret_cast<const uint4*>(src + panel * BN * C::PW + key * C::PW + sw * 16);
+          if (!real) w = make_uint4(0, 0, 0, 0);
+          // 16 values: two 16-byte chunks of the 64-dim panel ch / 4
+          uint8_t* row = dst + (ch / 4) * C::VPANEL + key * 128;
+          const int c0 = (ch % 4) * 2;
+          *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) =
+              make_uint4(codes_lo(w.x), codes_hi(w.x), codes_lo(w.y), codes_hi(w.y));
+          *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
+              make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w));
+        }
+        mbar_arrive(&sh.cfree[vs]);
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.vfull[fs]);
+        if (++vs == C::VS) vs = 0, cpar ^= 1;
+        if (++fs == C::FS) fs = 0, fpar ^= 1;
       }
-      mbar_arrive(&sh.cfree[vs]);
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.vfull[fs]);
-      if (++vs == C::VS) vs = 0, cpar ^= 1;
-      if (++fs == C::FS) fs = 0, fpar ^= 1;
     }
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::RSOFT));
-    if (run) {  // ---------------------------------------------------------------------------- softmax, a row a thread
-    const int mt = warp >> 3, half = warp >> 2 & 1, wq = warp & 3;
-    const int row = mt * 128 + tid;  // in the block
-    const bool in = row < R;
-    const int64_t r = row0 + row;
-    const int tok = in ? (int)(r / G) : 0, g = in ? (int)(r - (int64_t)tok * G) : 0;
-    const int pos = max(in ? len - rows + tok : pos1, -1);
-    const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-    if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
-      constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP, UN = PASSES < 4 ? PASSES : 4;
-      const int part = threadIdx.x % TPR;
+    if (run) {  // -------------------------------------------------------------------------- softmax, two threads a row
+      const int mt = warp >> 3, half = warp >> 2 & 1, wq = warp & 3;
+      const int row = mt * 128 + tid;  // in the block
+      const bool in = row < R;
+      const int64_t r = row0 + row;
+      const int tok = in ? (int)(r / G) : 0, g = in ? (int)(r - (int64_t)tok * G) : 0;
+      const int pos = max(in ? len - rows + tok : pos1, -1);
+      const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+      if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
+        constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP, UN = PASSES < 4 ? PASSES : 4;
+        const int part = threadIdx.x % TPR;
 #pragma unroll 1
-      for (int p0 = 0; p0 < PASSES; p0 += UN) {
-        uint4 v[UN][2];
+        for (int p0 = 0; p0 < PASSES; p0 += UN) {
+          uint4 v[UN][2];
 #pragma unroll
-        for (int y = 0; y < UN; ++y) {
-          const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
-          v[y][0] = v[y][1] = make_uint4(0, 0, 0, 0);
-          if (qr < R) {
-            const int64_t rr = row0 + qr;
-            const int qt = (int)(rr / G), qg = (int)(rr - (int64_t)qt * G);
-            const uint4* qp = reinterpret_cast<const uint4*>(a.q + (int64_t)(start + qt) * a.ldq +
-                                                             (int64_t)(head * G + qg) * a.hsq + 16 * part);
-            v[y][0] = qp[0];
-            v[y][1] = qp[1];
+          for (int y = 0; y < UN; ++y) {
+            const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
+            v[y][0] = v[y][1] = make_uint4(0, 0, 0, 0);
+            if (qr < R) {
+              const int64_t rr = row0 + qr;
+              const int qt = (int)(rr / G), qg = (int)(rr - (int64_t)qt * G);
+              const uint4* qp = reinterpret_cast<const uint4*>(a.q + (int64_t)(start + qt) * a.ldq +
+                                                               (int64_t)(head * G + qg) * a.hsq + 16 * part);
+              v[y][0] = qp[0];
+              v[y][1] = qp[1];
+            }
+          }
+#pragma unroll
+          for (int y = 0; y < UN; ++y) {
+            const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
+            const uint32_t e[8] = {v[y][0].x, v[y][0].y, v[y][0].z, v[y][0].w, v[y][1].x, v[y][1].y, v[y][1].z, v[y][1].w};
+            float amax = 0.0f;
+#pragma unroll
+            for (int z = 0; z < 8; ++z)
+              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[z] << 16)), fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
+#pragma unroll
+            for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+            // a power of two that brings the row's largest element to [128, 256)
+            const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
+            uint4 hi, lo;
+            split_query(v[y], __int_as_float((127 - e2) << 23), &hi, &lo);
+            const int panel = part / (C::PW / 16), cc = part % (C::PW / 16), sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
+            uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;
+            *reinterpret_cast<uint4*>(at) = hi;
+            *reinterpret_cast<uint4*>(at + 128 * D) = lo;
+            if (part == 0) sh.rc[qr] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
           }
         }
-#pragma unroll
-        for (int y = 0; y < UN; ++y) {
-          const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
-          const uint32_t e[8] = {v[y][0].x, v[y][0].y, v[y][0].z, v[y][0].w, v[y][1].x, v[y][1].y, v[y][1].z, v[y][1].w};
-          float amax = 0.0f;
-#pragma unroll
-          for (int z = 0; z < 8; ++z)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[z] << 16)), fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
-#pragma unroll
-          for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-          // a power of two that brings the row's largest element to [128, 256)
-          const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
-          uint4 hi, lo;
-          split_query(v[y], __int_as_float((127 - e2) << 23), &hi, &lo);
-          const int panel = part / (C::PW / 16), cc = part % (C::PW / 16), sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
-          uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;
-          *reinterpret_cast<uint4*>(at) = hi;
-          *reinterpret_cast<uint4*>(at + 128 * D) = lo;
-          if (part == 0) sh.rc[qr] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
-        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sh.qfull);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.qfull);
-    }
-    float m = -INFINITY, l = 0.0f;
-    // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
-    const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
-    bool dead = false;
-    constexpr int GH = BN / 32;  // groups of 16 keys of this thread's half
-    const uint32_t ot = tmem + lane_base + C::OCOL + mt * D + half * (D / 2);
-    for (int i = 0; i < n && mt < tiles; ++i) {
-      const int sb = MT == 1 ? i & 1 : 0, buf = mt * C::SB + sb;
-      if (!wait(&sh.sfull[buf], (MT == 1 ? i >> 1 : i) & 1, c.status)) dead = true;
-      tc_fence_after();
-      const StepMeta& sm = sh.step[i & 7];
-      const uint32_t st = tmem + lane_base + buf * BN + half * (BN / 2);
-      const int t0 = first_key + i * BN + half * (BN / 2), g0 = half * GH;
-      const bool masked = sm.cut || t0 + BN / 2 - 1 > see || t0 <= skip;
-      const float rc = sh.rc[row];
-      // this thread's scores, read once; masked ones are -inf
-      uint32_t s[GH][16];
+      float m = -INFINITY, l = 0.0f;
+      // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
+      const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
+      bool dead = false;
+      constexpr int GH = BN / 32;  // groups of 16 keys of this thread's half
+      const uint32_t ot = tmem + lane_base + C::OCOL + mt * D + half * (D / 2);
+      for (int i = 0; i < n && mt < tiles; ++i) {
+        const int sb = MT == 1 ? i & 1 : 0, buf = mt * C::SB + sb;
+        if (!wait(&sh.sfull[buf], (MT == 1 ? i >> 1 : i) & 1, c.status)) dead = true;
+        tc_fence_after();
+        const StepMeta& sm = sh.step[i & 7];
+        const uint32_t st = tmem + lane_base + buf * BN + half * (BN / 2);
+        const int t0 = first_key + i * BN + half * (BN / 2), g0 = half * GH;
+        const bool masked = sm.cut || t0 + BN / 2 - 1 > see || t0 <= skip;
+        const float rc = sh.rc[row];
+        // this thread's scores, read once; masked ones are -inf
+        uint32_t s[GH][16];
 #pragma unroll
-      for (int gr = 0; gr < GH; ++gr) tmem_ld16(st + 16 * gr, s[gr]);
+        for (int gr = 0; gr < GH; ++gr) tmem_ld16(st + 16 * gr, s[gr]);
 #pragma unroll
-      for (int gr = 0; gr < GH; ++gr) tmem_ld_wait16(s[gr]);
-      if (masked) {
-        asm volatile("" ::: "memory");  // a branch: as predicates the masks took a third of every step's time
+        for (int gr = 0; gr < GH; ++gr) tmem_ld_wait16(s[gr]);
+        if (masked) {
+          asm volatile("" ::: "memory");  // a branch: as predicates the masks took a third of every step's time
+#pragma unroll
+          for (int gr = 0; gr < GH; ++gr) {
+            const bool hidden = sm.ks[g0 + gr] == 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int t = t0 + 16 * gr + e;
+              if (t > pos || t <= pos - a.window || hidden) s[gr][e] = 0xFF800000u;
+            }
+          }
+        }
+        // the row's largest t
+        float top = -INFINITY;
 #pragma unroll
         for (int gr = 0; gr < GH; ++gr) {
-          const bool hidden = sm.ks[g0 + gr] == 0.0f;
+          float mx[4];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int t = t0 + 16 * gr + e;
-            if (t > pos || t <= pos - a.window || hidden) s[gr][e] = 0xFF800000u;
+          for (int e = 0; e < 4; ++e)
+            mx[e] = fmaxf(fmaxf(__uint_as_float(s[gr][e]), __uint_as_float(s[gr][e + 4])),
+                          fmaxf(__uint_as_float(s[gr][e + 8]), __uint_as_float(s[gr][e + 12])));
+          // (a factor above 0, so that a masked score stays -inf)
+          top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f),
+                                sm.lvs[g0 + gr]));
+        }
+        float(&other)[2][128] = sh.other[i & 1][mt];
+        other[half][tid] = top;
+        dead = any_of_pair(mt, dead);
+        if (dead) break;
+        top = fmaxf(top, other[half ^ 1][tid]);
+        const bool grow = top > m + kLazy || (m == -INFINITY && top != -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float w = grow ? ex2(m - top) : 1.0f;
+          if (grow) m = top;
+          l *= w;
+          if (i > 0) {
+            // (heads of 256: the product before may still run)
+            if (MT == 1 && !wait(&sh.vfree[(i - 1) % C::FS], (uint32_t)((i - 1) / C::FS) & 1u, c.status)) dead = true;
+            tc_fence_after();
+#pragma unroll 1
+            for (int x = 0; x < D / 2; x += 16) {
+              uint32_t o[16];
+              tmem_ld16(ot + x, o);
+              tmem_ld_wait16(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
+              tmem_st16(ot + x, o);
+            }
+            tmem_st_wait();
           }
         }
-      }
-      // the row's largest t
-      float top = -INFINITY;
+        const float ref = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-      for (int gr = 0; gr < GH; ++gr) {
-        float mx[4];
+        for (int gr = 0; gr < GH; ++gr) {
+          uint32_t p[8];
+          const float off = sm.lvs[g0 + gr] - ref, f = fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f);
+          float sum0 = 0.0f, sum1 = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mx[e] = fmaxf(fmaxf(__uint_as_float(s[gr][e]), __uint_as_float(s[gr][e + 4])),
-                        fmaxf(__uint_as_float(s[gr][e + 8]), __uint_as_float(s[gr][e + 12])));
-        // (a factor above 0, so that a masked score stays -inf)
-        top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f),
-                              sm.lvs[g0 + gr]));
+          for (int e = 0; e < 16; e += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(s[gr][e]), f, off)), p1 = ex2(fmaf(__uint_as_float(s[gr][e + 1]), f, off));
+            sum0 += p0;
+            sum1 += p1;
+            p[e / 2] = f16x2(p0, p1);
+          }
+          l = fmaf(sum0 + sum1, sm.ivs[g0 + gr], l);
+          tmem_st8(st + 8 * gr, p);  // over the scores of this half
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&sh.pfull[buf]);
       }
-      float(&other)[2][128] = sh.other[i & 1][mt];
-      other[half][tid] = top;
-      dead = any_of_pair(mt, dead);
-      if (dead) break;
-      top = fmaxf(top, other[half ^ 1][tid]);
-      const bool grow = top > m + kLazy || (m == -INFINITY && top != -INFINITY);
-      if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float w = grow ? ex2(m - top) : 1.0f;
-        if (grow) m = top;
-        l *= w;
-        if (i > 0) {
-          // (heads of 256: the product before may still run)
-          if (MT == 1 && !wait(&sh.vfree[(i - 1) % C::FS], (uint32_t)((i - 1) / C::FS) & 1u, c.status)) dead = true;
-          tc_fence_after();
+      if (n > 0 && mt < tiles && !dead && !wait(&sh.odone[mt], 0, c.status)) dead = true;
+      if (mt < tiles) {
+        float(&other)[2][128] = sh.other[n & 1][mt];
+        other[half][tid] = l;
+        dead = any_of_pair(mt, dead);
+        l += other[half ^ 1][tid];
+        tc_fence_after();
+      }
+      if (!dead && mt < tiles) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t part = blockIdx.x;  // of (block, head), split by split
+        uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
 #pragma unroll 1
-          for (int x = 0; x < D / 2; x += 16) {
-            uint32_t o[16];
+        for (int x = 0; x < D / 2; x += 16) {
+          uint32_t o[16];
+          if (n > 0) {
             tmem_ld16(ot + x, o);
             tmem_ld_wait16(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
-            tmem_st16(ot + x, o);
-          }
-          tmem_st_wait();
-        }
-      }
-      const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-      for (int gr = 0; gr < GH; ++gr) {
-        uint32_t p[8];
-        const float off = sm.lvs[g0 + gr] - ref, f = fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f);
-        float sum0 = 0.0f, sum1 = 0.0f;
-#pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          const float p0 = ex2(fmaf(__uint_as_float(s[gr][e]), f, off)), p1 = ex2(fmaf(__uint_as_float(s[gr][e + 1]), f, off));
-          sum0 += p0;
-          sum1 += p1;
-          p[e / 2] = f16x2(p0, p1);
-        }
-        l = fmaf(sum0 + sum1, sm.ivs[g0 + gr], l);
-        tmem_st8(st + 8 * gr, p);  // over the scores of this half
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&sh.pfull[buf]);
-    }
-    if (n > 0 && mt < tiles && !dead && !wait(&sh.odone[mt], 0, c.status)) dead = true;
-    if (mt < tiles) {
-      float(&other)[2][128] = sh.other[n & 1][mt];
-      other[half][tid] = l;
-      dead = any_of_pair(mt, dead);
-      l += other[half ^ 1][tid];
-      tc_fence_after();
-    }
-    if (!dead && mt < tiles) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      const int64_t part = blockIdx.x;  // of (block, head), split by split
-      uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
-#pragma unroll 1
-      for (int x = 0; x < D / 2; x += 16) {
-        uint32_t o[16];
-        if (n > 0) {
-          tmem_ld16(ot + x, o);
-          tmem_ld_wait16(o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0u;
-        }
-        if (in) {
-          if (pa.splits == 1) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 8) {
-              uint32_t y[4];
-#pragma unroll
-              for (int z = 0; z < 4; ++z)
-                y[z] = bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
-              *reinterpret_cast<uint4*>(out + x + e) = make_uint4(y[0], y[1], y[2], y[3]);
-            }
           } else {
-            float* dst = pa.part_o + (part * C::ROWS + row) * D + half * (D / 2) + x;
 #pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 16; ++e) o[e] = 0u;
+          }
+          if (in) {
+            if (pa.splits == 1) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 8) {
+                uint32_t y[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+                  y[z] = bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
+                *reinterpret_cast<uint4*>(out + x + e) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
+            } else {
+              float* dst = pa.part_o + (part * C::ROWS + row) * D + half * (D / 2) + x;
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
           }
         }
+        if (in && half == 0 && pa.splits > 1) pa.part_ml[part * C::ROWS + row] = make_float2(m, l);
       }
-      if (in && half == 0 && pa.splits > 1) pa.part_ml[part * C::ROWS + row] = make_float2(m, l);
-    }
-    tc_fence_before();
+      tc_fence_before();
     }
   }
   __syncthreads();
@@ -642,7 +641,6 @@ int launch(const AttnArgs& a, const PrefillPlan& p, void* ws, cudaStream_t s) {
   PrefillArgs pa;
   pa.a = a;
   pa.splits = p.splits;
-  pa.blocks = p.blocks;
   uint8_t* w = static_cast<uint8_t*>(ws);
   pa.counters = reinterpret_cast<int*>(w + kWsHeader);
   pa.part_ml = reinterpret_cast<float2*>(w + p.off_ml);
