@@ -434,9 +434,13 @@ size_t qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  *   t in max(0, p - window + 1) .. p,  p the position of row i, G = n_q_heads / n_kv_heads.
  * window 0: no window.  A row that sees no key (p < 0, or lens 0) is zero.  scale is finite and > 0.
  * q and out: bf16, strides as in qkv_append; rows of no sequence are left as they are.
- * Keys beyond the position, whatever their bits, do not enter.  G is at most 128.
- * The workspace must be zero-filled before its first use; every call leaves it ready for
- * the next, and calls that overlap on the GPU must not share it.  Deterministic. */
+ * Keys that a row does not see, whatever their bits, do not enter it, and neither do tokens of a page whose key
+ * scale is 0.  NaN codes that it sees, and NaN or infinite queries, give NaN as the formula does.  Scores are
+ * fp32 numbers: |scale * q . k| below 2^120.  G is at most 128.
+ * The workspace must be zero-filled before its first use; every qattn call, of any sizes that it has room for,
+ * leaves it ready for the next one; calls that overlap on the GPU must not share it, and no other
+ * entry point may use it in between.  QG_ERR_UNSUPPORTED where a call's work passes 32-bit counts
+ * (some 2^27 row blocks, or 2^31 tiles of 128 keys over all sequences and KV heads).  Deterministic. */
 qg_status qattn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int n_q_heads,
                 const void* q, int64_t ldq, int64_t hsq, float scale, int64_t window,
                 void* out, int64_t ldo, int64_t hso, void* workspace, size_t workspace_bytes, void* stream);

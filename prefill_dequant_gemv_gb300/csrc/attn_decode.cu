@@ -92,13 +92,15 @@ struct TileMeta {
 };
 struct ValueMeta {
   int after, rows, groups, set;  // as above; rows before the sequence's end; bits of the groups that hold keys; its O, 4: last
+  int all0, all1;                // every row of the pair sees the keys all0 .. all1 - 1 of the tile
 };
 // What a query buffer holds besides the rows.
 template <int N>
 struct PairMeta {
   int R, n_tiles, i0, i1;       // rows, tiles, and which of this CTA's tiles they are
   int first, skipped;           // its first tile's place on the line, and how many tiles of it earlier CTAs have
-  int last, pad;                // the CTA's last pair
+  int last, head;               // whether it is the CTA's last pair; its KV head
+  const int32_t* pages;
   int64_t base;                 // its first row's output
   alignas(16) float rc[N];      // the row's power of two * scale * log2(e)
   int pos[N];
@@ -118,6 +120,7 @@ struct Shared {
   uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
   uint64_t summed[C::OB], joined[C::OB], ended[2], joinbar;
   uint32_t tmem;
+  int poison;     // a NaN value code was dropped
   int joins;      // pairs whose parts this CTA has to join in the end, at most two
   int join[2][4];  // rows, first CTA, parts, whether the first part is its CTA's first pair
   int64_t join_base[2];
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   if (most <= 2 * NG + kPairCost && c.n_seqs <= 32 && c.n_seqs * c.hkv <= (int)gridDim.x) w.pair_of(a, cta, lane, &u0, &u1);
   int place = u1;  // of this CTA's first tile
   if (warp > kMma && warp < kMma + 7) place = w.find(a, u0, u1, lane);
-  if (threadIdx.x == 0) sh.joins = 0;
+  if (threadIdx.x == 0) sh.joins = sh.poison = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       uint64_t* free_ = keys ? sh.kfree : sh.vfree;
       const CUtensorMap* map = keys ? &kmap : &vmap;
       const int P = 1 << c.page_log2, box = min(P, kTile);
-      int tok0 = 0, len = 0, head = 0, after = 0, id = -1, flags = 0, ready = 0, set = 0, pairs = 0, in_pair = 0;
+      int tok0 = 0, len = 0, head = 0, after = 0, id = -1, flags = 0, ready = 0, set = 0, pairs = 0, in_pair = 0, all0 = 0, all1 = 0;
       bool dead = false, done = place >= u1;
       int s = odd, i = odd, lap = 0;
       if (done && keys && odd == 0) {  // no tile for this CTA
@@ -413,6 +416,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
       }
       do {
         const int ctok0 = tok0, clen = len, chead = head, cafter = after, cid = id, cflags = flags, cready = ready, cset = set;
+        const int call0 = all0, call1 = all1;
         // the next four tiles (the first time, the first four)
         int b = w.b;
         len = 0;
@@ -421,7 +425,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           const int k = w.k + q, at = place + q + 1;
           b = w.b, head = w.h, len = w.sq.len, tok0 = w.lo + k * kTile, after = in_pair + q, set = pairs % C::OB;
           // the rows stand at len - rows .. len - 1
-          flags = tok0 + kTile - 1 > len - w.sq.rows || tok0 <= len - 1 - a.window ? 2 : 0;
+          all0 = min(max(max(len - a.window, 0) - tok0, 0), kTile);
+          all1 = min(max(len - w.sq.rows + 1 - tok0, 0), kTile);
+          flags = all0 > 0 || all1 < kTile ? 2 : 0;
           if (at >= u1 || (k == w.n - 1 && at + kPairCost >= u1)) flags |= 4;
         };
         auto walk = [&](int q) {
@@ -478,6 +484,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
               if (gl == 0) {
                 ValueMeta& vm = sh.value[i % C::METAS];
                 vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu), vm.set = cset | (cflags & 4);
+                vm.all0 = call0, vm.all1 = call1;
               }
             }
             if (ok && (16 * gl) % box == 0) {
@@ -555,9 +562,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
             // a power of two that brings the row's largest element to [128, 256)
             const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
-            const float down = __int_as_float((127 - e2) << 23);
             uint4 hi, lo;
-            split_query(x[y], down, &hi, &lo);
+            split_query(x[y], query_down(amax, e2), &hi, &lo);
             if (row < R) {
               // rows of PW bytes in the swizzle of the key tiles: term, then row (N is a multiple of the swizzle's 8 rows)
               const int panel = part / (C::PW / 16), chunk = part % (C::PW / 16);
@@ -578,6 +584,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         if (warp == kMma + 5 && lane == 0) {
           m.R = R, m.n_tiles = w.n, m.first = place - w.k, m.skipped = w.k;
           m.i0 = i0, m.i1 = i1, m.last = next >= u1;
+          m.head = w.h, m.pages = c.pages + (int64_t)w.b * c.page_stride;
           m.base = (int64_t)w.sq.start * a.ldo + (int64_t)w.h * G * a.hso;
         }
         fence_proxy_async_smem();
@@ -647,8 +654,22 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         const ValueMeta m = sh.value[i % C::METAS];
         if (m.after < 0) break;
         last = m.set & 4;
-        if (m.groups != 0xFF || m.rows < kTile) {  // rows without a key hold anything, NaN codes too: numbers for P = 0
+        // rows without a key hold anything, NaN codes too: numbers for P = 0
+        if (m.groups != 0xFF || m.rows < kTile || m.all0 > 0 || m.all1 < kTile) {
           uint8_t* vt = vring + vs * C::KV;
+          bool found = false;
+#pragma unroll 1
+          for (int side = 0; side < 2; ++side) {  // keys before and behind those that every row sees
+#pragma unroll 1
+            for (int e = (side ? m.all1 * (C::PW / 16) : 0) + lane; e < (side ? m.rows : m.all0) * (C::PW / 16); e += 32)
+#pragma unroll
+              for (int x = 0; x < C::NP; ++x) {
+                uint4* at = reinterpret_cast<uint4*>(vt + x * C::PANEL + e * 16);
+                *at = drop_nans(*at, &found);
+              }
+          }
+          if (found) sh.poison = 1;
+          __syncwarp();
 #pragma unroll 1
           for (int gr = 0; gr < 8; ++gr) {  // groups of 16 rows: from row `from` of each on
             const int from = (m.groups >> gr & 1) ? min(max(m.rows - 16 * gr, 0), 16) : 0;
@@ -816,8 +837,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
               float pr[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                // a row that has seen no key has no reference: -inf - -inf is no weight
-                pr[e] = rfs[e] == -INFINITY || r + q + e >= R ? 0.0f : ex2(x[r + q + e] - rfs[e] + kBias);
+                // a row that has seen no key has no reference: -inf - -inf is no weight (and a NaN stays one)
+                pr[e] = r + q + e >= R ? 0.0f : ex2(x[r + q + e] - (rfs[e] == -INFINITY ? 0.0f : rfs[e]) + kBias);
                 l[r + q + e] = fmaf(pr[e], ivs, l[r + q + e]);
               }
 #pragma unroll
@@ -862,7 +883,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           float v = lp[r * 64 + lane] + lp[r * 64 + 32 + lane];
 #pragma unroll
           for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-          if (lane == 0) sh.sum[set][grp][r] = v;
+          if (lane == 0) {
+            sh.sum[set][grp][r] = v;
+            if (v != v) ref[r] = INFINITY;  // a NaN outweighs the other groups and parts
+          }
         }
         any_of(grp, false);
       }
@@ -926,6 +950,13 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             }
           }
           if (d < D) {
+            if (sh.poison) {
+              const int last = pm.pos[R - 1], all0 = last - a.window + 1;
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                if (r + z < R && nan_dims(c, pm.pages, pm.head, D, d & ~15, pm.pos[r + z], a.window, all0, pm.pos[0]) >> (d & 15) & 1)
+                  o[z] = __int_as_float(0x7FFFFFFF);
+            }
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
               if (r + z < R) {

@@ -70,7 +70,7 @@ struct Shared {
   uint64_t qfull, sfull[C::MT * C::SB], pfull[C::MT * C::SB], odone[C::MT], ended;
   uint32_t tmem;
   int work[8];
-  int ticket;
+  int ticket, poison;  // poison: a NaN value code was dropped
 };
 
 struct PrefillArgs {
@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     for (int i = 0; i < MT; ++i) mbar_init(&sh.odone[i], 1);
     mbar_init(&sh.qfull, C::SOFT);
     mbar_init(&sh.ended, 1);
+    sh.poison = 0;
     fence_mbar_init();
   }
   if (warp == kMma) {
@@ -371,7 +372,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const uint8_t* src = cring + vs * C::KV;
         uint8_t* dst = vring + fs * C::VF;
         // keys that nobody may see hold anything, NaN codes too: they must be numbers for P = 0
-        const bool real = first_key + i * BN + key < key1 && sh.step[i & 7].ks[key >> 4] != 0.0f;
+        const int t = first_key + i * BN + key;
+        const bool real = t < key1 && sh.step[i & 7].ks[key >> 4] != 0.0f;
+        if (__any_sync(0xFFFFFFFFu, t > pos0 || t <= max(pos1, -1) - a.window)) {  // keys that not all rows see
+          bool found = false;
+#pragma unroll 1
+          for (int ch = part * CH; ch < (part + 1) * CH; ++ch) {
+            uint4* at = reinterpret_cast<uint4*>(cring + vs * C::KV + ch / (C::PW / 16) * BN * C::PW + key * C::PW +
+                                                 (D == 64 ? ch % 4 ^ ((key >> 1) & 3) : ch % 8 ^ (key & 7)) * 16);
+            if (t > pos0 || t <= max(pos1, -1) - a.window) *at = drop_nans(*at, &found);
+          }
+          if (found) sh.poison = 1;
+          fence_proxy_async_smem();  // the next copy into this place comes after these writes
+        }
 #pragma unroll
         for (int x = 0; x < CH; ++x) {
           const int ch = part * CH + x, panel = ch / (C::PW / 16), cc = ch % (C::PW / 16);
@@ -435,7 +448,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             // a power of two that brings the row's largest element to [128, 256)
             const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
             uint4 hi, lo;
-            split_query(v[y], __int_as_float((127 - e2) << 23), &hi, &lo);
+            split_query(v[y], query_down(amax, e2), &hi, &lo);
             const int panel = part / (C::PW / 16), cc = part % (C::PW / 16), sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
             uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;
             *reinterpret_cast<uint4*>(at) = hi;
@@ -549,6 +562,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (!dead && mt < tiles) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t part = blockIdx.x;  // of (block, head), split by split
+        const bool poison = sh.poison;
         uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
 #pragma unroll 1
         for (int x = 0; x < D / 2; x += 16) {
@@ -559,6 +573,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           } else {
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = 0u;
+          }
+          if (poison && in) {
+            const uint32_t nans = nan_dims(c, c.pages + (int64_t)seq * c.page_stride, head, D, half * (D / 2) + x, pos, a.window,
+                                           max(pos1, -1) - a.window + 1, pos0);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (nans >> e & 1) o[e] = 0x7FFFFFFFu;
           }
           if (in) {
             if (pa.splits == 1) {

@@ -132,6 +132,47 @@ __device__ __forceinline__ void split_query(const uint4 (&x)[2], float down, uin
   *hi = make_uint4(h[0], h[1], h[2], h[3]);
   *lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
+// What brings a query row's largest element, amax < 2^(e2 + 8), to [128, 256).  An infinity makes every score of its row
+// NaN (it meets a 0, or infinities of both signs, or none but equal ones), so the whole row becomes NaN here.
+__device__ __forceinline__ float query_down(float amax, int e2) {
+  return amax == INFINITY ? __int_as_float(0x7FFFFFFF) : __int_as_float((127 - e2) << 23);
+}
+
+// A NaN value code enters the output product of all rows, even times a weight of 0.  Where every row sees the key that is
+// right; the codes of keys that only some rows see (behind the first row's position, before the last row's
+// window) are looked at, a NaN becomes 0, and rows that do see it get their NaN in the end, from the cache.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {  // bit 7 of each byte that is 0x7F or 0xFF
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+__device__ __forceinline__ uint4 drop_nans(uint4 w, bool* found) {
+  const uint32_t n[4] = {nan_bytes(w.x), nan_bytes(w.y), nan_bytes(w.z), nan_bytes(w.w)};
+  if (n[0] | n[1] | n[2] | n[3]) *found = true;
+  return make_uint4(w.x & ~((n[0] >> 7) * 255u), w.y & ~((n[1] >> 7) * 255u), w.z & ~((n[2] >> 7) * 255u),
+                    w.w & ~((n[3] >> 7) * 255u));
+}
+// Bits of the 16 dims from d on (a multiple of 16) that are NaN in some key that the row at `pos` sees and not all rows do: all
+// see the keys all0 .. all1.
+static __device__ __noinline__ uint32_t nan_dims(const KvArgs& c, const int32_t* pages, int head, int head_dim, int d, int pos,
+                                                 int window, int all0, int all1) {
+  uint32_t bits = 0;
+#pragma unroll 1
+  for (int64_t t = max(pos - window + 1, 0); t <= pos; ++t) {
+    if (t >= all0 && t <= all1) {
+      t = all1;
+      continue;
+    }
+    const int id = pages[t >> c.page_log2];
+    if (id < 0 || id >= c.n_pages) continue;
+    const int64_t tile = (int64_t)id * c.hkv + head, row = (tile << c.page_log2) + (t & ((1 << c.page_log2) - 1));
+    if (c.ks[tile] == 0.0f) continue;
+    const uint4 w = *reinterpret_cast<const uint4*>(c.v + row * head_dim + d);
+    const uint32_t n[4] = {nan_bytes(w.x), nan_bytes(w.y), nan_bytes(w.z), nan_bytes(w.w)};
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      bits |= ((n[x] >> 7 & 1) | (n[x] >> 14 & 2) | (n[x] >> 21 & 4) | (n[x] >> 28 & 8)) << (4 * x);
+  }
+  return bits;
+}
 // Two codes of a word (its low or high half) -> two fp16 values.
 __device__ __forceinline__ uint32_t codes_lo(uint32_t w) { return codes_f16x2((uint16_t)w); }
 __device__ __forceinline__ uint32_t codes_hi(uint32_t w) { return codes_f16x2((uint16_t)(w >> 16)); }

@@ -424,3 +424,55 @@ def test_prompt_then_decode_on_another_stream():
     for (qn, out, *state), n, l in zip(steps, (70, 1, 1, 1), (70, 71, 72, 73)):
         kc, ks, vc, vs = (a.view(torch.uint8).cpu().numpy() if a.dtype != torch.float32 else a.cpu().numpy() for a in state)
         check_attention(out, oa.attention(to_f64(qn), [n], [l], c.pages, page, kc, ks, vc, vs, d ** -0.5), d, 73)
+
+
+NAN_SHAPES = [  # d, page, hkv, hq, news, lens, window: few rows a KV head, then row blocks, whole and cut along the keys
+    (128, 16, 2, 6, [4, 1, 3], [300, 90, 5], 0), (64, 32, 2, 8, [2, 1], [150, 400], 40), (256, 64, 1, 4, [5, 1], [200, 77], 33),
+    (128, 64, 2, 4, [3], [6000], 0), (256, 16, 2, 6, [1], [700], 300),
+    (64, 16, 2, 4, [150, 90], [400, 90], 0), (128, 32, 2, 8, [70, 100], [300, 101], 37), (256, 64, 1, 2, [130], [333], 50),
+    (128, 64, 1, 4, [100], [5000], 0)]
+
+
+@pytest.mark.parametrize("d,page,hkv,hq,news,lens,window", NAN_SHAPES)
+def test_nan_values_reach_only_rows_that_see_them(d, page, hkv, hq, news, lens, window):
+    q = qlib()
+    c = Case(d + sum(lens), news, lens, page, hkv, d)
+    qh = c.heads(hq)
+    clean = c.attention(qh, d ** -0.5, window)
+    for b, (t, length) in enumerate(zip(news, lens)):
+        for at in {length - 1, length - t + t // 2, length - t, max(0, length - window - 2 * (t // 3)) if window else length // 2}:
+            pg, h = c.pages[b, at // page], int(c.rng.integers(hkv))
+            c.vc[pg, h, at % page, c.rng.integers(0, d, 3)] = c.rng.choice([0x7F, 0xFF], 3)
+    nan = np.isnan(c.attention(qh, d ** -0.5, window)[0])
+    assert nan.any() and not nan.all()
+    cache, batch = c.device(q)
+    got = to_f64(q.attention(cache, batch, qh.cuda(), window=window))
+    assert np.array_equal(np.isnan(got), nan)
+    # (the other dims' exact values are those without the NaN codes)
+    check_attention(torch.from_numpy(np.where(nan, clean[0], got)), clean, d, max(lens))
+
+
+@pytest.mark.parametrize("d,page,hkv,hq,news,lens,window", NAN_SHAPES)
+def test_nan_scores_stay_in_their_rows(d, page, hkv, hq, news, lens, window):
+    """NaN key codes, and query rows with a NaN or an infinity: NaN where the formula has it, nowhere else."""
+    q = qlib()
+    c = Case(d + sum(lens) + 1, news, lens, page, hkv, d)
+    qh = c.heads(hq)
+    clean = c.attention(qh, d ** -0.5, window)
+    row = 0
+    for b, (t, length) in enumerate(zip(news, lens)):
+        if t > 1:
+            at = length - t + t // 2
+            c.kc[c.pages[b, at // page], 0, at % page, int(c.rng.integers(d))] = 0x7F
+            qh[row, hq - 1, int(c.rng.integers(d))] = float("inf")
+        elif window == 0 or length > window:
+            qh[row, 0, 1] = float("nan")
+            qh[row, hq - 1, 3] = float("-inf")
+        row += t
+    with np.errstate(invalid="ignore"):
+        nan = np.isnan(c.attention(qh, d ** -0.5, window)[0])
+    assert nan.any() and not nan.all()
+    cache, batch = c.device(q)
+    got = to_f64(q.attention(cache, batch, qh.cuda(), window=window))
+    assert np.array_equal(np.isnan(got), nan)
+    check_attention(torch.from_numpy(np.where(nan, clean[0], got)), clean, d, max(lens))
