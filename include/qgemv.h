@@ -440,7 +440,7 @@ size_t qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  * The workspace must be zero-filled before its first use; every qattn call, of any sizes that it has room for,
  * leaves it ready for the next one; calls that overlap on the GPU must not share it, and no other
  * entry point may use it in between.  QG_ERR_UNSUPPORTED where a call's work passes 32-bit counts
- * (some 2^27 row blocks, or 2^31 tiles of 128 keys over all sequences and KV heads).  Deterministic. */
+ * (2^26 row blocks, or 2^31 tiles of 128 keys over all sequences and KV heads).  Deterministic. */
 qg_status qattn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int n_q_heads,
                 const void* q, int64_t ldq, int64_t hsq, float scale, int64_t window,
                 void* out, int64_t ldo, int64_t hso, void* workspace, size_t workspace_bytes, void* stream);
