@@ -475,11 +475,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         const bool masked = sm.cut || t0 + BN / 2 - 1 > see || t0 <= skip;
         const float rc = sh.rc[row];
         // this thread's scores, read once; masked ones are -inf
-        uint32_t s[GH][16];
-#pragma unroll
-        for (int gr = 0; gr < GH; ++gr) tmem_ld16(st + 16 * gr, s[gr]);
-#pragma unroll
-        for (int gr = 0; gr < GH; ++gr) tmem_ld_wait16(s[gr]);
+        uint32_t s[16 * GH];
+        tmem_ld_now(st, s);
         if (masked) {
           asm volatile("" ::: "memory");  // a branch: as predicates the masks took a third of every step's time
 #pragma unroll
@@ -488,7 +485,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               const int t = t0 + 16 * gr + e;
-              if (t > pos || t <= pos - a.window || hidden) s[gr][e] = 0xFF800000u;
+              if (t > pos || t <= pos - a.window || hidden) s[16 * gr + e] = 0xFF800000u;
             }
           }
         }
@@ -496,14 +493,14 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         float top = -INFINITY;
 #pragma unroll
         for (int gr = 0; gr < GH; ++gr) {
-          float mx[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            mx[e] = fmaxf(fmaxf(__uint_as_float(s[gr][e]), __uint_as_float(s[gr][e + 4])),
-                          fmaxf(__uint_as_float(s[gr][e + 8]), __uint_as_float(s[gr][e + 12])));
+          auto at = [&](int e) { return __uint_as_float(s[16 * gr + e]); };
+          float m0 = max3(at(0), at(1), at(2)), m1 = max3(at(3), at(4), at(5));
+          m0 = max3(m0, at(6), at(7));
+          m1 = max3(m1, at(8), at(9));
+          m0 = max3(m0, at(10), at(11));
+          m1 = max3(m1, at(12), at(13));
           // (a factor above 0, so that a masked score stays -inf)
-          top = fmaxf(top, fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f),
-                                sm.lvs[g0 + gr]));
+          top = fmaxf(top, fmaf(fmaxf(max3(m0, at(14), at(15)), m1), fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f), sm.lvs[g0 + gr]));
         }
         float(&other)[2][128] = sh.other[i & 1][mt];
         other[half][tid] = top;
@@ -536,14 +533,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         for (int gr = 0; gr < GH; ++gr) {
           uint32_t p[8];
           const float off = sm.lvs[g0 + gr] - ref, f = fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f);
-          float sum0 = 0.0f, sum1 = 0.0f;
+          const uint64_t ff = pack2(f, f), oo = pack2(off, off);
+          uint64_t sum = 0;
 #pragma unroll
           for (int e = 0; e < 16; e += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(s[gr][e]), f, off)), p1 = ex2(fmaf(__uint_as_float(s[gr][e + 1]), f, off));
-            sum0 += p0;
-            sum1 += p1;
+            float t0, t1;
+            unpack2(fma2(pack2(__uint_as_float(s[16 * gr + e]), __uint_as_float(s[16 * gr + e + 1])), ff, oo), &t0, &t1);
+            const float p0 = ex2(t0), p1 = ex2(t1);
+            sum = add2(sum, pack2(p0, p1));
             p[e / 2] = f16x2(p0, p1);
           }
+          float sum0, sum1;
+          unpack2(sum, &sum0, &sum1);
           l = fmaf(sum0 + sum1, sm.ivs[g0 + gr], l);
           tmem_st8(st + 8 * gr, p);  // over the scores of this half
         }
