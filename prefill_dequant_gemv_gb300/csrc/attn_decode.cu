@@ -352,8 +352,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
     if (t < C::QB) mbar_init(&sh.qfull[t], 64), mbar_init(&sh.qfree[t], 1);
     if (t < NG) {
       mbar_init(&sh.sfull[t], 2);  // the MMAs' end, and the issuing thread's own arrival
-      mbar_init(&sh.sfree[t], 128);
-      mbar_init(&sh.pfull[t], 128);
+      mbar_init(&sh.sfree[t], 4);
+      mbar_init(&sh.pfull[t], 4);
       mbar_init(&sh.pvdone[t], 1);
     }
     if (t < C::OB) mbar_init(&sh.summed[t], NG), mbar_init(&sh.joined[t], 1);
@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           }
         }
         tc_fence_before();
-        mbar_arrive(&sh.sfree[grp]);
+        warp_arrive(&sh.sfree[grp]);
         const float ks = tm.ks[tid >> 4], vs = tm.vs[tid >> 4];
         const float lvs = lg2(vs), ivs = ks == 0.0f ? 0.0f : rcp(vs);
         const int flags = tm.flags, tok = tm.tok0 + tid, most = tm.len;
@@ -861,7 +861,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         }
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&sh.pfull[grp]);
+        warp_arrive(&sh.pfull[grp]);
         ++turn;
       }
       // the pair's end here: the group's sums, then all groups' outputs by the one that had the last tile

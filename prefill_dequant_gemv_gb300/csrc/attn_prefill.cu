@@ -129,11 +129,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KS; ++i) mbar_init(&sh.kfull[i], 9), mbar_init(&sh.kfree[i], 1);
-    for (int i = 0; i < C::VS; ++i) mbar_init(&sh.cfull[i], 8), mbar_init(&sh.cfree[i], 128);
-    for (int i = 0; i < C::FS; ++i) mbar_init(&sh.vfull[i], 128), mbar_init(&sh.vfree[i], 1);
-    for (int i = 0; i < MT * C::SB; ++i) mbar_init(&sh.sfull[i], 2), mbar_init(&sh.pfull[i], 256);
+    for (int i = 0; i < C::VS; ++i) mbar_init(&sh.cfull[i], 8), mbar_init(&sh.cfree[i], 4);
+    for (int i = 0; i < C::FS; ++i) mbar_init(&sh.vfull[i], 4), mbar_init(&sh.vfree[i], 1);
+    for (int i = 0; i < MT * C::SB; ++i) mbar_init(&sh.sfull[i], 2), mbar_init(&sh.pfull[i], 8);
     for (int i = 0; i < MT; ++i) mbar_init(&sh.odone[i], 1);
-    mbar_init(&sh.qfull, C::SOFT);
+    mbar_init(&sh.qfull, C::SOFT / 32);
     mbar_init(&sh.ended, 1);
     sh.poison = 0;
     fence_mbar_init();
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       for (int i = 0; i < n; ++i) {
         if (!wait(&sh.cfull[vs], cpar, c.status)) dead = true;
         if (i >= C::FS && !dead && !wait(&sh.vfree[fs], fpar, c.status)) dead = true;
-        if (dead) break;
+        if (__any_sync(0xFFFFFFFFu, dead)) break;
         const uint8_t* src = cring + vs * C::KV;
         uint8_t* dst = vring + fs * C::VF;
         // keys that nobody may see hold anything, NaN codes too: they must be numbers for P = 0
@@ -399,9 +399,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
               make_uint4(codes_lo(w.z), codes_hi(w.z), codes_lo(w.w), codes_hi(w.w));
         }
-        mbar_arrive(&sh.cfree[vs]);
         fence_proxy_async_smem();
-        mbar_arrive(&sh.vfull[fs]);
+        warp_arrive(&sh.cfree[vs]);
+        warp_arrive(&sh.vfull[fs]);
         if (++vs == C::VS) vs = 0, cpar ^= 1;
         if (++fs == C::FS) fs = 0, fpar ^= 1;
       }
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
         }
         fence_proxy_async_smem();
-        mbar_arrive(&sh.qfull);
+        warp_arrive(&sh.qfull);
       }
       float m = -INFINITY, l = 0.0f;
       // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
@@ -550,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&sh.pfull[buf]);
+        warp_arrive(&sh.pfull[buf]);
       }
       if (n > 0 && mt < tiles && !dead && !wait(&sh.odone[mt], 0, c.status)) dead = true;
       if (mt < tiles) {

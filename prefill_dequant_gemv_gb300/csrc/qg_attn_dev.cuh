@@ -92,6 +92,11 @@ __device__ __forceinline__ bool any_of(int group, bool v) {
       : "memory");
   return r != 0;
 }
+// One arrival for a warp, behind all its lanes' work: arrivals of 32 lanes are worked off one after the other.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
 // Two fp32 operations an instruction, each rounded as the single one is.
 __device__ __forceinline__ uint64_t pack2(float x, float y) {
   uint64_t r;
