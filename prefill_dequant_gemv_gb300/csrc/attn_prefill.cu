@@ -60,6 +60,14 @@ struct StepMeta {
   float ks[8], lvs[8], ivs[8];  // scale, log2 and reciprocal of the value scale of each 16 keys; ks 0: hidden
   int cut, pad[7];              // some of its keys are hidden
 };
+// What the CTA works on.  It stays in shared memory: registers are for scores.
+struct Block {
+  int run, seq, block;          // whether there is work; the sequence, and which of its row blocks
+  int start, rows, len;         // the sequence's
+  int R, tiles;                 // rows of the block, row tiles in use
+  int pos0, pos1;               // of its first and last row
+  int n, first_key, key1;       // steps, the first one's first key; the end of the block's keys
+};
 template <int D>
 struct Shared {
   using C = Cfg<D>;
@@ -69,7 +77,9 @@ struct Shared {
   float rc[C::ROWS];              // a row's power of two * scale * log2(e)
   uint64_t qfull, sfull[C::MT * C::SB], pfull[C::MT * C::SB], odone[C::MT], ended;
   uint32_t tmem;
-  int work[8];
+  Block b;
+  int pos[C::ROWS];    // a row's position
+  int2 edge[C::ROWS / 32];  // of 32 rows: the last key that all see, the last one that some do not see any more
   int ticket, poison;  // poison: a NaN value code was dropped
 };
 
@@ -116,7 +126,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   uint8_t* cring = kring + C::KS * C::KV;
   uint8_t* vring = cring + C::VS * C::KV;
   Shared<D>& sh = *reinterpret_cast<Shared<D>*>(vring + C::FS * C::VF);
-  static_assert(sizeof(Shared<D>) <= 7168, "shared memory");
+  static_assert(sizeof(Shared<D>) <= 8192, "shared memory");
   const AttnArgs& a = pa.a;
   const KvArgs& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tid = threadIdx.x & 127;
@@ -172,42 +182,51 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (left < all) {
         const int who = __ffs(__ballot_sync(0xFFFFFFFFu, sum > left)) - 1;
         if (lane == who) {
-          sh.work[0] = base + who;
-          sh.work[1] = left - (sum - nb);
-          sh.work[2] = s.start, sh.work[3] = s.rows, sh.work[4] = s.len;
+          sh.b.seq = base + who, sh.b.block = left - (sum - nb);
+          sh.b.start = s.start, sh.b.rows = s.rows, sh.b.len = s.len;
         }
         break;
       }
       left -= all;
     }
-    if (lane == 0) sh.work[5] = ok;
+    __syncwarp();
+    if (lane == 0) {
+      Block& b = sh.b;
+      b.run = ok;
+      b.n = 0;
+      if (ok) {
+        const int64_t row0 = (int64_t)b.block * C::ROWS;
+        b.R = (int)min((int64_t)C::ROWS, (int64_t)b.rows * G - row0);
+        b.tiles = MT == 2 && b.R <= 128 ? 1 : MT;
+        // its keys: from the first one that its first row sees (a whole page) to its last row's own
+        b.pos0 = b.len - b.rows + (int)(row0 / G);
+        b.pos1 = b.len - b.rows + (int)((row0 + b.R - 1) / G);
+        const int key0 = b.pos0 >= a.window ? (b.pos0 - a.window + 1) >> c.page_log2 << c.page_log2 : 0;
+        b.key1 = max(b.pos1 + 1, 0);
+        const int steps = b.key1 > key0 ? (b.key1 - key0 + BN - 1) / BN : 0;
+        const int s0 = (int)((int64_t)steps * split / pa.splits), s1 = (int)((int64_t)steps * (split + 1) / pa.splits);
+        b.n = s1 - s0;
+        b.first_key = key0 + s0 * BN;
+      }
+    }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  const bool run = sh.work[5] != 0;
-  const int seq = sh.work[0], start = sh.work[2], rows = sh.work[3], len = sh.work[4];
-  const int64_t row0 = (int64_t)sh.work[1] * C::ROWS, all_rows = (int64_t)rows * G;
-  const int R = run ? (int)min((int64_t)C::ROWS, all_rows - row0) : 0;  // rows of this block
-  // its keys: from the first one that its first row sees (a whole page) to its last row's own
-  const int pos0 = len - rows + (int)(row0 / G), pos1 = run ? len - rows + (int)((row0 + R - 1) / G) : 0;
-  const int plog = c.page_log2, P = 1 << plog;
-  const int key0 = pos0 >= a.window ? (pos0 - a.window + 1) >> plog << plog : 0, key1 = max(pos1 + 1, 0);
-  const int steps_all = key1 > key0 ? (key1 - key0 + BN - 1) / BN : 0;
-  const int s0 = (int)((int64_t)steps_all * split / pa.splits), s1 = (int)((int64_t)steps_all * (split + 1) / pa.splits);
-  const int n = run ? s1 - s0 : 0, first_key = key0 + s0 * BN;
-  const int tiles = MT == 2 && R <= 128 ? 1 : MT;  // row tiles in use
+  const Block& b = sh.b;
+  const bool run = b.run != 0;
+  const int n = b.n;
 
   if (warp >= kConv) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::RREST));
     if (run && warp == kMma + 1) {  // --------------------------------------------------------- tiles of codes
       // Lane g looks after keys 16g .. of a step (g < BN / 16); page ids come two steps ahead, scales one.
       constexpr int NG = BN / 16;
-      const int box = min(P, BN);
+      const int P = 1 << c.page_log2, box = min(P, BN), seq = b.seq, first_key = b.first_key, key1 = b.key1;
       auto page_of = [&](int i) {
         const int64_t tok = (int64_t)first_key + (int64_t)i * BN + 16 * lane;
-        return i < n && lane < NG && tok < key1 ? c.pages[(int64_t)seq * c.page_stride + (tok >> plog)] : -1;
+        return i < n && lane < NG && tok < key1 ? c.pages[(int64_t)seq * c.page_stride + (tok >> c.page_log2)] : -1;
       };
       int id = page_of(0), id1 = page_of(1);
       bool dead = false;
@@ -285,6 +304,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       constexpr uint32_t kQk = idesc_e4m3(BN, 0, 0), kPv = idesc_f16(D);
       const uint32_t q0 = desc_lo(smem_u32(qbuf), 16), k0 = desc_lo(smem_u32(kring), 16);
       const uint32_t v0 = desc_lo(smem_u32(vring), C::VPANEL);
+      const int tiles = b.tiles;
       int ks = 0, fs = 0;
       uint32_t kpar = 0, vpar = 0;
       auto scores = [&](int m, int sb) {
@@ -362,6 +382,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // a key a thread (two threads a key where there are 64)
       constexpr int TPK = 128 / BN, CH = D / 16 / TPK;  // chunks of 16 codes a thread
       const int key = tid % BN, part = tid / BN;
+      const int first_key = b.first_key, key1 = b.key1, all0 = max(b.pos1, -1) - a.window + 1, all1 = b.pos0;  // (all rows see all0 .. all1)
       bool dead = false;
       int vs = 0, fs = 0;
       uint32_t cpar = 0, fpar = 1;
@@ -374,13 +395,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // keys that nobody may see hold anything, NaN codes too: they must be numbers for P = 0
         const int t = first_key + i * BN + key;
         const bool real = t < key1 && sh.step[i & 7].ks[key >> 4] != 0.0f;
-        if (__any_sync(0xFFFFFFFFu, t > pos0 || t <= max(pos1, -1) - a.window)) {  // keys that not all rows see
+        if (__any_sync(0xFFFFFFFFu, t > all1 || t < all0)) {  // keys that not all rows see
           bool found = false;
 #pragma unroll 1
           for (int ch = part * CH; ch < (part + 1) * CH; ++ch) {
             uint4* at = reinterpret_cast<uint4*>(cring + vs * C::KV + ch / (C::PW / 16) * BN * C::PW + key * C::PW +
                                                  (D == 64 ? ch % 4 ^ ((key >> 1) & 3) : ch % 8 ^ (key & 7)) * 16);
-            if (t > pos0 || t <= max(pos1, -1) - a.window) *at = drop_nans(*at, &found);
+            if (t > all1 || t < all0) *at = drop_nans(*at, &found);
           }
           if (found) sh.poison = 1;
           fence_proxy_async_smem();  // the next copy into this place comes after these writes
@@ -411,14 +432,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
     if (run) {  // -------------------------------------------------------------------------- softmax, two threads a row
       const int mt = warp >> 3, half = warp >> 2 & 1, wq = warp & 3;
       const int row = mt * 128 + tid;  // in the block
-      const bool in = row < R;
-      const int64_t r = row0 + row;
-      const int tok = in ? (int)(r / G) : 0, g = in ? (int)(r - (int64_t)tok * G) : 0;
-      const int pos = max(in ? len - rows + tok : pos1, -1);
       const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
+      if (half == 0) {
+        const int pos = max(row < b.R ? b.len - b.rows + (int)(((int64_t)b.block * C::ROWS + row) / G) : b.pos1, -1);
+        sh.pos[row] = pos;
+        // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
+        const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
+        if (lane == 0) sh.edge[4 * mt + wq] = make_int2(see, skip);
+      }
+      any_of_pair(mt, false);
       if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
         constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP, UN = PASSES < 4 ? PASSES : 4;
-        const int part = threadIdx.x % TPR;
+        const int part = threadIdx.x % TPR, R = b.R, start = b.start;
+        const int64_t row0 = (int64_t)b.block * C::ROWS;
 #pragma unroll 1
         for (int p0 = 0; p0 < PASSES; p0 += UN) {
           uint4 v[UN][2];
@@ -460,25 +486,26 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         warp_arrive(&sh.qfull);
       }
       float m = -INFINITY, l = 0.0f;
-      // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
-      const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
       bool dead = false;
       constexpr int GH = BN / 32;  // groups of 16 keys of this thread's half
       const uint32_t ot = tmem + lane_base + C::OCOL + mt * D + half * (D / 2);
-      for (int i = 0; i < n && mt < tiles; ++i) {
+      const int mine = mt < b.tiles ? n : 0;
+      for (int i = 0; i < mine; ++i) {
         const int sb = MT == 1 ? i & 1 : 0, buf = mt * C::SB + sb;
         if (!wait(&sh.sfull[buf], (MT == 1 ? i >> 1 : i) & 1, c.status)) dead = true;
         tc_fence_after();
         const StepMeta& sm = sh.step[i & 7];
         const uint32_t st = tmem + lane_base + buf * BN + half * (BN / 2);
-        const int t0 = first_key + i * BN + half * (BN / 2), g0 = half * GH;
-        const bool masked = sm.cut || t0 + BN / 2 - 1 > see || t0 <= skip;
+        const int t0 = b.first_key + i * BN + half * (BN / 2), g0 = half * GH;
+        const int2 edge = sh.edge[4 * mt + wq];
+        const bool masked = sm.cut || t0 + BN / 2 - 1 > edge.x || t0 <= edge.y;
         const float rc = sh.rc[row];
         // this thread's scores, read once; masked ones are -inf
         uint32_t s[16 * GH];
         tmem_ld_now(st, s);
         if (masked) {
           asm volatile("" ::: "memory");  // a branch: as predicates the masks took a third of every step's time
+          const int pos = sh.pos[row];
 #pragma unroll
           for (int gr = 0; gr < GH; ++gr) {
             const bool hidden = sm.ks[g0 + gr] == 0.0f;
@@ -529,42 +556,61 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
+        // two groups at a time, each of the three steps over all of them: taken element by element, every exponential's
+        // latency is waited out
 #pragma unroll
-        for (int gr = 0; gr < GH; ++gr) {
-          uint32_t p[8];
-          const float off = sm.lvs[g0 + gr] - ref, f = fmaxf(rc * sm.ks[g0 + gr], 0x1p-126f);
-          const uint64_t ff = pack2(f, f), oo = pack2(off, off);
-          uint64_t sum = 0;
+        for (int gr = 0; gr < GH; gr += 2) {
+          uint64_t t[16];
 #pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float t0, t1;
-            unpack2(fma2(pack2(__uint_as_float(s[16 * gr + e]), __uint_as_float(s[16 * gr + e + 1])), ff, oo), &t0, &t1);
-            const float p0 = ex2(t0), p1 = ex2(t1);
-            sum = add2(sum, pack2(p0, p1));
-            p[e / 2] = f16x2(p0, p1);
+          for (int e = 0; e < 16; ++e) {
+            const int x = gr + e / 8;
+            const float off = sm.lvs[g0 + x] - ref, f = fmaxf(rc * sm.ks[g0 + x], 0x1p-126f);
+            t[e] = fma2(pack2(__uint_as_float(s[16 * gr + 2 * e]), __uint_as_float(s[16 * gr + 2 * e + 1])), pack2(f, f), pack2(off, off));
           }
-          float sum0, sum1;
-          unpack2(sum, &sum0, &sum1);
-          l = fmaf(sum0 + sum1, sm.ivs[g0 + gr], l);
-          tmem_st8(st + 8 * gr, p);  // over the scores of this half
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float t0, t1;
+            unpack2(t[e], &t0, &t1);
+            t[e] = pack2(ex2(t0), ex2(t1));
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t p[8];
+            float p0, p1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              unpack2(t[8 * x + e], &p0, &p1);
+              p[e] = f16x2(p0, p1);
+            }
+            tmem_st8(st + 8 * (gr + x), p);  // over the scores of this half
+#pragma unroll
+            for (int w = 4; w; w >>= 1)
+#pragma unroll
+              for (int e = 0; e < w; ++e) t[8 * x + e] = add2(t[8 * x + e], t[8 * x + e + w]);
+            unpack2(t[8 * x], &p0, &p1);
+            l = fmaf(p0 + p1, sm.ivs[g0 + gr + x], l);
+          }
         }
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(&sh.pfull[buf]);
       }
-      if (n > 0 && mt < tiles && !dead && !wait(&sh.odone[mt], 0, c.status)) dead = true;
-      if (mt < tiles) {
+      if (mine > 0 && !dead && !wait(&sh.odone[mt], 0, c.status)) dead = true;
+      if (mt < b.tiles) {
         float(&other)[2][128] = sh.other[n & 1][mt];
         other[half][tid] = l;
         dead = any_of_pair(mt, dead);
         l += other[half ^ 1][tid];
         tc_fence_after();
       }
-      if (!dead && mt < tiles) {
+      if (!dead && mt < b.tiles) {
+        const bool in = row < b.R;
+        const int64_t r = (int64_t)b.block * C::ROWS + row;
+        const int tok = in ? (int)(r / G) : 0, g = in ? (int)(r - (int64_t)tok * G) : 0;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t part = blockIdx.x;  // of (block, head), split by split
         const bool poison = sh.poison;
-        uint16_t* out = a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
+        uint16_t* out = a.out + (int64_t)(b.start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
 #pragma unroll 1
         for (int x = 0; x < D / 2; x += 16) {
           uint32_t o[16];
@@ -576,8 +622,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             for (int e = 0; e < 16; ++e) o[e] = 0u;
           }
           if (poison && in) {
-            const uint32_t nans = nan_dims(c, c.pages + (int64_t)seq * c.page_stride, head, D, half * (D / 2) + x, pos, a.window,
-                                           max(pos1, -1) - a.window + 1, pos0);
+            const uint32_t nans = nan_dims(c, c.pages + (int64_t)b.seq * c.page_stride, head, D, half * (D / 2) + x, sh.pos[row],
+                                           a.window, max(b.pos1, -1) - a.window + 1, b.pos0);
 #pragma unroll
             for (int e = 0; e < 16; ++e)
               if (nans >> e & 1) o[e] = 0x7FFFFFFFu;
@@ -617,6 +663,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   __syncthreads();
   if (sh.ticket != pa.splits - 1) return;
   const int64_t part0 = blockIdx.x / pa.splits * pa.splits;
+  const int R = b.R, start = b.start;
+  const int64_t row0 = (int64_t)b.block * C::ROWS;
   for (int e = threadIdx.x; e < R * (D / 8); e += C::THREADS) {
     const int row = e / (D / 8), d = e % (D / 8) * 8;
     float top = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
