@@ -15,7 +15,7 @@
 //   scores   S^T[key][row]  = K[128 keys x D]   * Q^T      (A: the key tile, B: the rows, N = 2 terms x rows)
 //   outputs  O^T[dim][row] += V^T[D x 128 keys] * P^T      (A: the value tile read transposed, N = 3 terms x rows)
 // A query row over a power of two is the sum of two E4M3 terms (bf16 has 8 significant bits, a term 4
-// and a sign; exact but for elements 2^-9 below the row's largest, off by 2^-18 of it at most).  P, rounded to
+// and a sign; exact but for elements 2^-9 below the row's largest, off by 2^-16 of it at most).  P, rounded to
 // fp16's 11 bits, is the sum of three, the second and third scaled up by 2^4 and 2^8; each term has its own
 // accumulator columns, so the scaling comes out at the end.  Keys as the M dimension fill it whatever R
 // is.  Accumulation and statistics are fp32.
@@ -553,11 +553,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           for (int y = 0; y < 4; ++y) {
             const int row = r0 + 2 * RPP * y;
             if (!__any_sync(0xFFFFFFFFu, row < R)) break;
-            const uint32_t v[8] = {x[y][0].x, x[y][0].y, x[y][0].z, x[y][0].w, x[y][1].x, x[y][1].y, x[y][1].z, x[y][1].w};
-            float amax = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
+            float amax = query_max(x[y]);
 #pragma unroll
             for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
             // a power of two that brings the row's largest element to [128, 256)

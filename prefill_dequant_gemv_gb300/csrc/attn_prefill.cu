@@ -62,8 +62,8 @@ struct StepMeta {
 };
 // What the CTA works on.  It stays in shared memory: registers are for scores.
 struct Block {
-  int run, seq, block;          // whether there is work; the sequence, and which of its row blocks
-  int start, rows, len;         // the sequence's
+  int run, seq;                 // whether there is work; the sequence
+  int tok0, rem0;               // the first row's token among the call's, and its query head
   int R, tiles;                 // rows of the block, row tiles in use
   int pos0, pos1;               // of its first and last row
   int n, first_key, key1;       // steps, the first one's first key; the end of the block's keys
@@ -158,19 +158,22 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   if (warp == 0) {
     bool bad = false;
     int total = 0;
+    Seq s = {0, 0, 0};
     auto blocks_of = [&](const Seq& s) { return (int)(((int64_t)s.rows * G + C::ROWS - 1) / C::ROWS); };
     for (int base = 0; base < c.n_seqs; base += 32) {
-      int nb = 0;
-      if (base + lane < c.n_seqs) nb = blocks_of(seq_of(c, base + lane, &bad));
-      total += __reduce_add_sync(0xFFFFFFFFu, nb);
+      s = {0, 0, 0};
+      if (base + lane < c.n_seqs) s = seq_of(c, base + lane, &bad);
+      total += __reduce_add_sync(0xFFFFFFFFu, blocks_of(s));
     }
     if (bad && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
     int left = total - 1 - block;
     int ok = left >= 0;
     for (int base = 0; ok && base < c.n_seqs; base += 32) {
-      Seq s = {0, 0, 0};
       bool ignore = false;
-      if (base + lane < c.n_seqs) s = seq_of(c, base + lane, &ignore);
+      if (c.n_seqs > 32) {  // (up to 32 are here already)
+        s = {0, 0, 0};
+        if (base + lane < c.n_seqs) s = seq_of(c, base + lane, &ignore);
+      }
       const int nb = blocks_of(s);
       int sum = nb;
 #pragma unroll
@@ -182,32 +185,31 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (left < all) {
         const int who = __ffs(__ballot_sync(0xFFFFFFFFu, sum > left)) - 1;
         if (lane == who) {
-          sh.b.seq = base + who, sh.b.block = left - (sum - nb);
-          sh.b.start = s.start, sh.b.rows = s.rows, sh.b.len = s.len;
+          Block& b = sh.b;
+          const int64_t row0 = (int64_t)(left - (sum - nb)) * C::ROWS;
+          const int first = row0 >> 32 ? (int)(row0 / G) : (int)((uint32_t)row0 / (uint32_t)G);  // (64-bit division is long)
+          b.seq = base + who;
+          b.R = (int)min((int64_t)C::ROWS, (int64_t)s.rows * G - row0);
+          b.tiles = MT == 2 && b.R <= 128 ? 1 : MT;
+          b.tok0 = s.start + first;
+          b.rem0 = (int)(row0 - (int64_t)first * G);
+          // its keys: from the first one that its first row sees (a whole page) to its last row's own
+          b.pos0 = s.len - s.rows + first;
+          b.pos1 = b.pos0 + (b.rem0 + b.R - 1) / G;
+          const int key0 = b.pos0 >= a.window ? (b.pos0 - a.window + 1) >> c.page_log2 << c.page_log2 : 0;
+          b.key1 = max(b.pos1 + 1, 0);
+          const int steps = b.key1 > key0 ? (b.key1 - key0 + BN - 1) / BN : 0;
+          const int s0 = steps * split / pa.splits, s1 = steps * (split + 1) / pa.splits;  // (below 2^25 steps, 32 splits)
+          b.n = s1 - s0;
+          b.first_key = key0 + s0 * BN;
         }
         break;
       }
       left -= all;
     }
-    __syncwarp();
     if (lane == 0) {
-      Block& b = sh.b;
-      b.run = ok;
-      b.n = 0;
-      if (ok) {
-        const int64_t row0 = (int64_t)b.block * C::ROWS;
-        b.R = (int)min((int64_t)C::ROWS, (int64_t)b.rows * G - row0);
-        b.tiles = MT == 2 && b.R <= 128 ? 1 : MT;
-        // its keys: from the first one that its first row sees (a whole page) to its last row's own
-        b.pos0 = b.len - b.rows + (int)(row0 / G);
-        b.pos1 = b.len - b.rows + (int)((row0 + b.R - 1) / G);
-        const int key0 = b.pos0 >= a.window ? (b.pos0 - a.window + 1) >> c.page_log2 << c.page_log2 : 0;
-        b.key1 = max(b.pos1 + 1, 0);
-        const int steps = b.key1 > key0 ? (b.key1 - key0 + BN - 1) / BN : 0;
-        const int s0 = (int)((int64_t)steps * split / pa.splits), s1 = (int)((int64_t)steps * (split + 1) / pa.splits);
-        b.n = s1 - s0;
-        b.first_key = key0 + s0 * BN;
-      }
+      sh.b.run = ok;
+      if (!ok) sh.b.n = 0;
     }
   }
   tc_fence_before();
@@ -386,6 +388,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       bool dead = false;
       int vs = 0, fs = 0;
       uint32_t cpar = 0, fpar = 1;
+      if (n > 0 && !wait(&sh.qfull, 0, c.status)) dead = true;  // the queries have been read from the ring
       for (int i = 0; i < n; ++i) {
         if (!wait(&sh.cfull[vs], cpar, c.status)) dead = true;
         if (i >= C::FS && !dead && !wait(&sh.vfree[fs], fpar, c.status)) dead = true;
@@ -434,7 +437,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const int row = mt * 128 + tid;  // in the block
       const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
       if (half == 0) {
-        const int pos = max(row < b.R ? b.len - b.rows + (int)(((int64_t)b.block * C::ROWS + row) / G) : b.pos1, -1);
+        const int pos = max(row < b.R ? b.pos0 + (b.rem0 + row) / G : b.pos1, -1);
         sh.pos[row] = pos;
         // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
         const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
@@ -442,45 +445,38 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       any_of_pair(mt, false);
       if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
-        constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP, UN = PASSES < 4 ? PASSES : 4;
-        const int part = threadIdx.x % TPR, R = b.R, start = b.start;
-        const int64_t row0 = (int64_t)b.block * C::ROWS;
+        // They come by way of the converted values' ring, which nobody needs yet, and in a loop that is not unrolled: what
+        // runs once runs as fast as its instructions arrive (four rows at a time from registers: 4000 cycles more).
+        constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP;
+        static_assert(C::ROWS * D * 2 <= C::FS * C::VF, "queries fit");
+        const int part = threadIdx.x % TPR;
+        uint8_t* raw = vring + threadIdx.x * 32;
 #pragma unroll 1
-        for (int p0 = 0; p0 < PASSES; p0 += UN) {
-          uint4 v[UN][2];
+        for (int y = 0; y < PASSES; ++y) {
+          const int qr = y * RPP + threadIdx.x / TPR, qt = (b.rem0 + qr) / G, qg = b.rem0 + qr - qt * G;
+          const bool in = qr < b.R;
+          const uint16_t* qp = a.q + (in ? (int64_t)(b.tok0 + qt) * a.ldq + (int64_t)(head * G + qg) * a.hsq + 16 * part : 0);
+          cp_async16(raw + y * C::SOFT * 32, qp, in ? 16 : 0);
+          cp_async16(raw + y * C::SOFT * 32 + 16, qp + (in ? 8 : 0), in ? 16 : 0);
+        }
+        cp_async_wait_all();  // (a thread reads what it has copied itself)
+#pragma unroll 1
+        for (int y = 0; y < PASSES; ++y) {
+          const int qr = y * RPP + threadIdx.x / TPR;
+          const uint4* src = reinterpret_cast<const uint4*>(raw + y * C::SOFT * 32);
+          const uint4 v[2] = {src[0], src[1]};
+          float amax = query_max(v);
 #pragma unroll
-          for (int y = 0; y < UN; ++y) {
-            const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
-            v[y][0] = v[y][1] = make_uint4(0, 0, 0, 0);
-            if (qr < R) {
-              const int64_t rr = row0 + qr;
-              const int qt = (int)(rr / G), qg = (int)(rr - (int64_t)qt * G);
-              const uint4* qp = reinterpret_cast<const uint4*>(a.q + (int64_t)(start + qt) * a.ldq +
-                                                               (int64_t)(head * G + qg) * a.hsq + 16 * part);
-              v[y][0] = qp[0];
-              v[y][1] = qp[1];
-            }
-          }
-#pragma unroll
-          for (int y = 0; y < UN; ++y) {
-            const int qr = (p0 + y) * RPP + threadIdx.x / TPR;
-            const uint32_t e[8] = {v[y][0].x, v[y][0].y, v[y][0].z, v[y][0].w, v[y][1].x, v[y][1].y, v[y][1].z, v[y][1].w};
-            float amax = 0.0f;
-#pragma unroll
-            for (int z = 0; z < 8; ++z)
-              amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(e[z] << 16)), fabsf(__uint_as_float(e[z] & 0xFFFF0000u))));
-#pragma unroll
-            for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
-            // a power of two that brings the row's largest element to [128, 256)
-            const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
-            uint4 hi, lo;
-            split_query(v[y], query_down(amax, e2), &hi, &lo);
-            const int panel = part / (C::PW / 16), cc = part % (C::PW / 16), sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
-            uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;
-            *reinterpret_cast<uint4*>(at) = hi;
-            *reinterpret_cast<uint4*>(at + 128 * D) = lo;
-            if (part == 0) sh.rc[qr] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
-          }
+          for (int o = TPR / 2; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, o));
+          // a power of two that brings the row's largest element to [128, 256)
+          const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
+          uint4 hi, lo;
+          split_query(v, query_down(amax, e2), &hi, &lo);
+          const int panel = part / (C::PW / 16), cc = part % (C::PW / 16), sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
+          uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;
+          *reinterpret_cast<uint4*>(at) = hi;
+          *reinterpret_cast<uint4*>(at + 128 * D) = lo;
+          if (part == 0) sh.rc[qr] = __int_as_float((127 + e2) << 23) * (a.scale * kLog2e);
         }
         fence_proxy_async_smem();
         warp_arrive(&sh.qfull);
@@ -505,15 +501,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         tmem_ld_now(st, s);
         if (masked) {
           asm volatile("" ::: "memory");  // a branch: as predicates the masks took a third of every step's time
-          const int pos = sh.pos[row];
+          const int pos = sh.pos[row], last = pos - t0, first = max(pos - a.window + 1, 0) - t0;  // of this half, seen
 #pragma unroll
-          for (int gr = 0; gr < GH; ++gr) {
-            const bool hidden = sm.ks[g0 + gr] == 0.0f;
+          for (int w = 0; w < GH / 2; ++w) {  // 32 keys, a bit each
+            const int u = last - 32 * w, v = first - 32 * w;
+            uint32_t keep = (u < 0 ? 0u : u > 30 ? ~0u : (2u << u) - 1u) & (v > 31 ? 0u : ~0u << max(v, 0));
+            if (sm.ks[g0 + 2 * w] == 0.0f) keep &= 0xFFFF0000u;
+            if (sm.ks[g0 + 2 * w + 1] == 0.0f) keep &= 0xFFFFu;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int t = t0 + 16 * gr + e;
-              if (t > pos || t <= pos - a.window || hidden) s[16 * gr + e] = 0xFF800000u;
-            }
+            for (int e = 0; e < 32; ++e)
+              if (!(keep >> e & 1)) s[32 * w + e] = 0xFF800000u;
           }
         }
         // the row's largest t
@@ -605,12 +602,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
       if (!dead && mt < b.tiles) {
         const bool in = row < b.R;
-        const int64_t r = (int64_t)b.block * C::ROWS + row;
-        const int tok = in ? (int)(r / G) : 0, g = in ? (int)(r - (int64_t)tok * G) : 0;
+        const int tok = in ? (b.rem0 + row) / G : 0, g = in ? b.rem0 + row - tok * G : 0;
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t part = blockIdx.x;  // of (block, head), split by split
         const bool poison = sh.poison;
-        uint16_t* out = a.out + (int64_t)(b.start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
+        uint16_t* out = a.out + (int64_t)(b.tok0 + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
 #pragma unroll 1
         for (int x = 0; x < D / 2; x += 16) {
           uint32_t o[16];
@@ -663,8 +659,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   __syncthreads();
   if (sh.ticket != pa.splits - 1) return;
   const int64_t part0 = blockIdx.x / pa.splits * pa.splits;
-  const int R = b.R, start = b.start;
-  const int64_t row0 = (int64_t)b.block * C::ROWS;
+  const int R = b.R, tok0 = b.tok0, rem0 = b.rem0;
   for (int e = threadIdx.x; e < R * (D / 8); e += C::THREADS) {
     const int row = e / (D / 8), d = e % (D / 8) * 8;
     float top = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -681,9 +676,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       l = fmaf(z.y, f, l);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t r = row0 + row;
-    const int tok = (int)(r / G), g = (int)(r - (int64_t)tok * G);
-    *reinterpret_cast<uint4*>(a.out + (int64_t)(start + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + d) =
+    const int tok = (rem0 + row) / G, g = rem0 + row - tok * G;
+    *reinterpret_cast<uint4*>(a.out + (int64_t)(tok0 + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + d) =
         make_uint4(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv), bf16x2(o[4] * inv, o[5] * inv),
                    bf16x2(o[6] * inv, o[7] * inv));
   }

@@ -134,30 +134,36 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-
-// 16 bf16 values of a query row, times the power of two `down`, as two E4M3 terms whose sum they are: bf16
-// has 8 significant bits, a term 4 and a sign.  Exact but for elements 2^-9 below the row's largest.
+// 16 elements of a query row (bf16 pairs) times the power of two `down`, as two E4M3 terms.  A bf16 has 8 significant bits:
+// the first term is its upper four, cut off, the second the rest.  Exact but for elements 2^-9 below the row's largest;
+// those are off by 2^-16 of it at most (a term is rounded to a multiple of 2^-9, the largest is 2^7 at least).
+__device__ __forceinline__ uint32_t bf16x2_codes(uint32_t lo, uint32_t hi) {  // two bf16 pairs -> four codes
+  uint16_t a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(__uint_as_float(lo & 0xFFFF0000u)), "f"(__uint_as_float(lo << 16)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(__uint_as_float(hi & 0xFFFF0000u)), "f"(__uint_as_float(hi << 16)));
+  return a | (uint32_t)b << 16;
+}
 __device__ __forceinline__ void split_query(const uint4 (&x)[2], float down, uint4* hi, uint4* lo) {
   const uint32_t v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
-  uint32_t h[4], l[4];
+  const uint32_t d = __byte_perm(__float_as_uint(down), 0, 0x3232);
+  uint32_t h[8], l[8];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    uint16_t hh[2], ll[2];
-#pragma unroll
-    for (int z = 0; z < 2; ++z) {
-      const uint32_t b = v[2 * e + z];
-      // bf16's bits fit fp16 at this size but for the smallest elements
-      const uint32_t h16 = f16x2(__uint_as_float(b << 16) * down, __uint_as_float(b & 0xFFFF0000u) * down);
-      hh[z] = e4m3x2(h16);
-      uint32_t d16;
-      asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d16) : "r"(h16), "r"(codes_f16x2(hh[z])));
-      ll[z] = e4m3x2(d16);
-    }
-    h[e] = hh[0] | (uint32_t)hh[1] << 16;
-    l[e] = ll[0] | (uint32_t)ll[1] << 16;
+  for (int e = 0; e < 8; ++e) {
+    uint32_t y;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(v[e]), "r"(d));
+    h[e] = y & 0xFFF0FFF0u;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(l[e]) : "r"(y), "r"(h[e]));
   }
-  *hi = make_uint4(h[0], h[1], h[2], h[3]);
-  *lo = make_uint4(l[0], l[1], l[2], l[3]);
+  *hi = make_uint4(bf16x2_codes(h[0], h[1]), bf16x2_codes(h[2], h[3]), bf16x2_codes(h[4], h[5]), bf16x2_codes(h[6], h[7]));
+  *lo = make_uint4(bf16x2_codes(l[0], l[1]), bf16x2_codes(l[2], l[3]), bf16x2_codes(l[4], l[5]), bf16x2_codes(l[6], l[7]));
+}
+// The largest magnitude of 16 bf16 elements; NaN does not count.
+__device__ __forceinline__ float query_max(const uint4 (&x)[2]) {
+  const uint32_t v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+  uint32_t m = v[0] & 0x7FFF7FFFu;
+#pragma unroll
+  for (int e = 1; e < 8; ++e) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(v[e] & 0x7FFF7FFFu));
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
 }
 // What brings a query row's largest element, amax < 2^(e2 + 8), to [128, 256).  An infinity makes every score of its row
 // NaN (it meets a 0, or infinities of both signs, or none but equal ones), so the whole row becomes NaN here.
