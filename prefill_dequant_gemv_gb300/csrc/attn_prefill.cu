@@ -64,10 +64,14 @@ struct StepMeta {
 struct Block {
   int run, seq;                 // whether there is work; the sequence
   int tok0, rem0;               // the first row's token among the call's, and its query head
+  float inv_g;                  // 1 / G
   int R, tiles;                 // rows of the block, row tiles in use
   int pos0, pos1;               // of its first and last row
   int n, first_key, key1;       // steps, the first one's first key; the end of the block's keys
 };
+// A row's token from the block's first one on: (rem0 + row) / G.  The quotient of numbers below 2^9 and the half
+// is 2^-8 at least away from a whole number, so its rounding does no harm.
+__device__ __forceinline__ int token_of(const Block& b, int row) { return (int)(((float)(b.rem0 + row) + 0.5f) * b.inv_g); }
 template <int D>
 struct Shared {
   using C = Cfg<D>;
@@ -193,6 +197,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           b.tiles = MT == 2 && b.R <= 128 ? 1 : MT;
           b.tok0 = s.start + first;
           b.rem0 = (int)(row0 - (int64_t)first * G);
+          b.inv_g = 1.0f / (float)G;
           // its keys: from the first one that its first row sees (a whole page) to its last row's own
           b.pos0 = s.len - s.rows + first;
           b.pos1 = b.pos0 + (b.rem0 + b.R - 1) / G;
@@ -337,42 +342,31 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         __syncwarp();
       };
-      bool ok = n == 0 || (wait(&sh.qfull, 0, c.status) && wait(&sh.kfull[0], 0, c.status));
-      ok = __all_sync(0xFFFFFFFFu, ok);
-      tc_fence_after();
-      if (n > 0 && ok) {
-        for (int m = 0; m < tiles; ++m) scores(m, 0);
-        if (++ks == C::KS) ks = 0, kpar ^= 1;
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        const int sb = MT == 1 ? i & 1 : 0;
-        const uint32_t ppar = (MT == 1 ? i >> 1 : i) & 1;
+      bool ok = __all_sync(0xFFFFFFFFu, n == 0 || wait(&sh.qfull, 0, c.status));
+      // Step i's outputs and step i + 1's scores; in a turn before the first, only scores (of one tile, a copy of the loop's
+      // code would have to be fetched anew).
+      for (int i = -1; i < n && ok; ++i) {
+        const bool more = i + 1 < n;
+        if (more) ok = wait(&sh.kfull[ks], kpar, c.status);
         if (MT == 1) {  // the next scores go to the other buffer, whose P has been multiplied by then
-          if (i + 1 < n) {
-            ok = __all_sync(0xFFFFFFFFu, wait(&sh.kfull[ks], kpar, c.status));
-            if (!ok) break;
-            tc_fence_after();
-            scores(0, sb ^ 1);
-            if (++ks == C::KS) ks = 0, kpar ^= 1;
-          }
-          ok = wait(&sh.vfull[fs], vpar, c.status) && wait(&sh.pfull[sb], ppar, c.status);
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
-          outputs(0, sb, i);
-        } else {  // a row tile's P lies over its scores: multiply it, then its next scores; the other tile's softmax meanwhile
-          for (int m = 0; m < tiles && ok; ++m) {
-            ok = (m > 0 || wait(&sh.vfull[fs], vpar, c.status)) && wait(&sh.pfull[m], ppar, c.status);
-            if (ok && m == 0 && i + 1 < n) ok = wait(&sh.kfull[ks], kpar, c.status);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            outputs(m, 0, i);
-            if (i + 1 < n) scores(m, 0);
-          }
-          if (i + 1 < n && ++ks == C::KS) ks = 0, kpar ^= 1;
+          if (more) scores(0, (i + 1) & 1);
         }
-        if (++fs == C::FS) fs = 0, vpar ^= 1;
+        if (i >= 0 && ok) ok = wait(&sh.vfull[fs], vpar, c.status);
+        // of two tiles, P lies over the scores: multiply it, then the tile's next scores; the other tile's softmax meanwhile
+        for (int m = 0; m < tiles; ++m) {
+          const int sb = MT == 1 ? i & 1 : 0;
+          if (i >= 0 && ok) ok = wait(&sh.pfull[m * C::SB + sb], (uint32_t)(MT == 1 ? i >> 1 : i) & 1u, c.status);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          if (i >= 0) outputs(m, sb, i);
+          if (MT > 1 && more) scores(m, 0);
+        }
+        if (more && ++ks == C::KS) ks = 0, kpar ^= 1;
+        if (i >= 0 && ++fs == C::FS) fs = 0, vpar ^= 1;
       }
       // every MMA has ended before the CTA's memory goes
       if (elect()) {
@@ -436,14 +430,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const int mt = warp >> 3, half = warp >> 2 & 1, wq = warp & 3;
       const int row = mt * 128 + tid;  // in the block
       const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-      if (half == 0) {
-        const int pos = max(row < b.R ? b.pos0 + (b.rem0 + row) / G : b.pos1, -1);
-        sh.pos[row] = pos;
-        // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
-        const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
-        if (lane == 0) sh.edge[4 * mt + wq] = make_int2(see, skip);
-      }
-      any_of_pair(mt, false);
       if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
         // They come by way of the converted values' ring, which nobody needs yet, and in a loop that is not unrolled: what
         // runs once runs as fast as its instructions arrive (four rows at a time from registers: 4000 cycles more).
@@ -453,11 +439,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         uint8_t* raw = vring + threadIdx.x * 32;
 #pragma unroll 1
         for (int y = 0; y < PASSES; ++y) {
-          const int qr = y * RPP + threadIdx.x / TPR, qt = (b.rem0 + qr) / G, qg = b.rem0 + qr - qt * G;
+          const int qr = y * RPP + threadIdx.x / TPR, qt = token_of(b, qr), qg = b.rem0 + qr - qt * G;
           const bool in = qr < b.R;
           const uint16_t* qp = a.q + (in ? (int64_t)(b.tok0 + qt) * a.ldq + (int64_t)(head * G + qg) * a.hsq + 16 * part : 0);
           cp_async16(raw + y * C::SOFT * 32, qp, in ? 16 : 0);
           cp_async16(raw + y * C::SOFT * 32 + 16, qp + (in ? 8 : 0), in ? 16 : 0);
+        }
+        if (half == 0) {
+          const int pos = max(row < b.R ? b.pos0 + token_of(b, row) : b.pos1, -1);
+          sh.pos[row] = pos;
+          // rows ascend, so the warp's first row sees the fewest keys, its last row's window begins last
+          const int see = __shfl_sync(0xFFFFFFFFu, pos, 0), skip = __reduce_max_sync(0xFFFFFFFFu, pos) - a.window;
+          if (lane == 0) sh.edge[4 * mt + wq] = make_int2(see, skip);
         }
         cp_async_wait_all();  // (a thread reads what it has copied itself)
 #pragma unroll 1
@@ -601,46 +594,63 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         tc_fence_after();
       }
       if (!dead && mt < b.tiles) {
-        const bool in = row < b.R;
-        const int tok = in ? (b.rem0 + row) / G : 0, g = in ? b.rem0 + row - tok * G : 0;
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        // A warp's rows go by way of shared memory (the queries are done with), so that lanes side by side write one row: a
+        // 16-byte piece of a row from each lane took 9300 cycles from here to the CTA's end, this 6000 (heads of 128).
+        const bool in = row < b.R, parts = pa.splits > 1;
+        const int tok = token_of(b, row), g = b.rem0 + row - tok * G;
+        const float inv = parts ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t part = blockIdx.x;  // of (block, head), split by split
         const bool poison = sh.poison;
-        uint16_t* out = a.out + (int64_t)(b.tok0 + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2);
+        const int64_t at = parts ? ((part * C::ROWS + row) * D + half * (D / 2)) * 4
+                                 : ((int64_t)(b.tok0 + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + half * (D / 2)) * 2;
+        uint8_t* base = parts ? reinterpret_cast<uint8_t*>(pa.part_o) : reinterpret_cast<uint8_t*>(a.out);
+        constexpr int CPR = D / 16;  // pieces of a row in a warp's D * 32 bytes
+        uint8_t* stage = qbuf + mt * C::Q + (warp & 7) * (C::Q / 8);
+        auto piece = [&](int r, int k) { return reinterpret_cast<uint4*>(stage + r * D + ((k ^ (D == 64 ? r >> 1 & 3 : r & 7)) << 4)); };
+        const int dims = parts ? D / 4 : D / 2;  // in a warp's bytes at a time
 #pragma unroll 1
-        for (int x = 0; x < D / 2; x += 16) {
-          uint32_t o[16];
-          if (n > 0) {
-            tmem_ld16(ot + x, o);
-            tmem_ld_wait16(o);
-          } else {
+        for (int x0 = 0; x0 < D / 2; x0 += dims) {
+#pragma unroll 1
+          for (int x = x0; x < x0 + dims; x += 16) {
+            uint32_t o[16];
+            if (n > 0) {
+              tmem_ld16(ot + x, o);
+              tmem_ld_wait16(o);
+            } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = 0u;
-          }
-          if (poison && in) {
-            const uint32_t nans = nan_dims(c, c.pages + (int64_t)b.seq * c.page_stride, head, D, half * (D / 2) + x, sh.pos[row],
-                                           a.window, max(b.pos1, -1) - a.window + 1, b.pos0);
+              for (int e = 0; e < 16; ++e) o[e] = 0u;
+            }
+            if (poison && in) {
+              const uint32_t nans = nan_dims(c, c.pages + (int64_t)b.seq * c.page_stride, head, D, half * (D / 2) + x, sh.pos[row],
+                                             a.window, max(b.pos1, -1) - a.window + 1, b.pos0);
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (nans >> e & 1) o[e] = 0x7FFFFFFFu;
-          }
-          if (in) {
-            if (pa.splits == 1) {
+              for (int e = 0; e < 16; ++e)
+                if (nans >> e & 1) o[e] = 0x7FFFFFFFu;
+            }
+            if (parts) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 8) {
+              for (int e = 0; e < 4; ++e) *piece(lane, (x - x0) / 4 + e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
                 uint32_t y[4];
 #pragma unroll
                 for (int z = 0; z < 4; ++z)
-                  y[z] = bf16x2(__uint_as_float(o[e + 2 * z]) * inv, __uint_as_float(o[e + 2 * z + 1]) * inv);
-                *reinterpret_cast<uint4*>(out + x + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                  y[z] = bf16x2(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
+                *piece(lane, x / 8 + e) = make_uint4(y[0], y[1], y[2], y[3]);
               }
-            } else {
-              float* dst = pa.part_o + (part * C::ROWS + row) * D + half * (D / 2) + x;
-#pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
+          __syncwarp();
+          const int xb = x0 * 4;  // (0 where the outputs go out at once)
+#pragma unroll 2
+          for (int e = 0; e < CPR; ++e) {
+            const int r = e * (32 / CPR) + lane / CPR, k = lane % CPR;
+            const int64_t to = __shfl_sync(0xFFFFFFFFu, at, r) + xb + 16 * k;
+            const uint4 v = *piece(r, k);
+            if (mt * 128 + wq * 32 + r < b.R) *reinterpret_cast<uint4*>(base + to) = v;
+          }
+          __syncwarp();
         }
         if (in && half == 0 && pa.splits > 1) pa.part_ml[part * C::ROWS + row] = make_float2(m, l);
       }
@@ -659,7 +669,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   __syncthreads();
   if (sh.ticket != pa.splits - 1) return;
   const int64_t part0 = blockIdx.x / pa.splits * pa.splits;
-  const int R = b.R, tok0 = b.tok0, rem0 = b.rem0;
+  const int R = b.R, tok0 = b.tok0;
   for (int e = threadIdx.x; e < R * (D / 8); e += C::THREADS) {
     const int row = e / (D / 8), d = e % (D / 8) * 8;
     float top = -INFINITY, l = 0.0f, o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
@@ -676,7 +686,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       l = fmaf(z.y, f, l);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int tok = (rem0 + row) / G, g = rem0 + row - tok * G;
+    const int tok = token_of(b, row), g = b.rem0 + row - tok * G;
     *reinterpret_cast<uint4*>(a.out + (int64_t)(tok0 + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + d) =
         make_uint4(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv), bf16x2(o[4] * inv, o[5] * inv),
                    bf16x2(o[6] * inv, o[7] * inv));
