@@ -48,6 +48,7 @@ constexpr int kTile = 128;           // keys a tile
 constexpr int kMostCtas = 256;
 constexpr float kBias = 2.0f;        // P of a key at the reference is 2^2 ...
 constexpr float kHead = 6.5f;        // ... and at most 2^8.5, below E4M3's 448
+constexpr float kNone = -3e38f;      // the reference of a row that has seen no key: -inf would make NaN of its masked scores
 
 // D: head dimension; N: rows it is built for (16, 32, 64).
 template <int D, int N>
@@ -91,7 +92,8 @@ struct TileMeta {
   float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
 };
 struct ValueMeta {
-  int after, rows, groups, set;  // as above; rows before the sequence's end; bits of the groups that hold keys; its O, 4: last
+  int after, rows, groups, set;  // as above; rows before the sequence's end; bits of the groups that hold keys; its O, 4: last,
+                                 // 8: some of its keys are hidden from all rows or some
   int all0, all1;                // every row of the pair sees the keys all0 .. all1 - 1 of the tile
 };
 // What a query buffer holds besides the rows.
@@ -480,10 +482,12 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
               if (gl == 0) m.tok0 = ctok0, m.len = clen, m.after = cafter, m.flags = cflags | (cut ? 3 : 0);
               if (!ok) m.ks[gl] = m.vs[gl] = 0.0f;
             } else {
-              const uint32_t groups = __ballot_sync(0xFFu << (8 * q), ok) >> (8 * q);
+              const uint32_t groups = __ballot_sync(0xFFu << (8 * q), ok) >> (8 * q) & 0xFFu;
               if (gl == 0) {
                 ValueMeta& vm = sh.value[i % C::METAS];
-                vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)(groups & 0xFFu), vm.set = cset | (cflags & 4);
+                const bool cut = groups != 0xFF || clen - ctok0 < kTile || (cflags & 2);
+                vm.after = cafter, vm.rows = min(clen - ctok0, kTile), vm.groups = (int)groups;
+                vm.set = cset | (cflags & 4) | (cut ? 8 : 0);
                 vm.all0 = call0, vm.all1 = call1;
               }
             }
@@ -651,7 +655,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         if (m.after < 0) break;
         last = m.set & 4;
         // rows without a key hold anything, NaN codes too: numbers for P = 0
-        if (m.groups != 0xFF || m.rows < kTile || m.all0 > 0 || m.all1 < kTile) {
+        if (m.set & 8) {
           uint8_t* vt = vring + vs * C::KV;
           bool found = false;
 #pragma unroll 1
@@ -683,7 +687,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         tc_fence_after();
         const uint32_t acc = m.after >= NG;  // not the group's first tile of the pair
         if (!dead && elect()) {
-          const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16), d = otm + (m.set & 3) * C::OSET + g * (C::MB * C::OCOL);
+          const uint32_t va = v0 + vs * (C::KV / 16), pa = p0 + g * (C::P / 16);
+          const uint32_t d = otm + (m.set & 3) * C::OSET + g * (C::MB * C::OCOL);
 #pragma unroll
           for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
@@ -792,7 +797,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             const float* red = sh.red[grp][0];
             const float top = fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid]));
             const float old = first ? -INFINITY : ref[tid];
-            const float now = fmaxf(top, old);
+            const float now = fmaxf(fmaxf(top, old), kNone);
             ref[tid] = now;
             grow[tid] = now == old ? 1.0f : ex2(old - now);
           }
@@ -833,8 +838,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
               float pr[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                // a row that has seen no key has no reference: -inf - -inf is no weight (and a NaN stays one)
-                pr[e] = r + q + e >= R ? 0.0f : ex2(x[r + q + e] - (rfs[e] == -INFINITY ? 0.0f : rfs[e]) + kBias);
+                pr[e] = r + q + e >= R ? 0.0f : ex2(x[r + q + e] - rfs[e] + kBias);
                 l[r + q + e] = fmaf(pr[e], ivs, l[r + q + e]);
               }
 #pragma unroll
