@@ -23,12 +23,19 @@
 //   * The pairs' keys, in tiles of 128, lie on one line, which the CTAs (one an SM) share out evenly
 //     whatever the lengths; a pair cut between CTAs leaves partial (m, l, O) rows in the workspace, and the
 //     CTA that finishes last adds them in order.  One launch.
-//   * One warp copies tiles into a ring by TMA, two bring a pair's query rows, one issues the MMAs, and
-//     groups of four warps turn S into P, a key a thread: its column of R scores comes from tensor
-//     memory, its terms go to shared memory as 16-byte rows.  The sums of P stay per thread until the
+//   * One or two warps copy key tiles into a ring by TMA and as many value tiles into another, two bring a
+//     pair's query rows, two issue the MMAs (scores, outputs), and groups of four warps turn
+//     S into P, a key a thread: its column of R scores comes from tensor memory, its terms go to shared memory as 16-byte rows.  The sums of P stay per thread until the
 //     pair ends.  A tile's way through these steps is a chain of about 2500 cycles, several
 //     times what its bytes take to arrive; so several groups work on
 //     as many tiles at once, each with its own reference and accumulators, joined at the pair's end.
+//
+// Measured (GB300; bytes are the codes and scales that the rows see, queries and outputs): 64 sequences of up to
+// 8193 tokens, 40/8 heads of 128: 109 us, 5.15 TB/s; one of 131001 tokens, 24/4 heads of 256: 59 us,
+// 4.55 TB/s; 16 x 4 rows on 8004 tokens, 24/4 of 256: 43 us, 2.56 TB/s; one token on 777, 40/8 of 128:
+// 14.1 us.  Long calls run at the memory's pace but for some 12 us: launch, first tiles
+// (2 us until the CTAs are ready, 1.5 until the first copy has landed), the chain of the last tile, and the join of cut
+// pairs (5 us); a few short pairs are that chain alone.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -92,8 +99,8 @@ struct TileMeta {
   float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
 };
 struct ValueMeta {
-  int after, rows, groups, set;  // as above; rows before the sequence's end; bits of the groups that hold keys; its O, 4: last,
-                                 // 8: some of its keys are hidden from all rows or some
+  int after, rows, groups;       // as above; rows before the sequence's end; bits of the groups that hold keys
+  int set;                       // its O; 4: the CTA's last; 8: some of its keys are hidden, from all rows or some
   int all0, all1;                // every row of the pair sees the keys all0 .. all1 - 1 of the tile
 };
 // What a query buffer holds besides the rows.
@@ -157,8 +164,8 @@ struct Share {
 };
 
 // A pair takes as long as its tiles and some six more (its rows, its end; 2, 3, 4, 6, 8 and 12 give 117, 110, 109,
-// 107, 110 and 111 us for 64 ragged sequences, and 50, 45, 43, 41, 42 and 43 us for 16 x 4 rows): the line counts a pair's tiles and
-// kPairCost places behind them, which no tile stands at.
+// 107, 110 and 111 us for 64 ragged sequences, and 50, 45, 43, 41, 42 and 43 us for 16 x 4 rows): the line
+// counts a pair's tiles and kPairCost places behind them, which no tile stands at.
 constexpr int kPairCost = 6;
 __device__ __forceinline__ int places_of(const Seq& s, const AttnArgs& a) {
   const int n = tiles_of(s, a);

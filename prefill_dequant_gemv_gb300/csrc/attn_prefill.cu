@@ -13,9 +13,18 @@
 //     of the second product; splitting it into E4M3 terms would cost three conversions an element where
 //     this needs one, and the value codes are converted once for all rows instead, by a
 //     warpgroup of their own, into the fp16 tile that the second product reads transposed;
-//   * a row belongs to two threads, each with half of a step's keys and of the outputs: with one thread a row the
-//     softmax of a step took 2300 cycles against the 1050 of its products, and two row tiles cannot hide that.
+//   * a row belongs to two threads, each with half of a step's keys and of the outputs: with one thread a row
+//     a prompt of 2048 tokens took 88 us where two took 84;
+//   * two row tiles of 128 take turns: one's products run during the other's softmax (heads of 256 have room in tensor
+//     memory for one tile and two buffers of scores).
 // Few tiles are split over the keys (parts of a row join in order in the CTA that finishes last).
+//
+// Measured (GB300): a prompt of 8192 tokens, 40/8 heads of 128: 631 us, 1090 TFLOP/s of the 4 D a query and key; 2048 tokens:
+// 68 us; 512 tokens on 32768, 24/4 heads of 256: 394 us, 1050 TFLOP/s; 6 prompts of up to 2777 tokens under a
+// window of 1024, 32/4 heads of 64: 187 us, 407 TFLOP/s.  A step of 256 rows x 128 keys takes 4020 cycles (heads of 128) or
+// 3370 (64), 128 x 64 at 256 takes 2060; the tensor cores' share at 128 is 2350, as the scores' two terms cost what the
+// outputs do.  The rest is the chain of one row tile, 2300 cycles from scores to weights and 300 until the
+// products start, which two tiles overlap in part.  A CTA's start and end take 20000 cycles, the work of five steps.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -36,7 +45,9 @@ constexpr float kLazy = 8.0f;  // P stays below 2^8
 template <int D>
 struct Cfg {
   static constexpr int MT = D == 256 ? 1 : 2;         // row tiles of 128
-  static constexpr int BN = D == 256 ? 64 : 128;      // keys a step
+  // keys a step (two row tiles with two buffers of 64 keys each: 843 us where one of 128 took 703, 8192 tokens, heads of
+  // 128: an MMA of 64 keys takes as long as one of 128)
+  static constexpr int BN = D == 256 ? 64 : 128;
   static constexpr int ROWS = 128 * MT;
   static constexpr int SOFT = 256 * MT;               // softmax threads: two a row
   static constexpr int THREADS = SOFT + 256;
@@ -336,7 +347,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           const uint32_t p = tmem + (m * C::SB + sb) * BN, d = tmem + C::OCOL + m * D;
 #pragma unroll
           for (int x = 0; x < BN / 16; ++x)
-            mma_f16_ts<kVHi, kPv>(d, p + (x < BN / 32 ? 8 * x : BN / 2 + 8 * (x - BN / 32)), v0 + (fs * C::VF + x * 16 * 128) / 16, (i > 0) | (x > 0));
+            mma_f16_ts<kVHi, kPv>(d, p + (x < BN / 32 ? 8 * x : BN / 2 + 8 * (x - BN / 32)), 
+                                  v0 + (fs * C::VF + x * 16 * 128) / 16, (i > 0) | (x > 0));
           if (m == tiles - 1) mma_commit(&sh.vfree[fs]);
           if (i == n - 1) mma_commit(&sh.odone[m]);
         }
@@ -378,7 +390,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       // a key a thread (two threads a key where there are 64)
       constexpr int TPK = 128 / BN, CH = D / 16 / TPK;  // chunks of 16 codes a thread
       const int key = tid % BN, part = tid / BN;
-      const int first_key = b.first_key, key1 = b.key1, all0 = max(b.pos1, -1) - a.window + 1, all1 = b.pos0;  // (all rows see all0 .. all1)
+      const int first_key = b.first_key, key1 = b.key1;
+      const int all0 = max(b.pos1, -1) - a.window + 1, all1 = b.pos0;  // all rows see all0 .. all1
       bool dead = false;
       int vs = 0, fs = 0;
       uint32_t cpar = 0, fpar = 1;
@@ -431,8 +444,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const int row = mt * 128 + tid;  // in the block
       const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
       if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
-        // They come by way of the converted values' ring, which nobody needs yet, and in a loop that is not unrolled: what
-        // runs once runs as fast as its instructions arrive (four rows at a time from registers: 4000 cycles more).
+        // They come by way of the converted values' ring, which nobody needs yet, all at once, and their terms are made in a
+        // loop that is not unrolled: what runs once runs as fast as its instructions arrive.
         constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP;
         static_assert(C::ROWS * D * 2 <= C::FS * C::VF, "queries fit");
         const int part = threadIdx.x % TPR;
@@ -465,7 +478,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
           uint4 hi, lo;
           split_query(v, query_down(amax, e2), &hi, &lo);
-          const int panel = part / (C::PW / 16), cc = part % (C::PW / 16), sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
+          const int panel = part / (C::PW / 16), cc = part % (C::PW / 16);
+          const int sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
           uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;
           *reinterpret_cast<uint4*>(at) = hi;
           *reinterpret_cast<uint4*>(at + 128 * D) = lo;
@@ -546,8 +560,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;
-        // two groups at a time, each of the three steps over all of them: taken element by element, every exponential's
-        // latency is waited out
+        // two groups at a time
 #pragma unroll
         for (int gr = 0; gr < GH; gr += 2) {
           uint64_t t[16];
@@ -555,7 +568,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           for (int e = 0; e < 16; ++e) {
             const int x = gr + e / 8;
             const float off = sm.lvs[g0 + x] - ref, f = fmaxf(rc * sm.ks[g0 + x], 0x1p-126f);
-            t[e] = fma2(pack2(__uint_as_float(s[16 * gr + 2 * e]), __uint_as_float(s[16 * gr + 2 * e + 1])), pack2(f, f), pack2(off, off));
+            const uint64_t y = pack2(__uint_as_float(s[16 * gr + 2 * e]), __uint_as_float(s[16 * gr + 2 * e + 1]));
+            t[e] = fma2(y, pack2(f, f), pack2(off, off));
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -606,7 +620,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         uint8_t* base = parts ? reinterpret_cast<uint8_t*>(pa.part_o) : reinterpret_cast<uint8_t*>(a.out);
         constexpr int CPR = D / 16;  // pieces of a row in a warp's D * 32 bytes
         uint8_t* stage = qbuf + mt * C::Q + (warp & 7) * (C::Q / 8);
-        auto piece = [&](int r, int k) { return reinterpret_cast<uint4*>(stage + r * D + ((k ^ (D == 64 ? r >> 1 & 3 : r & 7)) << 4)); };
+        auto piece = [&](int r, int k) {
+          return reinterpret_cast<uint4*>(stage + r * D + ((k ^ (D == 64 ? r >> 1 & 3 : r & 7)) << 4));
+        };
         const int dims = parts ? D / 4 : D / 2;  // in a warp's bytes at a time
 #pragma unroll 1
         for (int x0 = 0; x0 < D / 2; x0 += dims) {
@@ -621,15 +637,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
               for (int e = 0; e < 16; ++e) o[e] = 0u;
             }
             if (poison && in) {
-              const uint32_t nans = nan_dims(c, c.pages + (int64_t)b.seq * c.page_stride, head, D, half * (D / 2) + x, sh.pos[row],
-                                             a.window, max(b.pos1, -1) - a.window + 1, b.pos0);
+              const uint32_t nans = nan_dims(c, c.pages + (int64_t)b.seq * c.page_stride, head, D, half * (D / 2) + x,
+                                             sh.pos[row], a.window, max(b.pos1, -1) - a.window + 1, b.pos0);
 #pragma unroll
               for (int e = 0; e < 16; ++e)
                 if (nans >> e & 1) o[e] = 0x7FFFFFFFu;
             }
             if (parts) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) *piece(lane, (x - x0) / 4 + e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+              for (int e = 0; e < 4; ++e)
+                *piece(lane, (x - x0) / 4 + e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
             } else {
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
@@ -694,6 +711,22 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
   if (threadIdx.x == 0) *counter = 0;
 }
 
+// Parts along the keys of each of `items` blocks of some `keys` keys.  The CTAs come in waves of one an SM; a CTA takes
+// its keys' time and that of 640 more for its start and end, of 800 where it writes a part, and each part of a block
+// costs 160 in the join: the number with the shortest sum is taken.  (Measured: 96 items of 33280 keys 531 us whole, 394
+// in three parts, 436 in six; 152 of 8192 138 whole, 164 in two; 48 of 16384 111 in three, 125 in six; 40 of 4096 36 in
+// three, 48 in four or more; 8 of 2048 38 in two, 34 in four, 42 in eight; 20 of 2000 45 whole, 38 in three, 46 in seven.)
+int choose_splits(int64_t items, int64_t keys, int sms) {
+  if (items > (int64_t)(kAttnCounterBytes / sizeof(int))) return 1;
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int s = 1; s <= 32 && (s == 1 || keys / s >= 256); ++s) {
+    const int64_t cost = (items * s + sms - 1) / sms * (keys / s + (s > 1 ? 800 : 640)) + (s > 1 ? 160 * s : 0);
+    if (cost < least) best = s, least = cost;
+  }
+  return best;
+}
+
 template <int D>
 int launch(const AttnArgs& a, const PrefillPlan& p, void* ws, cudaStream_t s) {
   using C = Cfg<D>;
@@ -712,14 +745,19 @@ int launch(const AttnArgs& a, const PrefillPlan& p, void* ws, cudaStream_t s) {
   if (!encode_pages(&km, a.c.k, D, page, a.c.n_pages * a.c.hkv, box) ||
       !encode_pages(&vm, a.c.v, D, page, a.c.n_pages * a.c.hkv, box))
     return QG_ERR_CUDA;
+  // a window leaves a block fewer keys than the plan, which does not know it, has counted on
+  DeviceInfo info;
+  if (!current_device_info(&info)) return QG_ERR_CUDA;
+  const int64_t keys = std::min<int64_t>(a.c.max_len, (int64_t)a.window + C::ROWS / (a.hq / a.c.hkv) + page);
+  const int splits = std::min(p.splits, choose_splits(p.blocks * a.c.hkv, keys, info.sms));
   PrefillArgs pa;
   pa.a = a;
-  pa.splits = p.splits;
+  pa.splits = splits;
   uint8_t* w = static_cast<uint8_t*>(ws);
   pa.counters = reinterpret_cast<int*>(w + kWsHeader);
   pa.part_ml = reinterpret_cast<float2*>(w + p.off_ml);
   pa.part_o = reinterpret_cast<float*>(w + p.off_o);
-  return launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)(p.blocks * a.c.hkv * p.splits)), dim3(C::THREADS),
+  return launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)(p.blocks * a.c.hkv * splits)), dim3(C::THREADS),
                     C::SMEM, s, km, vm, pa) == cudaSuccess
              ? QG_OK
              : QG_ERR_CUDA;
@@ -735,11 +773,8 @@ bool plan_prefill(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_
   p->blocks = std::min<int64_t>(each * batch->n_seqs, n_tokens * G / rows + batch->n_seqs);
   const int64_t items = p->blocks * cache->n_kv_heads;
   if (items > 0x7FFFFFFF / 32) return false;
-  // blocks that leave the GPU's last wave emptier than half a wave of many are cut along the keys, into
-  // parts of 1024 keys at least
-  int64_t s = std::min<int64_t>(2 * (int64_t)dev.sms / std::max<int64_t>(items, 1), batch->max_len / 1024);
-  s = std::min<int64_t>(std::max<int64_t>(s, 1), 32);
-  p->splits = (int)s;
+  const int s = choose_splits(items, batch->max_len, dev.sms);
+  p->splits = s;
   p->off_ml = kWsHeader + kAttnCounterBytes;
   p->off_o = p->off_ml;
   p->ws_bytes = p->off_ml;
@@ -747,7 +782,7 @@ bool plan_prefill(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_
     p->off_o = p->off_ml + (size_t)(items * s * rows) * sizeof(float2);
     p->ws_bytes = p->off_o + (size_t)(items * s * rows) * cache->head_dim * sizeof(float);
   }
-  return s == 1 || items * sizeof(int) <= kAttnCounterBytes;
+  return true;
 }
 
 int launch_attn_prefill(const AttnArgs& a, int head_dim, const PrefillPlan& p, void* ws, void* stream) {

@@ -103,7 +103,9 @@ __device__ __forceinline__ uint64_t pack2(float x, float y) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
   return r;
 }
-__device__ __forceinline__ void unpack2(uint64_t v, float* x, float* y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v)); }
+__device__ __forceinline__ void unpack2(uint64_t v, float* x, float* y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(v));
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -139,8 +141,12 @@ __device__ __forceinline__ float lg2(float x) {
 // those are off by 2^-16 of it at most (a term is rounded to a multiple of 2^-9, the largest is 2^7 at least).
 __device__ __forceinline__ uint32_t bf16x2_codes(uint32_t lo, uint32_t hi) {  // two bf16 pairs -> four codes
   uint16_t a, b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(a) : "f"(__uint_as_float(lo & 0xFFFF0000u)), "f"(__uint_as_float(lo << 16)));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(b) : "f"(__uint_as_float(hi & 0xFFFF0000u)), "f"(__uint_as_float(hi << 16)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+      : "=h"(a)
+      : "f"(__uint_as_float(lo & 0xFFFF0000u)), "f"(__uint_as_float(lo << 16)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
+      : "=h"(b)
+      : "f"(__uint_as_float(hi & 0xFFFF0000u)), "f"(__uint_as_float(hi << 16)));
   return a | (uint32_t)b << 16;
 }
 __device__ __forceinline__ void split_query(const uint4 (&x)[2], float down, uint4* hi, uint4* lo) {
