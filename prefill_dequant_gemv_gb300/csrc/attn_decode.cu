@@ -1,5 +1,5 @@
 // Attention of a few rows a KV head over the 8-bit paged cache (decode, speculative
-// verification): the R = new * G query rows of one (sequence, KV head) pair, at most 64, against
+// verification): the R = new * G query rows of one (sequence, KV head) pair, at most 32, against
 // all its keys.
 //
 // The mathematics.  With codes k, v, page scales ks, vs and s_j = scale * ks_j * (q . k_j) * log2(e), each
@@ -57,15 +57,14 @@ constexpr float kBias = 2.0f;        // P of a key at the reference is 2^2 ...
 constexpr float kHead = 6.5f;        // ... and at most 2^8.5, below E4M3's 448
 constexpr float kNone = -3e38f;      // the reference of a row that has seen no key: -inf would make NaN of its masked scores
 
-// D: head dimension; N: rows it is built for (16, 32, 64).
+// D: head dimension; N: rows it is built for (16, 32).
 template <int D, int N>
 struct Cfg {
   // softmax groups of 128 threads (heads of 256: as many as the ring has stages)
   static constexpr int GROUPS = D == 256 && N == 16 ? 2 : 64 / N;
   static constexpr int THREADS = 128 * GROUPS + 256;
   // registers a thread: what the launch gives, what softmax threads take, what the other two warpgroups keep
-  static constexpr int REGS = GROUPS == 4 ? 80 : GROUPS == 2 ? 128 : 168;
-  static constexpr int RSOFT = GROUPS == 4 ? 96 : GROUPS == 2 ? 168 : 232, RREST = GROUPS == 4 ? 48 : GROUPS == 2 ? 80 : 104;
+  static constexpr int REGS = GROUPS == 4 ? 80 : 128, RSOFT = GROUPS == 4 ? 96 : 168, RREST = GROUPS == 4 ? 48 : 80;
   static_assert(128 * GROUPS * RSOFT + 256 * RREST <= THREADS * REGS && THREADS * REGS <= 65536, "registers");
   static constexpr int PW = D < 128 ? D : 128;       // bytes of a panel row (a TMA box row)
   static constexpr int NP = D / PW;                  // panels
@@ -1029,13 +1028,12 @@ int launch(const DecodeArgs& da, const CUtensorMap& km, const CUtensorMap& vm, i
 template <int D>
 int launch_rows(int rows, const DecodeArgs& da, const CUtensorMap& km, const CUtensorMap& vm, int grid, cudaStream_t s) {
   if (rows == 16) return launch<D, 16>(da, km, vm, grid, s);
-  if (rows == 32) return launch<D, 32>(da, km, vm, grid, s);
-  return launch<D, 64>(da, km, vm, grid, s);
+  return launch<D, 32>(da, km, vm, grid, s);
 }
 
 }  // namespace
 
-int decode_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 0; }
+int decode_rows(int64_t rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : 0; }
 
 size_t decode_workspace(int64_t rows, int head_dim, const DeviceInfo& dev) {
   const size_t r = (size_t)decode_rows(rows), slots = 2 * (size_t)dev.sms;

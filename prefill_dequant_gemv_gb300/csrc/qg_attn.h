@@ -58,7 +58,7 @@ struct PrefillPlan {
 };
 struct AttnPlan {
   size_t ws_bytes;
-  bool decode;  // few rows a KV head: the streaming kernel
+  bool decode;  // the streaming kernel
   PrefillPlan prefill;
 };
 // Counters of the joins, right behind the workspace's header whatever the call.
@@ -66,8 +66,8 @@ constexpr size_t kAttnCounterBytes = 4096;
 bool plan_attn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int hq, const DeviceInfo& dev,
                AttnPlan* p);
 int launch_attn(const AttnArgs& a, int head_dim, const AttnPlan& p, const DeviceInfo& dev, void* ws, void* stream);
-// The streaming kernel of up to 64 rows (new tokens x query heads a KV head).
-int decode_rows(int64_t rows);  // the row count it is built for: 16, 32, 64; 0: too many
+// The streaming kernel of up to 32 rows (new tokens x query heads a KV head).
+int decode_rows(int64_t rows);  // the row count it is built for: 16, 32; 0: too many
 size_t decode_workspace(int64_t rows, int head_dim, const DeviceInfo& dev);
 int launch_attn_decode(const AttnArgs& a, int head_dim, int64_t rows, const DeviceInfo& dev, void* ws, void* stream);
 // The row-block kernel of more rows.
