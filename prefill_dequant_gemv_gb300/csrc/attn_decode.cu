@@ -24,11 +24,11 @@
 //     whatever the lengths; a pair cut between CTAs leaves partial (m, l, O) rows in the workspace, and the
 //     CTA that finishes last adds them in order.  One launch.
 //   * One or two warps copy key tiles into a ring by TMA and as many value tiles into another, two bring a
-//     pair's query rows, two issue the MMAs (scores, outputs), and groups of four warps turn
-//     S into P, a key a thread: its column of R scores comes from tensor memory, its terms go to shared memory as 16-byte rows.  The sums of P stay per thread until the
-//     pair ends.  A tile's way through these steps is a chain of about 2500 cycles, several
-//     times what its bytes take to arrive; so several groups work on
-//     as many tiles at once, each with its own reference and accumulators, joined at the pair's end.
+//     pair's query rows, two issue the MMAs (scores, outputs), and groups of four warps turn S into P, a key a
+//     thread: its column of R scores comes from tensor memory, its terms go to shared memory as 16-byte rows.
+//     The sums of P stay per thread until the pair ends.  A tile's way through these steps is a chain of about
+//     2500 cycles, several times what its bytes take to arrive; so several groups work on as many tiles at once,
+//     each with its own reference and accumulators, joined at the pair's end.
 //
 // Measured (GB300; bytes are the codes and scales that the rows see, queries and outputs): 64 sequences of up to
 // 8193 tokens, 40/8 heads of 128: 109 us, 5.15 TB/s; one of 131001 tokens, 24/4 heads of 256: 59 us,

@@ -476,3 +476,39 @@ def test_nan_scores_stay_in_their_rows(d, page, hkv, hq, news, lens, window):
     got = to_f64(q.attention(cache, batch, qh.cuda(), window=window))
     assert np.array_equal(np.isnan(got), nan)
     check_attention(torch.from_numpy(np.where(nan, clean[0], got)), clean, d, max(lens))
+
+
+@pytest.mark.parametrize("d,hkv,hq,page,new,most,window", [(128, 4, 28, 32, 3, 900, 0), (64, 4, 32, 16, 4, 1100, 0), (256, 4, 24, 64, 4, 800, 0),
+                                                           (128, 8, 40, 64, 5, 2500, 300), (256, 8, 56, 16, 4, 700, 150)])
+def test_many_sequences_of_17_to_32_rows(d, hkv, hq, page, new, most, window):
+    """Enough keys for the streaming kernel at these rows (2^18 over all pairs), windows that begin inside pages, and NaN
+    value codes in the first and the last new token's places."""
+    q = qlib()
+    rng = np.random.default_rng(most + d)
+    lens = [int(x) for x in np.exp(rng.uniform(np.log(new), np.log(most), 96))] + [most, new]
+    assert 16 < new * hq // hkv <= 32 and len(lens) * hkv * most >= 1 << 18
+    c = Case(most + d, [new if i % 7 else 0 for i in range(len(lens))], lens, page, hkv, d)
+    qh = c.heads(hq)
+    cache, batch = c.device(q)
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, c.n, hq))
+    qd = qh.cuda()
+    first = q.attention(cache, batch, qd, window=window, workspace=ws).clone()
+    ref = _device_reference(c, qh, window, d ** -0.5)
+    check_attention(first, ref, d, most)
+    outs = [q.attention(cache, batch, qd, window=window, workspace=ws) for _ in range(100)]
+    assert ws.status() == 0
+    assert all(torch.equal(first, o) for o in outs)
+    # a NaN dim in the last new token (its row alone sees it) and, under a window, in the key that only the first row sees
+    nan = np.zeros((c.n, hq, d), bool)
+    grp = hq // hkv
+    for b, (t, length) in enumerate(zip(c.news, c.lens)):
+        if not t:
+            continue
+        h, dim, r = b % hkv, (17 * b) % d, c.starts[b]
+        for at, row in [(length - 1, r + t - 1)] + ([(length - t - window + 1, r)] if window and length - t - window + 1 >= 0 else []):
+            c.vc[c.pages[b, at // page], h, at % page, dim] = 0x7F
+            nan[row, h * grp:(h + 1) * grp, dim] = True
+    cache = c.device(q)[0]
+    got = to_f64(q.attention(cache, batch, qd, window=window))
+    assert np.array_equal(np.isnan(got), nan)
+    check_attention(torch.from_numpy(np.where(nan, ref[0], got)), ref, d, most)
