@@ -3,11 +3,11 @@
 // all its keys.
 //
 // The mathematics.  With codes k, v, page scales ks, vs and s_j = scale * ks_j * (q . k_j) * log2(e), each
-// row keeps t_j = s_j + log2(vs_j), a reference m near their maximum and P_j = 2^(t_j - m + 2):
+// row keeps t_j = s_j + log2(vs_j), a reference m near their maximum and P_j = 2^(t_j - m + 6):
 //   out = sum_j P_j v_j / sum_j P_j / vs_j.
 // The value scale sits in the exponent, so P is rounded relative to the largest contribution
 // whatever the scales' spread.  m need not be the maximum: it moves only when some t_j passes it by
-// 6.5, so no tile but the first few reduces anything over its keys.
+// 2.8, so few tiles but the first reduce anything over their keys.
 //
 // Bound by HBM: each key and value code is used for R rows only.  So nothing converts them: both
 // products run on the E4M3 tensor cores with the codes as they lie in the cache, and the 16-bit side
@@ -16,9 +16,10 @@
 //   outputs  O^T[dim][row] += V^T[D x 128 keys] * P^T      (A: the value tile read transposed, N = 3 terms x rows)
 // A query row over a power of two is the sum of two E4M3 terms (bf16 has 8 significant bits, a term 4
 // and a sign; exact but for elements 2^-9 below the row's largest, off by 2^-16 of it at most).  P, rounded to
-// fp16's 11 bits, is the sum of three, the second and third scaled up by 2^4 and 2^8; each term has its own
-// accumulator columns, so the scaling comes out at the end.  Keys as the M dimension fill it whatever R
-// is.  Accumulation and statistics are fp32.
+// fp16's 11 bits, is the sum of three, the second and third scaled up by 2^4 and 2^9; each term has its own
+// accumulator columns, so the scaling comes out at the end.  The third ends at steps of 2^-18, so a P below 2^-7 keeps
+// fewer bits: it is off by 2^-19 at most, 2^-25 of the row's largest weight, which is 2^6 at least.  Keys as the M
+// dimension fill it whatever R is.  Accumulation and statistics are fp32.
 //
 //   * The pairs' keys, in tiles of 128, lie on one line, which the CTAs (one an SM) share out evenly
 //     whatever the lengths; a pair cut between CTAs leaves partial (m, l, O) rows in the workspace, and the
@@ -53,8 +54,8 @@ namespace {
 
 constexpr int kTile = 128;           // keys a tile
 constexpr int kMostCtas = 256;
-constexpr float kBias = 2.0f;        // P of a key at the reference is 2^2 ...
-constexpr float kHead = 6.5f;        // ... and at most 2^8.5, below E4M3's 448
+constexpr float kBias = 6.0f;        // P of a key at the reference is 2^6 ...
+constexpr float kHead = 2.8f;        // ... and at most 2^8.8 = 446, below E4M3's 448
 constexpr float kNone = -3e38f;      // the reference of a row that has seen no key: -inf would make NaN of its masked scores
 
 // D: head dimension; N: rows it is built for (16, 32).
@@ -122,7 +123,9 @@ struct Shared {
   PairMeta<N> pair[C::QB];
   alignas(16) float ref[C::OB][C::GROUPS][N];
   alignas(16) float factor[C::GROUPS][N];  // of a group's O at the join
-  float sum[C::OB][C::GROUPS][N], grow[C::GROUPS][N], red[C::GROUPS][4][N], inv[N];
+  alignas(16) float grow[C::GROUPS][N];    // what a group's O and sums are multiplied by when references move
+  uint32_t moved[C::GROUPS];               // bits of the rows whose reference moves
+  float sum[C::OB][C::GROUPS][N], red[C::GROUPS][4][N], inv[N];
   uint64_t kfull[C::SK], kfree[C::SK], vfull[C::SV], vfree[C::SV];
   uint64_t qfull[C::QB], qfree[C::QB];
   uint64_t sfull[C::GROUPS], sfree[C::GROUPS], pfull[C::GROUPS], pvdone[C::GROUPS];
@@ -789,7 +792,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         }
         if (first || any_of(grp, over || dead)) {
           // some key passes its row's reference, or there is none yet: new references, and what was summed up
-          // moves to them
+          // moves to them (16 x 4 rows of 256: 45.4 us, 49.4 with all rows' outputs multiplied each time)
 #pragma unroll
           for (int r = 0; r < N; ++r) {
             if (r < R) {
@@ -799,32 +802,43 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           }
           if (any_of(grp, dead)) break;
           if (tid >= R && tid < N) ref[tid] = INFINITY;  // not a row: nothing passes it
-          if (tid < R) {
-            const float* red = sh.red[grp][0];
-            const float top = fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid]));
-            const float old = first ? -INFINITY : ref[tid];
-            const float now = fmaxf(fmaxf(top, old), kNone);
-            ref[tid] = now;
-            grow[tid] = now == old ? 1.0f : ex2(old - now);
+          if (tid < 32) {
+            float moved = 1.0f;
+            if (tid < R) {
+              const float* red = sh.red[grp][0];
+              const float top = fmaxf(fmaxf(red[tid], red[N + tid]), fmaxf(red[2 * N + tid], red[3 * N + tid]));
+              const float old = first ? -INFINITY : ref[tid];
+              const float now = fmaxf(fmaxf(top, old), kNone);
+              ref[tid] = now;
+              if (now != old) moved = ex2(old - now);
+              grow[tid] = moved;
+            }
+            const uint32_t rows = __ballot_sync(0xFFFFFFFFu, moved != 1.0f);
+            if (tid == 0) sh.moved[grp] = rows;
           }
           any_of(grp, false);
           if (!first) {
             if (!wait(&sh.pvdone[grp], (turn - 1) & 1, c.status)) dead = true;
             if (any_of(grp, dead)) break;
             tc_fence_after();
+            const uint32_t rows = sh.moved[grp];
 #pragma unroll
             for (int r = 0; r < N; ++r)
               if (r < R) l[r] *= grow[r];
 #pragma unroll 1
-            for (int col = 0; col < C::MB * C::OCOL; col += 16) {
-              const int r = col % N;
-              if (r < R) {
-                uint32_t u[16];
-                tmem_ld16(ot + col, u);
-                tmem_ld_wait();
+            for (int r = 0; r < R; r += 4) {  // four rows' outputs at a time, where one of them moves
+              if (!(rows >> r & 15)) continue;
+              uint32_t u[3 * C::MB][4];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * (r + e < R ? grow[r + e] : 0.0f));
-                tmem_st16(ot + col, u);
+              for (int e = 0; e < 3 * C::MB; ++e) tmem_ld4(ot + e * N + r, u[e]);
+              const float4 w = *reinterpret_cast<const float4*>(&grow[r]);
+              const float ws[4] = {w.x, w.y, w.z, w.w};
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 3 * C::MB; ++e) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) u[e][z] = __float_as_uint(__uint_as_float(u[e][z]) * (r + z < R ? ws[z] : 0.0f));
+                tmem_st4(ot + e * N + r, u[e]);
               }
             }
             tmem_st_wait();
@@ -851,9 +865,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
               for (int z = 0; z < 2; ++z) {
                 const uint32_t h = f16x2(pr[2 * z], pr[2 * z + 1]);
                 const uint16_t c0 = e4m3x2(h);
-                const uint32_t r1 = rest16(h, codes_f16x2(c0));
+                const uint32_t r1 = rest<16>(h, codes_f16x2(c0));  // 256 at most, as half of 448's last place is 16
                 const uint16_t c1 = e4m3x2(r1);
-                const uint16_t c2 = e4m3x2(rest16(r1, codes_f16x2(c1)));
+                const uint16_t c2 = e4m3x2(rest<32>(r1, codes_f16x2(c1)));  // 256 at most
                 t0[q / 4] |= (uint32_t)c0 << (16 * z);
                 t1[q / 4] |= (uint32_t)c1 << (16 * z);
                 t2[q / 4] |= (uint32_t)c2 << (16 * z);
@@ -950,7 +964,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int z = 0; z < 4; ++z) {
-              const float y = fmaf(__uint_as_float(v[gq][2][z]), 0x1p-8f,
+              const float y = fmaf(__uint_as_float(v[gq][2][z]), 0x1p-9f,
                                    fmaf(__uint_as_float(v[gq][1][z]), 0x1p-4f, __uint_as_float(v[gq][0][z])));
               if (f[z] != 0.0f) o[z] = fmaf(y, f[z], o[z]);  // a group without a tile of this pair holds anything
             }

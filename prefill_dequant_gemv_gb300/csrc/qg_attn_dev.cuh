@@ -43,11 +43,13 @@ __device__ __forceinline__ uint32_t codes_f16x2(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
-// 16 * (h - c) of two fp16 pairs: exact where c is h rounded to fewer bits
-__device__ __forceinline__ uint32_t rest16(uint32_t h, uint32_t c) {
+// F * (h - c) of two fp16 pairs, F 16 or 32: exact where c is h rounded to fewer bits
+template <int F>
+__device__ __forceinline__ uint32_t rest(uint32_t h, uint32_t c) {
+  static_assert(F == 16 || F == 32, "factor");
   uint32_t d, r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(c));
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(0x4C004C00u));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(F == 16 ? 0x4C004C00u : 0x50005000u));
   return r;
 }
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, uint64_t* bar) {
