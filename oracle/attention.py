@@ -86,7 +86,8 @@ def append(x, news, lens, pages, page_tokens, codes, scales):
 
 def attention(q, news, lens, pages, page_tokens, kc, ks, vc, vs, scale, window=0):
     """out [n, hq, d] in float64 for q [n, hq, d] and, for the tests' bounds, per row and head: the sum of
-    p |v| [n, hq, d], the largest sum over d of |q k| scale [n, hq], the keys seen and the largest |v|."""
+    p |v| [n, hq, d], the largest sum over d of |q k| scale [n, hq] and the largest |v|.  Tokens of a page whose
+    key scale is 0 do not enter."""
     q = np.asarray(q, dtype=np.float64)
     n, hq, d = q.shape
     hkv = kc.shape[1]
@@ -98,12 +99,15 @@ def attention(q, news, lens, pages, page_tokens, kc, ks, vc, vs, scale, window=0
         for g in range(hkv if length else 0):
             k, v = (np.concatenate([e4m3_decode(c[i, g]) * float(s[i, g]) for i in ids])[:length]
                     for c, s in ((kc, ks), (vc, vs)))
+            live = np.repeat([ks[i, g] != 0 for i in ids], page_tokens)[:length]
             for i in range(t):
                 pos = length - t + i
                 lo = max(0, pos - window + 1) if window else 0
                 if pos < 0:
                     continue
-                kk, vv = k[lo:pos + 1], v[lo:pos + 1]
+                kk, vv = k[lo:pos + 1][live[lo:pos + 1]], v[lo:pos + 1][live[lo:pos + 1]]
+                if not len(kk):
+                    continue
                 for h in range(g * (hq // hkv), (g + 1) * (hq // hkv)):
                     s = kk @ q[row + i, h] * scale
                     p = np.exp(s - s.max())

@@ -96,7 +96,7 @@ struct Cfg {
 struct TileMeta {
   int tok0, len, after;  // after: tiles of its pair in this CTA before it
   int flags;             // 1: some of its rows hold no key; 2: some row of the pair does not see all of it; 4: the CTA's last
-  float ks[8], vs[8];    // scales of its groups of 16 keys; 0: the group holds no key
+  float ks[8], vs[8];    // scales of its groups of 16 keys; key scale 0: the group holds no key that anyone sees
 };
 struct ValueMeta {
   int after, rows, groups;       // as above; rows before the sequence's end; bits of the groups that hold keys
@@ -336,6 +336,20 @@ __device__ __noinline__ void join_parts(const DecodeArgs& da, int R, int G, int6
           make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
     }
   }
+}
+
+// A key of a page whose key scale is 0, in any tile: its P is 0, but a NaN code times 0 is NaN, so its values become 0, once
+// they are here.  (Keys that not all rows see the output warp looks after.  With that warp reading the scales of every
+// tile 64 ragged sequences took up to 4 us more.)
+template <int D, int N>
+__device__ __noinline__ bool drop_values(uint8_t* vring, uint64_t* vfull, int i, int key, int* status) {
+  using C = Cfg<D, N>;
+  const bool ok = wait(&vfull[i % C::SV], (uint32_t)(i / C::SV) & 1u, status);
+  uint8_t* at = vring + i % C::SV * C::KV + key * C::PW;
+#pragma unroll 1
+  for (int e = 0; e < C::NP * C::PW; e += 16)
+    *reinterpret_cast<uint4*>(at + e / C::PW * C::PANEL + e % C::PW) = make_uint4(0, 0, 0, 0);
+  return ok;
 }
 
 template <int D, int N>
@@ -778,7 +792,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             }
           }
         }
-        if (flags & 2) {  // masks
+        if ((flags & 2) || ks == 0.0f) {  // masks; a page of key scale 0 may lie in any tile
+          if (ks == 0.0f && tok <= pm.pos[0] && tok > pm.pos[R - 1] - a.window &&
+              !drop_values<D, N>(vring, sh.vfull, i, tid, c.status))
+            dead = true;
           const bool hidden = ks == 0.0f || tok >= most;
           over = first;
 #pragma unroll

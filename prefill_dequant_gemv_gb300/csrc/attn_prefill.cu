@@ -284,11 +284,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         }
         // the step's description goes with the value codes' barrier to the converters, and with the keys' to the rest
         StepMeta& m = sh.step[i & 7];
-        const bool cut = __any_sync(0xFFFFFFFFu, lane < NG && (!ok || tok + 16 > key1));
+        const bool seen = ok && sk != 0.0f;
+        const bool cut = __any_sync(0xFFFFFFFFu, lane < NG && (!seen || tok + 16 > key1));
         if (lane < NG) {
           m.ks[lane] = sk;
-          m.lvs[lane] = ok ? lg2(sv) : 0.0f;
-          m.ivs[lane] = ok ? rcp(sv) : 0.0f;
+          m.lvs[lane] = seen ? lg2(sv) : 0.0f;
+          m.ivs[lane] = seen ? rcp(sv) : 0.0f;
         }
         if (lane == 0) m.cut = cut;
         __syncwarp();

@@ -57,3 +57,16 @@ def test_attention_closed_forms():
     assert np.allclose(out[:, 0], v[15:18])  # a window of one token: its own value
     out, *_ = oa.attention(q, [3], [2], [[1, 0]], 16, kc, np.ones((2, 1)), vc, vs, 0.3)
     assert not out[0].any() and out[1].any()  # the first row stands before the sequence and sees nothing
+
+
+def test_attention_leaves_out_pages_of_key_scale_zero():
+    rng = np.random.default_rng(3)
+    kc, vc = (oa.e4m3_encode(rng.standard_normal((3, 1, 16, 8))) for _ in range(2))
+    ks, vs = np.ones((3, 1)), np.ones((3, 1))
+    q = rng.standard_normal((1, 2, 8))
+    want, *_ = oa.attention(q, [1], [32], [[0, 2]], 16, kc, ks, vc, vs, 0.3)
+    ks[1], vs[1], kc[1], vc[1, :, ::3] = 0.0, np.nan, 0x7F, 0x7F
+    out, mag, load, vmax = oa.attention(q, [1], [48], [[0, 1, 2]], 16, kc, ks, vc, vs, 0.3)
+    assert np.array_equal(out, want) and np.all(np.isfinite([mag.max(), load.max(), vmax.max()]))
+    out, *_ = oa.attention(q, [1], [16], [[1]], 16, kc, ks, vc, vs, 0.3)
+    assert not out.any()

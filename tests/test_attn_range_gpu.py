@@ -5,6 +5,7 @@ import torch
 
 from oracle import attention as oa
 from tests.gpu_util import qlib, to_f64
+from tests.test_attn_gpu import Case, check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -56,3 +57,50 @@ def _check_sink(d, hkv, hq, new, n_seqs, length, gap, value, noise, floor):
 def test_weights_far_below_the_largest_streaming(d, hkv, hq, new, n_seqs, length, gap, value, noise):
     # P is 2^6 or more at the largest weight and off by 2^-19 at most
     _check_sink(d, hkv, hq, new, n_seqs, length, gap, value, noise, 2.0 ** -25)
+
+
+# ------------------------------------------------------------------ pages whose key scale is 0
+@pytest.mark.parametrize("d,page,hkv,hq,news,lens,window", [
+    (128, 64, 2, 10, [1, 1], [900, 300], 0), (64, 16, 4, 32, [1, 2], [1000, 400], 0), (256, 128, 1, 6, [2, 1], [1200, 640], 0),
+    (128, 32, 2, 6, [1], [5000], 700), (64, 128, 1, 4, [1, 1], [128, 700], 0),
+    (128, 64, 2, 10, [300, 2], [900, 640], 0), (64, 16, 2, 16, [100, 260], [700, 1000], 0), (256, 128, 1, 6, [150], [1200], 0),
+    (128, 32, 1, 8, [40], [6000], 900), (128, 128, 1, 64, [3], [700], 0)])
+def test_pages_of_key_scale_zero_do_not_enter(d, page, hkv, hq, news, lens, window):
+    """Inner pages too, with NaN codes in them, a value scale of 1, 0 or NaN; and a sequence of no other pages."""
+    q = qlib()
+    c = Case(d + page + sum(lens) + 2, news, lens, page, hkv, d)
+    for b, length in enumerate(lens):
+        for i in range(-(-length // page)):
+            if i % 3 == 1 or b == 1 and len(lens) > 1 and i < 2:
+                h = c.rng.integers(hkv)
+                c.ks[c.pages[b, i], h], c.vs[c.pages[b, i], h] = 0.0, [1.0, 0.0, np.nan][i % 9 // 3]
+                for codes in (c.kc, c.vc):
+                    codes[c.pages[b, i], h, :, ::5] = 0x7F
+    _check_hidden(q, c, hq, window)
+    c.ks[c.pages[0, :-(-lens[0] // page)]] = 0.0
+    got = _check_hidden(q, c, hq, window)
+    assert not to_f64(got)[:news[0]].any()
+
+
+def _check_hidden(q, c, hq, window):
+    qh = c.heads(hq, 2.0)
+    cache, batch = c.device(q)
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, c.n, hq))
+    got = q.attention(cache, batch, qh.cuda(), window=window, workspace=ws)
+    assert ws.status() == 0
+    check_attention(got, c.attention(qh, c.d ** -0.5, window), c.d, max(c.lens))
+    return got
+
+
+@pytest.mark.parametrize("d,hkv,hq,page,new", [(128, 4, 24, 32, 4), (256, 4, 32, 16, 3), (64, 4, 40, 128, 2)])
+def test_pages_of_key_scale_zero_17_to_32_rows(d, hkv, hq, page, new):
+    q = qlib()
+    rng = np.random.default_rng(d)
+    lens = [int(x) for x in rng.integers(new, 701, 97)] + [701]
+    assert 16 < new * hq // hkv <= 32 and len(lens) * hkv * max(lens) >= 1 << 18  # the streaming kernel
+    c = Case(d + page, [new] * len(lens), lens, page, hkv, d)
+    for b, length in enumerate(lens):
+        for i in range(b % 3, -(-length // page), 3):
+            c.ks[c.pages[b, i], b % hkv] = 0.0
+            c.vc[c.pages[b, i], b % hkv, :, 3::7] = 0xFF
+    _check_hidden(q, c, hq, 0)
