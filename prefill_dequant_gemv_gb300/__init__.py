@@ -554,7 +554,7 @@ class KVCache:
 class KVBatch:
     """The sequences of a call (``qg_kv_batch``): q_start int32 [n_seqs + 1], lens int32 [n_seqs] (with the new
     tokens) and pages int32 [n_seqs, m] on the device; max_new and max_len bound every sequence's new tokens
-    and length.  The tensors' contents may change between calls (within the bounds)."""
+    and length, max_len by m pages at most.  The tensors' contents may change between calls (within the bounds)."""
 
     def __init__(self, q_start, lens, pages, max_new: int, max_len: int):
         import torch
@@ -567,7 +567,7 @@ class KVBatch:
         _need(n == 1 or pages.stride(0) >= pages.shape[1], "KVBatch: pages' rows overlap")
         self.q_start, self.lens, self.pages = q_start, lens, pages
         self.n_seqs, self.max_new, self.max_len = n, int(max_new), int(max_len)
-        self._per_page = pages.shape[1]
+        self.width = int(pages.shape[1])  # (a row's stride may be longer)
         self.desc = qg_kv_batch(n, self.max_new, self.max_len, q_start.data_ptr(), lens.data_ptr(), pages.data_ptr(),
                                 pages.stride(0) if n > 1 else pages.shape[1])
 
@@ -595,6 +595,11 @@ class NormRope:
                                  0 if cos_sin is None else cos_sin.shape[1], 1 if interleaved else 0)
 
 
+def _table(cache, batch, what):
+    if batch.max_len > batch.width * cache.page_tokens:
+        raise QGError(1, f"{what}: max_len {batch.max_len} takes more than the {batch.width} pages a sequence of the table")
+
+
 def _heads(t, n, heads, cache, what):
     """(pointer, token stride, head stride) of bf16 [n, heads, head_dim]; n or heads None: any."""
     s, st = t.shape, t.stride()
@@ -610,6 +615,7 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, norm_rope: Optional[NormR
     """Norm and rotate the new tokens' q and k (bf16 [n, heads, head_dim]), write k and v into the cache and
     return the queries (``qkv_append``).  q may be None: only the cache is written."""
     hkv = cache.n_kv_heads
+    _table(cache, batch, "kv_append")
     kp, ldk, hsk = _heads(k, None, hkv, cache, "kv_append: k")
     n = k.shape[0]
     vp, ldv, hsv = _heads(v, n, hkv, cache, "kv_append: v")
@@ -643,6 +649,7 @@ def attention(cache: KVCache, batch: KVBatch, q, scale: Optional[float] = None, 
               workspace: Optional[Workspace] = None):
     """Causal attention of the new tokens q (bf16 [n, heads, head_dim]) over the cache (``qattn``);
     scale is 1/sqrt(head_dim) unless given, window 0 means none."""
+    _table(cache, batch, "attention")
     qp, ldq, hsq = _heads(q, None, None, cache, "attention: q")
     n, hq, d = q.shape
     if out is None:
