@@ -536,7 +536,7 @@ class KVCache:
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = (int(x) for x in k_codes.shape)
         # what each call needs of torch, looked up once: calls of a decode step are short
-        self.bf16, self.index = torch.bfloat16, k_codes.device.index
+        self.bf16, self.index = torch.bfloat16, k_codes.get_device()  # (a CPU's is -1)
         self.raw_stream = _raw_stream_getter()
         self.desc = qg_kv_cache(QG_KV_E4M3, self.page_tokens, self.n_kv_heads, self.head_dim, self.n_pages,
                                 k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
@@ -567,7 +567,7 @@ class KVBatch:
         _need(n == 1 or pages.stride(0) >= pages.shape[1], "KVBatch: pages' rows overlap")
         self.q_start, self.lens, self.pages = q_start, lens, pages
         self.n_seqs, self.max_new, self.max_len = n, int(max_new), int(max_len)
-        self.width = int(pages.shape[1])  # (a row's stride may be longer)
+        self.index, self.width = lens.get_device(), int(pages.shape[1])  # (a row's stride may be longer)
         self.desc = qg_kv_batch(n, self.max_new, self.max_len, q_start.data_ptr(), lens.data_ptr(), pages.data_ptr(),
                                 pages.stride(0) if n > 1 else pages.shape[1])
 
@@ -585,6 +585,9 @@ class NormRope:
         _need(cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()),
               "NormRope: cos_sin is contiguous float32 [positions, rotary_dim]")
         self.q_weight, self.k_weight, self.cos_sin = q_weight, k_weight, cos_sin
+        places = {t.get_device() for t in (q_weight, k_weight, cos_sin) if t is not None}
+        _need(len(places) < 2, "NormRope: tensors on one device")
+        self.index = places.pop() if places else None
         dims = {w.numel() for w in (q_weight, k_weight) if w is not None}
         _need(len(dims) < 2, "NormRope: weights of one length")
         self.dim = dims.pop() if dims else None
@@ -595,18 +598,21 @@ class NormRope:
                                  0 if cos_sin is None else cos_sin.shape[1], 1 if interleaved else 0)
 
 
-def _table(cache, batch, what):
+def _together(cache, batch, workspace, what):
+    """What the descriptors alone do not tell: the width of the page table, and where the tensors are."""
     if batch.max_len > batch.width * cache.page_tokens:
         raise QGError(1, f"{what}: max_len {batch.max_len} takes more than the {batch.width} pages a sequence of the table")
+    if cache.index < 0 or batch.index != cache.index or (workspace is not None and workspace.buf.get_device() != cache.index):
+        raise QGError(1, f"{what}: cache, batch and workspace on one CUDA device")
 
 
 def _heads(t, n, heads, cache, what):
     """(pointer, token stride, head stride) of bf16 [n, heads, head_dim]; n or heads None: any."""
     s, st = t.shape, t.stride()
     if (t.dtype is not cache.bf16 or len(s) != 3 or s[2] != cache.head_dim or st[2] != 1
-            or (n is not None and s[0] != n) or (heads is not None and s[1] != heads)):
+            or (n is not None and s[0] != n) or (heads is not None and s[1] != heads) or t.get_device() != cache.index):
         raise QGError(1, f"{what}: bfloat16 [{'tokens' if n is None else n}, {'heads' if heads is None else heads}, "
-                         f"{cache.head_dim}] with a contiguous last dimension")
+                         f"{cache.head_dim}] with a contiguous last dimension on the cache's device")
     return t.data_ptr(), st[0], st[1]
 
 
@@ -615,7 +621,7 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, norm_rope: Optional[NormR
     """Norm and rotate the new tokens' q and k (bf16 [n, heads, head_dim]), write k and v into the cache and
     return the queries (``qkv_append``).  q may be None: only the cache is written."""
     hkv = cache.n_kv_heads
-    _table(cache, batch, "kv_append")
+    _together(cache, batch, workspace, "kv_append")
     kp, ldk, hsk = _heads(k, None, hkv, cache, "kv_append: k")
     n = k.shape[0]
     vp, ldv, hsv = _heads(v, n, hkv, cache, "kv_append: v")
@@ -631,6 +637,7 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, norm_rope: Optional[NormR
     if norm_rope is not None:
         nr = norm_rope.desc
         _need(norm_rope.dim in (None, cache.head_dim), "kv_append: norm weights of head_dim elements")
+        _need(norm_rope.index in (None, cache.index), "kv_append: norm weights and rotation table on the cache's device")
     if workspace is None:
         workspace = Workspace(qkv_append_workspace_size(), k.device)
     st = (_lib or lib()).qkv_append(cache.desc, batch.desc, nr, n, hq, qp, ldq, hsq, kp, ldk, hsk, vp, ldv, hsv, op, ldo, hso,
@@ -649,7 +656,7 @@ def attention(cache: KVCache, batch: KVBatch, q, scale: Optional[float] = None, 
               workspace: Optional[Workspace] = None):
     """Causal attention of the new tokens q (bf16 [n, heads, head_dim]) over the cache (``qattn``);
     scale is 1/sqrt(head_dim) unless given, window 0 means none."""
-    _table(cache, batch, "attention")
+    _together(cache, batch, workspace, "attention")
     qp, ldq, hsq = _heads(q, None, None, cache, "attention: q")
     n, hq, d = q.shape
     if out is None:
