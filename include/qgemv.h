@@ -436,7 +436,8 @@ size_t qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  * q and out: bf16, strides as in qkv_append; rows of no sequence are left as they are.
  * Keys that a row does not see, whatever their bits, do not enter it, and neither do tokens of a page whose key
  * scale is 0.  NaN codes that it sees, and NaN or infinite queries, give NaN as the formula does.  Scores are
- * fp32 numbers: |scale * q . k| below 2^120.  G is at most 128.
+ * fp32 numbers: |scale * q . k| below 2^120.  A query row is taken relative to its largest element: elements of
+ * 2^-13 of it or more exactly, smaller ones to 2^-21 of it.  G is at most 128.
  * The workspace must be zero-filled before its first use; every qattn call, of any sizes that it has room for,
  * leaves it ready for the next one; calls that overlap on the GPU must not share it, and no other
  * entry point may use it in between.  QG_ERR_UNSUPPORTED where a call's work passes 32-bit counts

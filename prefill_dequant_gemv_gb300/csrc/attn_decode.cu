@@ -14,8 +14,8 @@
 // is split into E4M3 terms instead, which is little work for few rows:
 //   scores   S^T[key][row]  = K[128 keys x D]   * Q^T      (A: the key tile, B: the rows, N = 2 terms x rows)
 //   outputs  O^T[dim][row] += V^T[D x 128 keys] * P^T      (A: the value tile read transposed, N = 3 terms x rows)
-// A query row over a power of two is the sum of two E4M3 terms (bf16 has 8 significant bits, a term 4
-// and a sign; exact but for elements 2^-9 below the row's largest, off by 2^-16 of it at most).  P, rounded to
+// A query row over a power of two is the sum of two E4M3 terms (bf16 has 8 significant bits, a term 4 and a sign), the second
+// scaled up by 2^5: exact but for elements below 2^-13 of the row's largest, off by 2^-21 of it at most.  P, rounded to
 // fp16's 11 bits, is the sum of three, the second and third scaled up by 2^4 and 2^9; each term has its own
 // accumulator columns, so the scaling comes out at the end.  The third ends at steps of 2^-18, so a P below 2^-7 keeps
 // fewer bits: it is off by 2^-19 at most, 2^-25 of the row's largest weight, which is 2^6 at least.  Keys as the M
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             // a power of two that brings the row's largest element to [128, 256)
             const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
             uint4 hi, lo;
-            split_query(x[y], query_down(amax, e2), &hi, &lo);
+            split_query<false>(x[y], query_down(amax, e2), &hi, &lo);
             if (row < R) {
               // rows of PW bytes in the swizzle of the key tiles: term, then row (N is a multiple of the swizzle's 8 rows)
               const int panel = part / (C::PW / 16), chunk = part % (C::PW / 16);
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             tmem_ld16(st + N + r, v);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[r + e] = __uint_as_float(u[e]) + __uint_as_float(v[e]);
+            for (int e = 0; e < 16; ++e) x[r + e] = fmaf(__uint_as_float(v[e]), 0x1p-5f, __uint_as_float(u[e]));
           }
         }
         tc_fence_before();

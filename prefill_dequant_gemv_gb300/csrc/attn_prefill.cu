@@ -6,9 +6,10 @@
 //   out = sum P_j v_j / sum (P_j / vs_j),   m moving only when a row's maximum has grown by 2^8.
 //
 // Bound by the tensor cores and, about as much, by the softmax's exponentials and conversions, so:
-//   * scores run on the E4M3 tensor cores, the key codes as they come from the cache and a query row as
-//     the sum of two E4M3 terms (bf16's 8 significant bits), which costs what one fp16 product of
-//     converted keys would, without the conversion and at half its shared-memory traffic;
+//   * scores run on the 8-bit tensor cores, the key codes as they come from the cache and a query row as
+//     the sum of an E4M3 and an E5M2 term (bf16's 8 significant bits; the second's exponents keep what is left of small
+//     elements: exact but for those below 2^-13 of the row's largest, off by 2^-21 of it at most), which costs what one
+//     fp16 product of converted keys would, without the conversion and at half its shared-memory traffic;
 //   * P is rounded to fp16 and stays in tensor memory, over the scores it came from, as the A operand
 //     of the second product; splitting it into E4M3 terms would cost three conversions an element where
 //     this needs one, and the value codes are converted once for all rows instead, by a
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       }
     } else if (run && warp == kMma) {  // ------------------------------------------------------ MMAs
       constexpr uint32_t kSwz = D == 64 ? 4 : 2, kHi = desc_hi(8 * C::PW, kSwz), kVHi = desc_hi(1024, 2);
-      constexpr uint32_t kQk = idesc_e4m3(BN, 0, 0), kPv = idesc_f16(D);
+      constexpr uint32_t kQk = idesc_e4m3(BN, 0, 0), kQl = idesc_e4m3(BN, 0, 0, true), kPv = idesc_f16(D);
       const uint32_t q0 = desc_lo(smem_u32(qbuf), 16), k0 = desc_lo(smem_u32(kring), 16);
       const uint32_t v0 = desc_lo(smem_u32(vring), C::VPANEL);
       const int tiles = b.tiles;
@@ -334,8 +335,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
               const uint32_t panel = x * 32 / C::PW, off = x * 32 % C::PW;
-              mma_e4m3<kHi, kHi, kQk>(d, q0 + (m * C::Q + t * 128 * D + panel * 128 * C::PW + off) / 16,
-                                      k0 + (ks * C::KV + panel * BN * C::PW + off) / 16, t + x > 0);
+              const uint32_t qa = q0 + (m * C::Q + t * 128 * D + panel * 128 * C::PW + off) / 16;
+              const uint32_t ka = k0 + (ks * C::KV + panel * BN * C::PW + off) / 16;
+              if (t == 0)
+                mma_e4m3<kHi, kHi, kQk>(d, qa, ka, x > 0);
+              else
+                mma_e4m3<kHi, kHi, kQl>(d, qa, ka, 1);
             }
           mma_commit(&sh.sfull[m * C::SB + sb]);
           mbar_arrive(&sh.sfull[m * C::SB + sb]);  // passes the step's description on
@@ -444,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       const int mt = warp >> 3, half = warp >> 2 & 1, wq = warp & 3;
       const int row = mt * 128 + tid;  // in the block
       const uint32_t lane_base = (uint32_t)(32 * wq) << 16;
-      if (n > 0) {  // the query rows as two E4M3 terms: D / 16 lanes a row
+      if (n > 0) {  // the query rows as two 8-bit terms: D / 16 lanes a row
         // They come by way of the converted values' ring, which nobody needs yet, all at once, and their terms are made in a
         // loop that is not unrolled: what runs once runs as fast as its instructions arrive.
         constexpr int TPR = D / 16, RPP = C::SOFT / TPR, PASSES = C::ROWS / RPP;
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
           // a power of two that brings the row's largest element to [128, 256)
           const int e2 = min(max((__float_as_int(amax) >> 23) - 127 - 7, -125), 125);
           uint4 hi, lo;
-          split_query(v, query_down(amax, e2), &hi, &lo);
+          split_query<true>(v, query_down(amax, e2), &hi, &lo);
           const int panel = part / (C::PW / 16), cc = part % (C::PW / 16);
           const int sw = D == 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
           uint8_t* at = qbuf + qr / 128 * C::Q + panel * 128 * C::PW + qr % 128 * C::PW + sw * 16;

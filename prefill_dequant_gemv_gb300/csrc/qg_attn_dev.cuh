@@ -43,12 +43,18 @@ __device__ __forceinline__ uint32_t codes_f16x2(uint16_t c) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
   return r;
 }
-// F * (h - c) of two fp16 pairs, F 16 or 32: exact where c is h rounded to fewer bits
+__device__ __forceinline__ uint16_t e5m2x2(uint32_t h) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+  return r;
+}
+// F * (h - c) of two fp16 pairs, F 1, 16 or 32: exact where c is h rounded to fewer bits
 template <int F>
 __device__ __forceinline__ uint32_t rest(uint32_t h, uint32_t c) {
-  static_assert(F == 16 || F == 32, "factor");
+  static_assert(F == 1 || F == 16 || F == 32, "factor");
   uint32_t d, r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(h), "r"(c));
+  if (F == 1) return d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(d), "r"(F == 16 ? 0x4C004C00u : 0x50005000u));
   return r;
 }
@@ -66,9 +72,9 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
 // byte offset and swizzle (0 none, 2 128 bytes, 4 64 bytes).  Adding bytes / 16 to the low half moves the start.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr & 0x3FFFFu) >> 4 | (lbo >> 4) << 16; }
 constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return sbo >> 4 | 1u << 14 | swizzle << 29; }
-// kind::f8f6f4, E4M3 x E4M3 -> fp32, M = 128; ta, tb: A, B lie M- or N-contiguous.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int n, int ta, int tb) {
-  return (1u << 4) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
+// kind::f8f6f4, E4M3 (A also E5M2) x E4M3 -> fp32, M = 128; ta, tb: A, B lie M- or N-contiguous.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int n, int ta, int tb, bool a_e5m2 = false) {
+  return (1u << 4) | ((uint32_t)a_e5m2 << 7) | ((uint32_t)ta << 15) | ((uint32_t)tb << 16) | ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 template <uint32_t AHI, uint32_t BHI, uint32_t IDESC>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t alo, uint32_t blo, uint32_t acc) {
@@ -138,32 +144,28 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// 16 elements of a query row (bf16 pairs) times the power of two `down`, as two E4M3 terms.  A bf16 has 8 significant bits:
-// the first term is its upper four, cut off, the second the rest.  Exact but for elements 2^-9 below the row's largest;
-// those are off by 2^-16 of it at most (a term is rounded to a multiple of 2^-9, the largest is 2^7 at least).
-__device__ __forceinline__ uint32_t bf16x2_codes(uint32_t lo, uint32_t hi) {  // two bf16 pairs -> four codes
-  uint16_t a, b;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-      : "=h"(a)
-      : "f"(__uint_as_float(lo & 0xFFFF0000u)), "f"(__uint_as_float(lo << 16)));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-      : "=h"(b)
-      : "f"(__uint_as_float(hi & 0xFFFF0000u)), "f"(__uint_as_float(hi << 16)));
-  return a | (uint32_t)b << 16;
-}
+// 16 elements of a query row (bf16 pairs) times the power of two `down`, as an E4M3 term and one for what is left of
+// them, 8 units of a bf16's last place at most and so 3 significant bits with a sign: E5M2 (WIDE), or E4M3 scaled up by
+// 2^5.  Exact for elements that `down` brings to 2^-6 or more, 2^-13 of the row's largest (which it brings to 2^7 at
+// least); smaller ones, of which the first term has steps of 2^-9, are off by 2^-14 at most (E4M3: 2^-15), 2^-21 of
+// the largest.
+template <bool WIDE>
 __device__ __forceinline__ void split_query(const uint4 (&x)[2], float down, uint4* hi, uint4* lo) {
   const uint32_t v[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
   const uint32_t d = __byte_perm(__float_as_uint(down), 0, 0x3232);
-  uint32_t h[8], l[8];
+  uint32_t h[4] = {0, 0, 0, 0}, l[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     uint32_t y;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(v[e]), "r"(d));
-    h[e] = y & 0xFFF0FFF0u;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(l[e]) : "r"(y), "r"(h[e]));
+    const uint32_t f = f16x2(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u));  // 11 bits hold a bf16's 8
+    const uint16_t c = e4m3x2(f);
+    h[e / 2] |= (uint32_t)c << (16 * (e & 1));
+    const uint32_t left = codes_f16x2(c);
+    l[e / 2] |= (uint32_t)(WIDE ? e5m2x2(rest<1>(f, left)) : e4m3x2(rest<32>(f, left))) << (16 * (e & 1));
   }
-  *hi = make_uint4(bf16x2_codes(h[0], h[1]), bf16x2_codes(h[2], h[3]), bf16x2_codes(h[4], h[5]), bf16x2_codes(h[6], h[7]));
-  *lo = make_uint4(bf16x2_codes(l[0], l[1]), bf16x2_codes(l[2], l[3]), bf16x2_codes(l[4], l[5]), bf16x2_codes(l[6], l[7]));
+  *hi = make_uint4(h[0], h[1], h[2], h[3]);
+  *lo = make_uint4(l[0], l[1], l[2], l[3]);
 }
 // The largest magnitude of 16 bf16 elements; NaN does not count.
 __device__ __forceinline__ float query_max(const uint4 (&x)[2]) {

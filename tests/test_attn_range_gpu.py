@@ -104,3 +104,30 @@ def test_pages_of_key_scale_zero_17_to_32_rows(d, hkv, hq, page, new):
             c.ks[c.pages[b, i], b % hkv] = 0.0
             c.vc[c.pages[b, i], b % hkv, :, 3::7] = 0xFF
     _check_hidden(q, c, hq, 0)
+
+
+# ------------------------------------------------------------------ queries with a channel far above the others
+@pytest.mark.parametrize("d,page,hkv,hq,news,lens", [
+    (128, 64, 2, 10, [1, 1], [900, 300]), (64, 16, 1, 8, [2], [500]), (256, 32, 1, 6, [4], [700]),
+    (128, 64, 2, 8, [100], [700]), (64, 32, 1, 16, [60], [500]), (256, 64, 1, 4, [70], [400])])
+@pytest.mark.parametrize("size", [64.0, 512.0, 2048.0, 65536.0])
+def test_queries_with_outlier_channels(d, page, hkv, hq, news, lens, size):
+    """Keys are small in those channels.  An element of 2^-13 of its row's largest or more is exact, a smaller one off by 2^-21
+    of the largest at most; the scores' bound takes that beside their fp32 roundings."""
+    q = qlib()
+    c = Case(d + int(size), news, lens, page, hkv, d)
+    out = c.rng.integers(0, d, 2)
+    k = oa.e4m3_decode(c.kc[..., out])
+    c.kc[..., out] = np.where(np.isnan(k), c.kc[..., out], oa.e4m3_encode(np.nan_to_num(k) / size))
+    qh = c.heads(hq)
+    qh[..., out] = (size * (1 + torch.from_numpy(c.rng.random((c.n, hq, 2))))).to(torch.bfloat16)
+    cache, batch = c.device(q)
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, c.n, hq))
+    got = q.attention(cache, batch, qh.cuda(), scale=2 * d ** -0.5, workspace=ws)
+    assert ws.status() == 0
+    ref = list(c.attention(qh, 2 * d ** -0.5))
+    x = np.abs(to_f64(qh))
+    top = x.max(-1, keepdims=True)
+    off = torch.from_numpy(np.where(x < top * 2.0 ** -13, top * 2.0 ** -21, 0.0)).float()
+    ref[2] = ref[2] + c.attention(off, 2 * d ** -0.5)[2] / (2 * d * 2.0 ** -24)  # (attention_bound's factor of it)
+    check_attention(got, ref, d, max(lens))
