@@ -2,7 +2,7 @@
 // takes MT tiles of 128 query rows of one (sequence, KV head) -- row = token * G + query head, so the G
 // heads share what is loaded -- through the keys that they see, BN at a time, with an online softmax.
 //
-// The mathematics is the few-row kernel's: t_j = scale * ks_j * (q . k_j) * log2(e) + log2(vs_j), P_j = 2^(t_j - m),
+// The mathematics is the few-row kernel's: t_j = scale * ks_j * (q . k_j) * log2(e) + log2(vs_j), P_j = 2^(t_j - m + 7),
 //   out = sum P_j v_j / sum (P_j / vs_j),   m moving only when a row's maximum has grown by 2^8.
 //
 // Bound by the tensor cores and, about as much, by the softmax's exponentials and conversions, so:
@@ -10,7 +10,7 @@
 //     the sum of an E4M3 and an E5M2 term (bf16's 8 significant bits; the second's exponents keep what is left of small
 //     elements: exact but for those below 2^-13 of the row's largest, off by 2^-21 of it at most), which costs what one
 //     fp16 product of converted keys would, without the conversion and at half its shared-memory traffic;
-//   * P is rounded to fp16 and stays in tensor memory, over the scores it came from, as the A operand
+//   * P is rounded to fp16 (11 bits of it, or 2^-32 of the row's largest weight) and stays in tensor memory, over the scores it came from, as the A operand
 //     of the second product; splitting it into E4M3 terms would cost three conversions an element where
 //     this needs one, and the value codes are converted once for all rows instead, by a
 //     warpgroup of their own, into the fp16 tile that the second product reads transposed;
@@ -41,7 +41,10 @@
 namespace qg {
 namespace {
 
-constexpr float kLazy = 8.0f;  // P stays below 2^8
+constexpr float kLazy = 8.0f;           // a row's reference moves when its maximum has grown by this
+// P of a key at the reference is 2^7 and below 2^15 then, what fp16 holds: 11 bits down to 2^-21 of the reference's
+// weight, and off by 2^-32 of it below.  The sums take P * 2^-7, so that they have the room of plain weights.
+constexpr float kBias = 7.0f, kUnbias = 0x1p-7f;
 
 template <int D>
 struct Cfg {
@@ -69,7 +72,7 @@ struct Cfg {
 };
 
 struct StepMeta {
-  float ks[8], lvs[8], ivs[8];  // scale, log2 and reciprocal of the value scale of each 16 keys; ks 0: hidden
+  float ks[8], lvs[8], ivs[8];  // scale, log2 and reciprocal (times kUnbias) of the value scale of each 16 keys; ks 0: hidden
   int cut, pad[7];              // some of its keys are hidden
 };
 // What the CTA works on.  It stays in shared memory: registers are for scores.
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         if (lane < NG) {
           m.ks[lane] = sk;
           m.lvs[lane] = seen ? lg2(sv) : 0.0f;
-          m.ivs[lane] = seen ? rcp(sv) : 0.0f;
+          m.ivs[lane] = seen ? rcp(sv) * kUnbias : 0.0f;
         }
         if (lane == 0) m.cut = cut;
         __syncwarp();
@@ -565,7 +568,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
             tmem_st_wait();
           }
         }
-        const float ref = m == -INFINITY ? 0.0f : m;
+        const float ref = (m == -INFINITY ? 0.0f : m) - kBias;
         // two groups at a time
 #pragma unroll
         for (int gr = 0; gr < GH; gr += 2) {
@@ -618,7 +621,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         // 16-byte piece of a row from each lane took 9300 cycles from here to the CTA's end, this 6000 (heads of 128).
         const bool in = row < b.R, parts = pa.splits > 1;
         const int tok = token_of(b, row), g = b.rem0 + row - tok * G;
-        const float inv = parts ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = parts ? 1.0f : l == 0.0f ? 0.0f : kUnbias / l;
         const int64_t part = blockIdx.x;  // of (block, head), split by split
         const bool poison = sh.poison;
         const int64_t at = parts ? ((part * C::ROWS + row) * D + half * (D / 2)) * 4
@@ -708,7 +711,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       for (int k = 0; k < 8; ++k) o[k] = fmaf(y[k], f, o[k]);
       l = fmaf(z.y, f, l);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float inv = l == 0.0f ? 0.0f : kUnbias / l;
     const int tok = token_of(b, row), g = b.rem0 + row - tok * G;
     *reinterpret_cast<uint4*>(a.out + (int64_t)(tok0 + tok) * a.ldo + (int64_t)(head * G + g) * a.hso + d) =
         make_uint4(bf16x2(o[0] * inv, o[1] * inv), bf16x2(o[2] * inv, o[3] * inv), bf16x2(o[4] * inv, o[5] * inv),

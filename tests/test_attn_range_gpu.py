@@ -59,6 +59,14 @@ def test_weights_far_below_the_largest_streaming(d, hkv, hq, new, n_seqs, length
     _check_sink(d, hkv, hq, new, n_seqs, length, gap, value, noise, 2.0 ** -25)
 
 
+@pytest.mark.parametrize("d,hkv,hq,new,n_seqs,length,gap,value,noise", [
+    (128, 2, 8, 40, 8, 20001, 14.5, 0.0, 0.0), (64, 1, 16, 20, 160, 20001, 14.5, -1.0, 0.0), (256, 1, 6, 50, 2, 20001, 13.0, 0.0, 0.0),
+    (128, 1, 8, 33, 1, 60001, 16.0, 0.0, 0.0)])
+def test_weights_far_below_the_largest_row_blocks(d, hkv, hq, new, n_seqs, length, gap, value, noise):
+    # P is 2^7 or more at the largest weight, in fp16: off by 2^-25 at most
+    _check_sink(d, hkv, hq, new, n_seqs, length, gap, value, noise, 2.0 ** -32)
+
+
 # ------------------------------------------------------------------ pages whose key scale is 0
 @pytest.mark.parametrize("d,page,hkv,hq,news,lens,window", [
     (128, 64, 2, 10, [1, 1], [900, 300], 0), (64, 16, 4, 32, [1, 2], [1000, 400], 0), (256, 128, 1, 6, [2, 1], [1200, 640], 0),
