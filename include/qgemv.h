@@ -163,7 +163,9 @@ size_t qg_gemv_workspace_size(int fmt, int64_t n, int64_t k, int m);
 qg_status qg_workspace_init(void* workspace, size_t bytes, void* stream);
 
 /* Read (and clear) the device status word at the start of a workspace: QG_OK, or
- * QG_ERR_TIMEOUT if a bounded wait inside a kernel gave up.  Synchronises `stream`. */
+ * QG_ERR_TIMEOUT if a bounded wait inside a kernel gave up.  Synchronises `stream`.  A call
+ * that gave up may have left counters behind: after QG_ERR_TIMEOUT the workspace must be
+ * zero-filled (qg_workspace_init) before its next use. */
 qg_status qg_workspace_status(void* workspace, int* status, void* stream);
 
 /* Quantized GEMV for 1..4 activation rows (speculative-verify widths):
@@ -438,8 +440,8 @@ size_t qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  * scale is 0.  NaN codes that it sees, and NaN or infinite queries, give NaN as the formula does.  Scores are
  * fp32 numbers: |scale * q . k| below 2^120.  A query row is taken relative to its largest element: elements of
  * 2^-13 of it or more exactly, smaller ones to 2^-21 of it.  G is at most 128.
- * The workspace must be zero-filled before its first use; every qattn call, of any sizes that it has room for,
- * leaves it ready for the next one; calls that overlap on the GPU must not share it, and no other
+ * The workspace must be zero-filled before its first use and after QG_ERR_TIMEOUT; every other qattn call, of any
+ * sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not share it, and no other
  * entry point may use it in between.  QG_ERR_UNSUPPORTED where a call's work passes 32-bit counts
  * (2^26 row blocks, or 2^31 tiles of 128 keys over all sequences and KV heads).  Deterministic. */
 qg_status qattn(const qg_kv_cache* cache, const qg_kv_batch* batch, int64_t n_tokens, int n_q_heads,

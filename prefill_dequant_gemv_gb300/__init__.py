@@ -322,7 +322,12 @@ class Workspace:
         return self.buf.data_ptr()
 
     def status(self) -> int:
-        return qg_workspace_status(self.ptr, _stream_ptr())
+        """The status word, read and cleared; after a wait that gave up the whole workspace is zeroed, as the kernels'
+        counters may have been left behind."""
+        st = qg_workspace_status(self.ptr, _stream_ptr())
+        if st == 6:
+            self.buf.zero_()
+        return st
 
 
 def dequant(pw: PackedWeight, out_dtype: int = OUT_F32):

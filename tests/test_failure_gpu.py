@@ -26,3 +26,15 @@ def test_bounded_wait_times_out_and_context_survives():
     ref, _ = oracle.gemv(w, x)
     tol = oracle.tolerance(w, x, None, ref=ref)
     assert np.all(np.abs(to_f64(y) - ref) <= tol)
+
+
+def test_a_workspace_is_ready_again_after_a_wait_gave_up():
+    """Counters that a call which gave up has left behind must not reach the next one."""
+    q = qlib()
+    ws = q.Workspace(4096)
+    ws.buf[256:] = 1  # as tickets taken by some CTAs only would be
+    q.qg_selftest_wait_timeout(ws.ptr, ws.nbytes, 0)
+    assert q.STATUS[ws.status()] == "QG_ERR_TIMEOUT"
+    assert not ws.buf.any()
+    ws.buf[256:] = 1
+    assert ws.status() == 0 and bool((ws.buf[256:] == 1).all())  # otherwise it stays as it is
