@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   bool bad = false;
   int most = 0;
   const int total = w.count(a, lane, &bad, &most) * c.hkv;  // places
-  if (bad && warp == 0 && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
+  if (bad && warp == 0 && blockIdx.x == 0) atomicMax(c.status, kStatusInvalid);
   // with no more CTAs than places, each has one at least
   const int grid = min((int)gridDim.x, total), cta = blockIdx.x;
   const Share share = {total / max(grid, 1), total % max(grid, 1)};
@@ -496,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             bool ok = tok < clen;
             if (ok && (cid < 0 || cid >= c.n_pages)) {
               ok = false;
-              atomicExch(c.status, kStatusInvalid);
+              atomicMax(c.status, kStatusInvalid);
             }
             const int64_t tile = (int64_t)cid * c.hkv + chead;
             TileMeta& m = sh.tile[i % C::METAS];

@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
       if (base + lane < c.n_seqs) s = seq_of(c, base + lane, &bad);
       total += __reduce_add_sync(0xFFFFFFFFu, blocks_of(s));
     }
-    if (bad && blockIdx.x == 0) atomicExch(c.status, kStatusInvalid);
+    if (bad && blockIdx.x == 0) atomicMax(c.status, kStatusInvalid);
     int left = total - 1 - block;
     int ok = left >= 0;
     for (int base = 0; ok && base < c.n_seqs; base += 32) {
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1)
         bool ok = lane < NG && tok < key1;
         if (ok && (id < 0 || id >= c.n_pages)) {
           ok = false;
-          atomicExch(c.status, kStatusInvalid);
+          atomicMax(c.status, kStatusInvalid);
         }
         const int64_t tile = (int64_t)id * c.hkv + head;
         float sk = 0.0f, sv = 0.0f;

@@ -255,13 +255,13 @@ __device__ __forceinline__ void append_unit(const AppendArgs& a, int64_t unit, i
       }
     }
   }
-  if (bad && c.status) atomicExch(c.status, kStatusInvalid);
+  if (bad && c.status) atomicMax(c.status, kStatusInvalid);
   if (j < 0) return;
   const int P = 1 << c.page_log2, first = s.len - s.rows;
   const int pi = (first >> c.page_log2) + j;
   const int id = c.pages[(int64_t)b * c.page_stride + pi];
   if (id < 0 || id >= c.n_pages) {
-    if (g == 0 && c.status) atomicExch(c.status, kStatusInvalid);
+    if (g == 0 && c.status) atomicMax(c.status, kStatusInvalid);
     return;
   }
   const int base = pi << c.page_log2;

@@ -139,3 +139,20 @@ def test_queries_with_outlier_channels(d, page, hkv, hq, news, lens, size):
     off = torch.from_numpy(np.where(x < top * 2.0 ** -13, top * 2.0 ** -21, 0.0)).float()
     ref[2] = ref[2] + c.attention(off, 2 * d ** -0.5)[2] / (2 * d * 2.0 ** -24)  # (attention_bound's factor of it)
     check_attention(got, ref, d, max(lens))
+
+
+# ------------------------------------------------------------------ statuses
+def test_a_bad_batch_does_not_hide_a_wait_that_gave_up():
+    q = qlib()
+    c = Case(21, [1], [40], 16, 1, 64)
+    cache, batch = c.device(q)
+    batch.pages[0, 0] = 2 ** 31 - 1
+    qh = c.heads(2).cuda()
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, 1, 2))
+    for call in (lambda: q.attention(cache, batch, qh, workspace=ws),
+                 lambda: q.kv_append(cache, q.KVBatch(batch.q_start, batch.lens, batch.pages, 1, 8), qh, qh[:, :1], qh[:, :1], workspace=ws)):
+        q.qg_selftest_wait_timeout(ws.ptr, ws.nbytes, torch.cuda.current_stream().cuda_stream)
+        call()
+        assert q.STATUS[ws.status()] == "QG_ERR_TIMEOUT"
+        call()
+        assert q.STATUS[ws.status()] == "QG_ERR_INVALID_ARG"
