@@ -435,7 +435,8 @@ size_t qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  *   out[i][h] = bf16( sum_t softmax_t(scale * q[i][h] . k[t][h / G]) v[t][h / G] ),
  *   t in max(0, p - window + 1) .. p,  p the position of row i, G = n_q_heads / n_kv_heads.
  * window 0: no window.  A row that sees no key (p < 0, or lens 0) is zero.  scale is finite and > 0.
- * q and out: bf16, strides as in qkv_append; rows of no sequence are left as they are.
+ * q and out: bf16, strides as in qkv_append; out may be q itself with the same strides; rows of no sequence are
+ * left as they are.
  * Keys that a row does not see, whatever their bits, do not enter it, and neither do tokens of a page whose key
  * scale is 0.  NaN codes that it sees, and NaN or infinite queries, give NaN as the formula does.  Scores are
  * fp32 numbers: |scale * q . k| below 2^120.  A query row is taken relative to its largest element: elements of

@@ -170,6 +170,7 @@ extern "C" qg_status qattn(const qg_kv_cache* cache, const qg_kv_batch* batch, i
   if (st == QG_OK) st = check_heads(q, ldq, hsq, n_tokens, n_q_heads, cache->head_dim);
   if (st == QG_OK) st = check_heads(out, ldo, hso, n_tokens, n_q_heads, cache->head_dim);
   if (st != QG_OK) return (qg_status)st;
+  if (q == out && (ldq != ldo || hsq != hso)) return QG_ERR_INVALID_ARG;
   if (!workspace) return QG_ERR_INVALID_ARG;
   if (!aligned16(workspace)) return QG_ERR_MISALIGNED;
   DeviceInfo dev;

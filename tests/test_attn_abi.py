@@ -123,3 +123,8 @@ def test_python_helpers_refuse_wrong_tensors(q):
             bad()
         assert e.value.status == INVALID
     assert isinstance(kv.desc, ctypes.Structure)
+
+
+def test_attention_in_place_needs_the_same_strides(q):
+    for over in (dict(ldo=1024), dict(hso=256, ldo=1024), dict(ldq=1024)):
+        assert attn(q, out=0x10000, **over) == INVALID

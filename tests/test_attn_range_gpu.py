@@ -156,3 +156,19 @@ def test_a_bad_batch_does_not_hide_a_wait_that_gave_up():
         assert q.STATUS[ws.status()] == "QG_ERR_TIMEOUT"
         call()
         assert q.STATUS[ws.status()] == "QG_ERR_INVALID_ARG"
+
+
+# ------------------------------------------------------------------ in place
+@pytest.mark.parametrize("d,hkv,hq,page,news,lens", [
+    (128, 2, 10, 64, [1] * 40, [1000 + 50 * i for i in range(40)]), (256, 4, 24, 64, [4], [6000]), (64, 4, 8, 32, [1, 1], [70, 5]),
+    (128, 2, 8, 64, [300, 70], [900, 70]), (256, 1, 6, 32, [60], [5000]), (64, 2, 16, 16, [200, 1], [201, 600])])
+def test_attention_over_its_own_queries(d, hkv, hq, page, news, lens):
+    q = qlib()
+    c = Case(sum(lens), news, lens, page, hkv, d)
+    qh = c.heads(hq).cuda()
+    cache, batch = c.device(q)
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, c.n, hq))
+    want = q.attention(cache, batch, qh, workspace=ws)
+    fused = torch.cat([qh, torch.full((c.n, 2 * hkv, d), 3.0, dtype=torch.bfloat16, device="cuda")], 1)
+    got = q.attention(cache, batch, fused[:, :hq], out=fused[:, :hq], workspace=ws)
+    assert ws.status() == 0 and torch.equal(got, want) and bool((fused[:, hq:] == 3.0).all())
