@@ -354,7 +354,8 @@ qg_status qgemm_grouped(const qg_moe_layer* layer, int stage, const void* in, in
  * The cache is a pool of pages of page_tokens tokens each.  Keys and values are E4M3 codes with
  * one fp32 scale per (page, KV head), value = code * scale:
  *   k_codes, v_codes   : uint8 [n_pages][n_kv_heads][page_tokens][head_dim]
- *   k_scales, v_scales : fp32 [n_pages][n_kv_heads], positive and finite in every page in use
+ *   k_scales, v_scales : fp32 [n_pages][n_kv_heads], 2^-100 to 2^120 in every page in use (what
+ *                        qkv_append writes; other writers keep to it)
  * A sequence's token t lies in row t % page_tokens of page pages[t / page_tokens].
  * page_tokens is 16, 32, 64 or 128; head_dim 64, 128 or 256. */
 typedef enum { QG_KV_E4M3 = 1 } qg_kv_format;
@@ -440,7 +441,9 @@ size_t qattn_workspace_size(const qg_kv_cache* cache, const qg_kv_batch* batch, 
  * Keys that a row does not see, whatever their bits, do not enter it, and neither do tokens of a page whose key
  * scale is 0.  NaN codes that it sees, and NaN or infinite queries, give NaN as the formula does.  Scores are
  * fp32 numbers: |scale * q . k| below 2^120.  A query row is taken relative to its largest element: elements of
- * 2^-13 of it or more exactly, smaller ones to 2^-21 of it.  G is at most 128.
+ * 2^-13 of it or more exactly, smaller ones to 2^-21 of it.  A weight times its value scale is kept to 11 bits, or
+ * to 2^-25 of the row's largest such product; one below 2^-126 of it counts as 0, so the value scales that a row sees
+ * should lie within 2^100 of one another.  G is at most 128.
  * The workspace must be zero-filled before its first use and after QG_ERR_TIMEOUT; every other qattn call, of any
  * sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not share it, and no other
  * entry point may use it in between.  QG_ERR_UNSUPPORTED where a call's work passes 32-bit counts

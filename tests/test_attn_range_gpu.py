@@ -172,3 +172,38 @@ def test_attention_over_its_own_queries(d, hkv, hq, page, news, lens):
     fused = torch.cat([qh, torch.full((c.n, 2 * hkv, d), 3.0, dtype=torch.bfloat16, device="cuda")], 1)
     got = q.attention(cache, batch, fused[:, :hq], out=fused[:, :hq], workspace=ws)
     assert ws.status() == 0 and torch.equal(got, want) and bool((fused[:, hq:] == 3.0).all())
+
+
+# ------------------------------------------------------------------ page scales at the ends of their range
+@pytest.mark.parametrize("d,page,hkv,hq,news,lens", [
+    (128, 16, 2, 6, [1, 1], [500, 90]), (256, 64, 1, 6, [4], [700]), (64, 16, 2, 16, [100, 30], [260, 1000]),
+    (256, 32, 1, 4, [70], [3000]), (128, 32, 1, 5, [40], [3000])])
+@pytest.mark.parametrize("ends", ["low", "high", "apart"])
+def test_scales_at_both_ends(d, page, hkv, hq, news, lens, ends):
+    """Value scales of 2^-100, of 2^120, and 2^100 apart (pages of zeros beside others); key scales likewise, with queries
+    to match."""
+    q = qlib()
+    c = Case(d + sum(lens), news, lens, page, hkv, d)
+    small = lambda codes: np.where(np.isnan(oa.e4m3_decode(codes)), codes, oa.e4m3_encode(np.nan_to_num(oa.e4m3_decode(codes)) / 64))  # noqa: E731
+    qh, scale = c.heads(hq), d ** -0.5
+    if ends == "low":
+        c.ks *= np.float32(2.0 ** -90)
+        c.vs[:] = 2.0 ** -100
+        scale *= 2.0 ** 90
+    elif ends == "high":
+        c.ks *= np.float32(2.0 ** 120)
+        c.vc = small(c.vc)  # so that the outputs are finite
+        c.vs[:] = 2.0 ** 120
+        qh = (qh.float() * 2.0 ** -100).to(torch.bfloat16)
+        scale *= 2.0 ** -20
+    else:
+        dead = c.rng.random(c.vs.shape) < 0.5
+        c.vs[dead] = 2.0 ** -100
+        c.vc[dead] = np.where(np.isnan(oa.e4m3_decode(c.vc[dead])), c.vc[dead], 0)
+    cache, batch = c.device(q)
+    ws = q.Workspace(q.attention_workspace_size(cache, batch, c.n, hq))
+    got = q.attention(cache, batch, qh.cuda(), scale=scale, workspace=ws)
+    assert ws.status() == 0
+    ref = c.attention(qh, scale)
+    assert np.abs(ref[0]).max() < 2.0 ** 127 and np.abs(ref[0]).max() > 0
+    check_attention(got, ref, d, max(lens))
