@@ -767,6 +767,8 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             tmem_ld16(st + r, u);
             tmem_ld16(st + N + r, v);
             tmem_ld_wait();
+            tmem_arrived(u);
+            tmem_arrived(v);
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[r + e] = fmaf(__uint_as_float(v[e]), 0x1p-5f, __uint_as_float(u[e]));
           }
@@ -853,6 +855,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
               tmem_ld_wait();
 #pragma unroll
               for (int e = 0; e < 3 * C::MB; ++e) {
+                tmem_arrived(u[e]);
 #pragma unroll
                 for (int z = 0; z < 4; ++z) u[e][z] = __float_as_uint(__uint_as_float(u[e][z]) * (r + z < R ? ws[z] : 0.0f));
                 tmem_st4(ot + e * N + r, u[e]);
@@ -974,6 +977,10 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
 #pragma unroll
             for (int t = 0; t < 3; ++t) tmem_ld4(otm + lane_base + set * C::OSET + (gq * C::MB + mb) * C::OCOL + t * N + r, v[gq][t]);
           tmem_ld_wait();
+#pragma unroll
+          for (int gq = 0; gq < NG; ++gq)
+#pragma unroll
+            for (int t = 0; t < 3; ++t) tmem_arrived(v[gq][t]);
           float o[4] = {0, 0, 0, 0};
 #pragma unroll
           for (int gq = 0; gq < NG; ++gq) {

@@ -195,6 +195,7 @@ __device__ __forceinline__ void tmem_ld_now(uint32_t taddr, uint32_t (&v)[64]) {
       : "r"(taddr), "r"(taddr + 32)
       : "memory");
 }
+// tmem_ld_wait that the given registers pass through, so that no use of them moves before it.
 __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&v)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
@@ -202,7 +203,12 @@ __device__ __forceinline__ void tmem_ld_wait16(uint32_t (&v)[16]) {
                :
                : "memory");
 }
-// tmem_ld_wait that the given registers pass through, so that no use of them moves before it.
+// The same behind a tmem_ld_wait for several arrays: no use of v is moved before this, nor this before the wait.
+template <int N>
+__device__ __forceinline__ void tmem_arrived(uint32_t (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
 
 // ---------------------------------------------------------------- TMA
 // 2-D tile load; c0 is the innermost (contiguous) coordinate in elements and must be a
