@@ -355,7 +355,8 @@ qg_status qgemm_grouped(const qg_moe_layer* layer, int stage, const void* in, in
  * one fp32 scale per (page, KV head), value = code * scale:
  *   k_codes, v_codes   : uint8 [n_pages][n_kv_heads][page_tokens][head_dim]
  *   k_scales, v_scales : fp32 [n_pages][n_kv_heads], 2^-100 to 2^120 in every page in use (what
- *                        qkv_append writes; other writers keep to it)
+ *                        qkv_append writes; other writers keep to it); a key scale of 0
+ *                        hides its page from qattn
  * A sequence's token t lies in row t % page_tokens of page pages[t / page_tokens].
  * page_tokens is 16, 32, 64 or 128; head_dim 64, 128 or 256. */
 typedef enum { QG_KV_E4M3 = 1 } qg_kv_format;

@@ -313,7 +313,7 @@ __device__ __noinline__ void join_parts(const DecodeArgs& da, int R, int G, int6
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         for (int q = lane; q < parts; q += 32) {
           const float z = wt[q * N + row];
-          wt[q * N + row] = z == -INFINITY ? 0.0f : ex2(z - top) * inv;
+          wt[q * N + row] = ex2(z - top) * inv;
         }
       }
       named_sync(15, T);
@@ -327,9 +327,8 @@ __device__ __noinline__ void join_parts(const DecodeArgs& da, int R, int G, int6
 #pragma unroll 4
       for (int q = 0; q < parts; ++q) {
         const float4 y = *reinterpret_cast<const float4*>(buf + (q * floats + e) * 4);
-        const float f = wt[q * N + row];
-        if (f != 0.0f)  // a part without a key holds anything
-          v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
+        const float f = wt[q * N + row];  // (a part of no weight may hold a NaN that its row sees)
+        v.x = fmaf(y.x, f, v.x), v.y = fmaf(y.y, f, v.y), v.z = fmaf(y.z, f, v.z), v.w = fmaf(y.w, f, v.w);
       }
       const __nv_bfloat162 y0 = __floats2bfloat162_rn(v.x, v.y), y1 = __floats2bfloat162_rn(v.z, v.w);
       *reinterpret_cast<uint2*>(a.out + base + t * a.ldo + g * a.hso + d) =
@@ -947,7 +946,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
         const int n_tiles = pm.n_tiles, parts_here = min(NG, i1 - i0);
         const bool whole = pm.skipped == 0 && i1 - i0 == n_tiles;
         const int slot = 2 * cta + (i0 == 0 ? 0 : 1);
-        // row's factors of the groups (0 without a tile of this pair), and its reference and sum
+        // row's factors of the groups (below 0 without a tile of this pair), and its reference and sum
         if (tid < R) {
           float top = -INFINITY, sum = 0.0f, m[NG];
 #pragma unroll
@@ -958,8 +957,9 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
           }
 #pragma unroll
           for (int gq = 0; gq < NG; ++gq) {
-            const float f = m[gq] == -INFINITY ? 0.0f : ex2(m[gq] - top);
-            if (f != 0.0f) sum = fmaf(sh.sum[set][gq][tid], f, sum);
+            const bool none = m[gq] == -INFINITY;
+            const float f = none ? -1.0f : ex2(m[gq] - top);
+            if (!none && f != 0.0f) sum = fmaf(sh.sum[set][gq][tid], f, sum);
             sh.factor[gq][tid] = f;
           }
           if (whole)
@@ -990,7 +990,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
             for (int z = 0; z < 4; ++z) {
               const float y = fmaf(__uint_as_float(v[gq][2][z]), 0x1p-9f,
                                    fmaf(__uint_as_float(v[gq][1][z]), 0x1p-4f, __uint_as_float(v[gq][0][z])));
-              if (f[z] != 0.0f) o[z] = fmaf(y, f[z], o[z]);  // a group without a tile of this pair holds anything
+              if (!(f[z] < 0.0f)) o[z] = fmaf(y, f[z], o[z]);  // a group without a tile of this pair holds anything
             }
           }
           if (d < D) {

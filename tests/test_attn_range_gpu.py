@@ -207,3 +207,28 @@ def test_scales_at_both_ends(d, page, hkv, hq, news, lens, ends):
     ref = c.attention(qh, scale)
     assert np.abs(ref[0]).max() < 2.0 ** 127 and np.abs(ref[0]).max() > 0
     check_attention(got, ref, d, max(lens))
+
+
+# ------------------------------------------------------------------ NaN values of no weight
+@pytest.mark.parametrize("d,hkv,hq,new,n_seqs,length", [
+    (128, 2, 10, 1, 1, 20001), (256, 1, 6, 4, 1, 20001), (64, 1, 8, 1, 200, 2001), (128, 1, 16, 2, 160, 3001), (64, 1, 16, 20, 1, 20001),
+    (256, 1, 6, 40, 40, 3001)])
+def test_nan_values_of_no_weight(d, hkv, hq, new, n_seqs, length):
+    """A key 150 nats above all others, whose weights are 0 in fp32: a NaN value code among them is a NaN in its dim all the
+    same, wherever the work is cut between the two keys."""
+    q = qlib()
+    page, kc, vc, ones, x, scale = _sink(d, hkv, hq, new, length, 150.0, 0.5, 0.0, d + new)
+    rng = np.random.default_rng(new)
+    dims = rng.permutation(d)[:12]
+    for i, dim in enumerate(dims):
+        at = (length - new) * (i + 1) // 13  # (a key that every row sees)
+        vc[at // page, :, at % page, dim] = 0x7F
+    t = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
+    cache = q.KVCache(t(kc), t(vc), t(ones), t(ones.copy()))
+    batch = q.KVBatch(torch.arange(0, n_seqs * new + 1, new, dtype=torch.int32, device="cuda"),
+                      torch.full((n_seqs,), length, dtype=torch.int32, device="cuda"),
+                      t(np.tile(np.arange(len(kc), dtype=np.int32), (n_seqs, 1))), new, length)
+    got = to_f64(q.attention(cache, batch, x.repeat(n_seqs, 1, 1).cuda(), scale))
+    want = np.full(d, 0.5)
+    want[dims] = np.nan
+    assert np.array_equal(got, np.broadcast_to(want, got.shape), equal_nan=True)
