@@ -316,6 +316,7 @@ class Workspace:
         import torch
         self.nbytes = max(int(nbytes), 256)
         self.buf = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        self.index = self.buf.get_device()
 
     @property
     def ptr(self) -> int:
@@ -541,7 +542,8 @@ class KVCache:
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.n_pages, self.n_kv_heads, self.page_tokens, self.head_dim = (int(x) for x in k_codes.shape)
         # what each call needs of torch, looked up once: calls of a decode step are short
-        self.bf16, self.index = torch.bfloat16, k_codes.get_device()  # (a CPU's is -1)
+        self.bf16 = torch.bfloat16
+        self.index = k_codes.get_device() if k_codes.is_cuda else -2  # where no tensor is
         self.raw_stream = _raw_stream_getter()
         self.desc = qg_kv_cache(QG_KV_E4M3, self.page_tokens, self.n_kv_heads, self.head_dim, self.n_pages,
                                 k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr())
@@ -603,12 +605,11 @@ class NormRope:
                                  0 if cos_sin is None else cos_sin.shape[1], 1 if interleaved else 0)
 
 
-def _together(cache, batch, workspace, what):
-    """What the descriptors alone do not tell: the width of the page table, and where the tensors are."""
+def _refuse(cache, batch, what):
+    """What the descriptors do not tell: the width of the page table, and where the tensors are."""
     if batch.max_len > batch.width * cache.page_tokens:
         raise QGError(1, f"{what}: max_len {batch.max_len} takes more than the {batch.width} pages a sequence of the table")
-    if cache.index < 0 or batch.index != cache.index or (workspace is not None and workspace.buf.get_device() != cache.index):
-        raise QGError(1, f"{what}: cache, batch and workspace on one CUDA device")
+    raise QGError(1, f"{what}: cache, batch and workspace on one CUDA device")
 
 
 def _heads(t, n, heads, cache, what):
@@ -626,7 +627,9 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, norm_rope: Optional[NormR
     """Norm and rotate the new tokens' q and k (bf16 [n, heads, head_dim]), write k and v into the cache and
     return the queries (``qkv_append``).  q may be None: only the cache is written."""
     hkv = cache.n_kv_heads
-    _together(cache, batch, workspace, "kv_append")
+    if (batch.max_len > batch.width * cache.page_tokens or batch.index != cache.index
+            or (workspace is not None and workspace.index != cache.index)):
+        _refuse(cache, batch, "kv_append")
     kp, ldk, hsk = _heads(k, None, hkv, cache, "kv_append: k")
     n = k.shape[0]
     vp, ldv, hsv = _heads(v, n, hkv, cache, "kv_append: v")
@@ -641,8 +644,10 @@ def kv_append(cache: KVCache, batch: KVBatch, q, k, v, norm_rope: Optional[NormR
     nr = None
     if norm_rope is not None:
         nr = norm_rope.desc
-        _need(norm_rope.dim in (None, cache.head_dim), "kv_append: norm weights of head_dim elements")
-        _need(norm_rope.index in (None, cache.index), "kv_append: norm weights and rotation table on the cache's device")
+        if norm_rope.dim is not None and norm_rope.dim != cache.head_dim:
+            raise QGError(1, "kv_append: norm weights of head_dim elements")
+        if norm_rope.index is not None and norm_rope.index != cache.index:
+            raise QGError(1, "kv_append: norm weights and rotation table on the cache's device")
     if workspace is None:
         workspace = Workspace(qkv_append_workspace_size(), k.device)
     st = (_lib or lib()).qkv_append(cache.desc, batch.desc, nr, n, hq, qp, ldq, hsq, kp, ldk, hsk, vp, ldv, hsv, op, ldo, hso,
@@ -661,7 +666,9 @@ def attention(cache: KVCache, batch: KVBatch, q, scale: Optional[float] = None, 
               workspace: Optional[Workspace] = None):
     """Causal attention of the new tokens q (bf16 [n, heads, head_dim]) over the cache (``qattn``);
     scale is 1/sqrt(head_dim) unless given, window 0 means none."""
-    _together(cache, batch, workspace, "attention")
+    if (batch.max_len > batch.width * cache.page_tokens or batch.index != cache.index
+            or (workspace is not None and workspace.index != cache.index)):
+        _refuse(cache, batch, "attention")
     qp, ldq, hsq = _heads(q, None, None, cache, "attention: q")
     n, hq, d = q.shape
     if out is None:
