@@ -1,10 +1,13 @@
 // qattn's dispatch: few rows a KV head stream the cache, more take row blocks through it.
 //
-// Up to 16 rows the streaming kernel is the faster one from one sequence of 1000 keys (16.8 us, row blocks 19.8;
-// 5 rows, 8 KV heads of 128) to 16 of 8000 (62 against 122).  With 17 to 32 it needs some 2^18 keys over all pairs to
-// win: 16 sequences of 2000, 8 heads of 128, 44 us against 39, of 4000 59 against 69, of 8000 85 against 122; 4 heads of
-// 256, 16 of 4000 51 against 51, of 8000 69 against 82; one of 16000 59 against 46.  A form for 33 to 64 rows was
-// slower everywhere (16 of 8000: 245 against 121).
+// Up to 16 rows the streaming kernel is the faster one from one sequence of 1000 keys (19 us, row blocks 21;
+// 5 rows, 8 KV heads of 128) to 16 of 8000 (66 against 123); at 15 rows only one of 1000 is not (22 against 21).  With 17
+// to 32 it needs some 2^18 keys over all pairs to win: 16 sequences of 2000, 8 heads of 128, 49 us against 41, of 4000 68
+// against 69, of 8000 98 against 123; 4 heads of 256, 16 of 4000 52 against 53, of 8000 71 against 84; one of 16000 53
+// against 47; of 64, 16 of 4000 42 against 36, of 8000 56 against 58 (64 of 2000: 67 against 62).  A form for 33 to 64
+// rows was slower everywhere (16 of 8000: 245 against 121).  The rule takes max_len for the keys and does not know the
+// window, which the workspace's size does not depend on: with 17 to 32 rows under a window the row blocks would be
+// faster (16 of 8000, window 128: 17 us against 22; 64 of 8000, window 1024: 102 against 106, heads of 64 44 against 53).
 #include "qg_attn.h"
 
 namespace qg {

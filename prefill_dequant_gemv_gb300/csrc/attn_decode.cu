@@ -32,11 +32,13 @@
 //     each with its own reference and accumulators, joined at the pair's end.
 //
 // Measured (GB300; bytes are the codes and scales that the rows see, queries and outputs): 64 sequences of up to
-// 8193 tokens, 40/8 heads of 128: 109 us, 5.15 TB/s; one of 131001 tokens, 24/4 heads of 256: 59 us,
-// 4.55 TB/s; 16 x 4 rows on 8004 tokens, 24/4 of 256: 43 us, 2.56 TB/s; one token on 777, 40/8 of 128:
-// 14.1 us.  Long calls run at the memory's pace but for some 12 us: launch, first tiles
+// 8193 tokens, 40/8 heads of 128: 110 us, 5.1 TB/s; one of 131001 tokens, 24/4 heads of 256: 59 us,
+// 4.55 TB/s; 16 x 4 rows on 8004 tokens, 24/4 of 256: 45 us, 2.45 TB/s; one token on 777, 40/8 of 128:
+// 14.4 us.  Long calls run at the memory's pace but for some 12 us: launch, first tiles
 // (2 us until the CTAs are ready, 1.5 until the first copy has landed), the chain of the last tile, and the join of cut
-// pairs (5 us); a few short pairs are that chain alone.
+// pairs (5 us); a few short pairs are such a chain alone, of whose 14 us some 6 are not accounted for.  The forms of 80
+// registers (16 rows, heads of 64 and 128) spill some 370 bytes.
+// Batches of more than 32 sequences read each further one's lengths from memory on their way (Walk).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -165,8 +167,8 @@ struct Share {
   }
 };
 
-// A pair takes as long as its tiles and some six more (its rows, its end; 2, 3, 4, 6, 8 and 12 give 117, 110, 109,
-// 107, 110 and 111 us for 64 ragged sequences, and 50, 45, 43, 41, 42 and 43 us for 16 x 4 rows): the line
+// A pair takes as long as its tiles and some six more (its rows, its end; 2, 3, 4, 6, 8 and 12 give 125, 117, 114,
+// 110, 111 and 112 us for 64 ragged sequences, and 51, 48, 46, 45.5, 45.3 and 47 us for 16 x 4 rows): the line
 // counts a pair's tiles and kPairCost places behind them, which no tile stands at.
 constexpr int kPairCost = 6;
 __device__ __forceinline__ int places_of(const Seq& s, const AttnArgs& a) {
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(Cfg<D, N>::THREADS, 1)
   const Share share = {total / max(grid, 1), total % max(grid, 1)};
   int u0 = cta < grid ? share.begin(cta) : 0, u1 = cta < grid ? share.begin(cta + 1) : 0;
   // A few short pairs: a CTA a pair.  Its groups take most tiles at once, and a join between CTAs costs more
-  // than a second round (one sequence of 777 keys, 8 KV heads of 128: 13.9 us so, some 15 cut into 56 CTAs).
+  // than a second round (one sequence of 777 keys, 8 KV heads of 128: 14.4 us so, 15.1 cut into as many CTAs as there are places).
   if (most <= 2 * NG + kPairCost && c.n_seqs <= 32 && c.n_seqs * c.hkv <= (int)gridDim.x) w.pair_of(a, cta, lane, &u0, &u1);
   int place = u1;  // of this CTA's first tile
   if (warp > kMma && warp < kMma + 7) place = w.find(a, u0, u1, lane);

@@ -3,7 +3,8 @@
 // heads share what is loaded -- through the keys that they see, BN at a time, with an online softmax.
 //
 // The mathematics is the few-row kernel's: t_j = scale * ks_j * (q . k_j) * log2(e) + log2(vs_j), P_j = 2^(t_j - m + 7),
-//   out = sum P_j v_j / sum (P_j / vs_j),   m moving only when a row's maximum has grown by 2^8.
+//   out = sum P_j v_j / sum (P_j / vs_j),   m moving only when a row's maximum has grown by 2^8 (conditional rescaling, a
+//   published refinement of the online softmax).
 //
 // Bound by the tensor cores and, about as much, by the softmax's exponentials and conversions, so:
 //   * scores run on the 8-bit tensor cores, the key codes as they come from the cache and a query row as
@@ -25,7 +26,8 @@
 // window of 1024, 32/4 heads of 64: 187 us, 407 TFLOP/s.  A step of 256 rows x 128 keys takes 4020 cycles (heads of 128) or
 // 3370 (64), 128 x 64 at 256 takes 2060; the tensor cores' share at 128 is 2350, as the scores' two terms cost what the
 // outputs do.  The rest is the chain of one row tile, 2300 cycles from scores to weights and 300 until the
-// products start, which two tiles overlap in part.  A CTA's start and end take 20000 cycles, the work of five steps.
+// products start, which two tiles overlap in part.  A CTA's start and end take 20000 cycles, the work of five steps.  The
+// forms of 80 registers (heads of 64 and 128) spill 28 and 48 bytes.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -17,10 +17,11 @@
 // and a later, larger scale moves the codes' exponents only.
 //
 // Bound by HBM: bf16 in, bf16 and bytes out.  Measured (GB300): 4096 tokens of 40/8 heads of 128: 28 us, 4.0 TB/s; seven
-// prompts of up to 1201 tokens, 24/4 heads of 256, pages of 16: 34 us, 3.9 TB/s; one token 6.8 us, 64 sequences of one 7.2 us,
-// which is the launch and three dependent loads.  The long calls are about half issue (57% of the slots: the norms' and codes'
-// arithmetic, 17 M warp instructions) and half waiting for their one round of loads: a unit's values are held in
-// registers until its scale is known, so a block has no next loads to send meanwhile.
+// prompts of up to 1201 tokens, 24/4 heads of 256, pages of 16: 34 us, 3.9 TB/s; one token 7.1 us, 64 sequences of one 7.5 us,
+// which is the host's call, the launch and three dependent loads.  The long calls are about half issue (57% of the slots: the
+// norms' and codes' arithmetic, 17 M warp instructions) and half waiting for their one round of loads: a unit's values are held
+// in registers until its scale is known, so its block has no next loads to send meanwhile.  The queries, 77% of the bytes
+// at 40/8 heads, need no scale; their blocks could, and do not.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
