@@ -241,6 +241,67 @@ qg_status qgemm_w4a4(const qg_weight* w, const void* x, int64_t m_rows, int64_t 
                      const void* residual, int64_t ldr, void* y, int64_t ldy,
                      void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------ RMS norm before a layer's products
+ * h = bf16(x + residual) (h = x without a residual), then over each row of k elements, in fp32,
+ *     y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)
+ * stored in bf16, in E4M3 codes with scales, or both; each value is rounded to its type once.
+ * E4M3: a group of `group` consecutive elements of a row (32, 64 or 128; the last may be shorter),
+ * or the whole row (group 0), has the fp32 scale s = max(amax / 448, 2^-100), amax its largest finite
+ * |y|, and the codes E4M3(y * (1/s)), nearest even and saturating at 448: infinities saturate,
+ * NaN stays NaN and neither moves a scale.  A row with a NaN in it is NaN, as the formula gives it;
+ * the squares are summed in fp32, so a row whose
+ * sum passes 2^128 comes out as zeros (NaN where h is infinite). */
+typedef struct {
+  void* sum;              /* device bf16 [m][ldh]: h, or NULL; without a residual NULL */
+  int64_t ldh;
+  void* y;                /* device bf16 [m][ldy], or NULL */
+  int64_t ldy;
+  uint8_t* codes;         /* device E4M3 [m][ldc], or NULL; ldc a multiple of 8 */
+  int64_t ldc;
+  float* scales;          /* device fp32 [m][lds], ceil(k / group) a row (one with group 0); NULL iff codes is */
+  int64_t lds;
+  int64_t group;          /* 32, 64, 128 or 0 (ignored without codes) */
+} qg_norm_out;
+
+/* x and residual (may be NULL): bf16 [m_rows][ldx] / [m_rows][ldr]; weight: bf16 [k], 16-byte
+ * aligned like every matrix (scales: 4-byte aligned, any lds).  k is 1 to 65536; m_rows may be 0.
+ * sum or y may be x or residual itself with the same stride; no other overlap.  eps >= 0.
+ * No workspace; one launch; deterministic. */
+qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t m_rows, int64_t k,
+                      const void* weight, float eps, float weight_offset, const qg_norm_out* out, void* stream);
+
+/* ------------------------------------------------------------------ low-rank adapters beside a shared projection
+ * Adapters of many requests at once: row i of the projection's output y = W x gets its own
+ * adapter's share, e = ids[i]:
+ *     h = a_e x[i]              (rank_e sums over k, fp32)
+ *     out[i][n] = bf16( y[i][n] + scales[e] * sum_j b_e[n][j] * h_j )        (fp32, rounded once)
+ * ids[i] = -1: no adapter, out[i] = y[i].  Rows of one adapter may lie anywhere; its weights are
+ * read once for up to 64 of them.  Elements of a and b past an adapter's rank, whatever their
+ * bits, do not enter. */
+typedef struct {
+  int32_t n_adapters;     /* 1 .. 1024 */
+  int32_t max_rank;       /* rows of a and columns of b that each adapter has room for: a multiple of 8, 8 .. 128 */
+  int64_t n;              /* outputs of the projection */
+  int64_t k;              /* inputs */
+  const void* a;          /* device bf16 [n_adapters][max_rank][lda], 16-byte aligned */
+  int64_t lda;            /* >= k, a multiple of 8 */
+  const void* b;          /* device bf16 [n_adapters][n][max_rank], 16-byte aligned */
+  const float* scales;    /* device fp32 [n_adapters] */
+  const int32_t* ranks;   /* device int32 [n_adapters], each 0 .. max_rank, or NULL: all max_rank */
+} qg_lora;
+
+/* Workspace bytes of qlora: the status word. */
+size_t qlora_workspace_size(void);
+
+/* ids: int32 [m_rows] on the device; x bf16 [m_rows][ldx]; y and out bf16 [m_rows][ldy] / [m_rows][ldo].  out may be
+ * y itself with the same stride: rows without an adapter, or whose adapter has rank 0, are then not touched; no other overlap.
+ * ids and ranks are checked on the device: an id outside -1 .. n_adapters-1 or a rank outside
+ * 0 .. max_rank counts as no adapter and puts QG_ERR_INVALID_ARG into the workspace's status word
+ * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^30.  Any number of calls may
+ * share a workspace.  Deterministic; one launch. */
+qg_status qlora(const qg_lora* lora, const int32_t* ids, int64_t m_rows, const void* x, int64_t ldx, const void* y,
+                int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------------ mixture of experts
  * A layer of n_experts routed experts plus an optional shared expert, each an FFN with
  * gate/up (2F x H: rows 0..F-1 gate, F..2F-1 up) and down (H x F) quantized matrices.
@@ -276,6 +337,34 @@ size_t qmoe_route_workspace_size(int64_t t, int n_experts, int topk);
  * table; deterministic, one launch for up to 32 tokens.  logits: fp32 [t][n_experts]. */
 qg_status qmoe_route(const float* logits, int64_t t, int n_experts, int topk,
                      int32_t* topk_ids, float* topk_w, void* route_ws, size_t route_ws_bytes, void* stream);
+
+/* Routing by other scores than qmoe_route's.  For each token, in exact arithmetic (see below),
+ *     s_e = sigmoid(logit_e), or softmax over all experts
+ *     c_e = s_e + bias_e                       the choice value; the bias does not enter the weights
+ *   With n_groups > 1 (groups of n_experts / n_groups consecutive experts): a group's value is the sum of its
+ *   group_best largest c; the topk_groups groups of largest value are kept (ties to the lower
+ *   index), the others' experts are out.
+ *   The topk remaining experts of largest c, in descending order (ties to the lower index), are chosen;
+ *     w_e = scale * s_e, or scale * s_e / (sum of the chosen s) with renormalise.
+ * The choice is the one that scores in 64 bits give: c in fp32 decides where it is clear, and a
+ * token with two values nearer to each other than fp32's error is decided in 64 bits.  The
+ * weights are fp32.  NaN values of c come after every number; a weight is NaN where the formula's is
+ * (renormalised weights whose sum is 0 among them). */
+typedef enum { QG_SCORE_SOFTMAX = 1, QG_SCORE_SIGMOID = 2 } qg_score;
+typedef struct {
+  int32_t score;          /* qg_score */
+  int32_t n_groups;       /* 1 .. 32, a divisor of n_experts */
+  int32_t topk_groups;    /* 1 .. n_groups; topk <= topk_groups * (n_experts / n_groups) */
+  int32_t group_best;     /* 1 or 2 (2 needs groups of two experts or more); ignored with one group */
+  int32_t renormalise;    /* 0 or 1 */
+  float scale;            /* finite */
+  const float* bias;      /* device fp32 [n_experts], or NULL */
+} qg_route_rule;
+
+/* qmoe_route by a rule (NULL: qmoe_route itself): the same outputs, the same route_ws with the same
+ * size, taken by qmoe_ffn and qgemm_grouped alike. */
+qg_status qmoe_route_by(const qg_route_rule* rule, const float* logits, int64_t t, int n_experts, int topk,
+                        int32_t* topk_ids, float* topk_w, void* route_ws, size_t route_ws_bytes, void* stream);
 
 /* Workspace bytes qmoe_ffn needs for t tokens on the current device. */
 size_t qmoe_workspace_size(const qg_moe_layer* layer, int64_t t, int topk);

@@ -63,6 +63,24 @@ class qg_norm_rope(ctypes.Structure):
                 ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class qg_norm_out(ctypes.Structure):
+    _fields_ = [("sum", ctypes.c_void_p), ("ldh", ctypes.c_int64), ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64),
+                ("group", ctypes.c_int64)]
+
+
+class qg_lora(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("max_rank", ctypes.c_int32), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
+                ("a", ctypes.c_void_p), ("lda", ctypes.c_int64), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("ranks", ctypes.c_void_p)]
+
+
+class qg_route_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("bias", ctypes.c_void_p)]
+
+
 _lib = None
 _P, _I64, _I, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 _SIGNATURES = {
@@ -97,9 +115,14 @@ _SIGNATURES = {
     "qattn_workspace_size": (_SZ, [ctypes.POINTER(qg_kv_cache), ctypes.POINTER(qg_kv_batch), _I64, _I]),
     "qattn": (_I, [ctypes.POINTER(qg_kv_cache), ctypes.POINTER(qg_kv_batch), _I64, _I, _P, _I64, _I64, ctypes.c_float,
                    _I64, _P, _I64, _I64, _P, _SZ, _P]),
+    "qg_rms_norm": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, ctypes.c_float, ctypes.c_float, ctypes.POINTER(qg_norm_out), _P]),
+    "qlora_workspace_size": (_SZ, []),
+    "qlora": (_I, [ctypes.POINTER(qg_lora), _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P]),
+    "qmoe_route_by": (_I, [ctypes.POINTER(qg_route_rule), _P, _I64, _I, _I, _P, _P, _P, _SZ, _P]),
 }
 
 QG_KV_E4M3 = 1
+QG_SCORE_SOFTMAX, QG_SCORE_SIGMOID = 1, 2
 QG_MOE_GATE_UP_SWIGLU = 1
 QG_MOE_DOWN_COMBINE = 2
 
@@ -277,7 +300,40 @@ def qattn(cache: qg_kv_cache, batch: qg_kv_batch, n_tokens: int, n_q_heads: int,
                        ws_bytes, stream), "qattn")
 
 
+def qg_rms_norm(x_ptr: int, ldx: int, res_ptr: Optional[int], ldr: int, m: int, k: int, w_ptr: int, eps: float,
+                weight_offset: float, out: qg_norm_out, stream: int = 0):
+    _check(lib().qg_rms_norm(x_ptr, ldx, res_ptr, ldr, m, k, w_ptr, eps, weight_offset, out, stream), "qg_rms_norm")
+
+
+def qlora_workspace_size() -> int:
+    return lib().qlora_workspace_size()
+
+
+def qlora(lora: "qg_lora", ids_ptr: int, m: int, x_ptr: int, ldx: int, y_ptr: int, ldy: int, out_ptr: int, ldo: int, ws_ptr: int,
+          ws_bytes: int, stream: int = 0):
+    _check(lib().qlora(lora, ids_ptr, m, x_ptr, ldx, y_ptr, ldy, out_ptr, ldo, ws_ptr, ws_bytes, stream), "qlora")
+
+
+def qmoe_route_by(rule: Optional[qg_route_rule], logits_ptr: int, t: int, n_experts: int, topk: int, ids_ptr: int, w_ptr: int,
+                  ws_ptr: int, ws_bytes: int, stream: int = 0):
+    _check(lib().qmoe_route_by(rule, logits_ptr, t, n_experts, topk, ids_ptr, w_ptr, ws_ptr, ws_bytes, stream), "qmoe_route_by")
+
+
 # ------------------------------------------------------------------ torch helpers
+def _need(ok: bool, what: str):
+    if not ok:
+        raise QGError(1, what)
+
+
+def _on(index: int, call, *args):
+    """call(*args, the current stream of device `index`), with that device the current one."""
+    import torch
+    if torch._C._cuda_getDevice() == index:
+        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(index):
+        return call(*args, _raw_stream(index))
+
+
 def _stream_ptr(stream=None) -> int:
     import torch
     s = torch.cuda.current_stream() if stream is None else stream
@@ -434,8 +490,49 @@ class PackedMoE:
         return tot // self.n_experts
 
 
-def route(logits, topk: int, workspace: Optional[Workspace] = None):
-    """(topk_ids int32 [t, topk], topk_w fp32 [t, topk], route workspace) for fp32 logits [t, E] on the device."""
+class RouteRule:
+    """How experts are chosen and weighed (``qg_route_rule``): ``score`` "softmax" or "sigmoid"; ``bias`` fp32 [experts] added
+    for the choice alone; of ``groups`` groups of consecutive experts the ``topk_groups`` best are kept, a group valued by
+    the sum of its ``group_best`` (1 or 2) largest; the chosen scores, divided by their sum with ``renormalise``, times ``scale``."""
+
+    def __init__(self, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1, group_best: int = 2,
+                 renormalise: bool = True, scale: float = 1.0):
+        import torch
+        kinds = {"softmax": QG_SCORE_SOFTMAX, "sigmoid": QG_SCORE_SIGMOID}
+        _need(score in kinds, "RouteRule: score is softmax or sigmoid")
+        _need(bias is None or (bias.dtype == torch.float32 and bias.dim() == 1 and bias.is_contiguous()),
+              "RouteRule: bias is contiguous float32 [experts]")
+        self.bias = bias
+        self.desc = qg_route_rule(kinds[score], groups, topk_groups, group_best, 1 if renormalise else 0, scale,
+                                  None if bias is None else bias.data_ptr())
+
+
+def _route_by(rule: RouteRule, logits, topk: int, workspace: Optional[Workspace]):
+    import torch
+    t, e = logits.shape
+    index = logits.get_device()
+    if logits.dtype is not torch.float32 or not logits.is_contiguous() or index < 0:
+        raise QGError(1, "route: contiguous float32 logits [tokens, experts] on a CUDA device")
+    if rule.bias is not None and (rule.bias.shape[0] != e or rule.bias.get_device() != index):
+        raise QGError(1, "route: a bias for every expert, on the logits' device")
+    if workspace is None:
+        workspace = Workspace(qmoe_route_workspace_size(t, e, topk), logits.device)
+    elif workspace.index != index:
+        raise QGError(1, "route: the workspace on the logits' device")
+    ids = logits.new_empty((t, topk), dtype=torch.int32)
+    w = logits.new_empty((t, topk))
+    st = _on(index, (_lib or lib()).qmoe_route_by, rule.desc, logits.data_ptr(), t, e, topk, ids.data_ptr(), w.data_ptr(),
+             workspace.ptr, workspace.nbytes)
+    if st:
+        raise QGError(st, "qmoe_route_by")
+    return ids, w, workspace
+
+
+def route(logits, topk: int, workspace: Optional[Workspace] = None, rule: Optional[RouteRule] = None):
+    """(topk_ids int32 [t, topk], topk_w fp32 [t, topk], route workspace) for fp32 logits [t, E] on the device:
+    the largest logits and their softmax, or by a rule (``qmoe_route_by``)."""
+    if rule is not None:
+        return _route_by(rule, logits, topk, workspace)
     import torch
     t, e = logits.shape
     ids = torch.empty((t, topk), dtype=torch.int32, device=logits.device)
@@ -466,9 +563,12 @@ def moe_ffn(pm: PackedMoE, x, topk_w, route_ws: Workspace, out=None, workspace: 
 
 
 def moe_forward(pm: PackedMoE, x, logits, topk: int, out=None, workspace: Optional[Workspace] = None,
-                route_ws: Optional[Workspace] = None, shared_gate=None):
-    """Router and MoE FFN in one call (qmoe_forward) for x bf16 [t, H] and fp32 logits [t, E]:
-    returns (out bf16 [t, H], topk_ids int32 [t, topk], topk_w fp32 [t, topk], route workspace)."""
+                route_ws: Optional[Workspace] = None, shared_gate=None, rule: Optional[RouteRule] = None):
+    """Router and MoE FFN in one call (qmoe_forward; by a rule qmoe_route_by, then qmoe_ffn) for x bf16 [t, H] and fp32
+    logits [t, E]: returns (out bf16 [t, H], topk_ids int32 [t, topk], topk_w fp32 [t, topk], route workspace)."""
+    if rule is not None:
+        ids, w, route_ws = _route_by(rule, logits, topk, route_ws)
+        return moe_ffn(pm, x, w, route_ws, out, workspace, shared_gate), ids, w, route_ws
     import torch
     t = x.shape[0]
     e = logits.shape[1]
@@ -507,12 +607,135 @@ def moe_stage(pm: PackedMoE, stage: int, inp, t: int, topk: int, route_ws: Works
     return out
 
 
+# ------------------------------------------------------------------ RMS norm and low-rank adapters
+def _rows(t, m, k, dtype, index, what):
+    """(pointer, row stride) of a matrix [m, k] of `dtype` on device `index`; its rows' elements lie side by side."""
+    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != index or tuple(t.shape) != (m, k) or (k > 1 and t.stride(1) != 1):
+        raise QGError(1, f"{what}: {dtype} [{m}, {k}] with a contiguous last dimension, on the input's CUDA device")
+    return t.data_ptr(), (t.stride(0) if m > 1 else (k + 7) // 8 * 8)
+
+
+def _new_rows(x, m, k, dtype):
+    """A new matrix [m, k] whose rows start at multiples of 16 bytes."""
+    return x.new_empty((m, (k + 15) // 16 * 16), dtype=dtype)[:, :k]
+
+
+def _norm(x, weight, residual, eps, weight_offset, sum_out, what):
+    """The checked inputs of a norm: (arguments up to weight_offset, pointer and stride of the sum, the sum, device)."""
+    import torch
+    index = x.get_device()
+    if x.dim() != 2 or index < 0:
+        raise QGError(1, f"{what}: x is bfloat16 [rows, columns] on a CUDA device")
+    m, k = x.shape
+    xp, ldx = _rows(x, m, k, torch.bfloat16, index, f"{what}: x")
+    if (weight.dtype is not torch.bfloat16 or tuple(weight.shape) != (k,) or weight.get_device() != index
+            or (k > 1 and weight.stride(0) != 1)):
+        raise QGError(1, f"{what}: weight is contiguous bfloat16 [{k}] on x's device")
+    rp = hp = None
+    ldr = ldh = 0
+    if residual is not None:
+        rp, ldr = _rows(residual, m, k, torch.bfloat16, index, f"{what}: residual")
+        if sum_out is None:
+            sum_out = _new_rows(x, m, k, torch.bfloat16)
+        hp, ldh = _rows(sum_out, m, k, torch.bfloat16, index, f"{what}: sum_out")
+    elif sum_out is not None:
+        raise QGError(1, f"{what}: a sum needs a residual")
+    return (xp, ldx, rp, ldr, m, k, weight.data_ptr(), eps, weight_offset), hp, ldh, sum_out, index
+
+
+def rms_norm(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, out=None, sum_out=None):
+    """RMS norm of x (bf16 [m, k]), after the residual's addition if there is one (``qg_rms_norm``): returns (y bf16 [m, k],
+    the sum bf16 [m, k] or None).  out or sum_out may be x or the residual itself."""
+    import torch
+    args, hp, ldh, sum_out, index = _norm(x, weight, residual, eps, weight_offset, sum_out, "rms_norm")
+    if out is None:
+        out = _new_rows(x, args[4], args[5], torch.bfloat16)
+    yp, ldy = _rows(out, args[4], args[5], torch.bfloat16, index, "rms_norm: out")
+    st = _on(index, (_lib or lib()).qg_rms_norm, *args, qg_norm_out(hp, ldh, yp, ldy))
+    if st:
+        raise QGError(st, "qg_rms_norm")
+    return out, sum_out
+
+
+def rms_norm_fp8(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, group: int = 128, out=None, scales=None,
+                 sum_out=None, y_out=None):
+    """``rms_norm`` with its output in 8 bits: returns (codes float8_e4m3fn [m, k], scales fp32 [m, ceil(k / group)], the
+    sum or None); group 32, 64 or 128, or 0 for one scale a row.  y_out (bf16 [m, k]), if given, takes the output in bf16 too."""
+    import torch
+    args, hp, ldh, sum_out, index = _norm(x, weight, residual, eps, weight_offset, sum_out, "rms_norm_fp8")
+    m, k = args[4], args[5]
+    if group not in (0, 32, 64, 128):
+        raise QGError(2, "rms_norm_fp8: group is 32, 64, 128 or 0")
+    groups = -(-k // group) if group else 1
+    if out is None:
+        out = _new_rows(x, m, k, torch.float8_e4m3fn)
+    if scales is None:
+        scales = x.new_empty((m, groups), dtype=torch.float32)
+    cp, ldc = _rows(out, m, k, torch.float8_e4m3fn, index, "rms_norm_fp8: out")
+    sp, lds = _rows(scales, m, groups, torch.float32, index, "rms_norm_fp8: scales")
+    yp, ldy = (None, 0) if y_out is None else _rows(y_out, m, k, torch.bfloat16, index, "rms_norm_fp8: y_out")
+    st = _on(index, (_lib or lib()).qg_rms_norm, *args, qg_norm_out(hp, ldh, yp, ldy, cp, ldc, sp, lds, group))
+    if st:
+        raise QGError(st, "qg_rms_norm")
+    return out, scales, sum_out
+
+
+class LoraAdapters:
+    """Low-rank adapters of one projection (``qg_lora``): a bf16 [adapters, max_rank, k], b bf16 [adapters, n, max_rank],
+    scales fp32 [adapters] and, where they have not all max_rank, ranks int32 [adapters], on one device.  The tensors'
+    contents may change between calls."""
+
+    def __init__(self, a, b, scales, ranks=None):
+        import torch
+        _need(a.dtype == b.dtype == torch.bfloat16 and a.dim() == b.dim() == 3, "LoraAdapters: a and b are bfloat16 of 3 dimensions")
+        count, top, k = (int(v) for v in a.shape)
+        n = int(b.shape[1])
+        _need(b.shape == (count, n, top) and b.is_contiguous(), "LoraAdapters: b is contiguous [adapters, outputs, max_rank]")
+        _need(min(count, top, k, n) > 0, "LoraAdapters: no empty dimension")
+        lda = int(a.stride(1)) if top > 1 else (k + 7) // 8 * 8
+        _need((k == 1 or a.stride(2) == 1) and lda >= k and (count == 1 or a.stride(0) == top * lda),
+              "LoraAdapters: a is [adapters, max_rank, inputs] with rows at one distance")
+        _need(scales.dtype == torch.float32 and scales.shape == (count,) and scales.is_contiguous(),
+              "LoraAdapters: scales are contiguous float32 [adapters]")
+        _need(ranks is None or (ranks.dtype == torch.int32 and ranks.shape == (count,) and ranks.is_contiguous()),
+              "LoraAdapters: ranks are contiguous int32 [adapters]")
+        for t in (b, scales, ranks):
+            _need(t is None or t.device == a.device, "LoraAdapters: tensors on one device")
+        self.a, self.b, self.scales, self.ranks = a, b, scales, ranks
+        self.n, self.k, self.index = n, k, a.get_device()
+        self.desc = qg_lora(count, top, n, k, a.data_ptr(), lda, b.data_ptr(), scales.data_ptr(),
+                            None if ranks is None else ranks.data_ptr())
+
+
+def lora_workspace_size(adapters: LoraAdapters, m: int) -> int:
+    """Workspace bytes of ``lora`` for m rows."""
+    return qlora_workspace_size()
+
+
+def lora(adapters: LoraAdapters, ids, x, y, out=None, workspace: Optional[Workspace] = None):
+    """y plus each row's adapter's share (``qlora``): ids int32 [m] (-1: none), x bf16 [m, k] the projection's input, y bf16 [m, n]
+    its output.  Without ``out`` y is changed in place."""
+    import torch
+    index, m = adapters.index, x.shape[0]
+    if index < 0 or ids.dtype is not torch.int32 or tuple(ids.shape) != (m,) or ids.get_device() != index or (m > 1 and ids.stride(0) != 1):
+        raise QGError(1, f"lora: contiguous int32 ids [{m}] on the adapters' CUDA device")
+    xp, ldx = _rows(x, m, adapters.k, torch.bfloat16, index, "lora: x")
+    yp, ldy = _rows(y, m, adapters.n, torch.bfloat16, index, "lora: y")
+    if out is None:
+        out, op, ldo = y, yp, ldy
+    else:
+        op, ldo = _rows(out, m, adapters.n, torch.bfloat16, index, "lora: out")
+    if workspace is None:
+        workspace = Workspace(qlora_workspace_size(), x.device)
+    elif workspace.index != index:
+        raise QGError(1, "lora: the workspace on the adapters' device")
+    st = _on(index, (_lib or lib()).qlora, adapters.desc, ids.data_ptr(), m, xp, ldx, yp, ldy, op, ldo, workspace.ptr, workspace.nbytes)
+    if st:
+        raise QGError(st, "qlora")
+    return out
+
+
 # ------------------------------------------------------------------ attention over the 8-bit paged cache
-def _need(ok: bool, what: str):
-    if not ok:
-        raise QGError(1, what)
-
-
 def _raw_stream(index: int) -> int:
     """The current stream of a device, as torch keeps it."""
     import torch

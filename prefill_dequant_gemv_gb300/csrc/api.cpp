@@ -254,6 +254,40 @@ extern "C" qg_status qmoe_route(const float* logits, int64_t t, int n_experts, i
   return (qg_status)launch_route(logits, t, n_experts, topk, topk_ids, topk_w, route_ws, stream);
 }
 
+extern "C" qg_status qmoe_route_by(const qg_route_rule* rule, const float* logits, int64_t t, int n_experts, int topk,
+                                   int32_t* topk_ids, float* topk_w, void* route_ws, size_t route_ws_bytes,
+                                   void* stream) {
+  if (!rule) return qmoe_route(logits, t, n_experts, topk, topk_ids, topk_w, route_ws, route_ws_bytes, stream);
+  const qg_route_rule& q = *rule;
+  if (t < 1 || n_experts < 1 || topk < 1 || topk > n_experts) return QG_ERR_INVALID_ARG;
+  if ((q.score != QG_SCORE_SOFTMAX && q.score != QG_SCORE_SIGMOID) || q.n_groups < 1 || n_experts % q.n_groups ||
+      q.topk_groups < 1 || q.topk_groups > q.n_groups || (q.renormalise != 0 && q.renormalise != 1) ||
+      !std::isfinite(q.scale))
+    return QG_ERR_INVALID_ARG;
+  const int size = n_experts / q.n_groups;
+  if (topk > (int64_t)q.topk_groups * size) return QG_ERR_INVALID_ARG;
+  if (q.n_groups > 1 && ((q.group_best != 1 && q.group_best != 2) || q.group_best > size)) return QG_ERR_INVALID_ARG;
+  if (n_experts > kMaxExperts || topk > kMaxTopk || q.n_groups > 32 || t > 0x7FFFFFFF / topk) return QG_ERR_UNSUPPORTED;
+  if (!logits || !topk_ids || !topk_w || !route_ws) return QG_ERR_INVALID_ARG;
+  if (!aligned16(logits) || !aligned16(topk_ids) || !aligned16(topk_w) || !aligned16(route_ws) ||
+      reinterpret_cast<uintptr_t>(q.bias) % 4)
+    return QG_ERR_MISALIGNED;
+  if (route_ws_bytes < route_layout(t, n_experts, topk).total) return QG_ERR_WORKSPACE_TOO_SMALL;
+  RouteRule r;
+  r.sigmoid = q.score == QG_SCORE_SIGMOID;
+  r.renormalise = q.renormalise;
+  r.n_groups = q.n_groups;
+  r.topk_groups = q.topk_groups;
+  r.group_best = q.n_groups > 1 ? q.group_best : 1;
+  r.group_lanes = 32;
+  while (r.group_lanes * q.n_groups > 32) r.group_lanes /= 2;
+  r.group_mul = ((1u << 20) + size - 1) / size;
+  r.values = q.bias || r.group_best == 2;
+  r.scale = q.scale;
+  r.bias = q.bias;
+  return (qg_status)launch_route_by(r, logits, t, n_experts, topk, topk_ids, topk_w, route_ws, stream);
+}
+
 static int check_moe(const qg_moe_layer* m, int64_t t, int topk, Geometry* gu, Geometry* dn) {
   if (!m || t < 1 || topk < 1) return QG_ERR_INVALID_ARG;
   if (m->n_experts < 1 || topk > m->n_experts) return QG_ERR_INVALID_ARG;

@@ -62,7 +62,20 @@ struct RouteView {
   int* block_start;
 };
 
+// A qg_route_rule as the kernels take it.
+struct RouteRule {
+  int sigmoid, renormalise;
+  int n_groups, topk_groups, group_best;
+  int group_lanes;     // lanes that look through one group: 32 / n_groups rounded down to a power of two
+  uint32_t group_mul;  // ceil(2^20 / experts a group): e * group_mul >> 20 is the group of e < 512
+  int values;          // the choice goes by scores and bias; 0: by the logits, in the same order
+  float scale;
+  const float* bias;
+};
+
 RouteView route_view(void* ws, int64_t T, int E, int k);
 int launch_route(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws, void* stream);
+int launch_route_by(const RouteRule& rule, const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws,
+                    void* stream);
 
 }  // namespace qg

@@ -46,8 +46,8 @@ __device__ __forceinline__ void lane_best(const uint32_t (&key)[16], uint32_t& b
   bi = i8[0];
 }
 
-// Warp-level top-k of one token's logits (E <= 512): lane l holds the keys of logits l,
-// l+32, ... (16 registers; the expert of slot i is l + 32 i).  Each lane first extracts its
+// Warp-level top-k of up to 512 keys (0: none): lane l holds the keys of experts l, l+32, ...
+// (16 registers; the expert of slot i is l + 32 i).  Each lane first extracts its
 // three best keys in order (ties to the lower slot, i.e. the lower expert).  Each of k rounds
 // then takes the warp maximum of the lanes' current heads and the warp minimum of the experts
 // holding it (two single-instruction warp reductions), and the winner's lane steps to its
@@ -55,15 +55,9 @@ __device__ __forceinline__ void lane_best(const uint32_t (&key)[16], uint32_t& b
 // three times before the last round has no extracted key left: the rounds are then redone
 // from all 16 keys, the winner's lane searching its next best each time (the same result,
 // only slower; the fast rounds never pick a wrong key before that point).  Lane
-// j keeps the j-th winner and the k lanes compute the softmax over the kept logits in parallel.
-__device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t* ids, float* wts, int* ids_copy = nullptr) {
+// j keeps the j-th winner (mine, mine_id); top is the first one's key.
+__device__ __forceinline__ void warp_topk_keys(uint32_t (&key)[16], int k, uint32_t& mine, int& mine_id, uint32_t& top) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = e < E ? order_key(lg[e]) : 0u;
-  }
   uint32_t h0, h1, h2;  // the lane's three best keys, descending, and their experts
   int e0, e1, e2;
   {
@@ -82,8 +76,9 @@ __device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t
     lane_best(kk, h2, bi);
     e2 = lane + 32 * bi;
   }
-  uint32_t mine = 0u, top = 0u;
-  int mine_id = 0, taken = 0;
+  mine = top = 0u;
+  mine_id = 0;
+  int taken = 0;
   bool short_of_keys = false;
   for (int j = 0; j < k; ++j) {
     const uint32_t kmax = __reduce_max_sync(0xFFFFFFFFu, h0);
@@ -121,6 +116,20 @@ __device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t
       }
     }
   }
+}
+
+// Warp-level top-k of one token's logits (E <= 512) and the k lanes' softmax over the kept ones in parallel.
+__device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t* ids, float* wts, int* ids_copy = nullptr) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = e < E ? order_key(lg[e]) : 0u;
+  }
+  uint32_t mine, top;
+  int mine_id;
+  warp_topk_keys(key, k, mine, mine_id, top);
   // softmax over the k kept logits (descending order), shifted by the largest
   const float z = lane < k ? expf(key_value(mine) - key_value(top)) : 0.0f;
   float sum = z;

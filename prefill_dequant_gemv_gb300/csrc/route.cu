@@ -11,8 +11,11 @@
 // deterministic: ranks come from ordered scans, never from atomic arrival order.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "qg_internal.h"
 #include "qg_route.h"
+#include "qg_route_by.cuh"
 #include "qg_route_dev.cuh"
 #include "qg_sync.cuh"
 
@@ -25,6 +28,14 @@ __global__ void __launch_bounds__(256) route_topk_kernel(const float* logits, in
   const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
   if (t >= T) return;
   warp_topk(logits + t * E, E, k, ids + t * k, wts + t * k);
+}
+
+__global__ void __launch_bounds__(256) route_topk_by_kernel(RouteRule rule, const float* logits, int64_t T, int E, int k,
+                                                            int32_t* ids, float* wts) {
+  __shared__ float cs[8][kMaxExperts];
+  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (t >= T) return;
+  warp_route(rule, logits + t * E, E, k, cs[threadIdx.x >> 5], ids + t * k, wts + t * k, nullptr);
 }
 
 // Clear a shared array with 16-byte stores (bytes a multiple of 16, 16-byte aligned).
@@ -184,11 +195,13 @@ __global__ void __launch_bounds__(kRouteBlock) route_scatter_kernel(const int32_
   block_scatter(ids, P, E, k, blockIdx.x, r);
 }
 
-// Decode-sized routing (T*k <= kRouteBlock, T <= 32): every phase in one CTA, with the
-// histogram, the scan and the placement in shared memory; only the results go to device
-// memory.
+// Decode-sized routing (T*k <= kRouteBlock; T <= 32 without a rule): every phase in one CTA, with
+// the histogram, the scan and the placement in shared memory; only the results go to device
+// memory.  BY: by a rule, a warp taking every 32nd token; min(T, 32) * E floats of dynamic shared memory.
+template <bool BY>
 __global__ void __launch_bounds__(kRouteBlock) route_small_kernel(const float* logits, int T, int E, int k,
-                                                                  int32_t* ids, float* wts, int tile, RouteView r) {
+                                                                  int32_t* ids, float* wts, int tile, RouteView r,
+                                                                  RouteRule rule) {
   __shared__ int s_ids[kRouteBlock];
   __shared__ int hist[kMaxExperts];
   __shared__ int off[kMaxExperts];
@@ -202,7 +215,13 @@ __global__ void __launch_bounds__(kRouteBlock) route_small_kernel(const float* l
   for (int e = tid; e < E; e += blockDim.x) hist[e] = 0;
   zero_shared(&wc[0][0], sizeof(wc));
   pdl_wait();
-  if (warp < T) warp_topk(logits + (int64_t)warp * E, E, k, ids + warp * k, wts + warp * k, s_ids + warp * k);
+  if constexpr (BY) {
+    extern __shared__ float cs[];
+    for (int t = warp; t < T; t += kRouteBlock / 32)
+      warp_route(rule, logits + (int64_t)t * E, E, k, cs + warp * E, ids + t * k, wts + t * k, s_ids + t * k);
+  } else {
+    if (warp < T) warp_topk(logits + (int64_t)warp * E, E, k, ids + warp * k, wts + warp * k, s_ids + warp * k);
+  }
   __syncthreads();
   // pairs p = t*k + j: histogram (order-free integer counts) and rank within the warp
   const int P = T * k;
@@ -268,20 +287,44 @@ RouteView route_view(void* ws, int64_t T, int E, int k) {
   return v;
 }
 
+// The tables of pairs whose ids are on their way: counts, scan, placement.
+static void launch_group(const int32_t* ids, int64_t P, int E, int k, const RouteView& r, cudaStream_t s) {
+  const int64_t nb = (P + kRouteBlock - 1) / kRouteBlock;
+  route_count_kernel<<<(unsigned)nb, kRouteBlock, 0, s>>>(ids, P, E, r);
+  route_scan_kernel<<<1, kRouteBlock, 0, s>>>(E, (int)nb, kRouteTile, r);
+  route_scatter_kernel<<<(unsigned)nb, kRouteBlock, 0, s>>>(ids, P, E, k, r);
+}
+
 int launch_route(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RouteView r = route_view(ws, T, E, k);
   const int64_t P = T * k;
   if (P <= kRouteBlock && T <= 32) {
-    if (launch_pdl(route_small_kernel, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts,
-                   (int)kRouteTile, r) != cudaSuccess)
+    if (launch_pdl(route_small_kernel<false>, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts,
+                   (int)kRouteTile, r, RouteRule()) != cudaSuccess)
       return QG_ERR_CUDA;
   } else {
-    const int64_t nb = (P + kRouteBlock - 1) / kRouteBlock;
     route_topk_kernel<<<(unsigned)((T + 7) / 8), 256, 0, s>>>(logits, T, E, k, ids, wts);
-    route_count_kernel<<<(unsigned)nb, kRouteBlock, 0, s>>>(ids, P, E, r);
-    route_scan_kernel<<<1, kRouteBlock, 0, s>>>(E, (int)nb, kRouteTile, r);
-    route_scatter_kernel<<<(unsigned)nb, kRouteBlock, 0, s>>>(ids, P, E, k, r);
+    launch_group(ids, P, E, k, r, s);
+  }
+  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+}
+
+int launch_route_by(const RouteRule& rule, const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws,
+                    void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  RouteView r = route_view(ws, T, E, k);
+  const int64_t P = T * k;
+  if (P <= kRouteBlock && T <= 128) {
+    const size_t smem = sizeof(float) * std::min<int64_t>(T, kRouteBlock / 32) * E;
+    if (cudaFuncSetAttribute(route_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)(sizeof(float) * kRouteBlock / 32 * kMaxExperts)) != cudaSuccess ||
+        launch_pdl(route_small_kernel<true>, dim3(1), dim3(kRouteBlock), smem, s, logits, (int)T, E, k, ids, wts,
+                   (int)kRouteTile, r, rule) != cudaSuccess)
+      return QG_ERR_CUDA;
+  } else {
+    route_topk_by_kernel<<<(unsigned)((T + 7) / 8), 256, 0, s>>>(rule, logits, T, E, k, ids, wts);
+    launch_group(ids, P, E, k, r, s);
   }
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
