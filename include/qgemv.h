@@ -276,7 +276,7 @@ qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
  *     h = a_e x[i]              (rank_e sums over k, fp32)
  *     out[i][n] = bf16( y[i][n] + scales[e] * sum_j b_e[n][j] * h_j )        (fp32, rounded once)
  * ids[i] = -1: no adapter, out[i] = y[i].  Rows of one adapter may lie anywhere; its weights are
- * read once for up to 64 of them.  Elements of a and b past an adapter's rank, whatever their
+ * read once for 16 of them (64 where there are more than 256 rows).  Elements of a and b past an adapter's rank, whatever their
  * bits, do not enter. */
 typedef struct {
   int32_t n_adapters;     /* 1 .. 1024 */
@@ -290,15 +290,17 @@ typedef struct {
   const int32_t* ranks;   /* device int32 [n_adapters], each 0 .. max_rank, or NULL: all max_rank */
 } qg_lora;
 
-/* Workspace bytes of qlora: the status word. */
-size_t qlora_workspace_size(void);
+/* Workspace bytes qlora needs for m rows on the current device (0 for sizes that it rejects): the status word and, for
+ * many rows, h in parts.  Reads the sizes of `lora`, no pointer. */
+size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
 
 /* ids: int32 [m_rows] on the device; x bf16 [m_rows][ldx]; y and out bf16 [m_rows][ldy] / [m_rows][ldo].  out may be
  * y itself with the same stride: rows without an adapter, or whose adapter has rank 0, are then not touched; no other overlap.
  * ids and ranks are checked on the device: an id outside -1 .. n_adapters-1 or a rank outside
  * 0 .. max_rank counts as no adapter and puts QG_ERR_INVALID_ARG into the workspace's status word
- * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^30.  Any number of calls may
- * share a workspace.  Deterministic; one launch. */
+ * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^30.  The
+ * workspace need not be zero-filled but for its status word; calls that overlap on the GPU must not share it.
+ * Deterministic; one launch for up to 256 rows, two more for every 16384 of more rows. */
 qg_status qlora(const qg_lora* lora, const int32_t* ids, int64_t m_rows, const void* x, int64_t ldx, const void* y,
                 int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -116,7 +116,7 @@ _SIGNATURES = {
     "qattn": (_I, [ctypes.POINTER(qg_kv_cache), ctypes.POINTER(qg_kv_batch), _I64, _I, _P, _I64, _I64, ctypes.c_float,
                    _I64, _P, _I64, _I64, _P, _SZ, _P]),
     "qg_rms_norm": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, ctypes.c_float, ctypes.c_float, ctypes.POINTER(qg_norm_out), _P]),
-    "qlora_workspace_size": (_SZ, []),
+    "qlora_workspace_size": (_SZ, [ctypes.POINTER(qg_lora), _I64]),
     "qlora": (_I, [ctypes.POINTER(qg_lora), _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _SZ, _P]),
     "qmoe_route_by": (_I, [ctypes.POINTER(qg_route_rule), _P, _I64, _I, _I, _P, _P, _P, _SZ, _P]),
 }
@@ -305,8 +305,8 @@ def qg_rms_norm(x_ptr: int, ldx: int, res_ptr: Optional[int], ldr: int, m: int, 
     _check(lib().qg_rms_norm(x_ptr, ldx, res_ptr, ldr, m, k, w_ptr, eps, weight_offset, out, stream), "qg_rms_norm")
 
 
-def qlora_workspace_size() -> int:
-    return lib().qlora_workspace_size()
+def qlora_workspace_size(lora: "qg_lora", m: int) -> int:
+    return lib().qlora_workspace_size(lora, m)
 
 
 def qlora(lora: "qg_lora", ids_ptr: int, m: int, x_ptr: int, ldx: int, y_ptr: int, ldy: int, out_ptr: int, ldo: int, ws_ptr: int,
@@ -709,7 +709,7 @@ class LoraAdapters:
 
 def lora_workspace_size(adapters: LoraAdapters, m: int) -> int:
     """Workspace bytes of ``lora`` for m rows."""
-    return qlora_workspace_size()
+    return qlora_workspace_size(adapters.desc, m)
 
 
 def lora(adapters: LoraAdapters, ids, x, y, out=None, workspace: Optional[Workspace] = None):
@@ -726,7 +726,7 @@ def lora(adapters: LoraAdapters, ids, x, y, out=None, workspace: Optional[Worksp
     else:
         op, ldo = _rows(out, m, adapters.n, torch.bfloat16, index, "lora: out")
     if workspace is None:
-        workspace = Workspace(qlora_workspace_size(), x.device)
+        workspace = Workspace(qlora_workspace_size(adapters.desc, m), x.device)
     elif workspace.index != index:
         raise QGError(1, "lora: the workspace on the adapters' device")
     st = _on(index, (_lib or lib()).qlora, adapters.desc, ids.data_ptr(), m, xp, ldx, yp, ldy, op, ldo, workspace.ptr, workspace.nbytes)

@@ -19,43 +19,15 @@
 // dealt to the MMAs' columns so that a lane ends up with eight contiguous outputs of a row: y
 // is read and written 16 bytes a lane.  h is split into two bf16 terms (16 bits of it), so the
 // only rounding to 16 bits is the output's.
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <stdint.h>
-
 #include <algorithm>
 
-#include "qg_internal.h"
-#include "qg_lora.h"
-#include "qg_sync.cuh"
+#include "qg_lora_dev.cuh"
 
 namespace qg {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-// The first `valid` (0 to 8) of eight bf16.
-__device__ __forceinline__ uint4 keep_first(uint4 v, int valid) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] &= 2 * i + 1 < valid ? 0xFFFFFFFFu : 2 * i < valid ? 0xFFFFu : 0u;
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
 // Eight elements of a row of k from column c, those past its end 0 and not read.
 __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int k) {
   if (c + 8 <= k) return __ldg(reinterpret_cast<const uint4*>(row + c));
@@ -64,29 +36,6 @@ __device__ __forceinline__ uint4 load8(const uint16_t* row, int c, int k) {
   for (int i = 0; i < 8; ++i)
     if (c + i < k) w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
   return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// Exclusive prefix sum of one count a thread over the block; the total in *total.
-__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int s = v;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int o = __shfl_up_sync(0xFFFFFFFFu, s, off);
-    if (lane >= off) s += o;
-  }
-  if (lane == 31) warp_sums[warp] = s;
-  __syncthreads();
-  int before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int c = warp_sums[w];
-    before += w < warp ? c : 0;
-    all += c;
-  }
-  __syncthreads();
-  *total = all;
-  return before + s - v;
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -109,24 +58,13 @@ struct Shape {
   static_assert((kTiles / kMt) * kKgroups == kWarps, "warps");
 };
 
-// What a CTA knows of the tiles: first[e] is adapter e's first tile; the last entry, number
-// n_adapters, are the rows without an adapter.
-struct Tiles {
-  int first[kLoraMaxAdapters + 2];
-  int warp_sums[kWarps];
-  int bin;
-};
-
-// Adapter of row i, n_adapters for none (and for an id out of range).
-__device__ __forceinline__ int bin_of(int id, int n_adapters) { return (unsigned)id < (unsigned)n_adapters ? id : n_adapters; }
-
 template <int R, int T>
 __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
   using S = Shape<R, T>;
   extern __shared__ __align__(16) uint8_t smem[];
   float* part = reinterpret_cast<float*>(smem);
   uint16_t* hs = reinterpret_cast<uint16_t*>(smem + S::kPartBytes);
-  __shared__ Tiles tl;
+  __shared__ Tiles<kThreads> tl;
   __shared__ int rows[T];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint32_t n_cta, rank;
@@ -136,80 +74,10 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
   if (tid == 0) pdl_launch_dependents();
   pdl_wait();
 
-  // rows of every adapter: a thread counts a run of rows of one adapter before it adds to it
-  const int bins = p.n_adapters + 1;
-  for (int e = tid; e <= bins; e += kThreads) tl.first[e] = 0;
-  __syncthreads();
-  const int per = (p.m + kThreads - 1) / kThreads, i0 = min(p.m, tid * per), i1 = min(p.m, i0 + per);
-  {
-    int run = 0, cur = -1;
-    bool bad = false;
-    for (int i = i0; i < i1; ++i) {
-      const int id = p.ids[i], e = bin_of(id, p.n_adapters);
-      bad |= id < -1 || id >= p.n_adapters;
-      if (e != cur) {
-        if (run) atomicAdd(&tl.first[cur], run);  // integer counts: order-free
-        cur = e;
-        run = 0;
-      }
-      ++run;
-    }
-    if (run) atomicAdd(&tl.first[cur], run);
-    if (bad) atomicCAS(p.status, 0, kStatusInvalid);
-  }
-  __syncthreads();
-  int n_tiles = 0;
-  {
-    constexpr int kPer = (kLoraMaxAdapters + 1 + kThreads - 1) / kThreads;
-    const int per_bin = (bins + kThreads - 1) / kThreads, e0 = tid * per_bin;
-    int c[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      c[i] = i < per_bin && e0 + i < bins ? (tl.first[e0 + i] + T - 1) / T : 0;
-      if (e0 + i == p.n_adapters && p.out == p.y) c[i] = 0;  // in place: nothing to do for rows without an adapter
-      sum += c[i];
-    }
-    int at = block_prefix(sum, tl.warp_sums, &n_tiles);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < per_bin && e0 + i < bins) {
-        tl.first[e0 + i] = at;
-        at += c[i];
-      }
-    if (tid == 0) tl.first[bins] = n_tiles;
-  }
-  __syncthreads();
-
+  tl.count(p, T);
+  const int n_tiles = tl.first[p.n_adapters + 1];
   for (int tile = cluster; tile < n_tiles; tile += n_clusters) {
-    // the tile's adapter and rows
-    for (int e = tid; e < bins; e += kThreads)
-      if (tl.first[e] <= tile && tile < tl.first[e + 1]) tl.bin = e;
-    if (tid < T) rows[tid] = -1;
-    __syncthreads();
-    const int e = tl.bin;
-    {
-      const int skip = (tile - tl.first[e]) * T;
-      int mine = 0;
-      for (int i = i0; i < i1; ++i) mine += bin_of(p.ids[i], p.n_adapters) == e;
-      int total;
-      int at = block_prefix(mine, tl.warp_sums, &total) - skip;
-      if (mine && at < T && at + mine > 0)
-        for (int i = i0; i < i1; ++i)
-          if (bin_of(p.ids[i], p.n_adapters) == e) {
-            if (at >= 0 && at < T) rows[at] = i;
-            ++at;
-          }
-    }
-    int ra = 0;
-    if (e < p.n_adapters) {
-      ra = p.ranks ? p.ranks[e] : p.max_rank;
-      if (ra < 0 || ra > p.max_rank) {
-        ra = 0;
-        if (tid == 0) atomicCAS(p.status, 0, kStatusInvalid);
-      }
-    }
-    __syncthreads();
-
+    const int e = tl.collect(p, T, tile, rows), ra = rank_of(p, e);
     if (ra) {  // phase 1
       const uint16_t* ea = p.a + (int64_t)e * p.max_rank * p.lda;
       const int kg = warp % S::kKgroups, rg = warp / S::kKgroups;
@@ -281,17 +149,10 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
           const float4 o = n_cta > 1 ? ld_cluster_f4(cluster_map(at, c)) : *reinterpret_cast<const float4*>(at);
           v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
         }
-        const float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
-        uint32_t top[2], rest[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          top[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
-          const float l = f[2 * j] - lo(top[j]), h = f[2 * j + 1] - hi(top[j]);
-          // an infinite h is its first term alone
-          rest[j] = pack_bf16(isinf(f[2 * j]) ? 0.0f : l, isinf(f[2 * j + 1]) ? 0.0f : h);
-        }
-        *reinterpret_cast<uint2*>(hs + row * S::kHRow + col) = make_uint2(top[0], top[1]);
-        *reinterpret_cast<uint2*>(hs + row * S::kHRow + R + col) = make_uint2(rest[0], rest[1]);
+        uint2 top, rest;
+        split_h(v, scale, top, rest);
+        *reinterpret_cast<uint2*>(hs + row * S::kHRow + col) = top;
+        *reinterpret_cast<uint2*>(hs + row * S::kHRow + R + col) = rest;
       }
       __syncthreads();
     }
@@ -363,13 +224,13 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
               uint32_t w[4] = {v.x, v.y, v.z, v.w};
               if (ra)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[j] = pack_bf16(lo(w[j]) + acc[j][2 * h], hi(w[j]) + acc[j][2 * h + 1]);
+                for (int j = 0; j < 4; ++j) w[j] = pack_bf16(bf_lo(w[j]) + acc[j][2 * h], bf_hi(w[j]) + acc[j][2 * h + 1]);
               *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
 #pragma unroll
               for (int c = 0; c < 8; ++c)
                 if (col + c < p.n)
-                  to[c] = ra ? (uint16_t)pack_bf16(lo(from[c]) + acc[c >> 1][2 * h + (c & 1)], 0.0f) : from[c];
+                  to[c] = ra ? (uint16_t)pack_bf16(bf_lo(from[c]) + acc[c >> 1][2 * h + (c & 1)], 0.0f) : from[c];
             }
           }
         }
@@ -386,9 +247,8 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
 template <int R, int T>
 int launch(const LoraArgs& p, const DeviceInfo& dev, cudaStream_t s) {
   using S = Shape<R, T>;
-  if (S::kSmem > 40 * 1024 &&  // static shared memory counts too
-      cudaFuncSetAttribute(lora_kernel<R, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) != cudaSuccess)
-    return QG_ERR_CUDA;
+  static std::atomic<unsigned long long> configured{0};
+  if (!allow_smem((const void*)lora_kernel<R, T>, S::kSmem, configured)) return QG_ERR_CUDA;
   // about as many tiles as there are: full ones, or one for each adapter
   const int adapters = std::min(p.n_adapters + 1, p.m);
   const int full = (p.m + T - 1) / T, likely = std::max(full, std::min(p.n_adapters, p.m)), most = std::min(p.m, full + adapters);
@@ -424,8 +284,7 @@ int launch_rank(const LoraArgs& p, const DeviceInfo& dev, cudaStream_t s) {
 }  // namespace
 
 int launch_lora(const LoraArgs& p, const DeviceInfo& dev, void* stream) {
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return p.m <= 256 ? launch_rank<16>(p, dev, s) : launch_rank<64>(p, dev, s);
+  return launch_rank<16>(p, dev, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace qg

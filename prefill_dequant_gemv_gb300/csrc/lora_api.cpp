@@ -12,7 +12,14 @@ bool misaligned(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>
 
 }  // namespace
 
-extern "C" size_t qlora_workspace_size(void) { return kWsHeader; }
+extern "C" size_t qlora_workspace_size(const qg_lora* l, int64_t m) {
+  if (!l || m < 0 || m >= (1 << 27) || l->n_adapters < 1 || l->n_adapters > kLoraMaxAdapters || l->max_rank < 1 ||
+      l->max_rank > kLoraMaxRank)
+    return 0;
+  if (m <= kLoraFewRows) return kWsHeader;
+  DeviceInfo dev;
+  return current_device_info(&dev) ? kWsHeader + lora_rows_bytes(l->n_adapters, l->max_rank, m, dev) : 0;
+}
 
 extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, const void* x, int64_t ldx, const void* y,
                            int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
@@ -50,5 +57,7 @@ extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, cons
   p.ldy = ldy;
   p.ldo = ldo;
   p.status = static_cast<int*>(workspace);
-  return (qg_status)launch_lora(p, dev, stream);
+  if (m <= kLoraFewRows) return (qg_status)launch_lora(p, dev, stream);
+  if (workspace_bytes < kWsHeader + lora_rows_bytes(l->n_adapters, l->max_rank, m, dev)) return QG_ERR_WORKSPACE_TOO_SMALL;
+  return (qg_status)launch_lora_rows(p, dev, static_cast<char*>(workspace) + kWsHeader, stream);
 }

@@ -25,6 +25,11 @@ struct LoraArgs {
   int64_t ldx, ldy, ldo;
   int* status;
 };
+constexpr int64_t kLoraFewRows = 256;       // at most: one launch of clusters (lora.cu); more: shrink and expand (lora_rows.cu)
+constexpr int64_t kLoraRowsAtOnce = 16384;  // of a call of many rows: what a CTA counts and lists itself
 int launch_lora(const LoraArgs& a, const DeviceInfo& dev, void* stream);
+// Scratch of the many-row form for h's parts, and its launches.
+size_t lora_rows_bytes(int n_adapters, int max_rank, int64_t m, const DeviceInfo& dev);
+int launch_lora_rows(const LoraArgs& a, const DeviceInfo& dev, void* parts, void* stream);
 
 }  // namespace qg

@@ -1,0 +1,179 @@
+// Device functions shared by the low-rank adapters' kernels: the rows of every adapter as tiles,
+// and the warp-level product.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <atomic>
+
+#include "qg_lora.h"
+#include "qg_sync.cuh"
+
+namespace qg {
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device; once a device and kernel (`done`).
+inline bool allow_smem(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load() & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+  done.fetch_or(bit);
+  return true;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // a in the low half
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The first `valid` of eight bf16 (all of them from 8, none below 1).
+__device__ __forceinline__ uint4 keep_first(uint4 v, int valid) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] &= 2 * i + 1 < valid ? 0xFFFFFFFFu : 2 * i < valid ? 0xFFFFu : 0u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Four h as two bf16 terms each: 16 bits of the value; an infinite one is its first term alone.
+__device__ __forceinline__ void split_h(float4 v, float scale, uint2& top, uint2& rest) {
+  const float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+  uint32_t a[2], b[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    a[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
+    const float l = f[2 * j] - bf_lo(a[j]), h = f[2 * j + 1] - bf_hi(a[j]);
+    b[j] = pack_bf16(isinf(f[2 * j]) ? 0.0f : l, isinf(f[2 * j + 1]) ? 0.0f : h);
+  }
+  top = make_uint2(a[0], a[1]);
+  rest = make_uint2(b[0], b[1]);
+}
+
+// Exclusive prefix sum of one count a thread over a block of THREADS; the total in *total.
+template <int THREADS>
+__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int s = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, s, off);
+    if (lane >= off) s += o;
+  }
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    const int c = warp_sums[w];
+    before += w < warp ? c : 0;
+    all += c;
+  }
+  __syncthreads();
+  *total = all;
+  return before + s - v;
+}
+
+// Adapter of a row, n_adapters for none (and for an id out of range).
+__device__ __forceinline__ int bin_of(int id, int n_adapters) { return (unsigned)id < (unsigned)n_adapters ? id : n_adapters; }
+
+// The rows of every adapter in tiles of T, adapter by adapter; first[e] is adapter e's first tile.
+// first[n_adapters]: the rows without one; first[n_adapters + 1]: the number of tiles.
+// Every CTA builds the same table: ids are few bytes beside x and y.
+template <int THREADS>
+struct Tiles {
+  int first[kLoraMaxAdapters + 2];
+  int warp_sums[THREADS / 32];
+  int bin;
+
+  // The rows that this thread looks at.
+  static __device__ __forceinline__ void share(const LoraArgs& p, int* i0, int* i1) {
+    const int per = (p.m + THREADS - 1) / THREADS;
+    *i0 = min(p.m, (int)threadIdx.x * per);
+    *i1 = min(p.m, *i0 + per);
+  }
+
+  __device__ __forceinline__ void count(const LoraArgs& p, int T) {
+    const int tid = threadIdx.x, bins = p.n_adapters + 1;
+    for (int e = tid; e <= bins; e += THREADS) first[e] = 0;
+    __syncthreads();
+    int i0, i1, run = 0, cur = -1;  // a run of rows of one adapter is counted before it is added
+    share(p, &i0, &i1);
+    bool bad = false;
+    for (int i = i0; i < i1; ++i) {
+      const int id = p.ids[i], e = bin_of(id, p.n_adapters);
+      bad |= id < -1 || id >= p.n_adapters;
+      if (e != cur) {
+        if (run) atomicAdd(&first[cur], run);  // integer counts: order-free
+        cur = e;
+        run = 0;
+      }
+      ++run;
+    }
+    if (run) atomicAdd(&first[cur], run);
+    if (bad) atomicCAS(p.status, 0, kStatusInvalid);
+    __syncthreads();
+    constexpr int kPer = (kLoraMaxAdapters + 1 + THREADS - 1) / THREADS;
+    const int per_bin = (bins + THREADS - 1) / THREADS, e0 = tid * per_bin;
+    int c[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      c[i] = i < per_bin && e0 + i < bins ? (first[e0 + i] + T - 1) / T : 0;
+      if (e0 + i == p.n_adapters && p.out == p.y) c[i] = 0;  // in place: nothing to do without an adapter
+      sum += c[i];
+    }
+    int total, at = block_prefix<THREADS>(sum, warp_sums, &total);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (i < per_bin && e0 + i < bins) {
+        first[e0 + i] = at;
+        at += c[i];
+      }
+    if (tid == 0) first[bins] = total;
+    __syncthreads();
+  }
+
+  // Tile's adapter (the return value) and rows, in ascending order, -1 past the last.
+  __device__ __forceinline__ int collect(const LoraArgs& p, int T, int tile, int* rows) {
+    const int tid = threadIdx.x, bins = p.n_adapters + 1;
+    for (int e = tid; e < bins; e += THREADS)
+      if (first[e] <= tile && tile < first[e + 1]) bin = e;
+    for (int i = tid; i < T; i += THREADS) rows[i] = -1;
+    __syncthreads();
+    const int e = bin, skip = (tile - first[e]) * T;
+    int i0, i1, mine = 0, total;
+    share(p, &i0, &i1);
+    for (int i = i0; i < i1; ++i) mine += bin_of(p.ids[i], p.n_adapters) == e;
+    int at = block_prefix<THREADS>(mine, warp_sums, &total) - skip;
+    if (mine && at < T && at + mine > 0)
+      for (int i = i0; i < i1; ++i)
+        if (bin_of(p.ids[i], p.n_adapters) == e) {
+          if (at >= 0 && at < T) rows[at] = i;
+          ++at;
+        }
+    __syncthreads();
+    return e;
+  }
+};
+
+// Rank of adapter e (0 for the rows without one); one out of range counts as 0 and is reported.
+__device__ __forceinline__ int rank_of(const LoraArgs& p, int e) {
+  if (e >= p.n_adapters) return 0;
+  const int r = p.ranks ? p.ranks[e] : p.max_rank;
+  if (r >= 0 && r <= p.max_rank) return r;
+  atomicCAS(p.status, 0, kStatusInvalid);
+  return 0;
+}
+
+}  // namespace qg

@@ -73,7 +73,7 @@ def test_lora_refusals(q, over, want):
 
 def test_lora_refuses_no_descriptor(q):
     assert q.lib().qlora(None, 0x5000, 8, 0x10000, 512, 0x20000, 256, 0x30000, 256, 0x40000, 256, None) == INVALID
-    assert q.qlora_workspace_size() == 256
+    assert q.qlora_workspace_size(lora_desc(q), 8) == 256 and q.qlora_workspace_size(lora_desc(q, max_rank=136), 8) == 0
 
 
 def route(q, logits=0x10000, t=4, e=64, k=4, ids=0x20000, w=0x30000, ws=0x40000, wsb=1 << 30, rule="rule", **over):
