@@ -3,20 +3,19 @@
 //
 // Both stream their long operand once (x; y and out) and are bound by HBM; A, B and h
 // come from L2.  Rows of one adapter are taken 64 at a time (a tile).  The tiles' inputs (shrink)
-// or outputs (expand), cut into chunks, form one line of units that the CTAs, one an SM,
+// or outputs (expand), cut into chunks, form one line of units that the CTAs
 // share evenly whatever the sizes: a CTA's range may begin and end inside a tile.  In
 // shrink that leaves a tile's h in parts, one for every CTA on it; CTA c's part of tile t is
 // number c + t (each step along the line raises one of the two), and expand adds a tile's
 // parts in that order, so results do not depend on timing.
 //
-// Rows lie anywhere, so a chunk of a tile is one bulk copy per row (512 bytes of a row in expand), into a
-// ring in shared memory that one warp keeps filled; in expand the sum is written over y in the
-// ring and leaves by bulk copies too.  Row pitches of 64 bytes past a multiple of 128 put the
-// eight 16-byte pieces of a fragment's quarter into distinct banks.
+// Every lane copies the 16-byte pieces that it will multiply itself, into slots of shared memory of its
+// own, some chunks ahead (cp.async): rows may lie anywhere, nothing waits for another warp,
+// what lies past a row's end comes as zeros, and the loads in flight take no registers.
 //
-// The products are warp-level MMAs (m16n8k16): 1024 multiply-adds a clock and SM.  A tile of 64 rows and
-// rank 64 takes some 60% of that rate when HBM is saturated, h's two bf16 terms included, and the fragments'
-// layout is what lets a lane hold eight contiguous outputs of a row (see lora.cu).
+// The products are warp-level MMAs (m16n8k16): 1024 multiply-adds a clock and SM, measured.  A tile of 64 rows
+// and rank 64 takes some 75% of that rate when HBM is saturated, h's two bf16 terms included, and the
+// fragments' layout is what lets a lane hold eight contiguous outputs of a row (see lora.cu).
 #include <algorithm>
 
 #include "qg_lora_dev.cuh"
@@ -24,59 +23,67 @@
 namespace qg {
 namespace {
 
-// A bounded wait with one answer for the warp.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, int pass, int* status) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, pass & 1, status));
-}
-
 constexpr int T = 64;           // rows of a tile
 constexpr int kBatch = 16;      // tiles whose rows a CTA lists at a time
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 
-// 1-D bulk copy shared -> global.
-__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+// 16 bytes global -> shared, those past the first `bytes` (0: none is read) as zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+// The same by way of L1, for what another warp of the CTA reads as well.
+__device__ __forceinline__ void copy16_l1(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ int bytes_of(int left) { return 2 * max(0, min(8, left)); }
 
 // The line of units: CTA c's range, and the CTA of a unit.  Never more CTAs than units.
 __device__ __forceinline__ int64_t line_begin(int64_t units, int ctas, int c) { return units * c / ctas; }
 __device__ __forceinline__ int line_owner(int64_t units, int ctas, int64_t u) { return (int)(((u + 1) * ctas - 1) / units); }
 
+// The tiles of a batch: rows, adapter and rank.
+struct Batch {
+  int rows[kBatch][T];
+  int bins[kBatch], ranks[kBatch];
+  __device__ __forceinline__ void fill(const LoraArgs& p, Tiles<kThreads>& tl, int t0, int nt) {
+    for (int i = 0; i < nt; ++i) {
+      const int e = tl.collect(p, T, t0 + i, rows[i]);
+      if (threadIdx.x == 0) {
+        bins[i] = e;
+        ranks[i] = rank_of(p, e);
+      }
+    }
+    __syncthreads();
+  }
+};
+
 // ------------------------------------------------------------------ shrink
 template <int R>
 struct Shrink {
-  static constexpr int kWidth = R <= 32 ? 256 : 128;  // inputs of a chunk
-  static constexpr int kPitch = 2 * kWidth + 64;      // bytes
-  static constexpr int kStages = R == 16 || R == 64 ? 4 : 3;
-  static constexpr int kStage = (T + R) * kPitch;
-  static constexpr int kSumRow = R + 4;               // floats
-  static constexpr size_t kSmem = (size_t)kStages * kStage + T * kSumRow * 4;
-  static constexpr int kThreads = 288;                // eight warps of products, one of copies
+  static constexpr int kSplit = R <= 32 ? 1 : 2;          // groups of warps that share a tile's rows
+  static constexpr int kParts = kWarps / kSplit;          // warps that share a chunk's inputs, 32 each
+  static constexpr int kMt = T / 16 / kSplit;             // row tiles of 16 a warp
+  static constexpr int kWidth = 32 * kParts;              // inputs of a chunk
+  static constexpr int kPieces = 2 * kMt + R / 8;         // of 16 bytes a lane and chunk
+  static constexpr int kAhead = R <= 64 ? 3 : 2;          // chunks in flight: slots of a lane
+  static constexpr int kSumRow = R + 4;                   // floats
+  static constexpr size_t kRing = (size_t)kWarps * kAhead * kPieces * 512;
+  static constexpr size_t kSmem = kRing + T * kSumRow * 4;
 };
 
 template <int R>
-__global__ void __launch_bounds__(288, 1) lora_shrink_kernel(LoraArgs p, float* parts) {
+__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs p, float* parts) {
   using S = Shrink<R>;
   extern __shared__ __align__(128) uint8_t smem[];
-  float* sum = reinterpret_cast<float*>(smem + S::kStages * S::kStage);
-  __shared__ Tiles<S::kThreads> tl;
-  __shared__ int rows[kBatch][T];
-  __shared__ int bins[kBatch], ranks[kBatch];
-  __shared__ uint64_t full[S::kStages], empty[S::kStages];
+  float* sum = reinterpret_cast<float*>(smem + S::kRing);
+  __shared__ Tiles<kThreads> tl;
+  __shared__ Batch b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 8);
-    }
-    fence_mbar_init();
-  }
   pdl_wait();
   if (tid == 0) pdl_launch_dependents();  // after the wait: what this call reads is there for expand as well
   tl.count(p, T);
@@ -86,138 +93,113 @@ __global__ void __launch_bounds__(288, 1) lora_shrink_kernel(LoraArgs p, float* 
   if (c >= ctas) return;
   const int64_t u0 = line_begin(units, ctas, c), u1 = line_begin(units, ctas, c + 1);
   const int t_first = (int)(u0 / chunks), t_last = (int)((u1 - 1) / chunks);
+  const int half = warp % S::kSplit, part = warp / S::kSplit;
+  uint8_t* mine = smem + (size_t)warp * S::kAhead * S::kPieces * 512 + lane * 16;
+  const uint32_t mine_at = smem_u32(mine);
 
-  int it = 0;  // chunks so far: ring slot it % kStages, pass it / kStages
-  bool ok = true;
   for (int t0 = t_first; t0 <= t_last; t0 += kBatch) {
     const int nt = min(kBatch, t_last + 1 - t0);
-    for (int i = 0; i < nt; ++i) {
-      const int e = tl.collect(p, T, t0 + i, rows[i]);
-      if (tid == 0) {
-        bins[i] = e;
-        ranks[i] = rank_of(p, e);
+    b.fill(p, tl, t0, nt);
+    const int64_t b0 = max(u0, (int64_t)t0 * chunks);
+    const int n = (int)(min(u1, (int64_t)(t0 + nt) * chunks) - b0);
+    int fi = (int)(b0 / chunks) - t0, fc = (int)(b0 % chunks);  // tile and chunk of the next copies
+    auto fetch = [&](int j) {
+      if (j < n) {
+        const int e = b.bins[fi], ra = b.ranks[fi], col = fc * S::kWidth + part * 32 + 8 * t;
+        const uint32_t to = mine_at + (j % S::kAhead) * S::kPieces * 512;
+        const int left = ra ? bytes_of(p.k - col) : 0;
+#pragma unroll
+        for (int i = 0; i < 2 * S::kMt; ++i) {
+          const int r = b.rows[fi][half * (T / S::kSplit) + i * 8 + g];
+          copy16(to + i * 512, r >= 0 && left ? p.x + r * p.ldx + col : p.x, r >= 0 ? left : 0);
+        }
+        const uint16_t* ea = p.a + ((int64_t)e * p.max_rank + g) * p.lda + col;
+#pragma unroll
+        for (int i = 0; i < R / 8; ++i) {
+          const bool in = i * 8 + g < ra && left;
+          const uint16_t* from = in ? ea + (int64_t)i * 8 * p.lda : p.a;
+          if (S::kSplit > 1)
+            copy16_l1(to + (2 * S::kMt + i) * 512, from, in ? left : 0);
+          else
+            copy16(to + (2 * S::kMt + i) * 512, from, in ? left : 0);
+        }
+        if (++fc == chunks) fc = 0, ++fi;
       }
-    }
-    __syncthreads();
-    for (int i = 0; i < nt; ++i) {
-      const int tile = t0 + i, ra = ranks[i];
-      const int k0 = (int)(max(u0, (int64_t)tile * chunks) - (int64_t)tile * chunks);
-      const int k1 = (int)(min(u1, (int64_t)(tile + 1) * chunks) - (int64_t)tile * chunks);
-      if (ra == 0) continue;
-      if (warp == 8) {  // copies
-        const uint16_t* ea = p.a + (int64_t)bins[i] * p.max_rank * p.lda;
-        const int ra0 = rows[i][lane], ra1 = rows[i][lane + 32];
-        const int live = __popc(__ballot_sync(0xFFFFFFFFu, ra0 >= 0)) + __popc(__ballot_sync(0xFFFFFFFFu, ra1 >= 0));
-        for (int ch = k0; ch < k1 && ok; ++ch, ++it) {
-          const int s = it % S::kStages;
-          if (it >= S::kStages) ok = wait_warp(&empty[s], it / S::kStages - 1, p.status);
-          if (!ok) break;
-          uint8_t* st = smem + s * S::kStage;
-          const int col = ch * S::kWidth;
-          const uint32_t bytes = (uint32_t)(min(S::kWidth, p.k - col) + 7) / 8 * 16;  // up to the 16 bytes that hold the last
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes * (uint32_t)(live + ra));
-          __syncwarp();
-          if (ra0 >= 0) bulk_g2s(st + lane * S::kPitch, p.x + ra0 * p.ldx + col, bytes, &full[s]);
-          if (ra1 >= 0) bulk_g2s(st + (lane + 32) * S::kPitch, p.x + ra1 * p.ldx + col, bytes, &full[s]);
-          for (int j = lane; j < ra; j += 32) bulk_g2s(st + (T + j) * S::kPitch, ea + (int64_t)j * p.lda + col, bytes, &full[s]);
-        }
-      } else {  // products: two halves of the rows, four quarters of a chunk's inputs
-        const int half = warp & 1, part = warp >> 1;
-        float acc[2][R / 8][4] = {};
-        for (int ch = k0; ch < k1 && ok; ++ch, ++it) {
-          const int s = it % S::kStages;
-          ok = wait_warp(&full[s], it / S::kStages, p.status);
-          if (!ok) break;
-          const uint8_t* st = smem + s * S::kStage;
-          const int left = p.k - ch * S::kWidth;  // inputs from the chunk's start on
+      copy_commit();
+    };
 #pragma unroll
-          for (int q = 0; q < S::kWidth / 128; ++q) {
-            const int col = part * (S::kWidth / 4) + q * 32 + 8 * t;
-            const int valid = left - col;
-            uint4 xv[2][2];
+    for (int j = 0; j < S::kAhead; ++j) fetch(j);
+    int i = (int)(b0 / chunks) - t0, ch = (int)(b0 % chunks);
+    float acc[S::kMt][R / 8][4] = {};
+    for (int j = 0; j < n; ++j) {
+      copy_wait<S::kAhead - 1>();
+      const uint8_t* from = mine + (j % S::kAhead) * S::kPieces * 512;
+      const int ra = b.ranks[i];
+      uint4 xv[S::kMt][2];
 #pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2)
+      for (int m = 0; m < S::kMt; ++m)
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                xv[i2][h] = *reinterpret_cast<const uint4*>(st + (half * 32 + i2 * 16 + h * 8 + g) * S::kPitch + 2 * col);
-                if (valid < 8) xv[i2][h] = keep_first(xv[i2][h], valid);
-              }
+        for (int h = 0; h < 2; ++h) xv[m][h] = *reinterpret_cast<const uint4*>(from + (2 * m + h) * 512);
 #pragma unroll
-            for (int j = 0; j < R / 8; ++j) {
-              if (j * 8 >= ra) break;
-              uint4 av = *reinterpret_cast<const uint4*>(st + (T + j * 8 + g) * S::kPitch + 2 * col);
-              if (valid < 8 || j * 8 + g >= ra) av = keep_first(av, j * 8 + g < ra ? valid : 0);
+      for (int q = 0; q < R / 8; ++q)
+        if (q * 8 < ra) {
+          const uint4 av = *reinterpret_cast<const uint4*>(from + (2 * S::kMt + q) * 512);
 #pragma unroll
-              for (int i2 = 0; i2 < 2; ++i2) {
-                mma16816(acc[i2][j], xv[i2][0].x, xv[i2][1].x, xv[i2][0].y, xv[i2][1].y, av.x, av.y);
-                mma16816(acc[i2][j], xv[i2][0].z, xv[i2][1].z, xv[i2][0].w, xv[i2][1].w, av.z, av.w);
-              }
-            }
+          for (int m = 0; m < S::kMt; ++m) {
+            mma16816(acc[m][q], xv[m][0].x, xv[m][1].x, xv[m][0].y, xv[m][1].y, av.x, av.y);
+            mma16816(acc[m][q], xv[m][0].z, xv[m][1].z, xv[m][0].w, xv[m][1].w, av.z, av.w);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty[s]);
         }
-        // the four quarters' sums, one after the other: 3 to 2, 2 to 1, 1 to 0
-        float* mine = sum + (half * 32 + g) * S::kSumRow + 2 * t;
+      fetch(j + S::kAhead);  // into the slot whose pieces the products have taken
+      if (++ch < chunks && j + 1 < n) continue;
+      // the tile's end, or the CTA's: the warps' sums over their inputs, one after the other
+      if (ra) {
+        float* at = sum + (half * (T / S::kSplit) + g) * S::kSumRow + 2 * t;
+#pragma unroll 1
+        for (int w = 0; w < S::kParts; ++w) {
+          if (part == w) {
 #pragma unroll
-        for (int from = 3; from >= 1; --from) {
-          if (part == from) {
-#pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2)
+            for (int m = 0; m < S::kMt; ++m)
 #pragma unroll
               for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < R / 8; ++j)
-                  *reinterpret_cast<float2*>(mine + (i2 * 16 + h * 8) * S::kSumRow + j * 8) =
-                      make_float2(acc[i2][j][2 * h], acc[i2][j][2 * h + 1]);
-          }
-          named_sync(1, 256);
-          if (part == from - 1) {
-#pragma unroll
-            for (int i2 = 0; i2 < 2; ++i2)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < R / 8; ++j) {
-                  const float2 v = *reinterpret_cast<float2*>(mine + (i2 * 16 + h * 8) * S::kSumRow + j * 8);
-                  acc[i2][j][2 * h] += v.x;
-                  acc[i2][j][2 * h + 1] += v.y;
+                for (int q = 0; q < R / 8; ++q) {
+                  float2* to = reinterpret_cast<float2*>(at + (m * 16 + h * 8) * S::kSumRow + q * 8);
+                  float2 v = make_float2(acc[m][q][2 * h], acc[m][q][2 * h + 1]);
+                  if (w) v.x += to->x, v.y += to->y;
+                  *to = v;
                 }
           }
-          named_sync(1, 256);
+          __syncthreads();
         }
-        if (part == 0) {
-          float* to = parts + ((int64_t)(c + tile) * T + half * 32 + g) * R + 2 * t;
-#pragma unroll
-          for (int i2 = 0; i2 < 2; ++i2)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int j = 0; j < R / 8; ++j)
-                *reinterpret_cast<float2*>(to + (i2 * 16 + h * 8) * R + j * 8) = make_float2(acc[i2][j][2 * h], acc[i2][j][2 * h + 1]);
-        }
+        float* to = parts + (int64_t)(c + t0 + i) * T * R;
+        for (int x = tid; x < T * R / 4; x += kThreads)
+          reinterpret_cast<float4*>(to)[x] = *reinterpret_cast<const float4*>(sum + x / (R / 4) * S::kSumRow + x % (R / 4) * 4);
+        __syncthreads();
       }
+#pragma unroll
+      for (int m = 0; m < S::kMt; ++m)
+#pragma unroll
+        for (int q = 0; q < R / 8; ++q)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[m][q][x] = 0.0f;
+      ch = 0;
+      ++i;
     }
+    copy_wait<0>();
     __syncthreads();  // the lists are written again
   }
-  if (warp == 8)  // after a wait that gave up, copies may be in flight: not past the CTA's end
-    for (int i = max(0, it - S::kStages); i < it; ++i) wait_warp(&full[i % S::kStages], i / S::kStages, p.status);
 }
 
 // ------------------------------------------------------------------ expand
 template <int R>
 struct Expand {
-  static constexpr int kWidth = 256;              // outputs of a chunk
-  static constexpr int kPitch = 2 * kWidth + 64;  // bytes
-  static constexpr int kStages = 4;
-  static constexpr int kAhead = 2;                // chunks between a load and its use
-  static constexpr int kStage = T * kPitch;
-  static constexpr int kHRow = R == 16 ? 48 : 2 * R + 32;  // bf16
-  static constexpr size_t kSmem = (size_t)kStages * kStage + 2 * T * kHRow;
-  static constexpr int kSplit = 1;                // groups of warps that share a tile's rows
-  static constexpr int kWarps = 8 * kSplit;       // of products; one more of copies
-  static constexpr int kThreads = 32 * kWarps + 32;
-  static constexpr int kMt = T / 16 / kSplit;     // row tiles of 16 a warp
+  static constexpr int kWidth = 32 * kWarps;      // outputs of a chunk
+  static constexpr int kMt = T / 16;
+  static constexpr int kAhead = 3;
+  static constexpr int kHRow = R == 16 ? 48 : 2 * R + 32;  // bf16: a fragment's pieces in distinct banks
+  static constexpr size_t kRing = (size_t)kWarps * kAhead * 2 * kMt * 512;
+  static constexpr size_t kSmem = kRing + 2 * T * kHRow;
   static constexpr int kHalf = R <= 64 ? R : 64;  // ranks of B in registers at a time
   static constexpr int kSteps = kHalf == 16 ? 1 : kHalf / 32;
 };
@@ -251,23 +233,14 @@ __device__ __forceinline__ void load_b(const LoraArgs& p, const uint16_t* eb, in
 }
 
 template <int R>
-__global__ void __launch_bounds__(Expand<R>::kThreads, 1) lora_expand_kernel(LoraArgs p, const float* parts, int shrink_ctas, int shrink_width) {
+__global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs p, const float* parts, int shrink_ctas, int shrink_width) {
   using S = Expand<R>;
   extern __shared__ __align__(128) uint8_t smem[];
-  uint16_t* hs = reinterpret_cast<uint16_t*>(smem + S::kStages * S::kStage);
-  __shared__ Tiles<S::kThreads> tl;
-  __shared__ int rows[kBatch][T];
-  __shared__ int bins[kBatch], ranks[kBatch];
-  __shared__ uint64_t full[S::kStages], done[S::kStages];
+  uint16_t* hs = reinterpret_cast<uint16_t*>(smem + S::kRing);
+  __shared__ Tiles<kThreads> tl;
+  __shared__ Batch b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  if (tid == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      mbar_init(&full[i], 1);
-      mbar_init(&done[i], S::kWarps);
-    }
-    fence_mbar_init();
-    pdl_launch_dependents();
-  }
+  if (tid == 0) pdl_launch_dependents();
   tl.count(p, T);
   const int chunks = (p.n + S::kWidth - 1) / S::kWidth, n_tiles = tl.first[p.n_adapters + 1];
   const int64_t units = (int64_t)n_tiles * chunks;
@@ -281,156 +254,139 @@ __global__ void __launch_bounds__(Expand<R>::kThreads, 1) lora_expand_kernel(Lor
   const int k_chunks = (p.k + shrink_width - 1) / shrink_width;
   const int64_t k_units = (int64_t)tl.first[p.n_adapters] * k_chunks;
   const int k_ctas = (int)min((int64_t)shrink_ctas, k_units);
+  uint8_t* mine = smem + (size_t)warp * S::kAhead * 2 * S::kMt * 512 + lane * 16;
+  const uint32_t mine_at = smem_u32(mine);
 
-  int it = 0;
-  bool ok = true, waited = false;
   for (int t0 = t_first; t0 <= t_last; t0 += kBatch) {
     const int nt = min(kBatch, t_last + 1 - t0);
-    for (int i = 0; i < nt; ++i) {
-      const int e = tl.collect(p, T, t0 + i, rows[i]);
-      if (tid == 0) {
-        bins[i] = e;
-        ranks[i] = rank_of(p, e);
-      }
-    }
-    __syncthreads();
-    if (warp == S::kWarps) {  // copies: loads kAhead chunks before the stores
-      const int64_t b0 = max(u0, (int64_t)t0 * chunks), b1 = min(u1, (int64_t)(t0 + nt) * chunks);
-      const int n = (int)(b1 - b0);
-      for (int j = 0; j < n + S::kAhead && ok; ++j) {
-        if (j >= S::kAhead) {  // chunk j - kAhead leaves
-          const int64_t u = b0 + j - S::kAhead;
-          const int i = (int)(u / chunks) - t0, col = (int)(u % chunks) * S::kWidth, at = it + j - S::kAhead, s = at % S::kStages;
-          ok = wait_warp(&done[s], at / S::kStages, p.status);
-          if (!ok) break;
-          const uint32_t bytes = (uint32_t)min(S::kWidth, p.n - col) / 8 * 16;  // whole vectors; the products' warps store the rest
-          if (bytes && (ranks[i] || p.out != p.y))
-            for (int r = lane; r < T; r += 32)
-              if (rows[i][r] >= 0) bulk_s2g(p.out + rows[i][r] * p.ldo + col, smem + s * S::kStage + r * S::kPitch, bytes);
-          bulk_commit();
+    b.fill(p, tl, t0, nt);
+    const int64_t b0 = max(u0, (int64_t)t0 * chunks);
+    const int n = (int)(min(u1, (int64_t)(t0 + nt) * chunks) - b0);
+    int fi = (int)(b0 / chunks) - t0, fc = (int)(b0 % chunks);
+    auto fetch = [&](int j) {
+      if (j < n) {
+        const int col = fc * S::kWidth + warp * 32 + 8 * t, left = bytes_of(p.n - col);
+        const uint32_t to = mine_at + (j % S::kAhead) * 2 * S::kMt * 512;
+#pragma unroll
+        for (int i = 0; i < 2 * S::kMt; ++i) {
+          const int r = b.rows[fi][i * 8 + g];
+          copy16(to + i * 512, r >= 0 && left ? p.y + r * p.ldy + col : p.y, r >= 0 ? left : 0);
         }
-        if (j < n) {  // chunk j comes; the slot's last chunk, j - kStages, left kStages - kAhead stores ago
-          const int64_t u = b0 + j;
-          const int i = (int)(u / chunks) - t0, col = (int)(u % chunks) * S::kWidth, s = (it + j) % S::kStages;
-          bulk_wait_read<S::kStages - S::kAhead>();
-          __syncwarp();
-          const uint32_t bytes = (uint32_t)(min(S::kWidth, p.n - col) + 7) / 8 * 16;
-          const int r0 = rows[i][lane], r1 = rows[i][lane + 32];
-          const int live = __popc(__ballot_sync(0xFFFFFFFFu, r0 >= 0)) + __popc(__ballot_sync(0xFFFFFFFFu, r1 >= 0));
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], bytes * live);
-          __syncwarp();
-          if (r0 >= 0) bulk_g2s(smem + s * S::kStage + lane * S::kPitch, p.y + r0 * p.ldy + col, bytes, &full[s]);
-          if (r1 >= 0) bulk_g2s(smem + s * S::kStage + (lane + 32) * S::kPitch, p.y + r1 * p.ldy + col, bytes, &full[s]);
-        }
+        if (++fc == chunks) fc = 0, ++fi;
       }
-      it += n;
-    } else {  // products: eight groups of 32 outputs
-      const int group = warp & 7, half = warp >> 3;
-      if (!waited) pdl_wait();  // shrink has ended: its parts are there
-      waited = true;
-      for (int i = 0; i < nt && ok; ++i) {
-        const int tile = t0 + i, e = bins[i], ra = ranks[i];
-        const int c0 = (int)(max(u0, (int64_t)tile * chunks) - (int64_t)tile * chunks);
-        const int c1 = (int)(min(u1, (int64_t)(tile + 1) * chunks) - (int64_t)tile * chunks);
-        const uint16_t* eb = p.b + (int64_t)(e < p.n_adapters ? e : 0) * p.n * p.max_rank;
-        uint4 bv[S::kSteps][4];
-        if (ra) {
-          load_b<R>(p, eb, ra, c0 * S::kWidth + group * 32, 0, g, t, bv);
-          named_sync(1, 32 * S::kWarps);  // every warp is done with the last tile's h
-          const int p0 = line_owner(k_units, k_ctas, (int64_t)tile * k_chunks),
-                    p1 = line_owner(k_units, k_ctas, (int64_t)(tile + 1) * k_chunks - 1);
-          const float scale = p.scales[e];
-          for (int x = tid; x < T * R / 4; x += 32 * S::kWarps) {
-            const int row = x / (R / 4), col = (x % (R / 4)) * 4;
-            const float* from = parts + ((int64_t)(p0 + tile) * T + row) * R + col;
-            float4 v = __ldcg(reinterpret_cast<const float4*>(from));
-            for (int q = p0 + 1; q <= p1; ++q) {
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(from + (int64_t)(q - p0) * T * R));
-              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
-            uint2 top, rest;
-            split_h(v, scale, top, rest);
-            *reinterpret_cast<uint2*>(hs + row * S::kHRow + col) = top;
-            *reinterpret_cast<uint2*>(hs + row * S::kHRow + R + col) = rest;
+      copy_commit();
+    };
+#pragma unroll
+    for (int j = 0; j < S::kAhead; ++j) fetch(j);
+    if (t0 == t_first) pdl_wait();  // shrink has ended: its parts are there, and stores may begin
+    int i = (int)(b0 / chunks) - t0, ch = (int)(b0 % chunks);
+    bool fresh = true;  // a tile begins
+    uint4 bv[S::kSteps][4];
+    for (int j = 0; j < n; ++j) {
+      const int e = b.bins[i], ra = b.ranks[i], nb = ch * S::kWidth + warp * 32, col = nb + 8 * t;
+      const uint16_t* eb = p.b + (int64_t)(e < p.n_adapters ? e : 0) * p.n * p.max_rank;
+      if (fresh && ra) {
+        const int tile = t0 + i;
+        load_b<R>(p, eb, ra, nb, 0, g, t, bv);
+        __syncthreads();  // every warp is done with the last tile's h
+        const int p0 = line_owner(k_units, k_ctas, (int64_t)tile * k_chunks),
+                  p1 = line_owner(k_units, k_ctas, (int64_t)(tile + 1) * k_chunks - 1);
+        const float scale = p.scales[e];
+        for (int x = tid; x < T * R / 4; x += kThreads) {
+          const int row = x / (R / 4), at = (x % (R / 4)) * 4;
+          const float* from = parts + ((int64_t)(p0 + tile) * T + row) * R + at;
+          float4 v = __ldcg(reinterpret_cast<const float4*>(from));
+          for (int q = p0 + 1; q <= p1; ++q) {
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(from + (int64_t)(q - p0) * T * R));
+            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
           }
-          named_sync(1, 32 * S::kWarps);
+          uint2 top, rest;
+          split_h(v, scale, top, rest);
+          *reinterpret_cast<uint2*>(hs + row * S::kHRow + at) = top;
+          *reinterpret_cast<uint2*>(hs + row * S::kHRow + R + at) = rest;
         }
-        for (int ch = c0; ch < c1; ++ch, ++it) {
-          const int s = it % S::kStages, nb = ch * S::kWidth + group * 32, col = nb + 8 * t;
-          ok = wait_warp(&full[s], it / S::kStages, p.status);
-          if (!ok) break;
-          if (ra && nb < p.n) {
-            float acc[S::kMt][4][4] = {};
+        __syncthreads();
+      }
+      const bool last = ch + 1 == chunks;  // of the tile
+      float acc[S::kMt][4][4] = {};
+      if (ra && nb < p.n) {
 #pragma unroll
-            for (int r0 = 0; r0 < R; r0 += S::kHalf) {
-              uint4 cur[S::kSteps][4];
+        for (int r0 = 0; r0 < R; r0 += S::kHalf) {
+          uint4 cur[S::kSteps][4];
 #pragma unroll
-              for (int q = 0; q < S::kSteps; ++q)
+          for (int q = 0; q < S::kSteps; ++q)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) cur[q][j] = bv[q][j];
-              if (r0 + S::kHalf < R)  // the next fragments come during this step's products
-                load_b<R>(p, eb, ra, nb, r0 + S::kHalf, g, t, bv);
-              else if (ch + 1 < c1)
-                load_b<R>(p, eb, ra, nb + S::kWidth, 0, g, t, bv);
+            for (int x = 0; x < 4; ++x) cur[q][x] = bv[q][x];
+          if (r0 + S::kHalf < R)  // the next fragments come during this step's products
+            load_b<R>(p, eb, ra, nb, r0 + S::kHalf, g, t, bv);
+          else if (!last && j + 1 < n)
+            load_b<R>(p, eb, ra, nb + S::kWidth, 0, g, t, bv);
 #pragma unroll
-              for (int i2 = 0; i2 < S::kMt; ++i2) {
-                const uint16_t* h0 = hs + (half * (T / S::kSplit) + i2 * 16 + g) * S::kHRow + r0;
-                const uint16_t* h1 = h0 + 8 * S::kHRow;
+          for (int m = 0; m < S::kMt; ++m) {
+            const uint16_t* h0 = hs + (m * 16 + g) * S::kHRow + r0;
+            const uint16_t* h1 = h0 + 8 * S::kHRow;
 #pragma unroll
-                for (int q = 0; q < S::kSteps; ++q)
+            for (int q = 0; q < S::kSteps; ++q)
 #pragma unroll
-                  for (int term = 0; term < 2; ++term) {
-                    if (R == 16) {
-                      const uint2 u = *reinterpret_cast<const uint2*>(h0 + term * R + 4 * t);
-                      const uint2 v = *reinterpret_cast<const uint2*>(h1 + term * R + 4 * t);
+              for (int term = 0; term < 2; ++term) {
+                if (R == 16) {
+                  const uint2 u = *reinterpret_cast<const uint2*>(h0 + term * R + 4 * t);
+                  const uint2 v = *reinterpret_cast<const uint2*>(h1 + term * R + 4 * t);
 #pragma unroll
-                      for (int j = 0; j < 4; ++j) mma16816(acc[i2][j], u.x, v.x, u.y, v.y, cur[q][j].x, cur[q][j].y);
-                    } else {
-                      const uint4 u = *reinterpret_cast<const uint4*>(h0 + term * R + q * 32 + 8 * t);
-                      const uint4 v = *reinterpret_cast<const uint4*>(h1 + term * R + q * 32 + 8 * t);
+                  for (int x = 0; x < 4; ++x) mma16816(acc[m][x], u.x, v.x, u.y, v.y, cur[q][x].x, cur[q][x].y);
+                } else {
+                  const uint4 u = *reinterpret_cast<const uint4*>(h0 + term * R + q * 32 + 8 * t);
+                  const uint4 v = *reinterpret_cast<const uint4*>(h1 + term * R + q * 32 + 8 * t);
 #pragma unroll
-                      for (int j = 0; j < 4; ++j) {
-                        mma16816(acc[i2][j], u.x, v.x, u.y, v.y, cur[q][j].x, cur[q][j].y);
-                        mma16816(acc[i2][j], u.z, v.z, u.w, v.w, cur[q][j].z, cur[q][j].w);
-                      }
-                    }
+                  for (int x = 0; x < 4; ++x) {
+                    mma16816(acc[m][x], u.x, v.x, u.y, v.y, cur[q][x].x, cur[q][x].y);
+                    mma16816(acc[m][x], u.z, v.z, u.w, v.w, cur[q][x].z, cur[q][x].w);
                   }
-              }
-            }
-#pragma unroll
-            for (int i2 = 0; i2 < S::kMt; ++i2)
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const int r = half * (T / S::kSplit) + i2 * 16 + h * 8 + g;
-                uint4* at = reinterpret_cast<uint4*>(smem + s * S::kStage + r * S::kPitch + 2 * (group * 32 + 8 * t));
-                const uint4 v = *at;
-                uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  w[j] = pack_bf16(bf_lo(w[j]) + acc[i2][j][2 * h], bf_hi(w[j]) + acc[i2][j][2 * h + 1]);
-                *at = make_uint4(w[0], w[1], w[2], w[3]);
+                }
               }
           }
-          if (col < p.n && col + 8 > p.n && (ra || p.out != p.y))  // the row's last outputs, fewer than a vector
-            for (int r = g; r < T / S::kSplit; r += 8) {
-              const int row = rows[i][half * (T / S::kSplit) + r];
-              const uint16_t* from = reinterpret_cast<const uint16_t*>(smem + s * S::kStage + (half * (T / S::kSplit) + r) * S::kPitch) + group * 32 + 8 * t;
-              if (row >= 0)
-                for (int x = 0; col + x < p.n; ++x) p.out[row * p.ldo + col + x] = from[x];
-            }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&done[s]);
         }
       }
+      copy_wait<S::kAhead - 1>();
+      const uint8_t* from = mine + (j % S::kAhead) * 2 * S::kMt * 512;
+      if (col < p.n) {
+#pragma unroll
+        for (int m = 0; m < S::kMt; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int r = b.rows[i][m * 16 + h * 8 + g];
+            if (r < 0 || (ra == 0 && p.out == p.y)) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * m + h) * 512);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (ra)
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                w[x] = pack_bf16(bf_lo(w[x]) + acc[m][x][2 * h], bf_hi(w[x]) + acc[m][x][2 * h + 1]);
+            uint16_t* to = p.out + r * p.ldo + col;
+            if (col + 8 <= p.n) {
+              *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if (col + x < p.n) to[x] = (uint16_t)(w[x >> 1] >> (16 * (x & 1)));
+            }
+          }
+      }
+      fetch(j + S::kAhead);
+      fresh = last;
+      ++ch;
+      if (last) ch = 0, ++i;
     }
-    __syncthreads();
-  }
-  if (warp == S::kWarps) {
-    for (int i = max(0, it - S::kStages); i < it; ++i) wait_warp(&full[i % S::kStages], i / S::kStages, p.status);
-    bulk_wait_all();
+    copy_wait<0>();
+    __syncthreads();  // the lists are written again
   }
 }
+
+// CTAs an SM: as many as fit.
+template <int R>
+struct PerSm {
+  static constexpr int kShrink = 1, kExpand = R <= 16 ? 2 : 1;
+};
 
 template <int R>
 int launch(const LoraArgs& p, const DeviceInfo& dev, float* parts, cudaStream_t s) {
@@ -438,9 +394,10 @@ int launch(const LoraArgs& p, const DeviceInfo& dev, float* parts, cudaStream_t 
   if (!allow_smem((const void*)lora_shrink_kernel<R>, Shrink<R>::kSmem, a) ||
       !allow_smem((const void*)lora_expand_kernel<R>, Expand<R>::kSmem, b))
     return QG_ERR_CUDA;
-  if (launch_pdl(lora_shrink_kernel<R>, dim3(dev.sms), dim3(Shrink<R>::kThreads), Shrink<R>::kSmem, s, p, parts) != cudaSuccess ||
-      launch_pdl(lora_expand_kernel<R>, dim3(dev.sms), dim3(Expand<R>::kThreads), Expand<R>::kSmem, s, p,
-                 static_cast<const float*>(parts), dev.sms, Shrink<R>::kWidth) != cudaSuccess)
+  const int shrink = dev.sms * PerSm<R>::kShrink, expand = dev.sms * PerSm<R>::kExpand;
+  if (launch_pdl(lora_shrink_kernel<R>, dim3(shrink), dim3(kThreads), Shrink<R>::kSmem, s, p, parts) != cudaSuccess ||
+      launch_pdl(lora_expand_kernel<R>, dim3(expand), dim3(kThreads), Expand<R>::kSmem, s, p,
+                 static_cast<const float*>(parts), shrink, Shrink<R>::kWidth) != cudaSuccess)
     return QG_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
@@ -452,7 +409,7 @@ int padded_rank(int max_rank) { return max_rank <= 16 ? 16 : max_rank <= 32 ? 32
 size_t lora_rows_bytes(int n_adapters, int max_rank, int64_t m, const DeviceInfo& dev) {
   const int64_t rows = std::min<int64_t>(m, kLoraRowsAtOnce);
   const int64_t tiles = (rows + T - 1) / T + std::min<int64_t>(rows, n_adapters);
-  return (size_t)(tiles + dev.sms) * T * padded_rank(max_rank) * sizeof(float);
+  return (size_t)(tiles + 2 * dev.sms) * T * padded_rank(max_rank) * sizeof(float);
 }
 
 int launch_lora_rows(const LoraArgs& all, const DeviceInfo& dev, void* parts, void* stream) {

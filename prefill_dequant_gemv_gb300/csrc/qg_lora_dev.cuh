@@ -97,31 +97,43 @@ struct Tiles {
   int warp_sums[THREADS / 32];
   int bin;
 
-  // The rows that this thread looks at.
+  // The rows that this warp looks at, 32 at a time: a run of whole 32s.
   static __device__ __forceinline__ void share(const LoraArgs& p, int* i0, int* i1) {
-    const int per = (p.m + THREADS - 1) / THREADS;
-    *i0 = min(p.m, (int)threadIdx.x * per);
+    const int per = ((p.m + 31) / 32 + THREADS / 32 - 1) / (THREADS / 32) * 32;
+    *i0 = min(p.m, (int)(threadIdx.x >> 5) * per);
     *i1 = min(p.m, *i0 + per);
+  }
+  // Bins of kLoads x 32 rows from i, -1 past the warp's rows; all loads before the first use.
+  static constexpr int kLoads = 8;
+  static __device__ __forceinline__ void load(const LoraArgs& p, int i, int i1, int (&e)[kLoads], bool* bad) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) e[u] = i + 32 * u + lane < i1 ? p.ids[i + 32 * u + lane] : -2;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const bool in = i + 32 * u + lane < i1;
+      *bad |= in && (e[u] < -1 || e[u] >= p.n_adapters);
+      e[u] = in ? bin_of(e[u], p.n_adapters) : -1;
+    }
   }
 
   __device__ __forceinline__ void count(const LoraArgs& p, int T) {
-    const int tid = threadIdx.x, bins = p.n_adapters + 1;
+    const int tid = threadIdx.x, lane = tid & 31, bins = p.n_adapters + 1;
     for (int e = tid; e <= bins; e += THREADS) first[e] = 0;
     __syncthreads();
-    int i0, i1, run = 0, cur = -1;  // a run of rows of one adapter is counted before it is added
+    int i0, i1;
     share(p, &i0, &i1);
     bool bad = false;
-    for (int i = i0; i < i1; ++i) {
-      const int id = p.ids[i], e = bin_of(id, p.n_adapters);
-      bad |= id < -1 || id >= p.n_adapters;
-      if (e != cur) {
-        if (run) atomicAdd(&first[cur], run);  // integer counts: order-free
-        cur = e;
-        run = 0;
+    for (int i = i0; i < i1; i += 32 * kLoads) {
+      int e[kLoads];
+      load(p, i, i1, e, &bad);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        if (i + 32 * u >= i1) break;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, e[u]);
+        if (e[u] >= 0 && lane == __ffs(same) - 1) atomicAdd(&first[e[u]], __popc(same));  // integer counts: order-free
       }
-      ++run;
     }
-    if (run) atomicAdd(&first[cur], run);
     if (bad) atomicCAS(p.status, 0, kStatusInvalid);
     __syncthreads();
     constexpr int kPer = (kLoraMaxAdapters + 1 + THREADS - 1) / THREADS;
@@ -146,22 +158,37 @@ struct Tiles {
 
   // Tile's adapter (the return value) and rows, in ascending order, -1 past the last.
   __device__ __forceinline__ int collect(const LoraArgs& p, int T, int tile, int* rows) {
-    const int tid = threadIdx.x, bins = p.n_adapters + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = p.n_adapters + 1;
     for (int e = tid; e < bins; e += THREADS)
       if (first[e] <= tile && tile < first[e + 1]) bin = e;
     for (int i = tid; i < T; i += THREADS) rows[i] = -1;
     __syncthreads();
     const int e = bin, skip = (tile - first[e]) * T;
-    int i0, i1, mine = 0, total;
+    int i0, i1, mine = 0;
     share(p, &i0, &i1);
-    for (int i = i0; i < i1; ++i) mine += bin_of(p.ids[i], p.n_adapters) == e;
-    int at = block_prefix<THREADS>(mine, warp_sums, &total) - skip;
-    if (mine && at < T && at + mine > 0)
-      for (int i = i0; i < i1; ++i)
-        if (bin_of(p.ids[i], p.n_adapters) == e) {
-          if (at >= 0 && at < T) rows[at] = i;
-          ++at;
+    bool bad = false;
+    for (int i = i0; i < i1; i += 32 * kLoads) {
+      int v[kLoads];
+      load(p, i, i1, v, &bad);
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) mine += __popc(__ballot_sync(0xFFFFFFFFu, v[u] == e));
+    }
+    if (lane == 0) warp_sums[warp] = mine;
+    __syncthreads();
+    int at = -skip;
+    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    if (at < T && at + mine > 0)
+      for (int i = i0; i < i1 && at < T; i += 32 * kLoads) {
+        int v[kLoads];
+        load(p, i, i1, v, &bad);
+#pragma unroll
+        for (int u = 0; u < kLoads; ++u) {
+          const unsigned hit = __ballot_sync(0xFFFFFFFFu, v[u] == e);
+          const int to = at + __popc(hit & ((1u << lane) - 1u));
+          if (v[u] == e && to >= 0 && to < T) rows[to] = i + 32 * u + lane;
+          at += __popc(hit);
         }
+      }
     __syncthreads();
     return e;
   }
