@@ -298,8 +298,8 @@ size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
  * y itself with the same stride: rows without an adapter, or whose adapter has rank 0, are then not touched; no other overlap.
  * ids and ranks are checked on the device: an id outside -1 .. n_adapters-1 or a rank outside
  * 0 .. max_rank counts as no adapter and puts QG_ERR_INVALID_ARG into the workspace's status word
- * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^30.  The
- * workspace need not be zero-filled but for its status word; calls that overlap on the GPU must not share it.
+ * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^30, the leading
+ * dimensions below 2^31.  The workspace need not be zero-filled but for its status word; calls that overlap on the GPU must not share it.
  * Deterministic; one launch for up to 256 rows, two more for every 16384 of more rows. */
 qg_status qlora(const qg_lora* lora, const int32_t* ids, int64_t m_rows, const void* x, int64_t ldx, const void* y,
                 int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);

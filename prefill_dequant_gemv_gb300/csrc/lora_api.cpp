@@ -30,6 +30,7 @@ extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, cons
   if (m == 0) return QG_OK;
   if (!l->a || !l->b || !l->scales || !ids || !x || !y || !out || !workspace) return QG_ERR_INVALID_ARG;
   if (l->lda < l->k || ldx < l->k || ldy < l->n || ldo < l->n) return QG_ERR_INVALID_ARG;
+  if (l->lda > 0x7FFFFFFF || ldx > 0x7FFFFFFF || ldy > 0x7FFFFFFF || ldo > 0x7FFFFFFF) return QG_ERR_UNSUPPORTED;
   if (misaligned(l->a, l->lda) || misaligned(l->b, 0) || misaligned(x, ldx) || misaligned(y, ldy) || misaligned(out, ldo) ||
       misaligned(workspace, 0) || reinterpret_cast<uintptr_t>(ids) % 4 || reinterpret_cast<uintptr_t>(l->scales) % 4 ||
       reinterpret_cast<uintptr_t>(l->ranks) % 4)
@@ -43,7 +44,7 @@ extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, cons
   p.b = static_cast<const uint16_t*>(l->b);
   p.scales = l->scales;
   p.ranks = l->ranks;
-  p.lda = l->lda;
+  p.lda = (int)l->lda;
   p.n_adapters = l->n_adapters;
   p.max_rank = l->max_rank;
   p.n = (int)l->n;
@@ -53,9 +54,9 @@ extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, cons
   p.x = static_cast<const uint16_t*>(x);
   p.y = static_cast<const uint16_t*>(y);
   p.out = static_cast<uint16_t*>(out);
-  p.ldx = ldx;
-  p.ldy = ldy;
-  p.ldo = ldo;
+  p.ldx = (int)ldx;
+  p.ldy = (int)ldy;
+  p.ldo = (int)ldo;
   p.status = static_cast<int*>(workspace);
   if (m <= kLoraFewRows) return (qg_status)launch_lora(p, dev, stream);
   if (workspace_bytes < kWsHeader + lora_rows_bytes(l->n_adapters, l->max_rank, m, dev)) return QG_ERR_WORKSPACE_TOO_SMALL;

@@ -25,7 +25,6 @@ namespace {
 
 constexpr int T = 64;           // rows of a tile
 constexpr int kBatch = 16;      // tiles whose rows a CTA lists at a time
-constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 // 16 bytes global -> shared, those past the first `bytes` (0: none is read) as zeros.
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
@@ -46,14 +45,20 @@ __device__ __forceinline__ int bytes_of(int left) { return 2 * max(0, min(8, lef
 __device__ __forceinline__ int64_t line_begin(int64_t units, int ctas, int c) { return units * c / ctas; }
 __device__ __forceinline__ int line_owner(int64_t units, int ctas, int64_t u) { return (int)(((u + 1) * ctas - 1) / units); }
 
-// The tiles of a batch: rows, adapter and rank.
+// The tiles of a batch: rows (past the last the first again: what is computed of them is not stored), how many,
+// adapter and rank.
+template <int THREADS>
 struct Batch {
   int rows[kBatch][T];
-  int bins[kBatch], ranks[kBatch];
-  __device__ __forceinline__ void fill(const LoraArgs& p, Tiles<kThreads>& tl, int t0, int nt) {
+  int live[kBatch], bins[kBatch], ranks[kBatch];
+  __device__ __forceinline__ void fill(const LoraArgs& p, Tiles<THREADS>& tl, int t0, int nt) {
     for (int i = 0; i < nt; ++i) {
       const int e = tl.collect(p, T, t0 + i, rows[i]);
+      const int r = threadIdx.x < T ? rows[i][threadIdx.x] : 0;
+      const int n = __syncthreads_count(threadIdx.x < T && r >= 0);
+      if (r < 0) rows[i][threadIdx.x] = rows[i][0];
       if (threadIdx.x == 0) {
+        live[i] = n;
         bins[i] = e;
         ranks[i] = rank_of(p, e);
       }
@@ -65,7 +70,8 @@ struct Batch {
 // ------------------------------------------------------------------ shrink
 template <int R>
 struct Shrink {
-  static constexpr int kSplit = R <= 32 ? 1 : 2;          // groups of warps that share a tile's rows
+  static constexpr int kThreads = R <= 32 ? 512 : 256, kWarps = kThreads / 32;
+  static constexpr int kSplit = 2;                        // groups of warps that share a tile's rows
   static constexpr int kParts = kWarps / kSplit;          // warps that share a chunk's inputs, 32 each
   static constexpr int kMt = T / 16 / kSplit;             // row tiles of 16 a warp
   static constexpr int kWidth = 32 * kParts;              // inputs of a chunk
@@ -77,12 +83,12 @@ struct Shrink {
 };
 
 template <int R>
-__global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs p, float* parts) {
+__global__ void __launch_bounds__(Shrink<R>::kThreads) lora_shrink_kernel(LoraArgs p, float* parts) {
   using S = Shrink<R>;
   extern __shared__ __align__(128) uint8_t smem[];
   float* sum = reinterpret_cast<float*>(smem + S::kRing);
-  __shared__ Tiles<kThreads> tl;
-  __shared__ Batch b;
+  __shared__ Tiles<S::kThreads> tl;
+  __shared__ Batch<S::kThreads> b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   pdl_wait();
   if (tid == 0) pdl_launch_dependents();  // after the wait: what this call reads is there for expand as well
@@ -93,48 +99,66 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs p, float
   if (c >= ctas) return;
   const int64_t u0 = line_begin(units, ctas, c), u1 = line_begin(units, ctas, c + 1);
   const int t_first = (int)(u0 / chunks), t_last = (int)((u1 - 1) / chunks);
-  const int half = warp % S::kSplit, part = warp / S::kSplit;
+  const int half = warp % S::kSplit, part = warp / S::kSplit, row0 = half * (T / S::kSplit) + g;
   uint8_t* mine = smem + (size_t)warp * S::kAhead * S::kPieces * 512 + lane * 16;
   const uint32_t mine_at = smem_u32(mine);
+  constexpr uint32_t kSlot = S::kPieces * 512, kSlots = S::kAhead * kSlot;
 
   for (int t0 = t_first; t0 <= t_last; t0 += kBatch) {
     const int nt = min(kBatch, t_last + 1 - t0);
     b.fill(p, tl, t0, nt);
     const int64_t b0 = max(u0, (int64_t)t0 * chunks);
     const int n = (int)(min(u1, (int64_t)(t0 + nt) * chunks) - b0);
-    int fi = (int)(b0 / chunks) - t0, fc = (int)(b0 % chunks);  // tile and chunk of the next copies
+    // the copies' state: tile, input and pointers of the next chunk
+    int fi = (int)(b0 / chunks) - t0, col = (int)(b0 % chunks) * S::kWidth + part * 32 + 8 * t, ra_f = 0;
+    uint32_t slot_f = 0;
+    const uint16_t *xp[2 * S::kMt], *ap;
+    auto aim = [&]() {
+      ra_f = b.ranks[fi];
+#pragma unroll
+      for (int i = 0; i < 2 * S::kMt; ++i) xp[i] = p.x + (int64_t)b.rows[fi][row0 + 8 * i] * p.ldx + col;
+      ap = p.a + ((int64_t)(ra_f ? b.bins[fi] : 0) * p.max_rank + (g < p.max_rank ? g : 0)) * p.lda + col;
+    };
+    aim();
     auto fetch = [&](int j) {
       if (j < n) {
-        const int e = b.bins[fi], ra = b.ranks[fi], col = fc * S::kWidth + part * 32 + 8 * t;
-        const uint32_t to = mine_at + (j % S::kAhead) * S::kPieces * 512;
-        const int left = ra ? bytes_of(p.k - col) : 0;
+        const int left = bytes_of(p.k - col);
+        const uint32_t to = mine_at + slot_f;
+        slot_f = slot_f + kSlot == kSlots ? 0 : slot_f + kSlot;
+        if (left && ra_f) {
 #pragma unroll
-        for (int i = 0; i < 2 * S::kMt; ++i) {
-          const int r = b.rows[fi][half * (T / S::kSplit) + i * 8 + g];
-          copy16(to + i * 512, r >= 0 && left ? p.x + r * p.ldx + col : p.x, r >= 0 ? left : 0);
-        }
-        const uint16_t* ea = p.a + ((int64_t)e * p.max_rank + g) * p.lda + col;
+          for (int i = 0; i < 2 * S::kMt; ++i) copy16(to + i * 512, xp[i], left);
 #pragma unroll
-        for (int i = 0; i < R / 8; ++i) {
-          const bool in = i * 8 + g < ra && left;
-          const uint16_t* from = in ? ea + (int64_t)i * 8 * p.lda : p.a;
-          if (S::kSplit > 1)
-            copy16_l1(to + (2 * S::kMt + i) * 512, from, in ? left : 0);
-          else
-            copy16(to + (2 * S::kMt + i) * 512, from, in ? left : 0);
+          for (int i = 0; i < R / 8; ++i)
+            if (i * 8 < ra_f) {
+              const bool in = i * 8 + g < ra_f;
+              copy16_l1(to + (2 * S::kMt + i) * 512, in ? ap + (int64_t)(i * 8) * p.lda : p.a, in ? left : 0);
+            }
+        } else {  // past the row's end: zeros
+#pragma unroll
+          for (int i = 0; i < S::kPieces; ++i) copy16(to + i * 512, p.x, 0);
         }
-        if (++fc == chunks) fc = 0, ++fi;
+        col += S::kWidth;
+        if (col - 8 * t >= chunks * S::kWidth) {
+          col = part * 32 + 8 * t;
+          if (++fi < nt) aim();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 2 * S::kMt; ++i) xp[i] += S::kWidth;
+          ap += S::kWidth;
+        }
       }
       copy_commit();
     };
 #pragma unroll
     for (int j = 0; j < S::kAhead; ++j) fetch(j);
-    int i = (int)(b0 / chunks) - t0, ch = (int)(b0 % chunks);
+    int i = (int)(b0 / chunks) - t0, ch = (int)(b0 % chunks), ra = b.ranks[i];
+    uint32_t slot = 0;
     float acc[S::kMt][R / 8][4] = {};
     for (int j = 0; j < n; ++j) {
       copy_wait<S::kAhead - 1>();
-      const uint8_t* from = mine + (j % S::kAhead) * S::kPieces * 512;
-      const int ra = b.ranks[i];
+      const uint8_t* from = mine + slot;
+      slot = slot + kSlot == kSlots ? 0 : slot + kSlot;
       uint4 xv[S::kMt][2];
 #pragma unroll
       for (int m = 0; m < S::kMt; ++m)
@@ -154,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs p, float
       if (++ch < chunks && j + 1 < n) continue;
       // the tile's end, or the CTA's: the warps' sums over their inputs, one after the other
       if (ra) {
-        float* at = sum + (half * (T / S::kSplit) + g) * S::kSumRow + 2 * t;
+        float* at = sum + row0 * S::kSumRow + 2 * t;
 #pragma unroll 1
         for (int w = 0; w < S::kParts; ++w) {
           if (part == w) {
@@ -173,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs p, float
           __syncthreads();
         }
         float* to = parts + (int64_t)(c + t0 + i) * T * R;
-        for (int x = tid; x < T * R / 4; x += kThreads)
+        for (int x = tid; x < T * R / 4; x += S::kThreads)
           reinterpret_cast<float4*>(to)[x] = *reinterpret_cast<const float4*>(sum + x / (R / 4) * S::kSumRow + x % (R / 4) * 4);
         __syncthreads();
       }
@@ -184,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs p, float
 #pragma unroll
           for (int x = 0; x < 4; ++x) acc[m][q][x] = 0.0f;
       ch = 0;
-      ++i;
+      if (++i < nt) ra = b.ranks[i];
     }
     copy_wait<0>();
     __syncthreads();  // the lists are written again
@@ -194,8 +218,10 @@ __global__ void __launch_bounds__(kThreads) lora_shrink_kernel(LoraArgs p, float
 // ------------------------------------------------------------------ expand
 template <int R>
 struct Expand {
-  static constexpr int kWidth = 32 * kWarps;      // outputs of a chunk
-  static constexpr int kMt = T / 16;
+  static constexpr int kThreads = 512, kWarps = kThreads / 32;
+  static constexpr int kSplit = 2;                // groups of warps that share a tile's rows
+  static constexpr int kWidth = 32 * kWarps / kSplit;  // outputs of a chunk
+  static constexpr int kMt = T / 16 / kSplit;
   static constexpr int kAhead = 3;
   static constexpr int kHRow = R == 16 ? 48 : 2 * R + 32;  // bf16: a fragment's pieces in distinct banks
   static constexpr size_t kRing = (size_t)kWarps * kAhead * 2 * kMt * 512;
@@ -204,41 +230,43 @@ struct Expand {
   static constexpr int kSteps = kHalf == 16 ? 1 : kHalf / 32;
 };
 
-// B's fragments: 32 outputs from nb, kHalf ranks from r0, of an adapter of rank ra.
+// B's fragments of 32 outputs, kHalf ranks from r0, of an adapter of rank ra: bp is the lane's place in the row of its first
+// output, whose others lie two outputs apart; `outs` of them exist.
 template <int R>
-__device__ __forceinline__ void load_b(const LoraArgs& p, const uint16_t* eb, int ra, int nb, int r0, int g, int t,
+__device__ __forceinline__ void load_b(const uint16_t* bp, int max_rank, int ra, int outs, int r0, int t,
                                        uint4 (&bv)[Expand<R>::kSteps][4]) {
+  constexpr int kLane = R == 16 ? 4 : 8;  // ranks a lane
 #pragma unroll
-  for (int q = 0; q < Expand<R>::kSteps; ++q)
+  for (int q = 0; q < Expand<R>::kSteps; ++q) {
+    const int c = r0 + q * 32 + kLane * t;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int nr = nb + 8 * (g >> 1) + 2 * j + (g & 1);
-      const uint16_t* from = eb + (int64_t)nr * p.max_rank;
       bv[q][j] = make_uint4(0, 0, 0, 0);
-      if (R == 16) {  // four ranks a lane
-        const int c = 4 * t;
-        if (nr < p.n && c < ra) {
-          const uint2 v = __ldg(reinterpret_cast<const uint2*>(from + c));
+      if (c < ra && 2 * j < outs) {
+        const uint16_t* from = bp + 2 * j * max_rank + r0 + q * 32;
+        if (R == 16) {
+          const uint2 v = __ldg(reinterpret_cast<const uint2*>(from));
           bv[q][j] = make_uint4(v.x, v.y, 0, 0);
-          if (c + 4 > ra) bv[q][j] = keep_first(bv[q][j], ra - c);
-        }
-      } else {
-        const int c = r0 + q * 32 + 8 * t;
-        if (nr < p.n && c < ra) {
-          bv[q][j] = __ldg(reinterpret_cast<const uint4*>(from + c));
-          if (c + 8 > ra) bv[q][j] = keep_first(bv[q][j], ra - c);
+        } else {
+          bv[q][j] = __ldg(reinterpret_cast<const uint4*>(from));
         }
       }
     }
+    if (ra & (kLane - 1)) {  // the rank ends inside a piece
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bv[q][j] = keep_first(bv[q][j], ra - c);
+    }
+  }
 }
 
 template <int R>
-__global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs p, const float* parts, int shrink_ctas, int shrink_width) {
+__global__ void __launch_bounds__(Expand<R>::kThreads) lora_expand_kernel(LoraArgs p, const float* parts, int shrink_ctas,
+                                                                          int shrink_width) {
   using S = Expand<R>;
   extern __shared__ __align__(128) uint8_t smem[];
   uint16_t* hs = reinterpret_cast<uint16_t*>(smem + S::kRing);
-  __shared__ Tiles<kThreads> tl;
-  __shared__ Batch b;
+  __shared__ Tiles<S::kThreads> tl;
+  __shared__ Batch<S::kThreads> b;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   if (tid == 0) pdl_launch_dependents();
   tl.count(p, T);
@@ -254,76 +282,95 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs p, const
   const int k_chunks = (p.k + shrink_width - 1) / shrink_width;
   const int64_t k_units = (int64_t)tl.first[p.n_adapters] * k_chunks;
   const int k_ctas = (int)min((int64_t)shrink_ctas, k_units);
+  const int half = warp % S::kSplit, group = warp / S::kSplit, row0 = half * (T / S::kSplit) + g;
   uint8_t* mine = smem + (size_t)warp * S::kAhead * 2 * S::kMt * 512 + lane * 16;
   const uint32_t mine_at = smem_u32(mine);
+  constexpr uint32_t kSlot = 2 * S::kMt * 512, kSlots = S::kAhead * kSlot;
+  const bool in_place = p.out == p.y;
 
   for (int t0 = t_first; t0 <= t_last; t0 += kBatch) {
     const int nt = min(kBatch, t_last + 1 - t0);
     b.fill(p, tl, t0, nt);
     const int64_t b0 = max(u0, (int64_t)t0 * chunks);
     const int n = (int)(min(u1, (int64_t)(t0 + nt) * chunks) - b0);
-    int fi = (int)(b0 / chunks) - t0, fc = (int)(b0 % chunks);
+    int i = (int)(b0 / chunks) - t0, ch = (int)(b0 % chunks);
+    // the copies' state: tile, output and pointers of the next chunk
+    int fi = i, fc = ch * S::kWidth + group * 32 + 8 * t;
+    uint32_t slot_f = 0, slot = 0;
+    const uint16_t* yp[2 * S::kMt];
+    auto aim = [&]() {
+#pragma unroll
+      for (int m = 0; m < 2 * S::kMt; ++m) yp[m] = p.y + (int64_t)b.rows[fi][row0 + 8 * m] * p.ldy + fc;
+    };
+    aim();
     auto fetch = [&](int j) {
       if (j < n) {
-        const int col = fc * S::kWidth + warp * 32 + 8 * t, left = bytes_of(p.n - col);
-        const uint32_t to = mine_at + (j % S::kAhead) * 2 * S::kMt * 512;
+        const int left = bytes_of(p.n - fc);
+        const uint32_t to = mine_at + slot_f;
+        slot_f = slot_f + kSlot == kSlots ? 0 : slot_f + kSlot;
+        if (left) {
 #pragma unroll
-        for (int i = 0; i < 2 * S::kMt; ++i) {
-          const int r = b.rows[fi][i * 8 + g];
-          copy16(to + i * 512, r >= 0 && left ? p.y + r * p.ldy + col : p.y, r >= 0 ? left : 0);
+          for (int m = 0; m < 2 * S::kMt; ++m) copy16(to + m * 512, yp[m], left);
         }
-        if (++fc == chunks) fc = 0, ++fi;
+        fc += S::kWidth;
+        if (fc - 8 * t >= chunks * S::kWidth) {
+          fc = group * 32 + 8 * t;
+          if (++fi < nt) aim();
+        } else {
+#pragma unroll
+          for (int m = 0; m < 2 * S::kMt; ++m) yp[m] += S::kWidth;
+        }
       }
       copy_commit();
     };
 #pragma unroll
     for (int j = 0; j < S::kAhead; ++j) fetch(j);
     if (t0 == t_first) pdl_wait();  // shrink has ended: its parts are there, and stores may begin
-    int i = (int)(b0 / chunks) - t0, ch = (int)(b0 % chunks);
     bool fresh = true;  // a tile begins
-    uint4 bv[S::kSteps][4];
+    int ra = 0, live = 0, nb = 0;
+    uint16_t* op[2 * S::kMt];
+    const uint16_t* bp = p.b;
+    const int bg = 8 * (g >> 1) + (g & 1);  // the lane's outputs in B: bg, bg + 2, bg + 4, bg + 6
     for (int j = 0; j < n; ++j) {
-      const int e = b.bins[i], ra = b.ranks[i], nb = ch * S::kWidth + warp * 32, col = nb + 8 * t;
-      const uint16_t* eb = p.b + (int64_t)(e < p.n_adapters ? e : 0) * p.n * p.max_rank;
-      if (fresh && ra) {
-        const int tile = t0 + i;
-        load_b<R>(p, eb, ra, nb, 0, g, t, bv);
-        __syncthreads();  // every warp is done with the last tile's h
-        const int p0 = line_owner(k_units, k_ctas, (int64_t)tile * k_chunks),
-                  p1 = line_owner(k_units, k_ctas, (int64_t)(tile + 1) * k_chunks - 1);
-        const float scale = p.scales[e];
-        for (int x = tid; x < T * R / 4; x += kThreads) {
-          const int row = x / (R / 4), at = (x % (R / 4)) * 4;
-          const float* from = parts + ((int64_t)(p0 + tile) * T + row) * R + at;
-          float4 v = __ldcg(reinterpret_cast<const float4*>(from));
-          for (int q = p0 + 1; q <= p1; ++q) {
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(from + (int64_t)(q - p0) * T * R));
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      if (fresh) {
+        const int e = b.bins[i], tile = t0 + i;
+        ra = b.ranks[i];
+        live = b.live[i] - row0;  // row m of this lane exists if 8 m < live
+        nb = ch * S::kWidth + group * 32;
+#pragma unroll
+        for (int m = 0; m < 2 * S::kMt; ++m) op[m] = p.out + (int64_t)b.rows[i][row0 + 8 * m] * p.ldo + nb + 8 * t;
+        if (ra) {
+          bp = p.b + ((int64_t)e * p.n + nb + bg) * p.max_rank + (R == 16 ? 4 : 8) * t;
+          __syncthreads();  // every warp is done with the last tile's h
+          const int p0 = line_owner(k_units, k_ctas, (int64_t)tile * k_chunks),
+                    p1 = line_owner(k_units, k_ctas, (int64_t)(tile + 1) * k_chunks - 1);
+          const float scale = p.scales[e];
+          for (int x = tid; x < T * R / 4; x += S::kThreads) {
+            const int row = x / (R / 4), at = (x % (R / 4)) * 4;
+            const float* from = parts + ((int64_t)(p0 + tile) * T + row) * R + at;
+            float4 v = __ldcg(reinterpret_cast<const float4*>(from));
+            for (int q = p0 + 1; q <= p1; ++q) {
+              const float4 o = __ldcg(reinterpret_cast<const float4*>(from + (int64_t)(q - p0) * T * R));
+              v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            uint2 top, rest;
+            split_h(v, scale, top, rest);
+            *reinterpret_cast<uint2*>(hs + row * S::kHRow + at) = top;
+            *reinterpret_cast<uint2*>(hs + row * S::kHRow + R + at) = rest;
           }
-          uint2 top, rest;
-          split_h(v, scale, top, rest);
-          *reinterpret_cast<uint2*>(hs + row * S::kHRow + at) = top;
-          *reinterpret_cast<uint2*>(hs + row * S::kHRow + R + at) = rest;
+          __syncthreads();
         }
-        __syncthreads();
       }
       const bool last = ch + 1 == chunks;  // of the tile
       float acc[S::kMt][4][4] = {};
       if (ra && nb < p.n) {
 #pragma unroll
         for (int r0 = 0; r0 < R; r0 += S::kHalf) {
-          uint4 cur[S::kSteps][4];
-#pragma unroll
-          for (int q = 0; q < S::kSteps; ++q)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) cur[q][x] = bv[q][x];
-          if (r0 + S::kHalf < R)  // the next fragments come during this step's products
-            load_b<R>(p, eb, ra, nb, r0 + S::kHalf, g, t, bv);
-          else if (!last && j + 1 < n)
-            load_b<R>(p, eb, ra, nb + S::kWidth, 0, g, t, bv);
+          uint4 bv[S::kSteps][4];
+          load_b<R>(bp, p.max_rank, ra, p.n - nb - bg, r0, t, bv);
 #pragma unroll
           for (int m = 0; m < S::kMt; ++m) {
-            const uint16_t* h0 = hs + (m * 16 + g) * S::kHRow + r0;
+            const uint16_t* h0 = hs + (row0 + m * 16) * S::kHRow + r0;
             const uint16_t* h1 = h0 + 8 * S::kHRow;
 #pragma unroll
             for (int q = 0; q < S::kSteps; ++q)
@@ -333,14 +380,14 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs p, const
                   const uint2 u = *reinterpret_cast<const uint2*>(h0 + term * R + 4 * t);
                   const uint2 v = *reinterpret_cast<const uint2*>(h1 + term * R + 4 * t);
 #pragma unroll
-                  for (int x = 0; x < 4; ++x) mma16816(acc[m][x], u.x, v.x, u.y, v.y, cur[q][x].x, cur[q][x].y);
+                  for (int x = 0; x < 4; ++x) mma16816(acc[m][x], u.x, v.x, u.y, v.y, bv[q][x].x, bv[q][x].y);
                 } else {
                   const uint4 u = *reinterpret_cast<const uint4*>(h0 + term * R + q * 32 + 8 * t);
                   const uint4 v = *reinterpret_cast<const uint4*>(h1 + term * R + q * 32 + 8 * t);
 #pragma unroll
                   for (int x = 0; x < 4; ++x) {
-                    mma16816(acc[m][x], u.x, v.x, u.y, v.y, cur[q][x].x, cur[q][x].y);
-                    mma16816(acc[m][x], u.z, v.z, u.w, v.w, cur[q][x].z, cur[q][x].w);
+                    mma16816(acc[m][x], u.x, v.x, u.y, v.y, bv[q][x].x, bv[q][x].y);
+                    mma16816(acc[m][x], u.z, v.z, u.w, v.w, bv[q][x].z, bv[q][x].w);
                   }
                 }
               }
@@ -348,30 +395,33 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs p, const
         }
       }
       copy_wait<S::kAhead - 1>();
-      const uint8_t* from = mine + (j % S::kAhead) * 2 * S::kMt * 512;
-      if (col < p.n) {
+      const uint8_t* from = mine + slot;
+      slot = slot + kSlot == kSlots ? 0 : slot + kSlot;
+      const int left = p.n - nb - 8 * t;
 #pragma unroll
-        for (int m = 0; m < S::kMt; ++m)
+      for (int m = 0; m < S::kMt; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int r = b.rows[i][m * 16 + h * 8 + g];
-            if (r < 0 || (ra == 0 && p.out == p.y)) continue;
-            const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * m + h) * 512);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            if (ra)
+        for (int h = 0; h < 2; ++h) {
+          if (16 * m + 8 * h >= live || left <= 0 || (ra == 0 && in_place)) continue;
+          const uint4 v = *reinterpret_cast<const uint4*>(from + (2 * m + h) * 512);
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (ra)
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                w[x] = pack_bf16(bf_lo(w[x]) + acc[m][x][2 * h], bf_hi(w[x]) + acc[m][x][2 * h + 1]);
-            uint16_t* to = p.out + r * p.ldo + col;
-            if (col + 8 <= p.n) {
-              *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
+            for (int x = 0; x < 4; ++x)
+              w[x] = pack_bf16(bf_lo(w[x]) + acc[m][x][2 * h], bf_hi(w[x]) + acc[m][x][2 * h + 1]);
+          uint16_t* to = op[2 * m + h];
+          if (left >= 8) {
+            *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                if (col + x < p.n) to[x] = (uint16_t)(w[x >> 1] >> (16 * (x & 1)));
-            }
+            for (int x = 0; x < 8; ++x)
+              if (x < left) to[x] = (uint16_t)(w[x >> 1] >> (16 * (x & 1)));
           }
-      }
+        }
+#pragma unroll
+      for (int m = 0; m < 2 * S::kMt; ++m) op[m] += S::kWidth;
+      nb += S::kWidth;
+      bp += S::kWidth * p.max_rank;
       fetch(j + S::kAhead);
       fresh = last;
       ++ch;
@@ -385,7 +435,7 @@ __global__ void __launch_bounds__(kThreads) lora_expand_kernel(LoraArgs p, const
 // CTAs an SM: as many as fit.
 template <int R>
 struct PerSm {
-  static constexpr int kShrink = 1, kExpand = R <= 16 ? 2 : 1;
+  static constexpr int kShrink = 1, kExpand = 1;
 };
 
 template <int R>
@@ -395,8 +445,8 @@ int launch(const LoraArgs& p, const DeviceInfo& dev, float* parts, cudaStream_t 
       !allow_smem((const void*)lora_expand_kernel<R>, Expand<R>::kSmem, b))
     return QG_ERR_CUDA;
   const int shrink = dev.sms * PerSm<R>::kShrink, expand = dev.sms * PerSm<R>::kExpand;
-  if (launch_pdl(lora_shrink_kernel<R>, dim3(shrink), dim3(kThreads), Shrink<R>::kSmem, s, p, parts) != cudaSuccess ||
-      launch_pdl(lora_expand_kernel<R>, dim3(expand), dim3(kThreads), Expand<R>::kSmem, s, p,
+  if (launch_pdl(lora_shrink_kernel<R>, dim3(shrink), dim3(Shrink<R>::kThreads), Shrink<R>::kSmem, s, p, parts) != cudaSuccess ||
+      launch_pdl(lora_expand_kernel<R>, dim3(expand), dim3(Expand<R>::kThreads), Expand<R>::kSmem, s, p,
                  static_cast<const float*>(parts), shrink, Shrink<R>::kWidth) != cudaSuccess)
     return QG_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;

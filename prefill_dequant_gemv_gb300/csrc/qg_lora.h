@@ -15,14 +15,13 @@ struct LoraArgs {
   const uint16_t* b;  // [n_adapters][n][max_rank]
   const float* scales;
   const int32_t* ranks;  // or null: max_rank
-  int64_t lda;
-  int n_adapters, max_rank, n, k;
+  int lda, n_adapters, max_rank, n, k;
   const int32_t* ids;
   int m;
   const uint16_t* x;
   const uint16_t* y;
   uint16_t* out;  // y itself: rows without an adapter are not touched
-  int64_t ldx, ldy, ldo;
+  int ldx, ldy, ldo;
   int* status;
 };
 constexpr int64_t kLoraFewRows = 256;       // at most: one launch of clusters (lora.cu); more: shrink and expand (lora_rows.cu)
