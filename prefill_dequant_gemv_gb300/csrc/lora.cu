@@ -141,18 +141,21 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
       else
         __syncthreads();
       const float scale = p.scales[e];
-      for (int i = tid; i < T * R / 4; i += kThreads) {
-        const int row = i / (R / 4), col = (i % (R / 4)) * 4;
+      for (int i = tid; i < T * R / 8; i += kThreads) {
+        const int row = i / (R / 8), col = (i % (R / 8)) * 8;
         const float* at = part + row * S::kPartRow + col;
-        float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float v[8] = {};
         for (uint32_t c = 0; c < n_cta; ++c) {
-          const float4 o = n_cta > 1 ? ld_cluster_f4(cluster_map(at, c)) : *reinterpret_cast<const float4*>(at);
-          v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+          const uint32_t from = n_cta > 1 ? cluster_map(at, c) : 0;
+          const float4 a0 = n_cta > 1 ? ld_cluster_f4(from) : *reinterpret_cast<const float4*>(at);
+          const float4 a1 = n_cta > 1 ? ld_cluster_f4(from + 16) : *reinterpret_cast<const float4*>(at + 4);
+          v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
+          v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
         }
-        uint2 top, rest;
-        split_h(v, scale, top, rest);
-        *reinterpret_cast<uint2*>(hs + row * S::kHRow + col) = top;
-        *reinterpret_cast<uint2*>(hs + row * S::kHRow + R + col) = rest;
+        uint4 top, rest;
+        split_h(v, scale, ra - col, top, rest);
+        *reinterpret_cast<uint4*>(hs + row * S::kHRow + col) = top;
+        *reinterpret_cast<uint4*>(hs + row * S::kHRow + R + col) = rest;
       }
       __syncthreads();
     }

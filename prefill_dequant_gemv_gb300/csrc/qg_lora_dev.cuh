@@ -47,18 +47,20 @@ __device__ __forceinline__ uint4 keep_first(uint4 v, int valid) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Four h as two bf16 terms each: 16 bits of the value; an infinite one is its first term alone.
-__device__ __forceinline__ void split_h(float4 v, float scale, uint2& top, uint2& rest) {
-  const float f[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
-  uint32_t a[2], b[2];
+// Two h as two bf16 terms each: 16 bits of the value; an infinite one is its first term alone.
+__device__ __forceinline__ void split_h2(float x, float y, uint32_t& top, uint32_t& rest) {
+  top = pack_bf16(x, y);
+  const float l = x - bf_lo(top), h = y - bf_hi(top);
+  rest = pack_bf16(isinf(x) ? 0.0f : l, isinf(y) ? 0.0f : h);
+}
+// scale times eight h, those from `valid` on (ranks past the adapter's) as zeros.
+__device__ __forceinline__ void split_h(const float (&v)[8], float scale, int valid, uint4& top, uint4& rest) {
+  uint32_t a[4], b[4];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    a[j] = pack_bf16(f[2 * j], f[2 * j + 1]);
-    const float l = f[2 * j] - bf_lo(a[j]), h = f[2 * j + 1] - bf_hi(a[j]);
-    b[j] = pack_bf16(isinf(f[2 * j]) ? 0.0f : l, isinf(f[2 * j + 1]) ? 0.0f : h);
-  }
-  top = make_uint2(a[0], a[1]);
-  rest = make_uint2(b[0], b[1]);
+  for (int j = 0; j < 4; ++j)
+    split_h2(2 * j < valid ? v[2 * j] * scale : 0.0f, 2 * j + 1 < valid ? v[2 * j + 1] * scale : 0.0f, a[j], b[j]);
+  top = make_uint4(a[0], a[1], a[2], a[3]);
+  rest = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 // Exclusive prefix sum of one count a thread over a block of THREADS; the total in *total.
