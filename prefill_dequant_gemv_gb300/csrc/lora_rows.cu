@@ -33,12 +33,6 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, int pass, int* status) 
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, pass & 1, status));
 }
 
-// 16 bytes global -> shared, those past the first `bytes` (0: none is read) as zeros.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ int bytes_of(int left) { return 2 * max(0, min(8, left)); }
-
 // Fragments of 16 rows x 32 columns: lane 4 g + t has rows g and g + 8, columns 8 x + 2 t and the next of block x, in
 // v[4 x], v[4 x + 1] and v[4 x + 2], v[4 x + 3].
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[16]) {
@@ -392,7 +386,7 @@ __global__ void __launch_bounds__(Expand<ATOMS>::kThreads) lora_expand_kernel(Lo
             bp += kWidth * p.max_rank;
           }
         }
-        cp_async_commit();
+        copy_commit();
       };
 #pragma unroll
       for (int j = 0; j < S::kAhead; ++j) fetch(j);
@@ -448,7 +442,7 @@ __global__ void __launch_bounds__(Expand<ATOMS>::kThreads) lora_expand_kernel(Lo
           tc_fence_after();
           ++mm;
         }
-        cp_async_wait<S::kAhead - 1>();
+        copy_wait<S::kAhead - 1>();
         const uint8_t* from = mine + slot * S::kWarps * S::kY;
         slot = slot + 1 == S::kAhead ? 0 : slot + 1;
 #pragma unroll
@@ -490,7 +484,7 @@ __global__ void __launch_bounds__(Expand<ATOMS>::kThreads) lora_expand_kernel(Lo
         fresh = ++ch == chunks;
         if (fresh) ch = 0, ++i;
       }
-      cp_async_wait_all();
+      copy_wait<0>();
     }
     __syncthreads();  // the lists are written again
   }

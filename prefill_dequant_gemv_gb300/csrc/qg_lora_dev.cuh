@@ -39,13 +39,20 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // a in the l
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// The first `valid` of eight bf16 (all of them from 8, none below 1).
-__device__ __forceinline__ uint4 keep_first(uint4 v, int valid) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] &= 2 * i + 1 < valid ? 0xFFFFFFFFu : 2 * i < valid ? 0xFFFFu : 0u;
-  return make_uint4(w[0], w[1], w[2], w[3]);
+// 16 (or 8) bytes global -> shared, those past the first `bytes` (0: none is read) as zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// Bytes of a piece of eight elements of which `left` remain.
+__device__ __forceinline__ int bytes_of(int left) { return 2 * max(0, min(8, left)); }
 
 // Two h as two bf16 terms each: 16 bits of the value; an infinite one is its first term alone.
 __device__ __forceinline__ void split_h2(float x, float y, uint32_t& top, uint32_t& rest) {
