@@ -16,6 +16,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "qg_internal.h"
 #include "qg_norm.h"
@@ -44,7 +45,9 @@ __device__ __forceinline__ Vec load8(const uint16_t* row, int c, int k) {
     const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + c));
     v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
   } else {
-    for (int i = 0; c + i < k; ++i) v.w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < k) v.w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
   }
   return v;
 }
@@ -52,26 +55,37 @@ __device__ __forceinline__ void store8(uint16_t* row, int c, int k, const Vec& v
   if (c + 8 <= k) {
     *reinterpret_cast<uint4*>(row + c) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
   } else {
-    for (int i = 0; c + i < k; ++i) row[c + i] = (uint16_t)(v.w[i >> 1] >> (16 * (i & 1)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < k) row[c + i] = (uint16_t)(v.w[i >> 1] >> (16 * (i & 1)));
   }
 }
 
-// Block-wide sum or maximum of one value a thread, the same in every thread.  `slots` holds
-// a float per warp; a caller that comes again alternates between two of them.
+// Block-wide sum of one value a thread and, with MAX, the maximum of another (a magnitude), the same in every thread.  The
+// slots hold a float per warp, 0 past the last warp; a caller that comes again alternates between two of them.
 template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float* slots) {
+__device__ __forceinline__ void block_reduce(float& v, float& m, float* sums, float* maxima) {
 #pragma unroll
   for (int off = 16; off; off >>= 1) {
-    const float o = __shfl_xor_sync(0xFFFFFFFFu, v, off);
-    v = MAX ? fmaxf(v, o) : v + o;
+    v += __shfl_xor_sync(0xFFFFFFFFu, v, off);
+    if (MAX) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
   }
   const int warps = blockDim.x >> 5;
-  if (warps == 1) return v;
-  if ((threadIdx.x & 31) == 0) slots[threadIdx.x >> 5] = v;
+  if (warps == 1) return;
+  if ((threadIdx.x & 31) == 0) {
+    sums[threadIdx.x >> 5] = v;
+    if (MAX) maxima[threadIdx.x >> 5] = m;
+  }
   __syncthreads();
-  v = slots[0];
-  for (int i = 1; i < warps; ++i) v = MAX ? fmaxf(v, slots[i]) : v + slots[i];
-  return v;
+  v = m = 0.0f;
+  for (int i = 0; i < warps; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(sums + i);
+    v += (f.x + f.y) + (f.z + f.w);
+    if (MAX) {
+      const float4 g = *reinterpret_cast<const float4*>(maxima + i);
+      m = fmaxf(fmaxf(m, g.x), fmaxf(g.y, fmaxf(g.z, g.w)));
+    }
+  }
 }
 
 // Eight E4M3 codes: nearest even, saturating at 448, NaN stays NaN.
@@ -87,79 +101,153 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, int64_t r, int c,
   if (c + 8 <= k) {
     *reinterpret_cast<uint2*>(row + c) = make_uint2(w[0], w[1]);
   } else {
-    for (int i = 0; c + i < k; ++i) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < k) row[c + i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
   }
+}
+
+// h times the row's 1 / sqrt and the weight.
+__device__ __forceinline__ void scaled(const Vec& h, const Vec& w, float inv, float woff, float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = lo(h.w[j]) * inv * (lo(w.w[j]) + woff);
+    v[2 * j + 1] = hi(h.w[j]) * inv * (hi(w.w[j]) + woff);
+  }
+}
+// The largest magnitude of eight values, NaN and (finite) infinities left out.
+__device__ __forceinline__ float largest(const float (&v)[8], bool finite) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, !finite || fabsf(v[j]) < INFINITY ? fabsf(v[j]) : 0.0f);
+  return m;
+}
+// Of the values themselves, infinities left out; rare, so out of line.
+__device__ __noinline__ float largest_value(Vec h, Vec w, float inv, float woff) {
+  float v[8];
+  scaled(h, w, inv, woff, v);
+  return largest(v, true);
+}
+// Over the `lanes` neighbouring lanes of a group.
+__device__ __forceinline__ float group_max(float m, int lanes) {
+  for (int off = lanes >> 1; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
+  return m;
 }
 
 template <int NV, bool RES, int FP8>  // FP8: 0 bf16 only, 1 a scale a group, 2 a scale a row
 __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
-  __shared__ float slots[2][2][32];
+  __shared__ __align__(16) float slots[2][2][32];
+  if (threadIdx.x < 128) (&slots[0][0][0])[threadIdx.x] = 0.0f;
+  if (blockDim.x < 128)
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) (&slots[0][0][0])[i] = 0.0f;
   if (threadIdx.x == 0) pdl_launch_dependents();
+  __syncthreads();
   pdl_wait();
-  const int k = (int)a.k, T = blockDim.x;
+  const int k = (int)a.k, T = blockDim.x, c0 = threadIdx.x * 8;
+  constexpr bool kAhead = NV <= 2;               // registers for the next row
+  constexpr bool kHold = kAhead && FP8 != 2;     // and for the weights (one scale a row takes others)
+  Vec w[kHold ? NV : 1], x[NV], q[NV];
+  auto load = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = load8(a.x + r * a.ldx, c0 + i * T * 8, k);
+      if (RES) q[i] = load8(a.res + r * a.ldr, c0 + i * T * 8, k);
+    }
+  };
+  if (kHold) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) w[kHold ? i : 0] = load8(a.w, c0 + i * T * 8, k);
+  }
+  if (kAhead) load(blockIdx.x);
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x, turn ^= 1) {
     Vec h[NV];
     float sq = 0.0f;
+    if (!kAhead) load(r);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (threadIdx.x + i * T) * 8;
-      h[i] = load8(a.x + r * a.ldx, c, k);
+      h[i] = x[i];
       if (RES) {
-        const Vec q = load8(a.res + r * a.ldr, c, k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[i].w[j] = pack_bf16(lo(h[i].w[j]) + lo(q.w[j]), hi(h[i].w[j]) + hi(q.w[j]));
-        if (a.sum) store8(a.sum + r * a.ldh, c, k, h[i]);
+        for (int j = 0; j < 4; ++j) h[i].w[j] = pack_bf16(lo(x[i].w[j]) + lo(q[i].w[j]), hi(x[i].w[j]) + hi(q[i].w[j]));
       }
+    }
+    if (kAhead && r + gridDim.x < a.m) load(r + gridDim.x);  // while this row is summed and stored
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if (RES && a.sum) store8(a.sum + r * a.ldh, c0 + i * T * 8, k, h[i]);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         sq = fmaf(lo(h[i].w[j]), lo(h[i].w[j]), sq);
         sq = fmaf(hi(h[i].w[j]), hi(h[i].w[j]), sq);
       }
     }
-    sq = block_reduce<false>(sq, slots[0][turn]);
-    const float inv = rsqrtf(sq * a.inv_k + a.eps);
-    float y[NV][8];
     float amax = 0.0f;
+    if (FP8 == 2) {  // of h times the weight: 1 / sqrt is not there yet
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const Vec g = kHold ? w[kHold ? i : 0] : load8(a.w, c0 + i * T * 8, k);
+        float v[8];
+        scaled(h[i], g, 1.0f, a.woff, v);
+        amax = fmaxf(amax, largest(v, false));
+      }
+    }
+    block_reduce<FP8 == 2>(sq, amax, slots[0][turn], slots[1][turn]);
+    const float inv = rsqrtf(sq * a.inv_k + a.eps);
+    float is = 0.0f;
+    if (FP8 == 2) {
+      if (amax >= 0x1p-100f && amax < INFINITY) {  // the same for the block
+        amax *= inv;
+      } else {  // of the values themselves: the products may have passed fp32's range where these do not
+        amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const Vec g = kHold ? w[kHold ? i : 0] : load8(a.w, c0 + i * T * 8, k);
+          amax = fmaxf(amax, largest_value(h[i], g, inv, a.woff));
+        }
+        float none = 0.0f;
+        __syncthreads();
+        block_reduce<true>(none, amax, slots[0][turn], slots[1][turn]);
+      }
+      const float s = fmaxf(__fdiv_rn(amax < INFINITY ? amax : 0.0f, 448.0f), kScaleMin);
+      if (threadIdx.x == 0) a.scales[r * a.lds] = s;
+      is = __frcp_rn(s);
+    }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (threadIdx.x + i * T) * 8;
-      const Vec w = load8(a.w, c, k);
-      if (FP8 == 1) amax = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float f = j & 1 ? hi(h[i].w[j >> 1]) : lo(h[i].w[j >> 1]);
-        const float g = (j & 1 ? hi(w.w[j >> 1]) : lo(w.w[j >> 1])) + a.woff;
-        y[i][j] = f * inv * g;
-        if (FP8) amax = fmaxf(amax, c + j < k && fabsf(y[i][j]) < INFINITY ? fabsf(y[i][j]) : 0.0f);
-      }
+      const int c = c0 + i * T * 8;
+      float v[8];
+      scaled(h[i], kHold ? w[kHold ? i : 0] : load8(a.w, c, k), inv, a.woff, v);
       if (FP8 == 0 || a.y) {
         Vec o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(y[i][2 * j], y[i][2 * j + 1]);
+        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
         store8(a.y + r * a.ldy, c, k, o);
       }
       if (FP8 == 1) {
-        for (int off = a.group_lanes >> 1; off; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, off));
+        // NaN does not enter a maximum; infinities are found out by it and left out in a second look.  What lies past the
+        // row's end is 0 (or NaN).
+        amax = group_max(largest(v, false), a.group_lanes);
+        if (__any_sync(0xFFFFFFFFu, amax == INFINITY)) amax = group_max(largest(v, true), a.group_lanes);
         const float s = fmaxf(__fdiv_rn(amax, 448.0f), kScaleMin);
-        if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + c / (a.group_lanes * 8)] = s;
-        store_codes(a, r, c, k, y[i], __frcp_rn(s));
+        if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + (c >> a.group_log2)] = s;
+        is = __frcp_rn(s);
       }
-    }
-    if (FP8 == 2) {
-      amax = block_reduce<true>(amax, slots[1][turn]);
-      const float s = fmaxf(__fdiv_rn(amax, 448.0f), kScaleMin);
-      if (threadIdx.x == 0) a.scales[r * a.lds] = s;
-      const float is = __frcp_rn(s);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) store_codes(a, r, (threadIdx.x + i * T) * 8, k, y[i], is);
+      if (FP8) store_codes(a, r, c, k, v, is);
     }
   }
 }
 
 template <int NV, bool RES, int FP8>
 int launch(const NormArgs& a, const DeviceInfo& dev, int threads, cudaStream_t s) {
-  const int64_t resident = (int64_t)dev.sms * std::max(1, 2048 / threads);
+  static std::atomic<int> per_sm[33];  // CTAs an SM by warps a CTA: asked once
+  int n = per_sm[threads / 32].load();
+  if (n == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rms_norm_kernel<NV, RES, FP8>, threads, 0) != cudaSuccess || n < 1)
+      return QG_ERR_CUDA;
+    per_sm[threads / 32].store(n);
+  }
+  const int64_t resident = (int64_t)dev.sms * n;
   if (launch_pdl(rms_norm_kernel<NV, RES, FP8>, dim3((unsigned)std::min(a.m, resident)), dim3(threads), 0, s, a) != cudaSuccess)
     return QG_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
@@ -180,7 +268,9 @@ int launch_nv(const NormArgs& a, const DeviceInfo& dev, int threads, cudaStream_
 int launch_rms_norm(const NormArgs& a, const DeviceInfo& dev, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t vecs = (a.k + 7) / 8;
-  const int nv = vecs <= 1024 ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 ? 4 : 8;
+  // Two vectors a thread where rows queue up (4096 x 5120: 27 us, one vector 31, four 28); one where every row has a CTA of its
+  // own (64 x 5120 to E4M3: 2.3 us, two vectors 3.4); more where the row takes more than 1024 threads.
+  const int nv = vecs <= 1024 && a.m <= dev.sms ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 ? 4 : 8;
   const int threads = (int)((vecs + nv - 1) / nv + 31) / 32 * 32;
   return nv == 1 ? launch_nv<1>(a, dev, threads, s) : nv == 2 ? launch_nv<2>(a, dev, threads, s)
          : nv == 4 ? launch_nv<4>(a, dev, threads, s) : launch_nv<8>(a, dev, threads, s);

@@ -65,5 +65,6 @@ extern "C" qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residua
   a.ldc = o.ldc;
   a.lds = o.lds;
   a.group_lanes = o.codes ? (int)(o.group / 8) : 0;
+  a.group_log2 = a.group_lanes == 4 ? 5 : a.group_lanes == 8 ? 6 : 7;
   return (qg_status)launch_rms_norm(a, dev, stream);
 }

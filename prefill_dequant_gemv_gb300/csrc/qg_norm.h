@@ -22,6 +22,7 @@ struct NormArgs {
   float* scales;
   int64_t ldc, lds;
   int group_lanes;  // eighths of a group: 4, 8 or 16; 0: one scale a row
+  int group_log2;
 };
 int launch_rms_norm(const NormArgs& a, const DeviceInfo& dev, void* stream);
 
