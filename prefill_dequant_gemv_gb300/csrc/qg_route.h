@@ -17,15 +17,28 @@ constexpr int kGroupInts = 8;
 // Pairs one CTA routes in the decode chain's gate/up launch (T <= 4 tokens, k <= 16).
 constexpr int kBlockRoutePairs = 64;
 
+// Tokens that one block of the large router's top-k takes: whole rounds of its eight warps, some 512 blocks at most; and
+// that one of its placing blocks takes: whole blocks of those, no more pairs than it has threads.
+constexpr int kRouteBlock = 1024;
+__host__ __device__ inline int route_block_tokens(int64_t T, int k) {
+  const int64_t even = ((T + 511) / 512 + 7) / 8 * 8, most = kRouteBlock / k / 8 * 8;
+  return (int)(even < most ? even : most);
+}
+__host__ __device__ inline int route_place_tokens(int64_t T, int k) {
+  const int tb = route_block_tokens(T, k);
+  return kRouteBlock / k / tb * tb;
+}
+
 struct RouteLayout {
-  size_t meta, counts, offsets, active, pair_list, pair_pos, tiles, groups, zidx, block_counts, block_start, total;
+  size_t meta, counts, offsets, active, pair_list, pair_pos, tiles, groups, zidx, block_counts, total;
   int64_t max_tiles, nblocks;
 };
 
 __host__ __device__ inline RouteLayout route_layout(int64_t T, int E, int k) {
   RouteLayout L;
   const int64_t P = T * k;
-  L.nblocks = (P + 1023) / 1024;
+  const int tb = route_block_tokens(T, k);
+  L.nblocks = (T + tb - 1) / tb;
   L.max_tiles = (P + kRouteTile - 1) / kRouteTile + E;
   size_t o = 0;
   auto take = [&o](size_t bytes) {
@@ -43,7 +56,6 @@ __host__ __device__ inline RouteLayout route_layout(int64_t T, int E, int k) {
   L.groups = take((size_t)E * kGroupInts * 4);  // group table, one entry per active expert
   L.zidx = take((size_t)E * 4);                 // expert -> its index in the active list
   L.block_counts = take((size_t)L.nblocks * E * 4);
-  L.block_start = take((size_t)L.nblocks * E * 4);
   L.total = o;
   return L;
 }
@@ -58,8 +70,7 @@ struct RouteView {
   int* tiles;
   int* groups;
   int* zidx;
-  int* block_counts;
-  int* block_start;
+  int* block_counts;  // [block][expert]: pairs, then pairs in the blocks before
 };
 
 // A qg_route_rule as the kernels take it.

@@ -8,13 +8,13 @@
 // thousand): first only the experts that can be among the topk, one a lane; or all of them
 // where the groups are in doubt, or more than 32 experts are.
 //
-// Error of c in fp32 (u = 2^-24): expf is within 2 u (relative), as is the reciprocal.  Sigmoid:
-// 1 + e and its reciprocal add 3 u: s is off by less than 6 u s <= 6 u.  Softmax: the
-// argument l - max is rounded (u |l - max|, at most 0.4 u of s = exp(l - max) / S relative to the
-// largest), S adds 21 sums of positive terms, its terms' errors and the arguments' rounding,
-// below 40 u together: s is off by less than 48 u / S.  The sum with the bias adds u |c|.  The
-// tolerance is twice that error and a margin: 2^-20 (sigmoid) or 2^-17 / S (softmax), and
-// 2^-22 |c|; for sums of two c twice as much.
+// Error of c in fp32 (u = 2^-24): __expf(x) is within 2 + 1.173 |x| ulps, an ulp being 2 u at most, the approximate
+// reciprocal within one.  Sigmoid: e^-l enters s with the weight s (1 - s), which leaves less than 0.65 ulps of it; 1 + e and the
+// reciprocal add 3 u: s is off by less than 5 u.  Softmax: with d = max - l, the terms e^-d are off by 2 u (2 + 1.173 d) e^-d and
+// their argument's rounding by u d e^-d, together below 6 u of the largest; in the sum S >= 1 the mean of d over e^-d / S is
+// at most log 512, so S is off by 2 (2 + 1.173 * 6.3) + 6.3 u, its 21 additions by 21 u, its reciprocal by 2 u: s
+// is off by less than 56 u / S.  The sum with the bias adds u |c|.  Two values may be off by twice that: the tolerance is 2^-20
+// (sigmoid; 16 u) or 2^-17 / S (softmax; 128 u), and 2^-22 |c| (4 u); for sums of two c twice as much.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -25,11 +25,18 @@
 
 namespace qg {
 
-// Score of a logit: sigmoid, or softmax with the largest logit m and 1 / S.
-template <class F>
-__device__ __forceinline__ F score_of(const RouteRule& r, F l, F m, F inv) {
-  if (r.sigmoid) return F(1) / (F(1) + (sizeof(F) == 4 ? F(expf(-(float)l)) : F(exp(-(double)l))));
-  return (sizeof(F) == 4 ? F(expf((float)(l - m))) : F(exp((double)(l - m)))) * inv;
+// Score of a logit in 64 bits: sigmoid, or softmax with the largest logit m and 1 / S.
+__device__ __forceinline__ double score_of(const RouteRule& r, double l, double m, double inv) {
+  return r.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - m) * inv;
+}
+// The same in fp32, with the error above.
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float quick_score(const RouteRule& r, float l, float m, float inv) {
+  return r.sigmoid ? rcp_approx(1.0f + __expf(-l)) : __expf(l - m) * inv;
 }
 
 // The two largest of a and b's (a0 >= a1, b0 >= b1).
@@ -84,7 +91,7 @@ __device__ __noinline__ void route_exact(const RouteRule& r, const float* lg, in
 #pragma unroll 1
   for (int i = 0; i < 16; ++i) {
     const int e = lane + 32 * i;
-    if (e < E) c[i] = score_of<double>(r, lg[e], m, inv) + (r.bias ? (double)r.bias[e] : 0.0);
+    if (e < E) c[i] = score_of(r, lg[e], m, inv) + (r.bias ? (double)r.bias[e] : 0.0);
   }
   uint32_t groups = 0xFFFFFFFFu;
   if (r.n_groups > 1) {
@@ -139,42 +146,100 @@ __device__ __noinline__ void route_exact(const RouteRule& r, const float* lg, in
   }
 }
 
-// A warp's choice for one token: ids and weights (and a copy of the ids).  `cs`: E floats of shared memory, the warp's own.
-__device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, int E, int k, float* cs, int32_t* ids, float* wts,
-                                           int* ids_copy) {
-  const int lane = threadIdx.x & 31;
-  float l[16];
-  float m = -INFINITY, inv = 1.0f;
+// One over the sum of a softmax in 64 bits; m its largest logit.
+__device__ __forceinline__ double exact_inverse(const RouteRule& r, const float* lg, int E, float m) {
+  if (r.sigmoid) return 1.0;
+  double s = 0.0;
+#pragma unroll 4
+  for (int e = threadIdx.x & 31; e < E; e += 32) s += lg[e] == lg[e] ? exp((double)lg[e] - m) : 0.0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < E ? lg[e] : __int_as_float(0x7FC00000);
-    m = fmaxf(m, l[i]);  // a NaN is passed over
+  for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
+  return 1.0 / s;
+}
+
+// The topk of `count` (k to 32) experts in `list` by their values in 64 bits, one a lane: as route_exact.
+__device__ __noinline__ void route_listed(const RouteRule& r, const float* lg, int E, int k, float m, const int* list, int count,
+                                          int* slot, int* id) {
+  const int lane = threadIdx.x & 31, e = lane < count ? list[lane] : 1 << 20;
+  const double inv = exact_inverse(r, lg, E, m);
+  const double d = lane < count ? score_of(r, lg[e], m, inv) + (r.bias ? (double)r.bias[e] : 0.0) : -(double)INFINITY;
+  int rank = 0;
+  for (int i = 0; i < count; ++i) {
+    const double o = __shfl_sync(0xFFFFFFFFu, d, i);
+    const int oe = __shfl_sync(0xFFFFFFFFu, e, i);
+    rank += o > d || (o == d && oe < e);
   }
+  *slot = lane < count && rank < k ? rank : -1;
+  *id = e;
+}
+
+// The kept groups by values in 64 bits; `list` has the experts that can be among the best of their groups (up to 32).
+__device__ __noinline__ uint32_t groups_listed(const RouteRule& r, const float* lg, int E, float m, const int* list, int count) {
+  const int lane = threadIdx.x & 31, e = lane < count ? list[lane] : 0, g = group_of(r, e);
+  const double inv = exact_inverse(r, lg, E, m);
+  const double d = lane < count ? score_of(r, lg[e], m, inv) + (r.bias ? (double)r.bias[e] : 0.0) : 0.0;
+  double a0 = -INFINITY, a1 = -INFINITY, gap;
+  for (int i = 0; i < count; ++i) {
+    const double o = __shfl_sync(0xFFFFFFFFu, d, i);
+    if (__shfl_sync(0xFFFFFFFFu, g, i) == lane) merge2(a0, a1, o, -(double)INFINITY);
+  }
+  return keep_groups(r.group_best == 2 ? a0 + a1 : a0, r.n_groups, r.topk_groups, &gap);
+}
+
+// The experts l + 32 i for the bits i of lane l's mask, in `list`; how many (past 32: none is written).
+__device__ __forceinline__ int list_experts(uint32_t mask, int* list) {
+  const int lane = threadIdx.x & 31, count = __reduce_add_sync(0xFFFFFFFFu, __popc(mask));
+  if (count > 32) return count;
+  int at = __popc(mask);
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xFFFFFFFFu, at, off);
+    if (lane >= off) at += o;
+  }
+  at -= __popc(mask);
+  __syncwarp();
+  for (; mask; mask &= mask - 1) list[at++] = lane + 32 * (__ffs(mask) - 1);
+  __syncwarp();
+  return count;
+}
+
+// A warp's choice for one token of up to 32 S experts: ids and weights, and a copy of the ids and a count of them in hist
+// where they are given.  `cs`: 32 S floats of shared memory, the warp's own.  Of the logits and biases only the choice values
+// stay in registers (three blocks of warps an SM instead of two); what is rare reads them again.
+template <int S>
+__device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, int E, int k, float* cs, int32_t* ids, float* wts,
+                                           int* ids_copy, int* hist) {
+  const int lane = threadIdx.x & 31;
+  float c[S];  // the logits first: lane l has expert l + 32 i's in c[i], NaN where there is none
+#pragma unroll
+  for (int i = 0; i < S; ++i) c[i] = lane + 32 * i < E ? lg[lane + 32 * i] : __int_as_float(0x7FC00000);
+  float m = -INFINITY, inv = 1.0f;
   if (!r.sigmoid && (r.values || !r.renormalise)) {
+#pragma unroll
+    for (int i = 0; i < S; ++i) m = fmaxf(m, c[i]);  // a NaN is passed over
 #pragma unroll
     for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += l[i] == l[i] ? expf(l[i] - m) : 0.0f;
+    for (int i = 0; i < S; ++i) s += c[i] == c[i] ? __expf(c[i] - m) : 0.0f;
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    inv = 1.0f / s;
+    inv = rcp_approx(s);
   }
-  float c[16];
+  float near = 0.0f;  // and 2^-22 |c|
+  if (r.values) {
+    near = r.sigmoid ? 0x1p-20f : 0x1p-17f * inv;
+    float bias[S];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int e = lane + 32 * i;
-    c[i] = l[i];
-    if (r.values && e < E) c[i] = score_of<float>(r, l[i], m, inv) + (r.bias ? r.bias[e] : 0.0f);
+    for (int i = 0; i < S; ++i) bias[i] = r.bias && lane + 32 * i < E ? r.bias[lane + 32 * i] : 0.0f;
+#pragma unroll
+    for (int i = 0; i < S; ++i) c[i] = quick_score(r, c[i], m, inv) + bias[i];
   }
-  const float near = r.values ? (r.sigmoid ? 0x1p-20f : 0x1p-17f * inv) : 0.0f;  // and 2^-22 |c|
+  uint32_t open = 0xFFFFFFFFu;  // bit i: the lane's expert i may be chosen
   bool doubt = false;
-  uint32_t groups = 0xFFFFFFFFu;
   if (r.n_groups > 1) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (lane + 32 * i < E) cs[lane + 32 * i] = c[i];
+    for (int i = 0; i < S; ++i) cs[lane + 32 * i] = c[i];
     __syncwarp();
     // `per` lanes (a power of two) to a group, each over every per-th of its experts
     const int per = r.group_lanes, size = E / r.n_groups, g = lane / per;
@@ -186,87 +251,71 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
       }
     for (int off = per >> 1; off; off >>= 1)
       merge2(a0, a1, __shfl_xor_sync(0xFFFFFFFFu, a0, off), __shfl_xor_sync(0xFFFFFFFFu, a1, off));
-    float value = r.group_best == 2 ? a0 + a1 : a0;
-    value = __shfl_sync(0xFFFFFFFFu, value, (lane * per) & 31);
-    float gap;
-    groups = keep_groups(value, r.n_groups, r.topk_groups, &gap);
-    float size_of = lane < r.n_groups && fabsf(value) < INFINITY ? fabsf(value) : 0.0f;
+    a0 = __shfl_sync(0xFFFFFFFFu, a0, (lane * per) & 31);
+    a1 = __shfl_sync(0xFFFFFFFFu, a1, (lane * per) & 31);
+    const float value = r.group_best == 2 ? a0 + a1 : a0;
+    float gap, size_of = lane < r.n_groups && fabsf(value) < INFINITY ? fabsf(value) : 0.0f;
+    uint32_t groups = keep_groups(value, r.n_groups, r.topk_groups, &gap);
+    if (r.values && r.topk_groups < r.n_groups) {
+      size_of = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(size_of)));
+      if (!(gap > 2.0f * near + 0x1p-21f * size_of)) {
+        // the groups' order hangs on values that are near each other: their best experts, and those near them, in 64 bits
+        __syncwarp();
+        const float last = r.group_best == 2 ? a1 : a0;
+        if (lane < r.n_groups) cs[lane] = last - (near + 0x1p-22f * fabsf(last));
+        __syncwarp();
+        uint32_t best = 0;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) size_of = fmaxf(size_of, __shfl_xor_sync(0xFFFFFFFFu, size_of, off));
-    doubt = r.values && r.topk_groups < r.n_groups && !(gap > 2.0f * near + 0x1p-21f * size_of);
-    __syncwarp();
-  }
-  int slot = -1, id = 0;
-  if (!doubt) {
-    uint32_t key[16], open = 0;
+        for (int i = 0; i < S; ++i)
+          if (lane + 32 * i < E && c[i] >= cs[group_of(r, lane + 32 * i)]) best |= 1u << i;
+        int* list = reinterpret_cast<int*>(cs) + 32;
+        const int count = list_experts(best, list);
+        doubt = count > 32;
+        if (!doubt) groups = groups_listed(r, lg, E, m, list, count);
+      }
+    }
+    open = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = lane + 32 * i;
-      const bool in = e < E && (r.n_groups == 1 || (groups >> group_of(r, e) & 1));
-      key[i] = in ? order_key(c[i]) : 0u;
+    for (int i = 0; i < S; ++i) {
+      const bool in = groups >> group_of(r, lane + 32 * i) & 1;
       open |= in ? 1u << i : 0u;
     }
-    uint32_t mine, top;
+    __syncwarp();
+  }
+  int slot = lane < k ? lane : -1, id = 0;
+  {
+    uint32_t key[S], mine, top;
+#pragma unroll
+    for (int i = 0; i < S; ++i) key[i] = lane + 32 * i < E && (open >> i & 1) ? order_key(c[i]) : 0u;
     warp_topk_keys(key, k, mine, id, top);
-    slot = lane < k ? lane : -1;
-    if (r.values) {
+    if (r.values && !doubt) {
       const float v = key_value(mine), vk = __shfl_sync(0xFFFFFFFFu, v, k - 1);
-      const float lm = lane < k ? lg[id] : 0.0f, bm = lane < k && r.bias ? r.bias[id] : 0.0f;
-      const float lk = __shfl_sync(0xFFFFFFFFu, lm, k - 1), bk = __shfl_sync(0xFFFFFFFFu, bm, k - 1);
-      // two winners in a row: near, and not the same logit and bias (then it is a tie indeed)
-      const float vn = __shfl_down_sync(0xFFFFFFFFu, v, 1), ln = __shfl_down_sync(0xFFFFFFFFu, lm, 1),
-                  bn = __shfl_down_sync(0xFFFFFFFFu, bm, 1);
-      const bool close = lane + 1 < k && v - vn <= near + 0x1p-22f * fabsf(v) && !(lm == ln && bm == bn);
-      // experts that may belong to the topk: at the last winner's value or less than the tolerance below it
-      const float least = vk - (near + 0x1p-22f * fabsf(vk));
-      uint32_t may = 0, other = 0;
+      // two winners in a row that are near each other; experts at the last winner's value or less than the tolerance below
+      // it, which are k where no other comes near the winners
+      const float vn = __shfl_down_sync(0xFFFFFFFFu, v, 1), least = vk - (near + 0x1p-22f * fabsf(vk));
+      const bool close = lane + 1 < k && v - vn <= near + 0x1p-22f * fabsf(v);
+      uint32_t may = 0;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int e = lane + 32 * i;
-        if ((open >> i & 1) && c[i] >= least) {
-          may |= 1u << i;
-          if (!(l[i] == lk && (!r.bias || r.bias[e] == bk))) other |= 1u << i;
+      for (int i = 0; i < S; ++i) may |= c[i] >= least ? 1u << i : 0u;
+      may &= open;
+      if (__any_sync(0xFFFFFFFFu, close) || __reduce_add_sync(0xFFFFFFFFu, __popc(may)) > k) {
+        // equal values of equal logits and biases are ties indeed, and the lower index has come first
+        const float lm = lane < k ? lg[id] : 0.0f, bm = lane < k && r.bias ? r.bias[id] : 0.0f;
+        const float lk = __shfl_sync(0xFFFFFFFFu, lm, k - 1), bk = __shfl_sync(0xFFFFFFFFu, bm, k - 1);
+        const float ln = __shfl_down_sync(0xFFFFFFFFu, lm, 1), bn = __shfl_down_sync(0xFFFFFFFFu, bm, 1);
+        uint32_t other = 0;
+        for (int i = 0; i < S; ++i) {
+          const int e = lane + 32 * i;
+          if ((may >> i & 1) && !(lg[e] == lk && (!r.bias || r.bias[e] == bk))) other |= 1u << i;
         }
-      }
-      const int others = __reduce_add_sync(0xFFFFFFFFu, __popc(other));
-      const int chosen = __popc(__ballot_sync(0xFFFFFFFFu, lane < k && v >= least && !(lm == lk && bm == bk)));
-      if (__any_sync(0xFFFFFFFFu, close) || others != chosen) {
-        const int count = __reduce_add_sync(0xFFFFFFFFu, __popc(may));
-        if (count > 32 || count < k) {
-          doubt = true;
-        } else {  // one of them a lane, in 64 bits
-          int at = __popc(may);
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xFFFFFFFFu, at, off);
-            if (lane >= off) at += o;
-          }
-          at -= __popc(may);
+        const int others = __reduce_add_sync(0xFFFFFFFFu, __popc(other));
+        const int chosen = __popc(__ballot_sync(0xFFFFFFFFu, lane < k && v >= least && !(lm == lk && bm == bk)));
+        if (__any_sync(0xFFFFFFFFu, close && !(lm == ln && bm == bn)) || others != chosen) {
           int* list = reinterpret_cast<int*>(cs);
-          for (int i = 0; i < 16; ++i)
-            if (may >> i & 1) list[at++] = lane + 32 * i;
+          const int count = list_experts(may, list);
+          doubt = count > 32 || count < k;
+          if (!doubt) route_listed(r, lg, E, k, m, list, count, &slot, &id);
           __syncwarp();
-          id = lane < count ? list[lane] : 1 << 20;
-          __syncwarp();
-          double dm = 0.0, dinv = 1.0;
-          if (!r.sigmoid) {
-            dm = m;
-            double s = 0.0;
-#pragma unroll 1
-            for (int e = lane; e < E; e += 32) s += lg[e] == lg[e] ? exp((double)lg[e] - dm) : 0.0;
-#pragma unroll
-            for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-            dinv = 1.0 / s;
-          }
-          const double d = lane < count ? score_of<double>(r, lg[id], dm, dinv) + (r.bias ? (double)r.bias[id] : 0.0)
-                                        : -(double)INFINITY;
-          int rank = 0;
-          for (int i = 0; i < count; ++i) {
-            const double o = __shfl_sync(0xFFFFFFFFu, d, i);
-            const int oi = __shfl_sync(0xFFFFFFFFu, id, i);
-            rank += o > d || (o == d && oi < id);
-          }
-          slot = lane < count && rank < k ? rank : -1;
         }
       }
     }
@@ -290,12 +339,13 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
     w = w / s;
   } else {
-    w = r.sigmoid && lw < 0.0f ? expf(lw) / (1.0f + expf(lw)) : score_of<float>(r, lw, m, inv);
+    w = !r.sigmoid ? expf(lw - m) * inv : lw < 0.0f ? expf(lw) / (1.0f + expf(lw)) : 1.0f / (1.0f + expf(-lw));
   }
   if (slot >= 0) {
     ids[slot] = id;
     wts[slot] = w * r.scale;
     if (ids_copy) ids_copy[slot] = id;
+    if (hist) atomicAdd(&hist[id], 1);  // integer counts: order-free
   }
 }
 

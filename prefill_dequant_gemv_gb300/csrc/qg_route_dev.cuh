@@ -23,56 +23,58 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k ^ 0x80000000u) : ~k);
 }
 
-// Largest key of a lane's 16 (ties to the lower slot, i.e. the lower expert index): a
-// 4-level tree over fixed register indices.
-__device__ __forceinline__ void lane_best(const uint32_t (&key)[16], uint32_t& bk, int& bi) {
-  uint32_t k8[8];
-  int i8[8];
+// Largest key of a lane's S (ties to the lower slot, i.e. the lower expert index): a tree over fixed
+// register indices.
+template <int S>
+__device__ __forceinline__ void lane_best(const uint32_t (&key)[S], uint32_t& bk, int& bi) {
+  uint32_t kk[S / 2];
+  int ii[S / 2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < S / 2; ++i) {
     const bool hi = key[2 * i + 1] > key[2 * i];
-    k8[i] = hi ? key[2 * i + 1] : key[2 * i];
-    i8[i] = hi ? 2 * i + 1 : 2 * i;
+    kk[i] = hi ? key[2 * i + 1] : key[2 * i];
+    ii[i] = hi ? 2 * i + 1 : 2 * i;
   }
 #pragma unroll
-  for (int w = 4; w >= 1; w >>= 1)
+  for (int w = S / 4; w >= 1; w >>= 1)
 #pragma unroll
     for (int i = 0; i < w; ++i) {
-      const bool hi = k8[i + w] > k8[i] || (k8[i + w] == k8[i] && i8[i + w] < i8[i]);
-      k8[i] = hi ? k8[i + w] : k8[i];
-      i8[i] = hi ? i8[i + w] : i8[i];
+      const bool hi = kk[i + w] > kk[i] || (kk[i + w] == kk[i] && ii[i + w] < ii[i]);
+      kk[i] = hi ? kk[i + w] : kk[i];
+      ii[i] = hi ? ii[i + w] : ii[i];
     }
-  bk = k8[0];
-  bi = i8[0];
+  bk = kk[0];
+  bi = ii[0];
 }
 
-// Warp-level top-k of up to 512 keys (0: none): lane l holds the keys of experts l, l+32, ...
-// (16 registers; the expert of slot i is l + 32 i).  Each lane first extracts its
+// Warp-level top-k of up to 32 S keys (0: none; S = 4, 8 or 16): lane l holds the keys of experts l, l+32, ...
+// (S registers; the expert of slot i is l + 32 i).  Each lane first extracts its
 // three best keys in order (ties to the lower slot, i.e. the lower expert).  Each of k rounds
 // then takes the warp maximum of the lanes' current heads and the warp minimum of the experts
 // holding it (two single-instruction warp reductions), and the winner's lane steps to its
 // next key with three selects -- no search on the rounds' serial path.  A lane that has won
 // three times before the last round has no extracted key left: the rounds are then redone
-// from all 16 keys, the winner's lane searching its next best each time (the same result,
+// from all S keys, the winner's lane searching its next best each time (the same result,
 // only slower; the fast rounds never pick a wrong key before that point).  Lane
 // j keeps the j-th winner (mine, mine_id); top is the first one's key.
-__device__ __forceinline__ void warp_topk_keys(uint32_t (&key)[16], int k, uint32_t& mine, int& mine_id, uint32_t& top) {
+template <int S>
+__device__ __forceinline__ void warp_topk_keys(uint32_t (&key)[S], int k, uint32_t& mine, int& mine_id, uint32_t& top) {
   const int lane = threadIdx.x & 31;
   uint32_t h0, h1, h2;  // the lane's three best keys, descending, and their experts
   int e0, e1, e2;
   {
-    uint32_t kk[16];
+    uint32_t kk[S];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) kk[i] = key[i];
+    for (int i = 0; i < S; ++i) kk[i] = key[i];
     int bi;
     lane_best(kk, h0, bi);
     e0 = lane + 32 * bi;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) kk[i] = (i == bi) ? 0u : kk[i];
+    for (int i = 0; i < S; ++i) kk[i] = (i == bi) ? 0u : kk[i];
     lane_best(kk, h1, bi);
     e1 = lane + 32 * bi;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) kk[i] = (i == bi) ? 0u : kk[i];
+    for (int i = 0; i < S; ++i) kk[i] = (i == bi) ? 0u : kk[i];
     lane_best(kk, h2, bi);
     e2 = lane + 32 * bi;
   }
@@ -97,7 +99,7 @@ __device__ __forceinline__ void warp_topk_keys(uint32_t (&key)[16], int k, uint3
     e1 = w ? e2 : e1;
     h2 = w ? 0u : h2;
   }
-  if (__any_sync(0xFFFFFFFFu, short_of_keys)) {  // a lane may have needed a fourth key: redo from all 16
+  if (__any_sync(0xFFFFFFFFu, short_of_keys)) {  // a lane may have needed a fourth key: redo from all of them
     uint32_t bk;
     int bi;
     lane_best(key, bk, bi);
@@ -111,15 +113,17 @@ __device__ __forceinline__ void warp_topk_keys(uint32_t (&key)[16], int k, uint3
       }
       if ((win & 31) == lane) {  // the winner's lane takes the slot out and finds its next best
 #pragma unroll
-        for (int i = 0; i < 16; ++i) key[i] = (i == (win >> 5)) ? 0u : key[i];
+        for (int i = 0; i < S; ++i) key[i] = (i == (win >> 5)) ? 0u : key[i];
         lane_best(key, bk, bi);
       }
     }
   }
 }
 
-// Warp-level top-k of one token's logits (E <= 512) and the k lanes' softmax over the kept ones in parallel.
-__device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t* ids, float* wts, int* ids_copy = nullptr) {
+// Warp-level top-k of one token's logits (E <= 512) and the k lanes' softmax over the kept ones in parallel; a copy of
+// the ids and a count of them in hist, each where it is given.
+__device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t* ids, float* wts, int* ids_copy = nullptr,
+                                          int* hist = nullptr) {
   const int lane = threadIdx.x & 31;
   uint32_t key[16];
 #pragma unroll
@@ -139,6 +143,7 @@ __device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t
     ids[lane] = mine_id;
     wts[lane] = z / sum;
     if (ids_copy) ids_copy[lane] = mine_id;
+    if (hist) atomicAdd(&hist[mine_id], 1);  // integer counts: order-free
   }
 }
 

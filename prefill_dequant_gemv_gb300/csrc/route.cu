@@ -11,8 +11,6 @@
 // deterministic: ranks come from ordered scans, never from atomic arrival order.
 #include <cuda_runtime.h>
 
-#include <algorithm>
-
 #include "qg_internal.h"
 #include "qg_route.h"
 #include "qg_route_by.cuh"
@@ -21,39 +19,12 @@
 
 namespace qg {
 
-constexpr int kRouteBlock = 1024;  // pairs per grouping block (one thread per pair)
-
-__global__ void __launch_bounds__(256) route_topk_kernel(const float* logits, int64_t T, int E, int k, int32_t* ids,
-                                                         float* wts) {
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= T) return;
-  warp_topk(logits + t * E, E, k, ids + t * k, wts + t * k);
-}
-
-__global__ void __launch_bounds__(256) route_topk_by_kernel(RouteRule rule, const float* logits, int64_t T, int E, int k,
-                                                            int32_t* ids, float* wts) {
-  __shared__ float cs[8][kMaxExperts];
-  const int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (t >= T) return;
-  warp_route(rule, logits + t * E, E, k, cs[threadIdx.x >> 5], ids + t * k, wts + t * k, nullptr);
-}
+constexpr int kRouteBySmall = 2;  // tokens that one CTA routes by a rule (shared memory holds no more than some)
 
 // Clear a shared array with 16-byte stores (bytes a multiple of 16, 16-byte aligned).
 __device__ __forceinline__ void zero_shared(void* p, int bytes) {
   uint4* q = static_cast<uint4*>(p);
   for (int i = threadIdx.x; i < bytes / 16; i += blockDim.x) q[i] = make_uint4(0, 0, 0, 0);
-}
-
-// Per-block histogram of the experts of pairs [b*kRouteBlock, ...).
-__device__ void block_count(const int32_t* ids, int64_t P, int E, int b, int* out) {
-  __shared__ int hist[kMaxExperts];
-  for (int e = threadIdx.x; e < E; e += blockDim.x) hist[e] = 0;
-  __syncthreads();
-  const int64_t p = (int64_t)b * kRouteBlock + threadIdx.x;
-  if (threadIdx.x < kRouteBlock && p < P) atomicAdd(&hist[ids[p]], 1);  // integer counts: order-free
-  __syncthreads();
-  for (int e = threadIdx.x; e < E; e += blockDim.x) out[e] = hist[e];
-  __syncthreads();
 }
 
 // Block-wide exclusive scan of three counters (every thread of the block calls it;
@@ -96,110 +67,134 @@ __device__ __forceinline__ int3 block_scan3(int3 x, int3* tot) {
   return make_int3(base.x + inc.x - x.x, base.y + inc.y - x.y, base.z + inc.z - x.z);
 }
 
-// Sum of n counters strided by E (per-block expert counts), loads batched for overlap.
-__device__ __forceinline__ int strided_sum(const int* p, int E, int n) {
-  int s = 0, b = 0;
-  for (; b + 8 <= n; b += 8) {
-    int t[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = p[(size_t)(b + i) * E];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s += t[i];
+// Large router, first launch: the experts and weights of a block of tokens, a warp a token, and how many of the block's
+// pairs every expert has.  S: 32 S experts at most.
+template <int S, bool BY>
+__global__ void __launch_bounds__(256, 3) route_topk_kernel(const float* logits, int64_t T, int E, int k, int tokens, int32_t* ids,
+                                                         float* wts, RouteView r, RouteRule rule) {
+  __shared__ int hist[32 * S];
+  __shared__ float cs[BY ? 8 : 1][BY ? 32 * S : 1];
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  for (int e = threadIdx.x; e < E; e += 256) hist[e] = 0;
+  __syncthreads();
+  pdl_wait();
+  const int64_t t0 = (int64_t)blockIdx.x * tokens, t1 = t0 + tokens < T ? t0 + tokens : T;
+  if constexpr (BY) {
+    for (int64_t t = t0 + warp; t < t1; t += 8)
+      warp_route<S>(rule, logits + t * E, E, k, cs[warp], ids + t * k, wts + t * k, nullptr, hist);
+  } else {
+    for (int64_t t = t0 + warp; t < t1; t += 8) warp_topk(logits + t * E, E, k, ids + t * k, wts + t * k, nullptr, hist);
   }
-  for (; b < n; ++b) s += p[(size_t)b * E];
-  return s;
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256) r.block_counts[(size_t)blockIdx.x * E + e] = hist[e];
 }
 
-// Totals, exclusive offsets, per-block starting positions, active list and tile table,
-// one thread per expert and block-wide scans (blockDim.x >= E).
-__device__ void scan_groups(const RouteView& r, int E, int nblocks, int tile) {
+// Second launch, where the blocks are many: counts become the pairs in the blocks before, and the experts' totals.  A CTA has
+// 32 experts, one a lane; its warps share the blocks.
+__global__ void __launch_bounds__(1024) route_prefix_kernel(int E, int nblocks, RouteView r) {
+  __shared__ int part[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+  if (threadIdx.x == 0) pdl_launch_dependents();
+  pdl_wait();
+  const int per = (nblocks + 31) / 32, b0 = min(nblocks, warp * per), b1 = min(nblocks, b0 + per);
+  int sum = 0;
+  if (e < E)
+#pragma unroll 8
+    for (int b = b0; b < b1; ++b) sum += r.block_counts[(size_t)b * E + e];
+  part[warp][lane] = sum;
+  __syncthreads();
+  int run = 0, tot = 0;
+#pragma unroll
+  for (int w = 0; w < 32; ++w) {
+    const int c = part[w][lane];
+    run += w < warp ? c : 0;
+    tot += c;
+  }
+  if (e >= E) return;
+  if (warp == 0) r.counts[e] = tot;
+#pragma unroll 8
+  for (int b = b0; b < b1; ++b) {
+    const int c = r.block_counts[(size_t)b * E + e];
+    r.block_counts[(size_t)b * E + e] = run;
+    run += c;
+  }
+}
+
+// Last launch: offsets, active list and tile table (stored by block 0), and the stable placement of each block's pairs:
+// experts ascending, pairs ascending within an expert.  `tokens` a block, `merged` blocks of the counts.  SUM: there was no second
+// launch, the block adds the counts itself.
+template <bool SUM>
+__global__ void __launch_bounds__(kRouteBlock) route_place_kernel(const int32_t* ids, int64_t P, int E, int k, int tokens, int merged,
+                                                                  int nblocks, int tile, RouteView r) {
   __shared__ int3 totals;
-  const int e = threadIdx.x;
-  const int tot = e < E ? strided_sum(r.block_counts + e, E, nblocks) : 0;
-  const int3 x = make_int3(tot, (tot + tile - 1) / tile, tot > 0 ? 1 : 0);
-  const int3 ex = block_scan3(x, &totals);
-  if (e < E) {
-    r.counts[e] = tot;
-    r.offsets[e] = ex.x;
-    if (tot > 0) {
-      r.active[ex.z] = e;
-      r.zidx[e] = ex.z;
-      int4* g = reinterpret_cast<int4*>(r.groups + (size_t)ex.z * kGroupInts);
-      g[0] = make_int4(e, ex.x, tot, 0);
-    }
-    for (int s = 0; s < x.y; ++s) {
-      r.tiles[3 * (ex.y + s)] = e;
-      r.tiles[3 * (ex.y + s) + 1] = ex.x + s * tile;
-      r.tiles[3 * (ex.y + s) + 2] = min(tile, tot - s * tile);
-    }
-    // starting position of block b's pairs of expert e
-    int run = ex.x, b = 0;
-    for (; b + 8 <= nblocks; b += 8) {
-      int t[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t[i] = r.block_counts[(size_t)(b + i) * E + e];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r.block_start[(size_t)(b + i) * E + e] = run;
-        run += t[i];
+  __shared__ int start[kMaxExperts], off[kMaxExperts], zid[kMaxExperts];
+  __shared__ __align__(16) unsigned short wc[kRouteBlock / 32][kMaxExperts];  // pairs per (warp, expert)
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+  if (tid == 0) pdl_launch_dependents();
+  zero_shared(&wc[0][0], sizeof(wc));
+  pdl_wait();
+  int tot = 0, before = 0;
+  if (tid < E) {
+    if (SUM) {
+#pragma unroll 8
+      for (int i = 0; i < nblocks; ++i) {
+        const int c = r.block_counts[(size_t)i * E + tid];
+        before += i < b * merged ? c : 0;
+        tot += c;
       }
-    }
-    for (; b < nblocks; ++b) {
-      const int c = r.block_counts[(size_t)b * E + e];
-      r.block_start[(size_t)b * E + e] = run;
-      run += c;
+    } else {
+      tot = r.counts[tid];
+      before = r.block_counts[(size_t)b * merged * E + tid];
     }
   }
-  if (threadIdx.x == 0) {
+  const int64_t p = (int64_t)b * tokens * k + tid;
+  const bool valid = tid < tokens * k && p < P;
+  const int e = valid ? ids[p] : -1;
+  const int3 ex = block_scan3(make_int3(tot, (tot + tile - 1) / tile, tot > 0 ? 1 : 0), &totals);
+  if (tid < E) {
+    start[tid] = ex.x + before;
+    off[tid] = ex.x;
+    zid[tid] = ex.z;
+    if (b == 0) {
+      r.counts[tid] = tot;
+      r.offsets[tid] = ex.x;
+      if (tot > 0) {
+        r.active[ex.z] = tid;
+        r.zidx[tid] = ex.z;
+        reinterpret_cast<int4*>(r.groups + (size_t)ex.z * kGroupInts)[0] = make_int4(tid, ex.x, tot, 0);
+      }
+      for (int s = 0; s * tile < tot; ++s) {
+        r.tiles[3 * (ex.y + s)] = tid;
+        r.tiles[3 * (ex.y + s) + 1] = ex.x + s * tile;
+        r.tiles[3 * (ex.y + s) + 2] = min(tile, tot - s * tile);
+      }
+    }
+  }
+  if (b == 0 && tid == 0) {
     r.offsets[E] = totals.x;
     r.meta[0] = totals.z;
     r.meta[1] = totals.y;
   }
-  __syncthreads();
-}
-
-// Stable placement of the pairs of block b: rank among equal experts = earlier pairs of
-// the block with the same expert (warp match + per-warp counts), in pair order.
-__device__ void block_scatter(const int32_t* ids, int64_t P, int E, int k, int b, const RouteView& r) {
-  __shared__ __align__(16) unsigned short wc[kRouteBlock / 32][kMaxExperts];  // pairs per (warp, expert)
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t p = (int64_t)b * kRouteBlock + tid;
-  const bool valid = tid < kRouteBlock && p < P;
-  const int e = valid ? ids[p] : -1;
-  zero_shared(&wc[0][0], sizeof(wc));
-  __syncthreads();
   const unsigned mask = __match_any_sync(0xFFFFFFFFu, e);
   const int rank_in_warp = __popc(mask & ((1u << lane) - 1u));
   if (valid && rank_in_warp == 0) wc[warp][e] = (unsigned short)__popc(mask);
   __syncthreads();
   if (valid) {
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += wc[w][e];
-    const int pos = r.block_start[(size_t)b * E + e] + before + rank_in_warp;
-    r.pair_list[pos] = (int)p;
-    r.pair_pos[p] = pos;
-    const int rank = pos - r.offsets[e];
-    if (rank < kGroupRows) r.groups[(size_t)r.zidx[e] * kGroupInts + 4 + rank] = (int)(p / k);
+    int at = start[e] + rank_in_warp;
+    for (int w = 0; w < warp; ++w) at += wc[w][e];
+    r.pair_list[at] = (int)p;
+    r.pair_pos[p] = at;
+    const int rank = at - off[e];
+    if (rank < kGroupRows) r.groups[(size_t)zid[e] * kGroupInts + 4 + rank] = (int)(p / k);
   }
-  __syncthreads();
 }
 
-__global__ void __launch_bounds__(kRouteBlock) route_count_kernel(const int32_t* ids, int64_t P, int E, RouteView r) {
-  block_count(ids, P, E, blockIdx.x, r.block_counts + (size_t)blockIdx.x * E);
-}
-__global__ void __launch_bounds__(kRouteBlock) route_scan_kernel(int E, int nblocks, int tile, RouteView r) {
-  scan_groups(r, E, nblocks, tile);
-}
-__global__ void __launch_bounds__(kRouteBlock) route_scatter_kernel(const int32_t* ids, int64_t P, int E, int k,
-                                                                    RouteView r) {
-  block_scatter(ids, P, E, k, blockIdx.x, r);
-}
-
-// Decode-sized routing (T*k <= kRouteBlock; T <= 32 without a rule): every phase in one CTA, with
+// Decode-sized routing (T*k <= kRouteBlock; T <= 32, or kRouteBySmall by a rule): every phase in one CTA, with
 // the histogram, the scan and the placement in shared memory; only the results go to device
-// memory.  BY: by a rule, a warp taking every 32nd token; min(T, 32) * E floats of dynamic shared memory.
-template <bool BY>
-__global__ void __launch_bounds__(kRouteBlock) route_small_kernel(const float* logits, int T, int E, int k,
+// memory.  BY: by a rule, of up to 32 BY experts; 0: without one.
+template <int BY>
+__global__ void __launch_bounds__(BY ? kMaxExperts : kRouteBlock) route_small_kernel(const float* logits, int T, int E, int k,
                                                                   int32_t* ids, float* wts, int tile, RouteView r,
                                                                   RouteRule rule) {
   __shared__ int s_ids[kRouteBlock];
@@ -216,9 +211,9 @@ __global__ void __launch_bounds__(kRouteBlock) route_small_kernel(const float* l
   zero_shared(&wc[0][0], sizeof(wc));
   pdl_wait();
   if constexpr (BY) {
-    extern __shared__ float cs[];
-    for (int t = warp; t < T; t += kRouteBlock / 32)
-      warp_route(rule, logits + (int64_t)t * E, E, k, cs + warp * E, ids + t * k, wts + t * k, s_ids + t * k);
+    __shared__ float cs[kRouteBySmall][32 * BY];
+    if (warp < T)
+      warp_route<BY>(rule, logits + (int64_t)warp * E, E, k, cs[warp], ids + warp * k, wts + warp * k, s_ids + warp * k, nullptr);
   } else {
     if (warp < T) warp_topk(logits + (int64_t)warp * E, E, k, ids + warp * k, wts + warp * k, s_ids + warp * k);
   }
@@ -283,50 +278,58 @@ RouteView route_view(void* ws, int64_t T, int E, int k) {
   v.groups = reinterpret_cast<int*>(b + L.groups);
   v.zidx = reinterpret_cast<int*>(b + L.zidx);
   v.block_counts = reinterpret_cast<int*>(b + L.block_counts);
-  v.block_start = reinterpret_cast<int*>(b + L.block_start);
   return v;
 }
 
-// The tables of pairs whose ids are on their way: counts, scan, placement.
-static void launch_group(const int32_t* ids, int64_t P, int E, int k, const RouteView& r, cudaStream_t s) {
-  const int64_t nb = (P + kRouteBlock - 1) / kRouteBlock;
-  route_count_kernel<<<(unsigned)nb, kRouteBlock, 0, s>>>(ids, P, E, r);
-  route_scan_kernel<<<1, kRouteBlock, 0, s>>>(E, (int)nb, kRouteTile, r);
-  route_scatter_kernel<<<(unsigned)nb, kRouteBlock, 0, s>>>(ids, P, E, k, r);
+// The large router: top-k and counts, the counts' sums where there are many blocks, placement.
+template <int S, bool BY>
+static int launch_large(const RouteRule& rule, const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts,
+                        const RouteView& r, cudaStream_t s) {
+  const int tokens = route_block_tokens(T, k), place = route_place_tokens(T, k), merged = place / tokens;
+  const int nb = (int)((T + tokens - 1) / tokens), np = (int)((T + place - 1) / place);
+  const int64_t P = T * k;
+  if (launch_pdl(route_topk_kernel<S, BY>, dim3(nb), dim3(256), 0, s, logits, T, E, k, tokens, ids, wts, r, rule) != cudaSuccess)
+    return QG_ERR_CUDA;
+  // up to 16 blocks' counts every placing block adds in less time than a launch takes
+  if (nb <= 16) {
+    if (launch_pdl(route_place_kernel<true>, dim3(np), dim3(kRouteBlock), 0, s, ids, P, E, k, place, merged, nb, (int)kRouteTile, r) !=
+        cudaSuccess)
+      return QG_ERR_CUDA;
+  } else if (launch_pdl(route_prefix_kernel, dim3((E + 31) / 32), dim3(1024), 0, s, E, nb, r) != cudaSuccess ||
+             launch_pdl(route_place_kernel<false>, dim3(np), dim3(kRouteBlock), 0, s, ids, P, E, k, place, merged, nb, (int)kRouteTile,
+                        r) != cudaSuccess) {
+    return QG_ERR_CUDA;
+  }
+  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
 int launch_route(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RouteView r = route_view(ws, T, E, k);
-  const int64_t P = T * k;
-  if (P <= kRouteBlock && T <= 32) {
-    if (launch_pdl(route_small_kernel<false>, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts,
-                   (int)kRouteTile, r, RouteRule()) != cudaSuccess)
-      return QG_ERR_CUDA;
-  } else {
-    route_topk_kernel<<<(unsigned)((T + 7) / 8), 256, 0, s>>>(logits, T, E, k, ids, wts);
-    launch_group(ids, P, E, k, r, s);
-  }
-  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+  if (T * k > kRouteBlock || T > 32) return launch_large<16, false>(RouteRule(), logits, T, E, k, ids, wts, r, s);
+  return launch_pdl(route_small_kernel<0>, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r,
+                    RouteRule()) == cudaSuccess && cudaGetLastError() == cudaSuccess
+             ? QG_OK
+             : QG_ERR_CUDA;
+}
+
+template <int S>
+static int launch_by(const RouteRule& rule, const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts,
+                     const RouteView& r, cudaStream_t s) {
+  // by a rule a token takes a warp some 3 us, and one SM's warps share its issue slots: more tokens go to more SMs
+  if (T > kRouteBySmall) return launch_large<S, true>(rule, logits, T, E, k, ids, wts, r, s);
+  return launch_pdl(route_small_kernel<S>, dim3(1), dim3(kMaxExperts), 0, s, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r,
+                    rule) == cudaSuccess && cudaGetLastError() == cudaSuccess
+             ? QG_OK
+             : QG_ERR_CUDA;
 }
 
 int launch_route_by(const RouteRule& rule, const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws,
                     void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RouteView r = route_view(ws, T, E, k);
-  const int64_t P = T * k;
-  if (P <= kRouteBlock && T <= 128) {
-    const size_t smem = sizeof(float) * std::min<int64_t>(T, kRouteBlock / 32) * E;
-    if (cudaFuncSetAttribute(route_small_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(sizeof(float) * kRouteBlock / 32 * kMaxExperts)) != cudaSuccess ||
-        launch_pdl(route_small_kernel<true>, dim3(1), dim3(kRouteBlock), smem, s, logits, (int)T, E, k, ids, wts,
-                   (int)kRouteTile, r, rule) != cudaSuccess)
-      return QG_ERR_CUDA;
-  } else {
-    route_topk_by_kernel<<<(unsigned)((T + 7) / 8), 256, 0, s>>>(rule, logits, T, E, k, ids, wts);
-    launch_group(ids, P, E, k, r, s);
-  }
-  return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
+  return E <= 128 ? launch_by<4>(rule, logits, T, E, k, ids, wts, r, s)
+         : E <= 256 ? launch_by<8>(rule, logits, T, E, k, ids, wts, r, s) : launch_by<16>(rule, logits, T, E, k, ids, wts, r, s);
 }
 
 }  // namespace qg
