@@ -276,7 +276,7 @@ qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
  *     h = a_e x[i]              (rank_e sums over k, fp32)
  *     out[i][n] = bf16( y[i][n] + scales[e] * sum_j b_e[n][j] * h_j )        (fp32, rounded once)
  * ids[i] = -1: no adapter, out[i] = y[i].  Rows of one adapter may lie anywhere; its weights are
- * read once for 16 of them (64 where there are more than 256 rows).  Elements of a and b past an adapter's rank, whatever their
+ * read once for 16 of them (128 where there are more than 256 rows).  Elements of a and b past an adapter's rank, whatever their
  * bits, do not enter. */
 typedef struct {
   int32_t n_adapters;     /* 1 .. 1024 */
@@ -299,8 +299,11 @@ size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
  * ids and ranks are checked on the device: an id outside -1 .. n_adapters-1 or a rank outside
  * 0 .. max_rank counts as no adapter and puts QG_ERR_INVALID_ARG into the workspace's status word
  * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^30, the leading
- * dimensions below 2^31.  The workspace need not be zero-filled but for its status word; calls that overlap on the GPU must not share it.
- * Deterministic; one launch for up to 256 rows, two more for every 16384 of more rows. */
+ * dimensions below 2^31.  The workspace must be zero-filled before its first use and after QG_ERR_TIMEOUT; every
+ * other qlora call, of any sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not
+ * share it, and no other entry point may use it in between.  More than 256 rows need a GPU of 96 SMs or more
+ * (QG_ERR_UNSUPPORTED otherwise) and run on all of its SMs at once, so such a call starts when no other kernel holds one.
+ * Deterministic; one launch for up to 256 rows, one for every 16384 of more. */
 qg_status qlora(const qg_lora* lora, const int32_t* ids, int64_t m_rows, const void* x, int64_t ldx, const void* y,
                 int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -18,7 +18,8 @@ extern "C" size_t qlora_workspace_size(const qg_lora* l, int64_t m) {
     return 0;
   if (m <= kLoraFewRows) return kWsHeader;
   DeviceInfo dev;
-  return current_device_info(&dev) ? kWsHeader + lora_rows_bytes(l->n_adapters, l->max_rank, m, dev) : 0;
+  if (!current_device_info(&dev)) return 0;
+  return kWsHeader + (dev.sms < kLoraMinSms ? 0 : lora_rows_bytes(l->n_adapters, l->max_rank, m, dev));
 }
 
 extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, const void* x, int64_t ldx, const void* y,
@@ -59,6 +60,7 @@ extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, cons
   p.ldo = (int)ldo;
   p.status = static_cast<int*>(workspace);
   if (m <= kLoraFewRows) return (qg_status)launch_lora(p, dev, stream);
+  if (dev.sms < kLoraMinSms) return QG_ERR_UNSUPPORTED;
   if (workspace_bytes < kWsHeader + lora_rows_bytes(l->n_adapters, l->max_rank, m, dev)) return QG_ERR_WORKSPACE_TOO_SMALL;
   return (qg_status)launch_lora_rows(p, dev, static_cast<char*>(workspace) + kWsHeader, stream);
 }

@@ -24,8 +24,9 @@ struct LoraArgs {
   int ldx, ldy, ldo;
   int* status;
 };
-constexpr int64_t kLoraFewRows = 256;       // at most: one launch of clusters (lora.cu); more: shrink and expand (lora_rows.cu)
-constexpr int64_t kLoraRowsAtOnce = 16384;  // of a call of many rows: what a CTA counts and lists itself
+constexpr int64_t kLoraFewRows = 256;       // at most: one launch of clusters (lora.cu); more: lora_rows.cu
+constexpr int64_t kLoraRowsAtOnce = 16384;  // in one launch of many rows: what a CTA looks through itself
+constexpr int kLoraMinSms = 96;             // of lora_rows.cu: fewer SMs' CTAs would have more tiles each than they list
 int launch_lora(const LoraArgs& a, const DeviceInfo& dev, void* stream);
 // Scratch of the many-row form for h's parts, and its launches.
 size_t lora_rows_bytes(int n_adapters, int max_rank, int64_t m, const DeviceInfo& dev);

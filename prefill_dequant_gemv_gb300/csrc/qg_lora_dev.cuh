@@ -104,41 +104,24 @@ template <int THREADS>
 struct Tiles {
   int first[kLoraMaxAdapters + 2];
   int warp_sums[THREADS / 32];
-  int bin;
 
-  // The rows that this warp looks at, 32 at a time: a run of whole 32s.
-  static __device__ __forceinline__ void share(const LoraArgs& p, int* i0, int* i1) {
-    const int per = ((p.m + 31) / 32 + THREADS / 32 - 1) / (THREADS / 32) * 32;
-    *i0 = min(p.m, (int)(threadIdx.x >> 5) * per);
-    *i1 = min(p.m, *i0 + per);
-  }
-  // Bins of kLoads x 32 rows from i, -1 past the warp's rows; all loads before the first use.
-  static constexpr int kLoads = 8;
-  static __device__ __forceinline__ void load(const LoraArgs& p, int i, int i1, int (&e)[kLoads], bool* bad) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) e[u] = i + 32 * u + lane < i1 ? p.ids[i + 32 * u + lane] : -2;
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const bool in = i + 32 * u + lane < i1;
-      *bad |= in && (e[u] < -1 || e[u] >= p.n_adapters);
-      e[u] = in ? bin_of(e[u], p.n_adapters) : -1;
-    }
-  }
-
-  __device__ __forceinline__ void count(const LoraArgs& p, int T) {
+  // Also notes every row's bin.  A warp has every THREADS / 32nd run of 32 rows; eight runs' loads before the first use.
+  __device__ __forceinline__ void count(const LoraArgs& p, int T, uint16_t* bins_of_rows) {
     const int tid = threadIdx.x, lane = tid & 31, bins = p.n_adapters + 1;
     for (int e = tid; e <= bins; e += THREADS) first[e] = 0;
     __syncthreads();
-    int i0, i1;
-    share(p, &i0, &i1);
     bool bad = false;
-    for (int i = i0; i < i1; i += 32 * kLoads) {
-      int e[kLoads];
-      load(p, i, i1, e, &bad);
+    for (int i0 = tid; i0 - lane < p.m; i0 += 8 * THREADS) {
+      int e[8];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        if (i + 32 * u >= i1) break;
+      for (int u = 0; u < 8; ++u) e[u] = i0 + u * THREADS < p.m ? p.ids[i0 + u * THREADS] : -1;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * THREADS;
+        if (i - lane >= p.m) break;
+        bad |= e[u] < -1 || e[u] >= p.n_adapters;
+        e[u] = i < p.m ? bin_of(e[u], p.n_adapters) : -1;
+        if (i < p.m) bins_of_rows[i] = (uint16_t)e[u];
         const unsigned same = __match_any_sync(0xFFFFFFFFu, e[u]);
         if (e[u] >= 0 && lane == __ffs(same) - 1) atomicAdd(&first[e[u]], __popc(same));  // integer counts: order-free
       }
@@ -163,43 +146,6 @@ struct Tiles {
       }
     if (tid == 0) first[bins] = total;
     __syncthreads();
-  }
-
-  // Tile's adapter (the return value) and rows, in ascending order, -1 past the last.
-  __device__ __forceinline__ int collect(const LoraArgs& p, int T, int tile, int* rows) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bins = p.n_adapters + 1;
-    for (int e = tid; e < bins; e += THREADS)
-      if (first[e] <= tile && tile < first[e + 1]) bin = e;
-    for (int i = tid; i < T; i += THREADS) rows[i] = -1;
-    __syncthreads();
-    const int e = bin, skip = (tile - first[e]) * T;
-    int i0, i1, mine = 0;
-    share(p, &i0, &i1);
-    bool bad = false;
-    for (int i = i0; i < i1; i += 32 * kLoads) {
-      int v[kLoads];
-      load(p, i, i1, v, &bad);
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u) mine += __popc(__ballot_sync(0xFFFFFFFFu, v[u] == e));
-    }
-    if (lane == 0) warp_sums[warp] = mine;
-    __syncthreads();
-    int at = -skip;
-    for (int w = 0; w < warp; ++w) at += warp_sums[w];
-    if (at < T && at + mine > 0)
-      for (int i = i0; i < i1 && at < T; i += 32 * kLoads) {
-        int v[kLoads];
-        load(p, i, i1, v, &bad);
-#pragma unroll
-        for (int u = 0; u < kLoads; ++u) {
-          const unsigned hit = __ballot_sync(0xFFFFFFFFu, v[u] == e);
-          const int to = at + __popc(hit & ((1u << lane) - 1u));
-          if (v[u] == e && to >= 0 && to < T) rows[to] = i + 32 * u + lane;
-          at += __popc(hit);
-        }
-      }
-    __syncthreads();
-    return e;
   }
 };
 
