@@ -298,7 +298,7 @@ size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
  * y itself with the same stride: rows without an adapter, or whose adapter has rank 0, are then not touched; no other overlap.
  * ids and ranks are checked on the device: an id outside -1 .. n_adapters-1 or a rank outside
  * 0 .. max_rank counts as no adapter and puts QG_ERR_INVALID_ARG into the workspace's status word
- * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^30, the leading
+ * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^24, the leading
  * dimensions below 2^31.  The workspace must be zero-filled before its first use and after QG_ERR_TIMEOUT; every
  * other qlora call, of any sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not
  * share it, and no other entry point may use it in between.  More than 256 rows need a GPU of 96 SMs or more

@@ -115,10 +115,10 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
     __syncthreads();
     // phase 1 in steps of 64 inputs, phase 2 in chunks of kOuts outputs: this warp's
     const int half = warp % S::kHalves, group = warp / S::kHalves, rank0 = half * S::kRanks;
-    const int steps = ra ? (p.k + 63) / 64 : 0, groups = n_cta * S::kGroups, me = rank * S::kGroups + group;
-    const int s0 = (int)((int64_t)steps * me / groups), n1 = (int)((int64_t)steps * (me + 1) / groups) - s0;
+    const int steps = ra ? (p.k + 63) / 64 : 0, groups = (int)n_cta * S::kGroups, me = (int)rank * S::kGroups + group;
+    const int s0 = steps * me / groups, n1 = steps * (me + 1) / groups - s0;
     const int chunks = (p.n + S::kOuts - 1) / S::kOuts;
-    const int c0 = (int)((int64_t)chunks * rank / n_cta), c1 = (int)((int64_t)chunks * (rank + 1) / n_cta);
+    const int c0 = chunks * (int)rank / (int)n_cta, c1 = chunks * ((int)rank + 1) / (int)n_cta;
     const int n2 = c0 + warp < c1 ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0, n = n1 + n2;
     // The copies' state.  A lane copies piece lane % 8 of every fourth row of x, A and y, so that a copy takes whole lines; and
     // of B, whose rows are shorter or longer, every 32nd piece.  A pointer may run past its row's end, or stand on a row that is

@@ -26,7 +26,7 @@ extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, cons
                            int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
   if (!l || m < 0 || l->n_adapters < 1 || l->max_rank < 1 || l->n < 1 || l->k < 1) return QG_ERR_INVALID_ARG;
   if (l->n_adapters > kLoraMaxAdapters || l->max_rank > kLoraMaxRank || l->max_rank % 8 || m >= (1 << 27) ||
-      l->n >= (1 << 30) || l->k >= (1 << 30))
+      l->n >= (1 << 24) || l->k >= (1 << 24))
     return QG_ERR_UNSUPPORTED;
   if (m == 0) return QG_OK;
   if (!l->a || !l->b || !l->scales || !ids || !x || !y || !out || !workspace) return QG_ERR_INVALID_ARG;

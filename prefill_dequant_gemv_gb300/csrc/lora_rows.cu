@@ -6,11 +6,10 @@
 // tiles' inputs (shrink) or outputs (expand), cut into chunks of 128, form one line of units that the
 // CTAs share evenly whatever the sizes: a CTA's range may begin and end inside a
 // tile.  In shrink that leaves a tile's h in parts, one for every CTA on it; CTA c's part of tile
-// t is number c + t (each step along the line raises one of the two).  The CTA whose part comes last
-// adds the tile's parts in that order, so results do not depend on timing, splits the sums into two bf16 terms and
-// raises the tile's flag; expand waits for the flags of its own tiles only (all CTAs run at once, and none waits before its
-// share of shrink is done).  A grid of its own for expand would start some 8 us later: two launches' ends, starts and
-// looks at the ids (7 prompts of 571 rows, rank 16: 44 us in two launches).
+// t is number c + t (each step along the line raises one of the two); a CTA that begins a tile in
+// expand adds the tile's parts in that order once all are there, so results do not depend on timing.  It waits for its
+// own tiles only (all CTAs run at once, and none waits before its share of shrink is done); y and B of its first chunks
+// are on their way meanwhile.
 //
 // Rows may lie anywhere: the operands are copied 16 bytes a thread (cp.async), some chunks ahead,
 // what lies past a row's end or an adapter's rank as zeros, into the 128-byte swizzled layout that
@@ -29,6 +28,7 @@ namespace {
 constexpr int T = 128;      // rows of a tile
 constexpr int kWidth = 128;  // inputs or outputs of a chunk
 constexpr int kList = 16;    // tiles of a CTA in either phase
+constexpr int kStart = 4;    // chunks of expand that take as long as a tile's h
 constexpr uint32_t kAtom = T * 128;  // bytes of 128 rows of 64 bf16
 
 // A bounded wait with one answer for the warp.
@@ -47,13 +47,23 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&v)[16]) 
       : "r"(taddr));
 }
 
-// The line of units: CTA c's range, and the CTA of a unit.  Never more CTAs than units.
-__device__ __forceinline__ int64_t line_begin(int64_t units, int ctas, int c) { return units * c / ctas; }
-__device__ __forceinline__ int line_owner(int64_t units, int ctas, int64_t u) { return (int)(((u + 1) * ctas - 1) / units); }
-// Shrink's CTAs on the line: a tile of few goes into about eight parts at most, as one CTA adds them all.
-__device__ __forceinline__ int shrink_ctas(int64_t units, int n_tiles, int grid) { return (int)min(units, (int64_t)min(grid, 8 * n_tiles)); }
+// The line of `units` shared by `ctas` CTAs, the first `more` of which have one more than `each`; never more CTAs than units.
+// (32 bits: a 64-bit division takes some 600 clocks.)
+struct Line {
+  int ctas, each, more;
+  __device__ __forceinline__ Line(int units, int most) {
+    ctas = min(units, most);
+    each = ctas ? units / ctas : 0;
+    more = units - each * ctas;
+  }
+  __device__ __forceinline__ int begin(int c) const { return c < ctas ? c * each + min(c, more) : ctas * each + more; }
+  __device__ __forceinline__ int owner(int u) const {
+    const int wide = more * (each + 1);
+    return u < wide ? u / (each + 1) : more + (u - wide) / each;
+  }
+};
 
-// A tile: its rows (past the last the first again: what is computed of them is not stored), how many, adapter, rank.
+// A tile: its rows, how many, adapter, rank.
 struct Tile {
   int rows[T];
   int live, bin, rank, pad;
@@ -64,10 +74,8 @@ __device__ __forceinline__ int up16(int rank) { return (rank + 15) & ~15; }
 // What the CTAs hand one another (device memory; the counters are zero between calls).
 struct Scratch {
   int* done;      // CTAs that have ended
-  int* tickets;   // [tile] parts that are there
-  int* flags;     // [tile] 1: its h is there
+  int* tickets;   // [tile] warps whose share of a part is there, eight a part
   float* parts;   // [CTA + tile][T][pitch]
-  uint8_t* h;     // [tile][term][ATOMS][T][128 bytes], as the MMAs read it
   int pitch;      // max_rank rounded up to 16
 };
 
@@ -90,36 +98,12 @@ struct Shape {
   static_assert(kShrink >= 2 * kLoraRowsAtOnce, "the rows' bins lie there first");
 };
 
-// One warp lists a tile's rows, in ascending order, from the bins of all rows.
-__device__ __forceinline__ void list_tile(const LoraArgs& p, const int* first, const uint16_t* bins, int tile, Tile& to) {
-  const int lane = threadIdx.x & 31;
-  int e = 0;  // the last with first[e] <= tile: those without tiles share their successor's first
+// The bin that a tile belongs to: the last with first[e] <= tile (those without tiles share their successor's first).
+__device__ __forceinline__ int bin_of_tile(const int* first, int n_adapters, int tile) {
+  int e = 0;
   for (int step = 1024; step; step >>= 1)
-    if (e + step <= p.n_adapters && first[e + step] <= tile) e += step;
-  const int skip = (tile - first[e]) * T;
-  int at = -skip;
-  for (int i = 0; i < p.m && at < T; i += 128) {
-    int v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = i + 32 * u + lane < p.m ? bins[i + 32 * u + lane] : -1;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const unsigned hit = __ballot_sync(0xFFFFFFFFu, v[u] == e);
-      const int place = at + __popc(hit & ((1u << lane) - 1u));
-      if (v[u] == e && place >= 0 && place < T) to.rows[place] = i + 32 * u + lane;
-      at += __popc(hit);
-    }
-  }
-  const int live = min(at, T);
-  __syncwarp();
-  const int row0 = to.rows[0];
-  for (int i = live + lane; i < T; i += 32) to.rows[i] = row0;
-  if (lane == 0) {
-    to.live = live;
-    to.bin = e;
-    to.rank = rank_of(p, e);
-  }
-  __syncwarp();
+    if (e + step <= n_adapters && first[e + step] <= tile) e += step;
+  return e;
 }
 
 __device__ __forceinline__ int load_acquire(const int* p) {
@@ -127,16 +111,16 @@ __device__ __forceinline__ int load_acquire(const int* p) {
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void store_release(int* p, int v) {
-  asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+__device__ __forceinline__ void red_release(int* p, int v) {
+  asm volatile("red.release.gpu.global.add.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
 }
-// Waits, up to the limit, for a tile's flag; one answer for the warp.
-__device__ __forceinline__ bool wait_flag(const int* flag, int* status) {
+// Waits, up to the limit, for a counter to reach n; one answer for the warp.
+__device__ __forceinline__ bool wait_count(const int* counter, int n, int* status) {
   bool up = false;
   if ((threadIdx.x & 31) == 0) {
     const unsigned long long t0 = global_ns();
-    while (!(up = load_acquire(flag) != 0)) {
-      __nanosleep(100);
+    while (!(up = load_acquire(counter) >= n)) {
+      __nanosleep(64);
       if (global_ns() - t0 > kWaitLimitNs) {
         atomicExch(status, kStatusTimeout);
         break;
@@ -144,7 +128,7 @@ __device__ __forceinline__ bool wait_flag(const int* flag, int* status) {
     }
   }
   up = __any_sync(0xFFFFFFFFu, up);
-  __syncwarp();  // what the flag stands for is there for every lane
+  __syncwarp();  // what the counter stands for is there for every lane
   return up;
 }
 
@@ -157,7 +141,7 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
   __shared__ uint64_t full[S::kStages], empty[S::kStages], sum_full[2], sum_empty[2];
   __shared__ uint64_t b_full[S::kAhead], d_full[2], d_empty[2], h_full, ring_free, fin;
   __shared__ uint32_t tmem_slot;
-  __shared__ int last_part, last_cta;
+  __shared__ int last_cta;
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, c = blockIdx.x;
@@ -173,7 +157,7 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
       mbar_init(&d_empty[i], S::kWarps);
     }
     for (int i = 0; i < S::kAhead; ++i) mbar_init(&b_full[i], 32 * S::kWarps);
-    mbar_init(&h_full, 32 * S::kWarps);
+    mbar_init(&h_full, S::kWarps);
     mbar_init(&ring_free, 1);
     mbar_init(&fin, 1);
     fence_mbar_init();
@@ -187,17 +171,61 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
   tl.count(p, T, bins);
   const int n_adapter = tl.first[p.n_adapters], n_tiles = tl.first[p.n_adapters + 1];  // tiles with an adapter, which come first, and all
   const int k_chunks = (p.k + kWidth - 1) / kWidth, n_chunks = (p.n + kWidth - 1) / kWidth;
-  const int64_t k_units = (int64_t)n_adapter * k_chunks, n_units = (int64_t)n_tiles * n_chunks;
-  const int k_ctas = shrink_ctas(k_units, n_adapter, gridDim.x), n_ctas = (int)min((int64_t)gridDim.x, n_units);
-  const int64_t ku0 = c < k_ctas ? line_begin(k_units, k_ctas, c) : 0, ku1 = c < k_ctas ? line_begin(k_units, k_ctas, c + 1) : 0;
-  const int64_t nu0 = c < n_ctas ? line_begin(n_units, n_ctas, c) : 0, nu1 = c < n_ctas ? line_begin(n_units, n_ctas, c + 1) : 0;
-  const int kt0 = (int)(ku0 / k_chunks), kt1 = ku1 > ku0 ? (int)((ku1 - 1) / k_chunks) + 1 : kt0;
-  const int nt0 = (int)(nu0 / n_chunks), nt1 = nu1 > nu0 ? (int)((nu1 - 1) / n_chunks) + 1 : nt0;
-  for (int i = warp; i < (kt1 - kt0) + (nt1 - nt0); i += S::kWarps + 1)
-    if (i < kt1 - kt0)
-      list_tile(p, tl.first, bins, kt0 + i, in_list[i]);
-    else
-      list_tile(p, tl.first, bins, nt0 + i - (kt1 - kt0), out_list[i - (kt1 - kt0)]);
+  // In shrink a tile of few goes into about eight parts at most, as one CTA adds them all.  In expand a tile begins with kStart units
+  // of no chunk: the time that its h takes.
+  const Line in_line(n_adapter * k_chunks, min((int)gridDim.x, 8 * n_adapter)), out_line(n_tiles * (n_chunks + kStart), gridDim.x);
+  const int ku0 = in_line.begin(c), ku1 = in_line.begin(c + 1), kt0 = ku0 / k_chunks, kt1 = ku1 > ku0 ? (ku1 - 1) / k_chunks + 1 : kt0;
+  const int nu0 = out_line.begin(c), nu1 = out_line.begin(c + 1);
+  int nt0 = nu0 / (n_chunks + kStart), ch = max(0, nu0 - nt0 * (n_chunks + kStart) - kStart);  // expand's first tile and chunk
+  const int nt_last = nu1 / (n_chunks + kStart), ch_last = max(0, nu1 - nt_last * (n_chunks + kStart) - kStart);
+  const int nt1 = nt_last + (ch_last > 0), n = (nt_last - nt0) * n_chunks + ch_last - ch;  // past its last tile; its chunks
+  // Each adapter's rows in ascending order to the places that they have in this CTA's tiles: every warp looks through a run of
+  // rows, counts first, as the place of its rows hangs on the runs before.
+  const int run = (p.m / 32 + S::kWarps + 1) / (S::kWarps + 1) * 32, i0 = min(p.m, warp * run), i1 = min(p.m, i0 + run);
+  auto list_adapter = [&](int e) {
+    int mine = 0;
+    for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < i1 && bins[i + lane] == e));
+    __syncthreads();
+    if (lane == 0) tl.warp_sums[warp] = mine;
+    __syncthreads();
+    int at = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < S::kWarps + 1; ++w) {
+      at += w < warp ? tl.warp_sums[w] : 0;
+      total += tl.warp_sums[w];
+    }
+    const int first = tl.first[e];
+    if (mine)
+      for (int i = i0; i < i1; i += 32) {
+        const bool hit = i + lane < i1 && bins[i + lane] == e;
+        const unsigned hits = __ballot_sync(0xFFFFFFFFu, hit);
+        const int place = at + __popc(hits & ((1u << lane) - 1u)), tile = first + place / T;
+        if (hit && tile >= kt0 && tile < kt1) in_list[tile - kt0].rows[place % T] = i + lane;
+        if (hit && tile >= nt0 && tile < nt1) out_list[tile - nt0].rows[place % T] = i + lane;
+        at += __popc(hits);
+      }
+    const int rank = tl.rank[e];
+    if (tid < kt1 - kt0 || (tid >= 32 && tid - 32 < nt1 - nt0)) {
+      const int tile = tid < 32 ? kt0 + tid : nt0 + tid - 32, left = total - (tile - first) * T;
+      Tile& to = tid < 32 ? in_list[tid] : out_list[tid - 32];
+      if (tile >= first && left > 0) {
+        to.live = min(left, T);
+        to.bin = e;
+        to.rank = rank;
+      }
+    }
+  };
+  for (int i = tid; i < kList * T; i += S::kThreads) in_list[i / T].rows[i % T] = out_list[i / T].rows[i % T] = 0;  // past the last: any row
+  for (int t = kt0; t < kt1;) {
+    const int e = bin_of_tile(tl.first, p.n_adapters, t);
+    list_adapter(e);
+    t = tl.first[e + 1];
+  }
+  for (int t = nt0; t < nt1;) {
+    const int e = bin_of_tile(tl.first, p.n_adapters, t);
+    if (tl.first[e] >= kt1 || tl.first[e + 1] <= kt0) list_adapter(e);  // not listed yet
+    t = tl.first[e + 1];
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -214,8 +242,7 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
       if (ra == 0) {  // no h; its flag is not waited for
         continue;
       }
-      const int k0 = (int)(max(ku0, (int64_t)tile * k_chunks) - (int64_t)tile * k_chunks);
-      const int k1 = (int)(min(ku1, (int64_t)(tile + 1) * k_chunks) - (int64_t)tile * k_chunks);
+      const int k0 = max(ku0 - tile * k_chunks, 0), k1 = min(ku1 - tile * k_chunks, k_chunks);
       if (warp < 8) {  // copies: a thread has one of a row's 16 pieces and every 16th row
         const int piece = tid & 15, r0 = tid >> 4;
         int col = k0 * kWidth + 8 * piece;
@@ -273,12 +300,9 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
       } else {  // h's part: lane = row, 16 ranks a warp in turns; of the last part's CTA all of h
         const int buf = sums & 1, quad = warp & 3;
         ok = ok && wait_warp(&sum_full[buf], sums / 2, p.status);
-        const int p0 = line_owner(k_units, k_ctas, (int64_t)tile * k_chunks),
-                  p1 = line_owner(k_units, k_ctas, (int64_t)(tile + 1) * k_chunks - 1);
-        const int64_t step = (int64_t)T * sc.pitch;
         if (ok) {
           tc_fence_after();
-          float* to = sc.parts + (c + tile) * step + (quad * 32 + lane) * sc.pitch;
+          float* to = sc.parts + ((int64_t)(c + tile) * T + quad * 32 + lane) * sc.pitch;
           for (int j = (warp >> 2 & 1) * 16; j < ra; j += 32) {
             uint32_t v[16];
             tmem_ld16(tmem + (quad << 21) + buf * S::kRank + j, v);
@@ -289,55 +313,20 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sum_empty[buf]);
+          if (lane == 0) {
+            mbar_arrive(&sum_empty[buf]);
+            red_release(&sc.tickets[tile], 1);
+          }
         }
         ++sums;
-        __threadfence();
-        named_sync(1, 256);
-        if (tid == 256) last_part = ok && ticket_add(&sc.tickets[tile], 1) == p1 - p0;
-        named_sync(1, 256);
-        if (last_part) {
-          __threadfence();
-          const int pieces = up16(ra) / 8;
-          const float scale = p.scales[b.bin];
-          for (int x = tid - 256; x < T * pieces; x += 256) {
-            const int row = x / pieces, pc = x - row * pieces;
-            const float* from = sc.parts + (p0 + tile) * step + row * sc.pitch + 8 * pc;
-            float v[8] = {};
-            for (int q = p0; q <= p1; q += 4) {  // four parts' loads at a time
-              float4 a[4][2];
-#pragma unroll
-              for (int y = 0; y < 4; ++y)
-#pragma unroll
-                for (int z = 0; z < 2; ++z)
-                  a[y][z] = q + y <= p1 ? __ldcg(reinterpret_cast<const float4*>(from + (q - p0 + y) * step) + z)
-                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                v[0] += a[y][0].x, v[1] += a[y][0].y, v[2] += a[y][0].z, v[3] += a[y][0].w;
-                v[4] += a[y][1].x, v[5] += a[y][1].y, v[6] += a[y][1].z, v[7] += a[y][1].w;
-              }
-            }
-            uint4 top, rest;
-            split_h(v, scale, ra - 8 * pc, top, rest);
-            uint8_t* to = sc.h + (int64_t)tile * 2 * S::kTerm + (pc >> 3) * kAtom + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
-            __stcg(reinterpret_cast<uint4*>(to), top);
-            __stcg(reinterpret_cast<uint4*>(to + S::kTerm), rest);
-          }
-          __threadfence();
-          named_sync(1, 256);
-          if (tid == 256) store_release(&sc.flags[tile], 1);
-        }
       }
     }
   }
-
   if (tid == 32 * S::kWarps) mma_commit(&ring_free);  // every MMA that reads shrink's ring has ended
 
   // ---------------------------------------------------------------- expand
   const uint32_t hs = base, bs = hs + 2 * S::kTerm, ys = bs + S::kAhead * S::kB;
-  const int n = (int)(nu1 - nu0);
-  int i = 0, ch = (int)(nu0 % n_chunks), mm = 0;  // tile, chunk, chunks multiplied so far
+  int i = 0, mm = 0;  // tile, chunks multiplied so far
   if (warp == S::kWarps) {  // MMAs: h's rows, both terms, by B's
     if (lane == 0) {
       // the sums of shrink have left tensor memory
@@ -441,16 +430,39 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
 #pragma unroll
         for (int m = 0; m < 4; ++m) op[m] = p.out + (int64_t)b.rows[row0 + 8 * m] * p.ldo + nb + 8 * t;
         if (ra) {  // h's terms; the last tile's MMAs have ended, as this warp has had their sums
-          ok = wait_flag(&sc.flags[nt0 + i], p.status);
+          const int tile = nt0 + i, pieces = up16(ra) / 8;
+          const int p0 = in_line.owner(tile * k_chunks), n_parts = in_line.owner((tile + 1) * k_chunks - 1) - p0 + 1;
+          const int64_t step = (int64_t)T * sc.pitch;
+          const float scale = p.scales[b.bin];
+          ok = wait_count(&sc.tickets[tile], 8 * n_parts, p.status);
           if (!ok) break;
-          const uint8_t* from = sc.h + (int64_t)(nt0 + i) * 2 * S::kTerm;
-          const int pieces = up16(ra) / 8;
-          for (int x = tid; x < 2 * T * pieces; x += 32 * S::kWarps) {
-            const int row = x / pieces, pc = x - row * pieces;  // rows of the first term, then of the second
-            const uint32_t at = (row >> 7) * S::kTerm + (pc >> 3) * kAtom + (row & 127) * 128 + (((pc & 7) ^ (row & 7)) << 4);
-            copy16(hs + at, from + at, 16);
+          for (int x = tid; x < T * pieces; x += 32 * S::kWarps) {
+            const int row = x / pieces, pc = x - row * pieces;
+            const float* from = sc.parts + (p0 + tile) * step + row * sc.pitch + 8 * pc;
+            float v[8] = {};
+            for (int q = 0; q < n_parts; q += 4) {  // four parts' loads at a time
+              float4 a[4][2];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                  a[y][z] = q + y < n_parts ? __ldcg(reinterpret_cast<const float4*>(from + (q + y) * step) + z)
+                                            : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                v[0] += a[y][0].x, v[1] += a[y][0].y, v[2] += a[y][0].z, v[3] += a[y][0].w;
+                v[4] += a[y][1].x, v[5] += a[y][1].y, v[6] += a[y][1].z, v[7] += a[y][1].w;
+              }
+            }
+            uint4 top, rest;
+            split_h(v, scale, ra - 8 * pc, top, rest);
+            uint8_t* to = smem + (pc >> 3) * kAtom + row * 128 + (((pc & 7) ^ (row & 7)) << 4);
+            *reinterpret_cast<uint4*>(to) = top;
+            *reinterpret_cast<uint4*>(to + S::kTerm) = rest;
           }
-          cp_async_arrive_noinc(&h_full);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&h_full);
         }
       }
       const int buf = mm & 1, left = p.n - nb - 8 * t;
@@ -512,14 +524,14 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
   if (tid == 0) last_cta = ticket_add(sc.done, 1) == (int)gridDim.x - 1;
   __syncthreads();
   if (last_cta) {
-    for (int x = tid; x < n_adapter; x += S::kThreads) sc.tickets[x] = sc.flags[x] = 0;
+    for (int x = tid; x < n_adapter; x += S::kThreads) sc.tickets[x] = 0;
     if (tid == 0) *sc.done = 0;
   }
 }
 
-// The scratch after the status word: counters, then h's parts and h.
+// The scratch after the status word: counters, then h's parts.
 struct Layout {
-  size_t tickets, flags, parts, h, total;
+  size_t tickets, parts, total;
   int pitch;
   Layout(int n_adapters, int max_rank, int64_t m, const DeviceInfo& dev) {
     const int64_t rows = std::min<int64_t>(m, kLoraRowsAtOnce);
@@ -527,10 +539,8 @@ struct Layout {
     pitch = (max_rank + 15) / 16 * 16;
     const auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     tickets = 256;  // the CTAs' counter before
-    flags = tickets + up(tiles * sizeof(int));
-    parts = flags + up(tiles * sizeof(int));
-    h = parts + up((size_t)(tiles + dev.sms) * T * pitch * sizeof(float));
-    total = h + (size_t)tiles * 2 * kAtom * (max_rank <= 64 ? 1 : 2);
+    parts = tickets + up(tiles * sizeof(int));
+    total = parts + (size_t)(tiles + dev.sms) * T * pitch * sizeof(float);
   }
 };
 
@@ -561,8 +571,8 @@ size_t lora_rows_bytes(int n_adapters, int max_rank, int64_t m, const DeviceInfo
 int launch_lora_rows(const LoraArgs& all, const DeviceInfo& dev, void* scratch, void* stream) {
   const Layout l(all.n_adapters, all.max_rank, all.m, dev);
   char* b = static_cast<char*>(scratch);
-  const Scratch sc = {reinterpret_cast<int*>(b), reinterpret_cast<int*>(b + l.tickets), reinterpret_cast<int*>(b + l.flags),
-                      reinterpret_cast<float*>(b + l.parts), reinterpret_cast<uint8_t*>(b + l.h), l.pitch};
+  const Scratch sc = {reinterpret_cast<int*>(b), reinterpret_cast<int*>(b + l.tickets), reinterpret_cast<float*>(b + l.parts),
+                      l.pitch};
   for (int64_t at = 0; at < all.m; at += kLoraRowsAtOnce) {
     LoraArgs p = all;
     p.m = (int)std::min<int64_t>(kLoraRowsAtOnce, all.m - at);

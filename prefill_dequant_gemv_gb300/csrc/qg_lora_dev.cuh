@@ -97,6 +97,15 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 // Adapter of a row, n_adapters for none (and for an id out of range).
 __device__ __forceinline__ int bin_of(int id, int n_adapters) { return (unsigned)id < (unsigned)n_adapters ? id : n_adapters; }
 
+// Rank of adapter e (0 for the rows without one); one out of range counts as 0 and is reported.
+__device__ __forceinline__ int rank_of(const LoraArgs& p, int e) {
+  if (e >= p.n_adapters) return 0;
+  const int r = p.ranks ? p.ranks[e] : p.max_rank;
+  if (r >= 0 && r <= p.max_rank) return r;
+  atomicCAS(p.status, 0, kStatusInvalid);
+  return 0;
+}
+
 // The rows of every adapter in tiles of T, adapter by adapter; first[e] is adapter e's first tile.
 // first[n_adapters]: the rows without one; first[n_adapters + 1]: the number of tiles.
 // Every CTA builds the same table: ids are few bytes beside x and y.
@@ -104,25 +113,29 @@ template <int THREADS>
 struct Tiles {
   int first[kLoraMaxAdapters + 2];
   int warp_sums[THREADS / 32];
+  uint8_t rank[kLoraMaxAdapters + 1];
 
-  // Also notes every row's bin.  A warp has every THREADS / 32nd run of 32 rows; eight runs' loads before the first use.
+  // Also notes every row's bin.  A warp has every THREADS / 32nd run of 32 rows; 16 runs' loads before the first use.
   __device__ __forceinline__ void count(const LoraArgs& p, int T, uint16_t* bins_of_rows) {
     const int tid = threadIdx.x, lane = tid & 31, bins = p.n_adapters + 1;
     for (int e = tid; e <= bins; e += THREADS) first[e] = 0;
+    for (int e = tid; e <= p.n_adapters; e += THREADS) rank[e] = (uint8_t)rank_of(p, e);
     __syncthreads();
     bool bad = false;
-    for (int i0 = tid; i0 - lane < p.m; i0 += 8 * THREADS) {
-      int e[8];
+    for (int i0 = tid; i0 - lane < p.m; i0 += 16 * THREADS) {
+      int e[16];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) e[u] = i0 + u * THREADS < p.m ? p.ids[i0 + u * THREADS] : -1;
+      for (int u = 0; u < 16; ++u) e[u] = i0 + u * THREADS < p.m ? p.ids[i0 + u * THREADS] : -1;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < 16; ++u) {
         const int i = i0 + u * THREADS;
         if (i - lane >= p.m) break;
         bad |= e[u] < -1 || e[u] >= p.n_adapters;
         e[u] = i < p.m ? bin_of(e[u], p.n_adapters) : -1;
         if (i < p.m) bins_of_rows[i] = (uint16_t)e[u];
-        const unsigned same = __match_any_sync(0xFFFFFFFFu, e[u]);
+        const int one = __shfl_sync(0xFFFFFFFFu, e[u], 0);
+        unsigned same = 0xFFFFFFFFu;  // rows of one adapter in a run: one sum for it
+        if (!__all_sync(0xFFFFFFFFu, e[u] == one)) same = __match_any_sync(0xFFFFFFFFu, e[u]);
         if (e[u] >= 0 && lane == __ffs(same) - 1) atomicAdd(&first[e[u]], __popc(same));  // integer counts: order-free
       }
     }
@@ -148,14 +161,5 @@ struct Tiles {
     __syncthreads();
   }
 };
-
-// Rank of adapter e (0 for the rows without one); one out of range counts as 0 and is reported.
-__device__ __forceinline__ int rank_of(const LoraArgs& p, int e) {
-  if (e >= p.n_adapters) return 0;
-  const int r = p.ranks ? p.ranks[e] : p.max_rank;
-  if (r >= 0 && r <= p.max_rank) return r;
-  atomicCAS(p.status, 0, kStatusInvalid);
-  return 0;
-}
 
 }  // namespace qg

@@ -58,8 +58,8 @@ def lora(q, d=None, ids=0x5000, m=8, x=0x10000, ldx=512, y=0x20000, ldy=256, out
 
 @pytest.mark.parametrize("over,want", [
     (dict(n_adapters=0), INVALID), (dict(n_adapters=1025), UNSUPPORTED), (dict(max_rank=0), INVALID), (dict(max_rank=12), UNSUPPORTED),
-    (dict(max_rank=136), UNSUPPORTED), (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(n=1 << 30, ldy=1 << 30, ldo=1 << 30), UNSUPPORTED),
-    (dict(k=1 << 30), UNSUPPORTED), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(scales=None), INVALID),
+    (dict(max_rank=136), UNSUPPORTED), (dict(n=0), INVALID), (dict(k=0), INVALID), (dict(n=1 << 24, ldy=1 << 24, ldo=1 << 24), UNSUPPORTED),
+    (dict(k=1 << 24), UNSUPPORTED), (dict(a=None), INVALID), (dict(b=None), INVALID), (dict(scales=None), INVALID),
     (dict(lda=504), INVALID), (dict(lda=516), MISALIGNED), (dict(a=0x1008), MISALIGNED), (dict(b=0x2008), MISALIGNED),
     (dict(scales=0x3002), MISALIGNED), (dict(ranks=0x4001), MISALIGNED), (dict(ids=None), INVALID), (dict(ids=0x5002), MISALIGNED),
     (dict(m=-1), INVALID), (dict(m=1 << 27), UNSUPPORTED), (dict(x=None), INVALID), (dict(y=None), INVALID), (dict(out=None), INVALID),
