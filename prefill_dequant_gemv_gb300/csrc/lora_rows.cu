@@ -95,7 +95,7 @@ struct Shape {
   static constexpr uint32_t kY = 4 * 512;             // a warp's share of y: 32 rows x 32 outputs
   static constexpr size_t kShrink = (size_t)kStages * kStage, kExpand = 2 * kTerm + kAhead * (kB + kWarps * kY);
   static constexpr size_t kSmem = (kShrink > kExpand ? kShrink : kExpand) + 1024;
-  static_assert(kShrink >= 2 * kLoraRowsAtOnce, "the rows' bins lie there first");
+  static_assert(kShrink >= 2 * (kLoraRowsAtOnce + kThreads * 8), "the rows' bins lie there first");
 };
 
 // The bin that a tile belongs to: the last with first[e] <= tile (those without tiles share their successor's first).
@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
   }
   // the rows' bins, the tiles, this CTA's units in both phases and its tiles' rows
   uint16_t* bins = reinterpret_cast<uint16_t*>(smem);
-  tl.count(p, T, bins);
+  tl.count(p, T, bins, (p.m + 8 * S::kThreads - 1) / (8 * S::kThreads) * (8 * S::kThreads));
   const int n_adapter = tl.first[p.n_adapters], n_tiles = tl.first[p.n_adapters + 1];  // tiles with an adapter, which come first, and all
   const int k_chunks = (p.k + kWidth - 1) / kWidth, n_chunks = (p.n + kWidth - 1) / kWidth;
   // In shrink a tile of few goes into about eight parts at most, as one CTA adds them all.  In expand a tile begins with kStart units
@@ -179,52 +179,73 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
   int nt0 = nu0 / (n_chunks + kStart), ch = max(0, nu0 - nt0 * (n_chunks + kStart) - kStart);  // expand's first tile and chunk
   const int nt_last = nu1 / (n_chunks + kStart), ch_last = max(0, nu1 - nt_last * (n_chunks + kStart) - kStart);
   const int nt1 = nt_last + (ch_last > 0), n = (nt_last - nt0) * n_chunks + ch_last - ch;  // past its last tile; its chunks
-  // Each adapter's rows in ascending order to the places that they have in this CTA's tiles: every warp looks through a run of
-  // rows, counts first, as the place of its rows hangs on the runs before.
-  const int run = (p.m / 32 + S::kWarps + 1) / (S::kWarps + 1) * 32, i0 = min(p.m, warp * run), i1 = min(p.m, i0 + run);
-  auto list_adapter = [&](int e) {
-    int mine = 0;
-    for (int i = i0; i < i1; i += 32) mine += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < i1 && bins[i + lane] == e));
-    __syncthreads();
-    if (lane == 0) tl.warp_sums[warp] = mine;
-    __syncthreads();
-    int at = 0, total = 0;
+  // Each adapter's rows in ascending order to the places that they have in this CTA's tiles.  A lane looks at eight rows side
+  // by side, a warp at 256 (more than 4352 rows: a run of such blocks); how many there are before them comes from a sum
+  // over the lanes and the warps.
+  const int blocks = (p.m + 256 * (S::kWarps + 1) - 1) / (256 * (S::kWarps + 1));
+  auto look = [&](int i, uint32_t e) {  // bit j: row i + j is e's
+    const uint4 v = *reinterpret_cast<const uint4*>(bins + i);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hits = 0;
 #pragma unroll
-    for (int w = 0; w < S::kWarps + 1; ++w) {
-      at += w < warp ? tl.warp_sums[w] : 0;
-      total += tl.warp_sums[w];
+    for (int j = 0; j < 4; ++j) hits |= ((w[j] & 0xFFFFu) == e ? 1u << 2 * j : 0u) | (w[j] >> 16 == e ? 2u << 2 * j : 0u);
+    return hits;
+  };
+  int t = kt0;
+  for (int phase = 0; phase < 2;) {  // (one copy of this code: it runs once, from cold instruction caches)
+    const int end = phase ? nt1 : kt1;
+    if (t >= end) {
+      ++phase;
+      t = nt0;
+      continue;
     }
-    const int first = tl.first[e];
-    if (mine)
-      for (int i = i0; i < i1; i += 32) {
-        const bool hit = i + lane < i1 && bins[i + lane] == e;
-        const unsigned hits = __ballot_sync(0xFFFFFFFFu, hit);
-        const int place = at + __popc(hits & ((1u << lane) - 1u)), tile = first + place / T;
-        if (hit && tile >= kt0 && tile < kt1) in_list[tile - kt0].rows[place % T] = i + lane;
-        if (hit && tile >= nt0 && tile < nt1) out_list[tile - nt0].rows[place % T] = i + lane;
-        at += __popc(hits);
+    const int e = bin_of_tile(tl.first, p.n_adapters, t), first = tl.first[e], row0 = warp * blocks * 256 + 8 * lane;
+    t = tl.first[e + 1];
+    if (phase && first < kt1 && t > kt0) continue;  // listed already
+    int mine = 0;
+#pragma unroll 1
+    for (int u = 0; u < blocks; ++u) mine += __popc(look(row0 + 256 * u, e));
+    const int all = __reduce_add_sync(0xFFFFFFFFu, mine);
+    __syncthreads();
+    if (lane == 0) tl.warp_sums[warp] = all;
+    __syncthreads();
+    const int v = lane < S::kWarps + 1 ? tl.warp_sums[lane] : 0;
+    int at = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? v : 0);
+    const int total = __reduce_add_sync(0xFFFFFFFFu, v);
+#pragma unroll 1
+    for (int u = 0; u < blocks && all; ++u) {
+      uint32_t h = look(row0 + 256 * u, e);
+      int place = __popc(h);
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xFFFFFFFFu, place, off);
+        if (lane >= off) place += o;
       }
-    const int rank = tl.rank[e];
+      const int sum = __shfl_sync(0xFFFFFFFFu, place, 31);
+      place += at - __popc(h);
+      at += sum;
+      for (; h; h &= h - 1, ++place) {
+        const int row = row0 + 256 * u + __ffs(h) - 1, tile = first + place / T;
+        if (tile >= kt0 && tile < kt1) in_list[tile - kt0].rows[place % T] = row;
+        if (tile >= nt0 && tile < nt1) out_list[tile - nt0].rows[place % T] = row;
+      }
+    }
     if (tid < kt1 - kt0 || (tid >= 32 && tid - 32 < nt1 - nt0)) {
       const int tile = tid < 32 ? kt0 + tid : nt0 + tid - 32, left = total - (tile - first) * T;
       Tile& to = tid < 32 ? in_list[tid] : out_list[tid - 32];
       if (tile >= first && left > 0) {
         to.live = min(left, T);
         to.bin = e;
-        to.rank = rank;
+        to.rank = tl.rank[e];
       }
     }
-  };
-  for (int i = tid; i < kList * T; i += S::kThreads) in_list[i / T].rows[i % T] = out_list[i / T].rows[i % T] = 0;  // past the last: any row
-  for (int t = kt0; t < kt1;) {
-    const int e = bin_of_tile(tl.first, p.n_adapters, t);
-    list_adapter(e);
-    t = tl.first[e + 1];
   }
-  for (int t = nt0; t < nt1;) {
-    const int e = bin_of_tile(tl.first, p.n_adapters, t);
-    if (tl.first[e] >= kt1 || tl.first[e + 1] <= kt0) list_adapter(e);  // not listed yet
-    t = tl.first[e + 1];
+  __syncthreads();
+  if (tid < T) {  // past a tile's last row: any
+    for (int i = 0; i < kt1 - kt0; ++i)
+      if (tid >= in_list[i].live) in_list[i].rows[tid] = 0;
+    for (int i = 0; i < nt1 - nt0; ++i)
+      if (tid >= out_list[i].live) out_list[i].rows[tid] = 0;
   }
   tc_fence_before();
   __syncthreads();

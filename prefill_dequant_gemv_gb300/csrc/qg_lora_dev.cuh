@@ -115,10 +115,11 @@ struct Tiles {
   int warp_sums[THREADS / 32];
   uint8_t rank[kLoraMaxAdapters + 1];
 
-  // Also notes every row's bin.  A warp has every THREADS / 32nd run of 32 rows; 16 runs' loads before the first use.
-  __device__ __forceinline__ void count(const LoraArgs& p, int T, uint16_t* bins_of_rows) {
+  // Also notes every row's bin, and 0xFFFF up to `padded` rows.  A warp has every THREADS / 32nd run of 32 rows; 16 runs' loads before the first use.
+  __device__ __forceinline__ void count(const LoraArgs& p, int T, uint16_t* bins_of_rows, int padded) {
     const int tid = threadIdx.x, lane = tid & 31, bins = p.n_adapters + 1;
     for (int e = tid; e <= bins; e += THREADS) first[e] = 0;
+    for (int i = p.m + tid; i < padded; i += THREADS) bins_of_rows[i] = 0xFFFF;
     for (int e = tid; e <= p.n_adapters; e += THREADS) rank[e] = (uint8_t)rank_of(p, e);
     __syncthreads();
     bool bad = false;
