@@ -301,9 +301,9 @@ size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
  * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^24, the leading
  * dimensions below 2^31.  The workspace must be zero-filled before its first use and after QG_ERR_TIMEOUT; every
  * other qlora call, of any sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not
- * share it, and no other entry point may use it in between.  More than 256 rows need a GPU of 96 SMs or more
- * (QG_ERR_UNSUPPORTED otherwise) and run on all of its SMs at once, so such a call starts when no other kernel holds one.
- * Deterministic; one launch for up to 256 rows, one for every 16384 of more. */
+ * share it, and no other entry point may use it in between.  More than 256 rows (512 where there are 16 adapters or more) need a GPU of
+ * 96 SMs or more (QG_ERR_UNSUPPORTED otherwise) and run on all of its SMs at once, so such a call starts when no other kernel
+ * holds one.  Deterministic; one launch for every 256 rows, or for every 16384 where they are more. */
 qg_status qlora(const qg_lora* lora, const int32_t* ids, int64_t m_rows, const void* x, int64_t ldx, const void* y,
                 int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 

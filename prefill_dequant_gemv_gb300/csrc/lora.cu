@@ -373,12 +373,20 @@ int launch(const LoraArgs& p, const DeviceInfo& dev, cudaStream_t s) {
 
 }  // namespace
 
-int launch_lora(const LoraArgs& p, const DeviceInfo& dev, void* stream) {
+int launch_lora(const LoraArgs& all, const DeviceInfo& dev, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (p.max_rank <= 16) return launch<16>(p, dev, s);
-  if (p.max_rank <= 32) return launch<32>(p, dev, s);
-  if (p.max_rank <= 64) return launch<64>(p, dev, s);
-  return launch<128>(p, dev, s);
+  for (int64_t at = 0; at < all.m; at += kLoraFewRows) {
+    LoraArgs p = all;
+    p.m = (int)std::min<int64_t>(kLoraFewRows, all.m - at);
+    p.ids += at;
+    p.x += at * p.ldx;
+    p.y += at * p.ldy;
+    p.out += at * p.ldo;
+    const int st = p.max_rank <= 16 ? launch<16>(p, dev, s) : p.max_rank <= 32 ? launch<32>(p, dev, s)
+                   : p.max_rank <= 64 ? launch<64>(p, dev, s) : launch<128>(p, dev, s);
+    if (st != QG_OK) return st;
+  }
+  return QG_OK;
 }
 
 }  // namespace qg

@@ -16,7 +16,7 @@ extern "C" size_t qlora_workspace_size(const qg_lora* l, int64_t m) {
   if (!l || m < 0 || m >= (1 << 27) || l->n_adapters < 1 || l->n_adapters > kLoraMaxAdapters || l->max_rank < 1 ||
       l->max_rank > kLoraMaxRank)
     return 0;
-  if (m <= kLoraFewRows) return kWsHeader;
+  if (lora_few(m, l->n_adapters)) return kWsHeader;
   DeviceInfo dev;
   if (!current_device_info(&dev)) return 0;
   return kWsHeader + (dev.sms < kLoraMinSms ? 0 : lora_rows_bytes(l->n_adapters, l->max_rank, m, dev));
@@ -59,7 +59,7 @@ extern "C" qg_status qlora(const qg_lora* l, const int32_t* ids, int64_t m, cons
   p.ldy = (int)ldy;
   p.ldo = (int)ldo;
   p.status = static_cast<int*>(workspace);
-  if (m <= kLoraFewRows) return (qg_status)launch_lora(p, dev, stream);
+  if (lora_few(m, l->n_adapters)) return (qg_status)launch_lora(p, dev, stream);
   if (dev.sms < kLoraMinSms) return QG_ERR_UNSUPPORTED;
   if (workspace_bytes < kWsHeader + lora_rows_bytes(l->n_adapters, l->max_rank, m, dev)) return QG_ERR_WORKSPACE_TOO_SMALL;
   return (qg_status)launch_lora_rows(p, dev, static_cast<char*>(workspace) + kWsHeader, stream);
