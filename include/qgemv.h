@@ -247,7 +247,7 @@ qg_status qgemm_w4a4(const qg_weight* w, const void* x, int64_t m_rows, int64_t 
  * stored in bf16, in E4M3 codes with scales, or both; each value is rounded to its type once.
  * E4M3: a group of `group` consecutive elements of a row (32, 64 or 128; the last may be shorter),
  * or the whole row (group 0), has the fp32 scale s = max(amax / 448, 2^-100), amax its largest finite
- * |y|, and the codes E4M3(y * (1/s)), nearest even and saturating at 448: infinities saturate,
+ * |y|, and the codes E4M3(y / s), nearest even and saturating at 448: infinities saturate,
  * NaN stays NaN and neither moves a scale.  A row with a NaN in it is NaN, as the formula gives it;
  * the squares are summed in fp32, so a row whose
  * sum passes 2^128 comes out as zeros (NaN where h is infinite). */

@@ -1,7 +1,7 @@
 // RMS norm with the residual's addition before it, its output in bf16 and / or in E4M3 codes
 // with fp32 scales:
 //   h = bf16(x + residual),  y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)
-//   scale = max(amax / 448, 2^-100) of a group of y (or a row),  code = E4M3(y * (1 / scale))
+//   scale = max(amax / 448, 2^-100) of a group of y (or a row),  code = E4M3(y / scale)
 //
 // A row belongs to one CTA and a thread holds NV vectors of eight of its elements in
 // registers, so that x and the residual are read once and the sum is written in the same
@@ -128,6 +128,8 @@ __device__ __noinline__ float largest_value(Vec h, Vec w, float inv, float woff)
   scaled(h, w, inv, woff, v);
   return largest(v, true);
 }
+// Whether the largest product of h and a weight leaves them and their product with inv well inside fp32's range.
+__device__ __forceinline__ bool in_range(float amax, float inv) { return amax >= 0x1p-100f && amax < INFINITY && amax * inv < INFINITY; }
 // Over the `lanes` neighbouring lanes of a group.
 __device__ __forceinline__ float group_max(float m, int lanes) {
   for (int off = lanes >> 1; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
@@ -193,47 +195,56 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
       }
     }
     block_reduce<FP8 == 2>(sq, amax, slots[0][turn], slots[1][turn]);
-    const float inv = rsqrtf(sq * a.inv_k + a.eps);
-    float is = 0.0f;
+    const float inv = __frsqrt_rn(__fdiv_rn(sq, (float)k) + a.eps);
+    // Codes are those of h * weight * (inv / scale), one rounding less than by way of y; where the products h * weight pass
+    // fp32's range or come near its end, of h * inv * weight / scale.
+    float first = 1.0f, then = inv, t = 0.0f;  // h * first * weight * then = y, h * first * weight * t = the code's value
+    auto step = [&](float am) {  // the scale, from the largest |h * first * weight|
+      const float s = fmaxf(am * then * (1.0f / 448.0f), kScaleMin);
+      t = __fdiv_rn(then, s);
+      return s;
+    };
     if (FP8 == 2) {
-      if (amax >= 0x1p-100f && amax < INFINITY) {  // the same for the block
-        amax *= inv;
-      } else {  // of the values themselves: the products may have passed fp32's range where these do not
-        amax = 0.0f;
+      if (!in_range(amax, inv)) {  // the same for the block
+        first = inv, then = 1.0f, amax = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const Vec g = kHold ? w[kHold ? i : 0] : load8(a.w, c0 + i * T * 8, k);
-          amax = fmaxf(amax, largest_value(h[i], g, inv, a.woff));
-        }
+        for (int i = 0; i < NV; ++i)
+          amax = fmaxf(amax, largest_value(h[i], kHold ? w[kHold ? i : 0] : load8(a.w, c0 + i * T * 8, k), inv, a.woff));
         float none = 0.0f;
         __syncthreads();
         block_reduce<true>(none, amax, slots[0][turn], slots[1][turn]);
       }
-      const float s = fmaxf(__fdiv_rn(amax < INFINITY ? amax : 0.0f, 448.0f), kScaleMin);
+      const float s = step(amax);
       if (threadIdx.x == 0) a.scales[r * a.lds] = s;
-      is = __frcp_rn(s);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = c0 + i * T * 8;
+      const Vec g = kHold ? w[kHold ? i : 0] : load8(a.w, c, k);
       float v[8];
-      scaled(h[i], kHold ? w[kHold ? i : 0] : load8(a.w, c, k), inv, a.woff, v);
+      if (FP8 == 1) {
+        // NaN does not enter a maximum.  What lies past the row's end is 0.
+        first = 1.0f, then = inv;
+        scaled(h[i], g, 1.0f, a.woff, v);
+        amax = group_max(largest(v, false), a.group_lanes);
+        if (__any_sync(0xFFFFFFFFu, !in_range(amax, inv))) {
+          first = inv, then = 1.0f;
+          scaled(h[i], g, inv, a.woff, v);
+          amax = group_max(largest(v, true), a.group_lanes);
+        }
+        const float s = step(amax);
+        if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + (c >> a.group_log2)] = s;
+      } else {
+        scaled(h[i], g, FP8 ? first : inv, a.woff, v);
+      }
       if (FP8 == 0 || a.y) {
+        const float f = FP8 ? then : 1.0f;
         Vec o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[2 * j] * f, v[2 * j + 1] * f);
         store8(a.y + r * a.ldy, c, k, o);
       }
-      if (FP8 == 1) {
-        // NaN does not enter a maximum; infinities are found out by it and left out in a second look.  What lies past the
-        // row's end is 0 (or NaN).
-        amax = group_max(largest(v, false), a.group_lanes);
-        if (__any_sync(0xFFFFFFFFu, amax == INFINITY)) amax = group_max(largest(v, true), a.group_lanes);
-        const float s = fmaxf(__fdiv_rn(amax, 448.0f), kScaleMin);
-        if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + (c >> a.group_log2)] = s;
-        is = __frcp_rn(s);
-      }
-      if (FP8) store_codes(a, r, c, k, v, is);
+      if (FP8) store_codes(a, r, c, k, v, t);
     }
   }
 }

@@ -55,7 +55,6 @@ extern "C" qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residua
   a.k = k;
   a.eps = eps;
   a.woff = weight_offset;
-  a.inv_k = 1.0f / (float)k;
   a.sum = static_cast<uint16_t*>(o.sum);
   a.ldh = o.ldh;
   a.y = static_cast<uint16_t*>(o.y);

@@ -14,7 +14,7 @@ struct NormArgs {
   const uint16_t* res;  // or null
   const uint16_t* w;
   int64_t ldx, ldr, m, k;
-  float eps, woff, inv_k;
+  float eps, woff;
   uint16_t* sum;  // or null
   uint16_t* y;    // or null (with codes)
   int64_t ldh, ldy;
