@@ -502,6 +502,8 @@ class RouteRule:
         _need(score in kinds, "RouteRule: score is softmax or sigmoid")
         _need(bias is None or (bias.dtype == torch.float32 and bias.dim() == 1 and bias.is_contiguous()),
               "RouteRule: bias is contiguous float32 [experts]")
+        _need(0 <= min(groups, topk_groups, group_best) and max(groups, topk_groups, group_best) < 1 << 31,
+              "RouteRule: groups, topk_groups and group_best are 32-bit counts")
         self.bias = bias
         self.desc = qg_route_rule(kinds[score], groups, topk_groups, group_best, 1 if renormalise else 0, scale,
                                   None if bias is None else bias.data_ptr())
@@ -709,7 +711,9 @@ class LoraAdapters:
 
 def lora_workspace_size(adapters: LoraAdapters, m: int) -> int:
     """Workspace bytes of ``lora`` for m rows."""
-    return qlora_workspace_size(adapters.desc, m)
+    import torch
+    with torch.cuda.device(adapters.index):  # -1, not on a GPU: the current one
+        return qlora_workspace_size(adapters.desc, m)
 
 
 def lora(adapters: LoraAdapters, ids, x, y, out=None, workspace: Optional[Workspace] = None):
@@ -726,7 +730,7 @@ def lora(adapters: LoraAdapters, ids, x, y, out=None, workspace: Optional[Worksp
     else:
         op, ldo = _rows(out, m, adapters.n, torch.bfloat16, index, "lora: out")
     if workspace is None:
-        workspace = Workspace(qlora_workspace_size(adapters.desc, m), x.device)
+        workspace = Workspace(lora_workspace_size(adapters, m), x.device)
     elif workspace.index != index:
         raise QGError(1, "lora: the workspace on the adapters' device")
     st = _on(index, (_lib or lib()).qlora, adapters.desc, ids.data_ptr(), m, xp, ldx, yp, ldy, op, ldo, workspace.ptr, workspace.nbytes)

@@ -14,7 +14,7 @@ bool misaligned(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>
 
 extern "C" size_t qlora_workspace_size(const qg_lora* l, int64_t m) {
   if (!l || m < 0 || m >= (1 << 27) || l->n_adapters < 1 || l->n_adapters > kLoraMaxAdapters || l->max_rank < 1 ||
-      l->max_rank > kLoraMaxRank)
+      l->max_rank > kLoraMaxRank || l->max_rank % 8 || l->n < 1 || l->n >= (1 << 24) || l->k < 1 || l->k >= (1 << 24))
     return 0;
   if (lora_few(m, l->n_adapters)) return kWsHeader;
   DeviceInfo dev;

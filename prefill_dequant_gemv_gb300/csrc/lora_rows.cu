@@ -550,7 +550,9 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
   }
 }
 
-// The scratch after the status word: counters, then h's parts.
+// The scratch after the status word: counters, at one place and of one size whatever the call's, as they are to be zero before the
+// next call of any sizes; then h's parts.
+constexpr int kTickets = (int)kLoraRowsAtOnce / T + kLoraMaxAdapters + 1;  // tiles at most
 struct Layout {
   size_t tickets, parts, total;
   int pitch;
@@ -560,7 +562,7 @@ struct Layout {
     pitch = (max_rank + 15) / 16 * 16;
     const auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     tickets = 256;  // the CTAs' counter before
-    parts = tickets + up(tiles * sizeof(int));
+    parts = tickets + up(kTickets * sizeof(int));
     total = parts + (size_t)(tiles + dev.sms) * T * pitch * sizeof(float);
   }
 };

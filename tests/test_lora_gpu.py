@@ -205,3 +205,70 @@ def test_no_rows():
     ad = adapters(q, 2, 8, 64, 64, 1)
     y = rows(0, 64, 1)
     assert q.lora(ad, torch.zeros(0, dtype=torch.int32, device="cuda"), rows(0, 64, 1), y) is y
+
+
+@pytest.mark.parametrize("kind", ["mixed", "runs", "one", "none"])
+@pytest.mark.parametrize("m,count", [(257, 16), (300, 48), (512, 16), (512, 15), (513, 16), (512, 200)])
+def test_launches_of_256_rows_and_the_border_to_many(m, count, kind):
+    q = qlib()
+    ad = adapters(q, count, 16, 200, 136, m + count)
+    ids, x, y = ids_of(kind, m, count, m), rows(m, 200, m), rows(m, 136, m + 1, fill=0.0)
+    check(ad, ids, x, y, run(q, ad, ids, x, y))
+
+
+def test_many_rows_captured_on_streams_and_with_one_workspace():
+    """One workspace for calls of falling and rising size, two graphs that share it, and a stream of its own for each of two
+    calls with theirs."""
+    q = qlib()
+    ad, wide = adapters(q, 5, 32, 512, 768, 7), adapters(q, 300, 128, 256, 264, 8)
+    most = 2000
+    ws = q.Workspace(max(q.lora_workspace_size(a, most) for a in (ad, wide)))
+    sized = {m: (torch.tensor(ids_of("mixed", m, 5, m), dtype=torch.int32, device="cuda"), rows(m, 512, m), rows(m, 768, m + 1, fill=0.0))
+             for m in (2000, 300, 40, 1100)}
+    graphs, outs = [], {}
+    for m, (ids, x, y) in sized.items():
+        outs[m] = torch.zeros_like(y)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.lora(ad, ids, x, y, out=outs[m], workspace=ws)
+        graphs.append(g)
+    big = torch.tensor(ids_of("mixed", most, 300, 9), dtype=torch.int32, device="cuda")
+    bx, by = rows(most, 256, 10), rows(most, 264, 11, fill=0.0)
+    for g in graphs + graphs[::-1]:
+        for o in outs.values():
+            o.zero_()
+        g.replay()
+        got = q.lora(wide, big, bx, by, out=torch.empty_like(by), workspace=ws)
+    for g in graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    assert ws.status() == 0
+    check(wide, big.tolist(), bx, by, got)
+    for m, (ids, x, y) in sized.items():
+        check(ad, ids.tolist(), x, y, outs[m])
+    streams, spaces = [torch.cuda.Stream() for _ in range(2)], [q.Workspace(q.lora_workspace_size(ad, 2000)) for _ in range(2)]
+    ids, x, y = sized[2000]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s, w in zip(streams, spaces):
+            with torch.cuda.stream(s):
+                got.append(q.lora(ad, ids, x, y, out=torch.empty_like(y), workspace=w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, outs[2000]) for g in got) and all(w.status() == 0 for w in spaces)
+
+
+def test_a_workspace_serves_on_after_bad_ids():
+    q = qlib()
+    ad = adapters(q, 4, 16, 256, 256, 3)
+    ws = q.Workspace(q.lora_workspace_size(ad, 600))
+    x, y = rows(600, 256, 1), rows(600, 256, 2, fill=0.0)
+    bad = torch.full((600,), 9, dtype=torch.int32, device="cuda")
+    ids = ids_of("mixed", 600, 4, 5)
+    good = torch.tensor(ids, dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        out = q.lora(ad, bad, x, y, out=torch.empty_like(y), workspace=ws)
+        assert ws.status() == 1 and torch.equal(out, y)
+        out = q.lora(ad, good, x, y, out=torch.empty_like(y), workspace=ws)
+        assert ws.status() == 0
+        check(ad, ids, x, y, out)
