@@ -247,10 +247,11 @@ qg_status qgemm_w4a4(const qg_weight* w, const void* x, int64_t m_rows, int64_t 
  * stored in bf16, in E4M3 codes with scales, or both; each value is rounded to its type once.
  * E4M3: a group of `group` consecutive elements of a row (32, 64 or 128; the last may be shorter),
  * or the whole row (group 0), has the fp32 scale s = max(amax / 448, 2^-100), amax its largest finite
- * |y|, and the codes E4M3(y / s), nearest even and saturating at 448: infinities saturate,
- * NaN stays NaN and neither moves a scale.  A row with a NaN in it is NaN, as the formula gives it;
- * the squares are summed in fp32, so a row whose
- * sum passes 2^128 comes out as zeros (NaN where h is infinite). */
+ * |y|, and the codes E4M3(y / s), nearest even and saturating at 448: infinities saturate, NaN stays
+ * NaN and neither moves a scale.  A row with a NaN in it is NaN, as the formula gives it; the squares
+ * are summed in fp32, so a row whose sum passes 2^128 comes out as zeros (NaN where h is infinite) and,
+ * with eps 0, one whose squares are all below 2^-149 as infinities (NaN where h is 0).  y has the same bits
+ * with codes and without. */
 typedef struct {
   void* sum;              /* device bf16 [m][ldh]: h, or NULL; without a residual NULL */
   int64_t ldh;
@@ -343,7 +344,7 @@ size_t qmoe_route_workspace_size(int64_t t, int n_experts, int topk);
 qg_status qmoe_route(const float* logits, int64_t t, int n_experts, int topk,
                      int32_t* topk_ids, float* topk_w, void* route_ws, size_t route_ws_bytes, void* stream);
 
-/* Routing by other scores than qmoe_route's.  For each token, in exact arithmetic (see below),
+/* Routing by other scores than qmoe_route's.  For each token
  *     s_e = sigmoid(logit_e), or softmax over all experts
  *     c_e = s_e + bias_e                       the choice value; the bias does not enter the weights
  *   With n_groups > 1 (groups of n_experts / n_groups consecutive experts): a group's value is the sum of its
@@ -352,8 +353,9 @@ qg_status qmoe_route(const float* logits, int64_t t, int n_experts, int topk,
  *   The topk remaining experts of largest c, in descending order (ties to the lower index), are chosen;
  *     w_e = scale * s_e, or scale * s_e / (sum of the chosen s) with renormalise.
  * The choice is the one that scores in 64 bits give: c in fp32 decides where it is clear, and a
- * token with two values nearer to each other than fp32's error is decided in 64 bits.  The
- * weights are fp32.  NaN values of c come after every number; a weight is NaN where the formula's is
+ * token with two values nearer to each other than fp32's error is decided in 64 bits.  Without a bias, and
+ * with groups valued by one expert if there are any, c is ordered as the logits are, and they decide.
+ * The weights are fp32.  NaN values of c come after every number; a weight is NaN where the formula's is
  * (renormalised weights whose sum is 0 among them). */
 typedef enum { QG_SCORE_SOFTMAX = 1, QG_SCORE_SIGMOID = 2 } qg_score;
 typedef struct {

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
     const float inv = __frsqrt_rn(__fdiv_rn(sq, (float)k) + a.eps);
     // Codes are those of h * weight * (inv / scale), one rounding less than by way of y; where the products h * weight pass
     // fp32's range or come near its end, of h * inv * weight / scale.
-    float first = 1.0f, then = inv, t = 0.0f;  // h * first * weight * then = y, h * first * weight * t = the code's value
+    float first = 1.0f, then = inv, t = 0.0f;  // y = h * first * weight * then, the code's value h * first * weight * t
     auto step = [&](float am) {  // the scale, from the largest |h * first * weight|
       const float s = fmaxf(am * then * (1.0f / 448.0f), kScaleMin);
       t = __fdiv_rn(then, s);
@@ -237,14 +237,14 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
       } else {
         scaled(h[i], g, FP8 ? first : inv, a.woff, v);
       }
-      if (FP8 == 0 || a.y) {
-        const float f = FP8 ? then : 1.0f;
+      if (FP8) store_codes(a, r, c, k, v, t);
+      if (FP8 == 0 || a.y) {  // the same bits with codes and without
+        if (FP8) scaled(h[i], g, inv, a.woff, v);
         Vec o;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[2 * j] * f, v[2 * j + 1] * f);
+        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
         store8(a.y + r * a.ldy, c, k, o);
       }
-      if (FP8) store_codes(a, r, c, k, v, t);
     }
   }
 }

@@ -262,7 +262,7 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
         // the groups' order hangs on values that are near each other: their best experts, and those near them, in 64 bits
         __syncwarp();
         const float last = r.group_best == 2 ? a1 : a0;
-        if (lane < r.n_groups) cs[lane] = last - (near + 0x1p-22f * fabsf(last));
+        if (lane < r.n_groups) cs[lane] = last == INFINITY ? last : last - (near + 0x1p-22f * fabsf(last));
         __syncwarp();
         uint32_t best = 0;
 #pragma unroll
@@ -277,7 +277,7 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
     open = 0;
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-      const bool in = groups >> group_of(r, lane + 32 * i) & 1;
+      const bool in = groups >> (group_of(r, lane + 32 * i) & 31) & 1;  // past the experts: any
       open |= in ? 1u << i : 0u;
     }
     __syncwarp();

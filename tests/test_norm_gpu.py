@@ -146,3 +146,40 @@ def test_no_rows():
     q = qlib()
     y, h = q.rms_norm(matrix(0, 64, 1), matrix(1, 64, 1)[0], matrix(0, 64, 1))
     assert y.shape == (0, 64) and h.shape == (0, 64)
+
+
+@pytest.mark.parametrize("group", [0, 32, 128])
+def test_products_beyond_fp32_and_the_same_bits_with_codes(group):
+    """h * weight past fp32's range or near its end, while y itself is an ordinary number."""
+    q = qlib()
+    k = 264
+    x = matrix(6, k, 21)
+    w = matrix(1, k, 22)[0]
+    for scale_x, scale_w in ((2.0 ** 50, 2.0 ** 100), (2.0 ** 58, 2.0 ** 69), (2.0 ** -50, 2.0 ** -60), (2.0 ** -60, 2.0 ** 90),
+                             (2.0 ** 58, 2.0 ** -90)):
+        xs, ws = (x.float() * scale_x).bfloat16(), (w.float() * scale_w).bfloat16()
+        xs[1, :k // 2] = 0.0   # groups of zeros
+        xs[2, 7:] = 0.0
+        _, want = ol.rms_norm(to_f64(xs), None, to_f64(ws), 0.0, 0.0)
+        both = torch.empty(6, k, dtype=torch.bfloat16, device="cuda")
+        codes, scales, _ = q.rms_norm_fp8(xs, ws, eps=0.0, group=group, y_out=both)
+        check_codes(codes, scales, want, group)
+        check_y(both, want)
+        assert torch.equal(both, q.rms_norm(xs, ws, eps=0.0)[0])
+
+
+@pytest.mark.parametrize("group", [0, 64])
+def test_two_streams_at_once(group):
+    q = qlib()
+    m, k = 700, 1024
+    x, r, w = matrix(m, k, 31), matrix(m, k, 32), matrix(1, k, 33)[0]
+    want = q.rms_norm_fp8(x, w, r, group=group)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(q.rms_norm_fp8(x, w, r, group=group))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip((t.contiguous() for t in g), (t.contiguous() for t in want)))

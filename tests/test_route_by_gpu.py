@@ -202,3 +202,49 @@ def test_graph_and_stream():
         i2, w2, ws2 = q.route(lg, 6, rule=rule)
         torch.cuda.synchronize()
         assert torch.equal(ids, i2) and torch.equal(w, w2) and tables_equal(q, ws.buf, ws2.buf, t, 64, 6)
+
+
+@pytest.mark.parametrize("t", [1, 2, 3, 50])
+def test_infinite_and_saturated_values(t):
+    """Biases of +infinity (in groups too, two in a group), logits of +infinity, and scores that are 1 to the last bit."""
+    q = qlib()
+    rng = np.random.default_rng(6)
+    e = 96
+    lg = rng.standard_normal((t, e)).astype(np.float32)
+    bias = 0.1 * rng.standard_normal(e)
+    one, two = bias.copy(), bias.copy()
+    one[70] = np.inf
+    two[[50, 51, 53, 90, 91]] = np.inf
+    for b in (one, two):
+        for kw in (dict(), dict(groups=8, topk_groups=2), dict(groups=8, topk_groups=2, group_best=1), dict(groups=32, topk_groups=9)):
+            for score in ("sigmoid", "softmax"):
+                compare(q, lg, 6, bias=b, score=score, **kw)
+    top = lg.copy()
+    top[:, [3, 40]] = np.inf
+    compare(q, top, 6, score="sigmoid")
+    for score in ("sigmoid", "softmax"):  # softmax: the logits choose (with a bias the index, every score being NaN), weights NaN
+        compare(q, top, 6, score=score)
+        compare(q, top, 6, score=score, bias=bias)
+    compare(q, 40 + 10 * np.abs(lg), 6, score="sigmoid")
+    compare(q, 40 + 10 * np.abs(lg), 6, score="sigmoid", bias=bias)
+    compare(q, 1e4 * lg, 6, score="softmax", bias=bias)
+
+
+def test_two_streams_at_once_and_wrong_devices():
+    q = qlib()
+    rule = q.RouteRule("softmax", bias=0.01 * torch.randn(128, device="cuda"), groups=8, topk_groups=4)
+    lg = torch.randn(3000, 128, device="cuda")
+    want = q.route(lg, 8, rule=rule)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for _ in range(3):
+        for s in streams:
+            with torch.cuda.stream(s):
+                got.append(q.route(lg, 8, rule=rule))
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1]) and tables_equal(q, g[2].buf, want[2].buf, 3000, 128, 8)
+    with pytest.raises(q.QGError):
+        q.route(lg.cpu(), 8, rule=rule)
+    with pytest.raises(q.QGError):
+        q.route(lg, 8, rule=q.RouteRule("softmax", bias=torch.zeros(128)))
