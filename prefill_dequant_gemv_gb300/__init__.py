@@ -328,8 +328,9 @@ def _need(ok: bool, what: str):
 def _on(index: int, call, *args):
     """call(*args, the current stream of device `index`), with that device the current one."""
     import torch
-    if torch._C._cuda_getDevice() == index:
-        return call(*args, torch._C._cuda_getCurrentRawStream(index))
+    c = torch._C
+    if c._cuda_getDevice() == index:
+        return call(*args, c._cuda_getCurrentRawStream(index))
     with torch.cuda.device(index):
         return call(*args, _raw_stream(index))
 
@@ -521,8 +522,8 @@ def _route_by(rule: RouteRule, logits, topk: int, workspace: Optional[Workspace]
         workspace = Workspace(qmoe_route_workspace_size(t, e, topk), logits.device)
     elif workspace.index != index:
         raise QGError(1, "route: the workspace on the logits' device")
-    ids = logits.new_empty((t, topk), dtype=torch.int32)
-    w = logits.new_empty((t, topk))
+    device = logits.device
+    ids, w = torch.empty(t, topk, dtype=torch.int32, device=device), torch.empty(t, topk, dtype=torch.float32, device=device)
     st = _on(index, (_lib or lib()).qmoe_route_by, rule.desc, logits.data_ptr(), t, e, topk, ids.data_ptr(), w.data_ptr(),
              workspace.ptr, workspace.nbytes)
     if st:
@@ -610,50 +611,50 @@ def moe_stage(pm: PackedMoE, stage: int, inp, t: int, topk: int, route_ws: Works
 
 
 # ------------------------------------------------------------------ RMS norm and low-rank adapters
-def _rows(t, m, k, dtype, index, what):
-    """(pointer, row stride) of a matrix [m, k] of `dtype` on device `index`; its rows' elements lie side by side."""
-    if t.dtype is not dtype or t.dim() != 2 or t.get_device() != index or tuple(t.shape) != (m, k) or (k > 1 and t.stride(1) != 1):
-        raise QGError(1, f"{what}: {dtype} [{m}, {k}] with a contiguous last dimension, on the input's CUDA device")
-    return t.data_ptr(), (t.stride(0) if m > 1 else (k + 7) // 8 * 8)
+def _rows(t, shape, dtype, index, what, name):
+    """(pointer, row stride) of a matrix of `shape` and `dtype` on device `index`; its rows' elements lie side by side."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index:
+        ld, step = t.stride()
+        if step == 1 or shape[1] == 1:
+            return t.data_ptr(), (ld if shape[0] > 1 else (shape[1] + 7) // 8 * 8)
+    raise QGError(1, f"{what}: {name} is {dtype} {[*shape]} with a contiguous last dimension, on the call's CUDA device")
 
 
-def _new_rows(x, m, k, dtype):
-    """A new matrix [m, k] whose rows start at multiples of 16 bytes."""
-    return x.new_empty((m, (k + 15) // 16 * 16), dtype=dtype)[:, :k]
+def _new_rows(x, shape, dtype):
+    """A new matrix whose rows start at multiples of 16 bytes."""
+    return x.new_empty((shape[0], (shape[1] + 15) // 16 * 16), dtype=dtype)[:, :shape[1]]
 
 
-def _norm(x, weight, residual, eps, weight_offset, sum_out, what):
-    """The checked inputs of a norm: (arguments up to weight_offset, pointer and stride of the sum, the sum, device)."""
-    import torch
-    index = x.get_device()
-    if x.dim() != 2 or index < 0:
+def _norm(x, weight, residual, sum_out, bf16, what):
+    """The checked inputs of a norm: (x's shape, device, the arguments up to the weight, pointer and stride of the sum, the sum)."""
+    index, shape = x.get_device(), x.shape
+    if len(shape) != 2 or index < 0:
         raise QGError(1, f"{what}: x is bfloat16 [rows, columns] on a CUDA device")
-    m, k = x.shape
-    xp, ldx = _rows(x, m, k, torch.bfloat16, index, f"{what}: x")
-    if (weight.dtype is not torch.bfloat16 or tuple(weight.shape) != (k,) or weight.get_device() != index
-            or (k > 1 and weight.stride(0) != 1)):
+    m, k = shape
+    xp, ldx = _rows(x, shape, bf16, index, what, "x")
+    if weight.dtype is not bf16 or weight.shape != (k,) or weight.get_device() != index or (k > 1 and weight.stride(0) != 1):
         raise QGError(1, f"{what}: weight is contiguous bfloat16 [{k}] on x's device")
-    rp = hp = None
-    ldr = ldh = 0
-    if residual is not None:
-        rp, ldr = _rows(residual, m, k, torch.bfloat16, index, f"{what}: residual")
-        if sum_out is None:
-            sum_out = _new_rows(x, m, k, torch.bfloat16)
-        hp, ldh = _rows(sum_out, m, k, torch.bfloat16, index, f"{what}: sum_out")
-    elif sum_out is not None:
-        raise QGError(1, f"{what}: a sum needs a residual")
-    return (xp, ldx, rp, ldr, m, k, weight.data_ptr(), eps, weight_offset), hp, ldh, sum_out, index
+    if residual is None:
+        if sum_out is not None:
+            raise QGError(1, f"{what}: a sum needs a residual")
+        return shape, index, (xp, ldx, None, 0, m, k, weight.data_ptr()), None, 0, None
+    rp, ldr = _rows(residual, shape, bf16, index, what, "residual")
+    if sum_out is None:
+        sum_out = _new_rows(x, shape, bf16)
+    hp, ldh = _rows(sum_out, shape, bf16, index, what, "sum_out")
+    return shape, index, (xp, ldx, rp, ldr, m, k, weight.data_ptr()), hp, ldh, sum_out
 
 
 def rms_norm(x, weight, residual=None, eps: float = 1e-6, weight_offset: float = 0.0, out=None, sum_out=None):
     """RMS norm of x (bf16 [m, k]), after the residual's addition if there is one (``qg_rms_norm``): returns (y bf16 [m, k],
     the sum bf16 [m, k] or None).  out or sum_out may be x or the residual itself."""
     import torch
-    args, hp, ldh, sum_out, index = _norm(x, weight, residual, eps, weight_offset, sum_out, "rms_norm")
+    bf16 = torch.bfloat16
+    shape, index, args, hp, ldh, sum_out = _norm(x, weight, residual, sum_out, bf16, "rms_norm")
     if out is None:
-        out = _new_rows(x, args[4], args[5], torch.bfloat16)
-    yp, ldy = _rows(out, args[4], args[5], torch.bfloat16, index, "rms_norm: out")
-    st = _on(index, (_lib or lib()).qg_rms_norm, *args, qg_norm_out(hp, ldh, yp, ldy))
+        out = _new_rows(x, shape, bf16)
+    yp, ldy = _rows(out, shape, bf16, index, "rms_norm", "out")
+    st = _on(index, (_lib or lib()).qg_rms_norm, *args, eps, weight_offset, qg_norm_out(hp, ldh, yp, ldy))
     if st:
         raise QGError(st, "qg_rms_norm")
     return out, sum_out
@@ -664,19 +665,23 @@ def rms_norm_fp8(x, weight, residual=None, eps: float = 1e-6, weight_offset: flo
     """``rms_norm`` with its output in 8 bits: returns (codes float8_e4m3fn [m, k], scales fp32 [m, ceil(k / group)], the
     sum or None); group 32, 64 or 128, or 0 for one scale a row.  y_out (bf16 [m, k]), if given, takes the output in bf16 too."""
     import torch
-    args, hp, ldh, sum_out, index = _norm(x, weight, residual, eps, weight_offset, sum_out, "rms_norm_fp8")
-    m, k = args[4], args[5]
+    bf16 = torch.bfloat16
+    shape, index, args, hp, ldh, sum_out = _norm(x, weight, residual, sum_out, bf16, "rms_norm_fp8")
     if group not in (0, 32, 64, 128):
         raise QGError(2, "rms_norm_fp8: group is 32, 64, 128 or 0")
-    groups = -(-k // group) if group else 1
+    groups = shape[0], (-(-shape[1] // group) if group else 1)
     if out is None:
-        out = _new_rows(x, m, k, torch.float8_e4m3fn)
+        out = _new_rows(x, shape, torch.float8_e4m3fn)
     if scales is None:
-        scales = x.new_empty((m, groups), dtype=torch.float32)
-    cp, ldc = _rows(out, m, k, torch.float8_e4m3fn, index, "rms_norm_fp8: out")
-    sp, lds = _rows(scales, m, groups, torch.float32, index, "rms_norm_fp8: scales")
-    yp, ldy = (None, 0) if y_out is None else _rows(y_out, m, k, torch.bfloat16, index, "rms_norm_fp8: y_out")
-    st = _on(index, (_lib or lib()).qg_rms_norm, *args, qg_norm_out(hp, ldh, yp, ldy, cp, ldc, sp, lds, group))
+        scales = x.new_empty(groups, dtype=torch.float32)
+    cp, ldc = _rows(out, shape, torch.float8_e4m3fn, index, "rms_norm_fp8", "out")
+    if scales.dtype is not torch.float32 or scales.shape != groups or scales.get_device() != index or \
+            (groups[1] > 1 and scales.stride(1) != 1):
+        raise QGError(1, f"rms_norm_fp8: scales are float32 {[*groups]} with a contiguous last dimension, on x's device")
+    lds = scales.stride(0) if groups[0] > 1 else groups[1]
+    yp, ldy = (None, 0) if y_out is None else _rows(y_out, shape, bf16, index, "rms_norm_fp8", "y_out")
+    st = _on(index, (_lib or lib()).qg_rms_norm, *args, eps, weight_offset,
+             qg_norm_out(hp, ldh, yp, ldy, cp, ldc, scales.data_ptr(), lds, group))
     if st:
         raise QGError(st, "qg_rms_norm")
     return out, scales, sum_out
@@ -720,15 +725,17 @@ def lora(adapters: LoraAdapters, ids, x, y, out=None, workspace: Optional[Worksp
     """y plus each row's adapter's share (``qlora``): ids int32 [m] (-1: none), x bf16 [m, k] the projection's input, y bf16 [m, n]
     its output.  Without ``out`` y is changed in place."""
     import torch
+    bf16 = torch.bfloat16
     index, m = adapters.index, x.shape[0]
-    if index < 0 or ids.dtype is not torch.int32 or tuple(ids.shape) != (m,) or ids.get_device() != index or (m > 1 and ids.stride(0) != 1):
+    if index < 0 or ids.dtype is not torch.int32 or ids.shape != (m,) or ids.get_device() != index or (m > 1 and ids.stride(0) != 1):
         raise QGError(1, f"lora: contiguous int32 ids [{m}] on the adapters' CUDA device")
-    xp, ldx = _rows(x, m, adapters.k, torch.bfloat16, index, "lora: x")
-    yp, ldy = _rows(y, m, adapters.n, torch.bfloat16, index, "lora: y")
+    xp, ldx = _rows(x, (m, adapters.k), bf16, index, "lora", "x")
+    shape = m, adapters.n
+    yp, ldy = _rows(y, shape, bf16, index, "lora", "y")
     if out is None:
         out, op, ldo = y, yp, ldy
     else:
-        op, ldo = _rows(out, m, adapters.n, torch.bfloat16, index, "lora: out")
+        op, ldo = _rows(out, shape, bf16, index, "lora", "out")
     if workspace is None:
         workspace = Workspace(lora_workspace_size(adapters, m), x.device)
     elif workspace.index != index:
