@@ -28,7 +28,9 @@ namespace {
 constexpr int T = 128;      // rows of a tile
 constexpr int kWidth = 128;  // inputs or outputs of a chunk
 constexpr int kList = 16;    // tiles of a CTA in either phase
-constexpr int kStart = 4;    // chunks of expand that take as long as a tile's h
+// Chunks of expand that take as long as a tile's h: by the rank, 3 at 16 and 8 at 64 (measured: 2.8 and 7.7; four at any rank
+// leaves 8192 rows of rank 64 to 17408 outputs 133 us, this 129).
+__device__ __forceinline__ int start_chunks(int pitch) { return 1 + (7 * pitch + 32) / 64; }
 constexpr uint32_t kAtom = T * 128;  // bytes of 128 rows of 64 bf16
 
 // A bounded wait with one answer for the warp.
@@ -171,13 +173,14 @@ __global__ void __launch_bounds__(Shape<ATOMS>::kThreads, 1) lora_rows_kernel(Lo
   tl.count(p, T, bins, (p.m + 8 * S::kThreads - 1) / (8 * S::kThreads) * (8 * S::kThreads));
   const int n_adapter = tl.first[p.n_adapters], n_tiles = tl.first[p.n_adapters + 1];  // tiles with an adapter, which come first, and all
   const int k_chunks = (p.k + kWidth - 1) / kWidth, n_chunks = (p.n + kWidth - 1) / kWidth;
-  // In shrink a tile of few goes into about eight parts at most, as one CTA adds them all.  In expand a tile begins with kStart units
+  // In shrink a tile of few goes into about eight parts at most, as one CTA adds them all.  In expand a tile begins with `start` units
   // of no chunk: the time that its h takes.
-  const Line in_line(n_adapter * k_chunks, min((int)gridDim.x, 8 * n_adapter)), out_line(n_tiles * (n_chunks + kStart), gridDim.x);
+  const int start = start_chunks(sc.pitch);
+  const Line in_line(n_adapter * k_chunks, min((int)gridDim.x, 8 * n_adapter)), out_line(n_tiles * (n_chunks + start), gridDim.x);
   const int ku0 = in_line.begin(c), ku1 = in_line.begin(c + 1), kt0 = ku0 / k_chunks, kt1 = ku1 > ku0 ? (ku1 - 1) / k_chunks + 1 : kt0;
   const int nu0 = out_line.begin(c), nu1 = out_line.begin(c + 1);
-  int nt0 = nu0 / (n_chunks + kStart), ch = max(0, nu0 - nt0 * (n_chunks + kStart) - kStart);  // expand's first tile and chunk
-  const int nt_last = nu1 / (n_chunks + kStart), ch_last = max(0, nu1 - nt_last * (n_chunks + kStart) - kStart);
+  int nt0 = nu0 / (n_chunks + start), ch = max(0, nu0 - nt0 * (n_chunks + start) - start);  // expand's first tile and chunk
+  const int nt_last = nu1 / (n_chunks + start), ch_last = max(0, nu1 - nt_last * (n_chunks + start) - start);
   const int nt1 = nt_last + (ch_last > 0), n = (nt_last - nt0) * n_chunks + ch_last - ch;  // past its last tile; its chunks
   // Each adapter's rows in ascending order to the places that they have in this CTA's tiles.  A lane looks at eight rows side
   // by side, a warp at 256 (more than 4352 rows: a run of such blocks); how many there are before them comes from a sum

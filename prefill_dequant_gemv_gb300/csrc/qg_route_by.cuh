@@ -157,17 +157,33 @@ __device__ __forceinline__ double exact_inverse(const RouteRule& r, const float*
   return 1.0 / s;
 }
 
-// The topk of `count` (k to 32) experts in `list` by their values in 64 bits, one a lane: as route_exact.
-__device__ __noinline__ void route_listed(const RouteRule& r, const float* lg, int E, int k, float m, const int* list, int count,
-                                          int* slot, int* id) {
+// The topk of `count` (k to 32) experts in `list` by their values in 64 bits, one a lane: as route_exact.  The sum of a softmax is
+// the dear part: first `near_inv`, its inverse in fp32, is taken for it, whose error is one factor of all s and so moves c_i
+// against c_j by less than 2^-18 |s_i - s_j|; the sum is redone in 64 bits if two values are not further apart than that
+// (and equal logits and biases are not the reason).
+__device__ __noinline__ void route_listed(const RouteRule& r, const float* lg, int E, int k, float m, float near_inv, const int* list,
+                                          int count, int* slot, int* id) {
   const int lane = threadIdx.x & 31, e = lane < count ? list[lane] : 1 << 20;
-  const double inv = exact_inverse(r, lg, E, m);
-  const double d = lane < count ? score_of(r, lg[e], m, inv) + (r.bias ? (double)r.bias[e] : 0.0) : -(double)INFINITY;
-  int rank = 0;
-  for (int i = 0; i < count; ++i) {
-    const double o = __shfl_sync(0xFFFFFFFFu, d, i);
-    const int oe = __shfl_sync(0xFFFFFFFFu, e, i);
-    rank += o > d || (o == d && oe < e);
+  const float l = lane < count ? lg[e] : 0.0f, b = lane < count && r.bias ? r.bias[e] : 0.0f;
+  const double s1 = score_of(r, l, m, 1.0);
+  double s = r.sigmoid ? s1 : s1 * (double)near_inv;
+  int rank;
+  for (int turn = 0; turn < 2; ++turn) {
+    const double d = lane < count ? s + (double)b : -(double)INFINITY;
+    bool doubt = false;
+    rank = 0;
+    for (int i = 0; i < count; ++i) {
+      const double o = __shfl_sync(0xFFFFFFFFu, d, i);
+      const int oe = __shfl_sync(0xFFFFFFFFu, e, i);
+      rank += o > d || (o == d && oe < e);
+      if (!r.sigmoid && !turn) {
+        const double os = __shfl_sync(0xFFFFFFFFu, s, i);
+        const float ol = __shfl_sync(0xFFFFFFFFu, l, i), ob = __shfl_sync(0xFFFFFFFFu, b, i);
+        doubt |= !(fabs(o - d) > 0x1p-18 * fabs(os - s) + 0x1p-48 * fabs(d)) && !(ol == l && ob == b);
+      }
+    }
+    if (r.sigmoid || turn || !__any_sync(0xFFFFFFFFu, doubt && lane < count)) break;
+    s = s1 * exact_inverse(r, lg, E, m);
   }
   *slot = lane < count && rank < k ? rank : -1;
   *id = e;
@@ -204,7 +220,7 @@ __device__ __forceinline__ int list_experts(uint32_t mask, int* list) {
 }
 
 // A warp's choice for one token of up to 32 S experts: ids and weights, and a copy of the ids and a count of them in hist
-// where they are given.  `cs`: 32 S floats of shared memory, the warp's own.  Of the logits and biases only the choice values
+// where they are given.  `cs`: 32 S + 32 floats of shared memory, the warp's own.  Of the logits and biases only the choice values
 // stay in registers (three blocks of warps an SM instead of two); what is rare reads them again.
 template <int S>
 __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, int E, int k, float* cs, int32_t* ids, float* wts,
@@ -268,10 +284,13 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
 #pragma unroll
         for (int i = 0; i < S; ++i)
           if (lane + 32 * i < E && c[i] >= cs[group_of(r, lane + 32 * i)]) best |= 1u << i;
-        int* list = reinterpret_cast<int*>(cs) + 32;
+        int* list = reinterpret_cast<int*>(cs) + 32 * S;
         const int count = list_experts(best, list);
         doubt = count > 32;
         if (!doubt) groups = groups_listed(r, lg, E, m, list, count);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < S; ++i) cs[lane + 32 * i] = c[i];  // (the groups' values lay there)
       }
     }
     open = 0;
@@ -279,47 +298,83 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
     for (int i = 0; i < S; ++i) {
       const bool in = groups >> (group_of(r, lane + 32 * i) & 31) & 1;  // past the experts: any
       open |= in ? 1u << i : 0u;
+      c[i] = in ? c[i] : __int_as_float(0x7FC00000);
     }
     __syncwarp();
   }
-  int slot = lane < k ? lane : -1, id = 0;
-  {
+  int slot = -1, id = 0;
+  // The winners are among the candidates: the experts that come up to the k-th largest of the lanes' largest values, or within
+  // the tolerance of it.  They are some k to 2 k, one a lane, and each counts those before it.
+  int* list = reinterpret_cast<int*>(cs) + 32 * S;
+  int count = 0;
+  if (!doubt) {
+    float best = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < S; ++i) best = fmaxf(best, c[i]);  // a NaN is passed over
+    uint32_t key = order_key(best), kth = 0u;
+    for (int j = 0; j < k; ++j) {
+      kth = __reduce_max_sync(0xFFFFFFFFu, key);
+      key = key == kth ? 0u : key;
+    }
+    const float top = key_value(kth), least = top - (near + (r.values ? 0x1p-22f * fabsf(top) : 0.0f));
+    uint32_t may = 0;
+#pragma unroll
+    for (int i = 0; i < S; ++i) may |= c[i] >= least ? 1u << i : 0u;
+    if (r.n_groups == 1) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) cs[lane + 32 * i] = c[i];
+    }
+    count = list_experts(may, list);
+  }
+  if (count >= k && count <= 32) {
+    const int e = lane < count ? list[lane] : 1 << 20;
+    const float v = lane < count ? cs[e] : -INFINITY, tol = near + 0x1p-22f * fabsf(v);
+    int rank = 0, close = 0;
+    for (int i = 0; i < count; ++i) {
+      const float o = __shfl_sync(0xFFFFFFFFu, v, i);
+      const int oe = __shfl_sync(0xFFFFFFFFu, e, i);
+      rank += o > v || (o == v && oe < e);
+      close += fabsf(o - v) <= tol;
+    }
+    slot = lane < count && rank < k ? rank : -1;
+    id = e;
+    if (r.values && __any_sync(0xFFFFFFFFu, slot >= 0 && close > 1)) {
+      // equal values of equal logits and biases are ties indeed, and the lower index has come first
+      const float l = lane < count ? lg[e] : 0.0f, b = lane < count && r.bias ? r.bias[e] : 0.0f;
+      bool other = false;
+      for (int i = 0; i < count; ++i) {
+        const float o = __shfl_sync(0xFFFFFFFFu, v, i), ol = __shfl_sync(0xFFFFFFFFu, l, i), ob = __shfl_sync(0xFFFFFFFFu, b, i);
+        other |= fabsf(o - v) <= tol && !(ol == l && ob == b);
+      }
+      if (__any_sync(0xFFFFFFFFu, slot >= 0 && other)) route_listed(r, lg, E, k, m, inv, list, count, &slot, &id);
+    }
+  } else if (!doubt) {  // many equal values, or fewer numbers than winners
     uint32_t key[S], mine, top;
 #pragma unroll
     for (int i = 0; i < S; ++i) key[i] = lane + 32 * i < E && (open >> i & 1) ? order_key(c[i]) : 0u;
     warp_topk_keys(key, k, mine, id, top);
-    if (r.values && !doubt) {
+    slot = lane < k ? lane : -1;
+    if (r.values) {
+      // equal values of equal logits and biases are ties; any other two that are near each other, among the winners or the
+      // last of them and the rest, are decided in 64 bits
       const float v = key_value(mine), vk = __shfl_sync(0xFFFFFFFFu, v, k - 1);
-      // two winners in a row that are near each other; experts at the last winner's value or less than the tolerance below
-      // it, which are k where no other comes near the winners
       const float vn = __shfl_down_sync(0xFFFFFFFFu, v, 1), least = vk - (near + 0x1p-22f * fabsf(vk));
-      const bool close = lane + 1 < k && v - vn <= near + 0x1p-22f * fabsf(v);
-      uint32_t may = 0;
+      const float lm = lane < k ? lg[id] : 0.0f, bm = lane < k && r.bias ? r.bias[id] : 0.0f;
+      const float lk = __shfl_sync(0xFFFFFFFFu, lm, k - 1), bk = __shfl_sync(0xFFFFFFFFu, bm, k - 1);
+      const float ln = __shfl_down_sync(0xFFFFFFFFu, lm, 1), bn = __shfl_down_sync(0xFFFFFFFFu, bm, 1);
+      const bool close = lane + 1 < k && v - vn <= near + 0x1p-22f * fabsf(v) && !(lm == ln && bm == bn);
+      uint32_t other = 0;
 #pragma unroll
-      for (int i = 0; i < S; ++i) may |= c[i] >= least ? 1u << i : 0u;
-      may &= open;
-      if (__any_sync(0xFFFFFFFFu, close) || __reduce_add_sync(0xFFFFFFFFu, __popc(may)) > k) {
-        // equal values of equal logits and biases are ties indeed, and the lower index has come first
-        const float lm = lane < k ? lg[id] : 0.0f, bm = lane < k && r.bias ? r.bias[id] : 0.0f;
-        const float lk = __shfl_sync(0xFFFFFFFFu, lm, k - 1), bk = __shfl_sync(0xFFFFFFFFu, bm, k - 1);
-        const float ln = __shfl_down_sync(0xFFFFFFFFu, lm, 1), bn = __shfl_down_sync(0xFFFFFFFFu, bm, 1);
-        uint32_t other = 0;
-        for (int i = 0; i < S; ++i) {
-          const int e = lane + 32 * i;
-          if ((may >> i & 1) && !(lg[e] == lk && (!r.bias || r.bias[e] == bk))) other |= 1u << i;
-        }
-        const int others = __reduce_add_sync(0xFFFFFFFFu, __popc(other));
-        const int chosen = __popc(__ballot_sync(0xFFFFFFFFu, lane < k && v >= least && !(lm == lk && bm == bk)));
-        if (__any_sync(0xFFFFFFFFu, close && !(lm == ln && bm == bn)) || others != chosen) {
-          int* list = reinterpret_cast<int*>(cs);
-          const int count = list_experts(may, list);
-          doubt = count > 32 || count < k;
-          if (!doubt) route_listed(r, lg, E, k, m, list, count, &slot, &id);
-          __syncwarp();
-        }
+      for (int i = 0; i < S; ++i) {
+        const int e = lane + 32 * i;
+        if (c[i] >= least && !(lg[e] == lk && (!r.bias || r.bias[e] == bk))) other |= 1u << i;
       }
+      const int others = __reduce_add_sync(0xFFFFFFFFu, __popc(other));
+      const int chosen = __popc(__ballot_sync(0xFFFFFFFFu, lane < k && v >= least && !(lm == lk && bm == bk)));
+      doubt = __any_sync(0xFFFFFFFFu, close) || others != chosen;
     }
   }
+  __syncwarp();
   if (doubt) route_exact(r, lg, E, k, &slot, &id);
   // weights of the winners, in fp32
   const float lw = slot >= 0 ? lg[id] : 0.0f;

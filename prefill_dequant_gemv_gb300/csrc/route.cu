@@ -73,7 +73,7 @@ template <int S, bool BY>
 __global__ void __launch_bounds__(256, 3) route_topk_kernel(const float* logits, int64_t T, int E, int k, int tokens, int32_t* ids,
                                                          float* wts, RouteView r, RouteRule rule) {
   __shared__ int hist[32 * S];
-  __shared__ float cs[BY ? 8 : 1][BY ? 32 * S : 1];
+  __shared__ float cs[BY ? 8 : 1][BY ? 32 * S + 32 : 1];
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) pdl_launch_dependents();
   for (int e = threadIdx.x; e < E; e += 256) hist[e] = 0;
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(BY ? kMaxExperts : kRouteBlock) route_small_ke
   zero_shared(&wc[0][0], sizeof(wc));
   pdl_wait();
   if constexpr (BY) {
-    __shared__ float cs[kRouteBySmall][32 * BY];
+    __shared__ float cs[kRouteBySmall][32 * BY + 32];
     if (warp < T)
       warp_route<BY>(rule, logits + (int64_t)warp * E, E, k, cs[warp], ids + warp * k, wts + warp * k, s_ids + warp * k, nullptr);
   } else {
