@@ -222,6 +222,13 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
       const int c = c0 + i * T * 8;
       const Vec g = kHold ? w[kHold ? i : 0] : load8(a.w, c, k);
       float v[8];
+      if (FP8 == 0 || a.y) {  // the same bits with codes and without
+        scaled(h[i], g, inv, a.woff, v);
+        Vec o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
+        store8(a.y + r * a.ldy, c, k, o);
+      }
       if (FP8 == 1) {
         // NaN does not enter a maximum.  What lies past the row's end is 0.
         first = 1.0f, then = inv;
@@ -234,17 +241,10 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
         }
         const float s = step(amax);
         if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + (c >> a.group_log2)] = s;
-      } else {
-        scaled(h[i], g, FP8 ? first : inv, a.woff, v);
+      } else if (FP8 == 2) {
+        scaled(h[i], g, first, a.woff, v);
       }
       if (FP8) store_codes(a, r, c, k, v, t);
-      if (FP8 == 0 || a.y) {  // the same bits with codes and without
-        if (FP8) scaled(h[i], g, inv, a.woff, v);
-        Vec o;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
-        store8(a.y + r * a.ldy, c, k, o);
-      }
     }
   }
 }
