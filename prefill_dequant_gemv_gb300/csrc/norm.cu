@@ -3,13 +3,17 @@
 //   h = bf16(x + residual),  y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset)
 //   scale = max(amax / 448, 2^-100) of a group of y (or a row),  code = E4M3(y / scale)
 //
-// A row belongs to one CTA and a thread holds NV vectors of eight of its elements in
-// registers, so that x and the residual are read once and the sum is written in the same
-// pass.  The row's sum of squares (and, with one scale a row, its largest magnitude) goes
-// through warp shuffles and one shared-memory exchange whose slots alternate from row to
-// row: one barrier a row and reduction, and every thread adds the warps' sums in the same
-// order.  A group of 32, 64 or 128 elements lies in 4, 8 or 16 neighbouring lanes, so its
-// scale needs shuffles only.
+// A row belongs to one CTA and a thread holds one or two vectors of eight of its elements in registers (a row of more than
+// 16384: in shared memory), so that x and the residual are read once and the sum is written in the same pass.  CTAs stay
+// for row after row, the next row's loads under way while one is summed and stored: what bounds many rows is HBM, and
+// with codes the instructions (with one scale a row issue 73%), a few rows the chain load - sum - store.  The row's sum of squares
+// (and, with one scale a row, its largest magnitude, of h * weight, as 1 / sqrt is not there yet) goes through warp
+// shuffles and one shared-memory exchange whose slots alternate from row to row: one barrier a row, and every thread adds the warps'
+// sums in the same order.  A group of 32, 64 or 128 elements lies in 4, 8 or 16 neighbouring lanes, so its scale needs shuffles only.
+//
+// Measured with residual, in a graph (share of the bytes at the copy rate, 6798 GB/s): one row of 5120 2.0 us, 64 to E4M3 in groups of
+// 128 2.2; 4096 x 5120 27.5 us (90%), to E4M3 in groups 26.0 (83%), one scale a row 29.4 (73%); 18001 x 2048 48.1 (90%), 41.0 (92%) and
+// 43.9 (86%); 2000 x 17408 48 (85%), 57 (63%) and 55 (65%).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -25,6 +29,10 @@
 namespace qg {
 namespace {
 
+constexpr int kLongThreads = 768;  // for a row in shared memory: 2000 x 17408 to bf16 48 us (512 threads, three CTAs an SM: 50; 256: 52 to 58)
+constexpr int kLongAhead = 2;      // and the vectors that a thread loads at a time (four: 52 us, fewer CTAs)
+// of the longest row, rounded up to whole turns of the threads
+constexpr size_t kLongBytes = (kNormMaxCols + 8 * kLongThreads - 1) / (8 * kLongThreads) * kLongThreads * 16;
 constexpr float kScaleMin = 0x1p-100f;  // keeps 1 / scale finite for a group of zeros
 
 struct Vec {
@@ -169,8 +177,12 @@ __device__ __forceinline__ float group_max(float m, int lanes) {
   return m;
 }
 
-template <int NV, bool RES, int FP8>  // FP8: 0 bf16 only, 1 a scale a group, 2 a scale a row
-__global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
+// FP8: 0 bf16 only, 1 a scale a group, 2 a scale a row.  NV: vectors a thread; 0: the row lies in shared memory, as
+// many a thread as it takes.
+template <int NV, bool RES, int FP8>
+__global__ void __launch_bounds__(NV ? 1024 : kLongThreads, NV ? 1 : 2) rms_norm_kernel(NormArgs a) {
+  constexpr bool LONG = NV == 0;
+  constexpr int kRegs = LONG ? kLongAhead : NV;
   __shared__ __align__(16) float slots[2][2][32];
   if (threadIdx.x < 128) (&slots[0][0][0])[threadIdx.x] = 0.0f;
   if (blockDim.x < 128)
@@ -180,51 +192,72 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
   pdl_wait();
   const int k = (int)a.k, T = blockDim.x, c0 = threadIdx.x * 8;
   constexpr bool P = FP8 == 2;
-  constexpr bool kAhead = NV <= 2;               // registers for the next row
-  constexpr bool kHold = kAhead && FP8 != 2;     // and for the weights (one scale a row takes others)
-  Vec w[kHold ? NV : 1], x[NV], q[NV];
-  auto load = [&](int64_t r) {
+  constexpr bool kHold = !LONG && FP8 != 2;  // registers for the weights (one scale a row takes others)
+  extern __shared__ __align__(16) Vec held[];  // LONG: a thread's own vectors
+  const int n = LONG ? (int)((a.k + 8 * T - 1) / (8 * T)) : NV;
+  Vec w[kHold ? kRegs : 1], x[kRegs], q[kRegs], h[LONG ? 1 : kRegs];
+  auto load = [&](int64_t r, int i0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      x[i] = load8(a.x + r * a.ldx, c0 + i * T * 8, k);
-      if (RES) q[i] = load8(a.res + r * a.ldr, c0 + i * T * 8, k);
+    for (int i = 0; i < kRegs; ++i) {
+      x[i] = load8(a.x + r * a.ldx, c0 + (i0 + i) * T * 8, k);
+      if (RES) q[i] = load8(a.res + r * a.ldr, c0 + (i0 + i) * T * 8, k);
     }
   };
   if (kHold) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) w[kHold ? i : 0] = load8(a.w, c0 + i * T * 8, k);
+    for (int i = 0; i < kRegs; ++i) w[kHold ? i : 0] = load8(a.w, c0 + i * T * 8, k);
   }
-  if (kAhead) load(blockIdx.x);
+  auto weight = [&](int i) { return kHold ? w[kHold ? i : 0] : load8(a.w, c0 + i * T * 8, k); };
+  auto value = [&](int i) {
+    if constexpr (LONG) return held[i * T + threadIdx.x];
+    else return h[i];
+  };
+  if (!LONG) load(blockIdx.x, 0);
   int turn = 0;
   for (int64_t r = blockIdx.x; r < a.m; r += gridDim.x, turn ^= 1) {
-    Vec h[NV];
     float2 sq2 = twice(0.0f);
-    if (!kAhead) load(r);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      h[i] = x[i];
+    float amax = 0.0f;
+    auto take = [&](int i, Vec& v) {  // vector i of the row, its residual added: stored, squared
       if (RES) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 f = add2<P>(both(x[i].w[j]), both(q[i].w[j]));
-          h[i].w[j] = pack_bf16(f.x, f.y);
+          const float2 f = add2<P>(both(x[i % kRegs].w[j]), both(q[i % kRegs].w[j]));
+          v.w[j] = pack_bf16(f.x, f.y);
+        }
+      } else {
+        v = x[i % kRegs];
+      }
+    };
+    auto square = [&](int i, const Vec& v) {
+      if (RES && a.sum) store8(a.sum + r * a.ldh, c0 + i * T * 8, k, v);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sq2 = add_squares<P>(both(v.w[j]), sq2);
+    };
+    if constexpr (LONG) {
+      for (int i0 = 0; i0 < n; i0 += kRegs) {
+        load(r, i0);
+#pragma unroll
+        for (int i = 0; i < kRegs; ++i) {
+          if (i0 + i >= n) break;
+          Vec v;
+          take(i, v);
+          held[(i0 + i) * T + threadIdx.x] = v;
+          square(i0 + i, v);
         }
       }
-    }
-    if (kAhead && r + gridDim.x < a.m) load(r + gridDim.x);  // while this row is summed and stored
+    } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (RES && a.sum) store8(a.sum + r * a.ldh, c0 + i * T * 8, k, h[i]);
+      for (int i = 0; i < kRegs; ++i) take(i, h[i]);
+      if (r + gridDim.x < a.m) load(r + gridDim.x, 0);  // while this row is summed and stored
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sq2 = add_squares<P>(both(h[i].w[j]), sq2);
+      for (int i = 0; i < kRegs; ++i) square(i, h[i]);
     }
-    float sq = sq2.x + sq2.y, amax = 0.0f;
+    float sq = sq2.x + sq2.y;
     if (FP8 == 2) {  // of h times the weight: 1 / sqrt is not there yet
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const Vec g = kHold ? w[kHold ? i : 0] : load8(a.w, c0 + i * T * 8, k);
+#pragma unroll(LONG ? 2 : NV)
+      for (int i = 0; i < n; ++i) {
         float2 v[4];
-        scaled<P, false>(h[i], g, 1.0f, a.woff, v);
+        scaled<P, false>(value(i), weight(i), 1.0f, a.woff, v);
         amax = fmaxf(amax, largest(v, false));
       }
     }
@@ -241,9 +274,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
     if (FP8 == 2) {
       if (!in_range(amax, inv)) {  // the same for the block
         first = inv, then = 1.0f, amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          amax = fmaxf(amax, largest_value(h[i], kHold ? w[kHold ? i : 0] : load8(a.w, c0 + i * T * 8, k), inv, a.woff));
+#pragma unroll(LONG ? 1 : NV)
+        for (int i = 0; i < n; ++i) amax = fmaxf(amax, largest_value(value(i), weight(i), inv, a.woff));
         float none = 0.0f;
         __syncthreads();
         block_reduce<true>(none, amax, slots[0][turn], slots[1][turn]);
@@ -251,13 +283,13 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
       const float s = step(amax);
       if (threadIdx.x == 0) a.scales[r * a.lds] = s;
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
+#pragma unroll(LONG ? 2 : NV)
+    for (int i = 0; i < n; ++i) {
       const int c = c0 + i * T * 8;
-      const Vec g = kHold ? w[kHold ? i : 0] : load8(a.w, c, k);
+      const Vec g = weight(i), f = value(i);
       float2 v[4];
       if (FP8 == 0 || a.y) {  // the same bits with codes and without
-        scaled<P, true>(h[i], g, inv, a.woff, v);
+        scaled<P, true>(f, g, inv, a.woff, v);
         Vec o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) o.w[j] = pack_bf16(v[j].x, v[j].y);
@@ -266,17 +298,17 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
       if (FP8 == 1) {
         // NaN does not enter a maximum.  What lies past the row's end is 0.
         first = 1.0f, then = inv;
-        scaled<P, false>(h[i], g, 1.0f, a.woff, v);
+        scaled<P, false>(f, g, 1.0f, a.woff, v);
         amax = group_max(largest(v, false), a.group_lanes);
         if (__any_sync(0xFFFFFFFFu, !in_range(amax, inv))) {
           first = inv, then = 1.0f;
-          scaled<P, true>(h[i], g, inv, a.woff, v);
+          scaled<P, true>(f, g, inv, a.woff, v);
           amax = group_max(largest(v, true), a.group_lanes);
         }
         const float s = step(amax);
         if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + (c >> a.group_log2)] = s;
       } else if (FP8 == 2) {
-        scaled<P, true>(h[i], g, first, a.woff, v);
+        scaled<P, true>(f, g, first, a.woff, v);
       }
       if (FP8) store_codes<P>(a, r, c, k, v, t);
     }
@@ -285,15 +317,20 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a) {
 
 template <int NV, bool RES, int FP8>
 int launch(const NormArgs& a, const DeviceInfo& dev, int threads, cudaStream_t s) {
-  static std::atomic<int> per_sm[33];  // CTAs an SM by warps a CTA: asked once
-  int n = per_sm[threads / 32].load();
+  // CTAs an SM by warps a CTA (NV 0: by vectors a thread), asked once; the GPUs that this is built for are alike
+  static std::atomic<int> per_sm[33];
+  static std::atomic<unsigned long long> allowed{0};
+  const int vecs = NV ? 0 : (int)((a.k + 8 * threads - 1) / (8 * threads)), at = NV ? threads / 32 : vecs;
+  const size_t smem = (size_t)vecs * threads * sizeof(Vec);
+  if (NV == 0 && !allow_smem((const void*)rms_norm_kernel<NV, RES, FP8>, kLongBytes, allowed)) return QG_ERR_CUDA;
+  int n = per_sm[at].load();
   if (n == 0) {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rms_norm_kernel<NV, RES, FP8>, threads, 0) != cudaSuccess || n < 1)
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, rms_norm_kernel<NV, RES, FP8>, threads, smem) != cudaSuccess || n < 1)
       return QG_ERR_CUDA;
-    per_sm[threads / 32].store(n);
+    per_sm[at].store(n);
   }
   const int64_t resident = (int64_t)dev.sms * n;
-  if (launch_pdl(rms_norm_kernel<NV, RES, FP8>, dim3((unsigned)std::min(a.m, resident)), dim3(threads), 0, s, a) != cudaSuccess)
+  if (launch_pdl(rms_norm_kernel<NV, RES, FP8>, dim3((unsigned)std::min(a.m, resident)), dim3(threads), smem, s, a) != cudaSuccess)
     return QG_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
@@ -314,11 +351,11 @@ int launch_rms_norm(const NormArgs& a, const DeviceInfo& dev, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t vecs = (a.k + 7) / 8;
   // Two vectors a thread where rows queue up (4096 x 5120: 27 us, one vector 31, four 28); one where every row has a CTA of its
-  // own (64 x 5120 to E4M3: 2.3 us, two vectors 3.4); more where the row takes more than 1024 threads.
-  const int nv = vecs <= 1024 && a.m <= dev.sms ? 1 : vecs <= 2048 ? 2 : vecs <= 4096 ? 4 : 8;
+  // own (64 x 5120 to E4M3: 2.2 us, two vectors 3.4); by way of shared memory what 1024 threads do not hold so.
+  const int nv = vecs <= 1024 && a.m <= dev.sms ? 1 : vecs <= 2048 ? 2 : 0;
+  if (nv == 0) return launch_nv<0>(a, dev, kLongThreads, s);
   const int threads = (int)((vecs + nv - 1) / nv + 31) / 32 * 32;
-  return nv == 1 ? launch_nv<1>(a, dev, threads, s) : nv == 2 ? launch_nv<2>(a, dev, threads, s)
-         : nv == 4 ? launch_nv<4>(a, dev, threads, s) : launch_nv<8>(a, dev, threads, s);
+  return nv == 1 ? launch_nv<1>(a, dev, threads, s) : launch_nv<2>(a, dev, threads, s);
 }
 
 }  // namespace qg

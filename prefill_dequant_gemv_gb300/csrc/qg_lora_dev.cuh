@@ -6,23 +6,10 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include <atomic>
-
 #include "qg_lora.h"
 #include "qg_sync.cuh"
 
 namespace qg {
-
-// Lets a kernel have `bytes` of dynamic shared memory on the current device; once a device and kernel (`done`).
-inline bool allow_smem(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return false;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (done.load() & bit) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
-  done.fetch_or(bit);
-  return true;
-}
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {

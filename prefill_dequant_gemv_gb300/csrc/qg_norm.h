@@ -7,7 +7,7 @@
 
 namespace qg {
 
-constexpr int64_t kNormMaxCols = 65536;  // 1024 threads of eight vectors of eight
+constexpr int64_t kNormMaxCols = 65536;  // a row of bf16 in shared memory
 
 struct NormArgs {
   const uint16_t* x;

@@ -7,7 +7,20 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace qg {
+
+// Lets a kernel have `bytes` of dynamic shared memory on the current device; once a device and kernel (`done`).
+inline bool allow_smem(const void* kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return false;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load() & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess) return false;
+  done.fetch_or(bit);
+  return true;
+}
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
 constexpr int kStatusTimeout = 6;                           // QG_ERR_TIMEOUT

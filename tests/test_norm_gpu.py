@@ -183,3 +183,19 @@ def test_two_streams_at_once(group):
     torch.cuda.synchronize()
     for g in got:
         assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip((t.contiguous() for t in g), (t.contiguous() for t in want)))
+
+
+@pytest.mark.parametrize("group", [None, 0, 32, 128])
+@pytest.mark.parametrize("m,k", [(400, 16392), (153, 24577), (307, 65536)])
+def test_long_rows_in_turn(m, k, group):
+    """Rows too long for registers, more of them than CTAs, in place."""
+    q = qlib()
+    x, r, w = matrix(m, k, k), matrix(m, k, k + 1, 2.0), matrix(1, k, 3)[0]
+    want_h, want = ol.rms_norm(to_f64(x), to_f64(r), to_f64(w), 1e-6, 0.0)
+    if group is None:
+        y, h = q.rms_norm(x, w, r, out=x, sum_out=r)
+        check_y(y, want)
+    else:
+        codes, scales, h = q.rms_norm_fp8(x, w, r, group=group, sum_out=r)
+        check_codes(codes, scales, want, group)
+    assert np.array_equal(to_f64(h), want_h)
