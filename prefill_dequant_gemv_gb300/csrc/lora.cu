@@ -43,7 +43,8 @@ template <int R>
 struct Shape {
   static constexpr int kHalves = R == 128 ? 2 : 1;              // warps that share the ranks of a step of phase 1
   static constexpr int kRanks = R / kHalves;                    // of a warp
-  static constexpr int kGroups = kWarps / kHalves;              // warps that share the inputs
+  static constexpr int kLogGroups = R == 128 ? 2 : 3, kGroups = 1 << kLogGroups;  // warps that share the inputs
+  static_assert(kGroups == kWarps / kHalves, "");
   static constexpr int kPieces = R / 8;                         // of 16 bytes in a row of B
   static constexpr int kSteps = R == 16 ? 1 : R / 32;           // of products over the ranks in phase 2
   // bytes a warp: 64 inputs of x's 16 rows and A's, or 64 outputs of y's rows and B's (rank 128: 32 outputs)
@@ -77,8 +78,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   uint32_t n_cta;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n_cta));
-  const uint32_t rank = cluster_rank();
-  const int cluster = blockIdx.x / n_cta, n_clusters = gridDim.x / n_cta;
+  const int log_n = __ffs(n_cta) - 1, cluster = blockIdx.x >> log_n, n_clusters = gridDim.x >> log_n;  // a power of two
   uint8_t* mine = smem + (size_t)warp * S::kAhead * S::kSlot;
   const uint32_t mine_at = smem_u32(mine);
   const bool in_place = p.out == p.y;
@@ -105,20 +105,38 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
   int n_tiles;
   const int number = block_prefix<kThreads>(first, warp_sums, &n_tiles);
 
-  for (int tile = cluster; tile < n_tiles; tile += n_clusters) {
+  // A cluster's CTAs work on one tile, or where there are more tiles than clusters in teams of half of them or fewer, each on
+  // its own tile.  The teams of a cluster keep step (its barrier is the whole cluster's).
+  int log_team = log_n;
+  while (log_team > 0 && n_tiles > n_clusters << (log_n - log_team)) --log_team;
+  const int team = 1 << log_team, rank = (int)cluster_rank() & (team - 1), lead = (int)cluster_rank() - rank;
+  const int teams = n_clusters << (log_n - log_team);
+  for (int at = 0; at < n_tiles; at += teams) {
+    const int tile = at + (cluster << (log_n - log_team)) + (lead >> log_team);
     if (first && number == tile) found[0] = id, found[1] = place;
+    if (tid == 0 && tile >= n_tiles) found[0] = -2, found[1] = 0;  // no tile
     if (tid < T) rows[tid] = -1;
     __syncthreads();
     const int e = found[0], place0 = found[1];
+    if (e == -2) {
+      if (team > 1) {
+        cluster_arrive();
+        cluster_wait();
+        cluster_arrive();
+        cluster_wait();
+      }
+      __syncthreads();
+      continue;
+    }
     if (id == e && place >= place0 && place < place0 + T) rows[place - place0] = tid;
     const int ra = e < 0 ? 0 : rank_of(p, e);
     __syncthreads();
     // phase 1 in steps of 64 inputs, phase 2 in chunks of kOuts outputs: this warp's
     const int half = warp % S::kHalves, group = warp / S::kHalves, rank0 = half * S::kRanks;
-    const int steps = ra ? (p.k + 63) / 64 : 0, groups = (int)n_cta * S::kGroups, me = (int)rank * S::kGroups + group;
-    const int s0 = steps * me / groups, n1 = steps * (me + 1) / groups - s0;
+    const int steps = ra ? (p.k + 63) / 64 : 0, me = rank * S::kGroups + group, all = log_team + S::kLogGroups;
+    const int s0 = steps * me >> all, n1 = (steps * (me + 1) >> all) - s0;
     const int chunks = (p.n + S::kOuts - 1) / S::kOuts;
-    const int c0 = chunks * (int)rank / (int)n_cta, c1 = chunks * ((int)rank + 1) / (int)n_cta;
+    const int c0 = chunks * rank >> log_team, c1 = chunks * (rank + 1) >> log_team;
     const int n2 = c0 + warp < c1 ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0, n = n1 + n2;
     // The copies' state.  A lane copies piece lane % 8 of every fourth row of x, A and y, so that a copy takes whole lines; and
     // of B, whose rows are shorter or longer, every 32nd piece.  A pointer may run past its row's end, or stand on a row that is
@@ -216,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
         for (int i = 0; i < S::kRanks / 8; ++i) *reinterpret_cast<float2*>(to_part + 8 * i) = make_float2(acc[i][2 * h], acc[i][2 * h + 1]);
       }
       __syncthreads();
-      // the CTA's sum over its warps, then the cluster's over its CTAs, both in order; of the rows that there are
+      // the CTA's sum over its warps, then the team's over its CTAs, both in order; of the rows that there are
       const int live = __popc(__ballot_sync(0xFFFFFFFFu, rows[lane & 15] >= 0) & 0xFFFFu);
       for (int i = tid; i < live * R / 4; i += kThreads) {
         float* at = part + (i / (R / 4)) * S::kPartRow + (i % (R / 4)) * 4;
@@ -228,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
         }
         *reinterpret_cast<float4*>(at) = v;
       }
-      if (n_cta > 1) {
+      if (team > 1) {
         cluster_arrive();
         cluster_wait();
       } else {
@@ -242,16 +260,16 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
           const float* at = part + r * S::kPartRow + col;
           float4 o[8][2];
 #pragma unroll
-          for (uint32_t c = 0; c < 8; ++c)  // a cluster has up to eight CTAs
-            if (c < n_cta) {
-              const uint32_t there = cluster_map(at, c);
+          for (int c = 0; c < 8; ++c)  // a team has up to eight CTAs
+            if (c < team) {
+              const uint32_t there = cluster_map(at, (uint32_t)(lead + c));
               o[c][0] = ld_cluster_f4(there);
               o[c][1] = ld_cluster_f4(there + 16);
             }
           float v[8] = {};
 #pragma unroll
-          for (uint32_t c = 0; c < 8; ++c)
-            if (c < n_cta) {
+          for (int c = 0; c < 8; ++c)
+            if (c < team) {
               v[0] += o[c][0].x, v[1] += o[c][0].y, v[2] += o[c][0].z, v[3] += o[c][0].w;
               v[4] += o[c][1].x, v[5] += o[c][1].y, v[6] += o[c][1].z, v[7] += o[c][1].w;
             }
@@ -262,8 +280,12 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
       }
       __syncthreads();
     }
+    if (ra == 0 && team > 1) {
+      cluster_arrive();
+      cluster_wait();
+    }
     // no CTA writes its sums again, or ends, before every CTA has read them
-    if (n_cta > 1) cluster_arrive();
+    if (team > 1) cluster_arrive();
 
     const int row[2] = {rows[g], rows[g + 8]};
     int col = (c0 + warp) * S::kOuts + 8 * t;
@@ -333,7 +355,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
       col += S::kOuts * kWarps;
     }
     copy_wait<0>();
-    if (n_cta > 1) cluster_wait();
+    if (team > 1) cluster_wait();
     __syncthreads();  // every warp is done with the tile's rows
   }
 }
@@ -343,17 +365,13 @@ int launch(const LoraArgs& p, const DeviceInfo& dev, cudaStream_t s) {
   using S = Shape<R>;
   static std::atomic<unsigned long long> configured{0};
   if (!allow_smem((const void*)lora_kernel<R>, S::kSmem, configured)) return QG_ERR_CUDA;
-  // About as many tiles as there are: full ones, or one for each adapter.
-  // So many adapters are met where every row draws its own.
+  // The tiles are counted on the device.  About as many: full ones, or one for each adapter that is met where every row draws its
+  // own.  The GPU's partitions hold 15 clusters of eight such CTAs and 36 of four (its occupancy query); more would wait for a turn
+  // of their own.
   const double met = p.n_adapters * -std::expm1(p.m * std::log1p(-1.0 / (p.n_adapters + 1)));
   const int full = (p.m + T - 1) / T, likely = std::max(full, std::min(p.m, (int)std::ceil(met)));
   const int most = std::min(p.m, full + std::min(p.n_adapters + 1, p.m));
-  // Clusters of the most CTAs of which so many run at once.  The GPU's partitions hold 15 clusters of eight such CTAs, 36 of
-  // four and 76 of two (its occupancy query); more wait for a turn of their own.
-  const int at_once[4] = {dev.sms, dev.sms / 2, dev.sms / 4 - 2, dev.sms / 10};
-  int c = 8, i = 3;
-  while (c > 1 && likely > at_once[i]) c /= 2, --i;
-  const int clusters = std::max(1, std::min(most, dev.sms / c));
+  const int c = likely <= dev.sms / 10 ? 8 : 4, clusters = std::max(1, std::min(most, c == 8 ? dev.sms / 10 : dev.sms / 4 - 2));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * c);
   cfg.blockDim = dim3(kThreads);
