@@ -19,6 +19,9 @@
 // dealt to the MMAs' columns so that a lane ends up with eight contiguous outputs of a row: y
 // is read and written 16 bytes a lane.  h is split into two bf16 terms (16 bits of it), so the
 // only rounding to 16 bits is the output's.
+//
+// Measured in a graph, 5120 inputs, 7168 outputs (us, rank 16 / 64; the bytes at the copy rate): one row 6.9 / 9.2 (0.5 / 1.9), 16 rows
+// of 16 adapters - / 14 (- / 3.8), 64 of 48 15 / 22 (3.1 / 11.5), 256 of 48 16.5 / 23 (4.2 / 12.6).
 #include <algorithm>
 #include <cmath>
 

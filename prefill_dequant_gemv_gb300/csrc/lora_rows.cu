@@ -17,6 +17,11 @@
 // multiplied one after the other into the same accumulator, and the outputs of a chunk are dealt to the MMA's columns
 // so that a lane that loads fragments of 16 rows x 8 columns from tensor memory holds eight contiguous outputs of
 // a row: y comes and the sum leaves 16 bytes a lane, y by way of slots in shared memory that are the lane's own.
+//
+// Measured in a graph (us; the bytes at the copy rate): 3999 rows of 5 adapters of rank 16, 6144 to 5120 38.7 (19.5); 8192 rows of 3
+// of rank 64, 5120 to 5120 66 (37.6), to 17408 128 (97.5); 2048 of rank 128, 5120 to 7168 47 (13.1); 300 rows of 4 of rank 16 19 (2.0).
+// What is over the bytes: the rows' sorting, 7 to 9 us, and the chain from a tile's last input to its first output, some 10.
+// y's first chunks sent for into L2 during that chain made it longer (39 -> 42, 133 -> 136).
 #include <algorithm>
 
 #include "qg_lora_dev.cuh"

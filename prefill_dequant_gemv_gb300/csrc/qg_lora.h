@@ -27,9 +27,10 @@ struct LoraArgs {
 constexpr int64_t kLoraFewRows = 256;       // in one launch of clusters (lora.cu)
 constexpr int64_t kLoraRowsAtOnce = 16384;  // in one launch of many rows: what a CTA looks through itself
 constexpr int kLoraMinSms = 96;             // of lora_rows.cu: fewer SMs' CTAs would have more tiles each than they list
-// Whether a call goes to lora.cu, 256 rows a launch, or to lora_rows.cu.  There every adapter has tiles of 128 rows, mostly empty
-// where adapters are many: 512 rows of 48 adapters 42 us (rank 16) and 52 (rank 64), in lora.cu 32 and 46; 1000 rows
-// 44 and 56 against 64 and 92; 300 rows of 4 adapters 18 and 24 against 24 and 33.
+// Whether a call goes to lora.cu, 256 rows a launch, or to lora_rows.cu.  There every adapter that is met has tiles of 128 rows,
+// mostly empty where adapters are many, but how many are met is known on the device only.  All of them met, us, rank 16 / 64,
+// lora.cu against lora_rows.cu: 512 rows of 48 adapters 25 / 33 against 43 / 55, of 16 25 / 34 against 25 / 32; 768 of 48 38 / 52
+// against 44 / 55, 1000 of 48 50 / 68 against 45 / 56; 300 rows of 4 adapters 24 / 33 against 19 / 24.
 inline bool lora_few(int64_t m, int n_adapters) { return m <= kLoraFewRows || (m <= 2 * kLoraFewRows && n_adapters >= 16); }
 int launch_lora(const LoraArgs& a, const DeviceInfo& dev, void* stream);
 // Scratch of the many-row form for h's parts, and its launches.

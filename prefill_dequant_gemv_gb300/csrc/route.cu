@@ -9,6 +9,10 @@
 // ascending list of active experts, and a tile table of (expert, first position, count)
 // with at most kRouteTile pairs per tile for the grouped prefill GEMM.  Everything is
 // deterministic: ranks come from ordered scans, never from atomic arrival order.
+//
+// Up to 32 tokens (two by a rule) take one CTA and one launch; more a launch of the top-k with counts of every block of tokens,
+// one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts, topk 10: 64 tokens 8.2 us
+// (12 with four launches), 8192 24 (27).
 #include <cuda_runtime.h>
 
 #include "qg_internal.h"
