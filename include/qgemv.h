@@ -340,7 +340,7 @@ size_t qmoe_route_workspace_size(int64_t t, int n_experts, int topk);
  *   topk_ids [t][topk] int32, topk_w [t][topk] fp32 (device),
  * and, in route_ws, the (token, slot) pairs grouped by expert -- experts ascending, tokens
  * ascending within an expert -- with counts, offsets, the active experts and a tile
- * table; deterministic, one launch for up to 32 tokens.  logits: fp32 [t][n_experts]. */
+ * table; deterministic, one launch for up to 64 tokens.  logits: fp32 [t][n_experts]. */
 qg_status qmoe_route(const float* logits, int64_t t, int n_experts, int topk,
                      int32_t* topk_ids, float* topk_w, void* route_ws, size_t route_ws_bytes, void* stream);
 

@@ -10,8 +10,8 @@
 // with at most kRouteTile pairs per tile for the grouped prefill GEMM.  Everything is
 // deterministic: ranks come from ordered scans, never from atomic arrival order.
 //
-// Up to 32 tokens (two by a rule) take one CTA and one launch; more a launch of the top-k with counts of every block of tokens,
-// one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts, topk 10: 64 tokens 8.2 us
+// Up to 32 tokens (two by a rule) take one CTA, up to 64 a cluster; more a launch of the top-k with counts of every block of tokens,
+// one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts, topk 10: 64 tokens 7.4 us
 // (12 with four launches), 8192 24 (27).
 #include <cuda_runtime.h>
 
@@ -23,7 +23,10 @@
 
 namespace qg {
 
-constexpr int kRouteBySmall = 2;  // tokens that one CTA routes by a rule (shared memory holds no more than some)
+// Tokens that one cluster routes, one a warp of its eight CTAs: 64 of 512 experts by softmax and bias 6.5 us, 7.2 with two launches, 32 6.1
+// and 7.4; 128, two a warp, 9.7 against 8.
+constexpr int kRouteCluster = 64;
+constexpr int kRouteBySmall = 2;  // tokens that one CTA alone routes by a rule: two 4.9 us, by a cluster of one 5.9
 
 // Clear a shared array with 16-byte stores (bytes a multiple of 16, 16-byte aligned).
 __device__ __forceinline__ void zero_shared(void* p, int bytes) {
@@ -268,6 +271,90 @@ __global__ void __launch_bounds__(BY ? kMaxExperts : kRouteBlock) route_small_ke
   }
 }
 
+// A batch of a few dozen tokens in one launch: a cluster of CTAs, a token to each of their warps, which read one another's counts from
+// shared memory.
+template <int S, bool BY>
+__global__ void __launch_bounds__(256) route_cluster_kernel(const float* logits, int T, int E, int k, int32_t* ids, float* wts,
+                                                            int tile, RouteView r, RouteRule rule) {
+  __shared__ __align__(16) int hist[kMaxExperts];
+  __shared__ float cs[BY ? 8 : 1][BY ? 32 * S + 32 : 1];
+  __shared__ int s_ids[8 * kMaxTopk], start[kMaxExperts], off[kMaxExperts], zid[kMaxExperts];
+  __shared__ __align__(16) unsigned short wc[8][kMaxExperts];  // pairs per (warp, expert)
+  __shared__ int3 totals;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
+  if (tid == 0) pdl_launch_dependents();
+  zero_shared(hist, sizeof(hist));
+  zero_shared(&wc[0][0], sizeof(wc));
+  __syncthreads();
+  pdl_wait();
+  const int t0 = b * 8, t1 = min(t0 + 8, T), t = t0 + warp;
+  if (t < t1) {
+    const float* lg = logits + (int64_t)t * E;
+    if constexpr (BY) warp_route<S>(rule, lg, E, k, cs[warp], ids + t * k, wts + t * k, s_ids + warp * k, hist);
+    else warp_topk(lg, E, k, ids + t * k, wts + t * k, s_ids + warp * k, hist);
+  }
+  cluster_sync_all();
+  // two experts a thread: their pairs in all CTAs and in those before
+  int tot[2] = {0, 0}, before[2] = {0, 0};
+  const int e0 = 2 * tid;
+  for (int i = 0; i < (int)gridDim.x; ++i) {
+    int a, c;
+    asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(a), "=r"(c) : "r"(cluster_map(hist + e0, (uint32_t)i)));
+    before[0] += i < b ? a : 0;
+    before[1] += i < b ? c : 0;
+    tot[0] += a;
+    tot[1] += c;
+  }
+  const int tiles[2] = {(tot[0] + tile - 1) / tile, (tot[1] + tile - 1) / tile};
+  int3 ex = block_scan3(make_int3(tot[0] + tot[1], tiles[0] + tiles[1], (tot[0] > 0) + (tot[1] > 0)), &totals);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = e0 + i, n = tot[i];
+    start[e] = ex.x + before[i];
+    off[e] = ex.x;
+    zid[e] = ex.z;
+    if (b == 0 && e < E) {
+      r.counts[e] = n;
+      r.offsets[e] = ex.x;
+      if (n > 0) {
+        r.active[ex.z] = e;
+        r.zidx[e] = ex.z;
+        reinterpret_cast<int4*>(r.groups + (size_t)ex.z * kGroupInts)[0] = make_int4(e, ex.x, n, 0);
+      }
+      for (int s = 0; s < tiles[i]; ++s) {
+        r.tiles[3 * (ex.y + s)] = e;
+        r.tiles[3 * (ex.y + s) + 1] = ex.x + s * tile;
+        r.tiles[3 * (ex.y + s) + 2] = min(tile, n - s * tile);
+      }
+    }
+    ex.x += n;
+    ex.y += tiles[i];
+    ex.z += n > 0;
+  }
+  if (b == 0 && tid == 0) {
+    r.offsets[E] = totals.x;
+    r.meta[0] = totals.z;
+    r.meta[1] = totals.y;
+  }
+  // stable placement: experts ascending, pairs ascending within an expert
+  const bool valid = tid < (t1 - t0) * k;
+  const int e = valid ? s_ids[tid] : -1;
+  const unsigned mask = __match_any_sync(0xFFFFFFFFu, e);
+  const int rank_in_warp = __popc(mask & ((1u << lane) - 1u));
+  if (valid && rank_in_warp == 0) wc[warp][e] = (unsigned short)__popc(mask);
+  __syncthreads();
+  if (valid) {
+    const int p = t0 * k + tid;
+    int at = start[e] + rank_in_warp;
+    for (int w = 0; w < warp; ++w) at += wc[w][e];
+    r.pair_list[at] = p;
+    r.pair_pos[p] = at;
+    const int rank = at - off[e];
+    if (rank < kGroupRows) r.groups[(size_t)zid[e] * kGroupInts + 4 + rank] = t0 + tid / k;
+  }
+  cluster_sync_all();  // no CTA ends before the others have read its counts
+}
+
 RouteView route_view(void* ws, int64_t T, int E, int k) {
   const RouteLayout L = route_layout(T, E, k);
   uint8_t* b = static_cast<uint8_t*>(ws);
@@ -307,10 +394,33 @@ static int launch_large(const RouteRule& rule, const float* logits, int64_t T, i
   return cudaGetLastError() == cudaSuccess ? QG_OK : QG_ERR_CUDA;
 }
 
+template <int S, bool BY>
+static int launch_cluster(const RouteRule& rule, const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts,
+                          const RouteView& r, cudaStream_t s) {
+  const int ctas = (int)((T + 7) / 8);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, route_cluster_kernel<S, BY>, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r, rule) ==
+                     cudaSuccess && cudaGetLastError() == cudaSuccess
+             ? QG_OK
+             : QG_ERR_CUDA;
+}
+
 int launch_route(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RouteView r = route_view(ws, T, E, k);
-  if (T * k > kRouteBlock || T > 32) return launch_large<16, false>(RouteRule(), logits, T, E, k, ids, wts, r, s);
+  if (T > 32 && T <= kRouteCluster) return launch_cluster<16, false>(RouteRule(), logits, T, E, k, ids, wts, r, s);
+  if (T > 32) return launch_large<16, false>(RouteRule(), logits, T, E, k, ids, wts, r, s);
   return launch_pdl(route_small_kernel<0>, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r,
                     RouteRule()) == cudaSuccess && cudaGetLastError() == cudaSuccess
              ? QG_OK
@@ -321,6 +431,7 @@ template <int S>
 static int launch_by(const RouteRule& rule, const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts,
                      const RouteView& r, cudaStream_t s) {
   // by a rule a token takes a warp some 3 us, and one SM's warps share its issue slots: more tokens go to more SMs
+  if (T > kRouteBySmall && T <= kRouteCluster) return launch_cluster<S, true>(rule, logits, T, E, k, ids, wts, r, s);
   if (T > kRouteBySmall) return launch_large<S, true>(rule, logits, T, E, k, ids, wts, r, s);
   return launch_pdl(route_small_kernel<S>, dim3(1), dim3(kMaxExperts), 0, s, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r,
                     rule) == cudaSuccess && cudaGetLastError() == cudaSuccess

@@ -248,3 +248,16 @@ def test_two_streams_at_once_and_wrong_devices():
         q.route(lg.cpu(), 8, rule=rule)
     with pytest.raises(q.QGError):
         q.route(lg, 8, rule=q.RouteRule("softmax", bias=torch.zeros(128)))
+
+
+@pytest.mark.parametrize("t", [2, 3, 7, 8, 9, 32, 33, 40, 57, 64, 65, 72, 128, 129])
+@pytest.mark.parametrize("e,k", [(16, 16), (130, 6), (512, 16)])
+def test_borders_between_the_launches(t, e, k):
+    """One CTA, a cluster, launches of blocks; and without a rule, whose tables are the same."""
+    q = qlib()
+    rng = np.random.default_rng(t + e)
+    lg = rng.standard_normal((t, e)).astype(np.float32)
+    compare(q, lg, k, bias=0.1 * rng.standard_normal(e), score="sigmoid")
+    dev = torch.from_numpy(lg).cuda()
+    (i1, w1, s1), (i2, w2, s2) = q.route(dev, k), q.route(dev, k, rule=q.RouteRule("softmax"))
+    assert torch.equal(i1, i2) and torch.allclose(w1, w2, rtol=2.0 ** -20, atol=0) and tables_equal(q, s1.buf, s2.buf, t, e, k)
