@@ -569,10 +569,15 @@ def moe_forward(pm: PackedMoE, x, logits, topk: int, out=None, workspace: Option
                 route_ws: Optional[Workspace] = None, shared_gate=None, rule: Optional[RouteRule] = None):
     """Router and MoE FFN in one call (qmoe_forward; by a rule qmoe_route_by, then qmoe_ffn) for x bf16 [t, H] and fp32
     logits [t, E]: returns (out bf16 [t, H], topk_ids int32 [t, topk], topk_w fp32 [t, topk], route workspace)."""
+    import torch
     if rule is not None:
+        if logits.get_device() >= 0 and logits.get_device() != torch._C._cuda_getDevice():
+            with torch.cuda.device(logits.device):
+                return moe_forward(pm, x, logits, topk, out, workspace, route_ws, shared_gate, rule)
+        if (x.shape[0], pm.n_experts) != tuple(logits.shape) or x.get_device() != logits.get_device():
+            raise QGError(1, f"moe_forward: logits [{x.shape[0]}, {pm.n_experts}] on x's device")
         ids, w, route_ws = _route_by(rule, logits, topk, route_ws)
         return moe_ffn(pm, x, w, route_ws, out, workspace, shared_gate), ids, w, route_ws
-    import torch
     t = x.shape[0]
     e = logits.shape[1]
     ids = torch.empty((t, topk), dtype=torch.int32, device=x.device)

@@ -118,3 +118,26 @@ def test_python_helpers_refuse_wrong_tensors(q):
         with pytest.raises(q.QGError) as e:
             bad()
         assert e.value.status == INVALID
+
+
+def test_a_layer_by_a_rule_refuses_logits_of_other_shapes(q):
+    torch = pytest.importorskip("torch")
+
+    class Experts:
+        n_experts = 8
+
+    x, rule = torch.zeros(4, 64, dtype=torch.bfloat16), q.RouteRule("sigmoid")
+    for logits in (torch.zeros(3, 8), torch.zeros(4, 9), torch.zeros(8, 4), torch.zeros(4, 8)):  # the last: no CUDA tensor
+        with pytest.raises(q.QGError) as e:
+            q.moe_forward(Experts(), x, logits, 2, rule=rule)
+        assert e.value.status == INVALID
+    for counts in (dict(groups=-1), dict(groups=1 << 32), dict(topk_groups=1 << 31), dict(group_best=-2)):
+        with pytest.raises(q.QGError):
+            q.RouteRule("sigmoid", **counts)
+
+
+def test_workspaces_of_refused_sizes(q):
+    size = lambda **over: q.qlora_workspace_size(lora_desc(q, **over), 8)  # noqa: E731
+    assert size() == 256
+    for bad in (dict(max_rank=12), dict(n=0), dict(k=0), dict(n=1 << 24), dict(k=1 << 24), dict(n_adapters=0), dict(n_adapters=1025)):
+        assert size(**bad) == 0
