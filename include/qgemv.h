@@ -354,7 +354,8 @@ qg_status qmoe_route(const float* logits, int64_t t, int n_experts, int topk,
  *     w_e = scale * s_e, or scale * s_e / (sum of the chosen s) with renormalise.
  * The choice is the one that scores in 64 bits give: c in fp32 decides where it is clear, and a
  * token with two values nearer to each other than fp32's error is decided in 64 bits.  Without a bias, and
- * with groups valued by one expert if there are any, c is ordered as the logits are, and they decide.
+ * with groups valued by one expert if there are any, c is ordered as the logits are, and they decide.  (Values
+ * that are one in exact arithmetic and not in 64 bits, such as sums of two with other summands, come as 64 bits have them.)
  * The weights are fp32.  NaN values of c come after every number; a weight is NaN where the formula's is
  * (renormalised weights whose sum is 0 among them). */
 typedef enum { QG_SCORE_SOFTMAX = 1, QG_SCORE_SIGMOID = 2 } qg_score;

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
       const int4 o = *reinterpret_cast<const int4*>(ids + j);
       place += (o.x == id) + (j + 1 < tid && o.y == id) + (j + 2 < tid && o.z == id) + (j + 3 < tid && o.w == id);
     }
-  const bool first = tid < p.m && place % T == 0 && !(id < 0 && in_place);  // in place: nothing to do without an adapter
+  const bool first = tid < p.m && place % T == 0;
   int n_tiles;
   const int number = block_prefix<kThreads>(first, warp_sums, &n_tiles);
 
@@ -140,7 +140,8 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
     const int s0 = steps * me >> all, n1 = (steps * (me + 1) >> all) - s0;
     const int chunks = (p.n + S::kOuts - 1) / S::kOuts;
     const int c0 = chunks * rank >> log_team, c1 = chunks * (rank + 1) >> log_team;
-    const int n2 = c0 + warp < c1 ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0, n = n1 + n2;
+    // in place there is nothing to do without an adapter (such tiles count all the same: the teams are those of a call that is not)
+    const int n2 = c0 + warp < c1 && !(ra == 0 && in_place) ? (c1 - c0 - warp + kWarps - 1) / kWarps : 0, n = n1 + n2;
     // The copies' state.  A lane copies piece lane % 8 of every fourth row of x, A and y, so that a copy takes whole lines; and
     // of B, whose rows are shorter or longer, every 32nd piece.  A pointer may run past its row's end, or stand on a row that is
     // not there: then no byte of it is read.
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads) lora_kernel(LoraArgs p) {
         const int left = p.n - col - 32 * o;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (row[h] < 0 || left <= 0 || (ra == 0 && in_place)) continue;
+          if (row[h] < 0 || left <= 0) continue;
           const uint4 v = *reinterpret_cast<const uint4*>(from + piece_at<kYLanes>(g + 8 * h, 4 * o + t));
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
           if (ra)

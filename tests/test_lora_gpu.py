@@ -272,3 +272,15 @@ def test_a_workspace_serves_on_after_bad_ids():
         out = q.lora(ad, good, x, y, out=torch.empty_like(y), workspace=ws)
         assert ws.status() == 0
         check(ad, ids, x, y, out)
+
+
+@pytest.mark.parametrize("top", [8, 32, 64, 104])
+@pytest.mark.parametrize("m", [16, 17, 40, 100, 256])
+def test_in_place_has_the_same_bits_with_rows_without_an_adapter(m, top):
+    """More tiles than clusters, some of rows without an adapter, which in place are left alone."""
+    q = qlib()
+    ad = adapters(q, 40, top, 304, 402, m + top)
+    for seed in range(4):
+        ids, x, y = ids_of("mixed", m, 40, seed), rows(m, 304, 1), rows(m, 402, 2, fill=0.0)
+        ids[::3] = [-1] * len(ids[::3])
+        check(ad, ids, x, y, run(q, ad, ids, x, y))
