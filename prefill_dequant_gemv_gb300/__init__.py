@@ -627,7 +627,11 @@ def _rows(t, shape, dtype, index, what, name):
 
 def _new_rows(x, shape, dtype):
     """A new matrix whose rows start at multiples of 16 bytes."""
-    return x.new_empty((shape[0], (shape[1] + 15) // 16 * 16), dtype=dtype)[:, :shape[1]]
+    import torch
+    m, k = shape
+    if k % 16 == 0:
+        return torch.empty(m, k, dtype=dtype, device=x.device)
+    return torch.empty(m, (k + 15) // 16 * 16, dtype=dtype, device=x.device)[:, :k]
 
 
 def _norm(x, weight, residual, sum_out, bf16, what):
@@ -678,7 +682,7 @@ def rms_norm_fp8(x, weight, residual=None, eps: float = 1e-6, weight_offset: flo
     if out is None:
         out = _new_rows(x, shape, torch.float8_e4m3fn)
     if scales is None:
-        scales = x.new_empty(groups, dtype=torch.float32)
+        scales = torch.empty(groups, dtype=torch.float32, device=x.device)
     cp, ldc = _rows(out, shape, torch.float8_e4m3fn, index, "rms_norm_fp8", "out")
     if scales.dtype is not torch.float32 or scales.shape != groups or scales.get_device() != index or \
             (groups[1] > 1 and scales.stride(1) != 1):
