@@ -267,7 +267,7 @@ typedef struct {
 /* x and residual (may be NULL): bf16 [m_rows][ldx] / [m_rows][ldr]; weight: bf16 [k], 16-byte
  * aligned like every matrix (scales: 4-byte aligned, any lds).  k is 1 to 65536; m_rows may be 0.
  * sum or y may be x or residual itself with the same stride; no other overlap.  eps >= 0.
- * No workspace; one launch; deterministic. */
+ * No workspace; one launch; deterministic (the order of a row's sum goes by k and by whether there are more rows than SMs). */
 qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t m_rows, int64_t k,
                       const void* weight, float eps, float weight_offset, const qg_norm_out* out, void* stream);
 
@@ -304,7 +304,8 @@ size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
  * other qlora call, of any sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not
  * share it, and no other entry point may use it in between.  More than 256 rows (512 where there are 16 adapters or more) need a GPU of
  * 96 SMs or more (QG_ERR_UNSUPPORTED otherwise) and run on all of its SMs at once, so such a call starts when no other kernel
- * holds one.  Deterministic; one launch for every 256 rows, or for every 16384 where they are more. */
+ * holds one.  Deterministic (the order in which h is summed goes by the call's sizes and ids); one launch for every 256
+ * rows, or for every 16384 where they are more. */
 qg_status qlora(const qg_lora* lora, const int32_t* ids, int64_t m_rows, const void* x, int64_t ldx, const void* y,
                 int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 
