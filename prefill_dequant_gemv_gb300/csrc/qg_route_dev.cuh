@@ -120,14 +120,15 @@ __device__ __forceinline__ void warp_topk_keys(uint32_t (&key)[S], int k, uint32
   }
 }
 
-// Warp-level top-k of one token's logits (E <= 512) and the k lanes' softmax over the kept ones in parallel; a copy of
+// Warp-level top-k of one token's logits (E <= 32 S) and the k lanes' softmax over the kept ones in parallel; a copy of
 // the ids and a count of them in hist, each where it is given.
+template <int S = 16>
 __device__ __forceinline__ void warp_topk(const float* lg, int E, int k, int32_t* ids, float* wts, int* ids_copy = nullptr,
                                           int* hist = nullptr) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[16];
+  uint32_t key[S];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < S; ++i) {
     const int e = lane + 32 * i;
     key[i] = e < E ? order_key(lg[e]) : 0u;
   }

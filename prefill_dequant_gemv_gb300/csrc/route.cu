@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(256, 3) route_topk_kernel(const float* logits,
     for (int64_t t = t0 + warp; t < t1; t += 8)
       warp_route<S>(rule, logits + t * E, E, k, cs[warp], ids + t * k, wts + t * k, nullptr, hist);
   } else {
-    for (int64_t t = t0 + warp; t < t1; t += 8) warp_topk(logits + t * E, E, k, ids + t * k, wts + t * k, nullptr, hist);
+    for (int64_t t = t0 + warp; t < t1; t += 8) warp_topk<S>(logits + t * E, E, k, ids + t * k, wts + t * k, nullptr, hist);
   }
   __syncthreads();
   for (int e = threadIdx.x; e < E; e += 256) r.block_counts[(size_t)blockIdx.x * E + e] = hist[e];
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(256) route_cluster_kernel(const float* logits,
   if (t < t1) {
     const float* lg = logits + (int64_t)t * E;
     if constexpr (BY) warp_route<S>(rule, lg, E, k, cs[warp], ids + t * k, wts + t * k, s_ids + warp * k, hist);
-    else warp_topk(lg, E, k, ids + t * k, wts + t * k, s_ids + warp * k, hist);
+    else warp_topk<S>(lg, E, k, ids + t * k, wts + t * k, s_ids + warp * k, hist);
   }
   cluster_sync_all();
   // two experts a thread: their pairs in all CTAs and in those before
@@ -416,11 +416,18 @@ static int launch_cluster(const RouteRule& rule, const float* logits, int64_t T,
              : QG_ERR_CUDA;
 }
 
+template <int S>
+static int launch_batch(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, const RouteView& r, cudaStream_t s) {
+  return T <= kRouteCluster ? launch_cluster<S, false>(RouteRule(), logits, T, E, k, ids, wts, r, s)
+                            : launch_large<S, false>(RouteRule(), logits, T, E, k, ids, wts, r, s);
+}
+
 int launch_route(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RouteView r = route_view(ws, T, E, k);
-  if (T > 32 && T <= kRouteCluster) return launch_cluster<16, false>(RouteRule(), logits, T, E, k, ids, wts, r, s);
-  if (T > 32) return launch_large<16, false>(RouteRule(), logits, T, E, k, ids, wts, r, s);
+  if (T > 32)
+    return E <= 128 ? launch_batch<4>(logits, T, E, k, ids, wts, r, s)
+           : E <= 256 ? launch_batch<8>(logits, T, E, k, ids, wts, r, s) : launch_batch<16>(logits, T, E, k, ids, wts, r, s);
   return launch_pdl(route_small_kernel<0>, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r,
                     RouteRule()) == cudaSuccess && cudaGetLastError() == cudaSuccess
              ? QG_OK
