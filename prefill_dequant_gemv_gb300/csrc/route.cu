@@ -10,9 +10,9 @@
 // with at most kRouteTile pairs per tile for the grouped prefill GEMM.  Everything is
 // deterministic: ranks come from ordered scans, never from atomic arrival order.
 //
-// Up to 32 tokens (two by a rule) take one CTA, up to 64 a cluster; more a launch of the top-k with counts of every block of tokens,
-// one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts, topk 10: 64 tokens 7.4 us
-// (12 with four launches), 8192 24 (27).
+// Up to 8 tokens (two by a rule) take one CTA, up to 64 a cluster; more a launch of the top-k with counts of every block of tokens,
+// one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts, topk 10: 32 tokens 6.1 us
+// (9.4 in one CTA), 64 7.2 (12 with four launches), 8192 24 (27).
 #include <cuda_runtime.h>
 
 #include "qg_internal.h"
@@ -26,6 +26,7 @@ namespace qg {
 // Tokens that one cluster routes, one a warp of its eight CTAs: 64 of 512 experts by softmax and bias 6.5 us, 7.2 with two launches, 32 6.1
 // and 7.4; 128, two a warp, 9.7 against 8.
 constexpr int kRouteCluster = 64;
+constexpr int kRouteSmall = 8;  // tokens that one CTA alone routes without a rule: 8 of 512 experts 4.2 us, by a cluster 5.9; 16 6.5 and 6.4
 constexpr int kRouteBySmall = 2;  // tokens that one CTA alone routes by a rule: two 4.9 us, by a cluster of one 5.9
 
 // Clear a shared array with 16-byte stores (bytes a multiple of 16, 16-byte aligned).
@@ -197,7 +198,7 @@ __global__ void __launch_bounds__(kRouteBlock) route_place_kernel(const int32_t*
   }
 }
 
-// Decode-sized routing (T*k <= kRouteBlock; T <= 32, or kRouteBySmall by a rule): every phase in one CTA, with
+// Decode-sized routing (T <= kRouteSmall, or kRouteBySmall by a rule): every phase in one CTA, with
 // the histogram, the scan and the placement in shared memory; only the results go to device
 // memory.  BY: by a rule, of up to 32 BY experts; 0: without one.
 template <int BY>
@@ -425,7 +426,7 @@ static int launch_batch(const float* logits, int64_t T, int E, int k, int32_t* i
 int launch_route(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RouteView r = route_view(ws, T, E, k);
-  if (T > 32)
+  if (T > kRouteSmall)
     return E <= 128 ? launch_batch<4>(logits, T, E, k, ids, wts, r, s)
            : E <= 256 ? launch_batch<8>(logits, T, E, k, ids, wts, r, s) : launch_batch<16>(logits, T, E, k, ids, wts, r, s);
   return launch_pdl(route_small_kernel<0>, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r,
