@@ -55,7 +55,10 @@ __host__ __device__ inline RouteLayout route_layout(int64_t T, int E, int k) {
   L.tiles = take((size_t)L.max_tiles * 12);  // (expert, first position, count)
   L.groups = take((size_t)E * kGroupInts * 4);  // group table, one entry per active expert
   L.zidx = take((size_t)E * 4);                 // expert -> its index in the active list
-  L.block_counts = take((size_t)L.nblocks * E * 4);
+  // Blocks grow from 8 tokens every 4096, so more tokens can have fewer of them: room for the most that any fewer tokens have
+  // (512 from 4096 tokens on; past the largest block they only become more), as one workspace serves them all.
+  const int64_t rounds = (T + 7) / 8, most = rounds < 512 ? rounds : 512;
+  L.block_counts = take((size_t)(L.nblocks > most ? L.nblocks : most) * E * 4);
   L.total = o;
   return L;
 }
