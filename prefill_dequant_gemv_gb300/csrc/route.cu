@@ -10,7 +10,7 @@
 // with at most kRouteTile pairs per tile for the grouped prefill GEMM.  Everything is
 // deterministic: ranks come from ordered scans, never from atomic arrival order.
 //
-// Up to 8 tokens (two by a rule) take one CTA, up to 64 a cluster; more a launch of the top-k with counts of every block of tokens,
+// Up to 8 tokens (12 of more than 256 experts, two by a rule) take one CTA, up to 64 a cluster; more a launch of the top-k with counts of every block of tokens,
 // one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts, topk 10: 32 tokens 6.1 us
 // (9.4 in one CTA), 64 7.2 (12 with four launches), 8192 24 (27).
 #include <cuda_runtime.h>
@@ -26,7 +26,10 @@ namespace qg {
 // Tokens that one cluster routes, one a warp of its eight CTAs: 64 of 512 experts by softmax and bias 6.5 us, 7.2 with two launches, 32 6.1
 // and 7.4; 128, two a warp, 9.7 against 8.
 constexpr int kRouteCluster = 64;
-constexpr int kRouteSmall = 8;  // tokens that one CTA alone routes without a rule: 8 of 512 experts 4.2 us, by a cluster 5.9; 16 6.5 and 6.4
+// Tokens that one CTA alone routes without a rule.  One CTA and a cluster, in a graph behind another kernel, us: 9 tokens of 64 experts
+// 4.6 and 4.2, of 256 5.0 and 4.9, of 384 5.0 and 5.4, of 512 5.9 and 6.3; 12 of 384 5.3 and 5.6, of 512 5.8 and 6.0; 16 of 384 5.9 and
+// 5.8, of 512 6.6 and 6.2.
+inline int route_small(int E) { return E > 256 ? 12 : 8; }
 constexpr int kRouteBySmall = 2;  // tokens that one CTA alone routes by a rule: two 4.9 us, by a cluster of one 5.9
 
 // Clear a shared array with 16-byte stores (bytes a multiple of 16, 16-byte aligned).
@@ -131,7 +134,9 @@ __global__ void __launch_bounds__(1024) route_prefix_kernel(int E, int nblocks, 
 
 // Last launch: offsets, active list and tile table (stored by block 0), and the stable placement of each block's pairs:
 // experts ascending, pairs ascending within an expert.  `tokens` a block, `merged` blocks of the counts.  SUM: there was no second
-// launch, the block adds the counts itself.
+// launch, the block adds the counts itself.  It does not ask for the next kernel's launch: where that is another call's top-k, its
+// blocks would come to lie beside one another on the SMs that are free by then (1000 tokens, 512 experts, topk 16, call after call:
+// 18.3 us, 15.1 so; behind another kernel 15.0 both ways).
 template <bool SUM>
 __global__ void __launch_bounds__(kRouteBlock) route_place_kernel(const int32_t* ids, int64_t P, int E, int k, int tokens, int merged,
                                                                   int nblocks, int tile, RouteView r) {
@@ -139,7 +144,6 @@ __global__ void __launch_bounds__(kRouteBlock) route_place_kernel(const int32_t*
   __shared__ int start[kMaxExperts], off[kMaxExperts], zid[kMaxExperts];
   __shared__ __align__(16) unsigned short wc[kRouteBlock / 32][kMaxExperts];  // pairs per (warp, expert)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, b = blockIdx.x;
-  if (tid == 0) pdl_launch_dependents();
   zero_shared(&wc[0][0], sizeof(wc));
   pdl_wait();
   int tot = 0, before = 0;
@@ -198,7 +202,7 @@ __global__ void __launch_bounds__(kRouteBlock) route_place_kernel(const int32_t*
   }
 }
 
-// Decode-sized routing (T <= kRouteSmall, or kRouteBySmall by a rule): every phase in one CTA, with
+// Decode-sized routing (T <= route_small, or kRouteBySmall by a rule): every phase in one CTA, with
 // the histogram, the scan and the placement in shared memory; only the results go to device
 // memory.  BY: by a rule, of up to 32 BY experts; 0: without one.
 template <int BY>
@@ -426,7 +430,7 @@ static int launch_batch(const float* logits, int64_t T, int E, int k, int32_t* i
 int launch_route(const float* logits, int64_t T, int E, int k, int32_t* ids, float* wts, void* ws, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   RouteView r = route_view(ws, T, E, k);
-  if (T > kRouteSmall)
+  if (T > route_small(E))
     return E <= 128 ? launch_batch<4>(logits, T, E, k, ids, wts, r, s)
            : E <= 256 ? launch_batch<8>(logits, T, E, k, ids, wts, r, s) : launch_batch<16>(logits, T, E, k, ids, wts, r, s);
   return launch_pdl(route_small_kernel<0>, dim3(1), dim3(kRouteBlock), 0, s, logits, (int)T, E, k, ids, wts, (int)kRouteTile, r,
