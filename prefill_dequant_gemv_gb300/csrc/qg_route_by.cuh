@@ -14,7 +14,9 @@
 // their argument's rounding by u d e^-d, together below 6 u of the largest; in the sum S >= 1 the mean of d over e^-d / S is
 // at most log 512, so S is off by 2 (2 + 1.173 * 6.3) + 6.3 u, its 21 additions by 21 u, its reciprocal by 2 u: s
 // is off by less than 56 u / S.  The sum with the bias adds u |c|.  Two values may be off by twice that: the tolerance is 2^-20
-// (sigmoid; 16 u) or 2^-17 / S (softmax; 128 u), and 2^-22 |c| (4 u); for sums of two c twice as much.
+// (sigmoid; 16 u) or 2^-17 / S (softmax; 128 u), and 2^-22 |c| (4 u).  A sum of two c is off by the errors of both, u times
+// each one's magnitude among them, and by its own rounding; the magnitudes may be far larger than the sum, so that the tolerance of two such
+// sums is twice the first part and 2^-21 of the largest |c| + |c'| (8 u, of which 4 u are needed).
 //
 // What bounds many tokens is a warp's instructions, one after the other (issue 54%; a token of 512 experts by sigmoid and bias
 // 1062).  So the winners are not taken one by one from all experts, in rounds that a warp's reductions make long (1539
@@ -279,7 +281,9 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
     a0 = __shfl_sync(0xFFFFFFFFu, a0, (lane * per) & 31);
     a1 = __shfl_sync(0xFFFFFFFFu, a1, (lane * per) & 31);
     const float value = r.group_best == 2 ? a0 + a1 : a0;
-    float gap, size_of = lane < r.n_groups && fabsf(value) < INFINITY ? fabsf(value) : 0.0f;
+    // the summands' magnitudes (past fp32's range: no group is clearly apart); infinite ones have no error
+    const float mag = r.group_best == 2 ? (fabsf(a1) < INFINITY ? fabsf(a0) + fabsf(a1) : 0.0f) : fabsf(a0);
+    float gap, size_of = lane < r.n_groups && fabsf(a0) < INFINITY ? mag : 0.0f;
     uint32_t groups = keep_groups(value, r.n_groups, r.topk_groups, &gap);
     if (r.values && r.topk_groups < r.n_groups) {
       size_of = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(size_of)));
