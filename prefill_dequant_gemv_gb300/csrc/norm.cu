@@ -117,10 +117,10 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
   return from_bits(d);
 }
-// The squares of a, added to a sum in two parts (P) or one.
+// The squares of a, added to a sum in two parts, in one order in every form: y has the same bits whatever is stored beside it.
 template <bool P>
 __device__ __forceinline__ float2 add_squares(float2 a, float2 sum) {
-  if (!P) return make_float2(fmaf(a.y, a.y, fmaf(a.x, a.x, sum.x)), 0.0f);
+  if (!P) return make_float2(fmaf(a.x, a.x, sum.x), fmaf(a.y, a.y, sum.y));
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(sum)));
   return from_bits(d);
