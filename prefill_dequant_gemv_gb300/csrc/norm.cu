@@ -33,7 +33,8 @@ constexpr int kLongThreads = 768;  // for a row in shared memory: 2000 x 17408 t
 constexpr int kLongAhead = 2;      // and the vectors that a thread loads at a time (four: 52 us, fewer CTAs)
 // of the longest row, rounded up to whole turns of the threads
 constexpr size_t kLongBytes = (kNormMaxCols + 8 * kLongThreads - 1) / (8 * kLongThreads) * kLongThreads * 16;
-constexpr float kScaleMin = 0x1p-100f;  // keeps 1 / scale finite for a group of zeros
+constexpr float kMost = 448.0f;            // the largest code's value
+constexpr float kLeast = kMost * 0x1p-100f;  // of a group's largest |y|: keeps 1 / scale finite for a group of zeros (448 * (1 / 448) is 1 in fp32)
 
 struct Vec {
   uint32_t w[4];  // eight bf16
@@ -169,8 +170,8 @@ __device__ __noinline__ float largest_value(Vec h, Vec w, float inv, float woff)
   scaled<false, true>(h, w, inv, woff, v);
   return largest(v, true);
 }
-// Whether the largest product of h and a weight leaves them and their product with inv well inside fp32's range.
-__device__ __forceinline__ bool in_range(float amax, float inv) { return amax >= 0x1p-100f && amax < INFINITY && amax * inv < INFINITY; }
+// Whether the largest product of h and a weight, and the largest y that comes of it, are well inside fp32's range, and above the least.
+__device__ __forceinline__ bool in_range(float amax, float ymax) { return amax >= 0x1p-100f && amax < INFINITY && ymax >= kLeast && ymax < INFINITY; }
 // Over the `lanes` neighbouring lanes of a group.
 __device__ __forceinline__ float group_max(float m, int lanes) {
   for (int off = lanes >> 1; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
@@ -263,25 +264,23 @@ __global__ void __launch_bounds__(NV ? 1024 : kLongThreads, NV ? 1 : 2) rms_norm
     }
     block_reduce<FP8 == 2>(sq, amax, slots[0][turn], slots[1][turn]);
     const float inv = __frsqrt_rn(__fdiv_rn(sq, (float)k) + a.eps);
-    // Codes are those of h * weight * (inv / scale), one rounding less than by way of y; where the products h * weight pass
-    // fp32's range or come near its end, of h * inv * weight / scale.
-    float first = 1.0f, then = inv, t = 0.0f;  // y = h * first * weight * then, the code's value h * first * weight * t
-    auto step = [&](float am) {  // the scale, from the largest |h * first * weight|
-      const float s = fmaxf(am * then * (1.0f / 448.0f), kScaleMin);
-      t = __fdiv_rn(then, s);
-      return s;
-    };
+    // A code is that of h * weight * 448 / (the largest |h * weight|), in which 1 / sqrt cancels: two roundings, and the
+    // same code whatever else the row holds.  Where the products h * weight pass fp32's range or come near its end, or the
+    // scale is its least, h * inv * weight stands for them.
+    float first = 1.0f, t = 0.0f;  // the value of a code is h * first * weight * t
     if (FP8 == 2) {
-      if (!in_range(amax, inv)) {  // the same for the block
-        first = inv, then = 1.0f, amax = 0.0f;
+      float ymax = amax * inv;
+      if (!in_range(amax, ymax)) {  // the same for the block
+        first = inv, amax = kLeast;
 #pragma unroll(LONG ? 1 : NV)
         for (int i = 0; i < n; ++i) amax = fmaxf(amax, largest_value(value(i), weight(i), inv, a.woff));
         float none = 0.0f;
         __syncthreads();
         block_reduce<true>(none, amax, slots[0][turn], slots[1][turn]);
+        ymax = amax;
       }
-      const float s = step(amax);
-      if (threadIdx.x == 0) a.scales[r * a.lds] = s;
+      t = __fdiv_rn(kMost, amax);
+      if (threadIdx.x == 0) a.scales[r * a.lds] = ymax * (1.0f / kMost);
     }
 #pragma unroll(LONG ? 2 : NV)
     for (int i = 0; i < n; ++i) {
@@ -297,16 +296,18 @@ __global__ void __launch_bounds__(NV ? 1024 : kLongThreads, NV ? 1 : 2) rms_norm
       }
       if (FP8 == 1) {
         // NaN does not enter a maximum.  What lies past the row's end is 0.
-        first = 1.0f, then = inv;
         scaled<P, false>(f, g, 1.0f, a.woff, v);
         amax = group_max(largest(v, false), a.group_lanes);
-        if (__any_sync(0xFFFFFFFFu, !in_range(amax, inv))) {
-          first = inv, then = 1.0f;
-          scaled<P, true>(f, g, inv, a.woff, v);
-          amax = group_max(largest(v, true), a.group_lanes);
+        float ymax = amax * inv;
+        const bool far = !in_range(amax, ymax);  // the same for a group
+        if (far) ymax = amax = kLeast;
+        if (__any_sync(0xFFFFFFFFu, far && c < k)) {
+          scaled<P, true>(f, g, far ? inv : 1.0f, a.woff, v);  // times 1: as before
+          const float m = group_max(largest(v, true), a.group_lanes);
+          if (far) ymax = amax = fmaxf(m, kLeast);
         }
-        const float s = step(amax);
-        if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + (c >> a.group_log2)] = s;
+        t = __fdiv_rn(kMost, amax);
+        if ((threadIdx.x & (a.group_lanes - 1)) == 0 && c < k) a.scales[r * a.lds + (c >> a.group_log2)] = ymax * (1.0f / kMost);
       } else if (FP8 == 2) {
         scaled<P, true>(f, g, first, a.woff, v);
       }
