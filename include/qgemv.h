@@ -274,8 +274,10 @@ qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
 /* ------------------------------------------------------------------ low-rank adapters beside a shared projection
  * Adapters of many requests at once: row i of the projection's output y = W x gets its own
  * adapter's share, e = ids[i]:
- *     h = a_e x[i]              (rank_e sums over k, fp32)
- *     out[i][n] = bf16( y[i][n] + scales[e] * sum_j b_e[n][j] * h_j )        (fp32, rounded once)
+ *     h = scales[e] * a_e x[i]  (rank_e sums over k and the product, fp32)
+ *     out[i][n] = bf16( y[i][n] + sum_j b_e[n][j] * h_j )                    (sums in fp32, rounded once)
+ * In the second product each h_j stands as two bf16 terms, 16 bits of it: off by 2^-16 of its magnitude at most.
+ * Infinities and NaN in x, a, b and y go by the formula (b's infinities where |h_j| is 2^-110 or more, or 0).
  * ids[i] = -1: no adapter, out[i] = y[i].  Rows of one adapter may lie anywhere; its weights are
  * read once for 16 of them (128 where there are more than 256 rows).  Elements of a and b past an adapter's rank, whatever their
  * bits, do not enter. */

@@ -41,11 +41,18 @@ __device__ __forceinline__ void copy_wait() {
 // Bytes of a piece of eight elements of which `left` remain.
 __device__ __forceinline__ int bytes_of(int left) { return 2 * max(0, min(8, left)); }
 
-// Two h as two bf16 terms each: 16 bits of the value; an infinite one is its first term alone.
+// The first of a value's two bf16 terms (in the upper half): the next one below its magnitude, so that the second has its sign and
+// neither is 0 unless the value is.  Then an infinite element of B gives the infinity of the formula, not inf - inf or inf * 0, and
+// a value beyond bf16's largest number stays finite.  (Below 2^-110 the second may be 0.)
+__device__ __forceinline__ uint32_t first_term(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (u & 0x7FFFFFFFu) ? (u - 1u) & 0xFFFF0000u : u;
+}
+// Two h as two bf16 terms each: 16 bits of the value (the second is at most one step of the first, and rounds by 2^-16 of the value).
 __device__ __forceinline__ void split_h2(float x, float y, uint32_t& top, uint32_t& rest) {
-  top = pack_bf16(x, y);
-  const float l = x - bf_lo(top), h = y - bf_hi(top);
-  rest = pack_bf16(isinf(x) ? 0.0f : l, isinf(y) ? 0.0f : h);
+  const uint32_t a = first_term(x), b = first_term(y);
+  top = b | a >> 16;
+  rest = pack_bf16(x - __uint_as_float(a), y - __uint_as_float(b));
 }
 // scale times eight h, those from `valid` on (ranks past the adapter's) as zeros.
 __device__ __forceinline__ void split_h(const float (&v)[8], float scale, int valid, uint4& top, uint4& rest) {
