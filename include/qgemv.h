@@ -299,8 +299,8 @@ size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
 
 /* ids: int32 [m_rows] on the device; x bf16 [m_rows][ldx]; y and out bf16 [m_rows][ldy] / [m_rows][ldo].  out may be
  * y itself with the same stride: rows without an adapter, or whose adapter has rank 0, are then not touched; no other overlap.
- * ids and ranks are checked on the device: an id outside -1 .. n_adapters-1 or a rank outside
- * 0 .. max_rank counts as no adapter and puts QG_ERR_INVALID_ARG into the workspace's status word
+ * ids and ranks are checked on the device: an id outside -1 .. n_adapters-1, or one whose adapter's rank is outside
+ * 0 .. max_rank, counts as no adapter and puts QG_ERR_INVALID_ARG into the workspace's status word
  * (qg_workspace_status).  m_rows may be 0, and is below 2^27; n and k are below 2^24, the leading
  * dimensions below 2^31.  The workspace must be zero-filled before its first use and after QG_ERR_TIMEOUT; every
  * other qlora call, of any sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not

@@ -91,12 +91,19 @@ __device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* total) {
 // Adapter of a row, n_adapters for none (and for an id out of range).
 __device__ __forceinline__ int bin_of(int id, int n_adapters) { return (unsigned)id < (unsigned)n_adapters ? id : n_adapters; }
 
-// Rank of adapter e (0 for the rows without one); one out of range counts as 0 and is reported.
-__device__ __forceinline__ int rank_of(const LoraArgs& p, int e) {
+// Rank of adapter e (0 for the rows without one), or kBadRank: out of range, to be taken as 0 and reported if a row names it.
+constexpr int kBadRank = 255;
+__device__ __forceinline__ int rank_or_bad(const LoraArgs& p, int e) {
   if (e >= p.n_adapters) return 0;
   const int r = p.ranks ? p.ranks[e] : p.max_rank;
+  return r >= 0 && r <= p.max_rank ? r : kBadRank;
+}
+__device__ __forceinline__ void report_invalid(const LoraArgs& p) { atomicCAS(p.status, 0, kStatusInvalid); }
+// Rank of the adapter e < n_adapters of a row; one out of range counts as 0 and is reported.
+__device__ __forceinline__ int rank_of(const LoraArgs& p, int e) {
+  const int r = p.ranks ? p.ranks[e] : p.max_rank;
   if (r >= 0 && r <= p.max_rank) return r;
-  atomicCAS(p.status, 0, kStatusInvalid);
+  report_invalid(p);
   return 0;
 }
 
@@ -114,7 +121,7 @@ struct Tiles {
     const int tid = threadIdx.x, lane = tid & 31, bins = p.n_adapters + 1;
     for (int e = tid; e <= bins; e += THREADS) first[e] = 0;
     for (int i = p.m + tid; i < padded; i += THREADS) bins_of_rows[i] = 0xFFFF;
-    for (int e = tid; e <= p.n_adapters; e += THREADS) rank[e] = (uint8_t)rank_of(p, e);
+    for (int e = tid; e <= p.n_adapters; e += THREADS) rank[e] = (uint8_t)rank_or_bad(p, e);
     __syncthreads();
     bool bad = false;
     for (int i0 = tid; i0 - lane < p.m; i0 += 16 * THREADS) {
@@ -134,7 +141,7 @@ struct Tiles {
         if (e[u] >= 0 && lane == __ffs(same) - 1) atomicAdd(&first[e[u]], __popc(same));  // integer counts: order-free
       }
     }
-    if (bad) atomicCAS(p.status, 0, kStatusInvalid);
+    if (bad) report_invalid(p);
     __syncthreads();
     constexpr int kPer = (kLoraMaxAdapters + 1 + THREADS - 1) / THREADS;
     const int per_bin = (bins + THREADS - 1) / THREADS, e0 = tid * per_bin;
@@ -142,6 +149,10 @@ struct Tiles {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       c[i] = i < per_bin && e0 + i < bins ? (first[e0 + i] + T - 1) / T : 0;
+      if (i < per_bin && e0 + i < bins && rank[e0 + i] == kBadRank) {
+        rank[e0 + i] = 0;
+        if (c[i]) report_invalid(p);
+      }
       if (e0 + i == p.n_adapters && p.out == p.y) c[i] = 0;  // in place: nothing to do without an adapter
       sum += c[i];
     }
