@@ -47,11 +47,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // a in the l
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Eight elements from column c of a row of k elements; those past its end are 0 and are not read.
+// Eight elements from column c of a row of k elements; those past its end are 0 and are not read.  (A plain load: an output may lie on
+// the row.)
 __device__ __forceinline__ Vec load8(const uint16_t* row, int c, int k) {
   Vec v = {{0u, 0u, 0u, 0u}};
   if (c + 8 <= k) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(row + c));
+    const uint4 u = *reinterpret_cast<const uint4*>(row + c);
     v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
   } else {
 #pragma unroll
