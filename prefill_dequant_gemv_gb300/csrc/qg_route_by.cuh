@@ -50,6 +50,22 @@ __device__ __forceinline__ float quick_score(const RouteRule& r, float l, float 
   return r.sigmoid ? rcp_approx(1.0f + __expf(-l)) : __expf(l - m) * inv;
 }
 
+// A lane's share of a softmax's sum as the weights need it: expf, added in pairs (S: a power of two), so that a large term
+// meets log2 S roundings and not S.
+template <int S>
+__device__ __forceinline__ float exp_sum(const float (&c)[S], float m) {
+  float part[6];  // part[b]: of the 2^b terms before, where they are complete
+  int b = 0;
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    float v = c[i] == c[i] ? expf(c[i] - m) : 0.0f;  // NaN: no expert, or one left out
+#pragma unroll
+    for (b = 0; i >> b & 1; ++b) v = part[b] + v;
+    part[b] = v;
+  }
+  return part[b];
+}
+
 // The two largest of a and b's (a0 >= a1, b0 >= b1).
 template <class F>
 __device__ __forceinline__ void merge2(F& a0, F& a1, F b0, F b1) {
@@ -247,11 +263,15 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
 #pragma unroll
     for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, off));
     float s = 0.0f;
+    if (r.renormalise) {  // the sum enters the choice alone
 #pragma unroll
-    for (int i = 0; i < S; ++i) s += c[i] == c[i] ? __expf(c[i] - m) : 0.0f;
+      for (int i = 0; i < S; ++i) s += c[i] == c[i] ? __expf(c[i] - m) : 0.0f;
+    } else {
+      s = exp_sum(c, m);
+    }
 #pragma unroll
     for (int off = 16; off; off >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, off);
-    inv = rcp_approx(s);
+    inv = r.renormalise ? rcp_approx(s) : __frcp_rn(s);
   }
   float near = 0.0f;  // and 2^-22 |c|
   if (r.values) {
