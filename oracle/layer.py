@@ -58,10 +58,15 @@ def lora(ids, x, y, a, b, scales, ranks):
 
 
 def route_by(logits, topk, score="softmax", bias=None, groups=1, topk_groups=1, group_best=2, renormalise=True, scale=1.0):
-    """(ids [t, topk], weights [t, topk] in float64) by a rule, token by token."""
+    """(ids [t, topk], weights [t, topk] in float64) by a rule, token by token.
+
+    A softmax is over the logits that are numbers: a NaN one adds nothing to its sum, comes after every number and has the weight NaN.
+    Scores in 64 bits order the experts.  Without a bias, and with groups valued by one expert if there are any, the scores meant are
+    exact ones: two that 64 bits round to one value (a sigmoid of 40 and of 50) are in their logits' order."""
     lg = np.asarray(logits, np.float32).astype(np.float64)
     t, n = lg.shape
     ids, weights = np.zeros((t, topk), np.int64), np.zeros((t, topk))
+    exact = bias is None and (groups == 1 or group_best == 1)
     for i in range(t):
         l = lg[i]
         num = ~np.isnan(l)
@@ -71,22 +76,28 @@ def route_by(logits, topk, score="softmax", bias=None, groups=1, topk_groups=1, 
             else:
                 e = np.exp(l - np.max(l[num], initial=-np.inf))
                 s = e / np.sum(e[num])
-            if bias is None and (groups == 1 or group_best == 1):
-                c = l.copy()  # the same order
-            else:
-                c = s + (0.0 if bias is None else np.asarray(bias, np.float32).astype(np.float64))
+            c = s + (0.0 if bias is None else np.asarray(bias, np.float32).astype(np.float64))
+
+            def place(e):  # smaller comes first: by value, then by the logit where exact scores are meant, then by the index
+                nan = np.isnan(l[e]) if exact else np.isnan(c[e])
+                return nan, 0.0 if np.isnan(c[e]) else -c[e], -l[e] if exact and not nan else 0.0, e
             out = np.zeros(n, bool)
             if groups > 1:
                 per = n // groups
-                value = np.full(groups, -np.inf)
-                for g in range(groups):
-                    part = np.sort(c[g * per:(g + 1) * per][~np.isnan(c[g * per:(g + 1) * per])])[::-1][:group_best]
-                    value[g] = np.sum(part) if len(part) == group_best else -np.inf
-                keep = sorted(range(groups), key=lambda g: (-value[g], g))[:topk_groups]
-                for g in range(groups):
-                    out[g * per:(g + 1) * per] = g not in keep
-            order = sorted(np.flatnonzero(~out), key=lambda e: (np.isnan(c[e]), -c[e] if not np.isnan(c[e]) else 0.0, e))
-            ids[i] = order[:topk]
+                if exact:  # a group's value is its first expert's
+                    value = [min(place(e) for e in range(g * per, g * per + per)) for g in range(groups)]
+                    value = [(False, 0.0, np.inf) if v[0] else v[:3] for v in value]  # no number in it: as minus infinity
+                    keep = sorted(range(groups), key=lambda g: value[g] + (g,))
+                else:
+                    value = np.full(groups, -np.inf)
+                    for g in range(groups):
+                        part = np.sort(c[g * per:(g + 1) * per][~np.isnan(c[g * per:(g + 1) * per])])[::-1][:group_best]
+                        value[g] = np.sum(part) if len(part) == group_best else -np.inf
+                        value[g] = -np.inf if np.isnan(value[g]) else value[g]
+                    keep = sorted(range(groups), key=lambda g: (-value[g], g))
+                for g in keep[topk_groups:]:
+                    out[g * per:(g + 1) * per] = True
+            ids[i] = sorted(np.flatnonzero(~out), key=place)[:topk]
             w = s[ids[i]]
             weights[i] = scale * (w / np.sum(w) if renormalise else w)
     return ids, weights
