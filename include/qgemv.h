@@ -356,11 +356,14 @@ qg_status qmoe_route(const float* logits, int64_t t, int n_experts, int topk,
  *   The topk remaining experts of largest c, in descending order (ties to the lower index), are chosen;
  *     w_e = scale * s_e, or scale * s_e / (sum of the chosen s) with renormalise.
  * The choice is the one that scores in 64 bits give: c in fp32 decides where it is clear, and a
- * token with two values nearer to each other than fp32's error is decided in 64 bits.  Without a bias, and
- * with groups valued by one expert if there are any, c is ordered as the logits are, and they decide.  (Values
- * that are one in exact arithmetic and not in 64 bits, such as sums of two with other summands, come as 64 bits have them.)
- * The weights are fp32.  NaN values of c come after every number; a weight is NaN where the formula's is
- * (renormalised weights whose sum is 0 among them). */
+ * token with two values nearer to each other than fp32's error is decided in 64 bits.  (Values that are one in
+ * exact arithmetic and not in 64 bits, such as sums of two with other summands, come as 64 bits have them.)  One
+ * exception: without a bias, and with groups valued by one expert if there are any, exact scores are meant, whose order is the
+ * logits', and these decide, also between scores that 64 bits round to one value (sigmoids of 40 and 50, a softmax's far tail).
+ * The weights are fp32, of exact scores: their sum is 0, and the renormalised weights NaN, only where all chosen logits are
+ * -infinity.  A softmax is over the logits that are numbers: a NaN logit adds nothing to its sum.  NaN values of c come after
+ * every number, in a group too (one with fewer than group_best numbers has the value -infinity); the weight of a NaN logit
+ * is NaN, and with renormalise all of its token's are; with a logit of +infinity a softmax's weights are NaN. */
 typedef enum { QG_SCORE_SOFTMAX = 1, QG_SCORE_SIGMOID = 2 } qg_score;
 typedef struct {
   int32_t score;          /* qg_score */

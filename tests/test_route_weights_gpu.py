@@ -43,3 +43,26 @@ def test_one_large_term_among_many_small_ones():
         lg[0, 3] = 0.0
         off, _ = errors(q, lg, 1)
         assert off.max() <= 11.3, (d, off.max())
+
+
+def test_scores_below_every_number():
+    """Renormalised weights are of exact scores: e^-800 and e^-801 are in the proportion of e to 1.  Each term 2 u and its argument's
+    rounding (none: whole numbers), the sum 5 u, a division, the factor: 10 u."""
+    q = qlib()
+    lg = torch.full((3, 40), -2000.0, device="cuda")
+    lg[:, 7], lg[:, 9] = -800.0, -801.0
+    want = 2.5 * np.array([1.0 / (1.0 + np.exp(-1.0)), 1.0 / (1.0 + np.exp(1.0))])
+    # by sigmoid, and by a softmax whose largest logit is in a group that a bias leaves out
+    groups = lg.clone()
+    groups[:, 30] = 100.0
+    bias = torch.zeros(40, device="cuda")
+    bias[20:] = -4.0
+    for ids, w, _ in (q.route(lg, 2, rule=q.RouteRule("sigmoid", scale=2.5)),
+                      q.route(groups, 2, rule=q.RouteRule("softmax", bias=bias, groups=2, topk_groups=1, group_best=1, scale=2.5))):
+        w = w.cpu().numpy().astype(np.float64)
+        if int(ids[0, 0]) == 7:
+            assert ids.tolist() == [[7, 9]] * 3 and np.all(np.abs(w - want) <= 10 * U * want)
+        else:  # the softmax's scores are 0 in 64 bits: the index decides, and the weights are those of the chosen logits
+            assert ids.tolist() == [[0, 1]] * 3 and np.all(np.abs(w - 1.25) <= 10 * U * 1.25)
+    lg.fill_(float("-inf"))
+    assert torch.isnan(q.route(lg, 2, rule=q.RouteRule("sigmoid"))[1]).all()
