@@ -248,7 +248,10 @@ qg_status qgemm_w4a4(const qg_weight* w, const void* x, int64_t m_rows, int64_t 
  * E4M3: a group of `group` consecutive elements of a row (32, 64 or 128; the last may be shorter),
  * or the whole row (group 0), has the fp32 scale s = max(amax / 448, 2^-100), amax its largest finite
  * |y|, and the codes E4M3(y / s), nearest even and saturating at 448: infinities saturate, NaN stays
- * NaN and neither moves a scale.  A row with a NaN in it is NaN, as the formula gives it; the squares
+ * NaN and neither moves a scale.  As 1 / sqrt cancels in y / s, the codes are those of h * (weight + weight_offset) * 448 / the
+ * group's largest such magnitude, the same whatever else the row holds (unless these leave fp32's range or s is 2^-100: then
+ * by way of h / sqrt).  No product of this library takes E4M3 activations; the codes are for products outside it.
+ * A row with a NaN in it is NaN, as the formula gives it; the squares
  * are summed in fp32, so a row whose sum passes 2^128 comes out as zeros (NaN where h is infinite) and,
  * with eps 0, one whose squares are all below 2^-149 as infinities (NaN where h is 0).  y has the same bits
  * with codes and without. */
@@ -278,9 +281,9 @@ qg_status qg_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t 
  *     out[i][n] = bf16( y[i][n] + sum_j b_e[n][j] * h_j )                    (sums in fp32, rounded once)
  * In the second product each h_j stands as two bf16 terms, 16 bits of it: off by 2^-16 of its magnitude at most.
  * Infinities and NaN in x, a, b and y go by the formula (b's infinities where |h_j| is 2^-110 or more, or 0).
- * ids[i] = -1: no adapter, out[i] = y[i].  Rows of one adapter may lie anywhere; its weights are
- * read once for 16 of them (128 where there are more than 256 rows).  Elements of a and b past an adapter's rank, whatever their
- * bits, do not enter. */
+ * ids[i] = -1: no adapter, out[i] = y[i].  Rows of one adapter may lie anywhere; its weights are read once for 16 of them in every
+ * 256 rows of the call, or, where it has more than 256 rows (512 with 16 adapters or more), once for 128 of them.  Elements of a and b
+ * past an adapter's rank, whatever their bits, do not enter. */
 typedef struct {
   int32_t n_adapters;     /* 1 .. 1024 */
   int32_t max_rank;       /* rows of a and columns of b that each adapter has room for: a multiple of 8, 8 .. 128 */
@@ -306,8 +309,8 @@ size_t qlora_workspace_size(const qg_lora* lora, int64_t m_rows);
  * other qlora call, of any sizes that it has room for, leaves it ready for the next one; calls that overlap on the GPU must not
  * share it, and no other entry point may use it in between.  More than 256 rows (512 where there are 16 adapters or more) need a GPU of
  * 96 SMs or more (QG_ERR_UNSUPPORTED otherwise) and run on all of its SMs at once, so such a call starts when no other kernel
- * holds one.  Deterministic (the order in which h is summed goes by the call's sizes and ids); one launch for every 256
- * rows, or for every 16384 where they are more. */
+ * holds one.  Deterministic (the order in which h is summed goes by the call's sizes and ids); one launch for every
+ * 256 rows up to those numbers, for every 16384 beyond. */
 qg_status qlora(const qg_lora* lora, const int32_t* ids, int64_t m_rows, const void* x, int64_t ldx, const void* y,
                 int64_t ldy, void* out, int64_t ldo, void* workspace, size_t workspace_bytes, void* stream);
 

@@ -370,8 +370,9 @@ int launch(const LoraArgs& p, const DeviceInfo& dev, cudaStream_t s) {
   static std::atomic<unsigned long long> configured{0};
   if (!allow_smem((const void*)lora_kernel<R>, S::kSmem, configured)) return QG_ERR_CUDA;
   // The tiles are counted on the device.  About as many: full ones, or one for each adapter that is met where every row draws its
-  // own.  The GPU's partitions hold 15 clusters of eight such CTAs and 36 of four (its occupancy query); more would wait for a turn
-  // of their own.
+  // own.  The 152 SMs' partitions hold 15 clusters of eight CTAs and 36 of four (the occupancy query's answer for each of the four
+  // forms, which all fill an SM's shared memory); more would wait for a turn of their own, and so would the last ones on a GPU that
+  // holds fewer: slower, with the same results.
   const double met = p.n_adapters * -std::expm1(p.m * std::log1p(-1.0 / (p.n_adapters + 1)));
   const int full = (p.m + T - 1) / T, likely = std::max(full, std::min(p.m, (int)std::ceil(met)));
   const int most = std::min(p.m, full + std::min(p.n_adapters + 1, p.m));

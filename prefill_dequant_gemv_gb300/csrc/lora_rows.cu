@@ -19,7 +19,8 @@
 // a row: y comes and the sum leaves 16 bytes a lane, y by way of slots in shared memory that are the lane's own.
 //
 // Measured in a graph (us; the bytes at the copy rate): 3999 rows of 5 adapters of rank 16, 6144 to 5120 38.7 (19.5); 8192 rows of 3
-// of rank 64, 5120 to 5120 66 (37.6), to 17408 128 (97.5); 2048 of rank 128, 5120 to 7168 47 (13.1); 300 rows of 4 of rank 16 19 (2.0).
+// of rank 64, a third each, 5120 to 5120 66 (37.6), to 17408 128 (97.5), the same with 5707 of the rows without an adapter and 1934 and 551
+// of two 142; 2048 of rank 128, 5120 to 7168 46 (13.1); 300 rows of 4 of rank 16 18 to 19 (2.0).  In a stream of calls 3 us more.
 // What is over the bytes: the rows' sorting, 7 to 9 us, and the chain from a tile's last input to its first output, some 10.
 // y's first chunks sent for into L2 during that chain made it longer (39 -> 42, 133 -> 136).
 #include <algorithm>

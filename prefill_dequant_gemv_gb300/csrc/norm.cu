@@ -12,8 +12,8 @@
 // sums in the same order.  A group of 32, 64 or 128 elements lies in 4, 8 or 16 neighbouring lanes, so its scale needs shuffles only.
 //
 // Measured with residual, in a graph (share of the bytes at the copy rate, 6798 GB/s): one row of 5120 2.0 us, 64 to E4M3 in groups of
-// 128 2.2; 4096 x 5120 27.5 us (90%), to E4M3 in groups 26.0 (83%), one scale a row 29.4 (73%); 18001 x 2048 48.1 (90%), 41.0 (92%) and
-// 43.9 (86%); 2000 x 17408 48 (85%), 57 (63%) and 55 (65%).
+// 128 2.2; 4096 x 5120 27.5 us (90%), to E4M3 in groups 26.2 (82%), one scale a row 29.0 (74%); 18001 x 2048 48.2 (90%), 41.1 (92%) and
+// 43.4 (87%); 2000 x 17408 48.1 (85%), 56.3 (64%) and 54.2 (66%).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>

@@ -23,9 +23,9 @@
 // instructions, 27.6 us for 8192 tokens under ncu against 20.9): the k-th largest of the lanes' largest values is below the winners, the few experts
 // above it go to one lane each, and each counts those that come before it.
 //
-// Measured in a graph, tables included (us): one token of 256 experts in groups 4.9, 64 of 512 by softmax and bias 6.5, 8192 by sigmoid
-// and bias 25 (their logits at the copy rate: 2.5), 8192 of 256 in groups 26, 5001 of 160 in groups by softmax 16.  A near tie of
-// sigmoids adds 2 us to a call, of softmax 3, or 16 where the softmax's sum is redone.
+// Measured in a graph, call after call, tables included (us): one token of 256 experts in groups 4.8, 64 of 512 by softmax and bias 6.6,
+// 8192 by sigmoid and bias 26 (their logits at the copy rate: 2.5), 8192 of 256 in groups 27, 5001 of 160 in groups by softmax 16.7, without
+// renormalising 17.2.  A near tie of sigmoids adds 2 us to a call, of softmax 3, or 16 where the softmax's sum is redone.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -10,9 +10,9 @@
 // with at most kRouteTile pairs per tile for the grouped prefill GEMM.  Everything is
 // deterministic: ranks come from ordered scans, never from atomic arrival order.
 //
-// Up to 8 tokens (12 of more than 256 experts, two by a rule) take one CTA, up to 64 a cluster; more a launch of the top-k with counts of every block of tokens,
-// one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts, topk 10: 32 tokens 6.1 us
-// (9.4 in one CTA), 64 7.2 (12 with four launches), 8192 24 (27).
+// Up to 8 tokens (12 of more than 256 experts, two by a rule) take one CTA, up to 64 a cluster; more a launch of the top-k with counts of
+// every block of tokens, one of the sums over the blocks where they are more than 16, and one of the placement.  In a graph, 512 experts,
+// topk 10: 32 tokens 6.4 us (9.3 in one CTA), 64 7.1 (12 with four launches); behind another kernel 1000 13.0 (15.7), 8192 24 (27).
 #include <cuda_runtime.h>
 
 #include "qg_internal.h"
