@@ -419,8 +419,8 @@ __device__ __forceinline__ void warp_route(const RouteRule& r, const float* lg, 
     for (int off = 16; off; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, off));
     if (r.sigmoid)
       w = lw > 0.0f ? 1.0f / (1.0f + expf(-lw)) : expf(lw - fminf(big, 0.0f)) / (1.0f + expf(lw));
-    else
-      w = expf(lw - big);
+    else  // NaN with a logit of +infinity, also where the index has chosen (a bias, every score NaN) and left it out
+      w = m < INFINITY ? expf(lw - big) : __int_as_float(0x7FC00000);
     w = slot >= 0 ? w : 0.0f;
     float s = w;
 #pragma unroll
